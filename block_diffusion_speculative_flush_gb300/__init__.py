@@ -30,6 +30,8 @@ __all__ = [
     "Target", "dflash_target_create", "dflash_target_destroy", "dflash_target_forward", "dflash_target_trim",
     "dflash_target_length", "dflash_target_argmax", "dflash_target_device_status",
     "dflash_logits_compare", "dflash_exactness_summarize", "dflash_target_exactness_probe", "exactness_rows",
+    "dflash_kv_append", "dflash_paged_attention", "dflash_prompt_attention", "dflash_attention_workspace",
+    "dflash_token_logprobs", "dflash_status_check",
 ]
 
 
@@ -486,3 +488,200 @@ def dflash_target_exactness_probe(target: Target, tokens: torch.Tensor, start: i
     _check(lib.dflash_target_exactness_probe(target.handle, _ptr(tokens), rows, start, _ptr(block_logits),
                                              _ptr(chain_logits), _ptr(out), C.byref(s)))
     return {k: getattr(s, k) for k, _ in s._fields_}
+
+
+# ---------------------------------------------------------------------------
+# target-side operators
+# ---------------------------------------------------------------------------
+_DTYPES = {torch.float32: DFLASH_DTYPE_F32, torch.bfloat16: DFLASH_DTYPE_BF16}
+
+
+def _stream_of(stream, device) -> C.c_void_p:
+    return C.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError("all tensors of a call live on one device")
+
+
+def _heads(t: torch.Tensor, dtype: torch.dtype, what: str) -> _abi.dflash_heads:
+    """[rows, heads, head_dim] with a dense last dimension."""
+    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+        raise ValueError(f"{what}: a CUDA {dtype} tensor [rows, heads, head_dim] with a dense last dimension")
+    # torch may report any stride for a dimension of one entry; the library asks for one a head fits in
+    row = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
+    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
+    return _abi.dflash_heads(t.data_ptr() if t.numel() else None, row, head)
+
+
+def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> _abi.dflash_kv_pages:
+    """[n_pages, page_size, n_kv_heads, head_dim] views of one shape and stride (a permuted
+    [n_pages, n_kv_heads, page_size, head_dim] cache too)."""
+    if not k_pages.is_cuda or k_pages.dtype not in _DTYPES or k_pages.dim() != 4 or k_pages.stride(3) != 1 or \
+            v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+        raise ValueError("k_pages, v_pages: CUDA fp32 or bf16 [n_pages, page_size, n_kv_heads, head_dim] of one shape "
+                         "and stride, with a dense last dimension")
+    n, page, heads, d = k_pages.shape
+    st = k_pages.stride()
+    return _abi.dflash_kv_pages(_DTYPES[k_pages.dtype], heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(),
+                                st[0] if n > 1 else max(st[0], d), st[1], st[2] if heads > 1 else d)
+
+
+def _int_vector(t: torch.Tensor, n: int | None, what: str) -> int:
+    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
+            (n is not None and t.numel() != n):
+        raise ValueError(f"{what}: a contiguous CUDA int32 vector" + (f" of {n}" if n is not None else ""))
+    return t.data_ptr()
+
+
+def _ragged(starts, lens, table, total: int, max_rows: int, max_len: int, status) -> _abi.dflash_ragged:
+    _int_vector(starts, None, "starts [batch + 1]")
+    batch = starts.numel() - 1
+    if status is not None:
+        _int_vector(status, 1, "status")
+    r = _abi.dflash_ragged(batch, total, max_rows, max_len, starts.data_ptr(), None, None, 0, 0,
+                           None if status is None else status.data_ptr())
+    if lens is not None:
+        r.lens = _int_vector(lens, batch, "lens")
+        if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch or \
+                (table.stride(1) != 1 and table.shape[1] > 1):
+            raise ValueError(f"table: CUDA int32 [{batch}, pages per sequence] with a dense last dimension")
+        r.table, r.table_width = table.data_ptr(), table.shape[1]
+        r.table_stride = table.stride(0) if batch > 1 else max(table.stride(0), table.shape[1])
+    return r
+
+
+def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse) -> _abi.dflash_attention:
+    if q.dtype not in _DTYPES:
+        raise ValueError("q: fp32 or bf16")
+    qh, oh = _heads(q, q.dtype, "q"), _heads(out, q.dtype, "out")
+    if out.shape != q.shape:
+        raise ValueError("out: the shape of q")
+    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or not lse.is_contiguous() or
+                            tuple(lse.shape) != tuple(q.shape[:2])):
+        raise ValueError("lse: contiguous CUDA fp32 [rows, n_q_heads]")
+    d = q.shape[2]
+    return _abi.dflash_attention(_DTYPES[q.dtype], q.shape[1], n_kv_heads, d, int(causal), int(window),
+                                 d ** -0.5 if scale is None else float(scale), qh, oh,
+                                 None if lse is None else lse.data_ptr(), None, 0)
+
+
+def _with_workspace(a, r, pages, workspace, stream, device):
+    """Points a at the caller's workspace, or at one from torch's allocator on the call's stream."""
+    need = lib.dflash_attention_workspace(C.byref(a), C.byref(r), pages)
+    _check(min(need, 0))
+    if workspace is None and need:
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA uint8 tensor")
+        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
+    return workspace
+
+
+def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                     starts: torch.Tensor, lens: torch.Tensor, table: torch.Tensor, status=None, stream=None) -> None:
+    """New rows k, v [rows, n_kv_heads, head_dim] of a ragged batch into their pages
+    [n_pages, page_size, n_kv_heads, head_dim]: sequence b's rows starts[b] .. starts[b + 1] - 1
+    become its last positions below lens[b]; table [batch, pages] names its pages."""
+    p = _pages(k_pages, v_pages)
+    if k.shape != v.shape or tuple(k.shape[1:]) != (p.n_kv_heads, p.head_dim):
+        raise ValueError(f"k, v: [rows, {p.n_kv_heads}, {p.head_dim}]")
+    kh, vh = _heads(k, k_pages.dtype, "k"), _heads(v, k_pages.dtype, "v")
+    _same_device(k_pages, k, v, v_pages, starts, lens, table, status)
+    r = _ragged(starts, lens, table, k.shape[0], max(1, k.shape[0]), 1 << 30, status)
+    with torch.cuda.device(k_pages.device):
+        _check(lib.dflash_kv_append(C.byref(p), C.byref(r), C.byref(kh), C.byref(vh),
+                                    _stream_of(stream, k_pages.device)))
+
+
+def dflash_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages) -> int:
+    """Bytes a dflash_paged_attention call of these tensors and bounds needs."""
+    p = _pages(k_pages, v_pages)
+    a = _attention(q, out, p.n_kv_heads, True, 0, None, None)
+    r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, None)
+    need = lib.dflash_attention_workspace(C.byref(a), C.byref(r), C.byref(p))
+    _check(min(need, 0))
+    return need
+
+
+def dflash_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, starts: torch.Tensor,
+                           lens: torch.Tensor, table: torch.Tensor, out: torch.Tensor, max_rows: int,
+                           max_len: int | None = None, causal: bool = True, window: int = 0,
+                           scale: float | None = None, lse: torch.Tensor | None = None, workspace=None, status=None,
+                           stream=None) -> None:
+    """Attention of each sequence's new rows q [rows, n_q_heads, head_dim] over its pages, which already
+    hold them.  max_rows and max_len bound the new rows and the length of every sequence (max_len: None
+    takes what the table can hold); scale: None is head_dim ** -0.5."""
+    p = _pages(k_pages, v_pages)
+    a = _attention(q, out, p.n_kv_heads, causal, window, scale, lse)
+    _same_device(q, k_pages, v_pages, starts, lens, table, out, lse, workspace, status)
+    if max_len is None:
+        max_len = min(1 << 30, table.shape[-1] * k_pages.shape[1])
+    r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, status)
+    with torch.cuda.device(q.device):
+        _with_workspace(a, r, C.byref(p), workspace, stream, q.device)
+        _check(lib.dflash_paged_attention(C.byref(a), C.byref(r), C.byref(p), _stream_of(stream, q.device)))
+
+
+def dflash_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, out: torch.Tensor,
+                            max_rows: int, causal: bool = True, window: int = 0, scale: float | None = None,
+                            lse: torch.Tensor | None = None, workspace=None, status=None, stream=None) -> None:
+    """Attention of whole packed prompts: sequence b is rows starts[b] .. starts[b + 1] - 1 of
+    q [rows, n_q_heads, head_dim] and of k, v [rows, n_kv_heads, head_dim]."""
+    if k.shape != v.shape or k.dim() != 3 or q.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("k, v: [rows, n_kv_heads, head_dim] with q's rows and head_dim")
+    a = _attention(q, out, k.shape[1], causal, window, scale, lse)
+    kh, vh = _heads(k, q.dtype, "k"), _heads(v, q.dtype, "v")
+    _same_device(q, k, v, starts, out, lse, workspace, status)
+    r = _ragged(starts, None, None, q.shape[0], max_rows, 0, status)
+    with torch.cuda.device(q.device):
+        _with_workspace(a, r, None, workspace, stream, q.device)
+        _check(lib.dflash_prompt_attention(C.byref(a), C.byref(r), C.byref(kh), C.byref(vh),
+                                           _stream_of(stream, q.device)))
+
+
+def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor,
+                          entropy: torch.Tensor | None = None, top_ids: torch.Tensor | None = None,
+                          top_logprobs: torch.Tensor | None = None, temperature: float = 1.0, status=None,
+                          stream=None) -> None:
+    """Log probability of tokens[r] (int32, -1: none) under softmax(logits[r] / temperature), the row's
+    entropy, and its top entries: top_ids int32 and top_logprobs fp32 [rows, k], k at most 32."""
+    if not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2 or \
+            (logits.stride(1) != 1 and logits.shape[1] > 1):
+        raise ValueError("logits: CUDA fp32 or bf16 [rows, vocab] with a dense last dimension")
+    R, V = logits.shape
+    _int_vector(tokens, R, "tokens [rows]")
+    for t, what in ((logprobs, "logprobs"), (entropy, "entropy")):
+        if t is not None and (not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or
+                              tuple(t.shape) != (R,)):
+            raise ValueError(f"{what}: contiguous CUDA fp32 [rows]")
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    top = 0
+    if top_ids is not None:
+        if not top_ids.is_cuda or top_ids.dtype != torch.int32 or not top_ids.is_contiguous() or \
+                top_ids.dim() != 2 or top_ids.shape[0] != R or not top_logprobs.is_cuda or \
+                top_logprobs.dtype != torch.float32 or not top_logprobs.is_contiguous() or \
+                top_logprobs.shape != top_ids.shape:
+            raise ValueError("top_ids int32 and top_logprobs fp32: contiguous CUDA [rows, k] of one shape")
+        top = top_ids.shape[1]
+    if status is not None:
+        _int_vector(status, 1, "status")
+    _same_device(logits, tokens, logprobs, entropy, top_ids, top_logprobs, status)
+    ptr = lambda t: None if t is None else t.data_ptr()
+    a = _abi.dflash_logprobs(logits.data_ptr(), max(logits.stride(0), V) if R <= 1 else logits.stride(0),
+                             _DTYPES[logits.dtype], R, V, top, float(temperature), ptr(tokens), ptr(logprobs),
+                             ptr(entropy), ptr(top_ids), ptr(top_logprobs), ptr(status))
+    with torch.cuda.device(logits.device):
+        _check(lib.dflash_token_logprobs(C.byref(a), _stream_of(stream, logits.device)))
+
+
+def dflash_status_check(status: torch.Tensor, stream=None) -> None:
+    """Waits for the stream, clears the operators' status word and raises DFlashError if a bit was set."""
+    _int_vector(status, 1, "status")
+    with torch.cuda.device(status.device):
+        _check(lib.dflash_status_check(status.data_ptr(), _stream_of(stream, status.device)))

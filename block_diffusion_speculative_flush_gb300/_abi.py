@@ -83,6 +83,36 @@ class dflash_exactness_summary(C.Structure):
                 ("disagreements", C.c_int32), ("allows", C.c_int32)]
 
 
+class dflash_heads(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("row_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class dflash_kv_pages(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+                ("n_pages", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("slot_stride", C.c_int64), ("head_stride", C.c_int64)]
+
+
+class dflash_ragged(C.Structure):
+    _fields_ = [("batch", C.c_int32), ("total_rows", C.c_int32), ("max_rows", C.c_int32), ("max_len", C.c_int32),
+                ("starts", C.c_void_p), ("lens", C.c_void_p), ("table", C.c_void_p), ("table_width", C.c_int32),
+                ("table_stride", C.c_int32), ("status", C.c_void_p)]
+
+
+class dflash_attention(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("n_q_heads", C.c_int32), ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32),
+                ("causal", C.c_int32), ("window", C.c_int32), ("scale", C.c_float), ("q", dflash_heads),
+                ("out", dflash_heads), ("lse", C.c_void_p), ("workspace", C.c_void_p),
+                ("workspace_bytes", C.c_int64)]
+
+
+class dflash_logprobs(C.Structure):
+    _fields_ = [("logits", C.c_void_p), ("row_stride", C.c_int64), ("dtype", C.c_int32), ("rows", C.c_int32),
+                ("vocab", C.c_int32), ("top", C.c_int32), ("temperature", C.c_float), ("tokens", C.c_void_p),
+                ("logprobs", C.c_void_p), ("entropy", C.c_void_p), ("top_ids", C.c_void_p),
+                ("top_logprobs", C.c_void_p), ("status", C.c_void_p)]
+
+
 P = C.c_void_p
 SessArr = C.POINTER(C.c_void_p)
 
@@ -131,6 +161,16 @@ SIGNATURES = {
                                              C.POINTER(dflash_exactness_summary)]),
     "dflash_target_exactness_probe": (C.c_int, [P, P, C.c_int32, C.c_int64, P, P, P,
                                                 C.POINTER(dflash_exactness_summary)]),
+    "dflash_kv_append": (C.c_int, [C.POINTER(dflash_kv_pages), C.POINTER(dflash_ragged), C.POINTER(dflash_heads),
+                                   C.POINTER(dflash_heads), P]),
+    "dflash_attention_workspace": (C.c_int64, [C.POINTER(dflash_attention), C.POINTER(dflash_ragged),
+                                               C.POINTER(dflash_kv_pages)]),
+    "dflash_paged_attention": (C.c_int, [C.POINTER(dflash_attention), C.POINTER(dflash_ragged),
+                                         C.POINTER(dflash_kv_pages), P]),
+    "dflash_prompt_attention": (C.c_int, [C.POINTER(dflash_attention), C.POINTER(dflash_ragged),
+                                          C.POINTER(dflash_heads), C.POINTER(dflash_heads), P]),
+    "dflash_token_logprobs": (C.c_int, [C.POINTER(dflash_logprobs), P]),
+    "dflash_status_check": (C.c_int, [P, P]),
 }
 
 

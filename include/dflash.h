@@ -505,6 +505,143 @@ DFLASH_API int dflash_target_exactness_probe(dflash_target* t, const int32_t* to
                                              float* block_logits, float* chain_logits,
                                              dflash_exactness_row* out_rows, dflash_exactness_summary* summary);
 
+/* ---------------------------------------------------------------------------
+ * Target-side operators.
+ *
+ * What a target that serves speculative rounds runs next to the draft: a K/V
+ * cache in pages that its requests share, the attention of a prompt and of the
+ * verified block over it, and the log probabilities that answer a request.
+ * They work on caller-owned device buffers, need no model or session, allocate
+ * nothing and may be captured into a CUDA graph: lengths and tables are read
+ * on the device at every replay, the host gives bounds on them.
+ *
+ * Sequence b of a ragged batch owns rows starts[b] .. starts[b + 1] - 1 of the
+ * packed arrays: its n_b new tokens, the last n_b of its length.  Row i of them
+ * is at position lens[b] - n_b + i (prompts: i, the length is n_b).  Rows at or
+ * behind starts[batch] are never read or written.
+ *
+ * What the device finds wrong is OR-ed into *status (a device word the caller
+ * zeroes, or NULL) and never read or written through:
+ *   2  a sequence's starts or length break the bounds below: its rows are left
+ *      as they were;
+ *   4  a page id outside [0, n_pages): read as zeros, an append to it dropped;
+ *   1  a token id that is neither -1 nor in [0, vocab) (dflash_token_logprobs);
+ *   8  a bounded wait expired: the outputs are incomplete.
+ * dflash_status_check reads and clears the word. */
+#define DFLASH_STATUS_TOKEN 1
+#define DFLASH_STATUS_BOUNDS 2
+#define DFLASH_STATUS_PAGE 4
+#define DFLASH_STATUS_WAIT 8
+
+/* [rows][heads][head_dim]: strides in elements, the last dimension dense.  The
+ * base is 16-byte aligned and both strides are multiples of 16 bytes. */
+typedef struct dflash_heads {
+  void* data;
+  int64_t row_stride, head_stride;
+} dflash_heads;
+
+/* The paged K/V cache of one layer: slot s of page p of KV head h is at
+ * p * page_stride + s * slot_stride + h * head_stride elements of k and of v
+ * (so [page][slot][head][d] and [page][head][slot][d] both serve), head_dim
+ * dense elements each.  Bases 16-byte aligned, strides multiples of 16 bytes. */
+typedef struct dflash_kv_pages {
+  int32_t dtype;      /* DFLASH_DTYPE_F32 or DFLASH_DTYPE_BF16 */
+  int32_t n_kv_heads;
+  int32_t head_dim;   /* bf16: 64 or 128; fp32: a multiple of 4 up to 128 */
+  int32_t page_size;  /* a power of two in 8..1024 */
+  int64_t n_pages;    /* 1..2^31 - 1 */
+  void* k;
+  void* v;
+  int64_t page_stride, slot_stride, head_stride;
+} dflash_kv_pages;
+
+/* A ragged batch.  Bounds that hold for every sequence, else it is skipped
+ * with status 2: 0 <= starts[b] <= starts[b + 1] <= total_rows; n_b <=
+ * max_rows; n_b <= lens[b] <= min(max_len, table_width * page_size). */
+typedef struct dflash_ragged {
+  int32_t batch;          /* 1..32768 */
+  int32_t total_rows;     /* rows of the packed arrays, 0..2^30 */
+  int32_t max_rows;       /* bound on n_b, 1..2^24 (work is laid out for it: keep it tight) */
+  int32_t max_len;        /* paged: bound on lens[b], 1..2^30 (keep it tight) */
+  const int32_t* starts;  /* device [batch + 1], non-decreasing */
+  const int32_t* lens;    /* paged: device [batch], cached tokens with the new ones */
+  const int32_t* table;   /* paged: device [batch][table_stride], page of position p at p / page_size */
+  int32_t table_width;    /* entries of a row that may be read */
+  int32_t table_stride;   /* entries from one row to the next */
+  int32_t* status;        /* device word or NULL */
+} dflash_ragged;
+
+/* One attention call: out = softmax(scale q k^T over the visible keys) v, query
+ * head h with KV head h / (n_q_heads / n_kv_heads).  A query at position p sees
+ * key r < length unless causal != 0 and r > p, or window > 0 and p - r >= window
+ * (causal == 0: the new rows see each other, as a bidirectional block does).  A
+ * row that sees no key gets zeros and lse -inf.  What a row does not see never
+ * reaches it, whatever its bits (NaN and infinities among them).
+ * Scores, sums and accumulators are fp32; a bf16 call rounds the probabilities
+ * to bf16 for the second product.  out overlaps no input. */
+typedef struct dflash_attention {
+  int32_t dtype;       /* of q, k, v and out */
+  int32_t n_q_heads;   /* a multiple of n_kv_heads, at most 128 per KV head */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t causal;      /* 0 or 1 */
+  int32_t window;      /* 0 or 1..2^30 */
+  float scale;         /* finite, > 0 */
+  dflash_heads q;      /* [total_rows][n_q_heads][head_dim] */
+  dflash_heads out;    /* the same shape */
+  float* lse;          /* [total_rows][n_q_heads] natural log of the softmax sum, or NULL */
+  void* workspace;     /* 16-byte aligned, used until the call's kernels end; not shared by calls that may overlap */
+  int64_t workspace_bytes;  /* at least dflash_attention_workspace */
+} dflash_attention;
+
+/* Writes the new rows of K and V into their pages.  The pages that receive new
+ * rows belong to one sequence each (shared prefix pages are only read); two
+ * rows sent to one slot leave either of them there. */
+DFLASH_API int dflash_kv_append(const dflash_kv_pages* pages, const dflash_ragged* batch, const dflash_heads* k,
+                                const dflash_heads* v, void* stream);
+/* Workspace bytes of a call of these shapes (pages: as the call's, or NULL for
+ * prompts), or a negative status.  Depends on the host fields only. */
+DFLASH_API int64_t dflash_attention_workspace(const dflash_attention* a, const dflash_ragged* batch,
+                                              const dflash_kv_pages* pages);
+/* Attention of a chunk of new tokens (one token, a verified block, a piece of a
+ * prompt) over the paged cache, which already holds them (dflash_kv_append). */
+DFLASH_API int dflash_paged_attention(const dflash_attention* a, const dflash_ragged* batch,
+                                      const dflash_kv_pages* pages, void* stream);
+/* Attention of whole packed prompts: k, v [total_rows][n_kv_heads][head_dim].
+ * Of the batch only batch, total_rows, max_rows, starts and status are used. */
+DFLASH_API int dflash_prompt_attention(const dflash_attention* a, const dflash_ragged* batch, const dflash_heads* k,
+                                       const dflash_heads* v, void* stream);
+
+/* Log probabilities of given tokens under softmax(logits / temperature), with
+ * the distribution's entropy (natural log) and its top entries.  Row r: logits
+ * + r * row_stride, vocab entries of fp32 or bf16.
+ * tokens [rows] int32, -1: no token (its logprob is 0); entropy [rows] or NULL;
+ * top in 0..32 (and at most vocab): top_ids and top_logprobs [rows][top], value
+ * descending, then id ascending (NULL at top == 0).  A NaN never becomes a top
+ * entry: places without one get id -1 and NaN; any NaN in a row makes its
+ * log probabilities NaN.  Entries of -inf have probability zero; a row of
+ * nothing else has no distribution: its log probabilities are NaN. */
+#define DFLASH_LOGPROBS_MAX_TOP 32
+typedef struct dflash_logprobs {
+  const void* logits;
+  int64_t row_stride;   /* elements, >= vocab */
+  int32_t dtype;        /* DFLASH_DTYPE_F32 or DFLASH_DTYPE_BF16 */
+  int32_t rows, vocab;  /* rows >= 0, vocab 1..2^24 */
+  int32_t top;
+  float temperature;    /* finite, > 0 */
+  const int32_t* tokens;
+  float* logprobs;      /* [rows] */
+  float* entropy;
+  int32_t* top_ids;
+  float* top_logprobs;
+  int32_t* status;      /* device word or NULL */
+} dflash_logprobs;
+DFLASH_API int dflash_token_logprobs(const dflash_logprobs* a, void* stream);
+
+/* Waits for the stream, then reads and clears a status word (device): 0, or
+ * DFLASH_ERR_DEVICE with the reasons in dflash_last_error. */
+DFLASH_API int dflash_status_check(int32_t* status, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
