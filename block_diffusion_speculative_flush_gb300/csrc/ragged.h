@@ -6,7 +6,6 @@
 #include <stdint.h>
 
 #include "dflash.h"
-#include "kernels.h"
 
 namespace dfl {
 
@@ -74,6 +73,10 @@ __device__ __forceinline__ int vis_hi(int p, int len, int causal) { return causa
 
 // The CUDA-core path (fp32): bytes of workspace, and the launches.
 int64_t attn_simt_workspace(const Ragged& r, const AttnCall& a);
-cudaError_t launch_attn_simt(DT dt, const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st);
+cudaError_t launch_attn_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st);
+
+// The tensor-core path (bf16, head_dim 64 or 128).
+cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes);
+cudaError_t launch_attn_tc(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st);
 
 }  // namespace dfl

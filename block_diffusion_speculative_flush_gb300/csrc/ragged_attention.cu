@@ -5,8 +5,6 @@
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - m_i) / l_i,  s_ij = scale q_i . k_j
 // over the keys j that row i sees, with the running maximum m and sum l of an
 // online softmax (fp32, in the exp2 domain), one pass over K and V.
-#include <cuda_bf16.h>
-
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
@@ -65,26 +63,14 @@ constexpr int BK = 64;           // keys per tile
 constexpr int kSimtSplit = 256;  // keys per split (a multiple of BK)
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-__device__ __forceinline__ float4 load4(const bf16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xffff0000u), __uint_as_float(u.y << 16),
-                     __uint_as_float(u.y & 0xffff0000u));
-}
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
-__device__ __forceinline__ void store4(bf16* p, float4 v) {
-  const __nv_bfloat162 a = __floats2bfloat162_rn(v.x, v.y), b = __floats2bfloat162_rn(v.z, v.w);
-  uint2 u;
-  u.x = *reinterpret_cast<const uint32_t*>(&a);
-  u.y = *reinterpret_cast<const uint32_t*>(&b);
-  *reinterpret_cast<uint2*>(p) = u;
-}
 
 // The CUDA-core attention works on 16 RM packed rows (token, head of the KV
 // head's group) per CTA and 64 keys per step; threads are 16 x 16, each with
 // RM rows x 4 keys of the scores and RM rows x DP / 16 columns of the output.
 // A row's arithmetic depends on its own keys only (tiles and splits start at
 // fixed positions), so a block of tokens and single tokens give the same bits.
-template <typename T, int DP, int RM>
+template <int DP, int RM>
 __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, KVView kv, int splits) {
   constexpr int BR = 16 * RM, LQ = DP + 4, LP = BK + 4;
   extern __shared__ float4 smem4[];
@@ -112,7 +98,7 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
     k_lo = max(k_lo, split * kSimtSplit);
     k_hi = min(k_hi, (split + 1) * kSimtSplit);
   }
-  const T* Q = reinterpret_cast<const T*>(a.q);
+  const float* Q = reinterpret_cast<const float*>(a.q);
   for (int e = tid; e < BR * (DP / 4); e += 256) {
     const int rr = e / (DP / 4), c = e % (DP / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -135,8 +121,8 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
     for (int c = 0; c < DP / 16; ++c) acc[i][c] = 0.f;
   }
   const float sl2 = a.scale * 1.4426950408889634f;
-  const T* Kb = reinterpret_cast<const T*>(kv.k) + kvh * kv.k_head;
-  const T* Vb = reinterpret_cast<const T*>(kv.v) + kvh * kv.v_head;
+  const float* Kb = reinterpret_cast<const float*>(kv.k) + kvh * kv.k_head;
+  const float* Vb = reinterpret_cast<const float*>(kv.v) + kvh * kv.v_head;
   for (int t0 = k_lo / BK * BK; t0 < k_hi; t0 += BK) {
     __syncthreads();
     for (int e = tid; e < BK * (DP / 4); e += 256) {
@@ -264,7 +250,7 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
       continue;
     }
     const float inv = m[i] == -INFINITY ? 0.f : 1.f / ls;
-    T* o = reinterpret_cast<T*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
+    float* o = reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
 #pragma unroll
     for (int cc = 0; cc < DP / 64; ++cc)
       if (cc * 64 + tx * 4 < a.d)
@@ -277,7 +263,6 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
 
 // Merge of the splits' partials, in split order: one warp per (token, head),
 // lanes over the columns.
-template <typename T>
 __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, int splits) {
   pdl_trigger();
   pdl_wait();
@@ -311,7 +296,7 @@ __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, i
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / L;
   if (4 * lane < a.d)
-    store4(reinterpret_cast<T*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + 4 * lane,
+    store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + 4 * lane,
            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
   if (a.lse && lane == 0) a.lse[w] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
@@ -324,7 +309,7 @@ int simt_splits(const Ragged& r, const AttnCall& a) {
   return (r.max_len + kSimtSplit - 1) / kSimtSplit;
 }
 
-template <typename T, int DP, int RM>
+template <int DP, int RM>
 cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
   constexpr int BR = 16 * RM;
   constexpr size_t smem = sizeof(float) * (BR * (DP + 4) + BK * (DP + 4) + BK * DP + BR * (BK + 4));
@@ -333,23 +318,16 @@ cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cu
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(k_attn_simt_ragged<T, DP, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    e = cudaFuncSetAttribute(k_attn_simt_ragged<DP, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
   const int splits = simt_splits(r, a);
   const int64_t tiles = ((int64_t)r.max_rows * (a.Hq / a.Hkv) + BR - 1) / BR;
-  e = launch_k(k_attn_simt_ragged<T, DP, RM>, dim3((unsigned)(tiles * splits), a.Hkv, r.batch), 256, smem, st, r, a,
+  e = launch_k(k_attn_simt_ragged<DP, RM>, dim3((unsigned)(tiles * splits), a.Hkv, r.batch), 256, smem, st, r, a,
                kv, splits);
   if (e != cudaSuccess || splits == 1) return e;
-  return launch_k(k_attn_simt_merge<T>, (unsigned)(((int64_t)r.total * a.Hq + 7) / 8), 256, 0, st, r, a, splits);
-}
-
-template <typename T>
-cudaError_t launch_simt_t(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
-  const bool few = (int64_t)r.max_rows * (a.Hq / a.Hkv) <= 16;
-  if (a.d <= 64) return few ? launch_simt<T, 64, 1>(r, a, kv, st) : launch_simt<T, 64, 4>(r, a, kv, st);
-  return few ? launch_simt<T, 128, 1>(r, a, kv, st) : launch_simt<T, 128, 4>(r, a, kv, st);
+  return launch_k(k_attn_simt_merge, (unsigned)(((int64_t)r.total * a.Hq + 7) / 8), 256, 0, st, r, a, splits);
 }
 
 }  // namespace
@@ -359,8 +337,10 @@ int64_t attn_simt_workspace(const Ragged& r, const AttnCall& a) {
   return splits == 1 ? 0 : (int64_t)r.total * a.Hq * splits * (a.d + 4) * 4;
 }
 
-cudaError_t launch_attn_simt(DT dt, const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
-  return dt == DT::F32 ? launch_simt_t<float>(r, a, kv, st) : launch_simt_t<bf16>(r, a, kv, st);
+cudaError_t launch_attn_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
+  const bool few = (int64_t)r.max_rows * (a.Hq / a.Hkv) <= 16;
+  if (a.d <= 64) return few ? launch_simt<64, 1>(r, a, kv, st) : launch_simt<64, 4>(r, a, kv, st);
+  return few ? launch_simt<128, 1>(r, a, kv, st) : launch_simt<128, 4>(r, a, kv, st);
 }
 
 namespace {
@@ -458,13 +438,20 @@ AttnCall make_call(const dflash_attention* a) {
                   a->q.head_stride, a->out.data, a->out.row_stride, a->out.head_stride, a->lse, (float*)a->workspace};
 }
 
+int64_t workspace_of(const dflash_attention* a, const Ragged& r) {
+  int64_t tc = 0;
+  if (a->dtype == DFLASH_DTYPE_F32) return attn_simt_workspace(r, make_call(a));
+  attn_tc_workspace(r, make_call(a), &tc);
+  return tc;
+}
+
 int run_attention(const char* call, const dflash_attention* a, const Ragged& r, const KVView& kv, cudaStream_t st) {
   if (r.total == 0) return DFLASH_OK;
   const AttnCall c = make_call(a);
-  const int64_t need = attn_simt_workspace(r, c);
+  const int64_t need = workspace_of(a, r);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need || (uintptr_t)a->workspace % 16))
     return rfail(DFLASH_ERR_INVALID_ARG, call, "workspace: 16-byte aligned, at least dflash_attention_workspace bytes");
-  return rcheck(launch_attn_simt(a->dtype == DFLASH_DTYPE_F32 ? DT::F32 : DT::BF16, r, c, kv, st), call);
+  return rcheck(a->dtype == DFLASH_DTYPE_F32 ? launch_attn_simt(r, c, kv, st) : launch_attn_tc(r, c, kv, st), call);
 }
 
 }  // namespace
@@ -506,7 +493,7 @@ DFLASH_API int64_t dflash_attention_workspace(const dflash_attention* a, const d
   Ragged paged = r;
   static const int32_t there = 0;
   paged.lens = pages ? &there : nullptr;  // only its presence counts here
-  return attn_simt_workspace(paged, make_call(a));
+  return workspace_of(a, paged);
 }
 
 DFLASH_API int dflash_paged_attention(const dflash_attention* a, const dflash_ragged* batch,

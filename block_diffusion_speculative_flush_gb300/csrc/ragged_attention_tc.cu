@@ -1,0 +1,1088 @@
+// Attention of ragged new rows over paged or packed K/V on the sm_103a tensor
+// cores (bf16, head_dim 64 or 128).
+//
+// Rows are (token, query head of one KV head's group) pairs: a tile of 128
+// rows holds floor(128 / G) tokens x G heads.  A CTA works on NQ tiles of one
+// sequence and KV head at a time (an item), 128 keys per step:
+//   S = Q K^T        tcgen05, K tile as it lies in shared memory
+//   P = 2^(S k - m)  one thread per row: S from TMEM, running maximum with lazy
+//                    rescaling (O and l move only when the maximum grew by more
+//                    than 2^8), P as bf16 back into S's own TMEM columns
+//   O += P V         A = P from TMEM, B = V as it lies in the cache (rows of d:
+//                    the N-contiguous operand form, no transposed copy)
+// bf16 P: each probability is rounded once (half a step, 2^-9 of itself at
+// most after normalisation of the mantissa); sums and accumulators are fp32.
+//
+// Warps: 4 NQ softmax warps (tile x: warps 4x .. 4x+3), a TMA producer, the
+// MMA issuer, a "fixer" and a scheduler.
+//   NQ = 2 (more than 128 rows): the two tiles share each K/V tile and alternate, one's
+//          softmax under the other's two products; bound by the tensor core.
+//   NQ = 1: one tile, S double-buffered; bound by the K/V stream.
+// V rows of hidden keys may hold anything, and 0 * NaN is NaN: in tiles with
+// hidden keys the fixer zeroes the rows behind the sequence and looks for
+// non-finite numbers in the others; if it finds one, the softmax warps redo
+// their rows on the CUDA cores from the definition (redo_rows).
+//
+// Work is laid out on the device from the lengths there, in one of two ways:
+//   items   whole items, longest first (by key tiles, counted by binary search,
+//           no sort), dealt to the persistent CTAs in snake order;
+//   ranges  the concatenation of all items' key tiles cut into equal ranges,
+//           one per CTA; the parts of a cut item meet in k_ragged_merge.
+// Every wait is bounded; an expired one sets DFLASH_STATUS_WAIT.
+#include <cudaTypedefs.h>
+#include <cuda_bf16.h>
+
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+#include "ragged.h"
+#include "tc_ptx.cuh"
+
+namespace dfl {
+
+namespace {
+
+using namespace tc;
+
+constexpr int KT = 128;          // keys per tile
+constexpr int NW = 4;            // work descriptors in flight
+constexpr uint32_t O_COL = 256;  // TMEM: S0 [0,128), S1 [128,256), O from 256
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+constexpr int kModeItems = 0, kModeRanges = 1;
+
+// The host's choices, the same for every CTA of a call.
+struct Plan {
+  int32_t mode;
+  int32_t tpt;          // tokens per 128-row tile
+  int32_t tok;          // tokens per item
+  int32_t hgroup;       // items: KV heads dealt out together (bounds the K/V that is live in L2)
+  int32_t min_tiles;    // ranges: key tiles a CTA gets at least
+  int32_t ws_rows;      // rows of a partial
+};
+
+// One stretch of key tiles [t0, t0 + max(nt)) of one item.
+struct Work {
+  int32_t b, start, n, len;
+  int32_t kvh, i0, t0;
+  int32_t nt[2];         // key tiles of each 128-row tile
+  int32_t part;          // partial slot, or -1: the whole item
+  int32_t clean_lo, clean_hi;  // keys that every row sees
+  int32_t bad;           // set by the fixer: a hidden key's V is not finite
+  int32_t done;
+};
+
+template <int D, int NQ>
+struct Cfg {
+  static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
+  static constexpr int RING = 7 * 32768 / SLOT - 2;       // K/V tiles in flight
+  static constexpr int DATA = (RING + 2) * SLOT;          // 224 KB
+  static constexpr int THREADS = (4 * NQ + 4) * 32;
+  static constexpr size_t SMEM = DATA + 1024 + 1024;      // + alignment, barriers and descriptors
+};
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float m;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(a), "f"(b), "f"(c));
+  return m;
+}
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint64_t f2pack(float a, float b) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+  return r;
+}
+__device__ __forceinline__ float2 f2unpack(uint64_t r) {
+  float2 v;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
+  return v;
+}
+__device__ __forceinline__ int warp_sum_i(int v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t warp_sum_l(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+// ---------------------------------------------------------------------------
+// the layout of the work
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int items_of(const Seq& s, const Plan& p) { return s.ok && s.n > 0 ? cdiv(s.n, p.tok) : 0; }
+// Items of the sequence whose keys reach into tile c (1-based) or further:
+// the last ones, as an item's keys end at its last token (or all at the length).
+__device__ __forceinline__ int items_reaching(const Seq& s, int c, const Plan& p, int causal) {
+  const int nq = items_of(s, p);
+  if (nq == 0) return 0;
+  const int y = KT * (c - 1) + 1;  // keys needed
+  if (s.len < y) return 0;
+  if (!causal) return nq;
+  const int need = y - (s.len - s.n);
+  const int first = need <= 0 ? 0 : cdiv(need, p.tok) - 1;
+  return nq - min(first, nq - 1);
+}
+// ranges: a sequence's key tiles [first, first + count), taken for each of its items
+__device__ __forceinline__ int tile_first(const Seq& s, int window) { return vis_lo(s.len - s.n, window) / KT; }
+__device__ __forceinline__ int tile_count(const Seq& s, int window) { return cdiv(s.len, KT) - tile_first(s, window); }
+__device__ __forceinline__ int64_t units_of(const Seq& s, const Plan& p, const AttnCall& a) {
+  const int nq = items_of(s, p);
+  return nq ? (int64_t)nq * a.Hkv * tile_count(s, a.window) : 0;
+}
+__device__ __forceinline__ int ranges_used(int64_t units, const Plan& p, int grid) {
+  const int64_t n = units / p.min_tiles;
+  return n < 1 ? 1 : n > grid ? grid : (int)n;
+}
+__device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
+
+// Fills in everything of w that follows from its sequence, head and tokens;
+// [t0, t0 + take) are the key tiles asked for.
+__device__ __forceinline__ void make_work(Work& w, const Seq& s, int b, int kvh, int qi, int t0, int take, int part,
+                                          const Plan& p, const AttnCall& a) {
+  w.b = b;
+  w.start = s.start;
+  w.n = s.n;
+  w.len = s.len;
+  w.kvh = kvh;
+  w.i0 = qi * p.tok;
+  w.part = part;
+  w.bad = 0;
+  w.done = 0;
+  const int ctx = s.len - s.n, i1 = min(w.i0 + p.tok, s.n);
+  const int lo = vis_lo(ctx + w.i0, a.window) / KT;
+  w.t0 = max(t0, lo);
+  w.clean_lo = vis_lo(ctx + i1 - 1, a.window);
+  w.clean_hi = vis_hi(ctx + w.i0, s.len, a.causal);
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int first = w.i0 + x * p.tpt, last = min(first + p.tpt, i1) - 1;
+    int t = 0;
+    if (last >= first) t = max(0, min(t0 + take, cdiv(vis_hi(ctx + last, s.len, a.causal), KT)) - w.t0);
+    w.nt[x] = t;
+  }
+}
+
+// The output or the partial of one row: O is scaled by 1 / l for an output.
+struct RowOut {
+  bf16* out;     // NULL: a partial
+  float* part;   // m, l, -, -, O
+  float* lse;
+};
+template <int D>
+__device__ __forceinline__ RowOut row_out(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G) {
+  const int tok = w.start + w.i0 + x * p.tpt + r / G, h = w.kvh * G + r % G;
+  RowOut o{nullptr, nullptr, nullptr};
+  if (w.part >= 0) {
+    o.part = a.ws + ((int64_t)w.part * p.ws_rows + x * 128 + r) * (D + 4);
+  } else {
+    o.out = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
+    if (a.lse) o.lse = a.lse + (int64_t)tok * a.Hq + h;
+  }
+  return o;
+}
+
+// The rows of tile x of a work stretch, from the definition, on the CUDA
+// cores: lanes over the keys for the scores, over the columns for the sums.
+// Only for stretches with a non-finite V among their hidden keys.
+template <int D>
+__device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, const Work& w, int x, int warp4) {
+  constexpr int C = D / 32;
+  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv, ctx = w.len - w.n;
+  const int rows = min(p.tpt, min(p.tok, w.n - w.i0) - x * p.tpt) * G;
+  const float sl2 = a.scale * kLog2e;
+  const int k0 = w.t0 * KT, k1 = min((w.t0 + max(w.nt[0], w.nt[1])) * KT, w.len);
+  for (int rr = warp4; rr < rows; rr += 4) {
+    const int i = w.i0 + x * p.tpt + rr / G, h = w.kvh * G + rr % G, pos = ctx + i;
+    const int lo = max(vis_lo(pos, a.window), k0), hi = min(vis_hi(pos, w.len, a.causal), k1);
+    const bf16* q = reinterpret_cast<const bf16*>(a.q) + (int64_t)(w.start + i) * a.q_row + (int64_t)h * a.q_head;
+    float m = -INFINITY, l = 0.f, acc[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) acc[c] = 0.f;
+    for (int base = lo; base < hi; base += 32) {
+      const int j = base + lane;
+      float s = -INFINITY;
+      int64_t vo = -1;
+      if (j < hi) {
+        int64_t ko;
+        bool ok = true;
+        if (kv.paged) {
+          const int pg = r.table[(int64_t)w.b * r.table_stride + (j >> kv.page_shift)];
+          const int sl = j & ((1 << kv.page_shift) - 1);
+          ok = pg >= 0 && pg < kv.n_pages;
+          ko = pg * kv.page + sl * kv.k_slot;
+          vo = pg * kv.page + sl * kv.v_slot;
+        } else {
+          ko = (int64_t)(w.start + j) * kv.k_slot;
+          vo = (int64_t)(w.start + j) * kv.v_slot;
+        }
+        s = 0.f;
+        if (ok) {
+          const bf16* k = reinterpret_cast<const bf16*>(kv.k) + ko + w.kvh * kv.k_head;
+          for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
+          s *= sl2;
+        } else {
+          vo = -1;
+        }
+      }
+      const float mn = fmaxf(m, warp_max(s)), mref = mn == -INFINITY ? 0.f : mn;
+      const float f = m == -INFINITY ? 0.f : exp2f(m - mref);
+      const float pv = j < hi ? exp2f(s - mref) : 0.f;
+      l = l * f + warp_sum(pv);
+      m = mn;
+#pragma unroll
+      for (int c = 0; c < C; ++c) acc[c] *= f;
+      const int cnt = min(32, hi - base);
+      for (int u = 0; u < cnt; ++u) {
+        const float pu = __shfl_sync(0xffffffffu, pv, u);
+        const int64_t o = __shfl_sync(0xffffffffu, vo, u);
+        if (o < 0) continue;
+        const bf16* v = reinterpret_cast<const bf16*>(kv.v) + o + w.kvh * kv.v_head;
+#pragma unroll
+        for (int c = 0; c < C; ++c) acc[c] = fmaf(pu, __bfloat162float(v[lane * C + c]), acc[c]);
+      }
+    }
+    const RowOut o = row_out<D>(a, p, w, x, rr, G);
+    if (o.part) {
+      if (lane == 0) *reinterpret_cast<float4*>(o.part) = make_float4(m, l, 0.f, 0.f);
+#pragma unroll
+      for (int c = 0; c < C; ++c) o.part[4 + lane * C + c] = acc[c];
+    } else {
+      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+#pragma unroll
+      for (int c = 0; c < C; ++c) o.out[lane * C + c] = __float2bfloat16_rn(acc[c] * inv);
+      if (o.lse && lane == 0) *o.lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+  }
+}
+
+template <int D, int NQ>
+__global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
+    k_ragged_tc(Ragged r, AttnCall a, KVView kv, Plan p, const __grid_constant__ CUtensorMap mq,
+                const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using C = Cfg<D, NQ>;
+  constexpr int SLOT = C::SLOT, RING = C::RING, NB = D / 64, SW = 4 * NQ;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  uint8_t* sQ = smem;
+  uint8_t* sR = sQ + 2 * SLOT;
+  uint64_t* full = (uint64_t*)(sR + RING * SLOT);
+  uint64_t* empty = full + RING;
+  uint64_t* v_fix = empty + RING;
+  uint64_t* q_full = v_fix + RING;
+  uint64_t* q_empty = q_full + 2;
+  uint64_t* s_full = q_empty + 2;
+  uint64_t* p_full = s_full + 2;
+  uint64_t* pv_done = p_full + 2;
+  uint64_t* w_full = pv_done + 2;
+  uint64_t* w_empty = w_full + NW;
+  uint64_t* all_done = w_empty + NW;
+  uint32_t* tmem_slot = (uint32_t*)(all_done + 1);
+  volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
+  Work* works = (Work*)(tmem_slot + 2);
+  static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 1024, "barriers and descriptors");
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int G = a.Hq / a.Hkv;
+
+  if (tid == 0) {
+    for (int s = 0; s < RING; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 2);  // the MMA's commit and the fixer
+      mbar_init(&v_fix[s], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(&q_full[s], 1);
+      mbar_init(&q_empty[s], 1);
+      mbar_init(&s_full[s], 1);
+      mbar_init(&p_full[s], 4);
+      mbar_init(&pv_done[s], 1);
+    }
+    for (int s = 0; s < NW; ++s) {
+      mbar_init(&w_full[s], 1);
+      mbar_init(&w_empty[s], SW + 3);
+    }
+    mbar_init(all_done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == SW + 1) {
+    tmem_alloc(tmem_slot, 512);
+    fence_before();
+  }
+  if (warp == SW && lane < 3) {
+    const CUtensorMap* m = lane == 0 ? &mq : lane == 1 ? &mk : &mv;
+    asm volatile("prefetch.tensormap [%0];" ::"l"((uint64_t)m) : "memory");
+  }
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *tmem_slot;
+  pdl_trigger();
+  pdl_wait();
+
+  auto give_up = [&]() {
+    if (lane == 0) flag_status(r.status, DFLASH_STATUS_WAIT);
+    *abort_flag = 1;
+  };
+
+  if (warp == SW + 3) {
+    // ---- scheduler
+    r.starts = after_wait(r.starts);
+    if (r.lens) r.lens = after_wait(r.lens);
+    int k = 0;
+    bool ok = true;
+    auto emit = [&](const Work& w) {
+      const int s = k % NW;
+      if (k >= NW && !__all_sync(0xffffffffu, mbar_wait(&w_empty[s], (uint32_t)(k / NW - 1) & 1u, abort_flag))) {
+        ok = false;
+        return;
+      }
+      if (lane == 0) {
+        works[s] = w;
+        mbar_arrive(&w_full[s]);
+      }
+      __syncwarp();
+      ++k;
+    };
+    const int cta = blockIdx.x, grid = gridDim.x;
+    const bool one = r.batch <= 32;  // then each lane keeps its sequence
+    Seq mine{0, 0, 0, false};
+    if (one && lane < r.batch) mine = load_seq(r, lane);
+    auto seq_at = [&](int b) { return one ? mine : load_seq(r, b); };  // b = base + lane
+    auto bcast = [&](const Seq& s, int src) {
+      Seq o;
+      o.start = __shfl_sync(0xffffffffu, s.start, src);
+      o.n = __shfl_sync(0xffffffffu, s.n, src);
+      o.len = __shfl_sync(0xffffffffu, s.len, src);
+      o.ok = __shfl_sync(0xffffffffu, (int)s.ok, src) != 0;
+      return o;
+    };
+    Work w;
+    if (p.mode == kModeItems) {
+      // items whose keys reach tile c: counted over the batch
+      auto count = [&](int c) {
+        int64_t s = 0;
+        for (int b = lane; b < r.batch; b += 32) s += items_reaching(seq_at(b), c, p, a.causal);
+        return warp_sum_l(s);
+      };
+      int max_t = 0;
+      for (int b = lane; b < r.batch; b += 32) {
+        const Seq s = seq_at(b);
+        if (!s.ok && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+        if (s.ok && s.n > 0) max_t = max(max_t, cdiv(s.len, KT));
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) max_t = max(max_t, __shfl_xor_sync(0xffffffffu, max_t, o));
+      const int64_t pairs = count(1), total = pairs * a.Hkv, per_group = pairs * p.hgroup;
+      for (int j = 0; ok; ++j) {
+        const int64_t idx = (int64_t)j * grid + ((j & 1) ? grid - 1 - cta : cta);
+        if ((int64_t)j * grid >= total) break;
+        if (idx >= total) continue;
+        const int g = (int)(idx / per_group), heads = min(p.hgroup, a.Hkv - g * p.hgroup);
+        const int64_t rest = idx - g * per_group, pair = rest / heads;
+        const int kvh = g * p.hgroup + (int)(rest - pair * heads);
+        int c = 1, hi = max_t + 1;
+        while (hi - c > 1) {
+          const int mid = (c + hi) >> 1;
+          if (count(mid) > pair) c = mid;
+          else hi = mid;
+        }
+        int64_t rank = pair - count(c + 1);
+        for (int base = 0; base < r.batch; base += 32) {
+          const int b = base + lane;
+          int here = 0, first = 0;
+          Seq s{0, 0, 0, false};
+          if (b < r.batch) {
+            s = seq_at(b);
+            const int ge = items_reaching(s, c, p, a.causal);
+            here = ge - items_reaching(s, c + 1, p, a.causal);
+            first = items_of(s, p) - ge;
+          }
+          int incl = here;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int u = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += u;
+          }
+          const int sum = __shfl_sync(0xffffffffu, incl, 31);
+          if (rank < sum) {
+            const int src = __ffs(__ballot_sync(0xffffffffu, incl > rank)) - 1;
+            const int qi = __shfl_sync(0xffffffffu, first - (incl - here), src) + (int)rank;
+            make_work(w, bcast(s, src), base + src, kvh, qi, 0, INT32_MAX / 2, -1, p, a);
+            emit(w);
+            break;
+          }
+          rank -= sum;
+        }
+      }
+    } else {
+      int64_t units = 0;
+      for (int b = lane; b < r.batch; b += 32) {
+        const Seq s = seq_at(b);
+        if (!s.ok && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+        units += units_of(s, p, a);
+      }
+      units = warp_sum_l(units);
+      const int n = ranges_used(units, p, grid);
+      int64_t u = cta < n ? range_start(units, cta, n) : units;
+      const int64_t u1 = cta < n ? range_start(units, cta + 1, n) : units;
+      int64_t before = 0;  // units in front of chunk `base`
+      int seg = 0;
+      for (int base = 0; base < r.batch && u < u1 && ok; base += 32) {
+        const int b = base + lane;
+        Seq s{0, 0, 0, false};
+        if (b < r.batch) s = seq_at(b);
+        const int64_t mine_u = units_of(s, p, a);
+        int64_t incl = mine_u;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+          if (lane >= o) incl += v;
+        }
+        const int64_t chunk_end = before + __shfl_sync(0xffffffffu, incl, 31);
+        while (u < u1 && u < chunk_end && ok) {
+          const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
+          const Seq q = bcast(s, src);
+          const int64_t off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
+          const int T = tile_count(q, a.window);
+          const int64_t item = off / T;
+          const int t = (int)(off - item * T), take = (int)min((int64_t)(T - t), u1 - u);
+          const int part = t == 0 && take == T ? -1 : 2 * cta + (seg > 0);
+          make_work(w, q, base + src, (int)(item % a.Hkv), (int)(item / a.Hkv), tile_first(q, a.window) + t, take, part,
+                    p, a);
+          emit(w);
+          u += take;
+          ++seg;
+        }
+        before = chunk_end;
+      }
+    }
+    w.done = 1;
+    if (ok) emit(w);
+    if (!ok) give_up();
+  } else if (warp == SW) {
+    // ---- TMA producer: Q tiles, then K and V tiles in turn through one ring
+    if (r.table) r.table = after_wait(r.table);
+    uint32_t it = 0, q_use[2] = {0, 0};
+    bool ok = true;
+    const int page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
+    const int boxes = KT / page_rows;
+    auto ring_wait = [&](uint32_t i) {
+      return i < (uint32_t)RING ||
+             __all_sync(0xffffffffu, mbar_wait(&empty[i % RING], (i / RING - 1) & 1u, abort_flag));
+    };
+    for (int k = 0; ok; ++k) {
+      const int ws = k % NW;
+      if (!__all_sync(0xffffffffu, mbar_wait(&w_full[ws], (uint32_t)(k / NW) & 1u, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const Work w = works[ws];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[ws]);
+      if (w.done) break;
+      const int T = max(w.nt[0], w.nt[1]);
+      auto load_q = [&](int x, int buf) {
+        if (q_use[buf] > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[buf], (q_use[buf] - 1) & 1u, abort_flag))) {
+          ok = false;
+          return;
+        }
+        if (lane == 0) {
+          mbar_expect_tx(&q_full[buf], (uint32_t)(G * p.tpt * 128 * NB));
+          for (int c = 0; c < NB; ++c)
+            tma_load_3d(sQ + buf * SLOT + c * (SLOT / NB), &mq, &q_full[buf], 64 * c, w.kvh * G,
+                        w.start + w.i0 + x * p.tpt);
+        }
+        ++q_use[buf];
+      };
+      if (NQ == 1) {
+        // double-buffered: the buffers alternate over the stretches that have tiles
+        if (w.nt[0] > 0) load_q(0, (int)((q_use[0] + q_use[1]) & 1u));
+      } else {
+        for (int x = 0; x < NQ && ok; ++x)
+          if (w.nt[x] > 0) load_q(x, x);
+      }
+      const int32_t* tab = kv.paged ? r.table + (int64_t)w.b * r.table_stride : nullptr;
+      // page of this lane's box of a tile; lanes past the sequence load nothing
+      auto page_of = [&](int t) {
+        const int pos = (w.t0 + t) * KT + lane * page_rows;
+        return kv.paged && t < T && lane < boxes && pos < w.len ? tab[pos >> kv.page_shift] : -1;
+      };
+      int pg = page_of(0);
+      for (int t = 0; t < T && ok; ++t) {
+        const int kt = (w.t0 + t) * KT;
+        const int next = page_of(t + 1);
+        const bool mine = kv.paged ? lane < boxes && kt + lane * page_rows < w.len : lane == 0;
+        if (kv.paged && mine && (pg < 0 || pg >= kv.n_pages)) {
+          flag_status(r.status, DFLASH_STATUS_PAGE);
+          pg = kv.n_pages;  // just outside the map: zeros arrive
+        }
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * 128 * NB;
+        for (int half = 0; half < 2 && ok; ++half, ++it) {
+          const int st = it % RING;
+          if (!ring_wait(it)) {
+            ok = false;
+            break;
+          }
+          if (lane == 0) mbar_expect_tx(&full[st], bytes);
+          __syncwarp();
+          if (mine) {
+            const CUtensorMap* m = half ? &mv : &mk;
+            uint8_t* dst = sR + st * SLOT + lane * page_rows * 128;
+            for (int c = 0; c < NB; ++c) {
+              if (kv.paged)
+                tma_load_4d(dst + c * (SLOT / NB), m, &full[st], 64 * c, kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
+              else
+                tma_load_4d(dst + c * (SLOT / NB), m, &full[st], 64 * c, w.start + kt, w.kvh, 0);
+            }
+          }
+        }
+        pg = next;
+      }
+    }
+    if (!ok || *abort_flag) {
+      // let this CTA's own copies land before leaving
+      give_up();
+      const uint64_t t0 = globaltimer_ns();
+      for (uint32_t i = it > (uint32_t)RING ? it - RING : 0; i < it; ++i)
+        while (!mbar_try_wait(&full[i % RING], (i / RING) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      for (int x = 0; x < 2; ++x)
+        while (q_use[x] > 0 && !mbar_try_wait(&q_full[x], (q_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+    }
+  } else if (warp == SW + 1) {
+    // ---- MMA issuer: the whole warp decides, one elected lane issues
+    constexpr uint32_t idS = idesc_bf16(128, KT), idPV = idesc_bf16(128, D) | kIdescBMnMajor;
+    uint32_t it = 0, q_use[2] = {0, 0}, s_cnt[2] = {0, 0}, fixpar = 0;
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+      if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag))) ok = false;
+      return ok;
+    };
+    auto issue_s = [&](int qbuf, uint32_t st, int sbuf) {
+      const uint32_t q0 = smem_u32(sQ + qbuf * SLOT), k0 = smem_u32(sR + st * SLOT), tS = tmem + sbuf * 128;
+#pragma unroll
+      for (int ks = 0; ks < D / 16; ++ks)
+        umma_bf16_warp(tS, sdesc_sw128(q0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32),
+                       sdesc_sw128(k0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
+      umma_commit_warp(&s_full[sbuf]);
+    };
+    auto issue_pv = [&](int x, uint32_t st, int sbuf, bool first) {
+      const uint32_t v0 = smem_u32(sR + st * SLOT), tP = tmem + sbuf * 128, tO = tmem + O_COL + x * D;
+#pragma unroll
+      for (int ks = 0; ks < KT / 16; ++ks)
+        umma_bf16_ts_warp(tO, tP + ks * 8, sdesc_sw128_mn(v0 + ks * 2048, SLOT / NB), idPV, first && ks == 0 ? 0u : 1u);
+      umma_commit_warp(&pv_done[x]);
+    };
+    for (int k = 0; ok; ++k) {
+      const int ws = k % NW;
+      if (!wait(&w_full[ws], (uint32_t)(k / NW))) break;
+      const Work w = works[ws];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[ws]);
+      if (w.done) break;
+      const int T = max(w.nt[0], w.nt[1]);
+      if (T == 0) continue;
+      auto dirty = [&](int t) {
+        const int kt = (w.t0 + t) * KT;
+        return kt < w.clean_lo || kt + KT > w.clean_hi;
+      };
+      auto wait_v = [&](int t) {
+        const uint32_t iv = it + 2 * t + 1, st = iv % RING;
+        if (!wait(&full[st], iv / RING)) return false;
+        if (dirty(t)) {
+          if (!wait(&v_fix[st], (fixpar >> st) & 1u)) return false;
+          fixpar ^= 1u << st;
+        }
+        return true;
+      };
+      if (NQ == 1) {
+        const int qb = (int)((q_use[0] + q_use[1]) & 1u);
+        if (!wait(&q_full[qb], q_use[qb])) break;
+        ++q_use[qb];
+        for (int t = -1; t < T && ok; ++t) {
+          if (t + 1 < T) {
+            const uint32_t ik = it + 2 * (t + 1), st = ik % RING;
+            if (!wait(&full[st], ik / RING)) break;
+            fence_after();
+            issue_s(qb, st, (int)(s_cnt[0] & 1u));
+            ++s_cnt[0];
+            umma_commit_warp(&empty[st]);
+            if (t + 2 == T) umma_commit_warp(&q_empty[qb]);
+          }
+          if (t >= 0) {
+            // tile t is the (s_cnt - 1)th S issued, or the one before when S(t + 1) went ahead
+            const uint32_t sc = s_cnt[0] - 1 - (t + 1 < T ? 1 : 0);
+            if (!wait_v(t) || !wait(&p_full[sc & 1u], sc >> 1)) break;
+            fence_after();
+            const uint32_t st = (it + 2 * t + 1) % RING;
+            issue_pv(0, st, (int)(sc & 1u), t == 0);
+            umma_commit_warp(&empty[st]);
+          }
+        }
+      } else {
+        for (int x = 0; x < 2 && ok; ++x)
+          if (w.nt[x] > 0) {
+            wait(&q_full[x], q_use[x]);
+            ++q_use[x];
+          }
+        if (!wait(&full[it % RING], it / RING)) break;
+        fence_after();
+        for (int x = 0; x < 2; ++x)
+          if (w.nt[x] > 0) {
+            issue_s(x, it % RING, x);
+            if (w.nt[x] == 1) umma_commit_warp(&q_empty[x]);
+          }
+        umma_commit_warp(&empty[it % RING]);
+        for (int t = 0; t < T && ok; ++t) {
+          if (!wait_v(t)) break;
+          const uint32_t sv = (it + 2 * t + 1) % RING, ik = it + 2 * (t + 1), sk = ik % RING;
+          for (int x = 0; x < 2 && ok; ++x) {
+            if (t >= w.nt[x]) continue;
+            if (!wait(&p_full[x], s_cnt[x])) break;
+            ++s_cnt[x];
+            fence_after();
+            issue_pv(x, sv, x, t == 0);
+            if (t + 1 < w.nt[x]) {
+              if (!wait(&full[sk], ik / RING)) break;
+              fence_after();
+              issue_s(x, sk, x);
+              if (t + 2 == w.nt[x]) umma_commit_warp(&q_empty[x]);
+            }
+          }
+          umma_commit_warp(&empty[sv]);
+          if (t + 1 < T) umma_commit_warp(&empty[sk]);
+        }
+      }
+      it += 2 * T;
+    }
+    if (!ok) give_up();
+    umma_commit_warp(all_done);  // every product issued above has ended before TMEM is given back
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(all_done, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
+    }
+  } else if (warp == SW + 2) {
+    // ---- fixer: V tiles with hidden keys
+    uint32_t it = 0;
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int ws = k % NW;
+      if (!__all_sync(0xffffffffu, mbar_wait(&w_full[ws], (uint32_t)(k / NW) & 1u, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const Work w = works[ws];
+      if (!w.done) {
+        const int T = max(w.nt[0], w.nt[1]);
+        // It follows the ring slot by slot, as one of the two readers a slot
+        // waits for: a barrier it only looked at now and then could be more
+        // than one phase away, which a parity cannot tell.
+        for (uint32_t i = it; i < it + 2 * T; ++i) {
+          const uint32_t st = i % RING;
+          if (!__all_sync(0xffffffffu, mbar_wait(&full[st], (i / RING) & 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          const int t = (int)(i - it) >> 1, kt = (w.t0 + t) * KT;
+          if (((i - it) & 1u) == 0 || (kt >= w.clean_lo && kt + KT <= w.clean_hi)) {  // K, or nothing hidden
+            if (lane == 0) mbar_arrive(&empty[st]);
+            continue;
+          }
+          uint8_t* v = sR + st * SLOT;
+          const int in = min(KT, w.len - kt);  // rows of the sequence
+          // rows behind the sequence: zeros (8 lanes a row of 128 bytes)
+          for (int e = in * 8 + lane; e < KT * 8; e += 32)
+            for (int c = 0; c < NB; ++c)
+              *reinterpret_cast<uint4*>(v + c * (SLOT / NB) + e * 16) = make_uint4(0, 0, 0, 0);
+          if (kt < w.clean_lo || kt + in > w.clean_hi) {
+            uint32_t found = 0;
+            for (int e = lane; e < in * 8; e += 32)
+              for (int c = 0; c < NB; ++c) {
+                const uint4 q = *reinterpret_cast<const uint4*>(v + c * (SLOT / NB) + e * 16);
+                // an exponent of ones carries into bit 15 (or 31)
+                found |= (q.x & 0x7f807f80u) + 0x00800080u;
+                found |= (q.y & 0x7f807f80u) + 0x00800080u;
+                found |= (q.z & 0x7f807f80u) + 0x00800080u;
+                found |= (q.w & 0x7f807f80u) + 0x00800080u;
+              }
+            if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0) && lane == 0) works[ws].bad = 1;
+          }
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&v_fix[st]);
+            mbar_arrive(&empty[st]);
+          }
+        }
+        it += 2 * T;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[ws]);
+      if (w.done) break;
+    }
+    if (!ok) give_up();
+  } else {
+    // ---- softmax: one thread per row
+    const int x = warp >> 2, row = tid & 127;
+    const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16, tO = tmem + lrow + O_COL + x * D;
+    const float sl2 = a.scale * kLog2e;
+    uint32_t cnt = 0;  // tiles of this warp's stream so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      const int ws = k % NW;
+      if (!__all_sync(0xffffffffu, mbar_wait(&w_full[ws], (uint32_t)(k / NW) & 1u, abort_flag))) {
+        ok = false;
+        break;
+      }
+      const Work& w = works[ws];
+      if (w.done) break;
+      const int i = w.i0 + x * p.tpt + row / G;
+      const bool valid = row < p.tpt * G && i < min(w.i0 + p.tok, w.n);
+      const bool live = __any_sync(0xffffffffu, valid);
+      int lo = 0, hi = INT32_MAX;  // padding rows ask for no mask
+      if (valid) {
+        const int pos = w.len - w.n + i;
+        lo = vis_lo(pos, a.window);
+        hi = vis_hi(pos, w.len, a.causal);
+      }
+      const int T = w.nt[x];
+      float m = -INFINITY, l = 0.f;
+      for (int t = 0; t < T; ++t, ++cnt) {
+        const int sb = NQ == 2 ? x : (int)(cnt & 1u);
+        const uint32_t par = NQ == 2 ? cnt & 1u : (cnt >> 1) & 1u;
+        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[sb], par, abort_flag))) {
+          ok = false;
+          break;
+        }
+        // The product before S is through too (NQ = 2: tile t - 1's, issued in
+        // front of S; NQ = 1: tile t - 2's).  Waiting here at every tile keeps
+        // each later wait on pv_done within one phase.
+        if (t >= 3 - NQ &&
+            !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - (3 - NQ)) & 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        if (live) {
+          const int kt = (w.t0 + t) * KT;
+          float s[128];
+          fence_after();
+          tmem_ld128(tmem + lrow + sb * 128, s);
+          if (!__all_sync(0xffffffffu, lo <= kt && hi >= kt + KT)) {
+            const int l0 = lo - kt, h0 = hi - kt;
+#pragma unroll
+            for (int j = 0; j < 128; ++j) s[j] = (j >= l0 && j < h0) ? s[j] : -INFINITY;
+          }
+          float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+          for (int j = 4; j < 124; j += 8) {
+            m0 = max3(m0, s[j], s[j + 1]);
+            m1 = max3(m1, s[j + 2], s[j + 3]);
+            m2 = max3(m2, s[j + 4], s[j + 5]);
+            m3 = max3(m3, s[j + 6], s[j + 7]);
+          }
+          m0 = max3(m0, s[124], s[125]);
+          m1 = max3(m1, s[126], s[127]);
+          const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
+          const bool grow = valid && mt > m + 8.f;
+          const float mn = grow ? mt : m;
+          const float f = grow && m != -INFINITY ? ex2(m - mn) : 1.f;
+          if (__any_sync(0xffffffffu, f != 1.f)) {
+            // O holds the previous tile's product before it is scaled
+            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
+              ok = false;
+              break;
+            }
+            fence_after();
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float o[32];
+              tmem_ld32(tO + c, o);
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] *= f;
+              tmem_st32(tO + c, o);
+            }
+            l *= f;
+          }
+          m = mn;
+          const float mref = m == -INFINITY ? 0.f : m;
+          const uint64_t k2 = f2pack(sl2, sl2), c2 = f2pack(-mref, -mref);
+          uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            uint32_t pk[32];
+#pragma unroll
+            for (int j = 0; j < 32; ++j) {
+              uint64_t e2;
+              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[64 * h + 2 * j], s[64 * h + 2 * j + 1])), "l"(k2), "l"(c2));
+              const float2 e = f2unpack(e2);
+              const float p0 = ex2(e.x), p1 = ex2(e.y);
+              if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(f2pack(p0, p1)));
+              else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(f2pack(p0, p1)));
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+              pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            tmem_st32u(tmem + lrow + sb * 128 + 32 * h, pk);
+          }
+          const float2 sa = f2unpack(sum0), sc = f2unpack(sum1);
+          l += (sa.x + sa.y) + (sc.x + sc.y);
+          tmem_wait_st();
+          fence_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&p_full[sb]);
+      }
+      if (!ok) break;
+      if (T > 0) {
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        fence_after();
+      }
+      if (T > 0 && *(volatile int32_t*)&w.bad) {
+        redo_rows<D>(r, a, kv, p, w, x, warp & 3);  // rows in turn over all four warps
+      } else if (live) {
+        const RowOut o = row_out<D>(a, p, w, x, valid ? row : 0, G);
+        const float inv = o.part ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
+        if (valid && o.part) *reinterpret_cast<float4*>(o.part) = make_float4(m, l, 0.f, 0.f);
+        if (valid && o.lse) *o.lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+#pragma unroll 1
+        for (int c = 0; c < D && T > 0; c += 32) {
+          float v[32];
+          tmem_ld32(tO + c, v);
+          if (valid && o.part) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 4)
+              *reinterpret_cast<float4*>(o.part + 4 + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+          } else if (valid) {
+#pragma unroll
+            for (int j = 0; j < 32; j += 8) {
+              uint32_t u[4];
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[j + 2 * q] * inv, v[j + 2 * q + 1] * inv);
+                u[q] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              *reinterpret_cast<uint4*>(o.out + c + j) = make_uint4(u[0], u[1], u[2], u[3]);
+            }
+          }
+        }
+      }
+      fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[ws]);
+    }
+    if (!ok) give_up();
+  }
+  fence_before();
+  __syncthreads();
+  if (warp == SW + 1) {
+    fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// Merge of the parts of each item that a range boundary cut.  CTA (c - 1, y):
+// boundary c, if it is the first inside its item; 8 rows per CTA, a warp per
+// row, parts in key order.
+template <int D>
+__global__ void __launch_bounds__(256) k_ragged_merge(Ragged r, AttnCall a, Plan p, int grid) {
+  constexpr int C = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  r.starts = after_wait(r.starts);
+  if (r.lens) r.lens = after_wait(r.lens);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int G = a.Hq / a.Hkv, row = blockIdx.y * 8 + warp, c = blockIdx.x + 1;
+  int64_t units = 0;
+  for (int b = lane; b < r.batch; b += 32) units += units_of(load_seq(r, b), p, a);
+  units = warp_sum_l(units);
+  const int n = ranges_used(units, p, grid);
+  if (c >= n) return;
+  const int64_t u = range_start(units, c, n);
+  int64_t before = 0;
+  for (int base = 0; base < r.batch; base += 32) {
+    const int b = base + lane;
+    Seq s{0, 0, 0, false};
+    if (b < r.batch) s = load_seq(r, b);
+    const int64_t mine = units_of(s, p, a);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += v;
+    }
+    const int64_t end = before + __shfl_sync(0xffffffffu, incl, 31);
+    if (u >= end) {
+      before = end;
+      continue;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
+    const int64_t seq_u = before + __shfl_sync(0xffffffffu, incl - mine, src);
+    const int start = __shfl_sync(0xffffffffu, s.start, src), sn = __shfl_sync(0xffffffffu, s.n, src);
+    const int T = __shfl_sync(0xffffffffu, s.ok && s.n > 0 ? tile_count(s, a.window) : 1, src);
+    const int64_t item = (u - seq_u) / T, i_begin = seq_u + item * T, i_end = i_begin + T;
+    if (u == i_begin || range_start(units, c - 1, n) > i_begin) return;  // no cut here, or not the item's first
+    const int kvh = (int)(item % a.Hkv), i0 = (int)(item / a.Hkv) * p.tok;
+    const int x = row / 128, rr = row % 128, i = i0 + x * p.tpt + rr / G;
+    if (rr >= p.tpt * G || i >= min(i0 + p.tok, sn)) return;
+    float M = -INFINITY, L = 0.f, acc[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[j] = 0.f;
+    for (int q = c - 1; q < n; ++q) {
+      const int64_t qs = range_start(units, q, n);
+      if (qs >= i_end) break;
+      const int slot = 2 * q + (qs < i_begin);  // a range's first stretch, or the one that it ends with
+      const float* pp = a.ws + ((int64_t)slot * p.ws_rows + row) * (D + 4);
+      const float m = pp[0], l = pp[1];
+      float v[C];
+#pragma unroll
+      for (int j = 0; j < C; ++j) v[j] = pp[4 + lane * C + j];
+      if (m == -INFINITY) continue;  // saw no key of this stretch; its sums are not written
+      const float Mn = fmaxf(M, m), f = M == -INFINITY ? 0.f : exp2f(M - Mn), g = exp2f(m - Mn);
+      M = Mn;
+      L = L * f + l * g;
+#pragma unroll
+      for (int j = 0; j < C; ++j) acc[j] = acc[j] * f + v[j] * g;
+    }
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const int tok = start + i, h = kvh * G + rr % G;
+    bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + lane * C;
+#pragma unroll
+    for (int j = 0; j < C; j += 2)
+      *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
+    if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+    return;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host
+// ---------------------------------------------------------------------------
+cudaError_t current_sms(int* sms) {
+  static int cached[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 64 && cached[dev]) {
+    *sms = cached[dev];
+    return cudaSuccess;
+  }
+  e = cudaDeviceGetAttribute(sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e == cudaSuccess && dev < 64) cached[dev] = *sms;
+  return e;
+}
+
+struct HostPlan {
+  Plan p;
+  int nq;       // 128-row tiles per item
+  int merge;    // parts may have to meet
+};
+
+HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
+  const int G = a.Hq / a.Hkv;
+  HostPlan h{};
+  Plan& p = h.p;
+  p.tpt = std::min(128 / G, std::max(r.max_rows, 1));
+  h.nq = (int64_t)r.max_rows * G <= (int64_t)p.tpt * G ? 1 : 2;
+  p.tok = p.tpt * h.nq;
+  p.ws_rows = h.nq == 1 ? p.tpt * G : 256;
+  const int64_t items = ((int64_t)r.total / p.tok + std::min(r.batch, r.total)) * a.Hkv;
+  const int tiles = (r.max_len + KT - 1) / KT;
+  p.mode = h.nq == 2 && (items >= 3 * sms / 2 || tiles <= 4) ? kModeItems : kModeRanges;
+  // items: heads dealt out together while their K/V (both, bf16) stay within 48 MB of L2
+  const int64_t per_head = std::max<int64_t>(1, (int64_t)(r.lens ? (int64_t)r.max_len * std::min(r.batch, r.total) : r.total) * a.d * 4);
+  p.hgroup = (int)std::max<int64_t>(1, std::min<int64_t>(a.Hkv, (48ll << 20) / per_head));
+  p.min_tiles = h.nq == 2 ? 4 : 1;
+  h.merge = p.mode == kModeRanges && tiles > 1;
+  return h;
+}
+
+cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+                   const cuuint32_t* box) {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return (PFN_cuTensorMapEncodeTiled_v12000)f;
+  }();
+  if (!fn) return cudaErrorNotSupported;
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
+
+template <int D, int NQ>
+cudaError_t launch_tc(const Ragged& r, const AttnCall& a, const KVView& kv, const Plan& p, int grid,
+                      const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
+  static bool attr[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !attr[dev]) {
+    e = cudaFuncSetAttribute(k_ragged_tc<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, NQ>::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) attr[dev] = true;
+  }
+  return launch_k(k_ragged_tc<D, NQ>, grid, Cfg<D, NQ>::THREADS, Cfg<D, NQ>::SMEM, st, r, a, kv, p, mq, mk, mv);
+}
+
+template <int D>
+cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const HostPlan& h, int sms, cudaStream_t st) {
+  const int G = a.Hq / a.Hkv;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)r.total};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.q_head * 2, (cuuint64_t)a.q_row * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)h.p.tpt};
+    if (cudaError_t e = encode(&mq, a.q, 3, dims, strides, box)) return e;
+  }
+  for (int i = 0; i < 2; ++i) {
+    const cuuint64_t slot = (cuuint64_t)(i ? kv.v_slot : kv.k_slot) * 2, head = (cuuint64_t)(i ? kv.v_head : kv.k_head) * 2;
+    const cuuint64_t dims[4] = {(cuuint64_t)D, kv.paged ? (cuuint64_t)1 << kv.page_shift : (cuuint64_t)kv.packed_rows,
+                                (cuuint64_t)a.Hkv, kv.paged ? (cuuint64_t)kv.n_pages : 1};
+    const cuuint64_t strides[3] = {slot, head, kv.paged ? (cuuint64_t)kv.page * 2 : slot};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(kv.paged ? std::min(1 << kv.page_shift, KT) : KT), 1, 1};
+    if (cudaError_t e = encode(i ? &mv : &mk, i ? kv.v : kv.k, 4, dims, strides, box)) return e;
+  }
+  cudaError_t e = h.nq == 1 ? launch_tc<D, 1>(r, a, kv, h.p, sms, mq, mk, mv, st)
+                            : launch_tc<D, 2>(r, a, kv, h.p, sms, mq, mk, mv, st);
+  if (e != cudaSuccess || !h.merge) return e;
+  const int rows = std::min<int64_t>(h.nq * 128, (int64_t)r.max_rows * G);
+  return launch_k(k_ragged_merge<D>, dim3(sms - 1, h.nq == 1 ? (rows + 7) / 8 : 32), 256, 0, st, r, a, h.p, sms);
+}
+
+}  // namespace
+
+cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes) {
+  int sms = 0;
+  // without a device (argument checks on a host) the largest part's count of SMs stands in
+  if (current_sms(&sms) != cudaSuccess) {
+    cudaGetLastError();
+    sms = 152;
+  }
+  const HostPlan h = make_plan(r, a, sms);
+  *bytes = h.merge ? (int64_t)2 * sms * h.p.ws_rows * (a.d + 4) * 4 : 0;
+  return cudaSuccess;
+}
+
+cudaError_t launch_attn_tc(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
+  int sms = 0;
+  if (cudaError_t e = current_sms(&sms)) return e;
+  const HostPlan h = make_plan(r, a, sms);
+  return a.d == 64 ? launch_d<64>(r, a, kv, h, sms, st) : launch_d<128>(r, a, kv, h, sms, st);
+}
+
+}  // namespace dfl
