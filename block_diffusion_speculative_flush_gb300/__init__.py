@@ -496,36 +496,53 @@ def dflash_target_exactness_probe(target: Target, tokens: torch.Tensor, start: i
 _DTYPES = {torch.float32: DFLASH_DTYPE_F32, torch.bfloat16: DFLASH_DTYPE_BF16}
 
 
-def _stream_of(stream, device) -> C.c_void_p:
-    return C.c_void_p((stream if stream is not None else torch.cuda.current_stream(device)).cuda_stream)
+def _stream_of(stream, t: torch.Tensor) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+
+
+class _on_device:
+    """torch.cuda.device(t.device) for the call, free when that device is current already."""
+
+    def __init__(self, t: torch.Tensor):
+        self.ctx = None if torch._C._cuda_getDevice() == t.get_device() else torch.cuda.device(t.device)
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
 
 
 def _same_device(first: torch.Tensor, *others) -> None:
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise ValueError("all tensors of a call live on one device")
 
 
 def _heads(t: torch.Tensor, dtype: torch.dtype, what: str) -> _abi.dflash_heads:
     """[rows, heads, head_dim] with a dense last dimension."""
-    if not t.is_cuda or t.dtype != dtype or t.dim() != 3 or (t.stride(2) != 1 and t.shape[2] > 1):
+    shape, st = t.shape, t.stride()
+    if not t.is_cuda or t.dtype != dtype or len(shape) != 3 or (st[2] != 1 and shape[2] > 1):
         raise ValueError(f"{what}: a CUDA {dtype} tensor [rows, heads, head_dim] with a dense last dimension")
     # torch may report any stride for a dimension of one entry; the library asks for one a head fits in
-    row = t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1] * t.shape[2])
-    head = t.stride(1) if t.shape[1] > 1 else t.shape[2]
-    return _abi.dflash_heads(t.data_ptr() if t.numel() else None, row, head)
+    rows, heads, d = shape
+    row = st[0] if rows > 1 else max(st[0], heads * d)
+    return _abi.dflash_heads(t.data_ptr() if rows else None, row, st[1] if heads > 1 else d)
 
 
 def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> _abi.dflash_kv_pages:
     """[n_pages, page_size, n_kv_heads, head_dim] views of one shape and stride (a permuted
     [n_pages, n_kv_heads, page_size, head_dim] cache too)."""
-    if not k_pages.is_cuda or k_pages.dtype not in _DTYPES or k_pages.dim() != 4 or k_pages.stride(3) != 1 or \
-            v_pages.dtype != k_pages.dtype or v_pages.shape != k_pages.shape or v_pages.stride() != k_pages.stride():
+    shape, st, dtype = k_pages.shape, k_pages.stride(), _DTYPES.get(k_pages.dtype)
+    if not k_pages.is_cuda or dtype is None or len(shape) != 4 or st[3] != 1 or \
+            v_pages.dtype != k_pages.dtype or v_pages.shape != shape or v_pages.stride() != st:
         raise ValueError("k_pages, v_pages: CUDA fp32 or bf16 [n_pages, page_size, n_kv_heads, head_dim] of one shape "
                          "and stride, with a dense last dimension")
-    n, page, heads, d = k_pages.shape
-    st = k_pages.stride()
-    return _abi.dflash_kv_pages(_DTYPES[k_pages.dtype], heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(),
+    n, page, heads, d = shape
+    return _abi.dflash_kv_pages(dtype, heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(),
                                 st[0] if n > 1 else max(st[0], d), st[1], st[2] if heads > 1 else d)
 
 
@@ -573,8 +590,11 @@ def _with_workspace(a, r, pages, workspace, stream, device):
     need = lib.dflash_attention_workspace(C.byref(a), C.byref(r), pages)
     _check(min(need, 0))
     if workspace is None and need:
-        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream(device)):
+        if stream is None:
             workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(stream):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
     if workspace is not None:
         if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA uint8 tensor")
@@ -593,9 +613,9 @@ def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     kh, vh = _heads(k, k_pages.dtype, "k"), _heads(v, k_pages.dtype, "v")
     _same_device(k_pages, k, v, v_pages, starts, lens, table, status)
     r = _ragged(starts, lens, table, k.shape[0], max(1, k.shape[0]), 1 << 30, status)
-    with torch.cuda.device(k_pages.device):
+    with _on_device(k_pages):
         _check(lib.dflash_kv_append(C.byref(p), C.byref(r), C.byref(kh), C.byref(vh),
-                                    _stream_of(stream, k_pages.device)))
+                                    _stream_of(stream, k_pages)))
 
 
 def dflash_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages) -> int:
@@ -622,9 +642,9 @@ def dflash_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     if max_len is None:
         max_len = min(1 << 30, table.shape[-1] * k_pages.shape[1])
     r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, status)
-    with torch.cuda.device(q.device):
+    with _on_device(q):
         _with_workspace(a, r, C.byref(p), workspace, stream, q.device)
-        _check(lib.dflash_paged_attention(C.byref(a), C.byref(r), C.byref(p), _stream_of(stream, q.device)))
+        _check(lib.dflash_paged_attention(C.byref(a), C.byref(r), C.byref(p), _stream_of(stream, q)))
 
 
 def dflash_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, out: torch.Tensor,
@@ -638,10 +658,10 @@ def dflash_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s
     kh, vh = _heads(k, q.dtype, "k"), _heads(v, q.dtype, "v")
     _same_device(q, k, v, starts, out, lse, workspace, status)
     r = _ragged(starts, None, None, q.shape[0], max_rows, 0, status)
-    with torch.cuda.device(q.device):
+    with _on_device(q):
         _with_workspace(a, r, None, workspace, stream, q.device)
         _check(lib.dflash_prompt_attention(C.byref(a), C.byref(r), C.byref(kh), C.byref(vh),
-                                           _stream_of(stream, q.device)))
+                                           _stream_of(stream, q)))
 
 
 def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor,
@@ -676,12 +696,12 @@ def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: 
     a = _abi.dflash_logprobs(logits.data_ptr(), max(logits.stride(0), V) if R <= 1 else logits.stride(0),
                              _DTYPES[logits.dtype], R, V, top, float(temperature), ptr(tokens), ptr(logprobs),
                              ptr(entropy), ptr(top_ids), ptr(top_logprobs), ptr(status))
-    with torch.cuda.device(logits.device):
-        _check(lib.dflash_token_logprobs(C.byref(a), _stream_of(stream, logits.device)))
+    with _on_device(logits):
+        _check(lib.dflash_token_logprobs(C.byref(a), _stream_of(stream, logits)))
 
 
 def dflash_status_check(status: torch.Tensor, stream=None) -> None:
     """Waits for the stream, clears the operators' status word and raises DFlashError if a bit was set."""
     _int_vector(status, 1, "status")
-    with torch.cuda.device(status.device):
-        _check(lib.dflash_status_check(status.data_ptr(), _stream_of(stream, status.device)))
+    with _on_device(status):
+        _check(lib.dflash_status_check(status.data_ptr(), _stream_of(stream, status)))

@@ -933,24 +933,58 @@ __global__ void __launch_bounds__(256) k_ragged_merge(Ragged r, AttnCall a, Plan
     const int kvh = (int)(item % a.Hkv), i0 = (int)(item / a.Hkv) * p.tok;
     const int x = row / 128, rr = row % 128, i = i0 + x * p.tpt + rr / G;
     if (rr >= p.tpt * G || i >= min(i0 + p.tok, sn)) return;
+    // parts: ranges c - 1 .. last; a range's first stretch is its slot 0, the
+    // one that it ends with its slot 1.  The parts' (max, sum) arrive a lane
+    // each, then O eight parts at a time: three trips to memory for 32 parts.
+    int parts = 1;
+    while (c - 1 + parts < n && range_start(units, c - 1 + parts, n) < i_end) ++parts;
+    const float* p0 = a.ws + (int64_t)row * (D + 4);
+    const int64_t slot_st = (int64_t)p.ws_rows * (D + 4);
+    const int slot0 = 2 * (c - 1) + (range_start(units, c - 1, n) < i_begin);
+    auto part_at = [&](int q) { return p0 + (q == 0 ? slot0 : 2 * (c - 1 + q)) * slot_st; };
     float M = -INFINITY, L = 0.f, acc[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[j] = 0.f;
-    for (int q = c - 1; q < n; ++q) {
-      const int64_t qs = range_start(units, q, n);
-      if (qs >= i_end) break;
-      const int slot = 2 * q + (qs < i_begin);  // a range's first stretch, or the one that it ends with
-      const float* pp = a.ws + ((int64_t)slot * p.ws_rows + row) * (D + 4);
-      const float m = pp[0], l = pp[1];
-      float v[C];
-#pragma unroll
-      for (int j = 0; j < C; ++j) v[j] = pp[4 + lane * C + j];
-      if (m == -INFINITY) continue;  // saw no key of this stretch; its sums are not written
-      const float Mn = fmaxf(M, m), f = M == -INFINITY ? 0.f : exp2f(M - Mn), g = exp2f(m - Mn);
+    for (int base = 0; base < parts; base += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (base + lane < parts) ml = *reinterpret_cast<const float2*>(part_at(base + lane));
+      const float Mn = fmaxf(M, warp_max(ml.x)), mref = Mn == -INFINITY ? 0.f : Mn;
+      const float f = M == -INFINITY ? 0.f : exp2f(M - mref);
+      // a part that saw no key has weight 0 and its sums were not written; a NaN maximum stays one
+      const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
       M = Mn;
-      L = L * f + l * g;
+      L = L * f + warp_sum(wt == 0.f ? 0.f : ml.y * wt);
 #pragma unroll
-      for (int j = 0; j < C; ++j) acc[j] = acc[j] * f + v[j] * g;
+      for (int j = 0; j < C; ++j) acc[j] *= f;
+      const int cnt = min(32, parts - base);
+      for (int q0 = 0; q0 < cnt; q0 += 8) {
+        float v[8][C], wq[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          wq[q] = __shfl_sync(0xffffffffu, wt, (q0 + q) & 31);
+          if (q0 + q >= cnt) wq[q] = 0.f;
+#pragma unroll
+          for (int j = 0; j < C; ++j) v[q][j] = 0.f;
+          if (wq[q] != 0.f) {
+            const float* pp = part_at(base + q0 + q) + 4 + lane * C;
+            if (C == 4) {
+              const float4 t = *reinterpret_cast<const float4*>(pp);
+              v[q][0] = t.x;
+              v[q][1] = t.y;
+              v[q][C - 2] = t.z;
+              v[q][C - 1] = t.w;
+            } else {
+              const float2 t = *reinterpret_cast<const float2*>(pp);
+              v[q][0] = t.x;
+              v[q][1] = t.y;
+            }
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+#pragma unroll
+          for (int j = 0; j < C; ++j) acc[j] = fmaf(wq[q], v[q][j], acc[j]);
+      }
     }
     const float inv = M == -INFINITY ? 0.f : 1.f / L;
     const int tok = start + i, h = kvh * G + rr % G;

@@ -626,9 +626,9 @@ typedef struct dflash_logprobs {
   const void* logits;
   int64_t row_stride;   /* elements, >= vocab */
   int32_t dtype;        /* DFLASH_DTYPE_F32 or DFLASH_DTYPE_BF16 */
-  int32_t rows, vocab;  /* rows >= 0, vocab 1..2^24 */
+  int32_t rows, vocab;  /* rows 0..2^26, vocab 1..2^24 */
   int32_t top;
-  float temperature;    /* finite, > 0 */
+  float temperature;    /* finite, > 0, 1.5 / temperature finite */
   const int32_t* tokens;
   float* logprobs;      /* [rows] */
   float* entropy;
