@@ -17,11 +17,13 @@
 // Top entries: an element counts only if it reaches the CTA's threshold, a
 // value that at least K of the CTA's entries reach; one compare per thread and
 // 16 or 32 elements decides that none does, the common case.  The first
-// threshold comes from the threads' maxima of the first batch: of each warp the
-// r-th largest, r = ceil(K / warps), of these the smallest.  Each warp keeps
-// its best 32 keys (value's order above, ~id below) sorted over its lanes and
-// raises the threshold with its K-th.  In the end the keys that reach the
-// threshold, little more than K, are ranked by counting the larger ones.
+// threshold is the K-th largest of the threads' maxima of the first batch (found
+// among those that reach the smallest, over the warps, of each warp's r-th,
+// r = ceil(K / warps)).  What reaches it goes into a shared buffer as a key
+// (value's order above, ~id below); after 2, 4, 8, ... batches and in the end
+// the keys are ranked by counting the larger ones, the best K stay and the K-th
+// becomes the threshold.  (A row in ascending order fills the buffer between
+// two rankings: what does not fit goes into sorted lists of 32, one per warp.)
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
@@ -41,6 +43,8 @@ namespace cg = cooperative_groups;
 
 constexpr int TH = 256, WARPS = TH / 32;
 constexpr int U = 4;  // 16-byte loads of a batch
+constexpr int H = 4;       // batches looked at together
+constexpr int CAP = TH;    // keys between two rankings (half of a buffer)
 constexpr int kMaxCluster = 16;
 
 __device__ __forceinline__ float lp_ex2(float x) {
@@ -139,31 +143,30 @@ __device__ __forceinline__ void list_insert(uint64_t& mine, uint64_t key, int la
   if (lane == pos) mine = key;
   else if (lane > pos) mine = up;
 }
-// The k-th largest (0-based) of the lanes' values.
-__device__ __forceinline__ float kth_of_lanes(float v, int k, int lane) {
-#pragma unroll
-  for (int size = 2; size <= 32; size <<= 1)
-#pragma unroll
-    for (int o = size >> 1; o > 0; o >>= 1) {
-      const float w = __shfl_xor_sync(0xffffffffu, v, o);
-      const bool desc = (lane & size) == 0, low = (lane & o) == 0;
-      v = desc == low ? fmaxf(v, w) : fminf(v, w);
-    }
-  return __shfl_sync(0xffffffffu, v, k);
+// The r-th largest (1-based) of the lanes' words.
+__device__ __forceinline__ uint32_t rth_of_lanes(uint32_t v, int r, int lane) {
+  uint32_t m = __reduce_max_sync(0xffffffffu, v);
+  for (; r > 1; --r) {
+    if (lane == __ffs(__ballot_sync(0xffffffffu, v == m)) - 1) v = 0;
+    m = __reduce_max_sync(0xffffffffu, v);
+  }
+  return m;
 }
 
 template <typename T>
 __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int cluster, float c) {
   constexpr int E = Elems<T>::E, N = U * E;
-  __shared__ uint64_t s_key[kMaxCluster * 32], s_out[32];
+  // keys of the running round: [0, CAP) in turn, [CAP, 2 CAP) the warps' lists
+  __shared__ uint64_t s_key[2][2 * CAP], s_all[kMaxCluster * 32], s_out[32];
   __shared__ Stat s_stat[WARPS], s_cta, s_row;
-  __shared__ float s_first[WARPS];
-  __shared__ uint32_t s_tau, s_n;  // float_order of the threshold; keys gathered
+  __shared__ uint32_t s_first[WARPS], s_max[TH];
+  __shared__ uint4 s_stage[WARPS][H][U];
+  __shared__ uint32_t s_tau, s_n[2], s_nlist[2], s_nall, s_nmax;  // float_order of the threshold; counts
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.x / cluster, rank = blockIdx.x % cluster, K = a.top;
   if (tid == 0) {
     s_tau = float_order(-INFINITY);
-    s_n = 0;
+    s_n[0] = s_n[1] = s_nlist[0] = s_nlist[1] = s_nall = s_nmax = 0;
   }
   if (tid < 32) s_out[tid] = 0;
   __syncthreads();
@@ -213,28 +216,82 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     st.s += sf.x + sf.y;
     st.t += tf.x + tf.y;
   };
-  // keys of the lanes' candidates (bit i: element i), re-read by id
-  auto select = [&](uint32_t bits, auto id_of) {
-    while (__any_sync(0xffffffffu, bits != 0)) {
-      uint64_t key = 0;
-      if (bits) {
-        const int id = id_of(__ffs(bits) - 1);
-        bits &= bits - 1;
-        key = order_key(to_f<T>(x[id]), id);
-      }
-      uint32_t todo = __ballot_sync(0xffffffffu, key > kth);
-      while (todo) {
-        const uint64_t k2 = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
-        todo &= todo - 1;
-        if (k2 > kth) {
-          list_insert(list, k2, lane);
-          kth = __shfl_sync(0xffffffffu, list, K - 1);
-        }
+  int side = 0;
+  // the lanes' keys (0: none) into the buffer, past its end into the warp's list
+  auto append = [&](uint64_t key) {
+    const uint32_t m = __ballot_sync(0xffffffffu, key != 0);
+    if (!m) return;
+    const int cnt = __popc(m);
+    int pos = 0;
+    if (lane == 0) pos = (int)atomicAdd(&s_n[side], (uint32_t)cnt);
+    const int base = __shfl_sync(0xffffffffu, pos, 0);
+    pos = base + __popc(m & ((1u << lane) - 1u));
+    if (key && pos < CAP) s_key[side][pos] = key;
+    if (base + cnt <= CAP) return;
+    uint32_t todo = __ballot_sync(0xffffffffu, pos >= CAP && key > kth);
+    while (todo) {
+      const uint64_t k2 = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
+      todo &= todo - 1;
+      if (k2 > kth) {
+        list_insert(list, k2, lane);
+        kth = __shfl_sync(0xffffffffu, list, K - 1);
       }
     }
     if (kth && lane == 0) atomicMax(&s_tau, (uint32_t)(kth >> 32));
   };
-
+  // The batches of the lanes in `hits`, four at a time through shared memory:
+  // the whole warp looks at one, an element a lane.
+  auto scan = [&](uint32_t hits, int base, float tau, const uint4* cur) {
+    while (hits) {
+      const int q = __popc(hits & ((1u << lane) - 1u));
+      if (((hits >> lane) & 1u) && q < H) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) s_stage[warp][q][u] = cur[u];
+      }
+      __syncwarp();
+#pragma unroll 1
+      for (int h = 0; h < H && hits; ++h) {
+        const int src = __ffs(hits) - 1;
+        hits &= hits - 1;
+        const int v = base + (lane / E) * TH + warp * 32 + src;
+        const float e = lane < N ? to_f<T>(reinterpret_cast<const T*>(s_stage[warp][h])[lane]) : 0.f;
+        append(lane < N && v < v1 && e >= tau ? order_key(e, head + v * E + lane % E) : 0ull);
+      }
+      __syncwarp();
+    }
+  };
+  // Ranks the round's keys; the best K go to dst in order (their count is the
+  // result), and the K-th becomes the threshold.  The next round is the other side.
+  auto rank_round = [&](uint64_t* dst) {
+    if (__any_sync(0xffffffffu, list != 0)) {  // rare: the buffer overflowed
+      uint32_t at = 0;
+      const uint32_t m = __ballot_sync(0xffffffffu, list != 0);
+      if (lane == 0) at = atomicAdd(&s_nlist[side], (uint32_t)__popc(m));
+      at = __shfl_sync(0xffffffffu, at, 0);
+      if (list) s_key[side][CAP + at + lane] = list;  // sorted: the first popc(m) lanes
+      list = kth = 0;
+    }
+    __syncthreads();
+    const int n = min((int)s_n[side], CAP), nl = (int)s_nlist[side], have = min(n + nl, K);
+    const uint64_t* buf = s_key[side];
+    for (int i = tid; i < n + nl; i += TH) {
+      const uint64_t key = buf[i < n ? i : CAP + i - n];
+      int r = 0;
+#pragma unroll 8
+      for (int j = 0; j < n; ++j) r += buf[j] > key;
+      for (int j = 0; j < nl; ++j) r += buf[CAP + j] > key;
+      if (r < K) dst[r] = key;
+      if (r == K - 1) atomicMax(&s_tau, (uint32_t)(key >> 32));
+    }
+    side ^= 1;
+    if (tid == 0) {
+      s_n[side] = have;
+      s_nlist[side] = 0;
+    }
+    __syncthreads();
+    return have;
+  };
+  int batch = 0, refresh = 2;
   if (v0 < v1) {
     uint4 cur[U], nxt[U];
     const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
@@ -252,13 +309,22 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       Elems<T>::template range<U>(cur, hi, lo);
       if (!(hi >= -INFINITY)) hi = -INFINITY;  // nothing but NaN
       if (K > 0 && base == v0) {
-        const float r = kth_of_lanes(hi, (K + WARPS - 1) / WARPS - 1, lane);
+        const uint32_t mine = float_order(hi), r = rth_of_lanes(mine, (K + WARPS - 1) / WARPS, lane);
         if (lane == 0) s_first[warp] = r;
         __syncthreads();
-        if (tid == 0) {
-          float m = s_first[0];
-          for (int w = 1; w < WARPS; ++w) m = fminf(m, s_first[w]);
-          atomicMax(&s_tau, float_order(m));
+        uint32_t t = s_first[0];
+#pragma unroll
+        for (int w = 1; w < WARPS; ++w) t = min(t, s_first[w]);
+        // of the maxima that reach it (K at least), the K-th is the threshold
+        if (mine >= t) s_max[atomicAdd(&s_nmax, 1u)] = mine;
+        __syncthreads();
+        const int n = (int)s_nmax;
+        if (tid < n) {
+          const uint32_t v = s_max[tid];
+          int r = 0;
+#pragma unroll 8
+          for (int j = 0; j < n; ++j) r += s_max[j] > v || (s_max[j] == v && j < tid);
+          if (r == K - 1) atomicMax(&s_tau, v);
         }
         __syncthreads();
       }
@@ -271,17 +337,11 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       }
       if (K > 0) {
         const float tau = float_of_order(*(volatile uint32_t*)&s_tau);
-        if (__any_sync(0xffffffffu, hi >= tau)) {
-          uint32_t bits = 0;
-#pragma unroll
-          for (int u = 0; u < U; ++u) {
-            float e[E];
-            Elems<T>::get(cur[u], e);
-#pragma unroll
-            for (int i = 0; i < E; ++i) bits |= (e[i] >= tau ? 1u : 0u) << (u * E + i);
-            if (base + u * TH + tid >= v1) bits &= ~(((1u << E) - 1u) << (u * E));
-          }
-          select(bits, [&](int i) { return head + (base + (i / E) * TH + tid) * E + i % E; });
+        const uint32_t hits = __ballot_sync(0xffffffffu, hi >= tau);
+        if (hits) scan(hits, base, tau, cur);
+        if (++batch == refresh) {
+          refresh *= 2;
+          rank_round(s_key[side ^ 1]);
         }
       }
 #pragma unroll
@@ -296,7 +356,7 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       const bool in = lane < cnt;
       const float e[2] = {in ? to_f<T>(x[id]) : -INFINITY, -INFINITY};
       add(std::integral_constant<int, 2>(), e, e[0] >= -INFINITY ? e[0] : -INFINITY, true);
-      if (K > 0) select(in ? 1u : 0u, [&](int) { return id; });
+      if (K > 0) append(in ? order_key(e[0], id) : 0ull);
     }
   }
 
@@ -304,48 +364,38 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
   st = warp_merge(st, c);
   if (lane == 0) s_stat[warp] = st;
   __syncthreads();
-  // ---- top entries: the warps' keys that reach the threshold, ranked
-  auto gather = [&](uint64_t key, uint32_t tau) {
-    if (key && (uint32_t)(key >> 32) >= tau) s_key[atomicAdd(&s_n, 1u)] = key;
-  };
-  auto rank_of = [&](uint64_t key, int n) {
-    int r = 0;
-    for (int j = 0; j < n; ++j) r += s_key[j] > key;
-    return r;
-  };
-  if (K > 0 && lane < K) gather(list, s_tau);
   if (warp == 0) {
     st = warp_merge(lane < WARPS ? s_stat[lane] : Stat{-INFINITY, 0.f, 0.f}, c);
-    if (lane == 0) s_cta = st;
+    if (lane == 0) s_cta = s_row = st;
   }
+  // ---- top entries: of the CTA, then of the cluster
+  int n = K > 0 ? rank_round(s_out) : 0;
   if (cluster > 1) {
     cg::cluster_group cl = cg::this_cluster();
-    __syncthreads();
-    if (tid < (int)s_n) {  // at most WARPS * 32 = TH
-      const uint64_t key = s_key[tid];
-      const int r = rank_of(key, (int)s_n);
-      if (r < K) s_out[r] = key;
-    }
     cl.sync();
     if (rank == 0) {
-      uint32_t tau = lane < cluster ? *cl.map_shared_rank(&s_tau, lane) : 0u;
-      tau = __reduce_max_sync(0xffffffffu, tau);
-      uint64_t k0 = 0, k1 = 0;
-      if (tid < cluster * K) k0 = *cl.map_shared_rank(&s_out[tid % K], tid / K);
-      if (tid + TH < cluster * K) k1 = *cl.map_shared_rank(&s_out[(tid + TH) % K], (tid + TH) / K);
+      // every CTA has ceil(K / cluster) entries that reach the smallest of these
+      // CTAs' entries of that place: K at least do
+      uint32_t t = 0xffffffffu;
+      if (lane < cluster) t = (uint32_t)(*cl.map_shared_rank(&s_out[(K + cluster - 1) / cluster - (K > 0)], lane) >> 32);
+      t = __reduce_min_sync(0xffffffffu, t);
+      uint64_t kk[2] = {0, 0};
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int j = tid + i * TH;
+        if (j < cluster * K) kk[i] = *cl.map_shared_rank(&s_out[j % K], j / K);
+      }
       if (warp == 0) {
         st = warp_merge(lane < cluster ? *cl.map_shared_rank(&s_cta, lane) : Stat{-INFINITY, 0.f, 0.f}, c);
         if (lane == 0) s_row = st;
       }
-      if (tid == 0) s_n = 0;
-      __syncthreads();
-      gather(k0, tau);
-      gather(k1, tau);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        if (kk[i] && (uint32_t)(kk[i] >> 32) >= t) s_all[atomicAdd(&s_nall, 1u)] = kk[i];
     }
     cl.sync();  // no CTA leaves while its shared memory is read
     if (rank != 0) return;
   } else {
-    if (tid == 0) s_row = st;
     __syncthreads();
   }
   st = s_row;
@@ -365,14 +415,22 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     if (a.entropy) a.entropy[row] = (ls - st.t / st.s) * ln2;
   }
   if (K > 0) {
-    const int n = (int)s_n;
     const int64_t o = (int64_t)row * K;
-    for (int i = tid; i < n; i += TH) {
-      const uint64_t key = s_key[i];
-      const int r = rank_of(key, n);
-      if (r >= K) continue;
-      a.top_ids[o + r] = (int32_t)(0xffffffffu - (uint32_t)key);
-      a.top_logprobs[o + r] = ((float_of_order((uint32_t)(key >> 32)) - st.m) * c - ls) * ln2;
+    auto put = [&](uint64_t k, int r) {
+      a.top_ids[o + r] = (int32_t)(0xffffffffu - (uint32_t)k);
+      a.top_logprobs[o + r] = ((float_of_order((uint32_t)(k >> 32)) - st.m) * c - ls) * ln2;
+    };
+    if (cluster > 1) {
+      n = (int)s_nall;
+      for (int i = tid; i < n; i += TH) {
+        const uint64_t k = s_all[i];
+        int r = 0;
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) r += s_all[j] > k;
+        if (r < K) put(k, r);
+      }
+    } else if (tid < n) {
+      put(s_out[tid], tid);
     }
     if (tid >= n && tid < K) {  // fewer than K entries are not NaN
       a.top_ids[o + tid] = -1;
