@@ -447,10 +447,11 @@ int64_t workspace_of(const dflash_attention* a, const Ragged& r) {
 
 int run_attention(const char* call, const dflash_attention* a, const Ragged& r, const KVView& kv, cudaStream_t st) {
   if (r.total == 0) return DFLASH_OK;
+  if ((int64_t)r.total * a->n_q_heads > INT32_MAX) return rfail(DFLASH_ERR_SHAPE, call, "total_rows x n_q_heads above 2^31 - 1");
   const AttnCall c = make_call(a);
   const int64_t need = workspace_of(a, r);
-  if (need > 0 && (!a->workspace || a->workspace_bytes < need || (uintptr_t)a->workspace % 16))
-    return rfail(DFLASH_ERR_INVALID_ARG, call, "workspace: 16-byte aligned, at least dflash_attention_workspace bytes");
+  if (need > 0 && (!a->workspace || a->workspace_bytes < need || (uintptr_t)a->workspace % 32))
+    return rfail(DFLASH_ERR_INVALID_ARG, call, "workspace: 32-byte aligned, at least dflash_attention_workspace bytes");
   return rcheck(a->dtype == DFLASH_DTYPE_F32 ? launch_attn_simt(r, c, kv, st) : launch_attn_tc(r, c, kv, st), call);
 }
 

@@ -14,7 +14,8 @@
 // most after normalisation of the mantissa); sums and accumulators are fp32.
 //
 // Warps: 4 NQ softmax warps (tile x: warps 4x .. 4x+3), a TMA producer, the
-// MMA issuer, a "fixer" and a scheduler.
+// MMA issuer, a "fixer" and a scheduler.  Stretches of work overlap: the first S
+// of the next one is issued behind the last product of its stream.
 //   NQ = 2 (more than 128 rows): the two tiles share each K/V tile and alternate, one's
 //          softmax under the other's two products; bound by the tensor core.
 //   NQ = 1: one tile, S double-buffered; bound by the K/V stream.
@@ -58,8 +59,9 @@ struct Plan {
   int32_t tpt;          // tokens per 128-row tile
   int32_t tok;          // tokens per item
   int32_t hgroup;       // items: KV heads dealt out together (bounds the K/V that is live in L2)
-  int32_t min_tiles;    // ranges: key tiles a CTA gets at least
+  int32_t min_tiles_log2;  // ranges: log2 of the key tiles a CTA gets at least
   int32_t ws_rows;      // rows of a partial
+  int32_t slots;        // partials there is room for
 };
 
 // One stretch of key tiles [t0, t0 + max(nt)) of one item.
@@ -79,7 +81,7 @@ struct Cfg {
   static constexpr int RING = 7 * 32768 / SLOT - 2;       // K/V tiles in flight
   static constexpr int DATA = (RING + 2) * SLOT;          // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
-  static constexpr size_t SMEM = DATA + 1024 + 1024;      // + alignment, barriers and descriptors
+  static constexpr size_t SMEM = DATA + 768;  // + barriers and descriptors
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -102,15 +104,30 @@ __device__ __forceinline__ float2 f2unpack(uint64_t r) {
   asm("mov.b64 {%0, %1}, %2;" : "=f"(v.x), "=f"(v.y) : "l"(r));
   return v;
 }
-__device__ __forceinline__ int warp_sum_i(int v) {
+__device__ __forceinline__ int warp_scan_i(int v, int lane) {  // inclusive
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
   return v;
 }
-__device__ __forceinline__ int64_t warp_sum_l(int64_t v) {
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  return v;
+// 32 bytes of a row, in one store where the row allows it
+__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool whole) {
+  if (whole) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+  } else {
+    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+}
+// Arrival that publishes no memory (the tensor-memory fence in front of it
+// orders what it hands over): unlike the default it does not wait for this
+// thread's earlier stores, 300 cycles a key tile where P is handed over.
+__device__ __forceinline__ void mbar_arrive_relaxed(uint64_t* bar) {
+  asm volatile("mbarrier.arrive.relaxed.cta.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ int cdiv(int a, int b) { return (a + b - 1) / b; }
 
@@ -133,15 +150,20 @@ __device__ __forceinline__ int items_reaching(const Seq& s, int c, const Plan& p
 // ranges: a sequence's key tiles [first, first + count), taken for each of its items
 __device__ __forceinline__ int tile_first(const Seq& s, int window) { return vis_lo(s.len - s.n, window) / KT; }
 __device__ __forceinline__ int tile_count(const Seq& s, int window) { return cdiv(s.len, KT) - tile_first(s, window); }
-__device__ __forceinline__ int64_t units_of(const Seq& s, const Plan& p, const AttnCall& a) {
-  const int nq = items_of(s, p);
-  return nq ? (int64_t)nq * a.Hkv * tile_count(s, a.window) : 0;
+// (the host takes ranges only where the sum of these fits 31 bits)
+__device__ __forceinline__ int units_of(const Seq& s, const Plan& p, const AttnCall& a) {
+  return items_of(s, p) * a.Hkv * (s.ok && s.n > 0 ? tile_count(s, a.window) : 0);
 }
-__device__ __forceinline__ int ranges_used(int64_t units, const Plan& p, int grid) {
-  const int64_t n = units / p.min_tiles;
-  return n < 1 ? 1 : n > grid ? grid : (int)n;
-}
-__device__ __forceinline__ int64_t range_start(int64_t units, int c, int n) { return units * c / n; }
+// The units' even split over the CTAs that take part: range c starts at start(c).
+struct Ranges {
+  int n, each, rest;
+  __device__ __forceinline__ Ranges(int units, const Plan& p, int grid) {
+    n = max(1, min(grid, units >> p.min_tiles_log2));
+    each = units / n;
+    rest = units - each * n;
+  }
+  __device__ __forceinline__ int start(int c) const { return c * each + min(c, rest); }
+};
 
 // Fills in everything of w that follows from its sequence, head and tokens;
 // [t0, t0 + take) are the key tiles asked for.
@@ -170,23 +192,34 @@ __device__ __forceinline__ void make_work(Work& w, const Seq& s, int b, int kvh,
   }
 }
 
-// The output or the partial of one row: O is scaled by 1 / l for an output.
-struct RowOut {
-  bf16* out;     // NULL: a partial
-  float* part;   // m, l, -, -, O
-  float* lse;
-};
+// Where a row's results go.  A partial is O (unscaled) in ws [2 grid][ws_rows][D]
+// and (m, l) behind it, [2 grid][ws_rows].
 template <int D>
-__device__ __forceinline__ RowOut row_out(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G) {
-  const int tok = w.start + w.i0 + x * p.tpt + r / G, h = w.kvh * G + r % G;
-  RowOut o{nullptr, nullptr, nullptr};
+__device__ __forceinline__ float* part_o(const AttnCall& a, const Plan& p, int slot, int row) {
+  return a.ws + ((int64_t)slot * p.ws_rows + row) * D;
+}
+template <int D>
+__device__ __forceinline__ float2* part_ml(const AttnCall& a, const Plan& p, int slot, int row) {
+  return reinterpret_cast<float2*>(a.ws + (int64_t)p.slots * p.ws_rows * D) + (int64_t)slot * p.ws_rows + row;
+}
+__device__ __forceinline__ int row_token(const Plan& p, const Work& w, int x, int r, int G) {
+  return w.start + w.i0 + x * p.tpt + r / G;
+}
+// (m, l) of a partial, or the row's log-sum-exp
+template <int D>
+__device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G,
+                                            float m, float l) {
   if (w.part >= 0) {
-    o.part = a.ws + ((int64_t)w.part * p.ws_rows + x * 128 + r) * (D + 4);
-  } else {
-    o.out = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
-    if (a.lse) o.lse = a.lse + (int64_t)tok * a.Hq + h;
+    *part_ml<D>(a, p, w.part, x * 128 + r) = make_float2(m, l);
+  } else if (a.lse) {
+    a.lse[(int64_t)row_token(p, w, x, r, G) * a.Hq + w.kvh * G + r % G] =
+        m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
   }
-  return o;
+}
+template <int D>
+__device__ __forceinline__ bf16* row_out(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G) {
+  return reinterpret_cast<bf16*>(a.out) + (int64_t)row_token(p, w, x, r, G) * a.o_row +
+         (int64_t)(w.kvh * G + r % G) * a.o_head;
 }
 
 // The rows of tile x of a work stretch, from the definition, on the CUDA
@@ -249,16 +282,16 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
         for (int c = 0; c < C; ++c) acc[c] = fmaf(pu, __bfloat162float(v[lane * C + c]), acc[c]);
       }
     }
-    const RowOut o = row_out<D>(a, p, w, x, rr, G);
-    if (o.part) {
-      if (lane == 0) *reinterpret_cast<float4*>(o.part) = make_float4(m, l, 0.f, 0.f);
+    if (lane == 0) store_stats<D>(a, p, w, x, rr, G, m, l);
+    if (w.part >= 0) {
+      float* o = part_o<D>(a, p, w.part, x * 128 + rr) + lane * C;
 #pragma unroll
-      for (int c = 0; c < C; ++c) o.part[4 + lane * C + c] = acc[c];
+      for (int c = 0; c < C; ++c) o[c] = acc[c];
     } else {
+      bf16* o = row_out<D>(a, p, w, x, rr, G) + lane * C;
       const float inv = m == -INFINITY ? 0.f : 1.f / l;
 #pragma unroll
-      for (int c = 0; c < C; ++c) o.out[lane * C + c] = __float2bfloat16_rn(acc[c] * inv);
-      if (o.lse && lane == 0) *o.lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+      for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
     }
   }
 }
@@ -268,9 +301,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     k_ragged_tc(Ragged r, AttnCall a, KVView kv, Plan p, const __grid_constant__ CUtensorMap mq,
                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using C = Cfg<D, NQ>;
-  constexpr int SLOT = C::SLOT, RING = C::RING, NB = D / 64, SW = 4 * NQ;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* smem = (uint8_t*)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+  constexpr int SLOT = C::SLOT, RING = C::RING, NB = D / 64;
+  constexpr int SW = 4 * NQ;  // the first warp behind the softmax
+  extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sR = sQ + 2 * SLOT;
   uint64_t* full = (uint64_t*)(sR + RING * SLOT);
@@ -287,14 +320,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(all_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Work* works = (Work*)(tmem_slot + 2);
-  static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 1024, "barriers and descriptors");
+  static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
     for (int s = 0; s < RING; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // the MMA's commit and the fixer
+      mbar_init(&empty[s], 2);  // the MMAs (seen by a softmax warp, or a commit) and the fixer
       mbar_init(&v_fix[s], 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -306,7 +339,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], SW + 3);
+      mbar_init(&w_empty[s], SW + 3);  // all warps but the scheduler
     }
     mbar_init(all_done, 1);
     *abort_flag = 0;
@@ -331,6 +364,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     *abort_flag = 1;
   };
 
+  if (warp >= SW) {
   if (warp == SW + 3) {
     // ---- scheduler
     r.starts = after_wait(r.starts);
@@ -367,9 +401,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     if (p.mode == kModeItems) {
       // items whose keys reach tile c: counted over the batch
       auto count = [&](int c) {
-        int64_t s = 0;
+        int s = 0;
         for (int b = lane; b < r.batch; b += 32) s += items_reaching(seq_at(b), c, p, a.causal);
-        return warp_sum_l(s);
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
       };
       int max_t = 0;
       for (int b = lane; b < r.batch; b += 32) {
@@ -377,23 +411,21 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (!s.ok && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
         if (s.ok && s.n > 0) max_t = max(max_t, cdiv(s.len, KT));
       }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) max_t = max(max_t, __shfl_xor_sync(0xffffffffu, max_t, o));
-      const int64_t pairs = count(1), total = pairs * a.Hkv, per_group = pairs * p.hgroup;
-      for (int j = 0; ok; ++j) {
-        const int64_t idx = (int64_t)j * grid + ((j & 1) ? grid - 1 - cta : cta);
-        if ((int64_t)j * grid >= total) break;
+      max_t = __reduce_max_sync(0xffffffffu, max_t);
+      const int pairs = count(1), total = pairs * a.Hkv, per_group = pairs * p.hgroup;
+      for (int j = 0; ok && j < total; j += grid) {
+        const int idx = j + (((j / grid) & 1) ? grid - 1 - cta : cta);
         if (idx >= total) continue;
-        const int g = (int)(idx / per_group), heads = min(p.hgroup, a.Hkv - g * p.hgroup);
-        const int64_t rest = idx - g * per_group, pair = rest / heads;
-        const int kvh = g * p.hgroup + (int)(rest - pair * heads);
+        const int g = idx / per_group, heads = min(p.hgroup, a.Hkv - g * p.hgroup);
+        const int rest = idx - g * per_group, pair = rest / heads;
+        const int kvh = g * p.hgroup + rest - pair * heads;
         int c = 1, hi = max_t + 1;
         while (hi - c > 1) {
           const int mid = (c + hi) >> 1;
           if (count(mid) > pair) c = mid;
           else hi = mid;
         }
-        int64_t rank = pair - count(c + 1);
+        int rank = pair - (c < max_t ? count(c + 1) : 0);
         for (int base = 0; base < r.batch; base += 32) {
           const int b = base + lane;
           int here = 0, first = 0;
@@ -404,16 +436,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
             here = ge - items_reaching(s, c + 1, p, a.causal);
             first = items_of(s, p) - ge;
           }
-          int incl = here;
-#pragma unroll
-          for (int o = 1; o < 32; o <<= 1) {
-            const int u = __shfl_up_sync(0xffffffffu, incl, o);
-            if (lane >= o) incl += u;
-          }
-          const int sum = __shfl_sync(0xffffffffu, incl, 31);
+          const int incl = warp_scan_i(here, lane), sum = __shfl_sync(0xffffffffu, incl, 31);
           if (rank < sum) {
             const int src = __ffs(__ballot_sync(0xffffffffu, incl > rank)) - 1;
-            const int qi = __shfl_sync(0xffffffffu, first - (incl - here), src) + (int)rank;
+            const int qi = __shfl_sync(0xffffffffu, first - (incl - here), src) + rank;
             make_work(w, bcast(s, src), base + src, kvh, qi, 0, INT32_MAX / 2, -1, p, a);
             emit(w);
             break;
@@ -422,40 +448,32 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         }
       }
     } else {
-      int64_t units = 0;
+      int units = 0;
       for (int b = lane; b < r.batch; b += 32) {
         const Seq s = seq_at(b);
         if (!s.ok && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
         units += units_of(s, p, a);
       }
-      units = warp_sum_l(units);
-      const int n = ranges_used(units, p, grid);
-      int64_t u = cta < n ? range_start(units, cta, n) : units;
-      const int64_t u1 = cta < n ? range_start(units, cta + 1, n) : units;
-      int64_t before = 0;  // units in front of chunk `base`
+      units = (int)__reduce_add_sync(0xffffffffu, (unsigned)units);
+      const Ranges rg(units, p, grid);
+      int u = cta < rg.n ? rg.start(cta) : units;
+      const int u1 = cta < rg.n ? rg.start(cta + 1) : units;
+      int before = 0;  // units in front of the 32 sequences at `base`
       int seg = 0;
       for (int base = 0; base < r.batch && u < u1 && ok; base += 32) {
         const int b = base + lane;
         Seq s{0, 0, 0, false};
         if (b < r.batch) s = seq_at(b);
-        const int64_t mine_u = units_of(s, p, a);
-        int64_t incl = mine_u;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-          if (lane >= o) incl += v;
-        }
-        const int64_t chunk_end = before + __shfl_sync(0xffffffffu, incl, 31);
+        const int mine_u = units_of(s, p, a), incl = warp_scan_i(mine_u, lane);
+        const int chunk_end = before + __shfl_sync(0xffffffffu, incl, 31);
         while (u < u1 && u < chunk_end && ok) {
           const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
           const Seq q = bcast(s, src);
-          const int64_t off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
-          const int T = tile_count(q, a.window);
-          const int64_t item = off / T;
-          const int t = (int)(off - item * T), take = (int)min((int64_t)(T - t), u1 - u);
+          const int off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
+          const int T = tile_count(q, a.window), item = off / T, qi = item / a.Hkv;
+          const int t = off - item * T, take = min(T - t, u1 - u);
           const int part = t == 0 && take == T ? -1 : 2 * cta + (seg > 0);
-          make_work(w, q, base + src, (int)(item % a.Hkv), (int)(item / a.Hkv), tile_first(q, a.window) + t, take, part,
-                    p, a);
+          make_work(w, q, base + src, item - qi * a.Hkv, qi, tile_first(q, a.window) + t, take, part, p, a);
           emit(w);
           u += take;
           ++seg;
@@ -558,110 +576,146 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         }
     }
   } else if (warp == SW + 1) {
-    // ---- MMA issuer: the whole warp decides, one elected lane issues
+    // ---- MMA issuer: the whole warp decides, one elected lane issues.  The
+    // tensor core takes MMAs little faster than it runs them (8 of them, one
+    // product, in 512 cycles), so whatever this warp does between two products
+    // is idle time, a commit 75 to 150 cycles of it (measured).  NQ = 2, which is
+    // bound by this pipe, commits once per S: the softmax warps, who see it,
+    // give the K/V and Q tiles back that were read in front of it.
     constexpr uint32_t idS = idesc_bf16(128, KT), idPV = idesc_bf16(128, D) | kIdescBMnMajor;
-    uint32_t it = 0, q_use[2] = {0, 0}, s_cnt[2] = {0, 0}, fixpar = 0;
+    uint32_t it = 0, fixpar = 0;
+    uint32_t q_cnt0 = 0, q_cnt1 = 0;    // Q tiles used (NQ = 1: one count, the buffers alternate)
+    uint32_t pv_cnt0 = 0, pv_cnt1 = 0;  // products P V of each stream
+    uint32_t s_cnt = 0;                 // NQ = 1: S issued, the buffers alternate
     bool ok = true;
     auto wait = [&](uint64_t* bar, uint32_t parity) {
       if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag))) ok = false;
       return ok;
     };
+    auto ring_full = [&](uint32_t i) { return wait(&full[i % RING], i / RING); };
     auto issue_s = [&](int qbuf, uint32_t st, int sbuf) {
       const uint32_t q0 = smem_u32(sQ + qbuf * SLOT), k0 = smem_u32(sR + st * SLOT), tS = tmem + sbuf * 128;
 #pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks)
+      for (int ks = 0; ks < D / 16; ++ks) {
         umma_bf16_warp(tS, sdesc_sw128(q0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32),
                        sdesc_sw128(k0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
+      }
       umma_commit_warp(&s_full[sbuf]);
     };
     auto issue_pv = [&](int x, uint32_t st, int sbuf, bool first) {
       const uint32_t v0 = smem_u32(sR + st * SLOT), tP = tmem + sbuf * 128, tO = tmem + O_COL + x * D;
 #pragma unroll
-      for (int ks = 0; ks < KT / 16; ++ks)
+      for (int ks = 0; ks < KT / 16; ++ks) {
         umma_bf16_ts_warp(tO, tP + ks * 8, sdesc_sw128_mn(v0 + ks * 2048, SLOT / NB), idPV, first && ks == 0 ? 0u : 1u);
-      umma_commit_warp(&pv_done[x]);
+      }
     };
-    for (int k = 0; ok; ++k) {
-      const int ws = k % NW;
-      if (!wait(&w_full[ws], (uint32_t)(k / NW))) break;
-      const Work w = works[ws];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&w_empty[ws]);
-      if (w.done) break;
-      const int T = max(w.nt[0], w.nt[1]);
-      if (T == 0) continue;
-      auto dirty = [&](int t) {
-        const int kt = (w.t0 + t) * KT;
-        return kt < w.clean_lo || kt + KT > w.clean_hi;
-      };
-      auto wait_v = [&](int t) {
-        const uint32_t iv = it + 2 * t + 1, st = iv % RING;
-        if (!wait(&full[st], iv / RING)) return false;
-        if (dirty(t)) {
-          if (!wait(&v_fix[st], (fixpar >> st) & 1u)) return false;
-          fixpar ^= 1u << st;
-        }
-        return true;
-      };
+    int k = 0;
+    // what this warp needs of a stretch
+    struct Span {
+      int nt0, nt1, T, t0, clean_lo, clean_hi;
+    };
+    // the next stretch with tiles; false at the end
+    auto fetch = [&](Span& o) {
+      for (;;) {
+        const int ws = k % NW;
+        if (!wait(&w_full[ws], (uint32_t)(k / NW))) return false;
+        const Work& w = works[ws];
+        o.nt0 = w.nt[0];
+        o.nt1 = w.nt[1];
+        o.T = max(o.nt0, o.nt1);
+        o.t0 = w.t0;
+        o.clean_lo = w.clean_lo;
+        o.clean_hi = w.clean_hi;
+        const int done = w.done;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[ws]);
+        ++k;
+        if (done) return false;
+        if (o.T > 0) return true;
+      }
+    };
+    // V of tile t, whose ring entry is i
+    auto wait_v = [&](const Span& w, int t, uint32_t i) {
+      if (!ring_full(i)) return;
+      const int kt = (w.t0 + t) * KT;
+      if (kt < w.clean_lo || kt + KT > w.clean_hi) {  // the fixer looks at it first
+        wait(&v_fix[i % RING], (fixpar >> (i % RING)) & 1u);
+        fixpar ^= 1u << (i % RING);
+      }
+    };
+    // S of a stretch's first tile: issued as soon as the tile before it in the
+    // same stream lets go of the columns, ahead of the other stream's work on
+    // the stretch before
+    auto first_s = [&](int x, int nt, uint32_t ring) {
+      if (nt == 0) return;
       if (NQ == 1) {
-        const int qb = (int)((q_use[0] + q_use[1]) & 1u);
-        if (!wait(&q_full[qb], q_use[qb])) break;
-        ++q_use[qb];
-        for (int t = -1; t < T && ok; ++t) {
-          if (t + 1 < T) {
-            const uint32_t ik = it + 2 * (t + 1), st = ik % RING;
-            if (!wait(&full[st], ik / RING)) break;
-            fence_after();
-            issue_s(qb, st, (int)(s_cnt[0] & 1u));
-            ++s_cnt[0];
-            umma_commit_warp(&empty[st]);
-            if (t + 2 == T) umma_commit_warp(&q_empty[qb]);
-          }
-          if (t >= 0) {
-            // tile t is the (s_cnt - 1)th S issued, or the one before when S(t + 1) went ahead
-            const uint32_t sc = s_cnt[0] - 1 - (t + 1 < T ? 1 : 0);
-            if (!wait_v(t) || !wait(&p_full[sc & 1u], sc >> 1)) break;
-            fence_after();
-            const uint32_t st = (it + 2 * t + 1) % RING;
-            issue_pv(0, st, (int)(sc & 1u), t == 0);
-            umma_commit_warp(&empty[st]);
-          }
-        }
+        if (!wait(&q_full[q_cnt0 & 1u], q_cnt0 >> 1) || !ring_full(ring)) return;
+        issue_s((int)(q_cnt0 & 1u), ring % RING, (int)(s_cnt & 1u));
+        umma_commit_warp(&empty[ring % RING]);
+        if (nt == 1) umma_commit_warp(&q_empty[q_cnt0 & 1u]);
+        ++q_cnt0;
+        ++s_cnt;
       } else {
-        for (int x = 0; x < 2 && ok; ++x)
-          if (w.nt[x] > 0) {
-            wait(&q_full[x], q_use[x]);
-            ++q_use[x];
+        if (!wait(&q_full[x], x ? q_cnt1 : q_cnt0) || !ring_full(ring)) return;
+        issue_s(x, ring % RING, x);
+        if (x) ++q_cnt1;
+        else ++q_cnt0;
+      }
+    };
+    Span w, nx;
+    bool have = fetch(w);
+    if (have) {
+      first_s(0, w.nt0, it);
+      if (NQ == 2) first_s(1, w.nt1, it);
+    }
+    while (have && ok) {
+      bool more = false;
+      for (int t = 0; t < w.T && ok; ++t) {
+        const bool last = t + 1 == w.T;
+        const uint32_t iv = it + 2 * t + 1, ik = it + 2 * (t + 1), sv = iv % RING, sk = ik % RING;
+        if (last) more = fetch(nx);
+        if (NQ == 1) {
+          // S of the next tile in the stream goes ahead of this tile's product
+          if (!last) {
+            if (!ring_full(ik)) break;
+            const int qb = (int)((q_cnt0 + 1) & 1u);  // the buffer in use
+            issue_s(qb, sk, (int)(s_cnt & 1u));
+            umma_commit_warp(&empty[sk]);
+            if (t + 2 == w.T) umma_commit_warp(&q_empty[qb]);
+            ++s_cnt;
+          } else if (more) {
+            first_s(0, nx.nt0, ik);
           }
-        if (!wait(&full[it % RING], it / RING)) break;
-        fence_after();
-        for (int x = 0; x < 2; ++x)
-          if (w.nt[x] > 0) {
-            issue_s(x, it % RING, x);
-            if (w.nt[x] == 1) umma_commit_warp(&q_empty[x]);
-          }
-        umma_commit_warp(&empty[it % RING]);
-        for (int t = 0; t < T && ok; ++t) {
-          if (!wait_v(t)) break;
-          const uint32_t sv = (it + 2 * t + 1) % RING, ik = it + 2 * (t + 1), sk = ik % RING;
-          for (int x = 0; x < 2 && ok; ++x) {
-            if (t >= w.nt[x]) continue;
-            if (!wait(&p_full[x], s_cnt[x])) break;
-            ++s_cnt[x];
-            fence_after();
-            issue_pv(x, sv, x, t == 0);
-            if (t + 1 < w.nt[x]) {
-              if (!wait(&full[sk], ik / RING)) break;
-              fence_after();
-              issue_s(x, sk, x);
-              if (t + 2 == w.nt[x]) umma_commit_warp(&q_empty[x]);
-            }
-          }
+          wait_v(w, t, iv);
+          if (!wait(&p_full[pv_cnt0 & 1u], pv_cnt0 >> 1)) break;
+          fence_after();
+          issue_pv(0, sv, (int)(pv_cnt0 & 1u), t == 0);
+          umma_commit_warp(&pv_done[0]);
           umma_commit_warp(&empty[sv]);
-          if (t + 1 < T) umma_commit_warp(&empty[sk]);
+          ++pv_cnt0;
+        } else {
+          wait_v(w, t, iv);
+#pragma unroll
+          for (int x = 0; x < 2; ++x) {
+            const int nt = x ? w.nt1 : w.nt0;
+            uint32_t& cnt = x ? pv_cnt1 : pv_cnt0;
+            if (ok && t < nt && wait(&p_full[x], cnt)) {
+              ++cnt;
+              fence_after();
+              issue_pv(x, sv, x, t == 0);
+              if (t + 1 < nt) {
+                if (ring_full(ik)) issue_s(x, sk, x);
+              } else {
+                umma_commit_warp(&pv_done[x]);
+              }
+            }
+            if (ok && last && more) first_s(x, x ? nx.nt1 : nx.nt0, ik);
+          }
         }
       }
-      it += 2 * T;
+      it += 2 * w.T;
+      w = nx;
+      have = more;
     }
     if (!ok) give_up();
     umma_commit_warp(all_done);  // every product issued above has ended before TMEM is given back
@@ -728,12 +782,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       if (w.done) break;
     }
     if (!ok) give_up();
+  }
   } else {
     // ---- softmax: one thread per row
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16, tO = tmem + lrow + O_COL + x * D;
     const float sl2 = a.scale * kLog2e;
-    uint32_t cnt = 0;  // tiles of this warp's stream so far
+    uint32_t cnt = 0;          // tiles of this warp's stream so far
+    uint32_t it = 0;           // ring entries so far
+    uint32_t q_cnt = 0;        // stretches with tiles of this stream so far
+    const bool teller = NQ == 2 && (warp & 3) == 0 && lane == 0;  // gives tiles back for its stream
+    // 32-byte stores where base and strides allow them
+    const bool whole = (((uintptr_t)a.out | (uintptr_t)(a.o_row * 2) | (uintptr_t)(a.o_head * 2)) & 31) == 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int ws = k % NW;
@@ -752,7 +812,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         lo = vis_lo(pos, a.window);
         hi = vis_hi(pos, w.len, a.causal);
       }
-      const int T = w.nt[x];
+      const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < T; ++t, ++cnt) {
         const int sb = NQ == 2 ? x : (int)(cnt & 1u);
@@ -761,23 +821,36 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           ok = false;
           break;
         }
-        // The product before S is through too (NQ = 2: tile t - 1's, issued in
-        // front of S; NQ = 1: tile t - 2's).  Waiting here at every tile keeps
-        // each later wait on pv_done within one phase.
-        if (t >= 3 - NQ &&
-            !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - (3 - NQ)) & 1u, abort_flag))) {
-          ok = false;
-          break;
+        if (teller) {
+          // S of this tile is through, and with it the product before it.  K
+          // goes back with the later stream's S, V with its product.
+          if (x == 1 || t >= nt_other) mbar_arrive(&empty[(it + 2 * t) % RING]);
+          if (t > 0 && (x == 1 || t > nt_other)) mbar_arrive(&empty[(it + 2 * t - 1) % RING]);
+          if (t + 1 == T) mbar_arrive(&q_empty[x]);
         }
+        // NQ = 1: every warp sees each of pv_done's phases, in order, before it
+        // lets the next product start, so the parity is never ambiguous.  (NQ =
+        // 2: S of this tile was issued behind the product before it.)
+        auto prior_product = [&]() {
+          if (NQ == 1 && cnt > 0) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag));
+          }
+          return ok;
+        };
         if (live) {
           const int kt = (w.t0 + t) * KT;
           float s[128];
           fence_after();
           tmem_ld128(tmem + lrow + sb * 128, s);
-          if (!__all_sync(0xffffffffu, lo <= kt && hi >= kt + KT)) {
-            const int l0 = lo - kt, h0 = hi - kt;
+          if (!__all_sync(0xffffffffu, hi >= kt + KT)) {
+            const int h0 = hi - kt;
 #pragma unroll
-            for (int j = 0; j < 128; ++j) s[j] = (j >= l0 && j < h0) ? s[j] : -INFINITY;
+            for (int j = 0; j < 128; ++j) s[j] = j < h0 ? s[j] : -INFINITY;
+          }
+          if (!__all_sync(0xffffffffu, lo <= kt)) {
+            const int l0 = lo - kt;
+#pragma unroll
+            for (int j = 0; j < 128; ++j) s[j] = j >= l0 ? s[j] : -INFINITY;
           }
           float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
 #pragma unroll
@@ -791,11 +864,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           m1 = max3(m1, s[126], s[127]);
           const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
           const bool grow = valid && mt > m + 8.f;
-          const float mn = grow ? mt : m;
-          const float f = grow && m != -INFINITY ? ex2(m - mn) : 1.f;
-          if (__any_sync(0xffffffffu, f != 1.f)) {
-            // O holds the previous tile's product before it is scaled
-            if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
+          if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+            const float f = grow && m != -INFINITY ? ex2(m - mt) : 1.f;
+            // O holds the previous tile's product before it is scaled (NQ = 2: S of
+            // this tile was issued behind it)
+            if (NQ == 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
               ok = false;
               break;
             }
@@ -810,17 +883,16 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
             }
             l *= f;
           }
-          m = mn;
+          if (grow) m = mt;
           const float mref = m == -INFINITY ? 0.f : m;
           const uint64_t k2 = f2pack(sl2, sl2), c2 = f2pack(-mref, -mref);
           uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
+          auto probs = [&](int c) {  // 32 keys
+            uint32_t pk[16];
 #pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            uint32_t pk[32];
-#pragma unroll
-            for (int j = 0; j < 32; ++j) {
+            for (int j = 0; j < 16; ++j) {
               uint64_t e2;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[64 * h + 2 * j], s[64 * h + 2 * j + 1])), "l"(k2), "l"(c2));
+              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
               const float2 e = f2unpack(e2);
               const float p0 = ex2(e.x), p1 = ex2(e.y);
               if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(f2pack(p0, p1)));
@@ -828,56 +900,67 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
               const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
               pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
             }
-            tmem_st32u(tmem + lrow + sb * 128 + 32 * h, pk);
-          }
-          const float2 sa = f2unpack(sum0), sc = f2unpack(sum1);
-          l += (sa.x + sa.y) + (sc.x + sc.y);
+            tmem_st16u(tmem + lrow + sb * 128 + c / 2, pk);
+          };
+          probs(0);
+          probs(32);
+          probs(64);
+          probs(96);
+          const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
+          l += (s0.x + s0.y) + (s1.x + s1.y);
           tmem_wait_st();
           fence_before();
+          if (!prior_product()) break;
+        } else {
+          if (!prior_product()) break;
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[sb]);
+        if (lane == 0) mbar_arrive_relaxed(&p_full[sb]);
       }
       if (!ok) break;
       if (T > 0) {
-        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
+        // the last product: NQ = 1 commits every one of them, NQ = 2 only this
+        if (!__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (NQ == 1 ? cnt - 1 : q_cnt) & 1u, abort_flag))) {
           ok = false;
           break;
         }
+        if (teller && (x == 1 || T > nt_other)) mbar_arrive(&empty[(it + 2 * T - 1) % RING]);
+        ++q_cnt;
         fence_after();
       }
-      if (T > 0 && *(volatile int32_t*)&w.bad) {
+      it += 2 * max(T, nt_other);
+      // ---- epilogue: O and (m, l) of the rows (a store is 32 bytes of one row)
+      if (T > 0 && *(volatile const int32_t*)&w.bad) {
         redo_rows<D>(r, a, kv, p, w, x, warp & 3);  // rows in turn over all four warps
       } else if (live) {
-        const RowOut o = row_out<D>(a, p, w, x, valid ? row : 0, G);
-        const float inv = o.part ? 1.f : m == -INFINITY ? 0.f : 1.f / l;
-        if (valid && o.part) *reinterpret_cast<float4*>(o.part) = make_float4(m, l, 0.f, 0.f);
-        if (valid && o.lse) *o.lse = m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        if (valid) store_stats<D>(a, p, w, x, row, G, m, l);
+        float* po = w.part >= 0 ? part_o<D>(a, p, w.part, x * 128 + row) : nullptr;
+        bf16* o = row_out<D>(a, p, w, x, valid ? row : 0, G);
 #pragma unroll 1
         for (int c = 0; c < D && T > 0; c += 32) {
           float v[32];
           tmem_ld32(tO + c, v);
-          if (valid && o.part) {
+          if (valid && w.part >= 0) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 4)
-              *reinterpret_cast<float4*>(o.part + 4 + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+            for (int j = 0; j < 32; j += 8) store32(po + c + j, reinterpret_cast<const uint32_t*>(v + j), true);
           } else if (valid) {
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t u[4];
+            for (int j = 0; j < 32; j += 16) {
+              uint32_t u[8];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
+              for (int q = 0; q < 8; ++q) {
                 const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[j + 2 * q] * inv, v[j + 2 * q + 1] * inv);
                 u[q] = *reinterpret_cast<const uint32_t*>(&b2);
               }
-              *reinterpret_cast<uint4*>(o.out + c + j) = make_uint4(u[0], u[1], u[2], u[3]);
+              store32(o + c + j, u, whole);
             }
           }
         }
+        fence_before();
       }
-      fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&w_empty[ws]);
+      if (lane == 0) mbar_arrive_relaxed(&w_empty[ws]);
     }
     if (!ok) give_up();
   }
@@ -901,53 +984,48 @@ __global__ void __launch_bounds__(256) k_ragged_merge(Ragged r, AttnCall a, Plan
   if (r.lens) r.lens = after_wait(r.lens);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int G = a.Hq / a.Hkv, row = blockIdx.y * 8 + warp, c = blockIdx.x + 1;
-  int64_t units = 0;
-  for (int b = lane; b < r.batch; b += 32) units += units_of(load_seq(r, b), p, a);
-  units = warp_sum_l(units);
-  const int n = ranges_used(units, p, grid);
-  if (c >= n) return;
-  const int64_t u = range_start(units, c, n);
-  int64_t before = 0;
+  const bool one = r.batch <= 32;
+  Seq mine_s{0, 0, 0, false};
+  if (one && lane < r.batch) mine_s = load_seq(r, lane);
+  int units = 0;
+  for (int b = lane; b < r.batch; b += 32) units += units_of(one ? mine_s : load_seq(r, b), p, a);
+  units = (int)__reduce_add_sync(0xffffffffu, (unsigned)units);
+  const Ranges rg(units, p, grid);
+  if (c >= rg.n) return;
+  const int u = rg.start(c), n = rg.n;
+  int before = 0;
   for (int base = 0; base < r.batch; base += 32) {
     const int b = base + lane;
     Seq s{0, 0, 0, false};
-    if (b < r.batch) s = load_seq(r, b);
-    const int64_t mine = units_of(s, p, a);
-    int64_t incl = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += v;
-    }
-    const int64_t end = before + __shfl_sync(0xffffffffu, incl, 31);
+    if (b < r.batch) s = one ? mine_s : load_seq(r, b);
+    const int mine = units_of(s, p, a), incl = warp_scan_i(mine, lane);
+    const int end = before + __shfl_sync(0xffffffffu, incl, 31);
     if (u >= end) {
       before = end;
       continue;
     }
     const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
-    const int64_t seq_u = before + __shfl_sync(0xffffffffu, incl - mine, src);
+    const int seq_u = before + __shfl_sync(0xffffffffu, incl - mine, src);
     const int start = __shfl_sync(0xffffffffu, s.start, src), sn = __shfl_sync(0xffffffffu, s.n, src);
     const int T = __shfl_sync(0xffffffffu, s.ok && s.n > 0 ? tile_count(s, a.window) : 1, src);
-    const int64_t item = (u - seq_u) / T, i_begin = seq_u + item * T, i_end = i_begin + T;
-    if (u == i_begin || range_start(units, c - 1, n) > i_begin) return;  // no cut here, or not the item's first
-    const int kvh = (int)(item % a.Hkv), i0 = (int)(item / a.Hkv) * p.tok;
+    const int item = (u - seq_u) / T, i_begin = seq_u + item * T, i_end = i_begin + T;
+    if (u == i_begin || rg.start(c - 1) > i_begin) return;  // no cut here, or not the item's first
+    const int qi = item / a.Hkv, kvh = item - qi * a.Hkv, i0 = qi * p.tok;
     const int x = row / 128, rr = row % 128, i = i0 + x * p.tpt + rr / G;
     if (rr >= p.tpt * G || i >= min(i0 + p.tok, sn)) return;
     // parts: ranges c - 1 .. last; a range's first stretch is its slot 0, the
     // one that it ends with its slot 1.  The parts' (max, sum) arrive a lane
     // each, then O eight parts at a time: three trips to memory for 32 parts.
     int parts = 1;
-    while (c - 1 + parts < n && range_start(units, c - 1 + parts, n) < i_end) ++parts;
-    const float* p0 = a.ws + (int64_t)row * (D + 4);
-    const int64_t slot_st = (int64_t)p.ws_rows * (D + 4);
-    const int slot0 = 2 * (c - 1) + (range_start(units, c - 1, n) < i_begin);
-    auto part_at = [&](int q) { return p0 + (q == 0 ? slot0 : 2 * (c - 1 + q)) * slot_st; };
+    while (c - 1 + parts < n && rg.start(c - 1 + parts) < i_end) ++parts;
+    const int slot0 = 2 * (c - 1) + (rg.start(c - 1) < i_begin);
+    auto slot_of = [&](int q) { return q == 0 ? slot0 : 2 * (c - 1 + q); };
     float M = -INFINITY, L = 0.f, acc[C];
 #pragma unroll
     for (int j = 0; j < C; ++j) acc[j] = 0.f;
     for (int base = 0; base < parts; base += 32) {
       float2 ml = make_float2(-INFINITY, 0.f);
-      if (base + lane < parts) ml = *reinterpret_cast<const float2*>(part_at(base + lane));
+      if (base + lane < parts) ml = *part_ml<D>(a, p, slot_of(base + lane), row);
       const float Mn = fmaxf(M, warp_max(ml.x)), mref = Mn == -INFINITY ? 0.f : Mn;
       const float f = M == -INFINITY ? 0.f : exp2f(M - mref);
       // a part that saw no key has weight 0 and its sums were not written; a NaN maximum stays one
@@ -966,7 +1044,7 @@ __global__ void __launch_bounds__(256) k_ragged_merge(Ragged r, AttnCall a, Plan
 #pragma unroll
           for (int j = 0; j < C; ++j) v[q][j] = 0.f;
           if (wq[q] != 0.f) {
-            const float* pp = part_at(base + q0 + q) + 4 + lane * C;
+            const float* pp = part_o<D>(a, p, slot_of(base + q0 + q), row) + lane * C;
             if (C == 4) {
               const float4 t = *reinterpret_cast<const float4*>(pp);
               v[q][0] = t.x;
@@ -1030,11 +1108,12 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
   p.ws_rows = h.nq == 1 ? p.tpt * G : 256;
   const int64_t items = ((int64_t)r.total / p.tok + std::min(r.batch, r.total)) * a.Hkv;
   const int tiles = (r.max_len + KT - 1) / KT;
-  p.mode = h.nq == 2 && (items >= 3 * sms / 2 || tiles <= 4) ? kModeItems : kModeRanges;
+  p.mode = (h.nq == 2 && (items >= 3 * sms / 2 || tiles <= 4)) || items * tiles > INT32_MAX ? kModeItems : kModeRanges;
   // items: heads dealt out together while their K/V (both, bf16) stay within 48 MB of L2
   const int64_t per_head = std::max<int64_t>(1, (int64_t)(r.lens ? (int64_t)r.max_len * std::min(r.batch, r.total) : r.total) * a.d * 4);
   p.hgroup = (int)std::max<int64_t>(1, std::min<int64_t>(a.Hkv, (48ll << 20) / per_head));
-  p.min_tiles = h.nq == 2 ? 4 : 1;
+  p.min_tiles_log2 = h.nq == 2 ? 2 : 0;
+  p.slots = 2 * sms;
   h.merge = p.mode == kModeRanges && tiles > 1;
   return h;
 }
@@ -1108,7 +1187,7 @@ cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes
     sms = 152;
   }
   const HostPlan h = make_plan(r, a, sms);
-  *bytes = h.merge ? (int64_t)2 * sms * h.p.ws_rows * (a.d + 4) * 4 : 0;
+  *bytes = h.merge ? (int64_t)h.p.slots * h.p.ws_rows * (a.d + 2) * 4 : 0;
   return cudaSuccess;
 }
 

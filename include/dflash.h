@@ -581,7 +581,7 @@ typedef struct dflash_ragged {
  * to bf16 for the second product.  out overlaps no input. */
 typedef struct dflash_attention {
   int32_t dtype;       /* of q, k, v and out */
-  int32_t n_q_heads;   /* a multiple of n_kv_heads, at most 128 per KV head */
+  int32_t n_q_heads;   /* a multiple of n_kv_heads, at most 128 per KV head; x total_rows below 2^31 */
   int32_t n_kv_heads;
   int32_t head_dim;
   int32_t causal;      /* 0 or 1 */
@@ -590,7 +590,7 @@ typedef struct dflash_attention {
   dflash_heads q;      /* [total_rows][n_q_heads][head_dim] */
   dflash_heads out;    /* the same shape */
   float* lse;          /* [total_rows][n_q_heads] natural log of the softmax sum, or NULL */
-  void* workspace;     /* 16-byte aligned, used until the call's kernels end; not shared by calls that may overlap */
+  void* workspace;     /* 32-byte aligned, used until the call's kernels end; not shared by calls that may overlap */
   int64_t workspace_bytes;  /* at least dflash_attention_workspace */
 } dflash_attention;
 
