@@ -78,8 +78,9 @@ struct Work {
 template <int D, int NQ>
 struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
-  static constexpr int RING = 7 * 32768 / SLOT - 2;       // K/V tiles in flight
-  static constexpr int DATA = (RING + 2) * SLOT;          // 224 KB
+  static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;    // 128 bytes of 32 rows for each softmax warp
+  static constexpr int RING = (7 * 32768 - STAGE) / SLOT - 2;  // K/V tiles in flight
+  static constexpr int DATA = (RING + 2) * SLOT + STAGE;  // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
   static constexpr size_t SMEM = DATA + 768;  // + barriers and descriptors
 };
@@ -112,16 +113,15 @@ __device__ __forceinline__ int warp_scan_i(int v, int lane) {  // inclusive
   }
   return v;
 }
-// 32 bytes of a row, in one store where the row allows it
-__device__ __forceinline__ void store32(void* p, const uint32_t* v, bool whole) {
-  if (whole) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-  } else {
-    reinterpret_cast<uint4*>(p)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    reinterpret_cast<uint4*>(p)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+// eight scaled values as bf16
+__device__ __forceinline__ uint4 pack8(const float* v, float f) {
+  uint32_t u[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[2 * q] * f, v[2 * q + 1] * f);
+    u[q] = *reinterpret_cast<const uint32_t*>(&b2);
   }
+  return make_uint4(u[0], u[1], u[2], u[3]);
 }
 // Arrival that publishes no memory (the tensor-memory fence in front of it
 // orders what it hands over): unlike the default it does not wait for this
@@ -202,24 +202,19 @@ template <int D>
 __device__ __forceinline__ float2* part_ml(const AttnCall& a, const Plan& p, int slot, int row) {
   return reinterpret_cast<float2*>(a.ws + (int64_t)p.slots * p.ws_rows * D) + (int64_t)slot * p.ws_rows + row;
 }
-__device__ __forceinline__ int row_token(const Plan& p, const Work& w, int x, int r, int G) {
-  return w.start + w.i0 + x * p.tpt + r / G;
-}
-// (m, l) of a partial, or the row's log-sum-exp
+// (m, l) of a partial (row r of tile x), or the log-sum-exp of token i, head h
 template <int D>
-__device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G,
+__device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int i, int h,
                                             float m, float l) {
   if (w.part >= 0) {
     *part_ml<D>(a, p, w.part, x * 128 + r) = make_float2(m, l);
   } else if (a.lse) {
-    a.lse[(int64_t)row_token(p, w, x, r, G) * a.Hq + w.kvh * G + r % G] =
+    a.lse[(int64_t)(w.start + i) * a.Hq + h] =
         m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
-template <int D>
-__device__ __forceinline__ bf16* row_out(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int G) {
-  return reinterpret_cast<bf16*>(a.out) + (int64_t)row_token(p, w, x, r, G) * a.o_row +
-         (int64_t)(w.kvh * G + r % G) * a.o_head;
+__device__ __forceinline__ bf16* row_out(const AttnCall& a, const Work& w, int i, int h) {
+  return reinterpret_cast<bf16*>(a.out) + (int64_t)(w.start + i) * a.o_row + (int64_t)h * a.o_head;
 }
 
 // The rows of tile x of a work stretch, from the definition, on the CUDA
@@ -282,13 +277,13 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
         for (int c = 0; c < C; ++c) acc[c] = fmaf(pu, __bfloat162float(v[lane * C + c]), acc[c]);
       }
     }
-    if (lane == 0) store_stats<D>(a, p, w, x, rr, G, m, l);
+    if (lane == 0) store_stats<D>(a, p, w, x, rr, i, h, m, l);
     if (w.part >= 0) {
       float* o = part_o<D>(a, p, w.part, x * 128 + rr) + lane * C;
 #pragma unroll
       for (int c = 0; c < C; ++c) o[c] = acc[c];
     } else {
-      bf16* o = row_out<D>(a, p, w, x, rr, G) + lane * C;
+      bf16* o = row_out(a, w, i, h) + lane * C;
       const float inv = m == -INFINITY ? 0.f : 1.f / l;
 #pragma unroll
       for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
@@ -306,7 +301,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sR = sQ + 2 * SLOT;
-  uint64_t* full = (uint64_t*)(sR + RING * SLOT);
+  uint8_t* sS = sR + RING * SLOT;
+  uint64_t* full = (uint64_t*)(sS + C::STAGE);
   uint64_t* empty = full + RING;
   uint64_t* v_fix = empty + RING;
   uint64_t* q_full = v_fix + RING;
@@ -791,9 +787,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     uint32_t cnt = 0;          // tiles of this warp's stream so far
     uint32_t it = 0;           // ring entries so far
     uint32_t q_cnt = 0;        // stretches with tiles of this stream so far
+    const int row_i = x * p.tpt + row / G, row_g = row % G;  // this row's token (in the item) and head (in the group)
     const bool teller = NQ == 2 && (warp & 3) == 0 && lane == 0;  // gives tiles back for its stream
-    // 32-byte stores where base and strides allow them
-    const bool whole = (((uintptr_t)a.out | (uintptr_t)(a.o_row * 2) | (uintptr_t)(a.o_head * 2)) & 31) == 0;
     bool ok = true;
     for (int k = 0; ok; ++k) {
       const int ws = k % NW;
@@ -803,7 +798,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       }
       const Work& w = works[ws];
       if (w.done) break;
-      const int i = w.i0 + x * p.tpt + row / G;
+      const int i = w.i0 + row_i, h = w.kvh * G + row_g;
       const bool valid = row < p.tpt * G && i < min(w.i0 + p.tok, w.n);
       const bool live = __any_sync(0xffffffffu, valid);
       int lo = 0, hi = INT32_MAX;  // padding rows ask for no mask
@@ -812,6 +807,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         lo = vis_lo(pos, a.window);
         hi = vis_hi(pos, w.len, a.causal);
       }
+      const int hi_min = __reduce_min_sync(0xffffffffu, hi);
+      const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
       for (int t = 0; t < T; ++t, ++cnt) {
@@ -824,9 +821,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (teller) {
           // S of this tile is through, and with it the product before it.  K
           // goes back with the later stream's S, V with its product.
-          if (x == 1 || t >= nt_other) mbar_arrive(&empty[(it + 2 * t) % RING]);
-          if (t > 0 && (x == 1 || t > nt_other)) mbar_arrive(&empty[(it + 2 * t - 1) % RING]);
-          if (t + 1 == T) mbar_arrive(&q_empty[x]);
+          if (x == 1 || t >= nt_other) mbar_arrive_relaxed(&empty[(it + 2 * t) % RING]);
+          if (t > 0 && (x == 1 || t > nt_other)) mbar_arrive_relaxed(&empty[(it + 2 * t - 1) % RING]);
+          if (t + 1 == T) mbar_arrive_relaxed(&q_empty[x]);
         }
         // NQ = 1: every warp sees each of pv_done's phases, in order, before it
         // lets the next product start, so the parity is never ambiguous.  (NQ =
@@ -842,12 +839,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           float s[128];
           fence_after();
           tmem_ld128(tmem + lrow + sb * 128, s);
-          if (!__all_sync(0xffffffffu, hi >= kt + KT)) {
+          if (hi_min < kt + KT) {  // keys that some row does not see
             const int h0 = hi - kt;
 #pragma unroll
             for (int j = 0; j < 128; ++j) s[j] = j < h0 ? s[j] : -INFINITY;
           }
-          if (!__all_sync(0xffffffffu, lo <= kt)) {
+          if (lo_max > kt) {
             const int l0 = lo - kt;
 #pragma unroll
             for (int j = 0; j < 128; ++j) s[j] = j >= l0 ? s[j] : -INFINITY;
@@ -924,36 +921,76 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           ok = false;
           break;
         }
-        if (teller && (x == 1 || T > nt_other)) mbar_arrive(&empty[(it + 2 * T - 1) % RING]);
+        if (teller && (x == 1 || T > nt_other)) mbar_arrive_relaxed(&empty[(it + 2 * T - 1) % RING]);
         ++q_cnt;
         fence_after();
       }
       it += 2 * max(T, nt_other);
-      // ---- epilogue: O and (m, l) of the rows (a store is 32 bytes of one row)
+      // ---- epilogue: O and (m, l) of the rows
       if (T > 0 && *(volatile const int32_t*)&w.bad) {
         redo_rows<D>(r, a, kv, p, w, x, warp & 3);  // rows in turn over all four warps
       } else if (live) {
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
-        if (valid) store_stats<D>(a, p, w, x, row, G, m, l);
-        float* po = w.part >= 0 ? part_o<D>(a, p, w.part, x * 128 + row) : nullptr;
-        bf16* o = row_out<D>(a, p, w, x, valid ? row : 0, G);
+        if (valid) store_stats<D>(a, p, w, x, row, i, h, m, l);
+        if constexpr (NQ == 1) {
+          // few rows: a row per lane
 #pragma unroll 1
-        for (int c = 0; c < D && T > 0; c += 32) {
-          float v[32];
-          tmem_ld32(tO + c, v);
-          if (valid && w.part >= 0) {
+          for (int c = 0; c < D && T > 0; c += 32) {
+            float v[32];
+            tmem_ld32(tO + c, v);
+            if (valid && w.part >= 0) {
+              uint4* o = reinterpret_cast<uint4*>(part_o<D>(a, p, w.part, row) + c);
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) store32(po + c + j, reinterpret_cast<const uint32_t*>(v + j), true);
-          } else if (valid) {
+              for (int j = 0; j < 8; ++j) o[j] = *reinterpret_cast<const uint4*>(v + 4 * j);
+            } else if (valid) {
+              uint4* o = reinterpret_cast<uint4*>(row_out(a, w, i, h) + c);
 #pragma unroll
-            for (int j = 0; j < 32; j += 16) {
-              uint32_t u[8];
+              for (int j = 0; j < 4; ++j) o[j] = pack8(v + 8 * j, inv);
+            }
+          }
+        } else {
+          // 128 bytes of each row at a time through shared memory, so that a store
+          // covers whole lines (a row per lane took five times as long): row r's
+          // 16-byte chunk c lies at chunk c ^ (r & 7).
+          const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+          uint8_t* st = sS + warp * 4096;
+          // where this lane's own row starts, in 16-byte units
+          const int64_t own =
+              w.part >= 0 ? ((int64_t)w.part * p.ws_rows + x * 128 + row) * (D / 4)
+                          : ((int64_t)(w.start + i) * a.o_row + (int64_t)h * a.o_head) / 8;
+          uint4* const base = reinterpret_cast<uint4*>(w.part >= 0 ? (void*)a.ws : a.out);
+          auto flush = [&](int at) {  // the staged 128 bytes of each row to 16-byte unit `at` of it
+            __syncwarp();
 #pragma unroll
-              for (int q = 0; q < 8; ++q) {
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(v[j + 2 * q] * inv, v[j + 2 * q + 1] * inv);
-                u[q] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int k = 0; k < 8; ++k) {
+              const int rr = 4 * k + (lane >> 3), c = lane & 7;
+              const int64_t o = __shfl_sync(0xffffffffu, own, rr);
+              const uint4 q = *reinterpret_cast<const uint4*>(st + rr * 128 + ((c ^ (rr & 7)) << 4));
+              if ((rows >> rr) & 1u) base[o + at + c] = q;
+            }
+            __syncwarp();
+          };
+          auto put = [&](int c, uint4 q) { *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4)) = q; };
+          if (T > 0 && w.part >= 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              float v[32];
+              tmem_ld32(tO + c, v);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) put(j, *reinterpret_cast<const uint4*>(v + 4 * j));
+              flush(c / 4);
+            }
+          } else if (T > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 64) {
+#pragma unroll
+              for (int h = 0; h < 2; ++h) {
+                float v[32];
+                tmem_ld32(tO + c + 32 * h, v);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) put(4 * h + j, pack8(v + 8 * j, inv));
               }
-              store32(o + c + j, u, whole);
+              flush(c / 8);
             }
           }
         }
