@@ -30,7 +30,7 @@ __all__ = [
     "Target", "dflash_target_create", "dflash_target_destroy", "dflash_target_forward", "dflash_target_trim",
     "dflash_target_length", "dflash_target_argmax", "dflash_target_device_status",
     "dflash_logits_compare", "dflash_exactness_summarize", "dflash_target_exactness_probe", "exactness_rows",
-    "dflash_kv_append", "dflash_paged_attention", "dflash_prompt_attention", "dflash_attention_workspace",
+    "dflash_target_create_paged", "dflash_kv_append", "dflash_paged_attention", "dflash_prompt_attention", "dflash_attention_workspace",
     "dflash_token_logprobs", "dflash_status_check",
 ]
 
@@ -354,10 +354,7 @@ class Target:
             self.handle = None
 
 
-def dflash_target_create(cfg: dict, weights: dict, max_ctx: int = 4096, stream=None) -> Target:
-    """cfg: hidden, n_heads, head_dim, intermediate, vocab, n_layers, rope_theta, rms_eps;
-    weights: fp32 CUDA tensors embed, unembed, final_norm and layers = [dict n1, wq, wk,
-    wv, wo, n2, wg, wu, wd]."""
+def _target_args(cfg: dict, weights: dict):
     c = _abi.dflash_target_config(hidden=cfg["hidden"], n_heads=cfg["n_heads"], head_dim=cfg["head_dim"],
                                   intermediate=cfg["intermediate"], vocab=cfg["vocab"], n_layers=cfg["n_layers"],
                                   rope_theta=cfg["rope_theta"], rms_eps=cfg["rms_eps"])
@@ -384,10 +381,39 @@ def dflash_target_create(cfg: dict, weights: dict, max_ctx: int = 4096, stream=N
     w = _abi.dflash_target_weights(embed=dev(weights["embed"], (V, H), "embed"),
                                    unembed=dev(weights["unembed"], (V, H), "unembed"),
                                    final_norm=dev(weights["final_norm"], (H,), "final_norm"), layers=layers)
+    return c, w, keep, layers
+
+
+def dflash_target_create(cfg: dict, weights: dict, max_ctx: int = 4096, stream=None) -> Target:
+    """cfg: hidden, n_heads, head_dim, intermediate, vocab, n_layers, rope_theta, rms_eps;
+    weights: fp32 CUDA tensors embed, unembed, final_norm and layers = [dict n1, wq, wk,
+    wv, wo, n2, wg, wu, wd]."""
+    c, w, keep, layers = _target_args(cfg, weights)
     stream = stream if stream is not None else torch.cuda.current_stream()
     out = C.c_void_p()
     _check(lib.dflash_target_create(C.byref(c), C.byref(w), max_ctx, C.c_void_p(stream.cuda_stream), C.byref(out)))
     return Target(out.value, dict(cfg), keep, layers)
+
+
+def dflash_target_create_paged(cfg: dict, weights: dict, pages, table: torch.Tensor, max_ctx: int | None = None,
+                               stream=None) -> Target:
+    """A target on a paged cache that it may share with others.  pages: one (k_pages, v_pages) pair per
+    layer, fp32 [n_pages, page_size, n_heads, head_dim]; table: int32 CUDA vector, the page of position p
+    at p // page_size; max_ctx: None is what the table can hold."""
+    c, w, keep, layers = _target_args(cfg, weights)
+    pages = list(pages)
+    if len(pages) != cfg["n_layers"]:
+        raise ValueError("pages: one (k_pages, v_pages) pair per layer")
+    arr = (_abi.dflash_kv_pages * len(pages))(*[_pages(k, v) for k, v in pages])
+    width = table.numel()
+    _int_vector(table, width, "table")
+    if max_ctx is None:
+        max_ctx = width * arr[0].page_size
+    stream = stream if stream is not None else torch.cuda.current_stream()
+    out = C.c_void_p()
+    _check(lib.dflash_target_create_paged(C.byref(c), C.byref(w), arr, table.data_ptr(), width, max_ctx,
+                                          C.c_void_p(stream.cuda_stream), C.byref(out)))
+    return Target(out.value, dict(cfg), keep + [t for kv in pages for t in kv] + [table], layers)
 
 
 def dflash_target_destroy(target: Target) -> None:

@@ -169,6 +169,9 @@ SIGNATURES = {
                                          C.POINTER(dflash_kv_pages), P]),
     "dflash_prompt_attention": (C.c_int, [C.POINTER(dflash_attention), C.POINTER(dflash_ragged),
                                           C.POINTER(dflash_heads), C.POINTER(dflash_heads), P]),
+    "dflash_target_create_paged": (C.c_int, [C.POINTER(dflash_target_config), C.POINTER(dflash_target_weights),
+                                             C.POINTER(dflash_kv_pages), P, C.c_int32, C.c_int64, P,
+                                             C.POINTER(C.c_void_p)]),
     "dflash_token_logprobs": (C.c_int, [C.POINTER(dflash_logprobs), P]),
     "dflash_status_check": (C.c_int, [P, P]),
 }

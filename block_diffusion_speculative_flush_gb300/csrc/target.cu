@@ -12,6 +12,11 @@
 // to the cache and to the earlier rows of the call, so a multi-row verify
 // forward and token-by-token decoding compute the same rows.
 //
+// A target may keep its K/V in pages that it shares with others
+// (dflash_target_create_paged): the rows of a forward then go through
+// dflash_kv_append and dflash_paged_attention (a forward at position 0 through
+// dflash_prompt_attention); everything else is the same.
+//
 // It reuses the draft's CUDA-core kernels: the RMSNorm, the split-key
 // attention and its merge (the new rows are the "block" rows, causal among
 // themselves), the residual add, SwiGLU and the row copy for the taps; its
@@ -75,6 +80,22 @@ __global__ void k_target_qkv(const float* __restrict__ qkv, const float2* __rest
     kp[j + half] = kb * cs.x + ka * cs.y;
   }
   for (int j = threadIdx.x; j < d; j += blockDim.x) vp[(int64_t)j * cap] = row[2 * qd + h * d + j];
+}
+
+// Rotate-half RoPE of the q and k columns of fused rows [rows][q | k | v], in
+// place (the paged target hands the row ranges on as they are).
+__global__ void k_target_rope_rows(float* __restrict__ qkv, const float2* __restrict__ rope, int nh, int d) {
+  pdl_trigger();
+  pdl_wait();
+  const int r = blockIdx.x, h = blockIdx.y, half = d / 2;
+  float* row = qkv + (int64_t)r * 3 * nh * d + h * d;  // h < 2 nh: q heads, then k heads
+  const float2* rt = rope + (int64_t)r * half;
+  for (int j = threadIdx.x; j < half; j += blockDim.x) {
+    const float2 cs = rt[j];
+    const float a = row[j], b = row[j + half];
+    row[j] = a * cs.x - b * cs.y;
+    row[j + half] = b * cs.x + a * cs.y;
+  }
 }
 
 // Y[M][N] = X[M][K] . W[N][K]^T for few rows: one warp per output column n,
@@ -269,6 +290,11 @@ struct dflash_target {
   cudaStream_t st = nullptr;
   int32_t* d_err = nullptr;
   DevBuf x, y, qkv, Q, O, tmp, gu, a, part, tables;
+  // paged (table set): one cache per layer, shared with other targets, and this
+  // sequence's pages in it; kv is unused
+  dflash_kv_pages pages[64] = {};
+  const int32_t* table = nullptr;
+  int32_t table_width = 0;
 };
 
 namespace {
@@ -288,8 +314,8 @@ constexpr int kTargetMaxRows = 64;  // rows per internal chunk of a forward
 
 extern "C" {
 
-DFLASH_API int dflash_target_create(const dflash_target_config* cfg, const dflash_target_weights* w, int64_t max_ctx,
-                                    void* stream, dflash_target** out) {
+static int create_target(const dflash_target_config* cfg, const dflash_target_weights* w, const dflash_kv_pages* pages,
+                         const int32_t* table, int32_t table_width, int64_t max_ctx, void* stream, dflash_target** out) {
   if (!cfg || !w || !out || !w->embed || !w->unembed || !w->final_norm || !w->layers)
     return tfail(DFLASH_ERR_INVALID_ARG, "dflash_target_create: null argument");
   const dflash_target_config& c = *cfg;
@@ -313,9 +339,14 @@ DFLASH_API int dflash_target_create(const dflash_target_config* cfg, const dflas
   t->cap = max_ctx;
   const int H = c.hidden, qd = c.n_heads * c.head_dim, I = c.intermediate;
   for (int j = 0; j < c.head_dim / 2; ++j) t->inv_freq.push_back(std::pow((double)c.rope_theta, -2.0 * j / c.head_dim));
+  if (pages) {
+    std::copy(pages, pages + c.n_layers, t->pages);
+    t->table = table;
+    t->table_width = table_width;
+  }
   cudaError_t e = cudaMalloc(&t->d_err, 16);
   if (e == cudaSuccess) e = cudaMemset(t->d_err, 0, 16);
-  if (e == cudaSuccess) e = cudaMalloc(&t->kv, (size_t)2 * c.n_layers * c.n_heads * max_ctx * c.head_dim * 4);
+  if (e == cudaSuccess && !pages) e = cudaMalloc(&t->kv, (size_t)2 * c.n_layers * c.n_heads * max_ctx * c.head_dim * 4);
   for (int l = 0; l < c.n_layers && e == cudaSuccess; ++l) {
     const dflash_target_layer& L = w->layers[l];
     dflash_target::Layer Lw{(const float*)L.n1, (const float*)L.wo, (const float*)L.n2, (const float*)L.wd, nullptr,
@@ -337,6 +368,31 @@ DFLASH_API int dflash_target_create(const dflash_target_config* cfg, const dflas
   }
   *out = t;
   return DFLASH_OK;
+}
+
+DFLASH_API int dflash_target_create(const dflash_target_config* cfg, const dflash_target_weights* w, int64_t max_ctx,
+                                    void* stream, dflash_target** out) {
+  return create_target(cfg, w, nullptr, nullptr, 0, max_ctx, stream, out);
+}
+
+DFLASH_API int dflash_target_create_paged(const dflash_target_config* cfg, const dflash_target_weights* w,
+                                          const dflash_kv_pages* pages, const int32_t* table, int32_t table_width,
+                                          int64_t max_ctx, void* stream, dflash_target** out) {
+  if (!cfg || !pages || !table || table_width <= 0)
+    return tfail(DFLASH_ERR_INVALID_ARG, "dflash_target_create_paged: null argument");
+  if (cfg->n_layers <= 0 || cfg->n_layers > 64) return tfail(DFLASH_ERR_SHAPE, "dflash_target_create_paged: unsupported shape");
+  for (int l = 0; l < cfg->n_layers; ++l) {
+    const dflash_kv_pages& p = pages[l];
+    // an empty append checks the layer's pages
+    const dflash_ragged none{1, 0, 1, 1, table, table, table, table_width, table_width, nullptr};
+    const dflash_heads rows{nullptr, 4096, 4096};
+    if (int rc = dflash_kv_append(&p, &none, &rows, &rows, stream)) return rc;
+    if (p.dtype != DFLASH_DTYPE_F32 || p.n_kv_heads != cfg->n_heads || p.head_dim != cfg->head_dim)
+      return tfail(DFLASH_ERR_SHAPE, "dflash_target_create_paged: pages are fp32 [n_heads][head_dim] of the target");
+    if (max_ctx > (int64_t)table_width * p.page_size || max_ctx > (1 << 30))
+      return tfail(DFLASH_ERR_CAPACITY, "dflash_target_create_paged: max_ctx beyond the table's pages");
+  }
+  return create_target(cfg, w, pages, table, table_width, max_ctx, stream, out);
 }
 
 DFLASH_API int dflash_target_destroy(dflash_target* t) {
@@ -407,6 +463,8 @@ DFLASH_API int dflash_target_forward(dflash_target* t, const int32_t* tokens, in
         const double ang = (double)(F + r) * t->inv_freq[j];
         rope[(size_t)r * (d / 2) + j] = make_float2((float)std::cos(ang), (float)std::sin(ang));
       }
+    const int32_t starts[2] = {0, R}, length = (int32_t)(F + R);
+    const size_t o_st = add(starts, sizeof starts), o_len = add(&length, 4);
     const size_t o_kv = add(&kvp, sizeof kvp), o_cap = add(&capv, 8), o_fr = add(&fr, 8), o_seq = add(&seq, 4),
                  o_map = add(&nomap, sizeof nomap), o_items = add(items.data(), items.size() * sizeof(AttnItem)),
                  o_first = add(&zero, 4), o_cnt = add(&S, 4), o_rope = add(rope.data(), rope.size() * sizeof(float2));
@@ -431,8 +489,37 @@ DFLASH_API int dflash_target_forward(dflash_target* t, const int32_t* tokens, in
     if (e == cudaSuccess) e = t->tmp.ensure((size_t)R * std::max(H, V) * f4, st);
     if (e == cudaSuccess) e = t->gu.ensure((size_t)R * 2 * I * f4, st);
     if (e == cudaSuccess) e = t->a.ensure((size_t)R * I * f4, st);
-    if (e == cudaSuccess) e = t->part.ensure(items.size() * (size_t)R * (d + 4) * f4, st);
+    // the paged target's attention: the rows of the fused product as they are
+    const bool paged = t->table != nullptr;
+    const dflash_ragged batch{1,
+                              R,
+                              R,
+                              length,
+                              (const int32_t*)(tb + o_st),
+                              (const int32_t*)(tb + o_len),
+                              t->table,
+                              t->table_width,
+                              t->table_width,
+                              t->d_err + 1};
+    dflash_attention att{};
+    att.dtype = DFLASH_DTYPE_F32;
+    att.n_q_heads = att.n_kv_heads = nh;
+    att.head_dim = d;
+    att.causal = 1;
+    att.scale = 1.f / std::sqrt((float)d);
+    if (paged) {
+      const int64_t need = dflash_attention_workspace(&att, &batch, t->pages);
+      if (need < 0) return (int)need;
+      att.workspace_bytes = need;
+      if (e == cudaSuccess) e = t->part.ensure((size_t)need + 32, st);
+    } else if (e == cudaSuccess) {
+      e = t->part.ensure(items.size() * (size_t)R * (d + 4) * f4, st);
+    }
     if ((rc = tcheck(e, "target buffers")) != DFLASH_OK) return rc;
+    att.q = dflash_heads{t->qkv.p, 3 * qd, d};
+    att.out = dflash_heads{t->O.p, qd, d};
+    att.workspace = t->part.p;
+    const dflash_heads k_rows{t->qkv.as<float>() + qd, 3 * qd, d}, v_rows{t->qkv.as<float>() + 2 * qd, 3 * qd, d};
     float* X = t->x.as<float>();
     float* Y = t->y.as<float>();
     float* tp = taps ? taps + (size_t)r0 * NT * H : nullptr;
@@ -447,13 +534,22 @@ DFLASH_API int dflash_target_forward(dflash_target* t, const int32_t* tokens, in
       const dflash_target::Layer& L = t->layers[l];
       launch_rmsnorm(DT::F32, true, X, R, nullptr, H, L.n1, Y, H, R, H, R, 0, 0, c.rms_eps, st);
       launch_gemm_rows(Y, H, L.wqkv, H, t->qkv.as<float>(), 3 * qd, R, 3 * qd, H, st);
-      launch_k(k_target_qkv, dim3(R, nh), 64, 0, st, (const float*)t->qkv.as<float>(),
-               (const float2*)(tb + o_rope), nh, d, F, t->cap, l, t->Q.as<float>(), t->kv);
-      ap.layer = l;
-      launch_attention_simt(DT::F32, t->Q.p, (const AttnItem*)(tb + o_items), (int)items.size(), tabs, ap,
-                            t->part.as<float>(), st);
-      launch_attention_combine(DT::F32, t->part.as<float>(), (const int32_t*)(tb + o_first),
-                               (const int32_t*)(tb + o_cnt), 1, ap, nullptr, t->O.p, st);
+      if (paged) {
+        launch_k(k_target_rope_rows, dim3(R, 2 * nh), 64, 0, st, t->qkv.as<float>(), (const float2*)(tb + o_rope), nh, d);
+        if ((rc = dflash_kv_append(&t->pages[l], &batch, &k_rows, &v_rows, st)) != DFLASH_OK) return rc;
+        // rows at the start see nothing but themselves
+        rc = F == 0 ? dflash_prompt_attention(&att, &batch, &k_rows, &v_rows, st)
+                    : dflash_paged_attention(&att, &batch, &t->pages[l], st);
+        if (rc != DFLASH_OK) return rc;
+      } else {
+        launch_k(k_target_qkv, dim3(R, nh), 64, 0, st, (const float*)t->qkv.as<float>(),
+                 (const float2*)(tb + o_rope), nh, d, F, t->cap, l, t->Q.as<float>(), t->kv);
+        ap.layer = l;
+        launch_attention_simt(DT::F32, t->Q.p, (const AttnItem*)(tb + o_items), (int)items.size(), tabs, ap,
+                              t->part.as<float>(), st);
+        launch_attention_combine(DT::F32, t->part.as<float>(), (const int32_t*)(tb + o_first),
+                                 (const int32_t*)(tb + o_cnt), 1, ap, nullptr, t->O.p, st);
+      }
       launch_gemm_rows(t->O.as<float>(), qd, L.wo, qd, t->tmp.as<float>(), H, R, H, qd, st);
       launch_residual(DT::F32, X, t->tmp.as<float>(), H, R, H, st);
       tap(1 + 2 * l);
@@ -525,7 +621,7 @@ DFLASH_API int dflash_target_device_status(dflash_target* t) {
   int32_t e = 0;
   if ((rc = tcheck(cudaMemcpy(&e, t->d_err, 4, cudaMemcpyDeviceToHost), "target status")) != DFLASH_OK) return rc;
   if (e) return tfail(DFLASH_ERR_DEVICE, "target: a token id outside [0, vocab)");
-  return DFLASH_OK;
+  return !t->table ? DFLASH_OK : dflash_status_check(t->d_err + 1, t->st);
 }
 
 }  // extern "C"

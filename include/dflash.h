@@ -612,6 +612,18 @@ DFLASH_API int dflash_paged_attention(const dflash_attention* a, const dflash_ra
 DFLASH_API int dflash_prompt_attention(const dflash_attention* a, const dflash_ragged* batch, const dflash_heads* k,
                                        const dflash_heads* v, void* stream);
 
+/* A target (dflash_target_create) whose K/V lives in pages that several targets
+ * may share: pages is a host array of n_layers caches (fp32, n_kv_heads = the
+ * target's n_heads), table (device [table_width], borrowed) names this
+ * sequence's pages, its own from the first row that it writes; max_ctx <=
+ * table_width * page_size, else DFLASH_ERR_CAPACITY.  The table is read at each
+ * forward, so pages may be entered as the sequence grows.  All other calls take
+ * the target as any other; dflash_target_device_status also reports the
+ * operators' status. */
+DFLASH_API int dflash_target_create_paged(const dflash_target_config* cfg, const dflash_target_weights* w,
+                                          const dflash_kv_pages* pages, const int32_t* table, int32_t table_width,
+                                          int64_t max_ctx, void* stream, dflash_target** out);
+
 /* Log probabilities of given tokens under softmax(logits / temperature), with
  * the distribution's entropy (natural log) and its top entries.  Row r: logits
  * + r * row_stride, vocab entries of fp32 or bf16.

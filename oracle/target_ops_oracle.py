@@ -82,8 +82,11 @@ def append(k_pages, k, starts, lens, table):
 
 def gather(k_pages, lens, table):
     page = k_pages.shape[1]
-    return [torch.stack([k_pages[int(table[b, p // page]), p % page] for p in range(L)]) if L else
-            k_pages.new_zeros((0,) + k_pages.shape[2:]) for b, L in enumerate(lens)]
+    out = []
+    for b, L in enumerate(lens):
+        p = torch.arange(L)
+        out.append(k_pages[table[b].long()[p // page], p % page])
+    return out
 
 
 def logprobs(logits, tokens, top, temperature):

@@ -147,6 +147,15 @@ def test_paged_attention_over_long_caches(dtype, rows, lens):
     check_attention(out, lse, ref_paged(B, True, 0), B.starts[-1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows,hq", [([1, 1, 1], 2), ([20, 9, 1], 4)])
+def test_paged_attention_with_many_key_tiles_per_cta(rows, hq, d):
+    """Enough keys that every CTA works through several tiles and more than one sequence."""
+    B = Batch("bf16", hq, 2, d, 256, rows, [30011, 17, 16384], seed=7, tail=0)
+    out, lse, _, _ = run_paged(B, True, 0)
+    check_attention(out, lse, ref_paged(B, True, 0), B.starts[-1])
+
+
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 50), (False, 20)])
 @pytest.mark.parametrize("heads,rows", [((4, 4), [1]), ((8, 2), [37]), ((6, 2), [1, 0, 200, 129]),

@@ -118,6 +118,28 @@ def test_a_call_that_needs_a_workspace_is_refused_without_one():
         assert D.lib.dflash_paged_attention(C.byref(a), C.byref(b), C.byref(p), None) == INVALID
 
 
+def test_a_paged_target_refuses_bad_pages():
+    cfg = _abi.dflash_target_config(hidden=256, n_heads=4, head_dim=64, intermediate=512, vocab=32, n_layers=1,
+                                    rope_theta=1e6, rms_eps=1e-6)
+    w, out = _abi.dflash_target_weights(embed=16, unembed=16, final_norm=16), C.c_void_p()
+    good = dict(dtype=0, n_kv_heads=4, head_dim=64, page_stride=4096, slot_stride=256, head_stride=64)
+
+    def call(p, table=BASE, width=8, max_ctx=64, config=cfg):
+        return D.lib.dflash_target_create_paged(C.byref(config), C.byref(w), C.byref(p), table, width, max_ctx, None,
+                                                C.byref(out))
+    for bad, code in PAGES:
+        if "dtype" not in bad and "head_dim" not in bad and "n_kv_heads" not in bad:
+            assert call(pages(**{**good, **bad})) == code, bad
+    for bad in (dict(dtype=1, head_dim=64), dict(n_kv_heads=2), dict(head_dim=32)):
+        assert call(pages(**{**good, **bad})) == SHAPE, bad
+    assert call(pages(**good), table=None) == INVALID
+    assert call(pages(**good), width=0) == INVALID
+    assert call(pages(**good), max_ctx=129) == _abi.DFLASH_ERR_CAPACITY
+    assert call(pages(**good)) == INVALID                      # no layer weights: refused as any target's
+    assert D.lib.dflash_target_create_paged(C.byref(cfg), C.byref(w), None, BASE, 8, 64, None, C.byref(out)) == INVALID
+    assert out.value is None
+
+
 def logprobs(**kw):
     f = dict(logits=BASE, row_stride=1000, dtype=0, rows=3, vocab=1000, top=5, temperature=1.0, tokens=BASE,
              logprobs=BASE, entropy=None, top_ids=BASE, top_logprobs=BASE, status=None)
