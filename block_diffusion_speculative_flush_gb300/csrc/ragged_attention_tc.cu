@@ -78,7 +78,8 @@ struct Work {
 template <int D, int NQ>
 struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
-  static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;    // 128 bytes of 32 rows for each softmax warp
+  // 128 bytes of 32 rows for each softmax warp (NQ = 1: in the Q tile it has done with)
+  static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;
   static constexpr int RING = (7 * 32768 - STAGE) / SLOT - 2;  // K/V tiles in flight
   static constexpr int DATA = (RING + 2) * SLOT + STAGE;  // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
@@ -328,7 +329,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
-      mbar_init(&q_empty[s], 1);
+      mbar_init(&q_empty[s], NQ == 2 ? 1 : 4);
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
@@ -648,7 +649,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (!wait(&q_full[q_cnt0 & 1u], q_cnt0 >> 1) || !ring_full(ring)) return;
         issue_s((int)(q_cnt0 & 1u), ring % RING, (int)(s_cnt & 1u));
         umma_commit_warp(&empty[ring % RING]);
-        if (nt == 1) umma_commit_warp(&q_empty[q_cnt0 & 1u]);
         ++q_cnt0;
         ++s_cnt;
       } else {
@@ -674,10 +674,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           // S of the next tile in the stream goes ahead of this tile's product
           if (!last) {
             if (!ring_full(ik)) break;
-            const int qb = (int)((q_cnt0 + 1) & 1u);  // the buffer in use
-            issue_s(qb, sk, (int)(s_cnt & 1u));
+            issue_s((int)((q_cnt0 + 1) & 1u), sk, (int)(s_cnt & 1u));  // the Q buffer in use
             umma_commit_warp(&empty[sk]);
-            if (t + 2 == w.T) umma_commit_warp(&q_empty[qb]);
             ++s_cnt;
           } else if (more) {
             first_s(0, nx.nt0, ik);
@@ -786,7 +784,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     const float sl2 = a.scale * kLog2e;
     uint32_t cnt = 0;          // tiles of this warp's stream so far
     uint32_t it = 0;           // ring entries so far
-    uint32_t q_cnt = 0;        // stretches with tiles of this stream so far
+    uint32_t q_cnt = 0, q_used = 0;  // stretches with tiles of this stream so far; the last one's number
     const int row_i = x * p.tpt + row / G, row_g = row % G;  // this row's token (in the item) and head (in the group)
     const bool teller = NQ == 2 && (warp & 3) == 0 && lane == 0;  // gives tiles back for its stream
     bool ok = true;
@@ -922,6 +920,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           break;
         }
         if (teller && (x == 1 || T > nt_other)) mbar_arrive_relaxed(&empty[(it + 2 * T - 1) % RING]);
+        q_used = q_cnt;
         ++q_cnt;
         fence_after();
       }
@@ -932,28 +931,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       } else if (live) {
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
         if (valid) store_stats<D>(a, p, w, x, row, i, h, m, l);
-        if constexpr (NQ == 1) {
-          // few rows: a row per lane
-#pragma unroll 1
-          for (int c = 0; c < D && T > 0; c += 32) {
-            float v[32];
-            tmem_ld32(tO + c, v);
-            if (valid && w.part >= 0) {
-              uint4* o = reinterpret_cast<uint4*>(part_o<D>(a, p, w.part, row) + c);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) o[j] = *reinterpret_cast<const uint4*>(v + 4 * j);
-            } else if (valid) {
-              uint4* o = reinterpret_cast<uint4*>(row_out(a, w, i, h) + c);
-#pragma unroll
-              for (int j = 0; j < 4; ++j) o[j] = pack8(v + 8 * j, inv);
-            }
-          }
-        } else {
+        {
           // 128 bytes of each row at a time through shared memory, so that a store
           // covers whole lines (a row per lane took five times as long): row r's
           // 16-byte chunk c lies at chunk c ^ (r & 7).
           const uint32_t rows = __ballot_sync(0xffffffffu, valid);
-          uint8_t* st = sS + warp * 4096;
+          uint8_t* st = NQ == 2 ? sS + warp * 4096 : sQ + (q_used & 1u) * SLOT + warp * 4096;
           // where this lane's own row starts, in 16-byte units
           const int64_t own =
               w.part >= 0 ? ((int64_t)w.part * p.ws_rows + x * 128 + row) * (D / 4)
@@ -995,6 +978,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           }
         }
         fence_before();
+      }
+      if (NQ == 1 && T > 0) {
+        fence_proxy_async();  // the next thing into this Q tile comes by TMA
+        __syncwarp();
+        if (lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
       }
       __syncwarp();
       if (lane == 0) mbar_arrive_relaxed(&w_empty[ws]);
@@ -1076,24 +1064,26 @@ __global__ void __launch_bounds__(256) k_ragged_merge(Ragged r, AttnCall a, Plan
         float v[8][C], wq[8];
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          wq[q] = __shfl_sync(0xffffffffu, wt, (q0 + q) & 31);
-          if (q0 + q >= cnt) wq[q] = 0.f;
-#pragma unroll
-          for (int j = 0; j < C; ++j) v[q][j] = 0.f;
-          if (wq[q] != 0.f) {
-            const float* pp = part_o<D>(a, p, slot_of(base + q0 + q), row) + lane * C;
-            if (C == 4) {
-              const float4 t = *reinterpret_cast<const float4*>(pp);
-              v[q][0] = t.x;
-              v[q][1] = t.y;
-              v[q][C - 2] = t.z;
-              v[q][C - 1] = t.w;
-            } else {
-              const float2 t = *reinterpret_cast<const float2*>(pp);
-              v[q][0] = t.x;
-              v[q][1] = t.y;
-            }
+          // (loaded whatever its weight: a load under a condition would be waited
+          // for on the spot)
+          const float* pp = part_o<D>(a, p, slot_of(base + min(q0 + q, cnt - 1)), row) + lane * C;
+          if constexpr (C == 4) {
+            const float4 t = *reinterpret_cast<const float4*>(pp);
+            v[q][0] = t.x;
+            v[q][1] = t.y;
+            v[q][2] = t.z;
+            v[q][3] = t.w;
+          } else {
+            const float2 t = *reinterpret_cast<const float2*>(pp);
+            v[q][0] = t.x;
+            v[q][1] = t.y;
           }
+        }
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          wq[q] = q0 + q < cnt ? __shfl_sync(0xffffffffu, wt, (q0 + q) & 31) : 0.f;
+#pragma unroll
+          for (int j = 0; j < C; ++j) v[q][j] = wq[q] == 0.f ? 0.f : v[q][j];
         }
 #pragma unroll
         for (int q = 0; q < 8; ++q)
