@@ -404,7 +404,7 @@ def dflash_target_create_paged(cfg: dict, weights: dict, pages, table: torch.Ten
     pages = list(pages)
     if len(pages) != cfg["n_layers"]:
         raise ValueError("pages: one (k_pages, v_pages) pair per layer")
-    arr = (_abi.dflash_kv_pages * len(pages))(*[_pages(k, v) for k, v in pages])
+    arr = (_abi.dflash_kv_pages * len(pages))(*[_abi.dflash_kv_pages(*_pages(k, v)) for k, v in pages])
     width = table.numel()
     _int_vector(table, width, "table")
     if max_ctx is None:
@@ -522,15 +522,15 @@ def dflash_target_exactness_probe(target: Target, tokens: torch.Tensor, start: i
 _DTYPES = {torch.float32: DFLASH_DTYPE_F32, torch.bfloat16: DFLASH_DTYPE_BF16}
 
 
-def _stream_of(stream, t: torch.Tensor) -> int:
-    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(t.get_device())
+def _stream_of(stream, device: int) -> int:
+    return stream.cuda_stream if stream is not None else torch._C._cuda_getCurrentRawStream(device)
 
 
 class _on_device:
-    """torch.cuda.device(t.device) for the call, free when that device is current already."""
+    """torch.cuda.device(device) for the call, free when that device is current already."""
 
-    def __init__(self, t: torch.Tensor):
-        self.ctx = None if torch._C._cuda_getDevice() == t.get_device() else torch.cuda.device(t.device)
+    def __init__(self, device: int):
+        self.ctx = None if torch._C._cuda_getDevice() == device else torch.cuda.device(device)
 
     def __enter__(self):
         if self.ctx is not None:
@@ -541,91 +541,88 @@ class _on_device:
             self.ctx.__exit__(*exc)
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
+def _same_device(first: torch.Tensor, *others) -> int:
     dev = first.get_device()
     for t in others:
         if t is not None and t.get_device() != dev:
-            raise ValueError("all tensors of a call live on one device")
+            raise ValueError("all tensors of a call live on one CUDA device")
+    if dev < 0:
+        raise ValueError("expected CUDA tensors")
+    return dev
 
 
-def _heads(t: torch.Tensor, dtype: torch.dtype, what: str) -> _abi.dflash_heads:
-    """[rows, heads, head_dim] with a dense last dimension."""
-    shape, st = t.shape, t.stride()
-    if not t.is_cuda or t.dtype != dtype or len(shape) != 3 or (st[2] != 1 and shape[2] > 1):
+def _heads(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> tuple:
+    """(pointer, row stride, head stride) of [rows, heads, head_dim] with a dense last dimension."""
+    st = t.stride()
+    if t.dtype != dtype or len(shape) != 3 or (st[2] != 1 and shape[2] > 1):
         raise ValueError(f"{what}: a CUDA {dtype} tensor [rows, heads, head_dim] with a dense last dimension")
     # torch may report any stride for a dimension of one entry; the library asks for one a head fits in
     rows, heads, d = shape
-    row = st[0] if rows > 1 else max(st[0], heads * d)
-    return _abi.dflash_heads(t.data_ptr() if rows else None, row, st[1] if heads > 1 else d)
+    return (t.data_ptr() if rows else 0, st[0] if rows > 1 else max(st[0], heads * d), st[1] if heads > 1 else d)
 
 
-def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> _abi.dflash_kv_pages:
-    """[n_pages, page_size, n_kv_heads, head_dim] views of one shape and stride (a permuted
-    [n_pages, n_kv_heads, page_size, head_dim] cache too)."""
+def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> tuple:
+    """The fields of dflash_kv_pages for [n_pages, page_size, n_kv_heads, head_dim] views of one shape and
+    stride (a permuted [n_pages, n_kv_heads, page_size, head_dim] cache too)."""
     shape, st, dtype = k_pages.shape, k_pages.stride(), _DTYPES.get(k_pages.dtype)
-    if not k_pages.is_cuda or dtype is None or len(shape) != 4 or st[3] != 1 or \
-            v_pages.dtype != k_pages.dtype or v_pages.shape != shape or v_pages.stride() != st:
+    if not k_pages.is_cuda or dtype is None or len(shape) != 4 or st[3] != 1 or v_pages.dtype != k_pages.dtype or \
+            v_pages.shape != shape or v_pages.stride() != st:
         raise ValueError("k_pages, v_pages: CUDA fp32 or bf16 [n_pages, page_size, n_kv_heads, head_dim] of one shape "
                          "and stride, with a dense last dimension")
     n, page, heads, d = shape
-    return _abi.dflash_kv_pages(dtype, heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(),
-                                st[0] if n > 1 else max(st[0], d), st[1], st[2] if heads > 1 else d)
+    return (dtype, heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(), st[0] if n > 1 else max(st[0], d), st[1],
+            st[2] if heads > 1 else d)
 
 
 def _int_vector(t: torch.Tensor, n: int | None, what: str) -> int:
-    if not t.is_cuda or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or \
-            (n is not None and t.numel() != n):
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() or (n is not None and t.numel() != n) or \
+            not t.is_cuda:
         raise ValueError(f"{what}: a contiguous CUDA int32 vector" + (f" of {n}" if n is not None else ""))
     return t.data_ptr()
 
 
-def _ragged(starts, lens, table, total: int, max_rows: int, max_len: int, status) -> _abi.dflash_ragged:
-    _int_vector(starts, None, "starts [batch + 1]")
-    batch = starts.numel() - 1
-    if status is not None:
-        _int_vector(status, 1, "status")
-    r = _abi.dflash_ragged(batch, total, max_rows, max_len, starts.data_ptr(), None, None, 0, 0,
-                           None if status is None else status.data_ptr())
-    if lens is not None:
-        r.lens = _int_vector(lens, batch, "lens")
-        if not table.is_cuda or table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != batch or \
-                (table.stride(1) != 1 and table.shape[1] > 1):
-            raise ValueError(f"table: CUDA int32 [{batch}, pages per sequence] with a dense last dimension")
-        r.table, r.table_width = table.data_ptr(), table.shape[1]
-        r.table_stride = table.stride(0) if batch > 1 else max(table.stride(0), table.shape[1])
-    return r
+def _ragged(starts, lens, table, total: int, max_rows: int, max_len: int, status) -> bytes:
+    first = _int_vector(starts, None, "starts [batch + 1]")
+    batch = starts.shape[0] - 1
+    word = 0 if status is None else _int_vector(status, 1, "status")
+    if lens is None:
+        return _abi.PACK_RAGGED(batch, total, max_rows, 0, first, 0, 0, 0, 0, word)
+    shape, st = table.shape, table.stride()
+    if table.dtype != torch.int32 or len(shape) != 2 or shape[0] != batch or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"table: CUDA int32 [{batch}, pages per sequence] with a dense last dimension")
+    return _abi.PACK_RAGGED(batch, total, max_rows, max_len, first, _int_vector(lens, batch, "lens"), table.data_ptr(),
+                            shape[1], st[0] if batch > 1 else max(st[0], shape[1]), word)
 
 
-def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse) -> _abi.dflash_attention:
-    if q.dtype not in _DTYPES:
+def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse, ragged: bytes, pages, workspace,
+               stream) -> tuple:
+    """The packed dflash_attention, and its workspace: the caller's, or one from torch's allocator on the
+    call's stream."""
+    dtype, shape = _DTYPES.get(q.dtype), q.shape
+    if dtype is None:
         raise ValueError("q: fp32 or bf16")
-    qh, oh = _heads(q, q.dtype, "q"), _heads(out, q.dtype, "out")
-    if out.shape != q.shape:
+    if out.shape != shape:
         raise ValueError("out: the shape of q")
-    if lse is not None and (not lse.is_cuda or lse.dtype != torch.float32 or not lse.is_contiguous() or
-                            tuple(lse.shape) != tuple(q.shape[:2])):
+    qh, oh = _heads(q, shape, q.dtype, "q"), _heads(out, shape, q.dtype, "out")
+    rows, heads, d = shape
+    if lse is not None and (lse.dtype != torch.float32 or not lse.is_contiguous() or lse.shape != shape[:2]):
         raise ValueError("lse: contiguous CUDA fp32 [rows, n_q_heads]")
-    d = q.shape[2]
-    return _abi.dflash_attention(_DTYPES[q.dtype], q.shape[1], n_kv_heads, d, int(causal), int(window),
-                                 d ** -0.5 if scale is None else float(scale), qh, oh,
-                                 None if lse is None else lse.data_ptr(), None, 0)
-
-
-def _with_workspace(a, r, pages, workspace, stream, device):
-    """Points a at the caller's workspace, or at one from torch's allocator on the call's stream."""
-    need = lib.dflash_attention_workspace(C.byref(a), C.byref(r), pages)
-    _check(min(need, 0))
-    if workspace is None and need:
+    head = (dtype, heads, n_kv_heads, d, 1 if causal else 0, int(window), d ** -0.5 if scale is None else float(scale),
+            *qh, *oh, 0 if lse is None else lse.data_ptr())
+    if workspace is None:
+        need = lib.dflash_attention_workspace(_abi.PACK_ATTENTION(*head, 0, 0), ragged, pages)
+        if need < 0:
+            _check(need)
+        if need == 0:
+            return _abi.PACK_ATTENTION(*head, 0, 0), None
         if stream is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
         else:
             with torch.cuda.stream(stream):
-                workspace = torch.empty(need, dtype=torch.uint8, device=device)
-    if workspace is not None:
-        if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
-            raise ValueError("workspace: a contiguous CUDA uint8 tensor")
-        a.workspace, a.workspace_bytes = workspace.data_ptr(), workspace.numel()
-    return workspace
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace: a contiguous CUDA uint8 tensor")
+    return _abi.PACK_ATTENTION(*head, workspace.data_ptr(), workspace.numel()), workspace
 
 
 def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
@@ -633,25 +630,28 @@ def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     """New rows k, v [rows, n_kv_heads, head_dim] of a ragged batch into their pages
     [n_pages, page_size, n_kv_heads, head_dim]: sequence b's rows starts[b] .. starts[b + 1] - 1
     become its last positions below lens[b]; table [batch, pages] names its pages."""
+    device = _same_device(k_pages, k, v, v_pages, starts, lens, table, status)
     p = _pages(k_pages, v_pages)
-    if k.shape != v.shape or tuple(k.shape[1:]) != (p.n_kv_heads, p.head_dim):
-        raise ValueError(f"k, v: [rows, {p.n_kv_heads}, {p.head_dim}]")
-    kh, vh = _heads(k, k_pages.dtype, "k"), _heads(v, k_pages.dtype, "v")
-    _same_device(k_pages, k, v, v_pages, starts, lens, table, status)
-    r = _ragged(starts, lens, table, k.shape[0], max(1, k.shape[0]), 1 << 30, status)
-    with _on_device(k_pages):
-        _check(lib.dflash_kv_append(C.byref(p), C.byref(r), C.byref(kh), C.byref(vh),
-                                    _stream_of(stream, k_pages)))
+    shape = k.shape
+    if v.shape != shape or len(shape) != 3 or shape[1] != p[1] or shape[2] != p[2]:
+        raise ValueError(f"k, v: [rows, {p[1]}, {p[2]}]")
+    kh = _abi.PACK_HEADS(*_heads(k, shape, k_pages.dtype, "k"))
+    vh = _abi.PACK_HEADS(*_heads(v, shape, k_pages.dtype, "v"))
+    rows = shape[0]
+    r = _ragged(starts, lens, table, rows, max(1, rows), 1 << 30, status)
+    with _on_device(device):
+        _check(lib.dflash_kv_append(_abi.PACK_PAGES(*p), r, kh, vh, _stream_of(stream, device)))
 
 
 def dflash_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages) -> int:
     """Bytes a dflash_paged_attention call of these tensors and bounds needs."""
+    device = _same_device(q, out, starts, lens, table, k_pages, v_pages)
     p = _pages(k_pages, v_pages)
-    a = _attention(q, out, p.n_kv_heads, True, 0, None, None)
     r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, None)
-    need = lib.dflash_attention_workspace(C.byref(a), C.byref(r), C.byref(p))
-    _check(min(need, 0))
-    return need
+    qh = _heads(q, q.shape, k_pages.dtype, "q")
+    a = _abi.PACK_ATTENTION(p[0], q.shape[1], p[1], p[2], 1, 0, 1.0, *qh, *qh, 0, 0, 0)
+    with _on_device(device):
+        return _check(lib.dflash_attention_workspace(a, r, _abi.PACK_PAGES(*p)))
 
 
 def dflash_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, starts: torch.Tensor,
@@ -662,15 +662,16 @@ def dflash_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torc
     """Attention of each sequence's new rows q [rows, n_q_heads, head_dim] over its pages, which already
     hold them.  max_rows and max_len bound the new rows and the length of every sequence (max_len: None
     takes what the table can hold); scale: None is head_dim ** -0.5."""
+    device = _same_device(q, k_pages, v_pages, starts, lens, table, out, lse, workspace, status)
     p = _pages(k_pages, v_pages)
-    a = _attention(q, out, p.n_kv_heads, causal, window, scale, lse)
-    _same_device(q, k_pages, v_pages, starts, lens, table, out, lse, workspace, status)
     if max_len is None:
-        max_len = min(1 << 30, table.shape[-1] * k_pages.shape[1])
+        max_len = min(1 << 30, table.shape[-1] * p[3])
     r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, status)
-    with _on_device(q):
-        _with_workspace(a, r, C.byref(p), workspace, stream, q.device)
-        _check(lib.dflash_paged_attention(C.byref(a), C.byref(r), C.byref(p), _stream_of(stream, q)))
+    pages = _abi.PACK_PAGES(*p)
+    with _on_device(device):
+        # (keep: the workspace lives until the launches are enqueued; the allocator orders its reuse)
+        a, keep = _attention(q, out, p[1], causal, window, scale, lse, r, pages, workspace, stream)
+        _check(lib.dflash_paged_attention(a, r, pages, _stream_of(stream, device)))
 
 
 def dflash_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, starts: torch.Tensor, out: torch.Tensor,
@@ -678,16 +679,16 @@ def dflash_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, s
                             lse: torch.Tensor | None = None, workspace=None, status=None, stream=None) -> None:
     """Attention of whole packed prompts: sequence b is rows starts[b] .. starts[b + 1] - 1 of
     q [rows, n_q_heads, head_dim] and of k, v [rows, n_kv_heads, head_dim]."""
-    if k.shape != v.shape or k.dim() != 3 or q.dim() != 3 or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    device = _same_device(q, k, v, starts, out, lse, workspace, status)
+    shape, qs = k.shape, q.shape
+    if v.shape != shape or len(shape) != 3 or len(qs) != 3 or shape[0] != qs[0] or shape[2] != qs[2]:
         raise ValueError("k, v: [rows, n_kv_heads, head_dim] with q's rows and head_dim")
-    a = _attention(q, out, k.shape[1], causal, window, scale, lse)
-    kh, vh = _heads(k, q.dtype, "k"), _heads(v, q.dtype, "v")
-    _same_device(q, k, v, starts, out, lse, workspace, status)
-    r = _ragged(starts, None, None, q.shape[0], max_rows, 0, status)
-    with _on_device(q):
-        _with_workspace(a, r, None, workspace, stream, q.device)
-        _check(lib.dflash_prompt_attention(C.byref(a), C.byref(r), C.byref(kh), C.byref(vh),
-                                           _stream_of(stream, q)))
+    kh = _abi.PACK_HEADS(*_heads(k, shape, q.dtype, "k"))
+    vh = _abi.PACK_HEADS(*_heads(v, shape, q.dtype, "v"))
+    r = _ragged(starts, None, None, shape[0], max_rows, 0, status)
+    with _on_device(device):
+        a, keep = _attention(q, out, shape[1], causal, window, scale, lse, r, None, workspace, stream)
+        _check(lib.dflash_prompt_attention(a, r, kh, vh, _stream_of(stream, device)))
 
 
 def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: torch.Tensor,
@@ -696,38 +697,34 @@ def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: 
                           stream=None) -> None:
     """Log probability of tokens[r] (int32, -1: none) under softmax(logits[r] / temperature), the row's
     entropy, and its top entries: top_ids int32 and top_logprobs fp32 [rows, k], k at most 32."""
-    if not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2 or \
-            (logits.stride(1) != 1 and logits.shape[1] > 1):
+    device = _same_device(logits, tokens, logprobs, entropy, top_ids, top_logprobs, status)
+    shape, st, dtype = logits.shape, logits.stride(), _DTYPES.get(logits.dtype)
+    if dtype is None or len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
         raise ValueError("logits: CUDA fp32 or bf16 [rows, vocab] with a dense last dimension")
-    R, V = logits.shape
-    _int_vector(tokens, R, "tokens [rows]")
+    R, V = shape
+    tok = _int_vector(tokens, R, "tokens [rows]")
     for t, what in ((logprobs, "logprobs"), (entropy, "entropy")):
-        if t is not None and (not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or
-                              tuple(t.shape) != (R,)):
+        if t is not None and (t.dtype != torch.float32 or t.dim() != 1 or t.shape[0] != R or not t.is_contiguous()):
             raise ValueError(f"{what}: contiguous CUDA fp32 [rows]")
     if (top_ids is None) != (top_logprobs is None):
         raise ValueError("top_ids and top_logprobs go together")
     top = 0
     if top_ids is not None:
-        if not top_ids.is_cuda or top_ids.dtype != torch.int32 or not top_ids.is_contiguous() or \
-                top_ids.dim() != 2 or top_ids.shape[0] != R or not top_logprobs.is_cuda or \
-                top_logprobs.dtype != torch.float32 or not top_logprobs.is_contiguous() or \
+        if top_ids.dtype != torch.int32 or not top_ids.is_contiguous() or top_ids.dim() != 2 or \
+                top_ids.shape[0] != R or top_logprobs.dtype != torch.float32 or not top_logprobs.is_contiguous() or \
                 top_logprobs.shape != top_ids.shape:
             raise ValueError("top_ids int32 and top_logprobs fp32: contiguous CUDA [rows, k] of one shape")
         top = top_ids.shape[1]
-    if status is not None:
-        _int_vector(status, 1, "status")
-    _same_device(logits, tokens, logprobs, entropy, top_ids, top_logprobs, status)
-    ptr = lambda t: None if t is None else t.data_ptr()
-    a = _abi.dflash_logprobs(logits.data_ptr(), max(logits.stride(0), V) if R <= 1 else logits.stride(0),
-                             _DTYPES[logits.dtype], R, V, top, float(temperature), ptr(tokens), ptr(logprobs),
-                             ptr(entropy), ptr(top_ids), ptr(top_logprobs), ptr(status))
-    with _on_device(logits):
-        _check(lib.dflash_token_logprobs(C.byref(a), _stream_of(stream, logits)))
+    ptr = lambda t: 0 if t is None else t.data_ptr()
+    a = _abi.PACK_LOGPROBS(logits.data_ptr(), st[0] if R > 1 else max(st[0], V), dtype, R, V, top, float(temperature),
+                           tok, logprobs.data_ptr(), ptr(entropy), ptr(top_ids), ptr(top_logprobs),
+                           0 if status is None else _int_vector(status, 1, "status"))
+    with _on_device(device):
+        _check(lib.dflash_token_logprobs(a, _stream_of(stream, device)))
 
 
 def dflash_status_check(status: torch.Tensor, stream=None) -> None:
     """Waits for the stream, clears the operators' status word and raises DFlashError if a bit was set."""
-    _int_vector(status, 1, "status")
-    with _on_device(status):
-        _check(lib.dflash_status_check(status.data_ptr(), _stream_of(stream, status)))
+    word, device = _int_vector(status, 1, "status"), status.get_device()
+    with _on_device(device):
+        _check(lib.dflash_status_check(word, _stream_of(stream, device)))

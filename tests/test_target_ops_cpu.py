@@ -178,6 +178,19 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes():
         D.dflash_status_check(i(1))
 
 
+def test_the_packed_layouts_are_the_structs():
+    for name, struct, n in (("PACK_HEADS", _abi.dflash_heads, 3), ("PACK_PAGES", _abi.dflash_kv_pages, 10),
+                            ("PACK_RAGGED", _abi.dflash_ragged, 10), ("PACK_LOGPROBS", _abi.dflash_logprobs, 13)):
+        values = list(range(1, n + 1))
+        assert getattr(_abi, name)(*values) == bytes(struct(*values))
+    h = _abi.dflash_heads(8, 9, 10)
+    want = bytes(_abi.dflash_attention(1, 2, 3, 4, 5, 6, 7.0, h, h, 14, 15, 16))
+    got = _abi.PACK_ATTENTION(1, 2, 3, 4, 5, 6, 7.0, 8, 9, 10, 8, 9, 10, 14, 15, 16)
+    assert len(got) == len(want) and _abi.dflash_attention.from_buffer_copy(got).workspace_bytes == 16
+    f = _abi.dflash_attention.from_buffer_copy(got)
+    assert (f.dtype, f.window, f.scale, f.q.data, f.out.head_stride, f.lse, f.workspace) == (1, 6, 7.0, 8, 10, 14, 15)
+
+
 def test_oracle_attention_by_hand():
     """Two keys, one query: the weights are the logistic function of the score difference."""
     q = torch.tensor([[[2.0, 0.0]]])
