@@ -8,6 +8,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdio>
+#include <type_traits>
 
 #include "common.cuh"
 #include "dflash.h"
@@ -57,54 +58,248 @@ __global__ void __launch_bounds__(256) k_kv_append(Ragged r, const uint4* __rest
 }
 
 // ---------------------------------------------------------------------------
-// attention on the CUDA cores
+// attention on the CUDA cores (fp32)
 // ---------------------------------------------------------------------------
-constexpr int BK = 64;           // keys per tile
-constexpr int kSimtSplit = 256;  // keys per split (a multiple of BK)
+// Two kernels: k_attn_few for up to 64 packed rows of a sequence and KV head
+// (single tokens, verified blocks, the first rows of a prompt), k_attn_tiles
+// for more.  A row's arithmetic in k_attn_few depends on its own keys only
+// (splits of the key axis start at fixed positions), so a block of tokens and
+// single tokens give the same bits.
+constexpr int kFewRows = 64;   // packed rows that k_attn_few takes
+constexpr int kSplit = 256;    // keys of a split: one per thread of k_attn_few
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
 __device__ __forceinline__ void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 
-// The CUDA-core attention works on 16 RM packed rows (token, head of the KV
-// head's group) per CTA and 64 keys per step; threads are 16 x 16, each with
-// RM rows x 4 keys of the scores and RM rows x DP / 16 columns of the output.
-// A row's arithmetic depends on its own keys only (tiles and splits start at
-// fixed positions), so a block of tokens and single tokens give the same bits.
-template <int DP, int RM>
-__global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, KVView kv, int splits) {
-  constexpr int BR = 16 * RM, LQ = DP + 4, LP = BK + 4;
+// Where position pos of sequence b (whose packed rows start at `start`) lies in
+// K and V, in elements; false: on a page that does not exist.
+__device__ __forceinline__ bool kv_at(const Ragged& r, const KVView& kv, int b, int start, int pos, int64_t& ko, int64_t& vo) {
+  if (!kv.paged) {
+    ko = (int64_t)(start + pos) * kv.k_slot;
+    vo = (int64_t)(start + pos) * kv.v_slot;
+    return true;
+  }
+  const int pg = r.table[(int64_t)b * r.table_stride + (pos >> kv.page_shift)], sl = pos & ((1 << kv.page_shift) - 1);
+  ko = pg * kv.page + sl * kv.k_slot;
+  vo = pg * kv.page + sl * kv.v_slot;
+  return pg >= 0 && pg < kv.n_pages;
+}
+
+// 16 packed rows (token, head of the group) x 256 keys per CTA.  Scores: a key
+// per thread, its K row straight from memory, the 16 rows of q broadcast from
+// shared memory (a row at a time through shared-memory tiles, as many rows
+// want it, left this kernel waiting for each 64 keys in turn: 20 us for three
+// blocks of 8 over 900 tokens, 11 now).  Then a softmax of two rows per warp,
+// and O = P V with the keys dealt to the warps.
+template <int DP>
+__global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView kv, int splits) {
+  constexpr int BR = 16, LQ = DP + 4, LP = BR + 4, LS = kSplit + 4;
+  constexpr int COLS = DP / 4, SLICES = 32 / (COLS < 32 ? COLS : 32);  // column groups; key slices within a warp
   extern __shared__ float4 smem4[];
-  float* sQ = reinterpret_cast<float*>(smem4);
-  float* sK = sQ + BR * LQ;
-  float* sV = sK + BK * LQ;
-  float* sP = sV + BK * DP;
+  float* sQ = reinterpret_cast<float*>(smem4);  // [16][LQ]
+  float* sS = sQ + BR * LQ;                     // [16][LS] scores; later the warps' sums [8][16][DP]
+  float* sO = sS;
+  float* sP = sS + (8 * BR * DP > BR * LS ? 8 * BR * DP : BR * LS);  // [256][LP]
+  int64_t* sV = reinterpret_cast<int64_t*>(sP + kSplit * LP);        // [256] where the key's V lies, -1: nowhere
+  float2* sML = reinterpret_cast<float2*>(sV + kSplit);              // [16]
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.z, kvh = blockIdx.y, split = blockIdx.x % splits, rt = blockIdx.x / splits;
+  const int b = blockIdx.z, kvh = blockIdx.y, split = blockIdx.x % splits, r0 = blockIdx.x / splits * BR;
   const Seq s = load_seq(r, b);
   if (!s.ok) {
     if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
     return;
   }
-  const int G = a.Hq / a.Hkv, R = s.n * G, r0 = rt * BR;
+  const int G = a.Hq / a.Hkv, R = s.n * G;
   if (r0 >= R) return;
-  const int ctx = s.len - s.n;
-  if (splits > 1 && split * kSimtSplit >= s.len && split > 0) return;  // the merge does not look at it either
-  const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
-  // keys that any of the tile's rows sees, within this split
+  if (split > 0 && split * kSplit >= s.len) return;  // the merge does not look at it either
+  const int ctx = s.len - s.n, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // keys that any of the rows sees, within this split
   const int p_first = ctx + r0 / G, p_last = ctx + (min(r0 + BR, R) - 1) / G;
-  int k_lo = vis_lo(p_first, a.window), k_hi = vis_hi(p_last, s.len, a.causal);
-  if (splits > 1) {
-    k_lo = max(k_lo, split * kSimtSplit);
-    k_hi = min(k_hi, (split + 1) * kSimtSplit);
+  const int k0 = split * kSplit;
+  const int k_lo = max(k0, vis_lo(p_first, a.window));
+  const int k_hi = min(k0 + kSplit, vis_hi(p_last, s.len, a.causal));
+  const int pos = k0 + tid;
+  int64_t ko = 0, vo = 0;
+  bool here = pos >= k_lo && pos < k_hi, exists = false;
+  if (here) {
+    exists = kv_at(r, kv, b, s.start, pos, ko, vo);
+    if (!exists) flag_status(r.status, DFLASH_STATUS_PAGE);
   }
-  const float* Q = reinterpret_cast<const float*>(a.q);
-  for (int e = tid; e < BR * (DP / 4); e += 256) {
+  for (int e = tid; e < BR * COLS; e += 256) {
+    const int rr = e / COLS, c = e % COLS * 4;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (r0 + rr < R && c < a.d) {
+      const int i = (r0 + rr) / G, g = (r0 + rr) % G;
+      x = load4(reinterpret_cast<const float*>(a.q) + (int64_t)(s.start + i) * a.q_row + (int64_t)(kvh * G + g) * a.q_head + c);
+    }
+    *reinterpret_cast<float4*>(sQ + rr * LQ + c) = x;
+  }
+  sV[tid] = here && exists ? vo : -1;
+  __syncthreads();
+  // ---- scores
+  float sc[BR];
+#pragma unroll
+  for (int i = 0; i < BR; ++i) sc[i] = 0.f;
+  if (here && exists) {
+    const float* kp = reinterpret_cast<const float*>(kv.k) + ko + kvh * kv.k_head;
+#pragma unroll 8
+    for (int c = 0; c < a.d; c += 4) {
+      const float4 k4 = load4(kp + c);
+#pragma unroll
+      for (int i = 0; i < BR; ++i) {
+        const float4 q4 = *reinterpret_cast<const float4*>(sQ + i * LQ + c);
+        sc[i] = fmaf(q4.x, k4.x, sc[i]);
+        sc[i] = fmaf(q4.y, k4.y, sc[i]);
+        sc[i] = fmaf(q4.z, k4.z, sc[i]);
+        sc[i] = fmaf(q4.w, k4.w, sc[i]);
+      }
+    }
+  }
+  const float sl2 = a.scale * 1.4426950408889634f;
+  bool hidden = false;
+#pragma unroll
+  for (int i = 0; i < BR; ++i) {
+    const int p = ctx + (r0 + i) / G;
+    const bool see = here && r0 + i < R && pos >= vis_lo(p, a.window) && pos < vis_hi(p, s.len, a.causal);
+    hidden |= !see;
+    sS[i * LS + tid] = see ? sc[i] * sl2 : -INFINITY;
+  }
+  const bool guard = __syncthreads_or(hidden && here);
+  // ---- softmax: warp w has rows 2 w and 2 w + 1
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int i = 2 * warp + u;
+    float x[kSplit / 32], m = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int j = 0; j < kSplit / 32; ++j) {
+      x[j] = sS[i * LS + lane + 32 * j];
+      m = fmaxf(m, x[j]);
+    }
+    m = warp_max(m);
+    const float mref = m == -INFINITY ? 0.f : m;
+#pragma unroll
+    for (int j = 0; j < kSplit / 32; ++j) {
+      const float e = exp2f(x[j] - mref);
+      l += e;
+      sP[(lane + 32 * j) * LP + i] = e;
+    }
+    l = warp_sum(l);
+    if (lane == 0) sML[i] = make_float2(m, l);
+  }
+  __syncthreads();
+  // ---- O: warp w takes keys 32 w .. 32 w + 31 (its lanes' slices every SLICES-th)
+  const int col = lane % COLS * 4, slice = lane / COLS;
+  float acc[BR][4];
+#pragma unroll
+  for (int i = 0; i < BR; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+  const float* vp = reinterpret_cast<const float*>(kv.v) + kvh * kv.v_head + col;
+  const bool in = col < a.d;
+#pragma unroll 4
+  for (int t = slice; t < 32; t += SLICES) {
+    const int key = warp * 32 + t;
+    const int64_t o = sV[key];
+    float4 v4 = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (o >= 0 && in) v4 = load4(vp + o);
+#pragma unroll
+    for (int i4 = 0; i4 < BR; i4 += 4) {
+      const float4 p4 = *reinterpret_cast<const float4*>(sP + key * LP + i4);
+      const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        // a row's hidden keys have P = 0, and V may be anything there
+        if (!guard || pv[i] != 0.f) {
+          acc[i4 + i][0] = fmaf(pv[i], v4.x, acc[i4 + i][0]);
+          acc[i4 + i][1] = fmaf(pv[i], v4.y, acc[i4 + i][1]);
+          acc[i4 + i][2] = fmaf(pv[i], v4.z, acc[i4 + i][2]);
+          acc[i4 + i][3] = fmaf(pv[i], v4.w, acc[i4 + i][3]);
+        }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < BR; ++i) {
+#pragma unroll
+    for (int o = COLS; o < 32; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[i][j] += __shfl_xor_sync(0xffffffffu, acc[i][j], o);
+    if (slice == 0) *reinterpret_cast<float4*>(sO + (warp * BR + i) * DP + col) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+  }
+  __syncthreads();
+  for (int e = tid; e < BR * COLS; e += 256) {
+    const int i = e / COLS, c = e % COLS * 4;
+    if (r0 + i >= R) continue;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < 8; ++w) {
+      const float4 t = *reinterpret_cast<const float4*>(sO + (w * BR + i) * DP + c);
+      o.x += t.x;
+      o.y += t.y;
+      o.z += t.z;
+      o.w += t.w;
+    }
+    const float2 ml = sML[i];
+    const int tok = s.start + (r0 + i) / G, h = kvh * G + (r0 + i) % G;
+    if (splits > 1) {
+      float* w = a.ws + (((int64_t)tok * a.Hq + h) * splits + split) * (a.d + 4);
+      if (c == 0) *reinterpret_cast<float4*>(w) = make_float4(ml.x, ml.y, 0.f, 0.f);
+      if (c < a.d) store4(w + 4 + c, o);
+      continue;
+    }
+    const float inv = ml.x == -INFINITY ? 0.f : 1.f / ml.y;
+    if (c < a.d)
+      store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + c,
+             make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+    if (a.lse && c == 0)
+      a.lse[(int64_t)tok * a.Hq + h] = ml.x == -INFINITY ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+  }
+}
+
+// 32 packed rows per CTA, 64 keys per step and group of 8 x 16 threads, each
+// with 4 rows x 4 keys of the scores and 4 rows x DP / 16 columns of the output:
+// 12 shared-memory passes for 64 products a thread.  Bound by the fp32 pipe, but
+// a group's step (load, scores, softmax, product) is one chain of about 9000
+// cycles: NG groups take every NG-th tile of keys, and their (m, l, O) meet in
+// shared memory.  The tiles with the most keys start first.
+constexpr int BK = 64;
+template <int DP> struct TileCfg {
+  static constexpr int NG = DP == 64 ? 4 : 2, BR = 32, LQ = DP + 4, LP = BK + 4;
+  static constexpr int GROUP = BK * LQ + BK * DP + BR * LP;  // floats of a group's K, V and P
+  static constexpr size_t SMEM = sizeof(float) * (BR * LQ + NG * GROUP);
+};
+template <int DP>
+__global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, AttnCall a, KVView kv) {
+  using C = TileCfg<DP>;
+  constexpr int RM = 4, BR = C::BR, LQ = C::LQ, LP = C::LP, NG = C::NG;
+  extern __shared__ float4 smem4[];
+  const int group = threadIdx.x >> 7, tid = threadIdx.x & 127;
+  float* sQ = reinterpret_cast<float*>(smem4);
+  float* sK = sQ + BR * LQ + group * C::GROUP;
+  float* sV = sK + BK * LQ;
+  float* sP = sV + BK * DP;
+  auto group_sync = [&] { asm volatile("bar.sync %0, 128;" ::"r"(group + 1) : "memory"); };
+  pdl_trigger();
+  pdl_wait();
+  // grid: (tile from the sequence's end, sequence, KV head), the head fastest
+  const int kvh = (int)(blockIdx.x % a.Hkv), b = (int)(blockIdx.x / a.Hkv % r.batch);
+  const int back = (int)(blockIdx.x / a.Hkv / r.batch);
+  const Seq s = load_seq(r, b);
+  if (!s.ok) {
+    if (threadIdx.x == 0 && back == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+    return;
+  }
+  const int G = a.Hq / a.Hkv, R = s.n * G, r0 = ((R + BR - 1) / BR - 1 - back) * BR;
+  if (r0 < 0) return;
+  const int ctx = s.len - s.n, tx = tid & 15, ty = tid >> 4;
+  const int p_first = ctx + r0 / G, p_last = ctx + (min(r0 + BR, R) - 1) / G;
+  const int k_lo = vis_lo(p_first, a.window), k_hi = vis_hi(p_last, s.len, a.causal);
+  for (int e = threadIdx.x; e < BR * (DP / 4); e += NG * 128) {
     const int rr = e / (DP / 4), c = e % (DP / 4) * 4;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + rr < R && c < a.d) {
       const int i = (r0 + rr) / G, g = (r0 + rr) % G;
-      x = load4(Q + (int64_t)(s.start + i) * a.q_row + (int64_t)(kvh * G + g) * a.q_head + c);
+      x = load4(reinterpret_cast<const float*>(a.q) + (int64_t)(s.start + i) * a.q_row + (int64_t)(kvh * G + g) * a.q_head + c);
     }
     *reinterpret_cast<float4*>(sQ + rr * LQ + c) = x;
   }
@@ -113,8 +308,8 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
 #pragma unroll
   for (int i = 0; i < RM; ++i) {
     const int rr = r0 + ty * RM + i, p = ctx + rr / G;
-    lo[i] = max(vis_lo(p, a.window), k_lo);
-    hi[i] = rr < R ? min(vis_hi(p, s.len, a.causal), k_hi) : 0;
+    lo[i] = vis_lo(p, a.window);
+    hi[i] = rr < R ? vis_hi(p, s.len, a.causal) : 0;
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
@@ -123,34 +318,26 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
   const float sl2 = a.scale * 1.4426950408889634f;
   const float* Kb = reinterpret_cast<const float*>(kv.k) + kvh * kv.k_head;
   const float* Vb = reinterpret_cast<const float*>(kv.v) + kvh * kv.v_head;
-  for (int t0 = k_lo / BK * BK; t0 < k_hi; t0 += BK) {
-    __syncthreads();
-    for (int e = tid; e < BK * (DP / 4); e += 256) {
+  __syncthreads();  // Q is there
+  for (int t0 = (k_lo / BK + group) * BK; t0 < k_hi; t0 += NG * BK) {
+    group_sync();
+#pragma unroll 4
+    for (int e = tid; e < BK * (DP / 4); e += 128) {
       const int kk = e / (DP / 4), c = e % (DP / 4) * 4, pos = t0 + kk;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
       if (pos < k_hi && c < a.d) {
         int64_t ko, vo;
-        bool ok = true;
-        if (kv.paged) {
-          const int pg = r.table[(int64_t)b * r.table_stride + (pos >> kv.page_shift)];
-          const int sl = pos & ((1 << kv.page_shift) - 1);
-          ok = pg >= 0 && pg < kv.n_pages;
-          if (!ok && c == 0) flag_status(r.status, DFLASH_STATUS_PAGE);
-          ko = pg * kv.page + sl * kv.k_slot;
-          vo = pg * kv.page + sl * kv.v_slot;
-        } else {
-          ko = (int64_t)(s.start + pos) * kv.k_slot;
-          vo = (int64_t)(s.start + pos) * kv.v_slot;
-        }
-        if (ok) {
+        if (kv_at(r, kv, b, s.start, pos, ko, vo)) {
           x = load4(Kb + ko + c);
           y = load4(Vb + vo + c);
+        } else if (c == 0) {
+          flag_status(r.status, DFLASH_STATUS_PAGE);
         }
       }
       *reinterpret_cast<float4*>(sK + kk * LQ + c) = x;
       *reinterpret_cast<float4*>(sV + kk * DP + c) = y;
     }
-    __syncthreads();
+    group_sync();
     float sc[RM][4];
 #pragma unroll
     for (int i = 0; i < RM; ++i)
@@ -204,52 +391,77 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
     }
     // P rows of this thread's row group come from the same half warp
     __syncwarp();
-    // A key that a row does not see has P = 0; its V may still be NaN or
-    // infinite, so tiles with hidden keys skip those products.
-    const bool guard = __any_sync(0xffffffffu, masked);
-    for (int kk = 0; kk < BK; kk += 4) {
-      float4 p4[RM];
+    auto product = [&](auto guarded) {
+#pragma unroll 2
+      for (int kk = 0; kk < BK; kk += 4) {
+        float4 p4[RM];
 #pragma unroll
-      for (int i = 0; i < RM; ++i) p4[i] = *reinterpret_cast<const float4*>(sP + (ty * RM + i) * LP + kk);
+        for (int i = 0; i < RM; ++i) p4[i] = *reinterpret_cast<const float4*>(sP + (ty * RM + i) * LP + kk);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 4; ++u) {
 #pragma unroll
-        for (int cc = 0; cc < DP / 64; ++cc) {
-          const float4 v4 = *reinterpret_cast<const float4*>(sV + (kk + u) * DP + cc * 64 + tx * 4);
+          for (int cc = 0; cc < DP / 64; ++cc) {
+            const float4 v4 = *reinterpret_cast<const float4*>(sV + (kk + u) * DP + cc * 64 + tx * 4);
 #pragma unroll
-          for (int i = 0; i < RM; ++i) {
-            const float pv = u == 0 ? p4[i].x : u == 1 ? p4[i].y : u == 2 ? p4[i].z : p4[i].w;
-            float* o = acc[i] + cc * 4;
-            if (!guard || pv != 0.f) {
-              o[0] = fmaf(pv, v4.x, o[0]);
-              o[1] = fmaf(pv, v4.y, o[1]);
-              o[2] = fmaf(pv, v4.z, o[2]);
-              o[3] = fmaf(pv, v4.w, o[3]);
+            for (int i = 0; i < RM; ++i) {
+              const float pv = u == 0 ? p4[i].x : u == 1 ? p4[i].y : u == 2 ? p4[i].z : p4[i].w;
+              float* o = acc[i] + cc * 4;
+              if (!decltype(guarded)::value || pv != 0.f) {
+                o[0] = fmaf(pv, v4.x, o[0]);
+                o[1] = fmaf(pv, v4.y, o[1]);
+                o[2] = fmaf(pv, v4.z, o[2]);
+                o[3] = fmaf(pv, v4.w, o[3]);
+              }
             }
           }
         }
       }
-    }
+    };
+    // A key that a row does not see has P = 0; its V may still be NaN or
+    // infinite, so tiles with hidden keys skip those products.
+    if (__any_sync(0xffffffffu, masked)) product(std::true_type());
+    else product(std::false_type());
   }
 #pragma unroll
-  for (int i = 0; i < RM; ++i) {
-    float ls = l[i];
+  for (int i = 0; i < RM; ++i)
 #pragma unroll
-    for (int o = 8; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+    for (int o = 8; o > 0; o >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], o);
+  // ---- the groups' parts meet in group order: (m, l) and O of groups 1.. in their K and V
+  __syncthreads();
+  if (group > 0) {
+#pragma unroll
+    for (int i = 0; i < RM; ++i) {
+      const int rr = ty * RM + i;
+      if (tx == 0) *reinterpret_cast<float2*>(sK + 2 * rr) = make_float2(m[i], l[i]);
+#pragma unroll
+      for (int cc = 0; cc < DP / 64; ++cc) store4(sV + rr * DP + cc * 64 + tx * 4, *reinterpret_cast<const float4*>(acc[i] + cc * 4));
+    }
+  }
+  __syncthreads();
+  if (group > 0) return;
+#pragma unroll
+  for (int i = 0; i < RM; ++i) {
     const int rr = r0 + ty * RM + i;
     if (rr >= R) continue;
-    const int tok = s.start + rr / G, h = kvh * G + rr % G;
-    if (splits > 1) {
-      float* w = a.ws + (((int64_t)tok * a.Hq + h) * splits + split) * (a.d + 4);
-      if (tx == 0) *reinterpret_cast<float4*>(w) = make_float4(m[i], ls, 0.f, 0.f);
 #pragma unroll
-      for (int cc = 0; cc < DP / 64; ++cc)
-        if (cc * 64 + tx * 4 < a.d)
-          *reinterpret_cast<float4*>(w + 4 + cc * 64 + tx * 4) =
-              make_float4(acc[i][cc * 4], acc[i][cc * 4 + 1], acc[i][cc * 4 + 2], acc[i][cc * 4 + 3]);
-      continue;
+    for (int g = 1; g < NG; ++g) {
+      const float2 ml = *reinterpret_cast<const float2*>(sK + g * C::GROUP + 2 * (ty * RM + i));
+      if (ml.x == -INFINITY) continue;
+      const float mn = fmaxf(m[i], ml.x), f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn), e = exp2f(ml.x - mn);
+      m[i] = mn;
+      l[i] = l[i] * f + ml.y * e;
+#pragma unroll
+      for (int cc = 0; cc < DP / 64; ++cc) {
+        const float4 v = load4(sV + g * C::GROUP + (ty * RM + i) * DP + cc * 64 + tx * 4);
+        float* o = acc[i] + cc * 4;
+        o[0] = o[0] * f + v.x * e;
+        o[1] = o[1] * f + v.y * e;
+        o[2] = o[2] * f + v.z * e;
+        o[3] = o[3] * f + v.w * e;
+      }
     }
-    const float inv = m[i] == -INFINITY ? 0.f : 1.f / ls;
+    const int tok = s.start + rr / G, h = kvh * G + rr % G;
+    const float inv = m[i] == -INFINITY ? 0.f : 1.f / l[i];
     float* o = reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
 #pragma unroll
     for (int cc = 0; cc < DP / 64; ++cc)
@@ -257,7 +469,7 @@ __global__ void __launch_bounds__(256) k_attn_simt_ragged(Ragged r, AttnCall a, 
         store4(o + cc * 64 + tx * 4, make_float4(acc[i][cc * 4] * inv, acc[i][cc * 4 + 1] * inv,
                                                  acc[i][cc * 4 + 2] * inv, acc[i][cc * 4 + 3] * inv));
     if (a.lse && tx == 0)
-      a.lse[(int64_t)tok * a.Hq + h] = m[i] == -INFINITY ? -INFINITY : (m[i] + log2f(ls)) * 0.6931471805599453f;
+      a.lse[(int64_t)tok * a.Hq + h] = m[i] == -INFINITY ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
   }
 }
 
@@ -273,7 +485,7 @@ __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, i
   if (b >= r.batch) return;
   const Seq s = load_seq(r, b);
   if (!s.ok || tok < s.start || tok >= s.start + s.n) return;
-  const int ns = max(1, min(splits, (s.len + kSimtSplit - 1) / kSimtSplit));
+  const int ns = max(1, min(splits, (s.len + kSplit - 1) / kSplit));
   const float* p = a.ws + w * splits * (a.d + 4);
   float M = -INFINITY;
   for (int j = lane; j < ns; j += 32) M = fmaxf(M, p[(int64_t)j * (a.d + 4)]);
@@ -281,18 +493,18 @@ __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, i
   const float mref = M == -INFINITY ? 0.f : M;
   float L = 0.f;
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int col = 4 * lane < a.d ? 4 * lane : 0;
+#pragma unroll 4
   for (int j = 0; j < ns; ++j) {
     const float* q = p + (int64_t)j * (a.d + 4);
-    if (q[0] == -INFINITY) continue;
-    const float f = exp2f(q[0] - mref);
-    L += q[1] * f;
-    if (4 * lane < a.d) {
-      const float4 v = *reinterpret_cast<const float4*>(q + 4 + 4 * lane);
-      acc.x = fmaf(f, v.x, acc.x);
-      acc.y = fmaf(f, v.y, acc.y);
-      acc.z = fmaf(f, v.z, acc.z);
-      acc.w = fmaf(f, v.w, acc.w);
-    }
+    const float2 ml = *reinterpret_cast<const float2*>(q);
+    const float4 v = load4(q + 4 + col);  // (zeros where the split saw no key)
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
+    L = fmaf(f, ml.y, L);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
   }
   const float inv = M == -INFINITY ? 0.f : 1.f / L;
   if (4 * lane < a.d)
@@ -301,31 +513,36 @@ __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, i
   if (a.lse && lane == 0) a.lse[w] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
 }
 
-// Splits of the key axis: only where one row tile holds a sequence's rows
-// (single tokens and verified blocks), where the length is what work there is.
-int simt_splits(const Ragged& r, const AttnCall& a) {
-  const int64_t rows = (int64_t)r.max_rows * (a.Hq / a.Hkv);
-  if (!r.lens || rows > 64) return 1;
-  return (r.max_len + kSimtSplit - 1) / kSimtSplit;
-}
+bool few_rows(const Ragged& r, const AttnCall& a) { return (int64_t)r.max_rows * (a.Hq / a.Hkv) <= kFewRows; }
+int simt_splits(const Ragged& r, const AttnCall& a) { return few_rows(r, a) ? (r.max_len + kSplit - 1) / kSplit : 1; }
 
-template <int DP, int RM>
-cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
-  constexpr int BR = 16 * RM;
-  constexpr size_t smem = sizeof(float) * (BR * (DP + 4) + BK * (DP + 4) + BK * DP + BR * (BK + 4));
-  static bool attr[64] = {};
+template <typename K>
+cudaError_t allow_smem(K kernel, size_t smem, bool (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(k_attn_simt_ragged<DP, RM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    if (dev < 64) attr[dev] = true;
+  if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess && dev < 64) done[dev] = true;
+  return e;
+}
+
+template <int DP>
+cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
+  const int64_t rows = (int64_t)r.max_rows * (a.Hq / a.Hkv);
+  if (!few_rows(r, a)) {
+    using C = TileCfg<DP>;
+    static bool done[64] = {};
+    if (cudaError_t e = allow_smem(k_attn_tiles<DP>, C::SMEM, done)) return e;
+    const int64_t tiles = (rows + C::BR - 1) / C::BR;
+    return launch_k(k_attn_tiles<DP>, (unsigned)(tiles * r.batch * a.Hkv), C::NG * 128, C::SMEM, st, r, a, kv);
   }
+  constexpr size_t area = 8 * 16 * DP > 16 * (kSplit + 4) ? 8 * 16 * DP : 16 * (kSplit + 4);
+  constexpr size_t smem = sizeof(float) * (16 * (DP + 4) + area + kSplit * 20) + kSplit * 8 + 16 * 8;
+  static bool done[64] = {};
+  if (cudaError_t e = allow_smem(k_attn_few<DP>, smem, done)) return e;
   const int splits = simt_splits(r, a);
-  const int64_t tiles = ((int64_t)r.max_rows * (a.Hq / a.Hkv) + BR - 1) / BR;
-  e = launch_k(k_attn_simt_ragged<DP, RM>, dim3((unsigned)(tiles * splits), a.Hkv, r.batch), 256, smem, st, r, a,
-               kv, splits);
+  cudaError_t e = launch_k(k_attn_few<DP>, dim3((unsigned)((rows + 15) / 16 * splits), a.Hkv, r.batch), 256, smem, st, r,
+                           a, kv, splits);
   if (e != cudaSuccess || splits == 1) return e;
   return launch_k(k_attn_simt_merge, (unsigned)(((int64_t)r.total * a.Hq + 7) / 8), 256, 0, st, r, a, splits);
 }
@@ -338,9 +555,7 @@ int64_t attn_simt_workspace(const Ragged& r, const AttnCall& a) {
 }
 
 cudaError_t launch_attn_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {
-  const bool few = (int64_t)r.max_rows * (a.Hq / a.Hkv) <= 16;
-  if (a.d <= 64) return few ? launch_simt<64, 1>(r, a, kv, st) : launch_simt<64, 4>(r, a, kv, st);
-  return few ? launch_simt<128, 1>(r, a, kv, st) : launch_simt<128, 4>(r, a, kv, st);
+  return a.d <= 64 ? launch_simt<64>(r, a, kv, st) : launch_simt<128>(r, a, kv, st);
 }
 
 namespace {
@@ -448,6 +663,9 @@ int64_t workspace_of(const dflash_attention* a, const Ragged& r) {
 int run_attention(const char* call, const dflash_attention* a, const Ragged& r, const KVView& kv, cudaStream_t st) {
   if (r.total == 0) return DFLASH_OK;
   if ((int64_t)r.total * a->n_q_heads > INT32_MAX) return rfail(DFLASH_ERR_SHAPE, call, "total_rows x n_q_heads above 2^31 - 1");
+  const int64_t rows = (int64_t)r.max_rows * (a->n_q_heads / a->n_kv_heads);
+  if (a->dtype == DFLASH_DTYPE_F32 && (rows + 31) / 32 * r.batch > INT32_MAX / a->n_kv_heads)
+    return rfail(DFLASH_ERR_SHAPE, call, "max_rows x batch x n_q_heads / 32 above 2^31 - 1");
   const AttnCall c = make_call(a);
   const int64_t need = workspace_of(a, r);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need || (uintptr_t)a->workspace % 32))

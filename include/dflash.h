@@ -561,7 +561,8 @@ typedef struct dflash_kv_pages {
 typedef struct dflash_ragged {
   int32_t batch;          /* 1..32768 */
   int32_t total_rows;     /* rows of the packed arrays, 0..2^30 */
-  int32_t max_rows;       /* bound on n_b, 1..2^24 (work is laid out for it: keep it tight) */
+  int32_t max_rows;       /* bound on n_b, 1..2^24 (work is laid out for it: keep it tight; fp32 attention:
+                             max_rows x batch x n_q_heads below 2^36) */
   int32_t max_len;        /* paged: bound on lens[b], 1..2^30 (keep it tight) */
   const int32_t* starts;  /* device [batch + 1], non-decreasing */
   const int32_t* lens;    /* paged: device [batch], cached tokens with the new ones */
