@@ -1344,7 +1344,8 @@ cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const
   CUtensorMap mq, mk, mv;
   {
     const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)r.total};
-    const cuuint64_t strides[2] = {(cuuint64_t)a.q_head * 2, (cuuint64_t)a.q_row * 2};
+    // (the stride of a dimension of one entry is never used, but may not be 0)
+    const cuuint64_t strides[2] = {std::max<cuuint64_t>(a.q_head * 2, 16), (cuuint64_t)a.q_row * 2};
     const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)h.p.tpt};
     if (cudaError_t e = encode(&mq, a.q, 3, dims, strides, box)) return e;
   }
@@ -1352,7 +1353,8 @@ cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const
     const cuuint64_t slot = (cuuint64_t)(i ? kv.v_slot : kv.k_slot) * 2, head = (cuuint64_t)(i ? kv.v_head : kv.k_head) * 2;
     const cuuint64_t dims[4] = {(cuuint64_t)D, kv.paged ? (cuuint64_t)1 << kv.page_shift : (cuuint64_t)kv.packed_rows,
                                 (cuuint64_t)a.Hkv, kv.paged ? (cuuint64_t)kv.n_pages : 1};
-    const cuuint64_t strides[3] = {slot, head, kv.paged ? (cuuint64_t)kv.page * 2 : slot};
+    const cuuint64_t strides[3] = {slot, std::max<cuuint64_t>(head, 16),
+                                   kv.paged ? std::max<cuuint64_t>(kv.page * 2, 16) : slot};
     const cuuint32_t box[4] = {64, (cuuint32_t)(kv.paged ? std::min(1 << kv.page_shift, KT) : KT), 1, 1};
     if (cudaError_t e = encode(i ? &mv : &mk, i ? kv.v : kv.k, 4, dims, strides, box)) return e;
   }

@@ -513,7 +513,9 @@ DFLASH_API int dflash_target_exactness_probe(dflash_target* t, const int32_t* to
  * verified block over it, and the log probabilities that answer a request.
  * They work on caller-owned device buffers, need no model or session, allocate
  * nothing and may be captured into a CUDA graph: lengths and tables are read
- * on the device at every replay, the host gives bounds on them.
+ * on the device at every replay, the host gives bounds on them.  The current
+ * device is the one that the buffers and the stream belong to (the Python
+ * binding makes it so).
  *
  * Sequence b of a ragged batch owns rows starts[b] .. starts[b + 1] - 1 of the
  * packed arrays: its n_b new tokens, the last n_b of its length.  Row i of them

@@ -212,6 +212,109 @@ def test_hidden_keys_never_reach_a_row(dtype, bits):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,lens,hq", [([16], [3000], 4), ([1, 5], [900, 2000], 8), ([200, 90], [900, 700], 4),
+                                          ([3] * 20, [1000 + 13 * b for b in range(20)], 8)])
+def test_hidden_values_that_are_not_finite_in_every_layout_of_the_work(dtype, rows, lens, hq):
+    """A window of 100 and K and V that are not finite outside it and behind the block's first row, in calls
+    that run as a cluster, as ranges and as whole items: what a row does not see never reaches it."""
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=3)
+    kp, vp = B.appended()
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        for p in list(range(0, L - n - 100)) + ([L - 1] if n > 1 else []):
+            pg, sl = int(B.table[b, p // 16]), p % 16
+            vp[pg, sl, :, p % 64], kp[pg, sl, :, (p + 1) % 64] = (math.nan, math.inf)[p % 2], (math.inf, math.nan)[p % 2]
+    B.kp, B.vp = kp, vp
+    ref = O.attention(B.q[:B.starts[-1]], O.gather(kp.nan_to_num(0, 0, 0), lens, B.table),
+                      O.gather(vp.nan_to_num(0, 0, 0), lens, B.table), B.starts, lens, True, 100, 0.125, dtype == "bf16")
+    out, lse, _, _ = run_paged(B, True, 100, append=False)
+    for b, n in enumerate(rows):   # the last row of a block of several sees the last key: not finite
+        sl = slice(B.starts[b], B.starts[b + 1] - (1 if n > 1 else 0))
+        check_attention(out[sl], lse[sl], tuple(x[sl] for x in ref), sl.stop - sl.start)
+        if n > 1:
+            assert not bool(torch.isfinite(out[B.starts[b + 1] - 1]).all())
+
+
+@pytest.mark.parametrize("dtype,hq,hkv", [("bf16", 24, 1), ("bf16", 128, 1), ("bf16", 100, 2), ("f32", 24, 1)])
+@pytest.mark.parametrize("rows,lens", [([1, 2], [200, 150]), ([7, 30], [77, 300])])
+def test_wide_groups(dtype, hq, hkv, rows, lens):
+    B = Batch(dtype, hq, hkv, 64, 32, rows, lens, seed=hq)
+    out, lse, _, _ = run_paged(B, True, 0)
+    check_attention(out, lse, ref_paged(B, True, 0), B.starts[-1])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_pages_beyond_two_to_the_31_elements(dtype):
+    """Pages whose offsets pass 32 bits in elements."""
+    D = lib()
+    hkv, d, page, n_pages = 8, 128, 1024, 2100           # 2.2e9 elements each of K and V
+    kp = torch.empty((n_pages, page, hkv, d), dtype=DT[dtype], device="cuda")
+    vp = torch.empty_like(kp)
+    g = torch.Generator().manual_seed(0)
+    rows, lens, ids = [3, 1], [1500, 700], [[2099, 2090], [2080, 0]]
+    table, starts = torch.tensor(ids, dtype=torch.int32), starts_of(rows)
+    seq = [[torch.randn((L, hkv, d), generator=g).to(DT[dtype]) for L in lens] for _ in range(2)]
+    for b, L in enumerate(lens):
+        for j in range((L + page - 1) // page):
+            m = min(page, L - j * page)
+            kp[ids[b][j], :m], vp[ids[b][j], :m] = (x[b][j * page:j * page + m].cuda() for x in seq)
+    new = [torch.cat([x[b][L - n:] for b, (n, L) in enumerate(zip(rows, lens))]).cuda() for x in seq]
+    for b, (n, L) in enumerate(zip(rows, lens)):          # the new rows come back through the append
+        kp[ids[b][(L - 1) // page], (L - n) % page:(L - 1) % page + 1] = 0
+    q = torch.randn((4, 16, d), generator=g).to(DT[dtype])
+    out, lse = torch.empty((4, 16, d), dtype=DT[dtype], device="cuda"), torch.empty((4, 16), device="cuda")
+    args = (i32(starts), i32(lens), table.cuda())
+    D.dflash_kv_append(*new, kp, vp, *args)
+    D.dflash_paged_attention(q.cuda(), kp, vp, *args, out, max_rows=3, lse=lse)
+    ref = O.attention(q, *seq, starts, lens, True, 0, d ** -0.5, dtype == "bf16")
+    check_attention(out, lse, ref, 4)
+
+
+def test_tensors_the_library_cannot_take_are_refused():
+    D = lib()
+    q = torch.zeros((4, 4, 64), device="cuda")
+    kv = torch.zeros((4, 2, 64), device="cuda")
+    out, st = torch.zeros_like(q), i32([0, 4])
+    ok = lambda **k: D.dflash_prompt_attention(k.get("q", q), k.get("k", kv), k.get("v", kv), st, k.get("out", out), 4)
+    ok()
+    wide = torch.zeros((4, 4, 65), device="cuda")
+    for bad in (dict(q=wide[..., 1:]), dict(out=wide[..., :64]), dict(k=kv[:1].expand(4, 2, 64)),
+                dict(q=q.transpose(0, 2).contiguous().transpose(0, 2)), dict(out=q)):
+        with pytest.raises((ValueError, D.DFlashError)):
+            ok(**bad)
+    with pytest.raises(ValueError):
+        ok(k=kv.bfloat16(), v=kv.bfloat16())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_two_graphs_replayed_at_once(dtype):
+    """Two captured calls (without a call before the capture) on two streams, each with its own workspace."""
+    D = lib()
+    Bs = [Batch(dtype, 8, 2, 128, 16, [6, 1], [2500 + 100 * i, 90], seed=i, tail=0) for i in range(2)]
+    refs = [ref_paged(B, True, 0) for B in Bs]
+    state, graphs = [], []
+    for B in Bs:
+        kp, vp = (x.cuda() for x in B.appended())
+        q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), B.table.cuda()
+        o, l = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+        need = D.dflash_attention_workspace(q, o, st, ln, tb, 6, 2700, kp, vp)
+        ws = torch.empty(max(need, 32), dtype=torch.uint8, device="cuda")
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            D.dflash_paged_attention(q, kp, vp, st, ln, tb, o, 6, max_len=2700, lse=l, workspace=ws)
+        state.append((kp, vp, q, st, ln, tb, o, l, ws))
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in Bs]
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for x, r in zip(state, refs):
+        check_attention(x[6], x[7], r, 7)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
 def test_one_token_at_a_time_agrees_with_the_block(dtype):
     """The verified block's rows and the same tokens one by one."""
     B = Batch(dtype, 8, 2, 128, 16, [8], [300], seed=9, tail=0)
