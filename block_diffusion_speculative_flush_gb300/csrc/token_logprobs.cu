@@ -217,18 +217,9 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     st.t += tf.x + tf.y;
   };
   int side = 0;
-  // the lanes' keys (0: none) into the buffer, past its end into the warp's list
-  auto append = [&](uint64_t key) {
-    const uint32_t m = __ballot_sync(0xffffffffu, key != 0);
-    if (!m) return;
-    const int cnt = __popc(m);
-    int pos = 0;
-    if (lane == 0) pos = (int)atomicAdd(&s_n[side], (uint32_t)cnt);
-    const int base = __shfl_sync(0xffffffffu, pos, 0);
-    pos = base + __popc(m & ((1u << lane) - 1u));
-    if (key && pos < CAP) s_key[side][pos] = key;
-    if (base + cnt <= CAP) return;
-    uint32_t todo = __ballot_sync(0xffffffffu, pos >= CAP && key > kth);
+  // the lanes' keys (0: none) into the warp's list
+  auto insert = [&](uint64_t key) {
+    uint32_t todo = __ballot_sync(0xffffffffu, key > kth);
     while (todo) {
       const uint64_t k2 = __shfl_sync(0xffffffffu, key, __ffs(todo) - 1);
       todo &= todo - 1;
@@ -239,9 +230,28 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     }
     if (kth && lane == 0) atomicMax(&s_tau, (uint32_t)(kth >> 32));
   };
+  // The elements of a batch that reach tau, into the buffer; bit i of the result:
+  // element i found it full.
+  auto append = [&](const uint4* cur, int base, float tau) {
+    uint32_t full = 0;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int v = base + u * TH + tid;
+      float e[E];
+      Elems<T>::get(cur[u], e);
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        if (e[i] >= tau && v < v1) {
+          const uint32_t pos = atomicAdd(&s_n[side], 1u);
+          if (pos < CAP) s_key[side][pos] = order_key(e[i], head + v * E + i);
+          else full |= 1u << (u * E + i);
+        }
+    }
+    return full;
+  };
   // The batches of the lanes in `hits`, four at a time through shared memory:
   // the whole warp looks at one, an element a lane.
-  auto scan = [&](uint32_t hits, int base, float tau, const uint4* cur) {
+  auto look = [&](uint32_t hits, const uint4* cur, int base, auto each) {
     while (hits) {
       const int q = __popc(hits & ((1u << lane) - 1u));
       if (((hits >> lane) & 1u) && q < H) {
@@ -255,9 +265,35 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
         hits &= hits - 1;
         const int v = base + (lane / E) * TH + warp * 32 + src;
         const float e = lane < N ? to_f<T>(reinterpret_cast<const T*>(s_stage[warp][h])[lane]) : 0.f;
-        append(lane < N && v < v1 && e >= tau ? order_key(e, head + v * E + lane % E) : 0ull);
+        each(src, lane < N && v < v1, e, head + v * E + lane % E);
       }
       __syncwarp();
+    }
+  };
+  auto candidates = [&](const uint4* cur, int base, float hi, float tau) {
+    if constexpr (E == 4) {
+      // 16 elements a lane: each lane offers its own.  What does not fit goes to the warps' lists
+      const uint32_t full = append(cur, base, tau), hits = __ballot_sync(0xffffffffu, full != 0);
+      if (hits)
+        look(hits, cur, base, [&](int src, bool in, float e, int id) {
+          const uint32_t bits = __shfl_sync(0xffffffffu, full, src);
+          insert(in && ((bits >> lane) & 1u) ? order_key(e, id) : 0ull);
+        });
+    } else {
+      // 32 elements a lane: unrolled as above they would not leave registers
+      // enough for the sums (97 -> 187 us for 2047 rows)
+      look(__ballot_sync(0xffffffffu, hi >= tau), cur, base, [&](int, bool in, float e, int id) {
+        const bool yes = in && e >= tau;
+        const uint32_t m = __ballot_sync(0xffffffffu, yes);
+        if (!m) return;
+        int pos = 0;
+        if (lane == 0) pos = (int)atomicAdd(&s_n[side], (uint32_t)__popc(m));
+        const int first = __shfl_sync(0xffffffffu, pos, 0);
+        pos = first + __popc(m & ((1u << lane) - 1u));
+        const uint64_t key = yes ? order_key(e, id) : 0ull;
+        if (yes && pos < CAP) s_key[side][pos] = key;
+        if (first + __popc(m) > CAP) insert(pos >= CAP ? key : 0ull);
+      });
     }
   };
   // Ranks the round's keys; the best K go to dst in order (their count is the
@@ -337,8 +373,9 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       }
       if (K > 0) {
         const float tau = float_of_order(*(volatile uint32_t*)&s_tau);
-        const uint32_t hits = __ballot_sync(0xffffffffu, hi >= tau);
-        if (hits) scan(hits, base, tau, cur);
+        if (__any_sync(0xffffffffu, hi >= tau)) {
+          candidates(cur, base, hi, tau);
+        }
         if (++batch == refresh) {
           refresh *= 2;
           rank_round(s_key[side ^ 1]);
@@ -356,7 +393,15 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       const bool in = lane < cnt;
       const float e[2] = {in ? to_f<T>(x[id]) : -INFINITY, -INFINITY};
       add(std::integral_constant<int, 2>(), e, e[0] >= -INFINITY ? e[0] : -INFINITY, true);
-      if (K > 0) append(in ? order_key(e[0], id) : 0ull);
+      if (K > 0) {
+        uint64_t left = 0;
+        if (in && e[0] >= float_of_order(*(volatile uint32_t*)&s_tau)) {
+          const uint32_t pos = atomicAdd(&s_n[side], 1u);
+          if (pos < CAP) s_key[side][pos] = order_key(e[0], id);
+          else left = order_key(e[0], id);
+        }
+        if (__any_sync(0xffffffffu, left != 0)) insert(left);
+      }
     }
   }
 
@@ -374,11 +419,21 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     if (rank == 0) {
-      // every CTA has ceil(K / cluster) entries that reach the smallest of these
-      // CTAs' entries of that place: K at least do
-      uint32_t t = 0xffffffffu;
-      if (lane < cluster) t = (uint32_t)(*cl.map_shared_rank(&s_out[(K + cluster - 1) / cluster - (K > 0)], lane) >> 32);
-      t = __reduce_min_sync(0xffffffffu, t);
+      // The first ceil(K / cluster) entries of every CTA, at most 32: K of them
+      // at least, and the K-th largest is a threshold that K entries reach.
+      uint32_t t = 0;
+      if (K > 0) {
+        const int r = (K + cluster - 1) / cluster;
+        uint32_t v = 0;
+        if (lane < cluster * r) v = (uint32_t)(*cl.map_shared_rank(&s_out[lane / cluster], lane % cluster) >> 32);
+        int above = 0;
+#pragma unroll 8
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t o = __shfl_sync(0xffffffffu, v, j);
+          above += o > v || (o == v && j < lane);
+        }
+        t = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, above == K - 1)) - 1);
+      }
       uint64_t kk[2] = {0, 0};
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
