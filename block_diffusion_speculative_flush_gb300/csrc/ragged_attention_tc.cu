@@ -91,6 +91,10 @@ struct Cfg {
   static constexpr int RING = (7 * 32768 - STAGE) / SLOT - 2;  // K/V tiles in flight
   static constexpr int DATA = (RING + 2) * SLOT + STAGE;  // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
+  // NQ = 2: registers of the softmax warps and of the other four; the launch's
+  // 168 for all spilled 100 bytes in the key loop (452 -> 424 us for the packed
+  // prompts of 1 to 8192 tokens).  8 x 200 + 4 x 104 = 12 x 168.
+  static constexpr int R_SOFTMAX = 200, R_REST = 104;
   static constexpr size_t SMEM = DATA + 768;  // + barriers and descriptors
 };
 
@@ -140,6 +144,8 @@ __device__ __forceinline__ bool mbar_wait_short(uint64_t* bar, uint32_t parity, 
     if (mbar_try_wait(bar, parity)) return true;
   return mbar_wait(bar, parity, abort_flag);
 }
+template <int R> __device__ __forceinline__ void regs_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R)); }
+template <int R> __device__ __forceinline__ void regs_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R)); }
 // Arrival that publishes no memory (the tensor-memory fence in front of it
 // orders what it hands over): unlike the default it does not wait for this
 // thread's earlier stores, 300 cycles a key tile where P is handed over.
@@ -388,6 +394,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   };
 
   if (warp >= SW) {
+  if constexpr (NQ == 2) regs_dec<C::R_REST>();
   if (warp == SW + 3) {
     // ---- scheduler
     r.starts = after_wait(r.starts);
@@ -816,6 +823,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   }
   } else {
     // ---- softmax: one thread per row
+    if constexpr (NQ == 2) regs_inc<C::R_SOFTMAX>();
     const int x = warp >> 2, row = tid & 127;
     const uint32_t lrow = (uint32_t)((warp & 3) * 32) << 16, tO = tmem + lrow + O_COL + x * D;
     const float sl2 = a.scale * kLog2e;
@@ -878,10 +886,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           float s[128];
           fence_after();
           tmem_ld128(tmem + lrow + sb * 128, s);
-          if (hi_min < kt + KT) {  // keys that some row does not see
+          if (hi_min < kt + KT) {  // keys that some row does not see, as a bit each
             const int h0 = hi - kt;
 #pragma unroll
-            for (int j = 0; j < 128; ++j) s[j] = j < h0 ? s[j] : -INFINITY;
+            for (int c = 0; c < 128; c += 32) {
+              const int n = min(max(h0 - c, 0), 32);
+              const uint32_t keep = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j) s[c + j] = (keep >> j) & 1u ? s[c + j] : -INFINITY;
+            }
           }
           if (lo_max > kt) {
             const int l0 = lo - kt;
