@@ -532,6 +532,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     bool ok = true;
     const int page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
     const int boxes = KT / page_rows;
+    // a copy per lane (the box of a page, one of its 128-byte halves), so that a
+    // tile goes out in one instruction whatever the page size
+    const int box = lane & (boxes - 1), half = lane / boxes;
+    const bool issuer = half < NB;
     auto ring_wait = [&](uint32_t i) {
       return i < (uint32_t)RING ||
              __all_sync(0xffffffffu, mbar_wait(&empty[i % RING], (i / RING - 1) & 1u, abort_flag));
@@ -563,8 +567,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       const int32_t* tab = kv.paged ? r.table + (int64_t)w.b * r.table_stride : nullptr;
       // page of this lane's box of a tile; lanes past the sequence load nothing
       auto page_of = [&](int t) {
-        const int pos = (w.t0 + t) * KT + lane * page_rows;
-        return kv.paged && t < T && lane < boxes && pos < w.len ? tab[pos >> kv.page_shift] : -1;
+        const int pos = (w.t0 + t) * KT + box * page_rows;
+        return kv.paged && t < T && issuer && pos < w.len ? tab[pos >> kv.page_shift] : -1;
       };
       int pg = page_of(0);  // on its way while Q is asked for
       if (NQ == 1) {
@@ -577,13 +581,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       for (int t = 0; t < T && ok; ++t) {
         const int kt = (w.t0 + t) * KT;
         const int next = page_of(t + 1);
-        const bool mine = kv.paged ? lane < boxes && kt + lane * page_rows < w.len : lane == 0;
+        const bool mine = issuer && (!kv.paged || kt + box * page_rows < w.len);
         if (kv.paged && mine && (pg < 0 || pg >= kv.n_pages)) {
           flag_status(r.status, DFLASH_STATUS_PAGE);
           pg = kv.n_pages;  // just outside the map: zeros arrive
         }
-        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * 128 * NB;
-        for (int half = 0; half < 2 && ok; ++half, ++it) {
+        const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * 128;
+        for (int is_v = 0; is_v < 2 && ok; ++is_v, ++it) {
           const int st = it % RING;
           if (!ring_wait(it)) {
             ok = false;
@@ -592,14 +596,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           if (lane == 0) mbar_expect_tx(&full[st], bytes);
           __syncwarp();
           if (mine) {
-            const CUtensorMap* m = half ? &mv : &mk;
-            uint8_t* dst = sR + st * SLOT + lane * page_rows * 128;
-            for (int c = 0; c < NB; ++c) {
-              if (kv.paged)
-                tma_load_4d(dst + c * (SLOT / NB), m, &full[st], 64 * c, kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
-              else
-                tma_load_4d(dst + c * (SLOT / NB), m, &full[st], 64 * c, w.start + kt, w.kvh, 0);
-            }
+            const CUtensorMap* m = is_v ? &mv : &mk;
+            uint8_t* dst = sR + st * SLOT + half * (SLOT / NB) + box * page_rows * 128;
+            if (kv.paged) tma_load_4d(dst, m, &full[st], 64 * half, kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
+            else tma_load_4d(dst, m, &full[st], 64 * half, w.start + kt, w.kvh, 0);
           }
         }
         pg = next;
