@@ -6,6 +6,7 @@
 // over the keys j that row i sees, with the running maximum m and sum l of an
 // online softmax (fp32, in the exp2 domain), one pass over K and V.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdio>
 #include <type_traits>
@@ -517,7 +518,7 @@ bool few_rows(const Ragged& r, const AttnCall& a) { return (int64_t)r.max_rows *
 int simt_splits(const Ragged& r, const AttnCall& a) { return few_rows(r, a) ? (r.max_len + kSplit - 1) / kSplit : 1; }
 
 template <typename K>
-cudaError_t allow_smem(K kernel, size_t smem, bool (&done)[64]) {
+cudaError_t allow_smem(K kernel, size_t smem, std::atomic<bool> (&done)[64]) {
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
@@ -531,14 +532,14 @@ cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cu
   const int64_t rows = (int64_t)r.max_rows * (a.Hq / a.Hkv);
   if (!few_rows(r, a)) {
     using C = TileCfg<DP>;
-    static bool done[64] = {};
+    static std::atomic<bool> done[64];
     if (cudaError_t e = allow_smem(k_attn_tiles<DP>, C::SMEM, done)) return e;
     const int64_t tiles = (rows + C::BR - 1) / C::BR;
     return launch_k(k_attn_tiles<DP>, (unsigned)(tiles * r.batch * a.Hkv), C::NG * 128, C::SMEM, st, r, a, kv);
   }
   constexpr size_t area = 8 * 16 * DP > 16 * (kSplit + 4) ? 8 * 16 * DP : 16 * (kSplit + 4);
   constexpr size_t smem = sizeof(float) * (16 * (DP + 4) + area + kSplit * 20) + kSplit * 8 + 16 * 8;
-  static bool done[64] = {};
+  static std::atomic<bool> done[64];
   if (cudaError_t e = allow_smem(k_attn_few<DP>, smem, done)) return e;
   const int splits = simt_splits(r, a);
   cudaError_t e = launch_k(k_attn_few<DP>, dim3((unsigned)((rows + 15) / 16 * splits), a.Hkv, r.batch), 256, smem, st, r,
@@ -643,9 +644,10 @@ int check_attention(const char* call, const dflash_attention* a, bool pointers, 
 }
 
 Ragged make_ragged(const dflash_ragged* b, const dflash_kv_pages* pages) {
-  int64_t max_len = b->max_rows;
+  const int32_t max_rows = std::min(b->max_rows, std::max(b->total_rows, 1));
+  int64_t max_len = max_rows;
   if (pages) max_len = std::min<int64_t>(b->max_len, (int64_t)b->table_width * pages->page_size);
-  return Ragged{b->batch, b->total_rows, std::min(b->max_rows, std::max(b->total_rows, 1)), (int32_t)max_len, b->starts,
+  return Ragged{b->batch, b->total_rows, max_rows, (int32_t)max_len, b->starts,
                 pages ? b->lens : nullptr, pages ? b->table : nullptr, b->table_stride, b->status};
 }
 AttnCall make_call(const dflash_attention* a) {

@@ -38,6 +38,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
@@ -70,6 +71,8 @@ struct Plan {
   int32_t min_tiles_log2;  // ranges: log2 of the key tiles a CTA gets at least
   int32_t ws_rows;      // rows of a partial
   int32_t slots;        // partials there is room for
+  int32_t max_items;    // items of one KV head, and key tiles of all items (ranges), that there can be
+  int32_t max_units;
 };
 
 // One stretch of key tiles [t0, t0 + max(nt)) of one item.
@@ -79,7 +82,7 @@ struct Work {
   int32_t nt[2];         // key tiles of each 128-row tile
   int32_t part;          // partial slot, or -1: the whole item
   int32_t clean_lo, clean_hi;  // keys that every row sees
-  int32_t bad;           // set by the fixer: a hidden key's V is not finite
+  int32_t bad;           // set by the fixer, a bit per 128-row tile: a hidden key's V is not finite
   int32_t done;
 };
 
@@ -173,9 +176,15 @@ __device__ __forceinline__ int items_reaching(const Seq& s, int c, const Plan& p
 // ranges: a sequence's key tiles [first, first + count), taken for each of its items
 __device__ __forceinline__ int tile_first(const Seq& s, int window) { return vis_lo(s.len - s.n, window) / KT; }
 __device__ __forceinline__ int tile_count(const Seq& s, int window) { return cdiv(s.len, KT) - tile_first(s, window); }
-// (the host takes ranges only where the sum of these fits 31 bits)
-__device__ __forceinline__ int units_of(const Seq& s, const Plan& p, const AttnCall& a) {
-  return items_of(s, p) * a.Hkv * (s.ok && s.n > 0 ? tile_count(s, a.window) : 0);
+__device__ __forceinline__ int64_t units_of(const Seq& s, const Plan& p, const AttnCall& a) {
+  return s.ok && s.n > 0 ? (int64_t)items_of(s, p) * a.Hkv * tile_count(s, a.window) : 0;
+}
+// The sum of the lanes' counts, or -1 where it is above what the host laid the
+// work out for: sequences that overlap (starts that decrease somewhere).
+__device__ __forceinline__ int sum_up_to(int64_t v, int most) {
+  const unsigned c = (unsigned)min(v, (int64_t)INT32_MAX);
+  const int64_t sum = ((int64_t)__reduce_add_sync(0xffffffffu, c >> 16) << 16) + __reduce_add_sync(0xffffffffu, c & 0xffffu);
+  return sum > most ? -1 : (int)sum;
 }
 // The units' even split over the CTAs that take part: range c starts at start(c).
 struct Ranges {
@@ -230,14 +239,14 @@ template <int D>
 __device__ __forceinline__ float2* part_ml(const AttnCall& a, const Plan& p, int slot, int row) {
   return reinterpret_cast<float2*>(a.ws + (int64_t)p.slots * p.ws_rows * D) + (int64_t)slot * p.ws_rows + row;
 }
-// (m, l) of a partial (row r of tile x), or the log-sum-exp of token i, head h
+// (m, l) of a partial (row r of tile x), or the log-sum-exp of packed row tok, head h
 template <int D>
-__device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, const Work& w, int x, int r, int i, int h,
+__device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, int part, int x, int r, int tok, int h,
                                             float m, float l) {
-  if (w.part >= 0) {
-    *part_ml<D>(a, p, w.part, x * 128 + r) = make_float2(m, l);
+  if (part >= 0) {
+    *part_ml<D>(a, p, part, x * 128 + r) = make_float2(m, l);
   } else if (a.lse) {
-    a.lse[(int64_t)(w.start + i) * a.Hq + h] =
+    a.lse[(int64_t)tok * a.Hq + h] =
         m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
   }
 }
@@ -309,7 +318,7 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
     const bool cluster = p.mode == kModeCluster;
     if (lane == 0) {
       if (cluster) c_ml[rr] = make_float2(m, l);
-      else store_stats<D>(a, p, w, x, rr, i, h, m, l);
+      else store_stats<D>(a, p, w.part, x, rr, w.start + i, h, m, l);
     }
     if (w.part >= 0) {
       float* o = (cluster ? c_o + rr * (D + 4) : part_o<D>(a, p, w.part, x * 128 + rr)) + lane * C;
@@ -442,9 +451,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     } else if (p.mode == kModeItems) {
       // items whose keys reach tile c: counted over the batch
       auto count = [&](int c) {
-        int s = 0;
+        int64_t s = 0;
         for (int b = lane; b < r.batch; b += 32) s += items_reaching(seq_at(b), c, p, a.causal);
-        return (int)__reduce_add_sync(0xffffffffu, (unsigned)s);
+        return sum_up_to(s, p.max_items);
       };
       int max_t = 0;
       for (int b = lane; b < r.batch; b += 32) {
@@ -453,7 +462,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (s.ok && s.n > 0) max_t = max(max_t, cdiv(s.len, KT));
       }
       max_t = __reduce_max_sync(0xffffffffu, max_t);
-      const int pairs = count(1), total = pairs * a.Hkv, per_group = pairs * p.hgroup;
+      const int found = count(1), pairs = max(found, 0), total = pairs * a.Hkv, per_group = pairs * p.hgroup;
+      if (found < 0 && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
       for (int j = 0; ok && j < total; j += grid) {
         const int idx = j + (((j / grid) & 1) ? grid - 1 - cta : cta);
         if (idx >= total) continue;
@@ -489,13 +499,17 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         }
       }
     } else {
-      int units = 0;
+      int64_t sum = 0;
       for (int b = lane; b < r.batch; b += 32) {
         const Seq s = seq_at(b);
         if (!s.ok && cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
-        units += units_of(s, p, a);
+        sum += units_of(s, p, a);
       }
-      units = (int)__reduce_add_sync(0xffffffffu, (unsigned)units);
+      int units = sum_up_to(sum, p.max_units);
+      if (units < 0) {
+        if (cta == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+        units = 0;
+      }
       const Ranges rg(units, p, grid);
       int u = cta < rg.n ? rg.start(cta) : units;
       const int u1 = cta < rg.n ? rg.start(cta + 1) : units;
@@ -505,7 +519,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         const int b = base + lane;
         Seq s{0, 0, 0, false};
         if (b < r.batch) s = seq_at(b);
-        const int mine_u = units_of(s, p, a), incl = warp_scan_i(mine_u, lane);
+        const int mine_u = (int)units_of(s, p, a), incl = warp_scan_i(mine_u, lane);
         const int chunk_end = before + __shfl_sync(0xffffffffu, incl, 31);
         while (u < u1 && u < chunk_end && ok) {
           const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
@@ -804,7 +818,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
                 found |= (q.z & 0x7f807f80u) + 0x00800080u;
                 found |= (q.w & 0x7f807f80u) + 0x00800080u;
               }
-            if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0) && lane == 0) works[ws].bad = 1;
+            // (only for the tiles that take this product: their warps all look
+            // behind it, a tile that has ended already might see it in some)
+            if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0) && lane == 0)
+              works[ws].bad |= (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0);
           }
           fence_proxy_async();
           __syncwarp();
@@ -979,9 +996,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         fence_after();
       }
       it += 2 * max(T, nt_other);
-      // ---- epilogue: O and (m, l) of the rows
-      if (T > 0 && *(volatile const int32_t*)&w.bad) {
+      // ---- epilogue: O and (m, l) of the rows.  The descriptor goes back in front
+      // of the stores: behind them the arrival, a release, would wait for them.
+      const int part = w.part, tok = w.start + i;
+      const bool bad = T > 0 && ((*(volatile const int32_t*)&w.bad >> x) & 1);
+      auto give_back = [&] {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[ws]);
+      };
+      if (!bad) give_back();
+      if (bad) {
         redo_rows<D>(r, a, kv, p, w, x, warp & 3, c_o, c_ml);  // rows in turn over all four warps
+        give_back();
       } else if (live) {
         const float inv = m == -INFINITY ? 0.f : 1.f / l;
         if (NQ == 1 && p.mode == kModeCluster) {
@@ -999,7 +1025,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           }
           if (valid) c_ml[row] = make_float2(T > 0 ? m : -INFINITY, l);
         } else {
-          if (valid) store_stats<D>(a, p, w, x, row, i, h, m, l);
+          if (valid) store_stats<D>(a, p, part, x, row, tok, h, m, l);
           // 128 bytes of each row at a time through shared memory, so that a store
           // covers whole lines (a row per lane took five times as long): row r's
           // 16-byte chunk c lies at chunk c ^ (r & 7).
@@ -1007,9 +1033,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           uint8_t* st = NQ == 2 ? sS + warp * 4096 : sQ + (q_used & 1u) * SLOT + warp * 4096;
           // where this lane's own row starts, in 16-byte units
           const int64_t own =
-              w.part >= 0 ? ((int64_t)w.part * p.ws_rows + x * 128 + row) * (D / 4)
-                          : ((int64_t)(w.start + i) * a.o_row + (int64_t)h * a.o_head) / 8;
-          uint4* const base = reinterpret_cast<uint4*>(w.part >= 0 ? (void*)a.ws : a.out);
+              part >= 0 ? ((int64_t)part * p.ws_rows + x * 128 + row) * (D / 4)
+                        : ((int64_t)tok * a.o_row + (int64_t)h * a.o_head) / 8;
+          uint4* const base = reinterpret_cast<uint4*>(part >= 0 ? (void*)a.ws : a.out);
           auto flush = [&](int at) {  // the staged 128 bytes of each row to 16-byte unit `at` of it
             __syncwarp();
 #pragma unroll
@@ -1022,7 +1048,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
             __syncwarp();
           };
           auto put = [&](int c, uint4 q) { *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4)) = q; };
-          if (T > 0 && w.part >= 0) {
+          if (T > 0 && part >= 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               float v[32];
@@ -1050,10 +1076,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       if (NQ == 1 && T > 0) {
         fence_proxy_async();  // the next thing into this Q tile comes by TMA
         __syncwarp();
-        if (lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
+        if (lane == 0) mbar_arrive(&q_empty[q_used & 1u]);
       }
-      __syncwarp();
-      if (lane == 0) mbar_arrive_relaxed(&w_empty[ws]);
     }
     if (!ok) give_up();
   }
@@ -1145,10 +1169,9 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
   const bool one = r.batch <= 32;
   Seq mine_s{0, 0, 0, false};
   if (one && lane < r.batch) mine_s = load_seq(r, lane);
-  int units = 0;
-  for (int b = lane; b < r.batch; b += 32) units += units_of(one ? mine_s : load_seq(r, b), p, a);
-  units = (int)__reduce_add_sync(0xffffffffu, (unsigned)units);
-  const Ranges rg(units, p, grid);
+  int64_t sum = 0;
+  for (int b = lane; b < r.batch; b += 32) sum += units_of(one ? mine_s : load_seq(r, b), p, a);
+  const Ranges rg(max(sum_up_to(sum, p.max_units), 0), p, grid);
   if (c >= rg.n) return;
   const int u = rg.start(c), n = rg.n;
   int before = 0;
@@ -1156,7 +1179,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
     const int b = base + lane;
     Seq s{0, 0, 0, false};
     if (b < r.batch) s = one ? mine_s : load_seq(r, b);
-    const int mine = units_of(s, p, a), incl = warp_scan_i(mine, lane);
+    const int mine = (int)units_of(s, p, a), incl = warp_scan_i(mine, lane);
     const int end = before + __shfl_sync(0xffffffffu, incl, 31);
     if (u >= end) {
       before = end;
@@ -1224,7 +1247,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
 // host
 // ---------------------------------------------------------------------------
 cudaError_t current_sms(int* sms) {
-  static int cached[64] = {};
+  static std::atomic<int> cached[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -1261,13 +1284,13 @@ int query_clusters(int S) {
   return n;
 }
 int clusters_at_once(int d, int S) {
-  static int cached[64][2][kMaxCluster + 1] = {};  // + 1; 0: not asked
+  static std::atomic<int> cached[64][2][kMaxCluster + 1];  // + 1; 0: not asked
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) {
     cudaGetLastError();
     return 0;
   }
-  int& c = cached[dev][d == 64][S];
+  std::atomic<int>& c = cached[dev][d == 64][S];
   if (!c) c = 1 + (d == 64 ? query_clusters<64>(S) : query_clusters<128>(S));
   return c - 1;
 }
@@ -1286,8 +1309,10 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
   h.nq = (int64_t)r.max_rows * G <= (int64_t)p.tpt * G ? 1 : 2;
   p.tok = p.tpt * h.nq;
   p.ws_rows = h.nq == 1 ? p.tpt * G : 256;
-  const int64_t items = ((int64_t)r.total / p.tok + std::min(r.batch, r.total)) * a.Hkv;
+  p.max_items = (int)std::min<int64_t>((int64_t)r.total / p.tok + std::min(r.batch, r.total), r.total);
+  const int64_t items = (int64_t)p.max_items * a.Hkv;
   const int tiles = (r.max_len + KT - 1) / KT;
+  p.max_units = (int)std::min<int64_t>(items * tiles, INT32_MAX);
   p.mode = (h.nq == 2 && (items >= 3 * sms / 2 || tiles <= 4)) || items * tiles > INT32_MAX ? kModeItems : kModeRanges;
   // cluster: a cluster per item, where all of them run at once and a CTA gets at
   // most 7 key tiles.  One user's block of 16, 8 KV heads: 15.8 us against 22.3
@@ -1336,7 +1361,7 @@ cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
 template <int D, int NQ>
 cudaError_t launch_tc(const Ragged& r, const AttnCall& a, const KVView& kv, const Plan& p, int sms,
                       const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
-  static bool attr[64] = {};
+  static std::atomic<bool> attr[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
