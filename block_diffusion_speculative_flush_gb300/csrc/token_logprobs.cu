@@ -27,6 +27,7 @@
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 
+#include <atomic>
 #include <cmath>
 #include <type_traits>
 
@@ -53,6 +54,10 @@ __device__ __forceinline__ float lp_ex2(float x) {
   return y;
 }
 
+// 2^d is 0 in fp32 far above this: a d below it (a masked entry at the type's
+// lowest value may be at -inf) is put here where it multiplies a 0.
+constexpr float kFar = -1000.f;
+
 // (m, s, t) of a set of entries; m = -inf: no entry above -inf.
 struct Stat {
   float m, s, t;
@@ -61,7 +66,7 @@ struct Stat {
 __device__ __forceinline__ Stat warp_merge(Stat a, float c) {
   const float M = warp_max(a.m);
   // a side at -inf has s = t = 0 (or NaN, which stays)
-  const float d = a.m == -INFINITY ? 0.f : (a.m - M) * c, f = exp2f(d);
+  const float d = a.m == -INFINITY ? 0.f : fmaxf((a.m - M) * c, kFar), f = exp2f(d);
   return Stat{M, warp_sum(a.s * f), warp_sum(f * (a.t + a.s * d))};
 }
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
@@ -154,7 +159,7 @@ __device__ __forceinline__ uint32_t rth_of_lanes(uint32_t v, int r, int lane) {
 }
 
 template <typename T>
-__global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int cluster, float c) {
+__global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int cluster, float c, float inv_t) {
   constexpr int E = Elems<T>::E, N = U * E;
   // keys of the running round: [0, CAP) in turn, [CAP, 2 CAP) the warps' lists
   __shared__ uint64_t s_key[2][2 * CAP], s_all[kMaxCluster * 32], s_out[32];
@@ -188,13 +193,13 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
 
   Stat st{-INFINITY, 0.f, 0.f};
   uint64_t list = 0, kth = 0;
-  // adds n elements with maximum hi; clamp: -inf among them (2^-inf is 0, but
-  // 0 (-inf) is not: the factor is kept finite; a NaN still comes in through p)
+  // adds n elements with maximum hi; clamp: some d may be below kFar (a NaN
+  // still comes in through p)
   auto add = [&](auto n_, const float* e, float hi, bool clamp) {
     constexpr int n = decltype(n_)::value;
     if (hi > st.m) {
-      const float dm = (st.m - hi) * c, f = lp_ex2(dm);
-      st.t = st.m == -INFINITY ? st.t : f * fmaf(st.s, dm, st.t);
+      const float dm = fmaxf((st.m - hi) * c, kFar), f = lp_ex2(dm);
+      st.t = f * fmaf(st.s, dm, st.t);
       st.s *= f;
       st.m = hi;
     }
@@ -208,7 +213,7 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
       asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(d), "l"(c2));
       float2 dd = unpack2(d);
       const uint64_t pp = pack2(lp_ex2(dd.x), lp_ex2(dd.y));
-      if (clamp) d = pack2(fmaxf(dd.x, -1000.f), fmaxf(dd.y, -1000.f));
+      if (clamp) d = pack2(fmaxf(dd.x, kFar), fmaxf(dd.y, kFar));
       asm("add.rn.f32x2 %0, %0, %1;" : "+l"(s2) : "l"(pp));
       asm("fma.rn.f32x2 %0, %1, %2, %0;" : "+l"(t2) : "l"(pp), "l"(d));
     }
@@ -368,7 +373,7 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
         float e[N];
 #pragma unroll
         for (int u = 0; u < U; ++u) Elems<T>::get(cur[u], e + u * E);
-        if (lo > -INFINITY) add(std::integral_constant<int, N>(), e, hi, false);
+        if ((lo - fmaxf(st.m, hi)) * c > kFar) add(std::integral_constant<int, N>(), e, hi, false);
         else add(std::integral_constant<int, N>(), e, hi, true);
       }
       if (K > 0) {
@@ -461,7 +466,7 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
   if (tid == 0) {
     float lp = 0.f;
     if (tok >= 0 && tok < a.vocab) {
-      lp = ((xt - st.m) * c - ls) * ln2;
+      lp = fmaf(xt - st.m, inv_t, -ls * ln2);
     } else if (tok != -1) {
       lp = nan;
       if (a.status) atomicOr(a.status, DFLASH_STATUS_TOKEN);
@@ -473,7 +478,7 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     const int64_t o = (int64_t)row * K;
     auto put = [&](uint64_t k, int r) {
       a.top_ids[o + r] = (int32_t)(0xffffffffu - (uint32_t)k);
-      a.top_logprobs[o + r] = ((float_of_order((uint32_t)(k >> 32)) - st.m) * c - ls) * ln2;
+      a.top_logprobs[o + r] = fmaf(float_of_order((uint32_t)(k >> 32)) - st.m, inv_t, -ls * ln2);
     };
     if (cluster > 1) {
       n = (int)s_nall;
@@ -502,7 +507,7 @@ cudaError_t launch_logprobs(const dflash_logprobs& a, int sms, cudaStream_t st) 
   while (cluster < kMaxCluster && (int64_t)a.rows * cluster < 2 * sms &&
          (int64_t)a.vocab * (int)sizeof(T) >= (int64_t)cluster * 2 * TH * U * 16)
     cluster *= 2;
-  static bool attr[64] = {};
+  static std::atomic<bool> attr[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
@@ -511,8 +516,8 @@ cudaError_t launch_logprobs(const dflash_logprobs& a, int sms, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
-  const float c = (float)(1.4426950408889634 / (double)a.temperature);
-  return launch_kc(k_token_logprobs<T>, (unsigned)(a.rows * cluster), TH, 0, st, cluster, a, cluster, c);
+  const float c = (float)(1.4426950408889634 / (double)a.temperature), inv_t = (float)(1 / (double)a.temperature);
+  return launch_kc(k_token_logprobs<T>, (unsigned)(a.rows * cluster), TH, 0, st, cluster, a, cluster, c, inv_t);
 }
 
 }  // namespace

@@ -544,3 +544,96 @@ def test_token_logprobs_of_rows_without_a_distribution(dtype):
     lp, ent, ids, tlp = run_logprobs(x.cuda(), i32([5, 5, 5, 9]), 4, 1.0)
     assert bool(torch.isnan(lp).all()) and bool(torch.isnan(ent).all()) and bool(torch.isnan(tlp).all())
     assert ids.cpu().tolist() == [[0, 1, 2, 3], [0, 1, 2, 3], [-1] * 4, [7, 0, 1, 2]]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("T", [1.0, 0.25, 4.0])
+def test_token_logprobs_of_rows_masked_with_the_lowest_value(dtype, T):
+    """Entries at the type's lowest value have probability zero and no share in the entropy, wherever they lie
+    (their distance to the maximum is past the fp32 range once it is scaled)."""
+    V, low = 40000, torch.finfo(DT[dtype]).min
+    x = torch.randn((5, V), generator=torch.Generator().manual_seed(8)).to(DT[dtype])
+    x[0, :30000] = low            # whole batches of a thread in front of the others,
+    x[1, 9000:] = low             # behind them,
+    x[2, ::2] = low               # between them,
+    x[3, :] = low                 # one entry left,
+    x[3, 31234] = 2.5
+    x[4, :] = low                 # and none: a uniform row
+    tok = torch.tensor([39999, 5, 33, 31234, -1], dtype=torch.int32)
+    if T >= 1:                    # (below, a masked token's log probability leaves fp32)
+        tok[2] = 34
+    got = run_logprobs(x.cuda(), tok.cuda(), 5, T)
+    ref = O.logprobs(x, tok, 5, T)
+    check_logprobs(tuple(a[:3] for a in got), tuple(a[:3] for a in ref))
+    lp, ent, ids, tlp = (a.cpu() for a in got)
+    # one entry left: exact; the masked ones behind it, in the order of their ids
+    assert float(lp[3]) == 0 and float(ent[3]) == 0 and ids[3].tolist() == [31234, 0, 1, 2, 3]
+    assert float(tlp[3, 0]) == 0 and (T < 1 or bool(torch.isfinite(tlp[3]).all()))
+    # a uniform row: sums of ones are exact, log2 and the product with ln 2 round (2 + 1 + 1 half steps at 11)
+    tol = 4 * 2.0 ** -24 * 16
+    assert abs(float(ent[4]) - math.log(V)) <= tol and float(lp[4]) == 0 and ids[4].tolist() == [0, 1, 2, 3, 4]
+    assert float((tlp[4] + math.log(V)).abs().max()) <= tol
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_token_logprobs_at_the_smallest_temperature(dtype):
+    """1 / T close to the end of the fp32 range: scaled distances overflow, the distribution is its maximum's."""
+    V = 20000
+    x = torch.randn((3, V), generator=torch.Generator().manual_seed(9)).to(DT[dtype])
+    x[:, 777] = 8.0
+    tok = torch.tensor([777, -1, 777], dtype=torch.int32)
+    lp, ent, ids, tlp = run_logprobs(x.cuda(), tok.cuda(), 1, 1e-38)
+    assert lp.tolist() == [0, 0, 0] and ent.tolist() == [0, 0, 0] and tlp.flatten().tolist() == [0, 0, 0]
+    assert ids.flatten().tolist() == [777] * 3
+
+
+@pytest.mark.parametrize("heads", [1, 4])
+def test_a_value_that_is_not_finite_in_the_last_tile_of_an_item(heads):
+    """Items of two row tiles whose second one alone reaches the last key tile, which holds a NaN that only the
+    sequence's last token sees: every other row, those of the first tile among them, is complete and right."""
+    D = lib()
+    n, d, seqs, hq, hkv = 256, 64, 40, heads, heads
+    g = torch.Generator().manual_seed(12)
+    t = n * seqs
+    q, k, v = (torch.randn((t, h, d), generator=g).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    starts = [b * n for b in range(seqs + 1)]
+    split = lambda x: [x[b * n:(b + 1) * n] for b in range(seqs)]
+    ref = O.attention(q, split(k), split(v), starts, [n] * seqs, True, 0, d ** -0.5, True)
+    v[n - 1::n, :, 7] = math.nan
+    seen = torch.ones(t, dtype=torch.bool)
+    seen[n - 1::n] = False
+    dev = q.cuda(), k.cuda(), v.cuda()
+    for _ in range(5):
+        out, lse = torch.full((t, hq, d), 7.0, dtype=torch.bfloat16, device="cuda"), torch.empty((t, hq), device="cuda")
+        D.dflash_prompt_attention(*dev, i32(starts), out, max_rows=n, lse=lse)
+        check_attention(out.cpu()[seen], lse.cpu()[seen], tuple(x[seen] for x in ref), int(seen.sum()))
+        assert bool(torch.isnan(out[n - 1::n, :, 7]).all()) and bool(torch.isfinite(out[n - 1::n, :, 8:]).all())
+
+
+def test_a_value_that_is_not_finite_in_the_last_tile_of_a_paged_item():
+    """The same with 8 heads a group: 32 new tokens over 112 cached ones, the first 16 of them end with a tile."""
+    B = Batch("bf16", 8, 1, 128, 16, [32] * 40, [144] * 40, seed=5)
+    ref = ref_paged(B, True, 0)
+    B.v[31:32 * 40:32, :, 7] = math.nan
+    seen = torch.ones(32 * 40, dtype=torch.bool)
+    seen[31::32] = False
+    for _ in range(5):
+        out, lse, _, _ = run_paged(B, True, 0)
+        check_attention(out[:1280].cpu()[seen], lse[:1280].cpu()[seen], tuple(x[seen] for x in ref), int(seen.sum()))
+        assert bool(torch.isnan(out[31:1280:32, :, 7]).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,lens", [(4, 40), (200, 300)])
+def test_starts_that_decrease_are_reported(dtype, rows, lens):
+    """64 sequences whose starts go back and forth: each of the good halves alone would be in bounds, together
+    they are more rows than the arrays hold."""
+    D = lib()
+    q = torch.randn((rows, 4, 64), device="cuda").to(DT[dtype])
+    pages = torch.zeros((20, 16, 1, 64), dtype=DT[dtype], device="cuda")
+    out, st = torch.full_like(q, 7.0), i32([0])
+    starts, table = i32([0, rows] * 32 + [0]), i32(list(range(20))).repeat(64, 1)
+    D.dflash_paged_attention(q, pages, pages.clone(), starts, i32([lens] * 64), table, out, max_rows=rows, status=st)
+    assert int(st.item()) == 2 and bool(((out == 7) | (out == 0)).all())
+    with pytest.raises(D.DFlashError):
+        D.dflash_status_check(st)
