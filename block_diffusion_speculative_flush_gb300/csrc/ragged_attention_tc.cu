@@ -1155,11 +1155,11 @@ __device__ __forceinline__ void load_if(float* v, const float* p, bool yes) {
 }
 
 // Merge of the parts of each item that a range boundary cut.  CTA (c - 1, y):
-// boundary c, if it is the first inside its item; a warp per row, parts in key
+// boundary c, if it is the first inside its item; RW rows per warp, parts in key
 // order.
-template <int D>
-__global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, Plan p, int grid, int rows_per_cta) {
-  constexpr int C = D / 32;
+template <int D, int RW>
+__global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, Plan p, int grid) {
+  constexpr int C = D / 32, rows_per_cta = 8 * RW;
   pdl_trigger();
   pdl_wait();
   r.starts = after_wait(r.starts);
@@ -1195,9 +1195,70 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
     const int parts = rg.of(i_end - 1) - (c - 1) + 1;
     const int slot0 = 2 * (c - 1) + (rg.start(c - 1) < i_begin);
     auto slot_of = [&](int q) { return q == 0 ? slot0 : 2 * (c - 1 + q); };
-    for (int row = blockIdx.y * rows_per_cta + warp; row < (int)(blockIdx.y + 1) * rows_per_cta; row += 8) {
+    const int row0 = blockIdx.y * rows_per_cta + warp;
+    // the token of a row of the item, or -1
+    auto token = [&](int row) {
       const int x = row / 128, rr = row % 128, i = i0 + x * p.tpt + rr / G;
-      if (rr >= p.tpt * G || i >= min(i0 + p.tok, sn)) continue;
+      return rr < p.tpt * G && i < min(i0 + p.tok, sn) ? start + i : -1;
+    };
+    auto put = [&](int row, int tok, float M, float L, const float* acc) {
+      const float inv = M == -INFINITY ? 0.f : 1.f / L;
+      const int h = kvh * G + row % 128 % G;
+      bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + lane * C;
+#pragma unroll
+      for (int j = 0; j < C; j += 2)
+        *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
+      if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+    };
+    constexpr int PP = 32 / RW;
+    if (RW > 1 && parts <= PP) {
+      // all rows of the warp at once: the statistics a lane per (row, part), O two
+      // parts of every row in flight
+      const int k_ml = lane / PP, q_ml = lane % PP, row_ml = row0 + 8 * k_ml;
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (q_ml < parts && token(row_ml) >= 0) ml = *part_ml<D>(a, p, slot_of(q_ml), row_ml);
+      float M = ml.x;
+#pragma unroll
+      for (int o = PP / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+      // a part that saw no key has weight 0 and its sums were not written; a NaN maximum stays one
+      const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      float L = wt == 0.f ? 0.f : ml.y * wt;
+#pragma unroll
+      for (int o = PP / 2; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+      float acc[RW][C];
+#pragma unroll
+      for (int k = 0; k < RW; ++k)
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[k][j] = 0.f;
+#pragma unroll 1
+      for (int q0 = 0; q0 < parts; q0 += 2) {
+        float v[2][RW][C], w[2][RW];
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < RW; ++k) {
+            w[u][k] = __shfl_sync(0xffffffffu, wt, k * PP + ((q0 + u) & (PP - 1)));
+            if (q0 + u >= parts) w[u][k] = 0.f;
+            load_if<C>(v[u][k], part_o<D>(a, p, slot_of(q0 + u), row0 + 8 * k) + lane * C, w[u][k] != 0.f);
+          }
+#pragma unroll
+        for (int u = 0; u < 2; ++u)
+#pragma unroll
+          for (int k = 0; k < RW; ++k)
+#pragma unroll
+            for (int j = 0; j < C; ++j) acc[k][j] = fmaf(w[u][k], v[u][k][j], acc[k][j]);
+      }
+#pragma unroll
+      for (int k = 0; k < RW; ++k) {
+        const float Mk = __shfl_sync(0xffffffffu, M, k * PP), Lk = __shfl_sync(0xffffffffu, L, k * PP);
+        const int row = row0 + 8 * k, tok = token(row);
+        if (tok >= 0) put(row, tok, Mk, Lk, acc[k]);
+      }
+      return;
+    }
+    for (int row = row0; row < (int)(blockIdx.y + 1) * rows_per_cta; row += 8) {
+      const int tok = token(row);
+      if (tok < 0) continue;
       float M = -INFINITY, L = 0.f, acc[C];
 #pragma unroll
       for (int j = 0; j < C; ++j) acc[j] = 0.f;
@@ -1231,13 +1292,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
           }
         }
       }
-      const float inv = M == -INFINITY ? 0.f : 1.f / L;
-      const int tok = start + i, h = kvh * G + rr % G;
-      bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + lane * C;
-#pragma unroll
-      for (int j = 0; j < C; j += 2)
-        *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
-      if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+      put(row, tok, M, L, acc);
     }
     return;
   }
@@ -1401,8 +1456,8 @@ cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const
   if (e != cudaSuccess || !h.merge) return e;
   const int rows = h.nq == 1 ? r.max_rows * G : 256;
   // rows of a CTA: few enough CTAs that finding the cuts, which each does, is one wave
-  const int per = h.nq == 1 ? 8 : 32;
-  return launch_k(k_ragged_merge<D>, dim3(sms - 1, (rows + per - 1) / per), 256, 0, st, r, a, h.p, sms, per);
+  return h.nq == 1 ? launch_k(k_ragged_merge<D, 1>, dim3(sms - 1, (rows + 7) / 8), 256, 0, st, r, a, h.p, sms)
+                   : launch_k(k_ragged_merge<D, 4>, dim3(sms - 1, rows / 32), 256, 0, st, r, a, h.p, sms);
 }
 
 }  // namespace
