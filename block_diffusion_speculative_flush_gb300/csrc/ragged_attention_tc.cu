@@ -69,6 +69,7 @@ struct Plan {
   int32_t hgroup;       // items: KV heads dealt out together (bounds the K/V that is live in L2)
   int32_t cluster;      // cluster: CTAs of an item
   int32_t min_tiles_log2;  // ranges: log2 of the key tiles a CTA gets at least
+  int32_t pad;          // ranges: what the start of an item costs, in key tiles
   int32_t ws_rows;      // rows of a partial
   int32_t slots;        // partials there is room for
   int32_t max_items;    // items of one KV head, and key tiles of all items (ranges), that there can be
@@ -173,11 +174,13 @@ __device__ __forceinline__ int items_reaching(const Seq& s, int c, const Plan& p
   const int first = need <= 0 ? 0 : cdiv(need, p.tok) - 1;
   return nq - min(first, nq - 1);
 }
-// ranges: a sequence's key tiles [first, first + count), taken for each of its items
+// ranges: a sequence's key tiles [first, first + count), taken for each of its
+// items; in the units that are split evenly, `pad` empty ones lie in front of
+// each item's tiles (a CTA that starts an item fills the pipeline anew)
 __device__ __forceinline__ int tile_first(const Seq& s, int window) { return vis_lo(s.len - s.n, window) / KT; }
 __device__ __forceinline__ int tile_count(const Seq& s, int window) { return cdiv(s.len, KT) - tile_first(s, window); }
 __device__ __forceinline__ int64_t units_of(const Seq& s, const Plan& p, const AttnCall& a) {
-  return s.ok && s.n > 0 ? (int64_t)items_of(s, p) * a.Hkv * tile_count(s, a.window) : 0;
+  return s.ok && s.n > 0 ? (int64_t)items_of(s, p) * a.Hkv * (tile_count(s, a.window) + p.pad) : 0;
 }
 // The sum of the lanes' counts, or -1 where it is above what the host laid the
 // work out for: sequences that overlap (starts that decrease somewhere).
@@ -525,12 +528,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
           const Seq q = bcast(s, src);
           const int off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
-          const int T = tile_count(q, a.window), item = off / T, qi = item / a.Hkv;
-          const int t = off - item * T, take = min(T - t, u1 - u);
-          const int part = t == 0 && take == T ? -1 : 2 * cta + (seg > 0);
-          make_work(w, q, base + src, item - qi * a.Hkv, qi, tile_first(q, a.window) + t, take, part, p, a);
+          const int T = tile_count(q, a.window), item = off / (T + p.pad), qi = item / a.Hkv;
+          const int t = off - item * (T + p.pad) - p.pad;  // < 0: in front of the item's tiles
+          const int take = min(T, t + u1 - u) - max(t, 0);
+          u += min(T - t, u1 - u);
+          if (take <= 0) continue;
+          const int part = take == T ? -1 : 2 * cta + (seg > 0);
+          make_work(w, q, base + src, item - qi * a.Hkv, qi, tile_first(q, a.window) + max(t, 0), take, part, p, a);
           emit(w);
-          u += take;
           ++seg;
         }
         before = chunk_end;
@@ -1188,9 +1193,10 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
     const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
     const int seq_u = before + __shfl_sync(0xffffffffu, incl - mine, src);
     const int start = __shfl_sync(0xffffffffu, s.start, src), sn = __shfl_sync(0xffffffffu, s.n, src);
-    const int T = __shfl_sync(0xffffffffu, s.ok && s.n > 0 ? tile_count(s, a.window) : 1, src);
+    const int T = __shfl_sync(0xffffffffu, s.ok && s.n > 0 ? tile_count(s, a.window) + p.pad : 1, src);
     const int item = (u - seq_u) / T, i_begin = seq_u + item * T, i_end = i_begin + T;
-    if (u == i_begin || rg.start(c - 1) > i_begin) return;  // no cut here, or not the item's first
+    // no cut here (in front of the item's tiles), or not the item's first
+    if (u <= i_begin + p.pad || rg.start(c - 1) > i_begin + p.pad) return;
     const int qi = item / a.Hkv, kvh = item - qi * a.Hkv, i0 = qi * p.tok;
     const int parts = rg.of(i_end - 1) - (c - 1) + 1;
     const int slot0 = 2 * (c - 1) + (rg.start(c - 1) < i_begin);
@@ -1364,11 +1370,23 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
   h.nq = (int64_t)r.max_rows * G <= (int64_t)p.tpt * G ? 1 : 2;
   p.tok = p.tpt * h.nq;
   p.ws_rows = h.nq == 1 ? p.tpt * G : 256;
-  p.max_items = (int)std::min<int64_t>((int64_t)r.total / p.tok + std::min(r.batch, r.total), r.total);
+  p.max_items = (int)std::min<int64_t>(std::min<int64_t>((int64_t)r.total / p.tok + std::min(r.batch, r.total), r.total),
+                                       (int64_t)r.batch * ((r.max_rows + p.tok - 1) / p.tok));
   const int64_t items = (int64_t)p.max_items * a.Hkv;
   const int tiles = (r.max_len + KT - 1) / KT;
-  p.max_units = (int)std::min<int64_t>(items * tiles, INT32_MAX);
-  p.mode = (h.nq == 2 && (items >= 3 * sms / 2 || tiles <= 4)) || items * tiles > INT32_MAX ? kModeItems : kModeRanges;
+  // 2, 4 and 6 are within 2% of each other for chunks; single tokens of 64
+  // sequences of 100 to 8000: 136 us without, 122 with 1, 124 with 3
+  p.pad = h.nq == 2 || a.d == 64 ? 2 : 1;
+  const int64_t units = items * (tiles + p.pad);
+  p.max_units = (int)std::min<int64_t>(units, INT32_MAX);
+  // Whole items where they fill the SMs one and a half times, or where the longest
+  // ones of each wave (packed causal prompts: of the first, the others are short)
+  // take no more key tiles than an even share and the 16 that cutting costs
+  // (partials, their merge).  Causal prompt of 1024: 22 us whole, 38 cut; of 1500 29
+  // and 53; 200 new tokens of 3 over 4096 62 and 65; 64 of 8 over 8192 111 and 79.
+  const int64_t waves = a.causal && !r.lens ? 1 : (items + sms - 1) / sms;
+  const bool whole = h.nq == 2 && (items >= 3 * sms / 2 || tiles * waves <= items * tiles / sms + 16);
+  p.mode = whole || units > INT32_MAX ? kModeItems : kModeRanges;
   // cluster: a cluster per item, where all of them run at once and a CTA gets at
   // most 7 key tiles.  One user's block of 16, 8 KV heads: 15.8 us against 22.3
   // over 4096 tokens, 22.4 against 23.6 over 8192, 29 against 25 over 12288.
