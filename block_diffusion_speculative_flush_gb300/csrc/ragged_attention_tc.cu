@@ -336,6 +336,115 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
   }
 }
 
+// One key tile of one row (a thread each): S from TMEM, m and l brought up to
+// date, P into S's first 64 columns.
+struct TileArgs {
+  uint32_t tS, tO;     // this warp's lanes of S and O
+  int hi, lo;          // keys of the tile that the row sees: [lo, hi)
+  bool masked_hi, masked_lo;  // some row of the warp misses keys there
+  bool valid;
+  float sl2;
+};
+template <int D, int NQ>
+__device__ __forceinline__ bool softmax_tile(const TileArgs& a, float& m, float& l, uint64_t* pv_done, uint32_t parity,
+                                             volatile int* abort_flag) {
+  float s[128];
+  fence_after();
+  const auto keep_of = [&](int c) {  // keys c .. c + 31 that the row sees, a bit each
+    const int n = min(max(a.hi - c, 0), 32);
+    return n == 32 ? 0xffffffffu : (1u << n) - 1u;
+  };
+  if (NQ == 1 && (a.masked_hi || a.masked_lo)) {
+    // masks on their own, 32 columns a turn and back into TMEM: the code of the
+    // 128 scores, run once an item, took 2100 cycles (it is not in the instruction
+    // cache by then)
+#pragma unroll 1
+    for (int c = 0; c < 128; c += 32) {
+      float v[32];
+      tmem_ld32(a.tS + c, v);
+      const int b = min(max(a.lo - c, 0), 32);
+      const uint32_t keep = keep_of(c) & (b == 32 ? 0u : ~0u << b);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = (keep >> j) & 1u ? v[j] : -INFINITY;
+      tmem_st32(a.tS + c, v);
+    }
+  }
+  tmem_ld128(a.tS, s);
+  if (NQ == 2 && a.masked_hi) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      const uint32_t keep = keep_of(c);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[c + j] = (keep >> j) & 1u ? s[c + j] : -INFINITY;
+    }
+  }
+  if (NQ == 2 && a.masked_lo) {
+#pragma unroll
+    for (int j = 0; j < 128; ++j) s[j] = j >= a.lo ? s[j] : -INFINITY;
+  }
+  float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+  for (int j = 4; j < 124; j += 8) {
+    m0 = max3(m0, s[j], s[j + 1]);
+    m1 = max3(m1, s[j + 2], s[j + 3]);
+    m2 = max3(m2, s[j + 4], s[j + 5]);
+    m3 = max3(m3, s[j + 6], s[j + 7]);
+  }
+  m0 = max3(m0, s[124], s[125]);
+  m1 = max3(m1, s[126], s[127]);
+  const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * a.sl2;
+  const bool grow = a.valid && mt > m + 8.f;
+  if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+    const float f = grow && m != -INFINITY ? ex2(m - mt) : 1.f;
+    // O holds the previous tile's product before it is scaled (NQ = 2: S of
+    // this tile was issued behind it)
+    if (NQ == 1 && !__all_sync(0xffffffffu, mbar_wait(pv_done, parity, abort_flag))) return false;
+    fence_after();
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tmem_ld32(a.tO + c, o);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] *= f;
+      tmem_st32(a.tO + c, o);
+    }
+    l *= f;
+  }
+  if (grow) m = mt;
+  const float mref = m == -INFINITY ? 0.f : m;
+  const uint64_t k2 = f2pack(a.sl2, a.sl2), c2 = f2pack(-mref, -mref);
+  uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
+  auto probs = [&](int c) {  // 32 keys
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      uint64_t e2;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
+      const float2 e = f2unpack(e2);
+      const float p0 = ex2(e.x), p1 = ex2(e.y);
+      if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(f2pack(p0, p1)));
+      else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(f2pack(p0, p1)));
+      const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+      pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
+    }
+    tmem_st16u(a.tS + c / 2, pk);
+  };
+  probs(0);
+  probs(32);
+  probs(64);
+  probs(96);
+  const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
+  l += (s0.x + s0.y) + (s1.x + s1.y);
+  return true;
+}
+// (NQ = 1 does not inline it: 64 single tokens over 1k to 16k 237 -> 231 us with
+// pages of 16, over 4096 178 -> 180 with pages of 64)
+template <int D>
+__device__ __noinline__ bool softmax_tile_call(const TileArgs a, float& m, float& l, uint64_t* pv_done, uint32_t parity,
+                                               volatile int* abort_flag) {
+  return softmax_tile<D, 1>(a, m, l, pv_done, parity, abort_flag);
+}
+
 template <int D, int NQ>
 __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     k_ragged_tc(Ragged r, AttnCall a, KVView kv, Plan p, const __grid_constant__ CUtensorMap mq,
@@ -880,6 +989,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
+      auto kt_of = [&](int t) { return (w.t0 + t) * KT; };
       for (int t = 0; t < T; ++t, ++cnt) {
         const int sb = NQ == 2 ? x : (int)(cnt & 1u);
         const uint32_t par = NQ == 2 ? cnt & 1u : (cnt >> 1) & 1u;
@@ -904,81 +1014,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           return ok;
         };
         if (live) {
-          const int kt = (w.t0 + t) * KT;
-          float s[128];
-          fence_after();
-          tmem_ld128(tmem + lrow + sb * 128, s);
-          if (hi_min < kt + KT) {  // keys that some row does not see, as a bit each
-            const int h0 = hi - kt;
-#pragma unroll
-            for (int c = 0; c < 128; c += 32) {
-              const int n = min(max(h0 - c, 0), 32);
-              const uint32_t keep = n == 32 ? 0xffffffffu : (1u << n) - 1u;
-#pragma unroll
-              for (int j = 0; j < 32; ++j) s[c + j] = (keep >> j) & 1u ? s[c + j] : -INFINITY;
-            }
-          }
-          if (lo_max > kt) {
-            const int l0 = lo - kt;
-#pragma unroll
-            for (int j = 0; j < 128; ++j) s[j] = j >= l0 ? s[j] : -INFINITY;
-          }
-          float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
-#pragma unroll
-          for (int j = 4; j < 124; j += 8) {
-            m0 = max3(m0, s[j], s[j + 1]);
-            m1 = max3(m1, s[j + 2], s[j + 3]);
-            m2 = max3(m2, s[j + 4], s[j + 5]);
-            m3 = max3(m3, s[j + 6], s[j + 7]);
-          }
-          m0 = max3(m0, s[124], s[125]);
-          m1 = max3(m1, s[126], s[127]);
-          const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * sl2;
-          const bool grow = valid && mt > m + 8.f;
-          if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-            const float f = grow && m != -INFINITY ? ex2(m - mt) : 1.f;
-            // O holds the previous tile's product before it is scaled (NQ = 2: S of
-            // this tile was issued behind it)
-            if (NQ == 1 && !__all_sync(0xffffffffu, mbar_wait(&pv_done[x], (cnt - 1) & 1u, abort_flag))) {
-              ok = false;
-              break;
-            }
-            fence_after();
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float o[32];
-              tmem_ld32(tO + c, o);
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] *= f;
-              tmem_st32(tO + c, o);
-            }
-            l *= f;
-          }
-          if (grow) m = mt;
-          const float mref = m == -INFINITY ? 0.f : m;
-          const uint64_t k2 = f2pack(sl2, sl2), c2 = f2pack(-mref, -mref);
-          uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
-          auto probs = [&](int c) {  // 32 keys
-            uint32_t pk[16];
-#pragma unroll
-            for (int j = 0; j < 16; ++j) {
-              uint64_t e2;
-              asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
-              const float2 e = f2unpack(e2);
-              const float p0 = ex2(e.x), p1 = ex2(e.y);
-              if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(f2pack(p0, p1)));
-              else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(f2pack(p0, p1)));
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-              pk[j] = *reinterpret_cast<const uint32_t*>(&b2);
-            }
-            tmem_st16u(tmem + lrow + sb * 128 + c / 2, pk);
-          };
-          probs(0);
-          probs(32);
-          probs(64);
-          probs(96);
-          const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
-          l += (s0.x + s0.y) + (s1.x + s1.y);
+          const TileArgs ta{tmem + lrow + sb * 128, tO, hi - kt_of(t), lo - kt_of(t), hi_min < kt_of(t) + KT, lo_max > kt_of(t),
+                            valid, sl2};
+          if constexpr (NQ == 1) ok = softmax_tile_call<D>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
+          else ok = softmax_tile<D, NQ>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
+          if (!ok) break;
           tmem_wait_st();
           fence_before();
           if (!prior_product()) break;
@@ -1010,6 +1050,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         if (lane == 0) mbar_arrive(&w_empty[ws]);
       };
       if (!bad) give_back();
+      // Up to 8 rows of a warp (single tokens) each lane stores its own, which is
+      // little code; more go through shared memory.
+      const uint32_t rows = __ballot_sync(0xffffffffu, valid);
+      const bool staged = NQ == 2 || (live && !bad && p.mode != kModeCluster && __popc(rows) > 8);
+      if (NQ == 1 && T > 0 && !staged && lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
       if (bad) {
         redo_rows<D>(r, a, kv, p, w, x, warp & 3, c_o, c_ml);  // rows in turn over all four warps
         give_back();
@@ -1031,54 +1076,72 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           if (valid) c_ml[row] = make_float2(T > 0 ? m : -INFINITY, l);
         } else {
           if (valid) store_stats<D>(a, p, part, x, row, tok, h, m, l);
-          // 128 bytes of each row at a time through shared memory, so that a store
-          // covers whole lines (a row per lane took five times as long): row r's
-          // 16-byte chunk c lies at chunk c ^ (r & 7).
-          const uint32_t rows = __ballot_sync(0xffffffffu, valid);
-          uint8_t* st = NQ == 2 ? sS + warp * 4096 : sQ + (q_used & 1u) * SLOT + warp * 4096;
           // where this lane's own row starts, in 16-byte units
           const int64_t own =
               part >= 0 ? ((int64_t)part * p.ws_rows + x * 128 + row) * (D / 4)
                         : ((int64_t)tok * a.o_row + (int64_t)h * a.o_head) / 8;
           uint4* const base = reinterpret_cast<uint4*>(part >= 0 ? (void*)a.ws : a.out);
-          auto flush = [&](int at) {  // the staged 128 bytes of each row to 16-byte unit `at` of it
-            __syncwarp();
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int rr = 4 * k + (lane >> 3), c = lane & 7;
-              const int64_t o = __shfl_sync(0xffffffffu, own, rr);
-              const uint4 q = *reinterpret_cast<const uint4*>(st + rr * 128 + ((c ^ (rr & 7)) << 4));
-              if ((rows >> rr) & 1u) base[o + at + c] = q;
-            }
-            __syncwarp();
-          };
-          auto put = [&](int c, uint4 q) { *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4)) = q; };
-          if (T > 0 && part >= 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
-              float v[32];
-              tmem_ld32(tO + c, v);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) put(j, *reinterpret_cast<const uint4*>(v + 4 * j));
-              flush(c / 4);
-            }
-          } else if (T > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D; c += 64) {
-#pragma unroll
-              for (int h = 0; h < 2; ++h) {
-                float v[32];
-                tmem_ld32(tO + c + 32 * h, v);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) put(4 * h + j, pack8(v + 8 * j, inv));
+          if (!staged) {
+            if (T > 0) {
+              float v[D];
+              if constexpr (D == 128) {
+                tmem_ld128(tO, v);
+              } else {
+                tmem_ld32(tO, v);
+                tmem_ld32(tO + 32, v + 32);
               }
-              flush(c / 8);
+              if (valid && part >= 0) {
+#pragma unroll
+                for (int j = 0; j < D / 4; ++j) base[own + j] = *reinterpret_cast<const uint4*>(v + 4 * j);
+              } else if (valid) {
+#pragma unroll
+                for (int j = 0; j < D / 8; ++j) base[own + j] = pack8(v + 8 * j, inv);
+              }
+            }
+          } else {
+            // 128 bytes of each row at a time through shared memory, so that a store
+            // covers whole lines (a row per lane took five times as long): row r's
+            // 16-byte chunk c lies at chunk c ^ (r & 7).
+            uint8_t* st = NQ == 2 ? sS + warp * 4096 : sQ + (q_used & 1u) * SLOT + warp * 4096;
+            auto flush = [&](int at) {  // the staged 128 bytes of each row to 16-byte unit `at` of it
+              __syncwarp();
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const int rr = 4 * k + (lane >> 3), c = lane & 7;
+                const int64_t o = __shfl_sync(0xffffffffu, own, rr);
+                const uint4 q = *reinterpret_cast<const uint4*>(st + rr * 128 + ((c ^ (rr & 7)) << 4));
+                if ((rows >> rr) & 1u) base[o + at + c] = q;
+              }
+              __syncwarp();
+            };
+            auto put = [&](int c, uint4 q) { *reinterpret_cast<uint4*>(st + lane * 128 + ((c ^ (lane & 7)) << 4)) = q; };
+            if (T > 0 && part >= 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 32) {
+                float v[32];
+                tmem_ld32(tO + c, v);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) put(j, *reinterpret_cast<const uint4*>(v + 4 * j));
+                flush(c / 4);
+              }
+            } else if (T > 0) {
+#pragma unroll 1
+              for (int c = 0; c < D; c += 64) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                  float v[32];
+                  tmem_ld32(tO + c + 32 * h, v);
+#pragma unroll
+                  for (int j = 0; j < 4; ++j) put(4 * h + j, pack8(v + 8 * j, inv));
+                }
+                flush(c / 8);
+              }
             }
           }
         }
         fence_before();
       }
-      if (NQ == 1 && T > 0) {
+      if (NQ == 1 && T > 0 && staged) {
         fence_proxy_async();  // the next thing into this Q tile comes by TMA
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_empty[q_used & 1u]);
