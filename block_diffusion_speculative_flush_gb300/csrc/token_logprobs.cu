@@ -5,7 +5,10 @@
 // (The difference before the product: the largest entry's d is exactly 0, and a
 // row of one possible token has entropy 0.)
 // One pass over the logits: (m, s, t) per thread, rescaled when its maximum
-// grows, and the top entries beside it.  Bound by reading the logits once.
+// grows, and the top entries beside it.  Bound by reading the logits once: 2047
+// rows of 151936 bf16 in 98 us without top entries, 6.3 TB/s (94% of a measured
+// copy), 116 with 5, 159 with 32.  16 rows of fp32 are latency: 6 us without, 13
+// with 20.
 //
 // A row belongs to a cluster of 1..16 CTAs, as many as give every SM two CTAs
 // when rows are few; each CTA streams its slice in 16-byte loads, four in
