@@ -5,6 +5,8 @@
 //   o_i = sum_j p_ij v_j,  p_ij = exp(s_ij - m_i) / l_i,  s_ij = scale q_i . k_j
 // over the keys j that row i sees, with the running maximum m and sum l of an
 // online softmax (fp32, in the exp2 domain), one pass over K and V.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -21,6 +23,8 @@ extern "C" int dflash__set_error(int code, const char* msg);
 
 namespace dfl {
 namespace {
+
+namespace cg = cooperative_groups;
 
 // ---------------------------------------------------------------------------
 // append
@@ -88,27 +92,64 @@ __device__ __forceinline__ bool kv_at(const Ragged& r, const KVView& kv, int b, 
   return pg >= 0 && pg < kv.n_pages;
 }
 
-// 16 packed rows (token, head of the group) x 256 keys per CTA.  Scores: a key
-// per thread, its K row straight from memory, the 16 rows of q broadcast from
-// shared memory (a row at a time through shared-memory tiles, as many rows
-// want it, left this kernel waiting for each 64 keys in turn: three blocks of 8
-// over 300 to 1500 tokens took 20 us with the merge, 16 now).  Bound by latency:
-// the key's row, the softmax, V, each a chain of loads, then the merge.  Then a softmax of two rows per warp,
-// and O = P V with the keys dealt to the warps.
-template <int DP>
-__global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView kv, int splits) {
-  constexpr int BR = 16, LQ = DP + 4, LP = BR + 4, LS = kSplit + 4;
+// The splits of one row and four columns, taken in split order.
+struct SplitMerge {
+  float M = -INFINITY, L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  __device__ __forceinline__ void max(float m) { M = fmaxf(M, m); }
+  // (sums of a split that saw no key are zeros)
+  __device__ __forceinline__ void add(float2 ml, float4 v) {
+    const float mref = M == -INFINITY ? 0.f : M;
+    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
+    L = fmaf(f, ml.y, L);
+    acc.x = fmaf(f, v.x, acc.x);
+    acc.y = fmaf(f, v.y, acc.y);
+    acc.z = fmaf(f, v.z, acc.z);
+    acc.w = fmaf(f, v.w, acc.w);
+  }
+  __device__ __forceinline__ void store(const AttnCall& a, int tok, int h, int c) const {
+    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    if (c < a.d)
+      store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + c,
+             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
+    if (a.lse && c == 0)
+      a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  }
+};
+
+// BR packed rows (token, head of the group) x 256 keys per CTA; BR = 4 or 8 where
+// a sequence and KV head has no more rows, else 16 (of 64 single tokens over 3900
+// the CTAs of 16 took 292 us, those of 4 132).  Scores: a key per thread, its K
+// row straight from memory, the rows of q broadcast from shared memory (a row at
+// a time through shared-memory tiles, as many rows want it, left this kernel
+// waiting for each 64 keys in turn).  Then a softmax, the rows dealt to the warps,
+// and O = P V with the keys dealt to the warps.  Up to 8 splits are a thread-block
+// cluster and meet in distributed shared memory, more meet through the workspace
+// (k_attn_simt_merge, by the same arithmetic).
+// Bound by latency where rows are few: the key's row, the softmax, V, each a chain
+// of loads, then the merge; three blocks of 8 over 300 to 1500 tokens, 4 heads of
+// 64: 11 us.  Many of them, 64 x 8 over 3900: 3.0 TB/s.
+template <int DP, int BR> struct FewCfg {
+  static constexpr int LQ = DP + 4, LP = BR + 4, LS = kSplit + 4;
+  static constexpr int AREA = BR * (8 * DP > LS ? 8 * DP : LS);  // scores, later the warps' sums
+  static constexpr size_t SMEM = sizeof(float) * (BR * LQ + AREA + kSplit * LP) + kSplit * 8 + BR * 8;
+};
+template <int DP, int BR>
+__global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView kv, int splits, int cluster) {
+  using C = FewCfg<DP, BR>;
+  constexpr int LQ = C::LQ, LP = C::LP, LS = C::LS;
   constexpr int COLS = DP / 4, SLICES = 32 / (COLS < 32 ? COLS : 32);  // column groups; key slices within a warp
   extern __shared__ float4 smem4[];
-  float* sQ = reinterpret_cast<float*>(smem4);  // [16][LQ]
-  float* sS = sQ + BR * LQ;                     // [16][LS] scores; later the warps' sums [8][16][DP]
+  float* sQ = reinterpret_cast<float*>(smem4);  // [BR][LQ]
+  float* sS = sQ + BR * LQ;                     // [BR][LS] scores; later the warps' sums [8][BR][DP]
   float* sO = sS;
-  float* sP = sS + (8 * BR * DP > BR * LS ? 8 * BR * DP : BR * LS);  // [256][LP]
+  float* sP = sS + C::AREA;                     // [256][LP]
   int64_t* sV = reinterpret_cast<int64_t*>(sP + kSplit * LP);        // [256] where the key's V lies, -1: nowhere
-  float2* sML = reinterpret_cast<float2*>(sV + kSplit);              // [16]
+  float2* sML = reinterpret_cast<float2*>(sV + kSplit);              // [BR]
   pdl_trigger();
   pdl_wait();
-  const int b = blockIdx.z, kvh = blockIdx.y, split = blockIdx.x % splits, r0 = blockIdx.x / splits * BR;
+  const int per = cluster > 1 ? cluster : splits;  // CTAs of 16 rows
+  const int b = blockIdx.z, kvh = blockIdx.y, split = blockIdx.x % per, r0 = blockIdx.x / per * BR;
   const Seq s = load_seq(r, b);
   if (!s.ok) {
     if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
@@ -116,7 +157,14 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
   }
   const int G = a.Hq / a.Hkv, R = s.n * G;
   if (r0 >= R) return;
-  if (split > 0 && split * kSplit >= s.len) return;  // the merge does not look at it either
+  const bool idle = split > 0 && split * kSplit >= s.len;  // the merge does not look at it either
+  if (idle && cluster == 1) return;
+  cg::cluster_group cl = cg::this_cluster();
+  if (idle) {
+    cl.sync();
+    cl.sync();
+    return;
+  }
   const int ctx = s.len - s.n, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   // keys that any of the rows sees, within this split
   const int p_first = ctx + r0 / G, p_last = ctx + (min(r0 + BR, R) - 1) / G;
@@ -170,10 +218,11 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
     sS[i * LS + tid] = see ? sc[i] * sl2 : -INFINITY;
   }
   const bool guard = __syncthreads_or(hidden && here);
-  // ---- softmax: warp w has rows 2 w and 2 w + 1
+  // ---- softmax: warp w has rows w, w + 8
 #pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int i = 2 * warp + u;
+  for (int u = 0; u < (BR + 7) / 8; ++u) {
+    const int i = warp + 8 * u;
+    if (BR < 8 && i >= BR) break;
     float x[kSplit / 32], m = -INFINITY, l = 0.f;
 #pragma unroll
     for (int j = 0; j < kSplit / 32; ++j) {
@@ -231,9 +280,7 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
     if (slice == 0) *reinterpret_cast<float4*>(sO + (warp * BR + i) * DP + col) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
   }
   __syncthreads();
-  for (int e = tid; e < BR * COLS; e += 256) {
-    const int i = e / COLS, c = e % COLS * 4;
-    if (r0 + i >= R) continue;
+  auto sum_warps = [&](int i, int c) {
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < 8; ++w) {
@@ -243,6 +290,34 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
       o.z += t.z;
       o.w += t.w;
     }
+    return o;
+  };
+  if (cluster > 1) {
+    float* sC = sP;  // [BR][DP], this split's sums (P has been used)
+    for (int e = tid; e < BR * COLS; e += 256) {
+      const int i = e / COLS, c = e % COLS * 4;
+      *reinterpret_cast<float4*>(sC + i * DP + c) = sum_warps(i, c);
+    }
+    cl.sync();
+    // rank q of the ns at work finishes every ns-th stretch of 256 column groups
+    const int ns = max(1, min(splits, (s.len + kSplit - 1) / kSplit));
+    for (int e = split * 32 + lane + warp * 32 * ns; e < BR * COLS; e += 8 * 32 * ns) {
+      const int i = e / COLS, c = e % COLS * 4;
+      if (r0 + i >= R) continue;
+      SplitMerge m;
+      for (int j = 0; j < ns; ++j) m.max(cl.map_shared_rank(sML, j)[i].x);
+#pragma unroll 4
+      for (int j = 0; j < ns; ++j)
+        m.add(cl.map_shared_rank(sML, j)[i], *reinterpret_cast<const float4*>(cl.map_shared_rank(sC, j) + i * DP + c));
+      m.store(a, s.start + (r0 + i) / G, kvh * G + (r0 + i) % G, c);
+    }
+    cl.sync();  // no CTA leaves while its sums are read
+    return;
+  }
+  for (int e = tid; e < BR * COLS; e += 256) {
+    const int i = e / COLS, c = e % COLS * 4;
+    if (r0 + i >= R) continue;
+    const float4 o = sum_warps(i, c);
     const float2 ml = sML[i];
     const int tok = s.start + (r0 + i) / G, h = kvh * G + (r0 + i) % G;
     if (splits > 1) {
@@ -493,33 +568,28 @@ __global__ void __launch_bounds__(256) k_attn_simt_merge(Ragged r, AttnCall a, i
   if (!s.ok || tok < s.start || tok >= s.start + s.n) return;
   const int ns = max(1, min(splits, (s.len + kSplit - 1) / kSplit));
   const float* p = a.ws + w * splits * (a.d + 4);
-  float M = -INFINITY;
-  for (int j = lane; j < ns; j += 32) M = fmaxf(M, p[(int64_t)j * (a.d + 4)]);
-  M = warp_max(M);
-  const float mref = M == -INFINITY ? 0.f : M;
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  SplitMerge m;
+  for (int j = lane; j < ns; j += 32) m.max(p[(int64_t)j * (a.d + 4)]);
+  m.M = warp_max(m.M);
   const int col = 4 * lane < a.d ? 4 * lane : 0;
 #pragma unroll 4
   for (int j = 0; j < ns; ++j) {
     const float* q = p + (int64_t)j * (a.d + 4);
-    const float2 ml = *reinterpret_cast<const float2*>(q);
-    const float4 v = load4(q + 4 + col);  // (zeros where the split saw no key)
-    const float f = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
-    L = fmaf(f, ml.y, L);
-    acc.x = fmaf(f, v.x, acc.x);
-    acc.y = fmaf(f, v.y, acc.y);
-    acc.z = fmaf(f, v.z, acc.z);
-    acc.w = fmaf(f, v.w, acc.w);
+    m.add(*reinterpret_cast<const float2*>(q), load4(q + 4 + col));
   }
-  const float inv = M == -INFINITY ? 0.f : 1.f / L;
-  if (4 * lane < a.d)
-    store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + 4 * lane,
-           make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
-  if (a.lse && lane == 0) a.lse[w] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+  m.store(a, tok, h, 4 * lane);
 }
 
 bool few_rows(const Ragged& r, const AttnCall& a) { return (int64_t)r.max_rows * (a.Hq / a.Hkv) <= kFewRows; }
+// (16 CTAs leave SMs of a GPC empty: one token each of 64 sequences over 3900 292 us
+// through the workspace, 371 in clusters of 16; over 1900 151 and 155, of 1 16.5 and 13)
+constexpr int kMaxSplitCluster = 8;
+// CTAs of a cluster that holds all splits; 1: too many, they meet in the workspace
+int split_cluster(int splits) {
+  int c = 1;
+  while (c < splits) c *= 2;
+  return c <= kMaxSplitCluster ? c : 1;
+}
 int simt_splits(const Ragged& r, const AttnCall& a) { return few_rows(r, a) ? (r.max_len + kSplit - 1) / kSplit : 1; }
 
 template <typename K>
@@ -528,6 +598,7 @@ cudaError_t allow_smem(K kernel, size_t smem, std::atomic<bool> (&done)[64]) {
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess || (dev < 64 && done[dev])) return e;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
   if (e == cudaSuccess && dev < 64) done[dev] = true;
   return e;
 }
@@ -542,14 +613,19 @@ cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cu
     const int64_t tiles = (rows + C::BR - 1) / C::BR;
     return launch_k(k_attn_tiles<DP>, (unsigned)(tiles * r.batch * a.Hkv), C::NG * 128, C::SMEM, st, r, a, kv);
   }
-  constexpr size_t area = 8 * 16 * DP > 16 * (kSplit + 4) ? 8 * 16 * DP : 16 * (kSplit + 4);
-  constexpr size_t smem = sizeof(float) * (16 * (DP + 4) + area + kSplit * 20) + kSplit * 8 + 16 * 8;
-  static std::atomic<bool> done[64];
-  if (cudaError_t e = allow_smem(k_attn_few<DP>, smem, done)) return e;
-  const int splits = simt_splits(r, a);
-  cudaError_t e = launch_k(k_attn_few<DP>, dim3((unsigned)((rows + 15) / 16 * splits), a.Hkv, r.batch), 256, smem, st, r,
-                           a, kv, splits);
-  if (e != cudaSuccess || splits == 1) return e;
+  const int splits = simt_splits(r, a), cluster = split_cluster(splits);
+  auto few = [&](auto br, std::atomic<bool> (&done)[64]) {
+    constexpr int BR = decltype(br)::value;
+    constexpr size_t smem = FewCfg<DP, BR>::SMEM;
+    if (cudaError_t e = allow_smem(k_attn_few<DP, BR>, smem, done)) return e;
+    return launch_kc(k_attn_few<DP, BR>, dim3((unsigned)((rows + BR - 1) / BR * (cluster > 1 ? cluster : splits)), a.Hkv, r.batch),
+                     256, smem, st, cluster, r, a, kv, splits, cluster);
+  };
+  static std::atomic<bool> done4[64], done8[64], done16[64];
+  const cudaError_t e = rows <= 4   ? few(std::integral_constant<int, 4>(), done4)
+                        : rows <= 8 ? few(std::integral_constant<int, 8>(), done8)
+                                    : few(std::integral_constant<int, 16>(), done16);
+  if (e != cudaSuccess || splits == 1 || cluster > 1) return e;
   return launch_k(k_attn_simt_merge, (unsigned)(((int64_t)r.total * a.Hq + 7) / 8), 256, 0, st, r, a, splits);
 }
 
@@ -557,7 +633,7 @@ cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cu
 
 int64_t attn_simt_workspace(const Ragged& r, const AttnCall& a) {
   const int64_t splits = simt_splits(r, a);
-  return splits == 1 ? 0 : (int64_t)r.total * a.Hq * splits * (a.d + 4) * 4;
+  return splits == 1 || split_cluster((int)splits) > 1 ? 0 : (int64_t)r.total * a.Hq * splits * (a.d + 4) * 4;
 }
 
 cudaError_t launch_attn_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st) {

@@ -637,3 +637,20 @@ def test_starts_that_decrease_are_reported(dtype, rows, lens):
     assert int(st.item()) == 2 and bool(((out == 7) | (out == 0)).all())
     with pytest.raises(D.DFlashError):
         D.dflash_status_check(st)
+
+
+@pytest.mark.parametrize("d", [64, 100])
+def test_fp32_rows_do_not_depend_on_the_bounds(d):
+    """Splits that meet in a cluster (up to 2048 tokens) and in the workspace (a larger max_len): the same bits;
+    and so for a block alone and beside a longer one (fewer and more rows to a CTA)."""
+    B = Batch("f32", 4, 2, d, 16, [1, 4, 30], [2000, 900, 300], seed=21)
+    B.table = torch.nn.functional.pad(B.table, (0, 200), value=-7)
+    n = B.starts[-1]
+    out, lse, _, _ = run_paged(B, True, 0, max_len=2000)
+    check_attention(out, lse, ref_paged(B, True, 0), n)
+    far, far_lse, _, _ = run_paged(B, True, 0, max_len=5000)
+    assert same_bits(out[:n], far[:n]) and torch.equal(lse[:n], far_lse[:n])
+    B.rows, B.lens, B.starts = B.rows[:2], B.lens[:2], B.starts[:3]
+    B.table = B.table[:2].contiguous()
+    few, few_lse, _, _ = run_paged(B, True, 0, max_len=2000)
+    assert same_bits(out[:5], few[:5]) and torch.equal(lse[:5], few_lse[:5])
