@@ -45,10 +45,8 @@ __global__ void __launch_bounds__(256) k_kv_append(Ragged r, const uint4* __rest
   if (b >= r.batch) return;  // behind the last sequence
   const Seq s = load_seq(r, b);
   const int i = row - s.start;
-  if (!s.ok || i < 0 || i >= s.n) {
-    if (lane == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
-    return;
-  }
+  if (!s.ok && lane == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+  if (!s.ok || i < 0 || i >= s.n) return;  // (in front of the first sequence: no one's row)
   const int pos = s.len - s.n + i;
   const int pg = r.table[(int64_t)b * r.table_stride + (pos >> page_shift)];
   if (pg < 0 || pg >= n_pages) {

@@ -654,3 +654,55 @@ def test_fp32_rows_do_not_depend_on_the_bounds(d):
     B.table = B.table[:2].contiguous()
     few, few_lse, _, _ = run_paged(B, True, 0, max_len=2000)
     assert same_bits(out[:5], few[:5]) and torch.equal(lse[:5], few_lse[:5])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows", [[2, 4, 1], [90, 1, 70]])
+def test_rows_in_front_of_the_first_sequence_are_left_alone(dtype, rows):
+    """starts[0] > 0: those rows belong to no sequence, and nothing is wrong with that."""
+    B = Batch(dtype, 4, 2, 64, 16, rows, [n + 40 for n in rows], seed=13)
+    ref = ref_paged(B, True, 0)
+    kp, vp = B.appended()
+    n, pad = B.starts[-1], 3
+    B.q, B.k, B.v = (torch.cat([torch.full_like(x[:pad], math.nan), x]) for x in (B.q, B.k, B.v))
+    B.starts = [s + pad for s in B.starts]
+    st = i32([0])
+    out, lse, gk, gv = run_paged(B, True, 0, status=st)
+    assert int(st.item()) == 0 and same_bits(gk.cpu(), kp) and same_bits(gv.cpu(), vp)
+    check_attention(out[pad:], lse[pad:], ref, n)
+    assert bool((out[:pad] == 7).all()) and bool((lse[:pad] == 7).all()) and bool((out[pad + n:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,lens", [([b % 3 for b in range(75)], [5 + 31 * b for b in range(75)]),
+                                       ([(37 * b) % 120 for b in range(70)], [130 + 3 * b for b in range(70)])])
+def test_batches_of_more_than_32_sequences(dtype, rows, lens):
+    """Sequences without rows among them, lengths from one key tile to many."""
+    B = Batch(dtype, 4, 1, 64, 32, rows, lens, seed=17)
+    st = i32([0])
+    out, lse, _, _ = run_paged(B, True, 0, status=st)
+    assert int(st.item()) == 0
+    check_attention(out, lse, ref_paged(B, True, 0), B.starts[-1])
+    assert bool((out[B.starts[-1]:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_largest_batch(dtype):
+    """32768 sequences of one token over a page each."""
+    D = lib()
+    n, d, L = 32768, 64, 8
+    g = torch.Generator(device="cuda").manual_seed(3)
+    q = torch.randn((n, 1, d), device="cuda", generator=g).to(DT[dtype])
+    kp, vp = (torch.randn((n, 8, 1, d), device="cuda", generator=g).to(DT[dtype]) for _ in range(2))
+    out, st = torch.empty_like(q), i32([0])
+    table = torch.arange(n, dtype=torch.int32, device="cuda").view(n, 1)
+    D.dflash_paged_attention(q, kp, vp, torch.arange(n + 1, dtype=torch.int32, device="cuda"),
+                             torch.full((n,), L, dtype=torch.int32, device="cuda"), table, out, max_rows=1, status=st)
+    assert int(st.item()) == 0
+    s = torch.einsum("nd,nld->nl", q[:, 0].double(), kp[:, :, 0].double()) * d ** -0.5
+    p = torch.softmax(s, 1)
+    ref = torch.einsum("nl,nld->nd", p, vp[:, :, 0].double())
+    # fp32: a few steps of the sums; bf16: P and the output round, half a step each of |p| |v| summed and of the result
+    av = torch.einsum("nl,nld->nd", p, vp[:, :, 0].double().abs())
+    tol = av * 2.0 ** -18 + (av * 2.0 ** -8 + ref.abs() * 2.0 ** -8 if dtype == "bf16" else 0)
+    assert bool(((out[:, 0].double() - ref).abs() <= tol).all())
