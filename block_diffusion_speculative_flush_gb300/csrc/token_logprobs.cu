@@ -335,7 +335,10 @@ __global__ void __launch_bounds__(TH, 4) k_token_logprobs(dflash_logprobs a, int
     __syncthreads();
     return have;
   };
-  int batch = 0, refresh = 2;
+  // first ranking of the candidates: after two batches; none of a slice of three
+  // (16 rows of fp32 with 20 entries 13.4 -> 12.9 us; long rows with 32 159 us, 165
+  // after four)
+  int batch = 0, refresh = v1 - v0 <= 3 * U * TH ? 4 : 2;
   if (v0 < v1) {
     uint4 cur[U], nxt[U];
     const uint32_t none = sizeof(T) == 4 ? 0xff800000u : 0xff80ff80u;  // -inf
