@@ -7,7 +7,7 @@
 // One pass over the logits: (m, s, t) per thread, rescaled when its maximum
 // grows, and the top entries beside it.  Bound by reading the logits once: 2047
 // rows of 151936 bf16 in 98 us without top entries, 6.3 TB/s (94% of a measured
-// copy), 116 with 5, 159 with 32.  16 rows of fp32 are latency: 6 us without, 13
+// copy), 116 with 5, 159 with 32.  16 rows of fp32 are latency: 6 us without, 12.5
 // with 20.
 //
 // A row belongs to a cluster of 1..16 CTAs, as many as give every SM two CTAs
