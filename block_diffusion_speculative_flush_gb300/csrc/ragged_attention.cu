@@ -90,6 +90,10 @@ __device__ __forceinline__ bool kv_at(const Ragged& r, const KVView& kv, int b, 
   return pg >= 0 && pg < kv.n_pages;
 }
 
+// The natural log-sum-exp of a row from (m, l) in the exp2 domain: -inf where every
+// score is, NaN where one is.  (Every row sees its own key: l is never 0 for want of one.)
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
+
 // The splits of one row and four columns, taken in split order.
 struct SplitMerge {
   float M = -INFINITY, L = 0.f;
@@ -106,12 +110,12 @@ struct SplitMerge {
     acc.w = fmaf(f, v.w, acc.w);
   }
   __device__ __forceinline__ void store(const AttnCall& a, int tok, int h, int c) const {
-    const float inv = M == -INFINITY ? 0.f : 1.f / L;
+    const float inv = 1.f / L;
     if (c < a.d)
       store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + c,
              make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv));
     if (a.lse && c == 0)
-      a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+      a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
   }
 };
 
@@ -324,12 +328,12 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
       if (c < a.d) store4(w + 4 + c, o);
       continue;
     }
-    const float inv = ml.x == -INFINITY ? 0.f : 1.f / ml.y;
+    const float inv = 1.f / ml.y;
     if (c < a.d)
       store4(reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + c,
              make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
     if (a.lse && c == 0)
-      a.lse[(int64_t)tok * a.Hq + h] = ml.x == -INFINITY ? -INFINITY : (ml.x + log2f(ml.y)) * 0.6931471805599453f;
+      a.lse[(int64_t)tok * a.Hq + h] = lse_of(ml.x, ml.y);
   }
 }
 
@@ -525,7 +529,7 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
 #pragma unroll
     for (int g = 1; g < NG; ++g) {
       const float2 ml = *reinterpret_cast<const float2*>(sK + g * C::GROUP + 2 * (ty * RM + i));
-      if (ml.x == -INFINITY) continue;
+      if (ml.y == 0.f) continue;  // no key, or none above -inf (a NaN score makes it NaN, m stays -inf)
       const float mn = fmaxf(m[i], ml.x), f = m[i] == -INFINITY ? 0.f : exp2f(m[i] - mn), e = exp2f(ml.x - mn);
       m[i] = mn;
       l[i] = l[i] * f + ml.y * e;
@@ -540,7 +544,7 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
       }
     }
     const int tok = s.start + rr / G, h = kvh * G + rr % G;
-    const float inv = m[i] == -INFINITY ? 0.f : 1.f / l[i];
+    const float inv = 1.f / l[i];
     float* o = reinterpret_cast<float*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head;
 #pragma unroll
     for (int cc = 0; cc < DP / 64; ++cc)
@@ -548,7 +552,7 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
         store4(o + cc * 64 + tx * 4, make_float4(acc[i][cc * 4] * inv, acc[i][cc * 4 + 1] * inv,
                                                  acc[i][cc * 4 + 2] * inv, acc[i][cc * 4 + 3] * inv));
     if (a.lse && tx == 0)
-      a.lse[(int64_t)tok * a.Hq + h] = m[i] == -INFINITY ? -INFINITY : (m[i] + log2f(l[i])) * 0.6931471805599453f;
+      a.lse[(int64_t)tok * a.Hq + h] = lse_of(m[i], l[i]);
   }
 }
 

@@ -249,15 +249,20 @@ template <int D>
 __device__ __forceinline__ float2* part_ml(const AttnCall& a, const Plan& p, int slot, int row) {
   return reinterpret_cast<float2*>(a.ws + (int64_t)p.slots * p.ws_rows * D) + (int64_t)slot * p.ws_rows + row;
 }
+// The statistics of a part as the merges take them.  A NaN score makes l NaN but
+// never becomes the maximum, so m may still be -inf, which is what a part that saw
+// no key has: NaN, it cannot be taken for one.
+__device__ __forceinline__ float2 part_stats(float m, float l) { return make_float2(l != l ? l : m, l); }
+// The natural log-sum-exp of a row: -inf where every score is, NaN where one is.
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * kLn2; }
 // (m, l) of a partial (row r of tile x), or the log-sum-exp of packed row tok, head h
 template <int D>
 __device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, int part, int x, int r, int tok, int h,
                                             float m, float l) {
   if (part >= 0) {
-    *part_ml<D>(a, p, part, x * 128 + r) = make_float2(m, l);
+    *part_ml<D>(a, p, part, x * 128 + r) = part_stats(m, l);
   } else if (a.lse) {
-    a.lse[(int64_t)tok * a.Hq + h] =
-        m == -INFINITY ? -INFINITY : (m + log2f(l)) * kLn2;
+    a.lse[(int64_t)tok * a.Hq + h] = lse_of(m, l);
   }
 }
 __device__ __forceinline__ bf16* row_out(const AttnCall& a, const Work& w, int i, int h) {
@@ -327,7 +332,7 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
     }
     const bool cluster = p.mode == kModeCluster;
     if (lane == 0) {
-      if (cluster) c_ml[rr] = make_float2(m, l);
+      if (cluster) c_ml[rr] = part_stats(m, l);
       else store_stats<D>(a, p, w.part, x, rr, w.start + i, h, m, l);
     }
     if (w.part >= 0) {
@@ -336,7 +341,7 @@ __device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, 
       for (int c = 0; c < C; ++c) o[c] = acc[c];
     } else {
       bf16* o = row_out(a, w, i, h) + lane * C;
-      const float inv = m == -INFINITY ? 0.f : 1.f / l;
+      const float inv = 1.f / l;
 #pragma unroll
       for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
     }
@@ -1066,7 +1071,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         redo_rows<D>(r, a, kv, p, w, x, warp & 3, c_o, c_ml);  // rows in turn over all four warps
         give_back();
       } else if (live) {
-        const float inv = m == -INFINITY ? 0.f : 1.f / l;
+        const float inv = 1.f / l;  // (every row sees its own key: l is 0 only where all scores are -inf)
         if (NQ == 1 && p.mode == kModeCluster) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -1080,7 +1085,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
                 *reinterpret_cast<float4*>(c_o + row * (D + 4) + c + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
             }
           }
-          if (valid) c_ml[row] = make_float2(T > 0 ? m : -INFINITY, l);
+          if (valid) c_ml[row] = part_stats(m, l);
         } else {
           if (valid) store_stats<D>(a, p, part, x, row, tok, h, m, l);
           // where this lane's own row starts, in 16-byte units
@@ -1177,6 +1182,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       float2 ml = make_float2(-INFINITY, 0.f);
       if (lane < S) ml = *cl.map_shared_rank(c_ml + rr, lane);
       const float M = warp_max(ml.x);
+      // a part that saw no key has weight 0; the NaN of a part with a NaN score stays one
       const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
       const float L = warp_sum(wt == 0.f ? 0.f : ml.y * wt);
       float acc[CL];
@@ -1193,13 +1199,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         for (int j = 0; j < CL; ++j) acc[j] = fmaf(wu, v[j], acc[j]);
       }
       const int i = rr / G, h = kvh * G + rr % G;
-      const float inv = M == -INFINITY ? 0.f : 1.f / L;
+      const float inv = 1.f / L;
       bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)(s.start + i) * a.o_row + (int64_t)h * a.o_head + lane * CL;
 #pragma unroll
       for (int j = 0; j < CL; j += 2)
         *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
       if (a.lse && lane == 0)
-        a.lse[(int64_t)(s.start + i) * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+        a.lse[(int64_t)(s.start + i) * a.Hq + h] = lse_of(M, L);
     }
     cluster_sync_relaxed();  // no CTA leaves while a peer reads its part
   }
@@ -1280,13 +1286,13 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
       return rr < p.tpt * G && i < min(i0 + p.tok, sn) ? start + i : -1;
     };
     auto put = [&](int row, int tok, float M, float L, const float* acc) {
-      const float inv = M == -INFINITY ? 0.f : 1.f / L;
+      const float inv = 1.f / L;
       const int h = kvh * G + row % 128 % G;
       bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + lane * C;
 #pragma unroll
       for (int j = 0; j < C; j += 2)
         *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(acc[j] * inv, acc[j + 1] * inv);
-      if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = M == -INFINITY ? -INFINITY : (M + log2f(L)) * kLn2;
+      if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
     };
     constexpr int PP = 32 / RW;
     if (RW > 1 && parts <= PP) {
@@ -1298,7 +1304,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
       float M = ml.x;
 #pragma unroll
       for (int o = PP / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-      // a part that saw no key has weight 0 and its sums were not written; a NaN maximum stays one
+      // a part that saw no key has weight 0 and its sums were not written; the NaN of a part stays one
       const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
       float L = wt == 0.f ? 0.f : ml.y * wt;
 #pragma unroll
@@ -1354,7 +1360,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
         load(0);
         const float Mn = fmaxf(M, warp_max(ml.x)), mref = Mn == -INFINITY ? 0.f : Mn;
         const float f = M == -INFINITY ? 0.f : exp2f(M - mref);
-        // a part that saw no key has weight 0 and its sums were not written; a NaN maximum stays one
+        // a part that saw no key has weight 0 and its sums were not written; the NaN of a part stays one
         const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
         M = Mn;
         L = L * f + warp_sum(wt == 0.f ? 0.f : ml.y * wt);

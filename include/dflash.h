@@ -579,7 +579,9 @@ typedef struct dflash_ragged {
  * key r < length unless causal != 0 and r > p, or window > 0 and p - r >= window
  * (causal == 0: the new rows see each other, as a bidirectional block does).  A
  * row that sees no key gets zeros and lse -inf.  What a row does not see never
- * reaches it, whatever its bits (NaN and infinities among them).
+ * reaches it, whatever its bits (NaN and infinities among them); a NaN among the
+ * scores that it sees makes its output and lse NaN, and where all of them are
+ * -inf there is no distribution: the output is NaN, lse -inf.
  * Scores, sums and accumulators are fp32; a bf16 call rounds the probabilities
  * to bf16 for the second product.  out overlaps no input. */
 typedef struct dflash_attention {

@@ -1,0 +1,85 @@
+"""Values that are not finite where a row sees them: the target-side
+attention answers NaN (or an infinity) whatever the layout of the work, and
+its rows beside them stay right.  What a row does not see never reaches it
+(tests/test_gpu_target_ops.py); here is the other half."""
+import math
+
+import pytest
+import torch
+
+from oracle import target_ops_oracle as O
+from tests.test_gpu_target_ops import DT, Batch, check_attention, i32, lib, ref_paged, run_paged
+
+pytestmark = pytest.mark.gpu
+
+# dtype, new rows, lengths, query heads: the bf16 calls run as a cluster, as ranges of one row tile, as whole items
+# of two and as ranges of two; the fp32 ones as splits that meet in a cluster, in the workspace, and as row tiles
+LAYOUTS = [("bf16", [16], [3000], 8), ("bf16", [1, 1, 1], [30011, 700, 16384], 8), ("bf16", [200, 90], [900, 700], 4),
+           ("bf16", [300, 2, 150], [2100, 3000, 150], 8), ("f32", [8, 1], [1500, 300], 4), ("f32", [8, 1], [5000, 300], 4),
+           ("f32", [90, 70], [700, 1100], 4)]
+IDS = ["cluster", "ranges-1", "items", "ranges-2", "few-cluster", "few-workspace", "tiles"]
+
+
+@pytest.mark.parametrize("layout", range(len(LAYOUTS)), ids=IDS)
+@pytest.mark.parametrize("components", [1, 64])
+def test_a_query_that_is_not_a_number(layout, components):
+    """One head of some rows holds NaN (one component, or all): that head's output and lse are NaN, not the zeros
+    and -inf of a row that sees no key; every other row is right."""
+    dtype, rows, lens, hq = LAYOUTS[layout]
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=layout)
+    ref = ref_paged(B, True, 0)
+    n = B.starts[-1]
+    hit = torch.zeros((n, hq), dtype=torch.bool)
+    for b in range(len(rows)):
+        hit[B.starts[b], 0] = hit[B.starts[b + 1] - 1, hq - 1] = True
+    B.q[:n][hit] = torch.where(torch.arange(64) < components, math.nan, B.q[:n][hit].float()).to(DT[dtype])
+    out, lse, _, _ = run_paged(B, True, 0)
+    out, lse = out[:n].cpu(), lse[:n].cpu()
+    assert bool(torch.isnan(out[hit]).all()) and bool(torch.isnan(lse[hit]).all())
+    out, lse = out[~hit][:, None], lse[~hit][:, None]
+    check_attention(out, lse, tuple(x[:n][~hit][:, None] for x in ref), out.shape[0])
+
+
+@pytest.mark.parametrize("layout", range(len(LAYOUTS)), ids=IDS)
+@pytest.mark.parametrize("which", ["first_half", "every_fourth_64"])
+def test_a_part_of_the_keys_is_not_a_number(layout, which):
+    """K of KV head 1 is NaN over whole parts of the key axis, finite elsewhere: every row of its query heads sees
+    such a key and is NaN; the other head's rows are right."""
+    dtype, rows, lens, hq = LAYOUTS[layout]
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=layout)
+    ref = ref_paged(B, True, 0)
+    n, half = B.starts[-1], hq // 2
+    B.kp, B.vp = B.appended()
+    for b, L in enumerate(lens):
+        for p in range(L - rows[b] + 1):   # keys that the first new row sees too
+            if (p < max(1, (L - rows[b]) // 2)) if which == "first_half" else p // 64 % 4 == (1 if L - rows[b] >= 64 else 0):
+                B.kp[int(B.table[b, p // 16]), p % 16, 1] = math.nan
+    out, lse, _, _ = run_paged(B, True, 0, append=False)
+    assert bool(torch.isnan(out[:n, half:]).all()) and bool(torch.isnan(lse[:n, half:]).all())
+    check_attention(out[:n, :half], lse[:n, :half], tuple(x[:n, :half] for x in ref), n)
+
+
+@pytest.mark.parametrize("layout", range(len(LAYOUTS)), ids=IDS)
+def test_scores_of_minus_infinity(layout):
+    """Scores that overflow to -inf on a part of the keys have probability zero; where a row sees nothing else
+    there is no distribution: NaN, and the log of an empty sum."""
+    dtype, rows, lens, hq = LAYOUTS[layout]
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=layout)
+    n, far = B.starts[-1], 3e38
+    B.kp, B.vp = B.appended()
+    B.q[:] = 1.0
+    for b, L in enumerate(lens):
+        for p in range(L):   # 64 x -3e38 is past the fp32 range; finite in fp64, where its exponential is 0 as well
+            if b > 0 or p < (L - rows[b]) // 2:
+                B.kp[int(B.table[b, p // 16]), p % 16] = -far
+    s1 = B.starts[1]
+    ref = O.attention(B.q[:s1], O.gather(B.kp, lens[:1], B.table), O.gather(B.vp, lens[:1], B.table), B.starts[:2],
+                      lens[:1], True, 0, 0.125, dtype == "bf16")
+    # (the oracle's bound takes its hidden weight's |q||k| along: here those keys count for nothing)
+    near = B.kp.clone()
+    near[near < -1e30] = -60.0
+    tol = O.attention(B.q[:s1], O.gather(near, lens[:1], B.table), O.gather(B.vp, lens[:1], B.table), B.starts[:2],
+                      lens[:1], True, 0, 0.125, dtype == "bf16")[2:]
+    out, lse, _, _ = run_paged(B, True, 0, append=False)
+    check_attention(out[:s1], lse[:s1], (*ref[:2], *tol), s1)
+    assert bool(torch.isnan(out[s1:n]).all()) and bool(torch.isneginf(lse[s1:n]).all())
