@@ -90,6 +90,19 @@ __device__ __forceinline__ bool kv_at(const Ragged& r, const KVView& kv, int b, 
   return pg >= 0 && pg < kv.n_pages;
 }
 
+// Hidden keys among the scores and the probabilities of k_attn_few: V may hold
+// anything there, and 0 x NaN is NaN, so their products are skipped.  Not every
+// product with P = 0 is: a NaN that the row sees is its own, although its
+// probability underflows.  The score of a hidden key is a NaN that no operation
+// makes (theirs are 0x7fffffff), which a maximum passes over; its probability is
+// -0, which exp2f never returns.
+constexpr uint32_t kHidden = 0xffc0de00u;
+__device__ __forceinline__ float masked_score(float s, bool see) { return see ? s : __uint_as_float(kHidden); }
+__device__ __forceinline__ float masked_prob(float s, float mref) {
+  return __float_as_uint(s) == kHidden ? -0.f : exp2f(s - mref);
+}
+__device__ __forceinline__ bool is_hidden(float p) { return __float_as_uint(p) == 0x80000000u; }
+
 // The natural log-sum-exp of a row from (m, l) in the exp2 domain: -inf where every
 // score is, NaN where one is.  (Every row sees its own key: l is never 0 for want of one.)
 __device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * 0.6931471805599453f; }
@@ -217,7 +230,7 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
     const int p = ctx + (r0 + i) / G;
     const bool see = here && r0 + i < R && pos >= vis_lo(p, a.window) && pos < vis_hi(p, s.len, a.causal);
     hidden |= !see;
-    sS[i * LS + tid] = see ? sc[i] * sl2 : -INFINITY;
+    sS[i * LS + tid] = masked_score(sc[i] * sl2, see);
   }
   const bool guard = __syncthreads_or(hidden && here);
   // ---- softmax: warp w has rows w, w + 8
@@ -235,7 +248,7 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
     const float mref = m == -INFINITY ? 0.f : m;
 #pragma unroll
     for (int j = 0; j < kSplit / 32; ++j) {
-      const float e = exp2f(x[j] - mref);
+      const float e = masked_prob(x[j], mref);
       l += e;
       sP[(lane + 32 * j) * LP + i] = e;
     }
@@ -264,8 +277,7 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
       const float pv[4] = {p4.x, p4.y, p4.z, p4.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        // a row's hidden keys have P = 0, and V may be anything there
-        if (!guard || pv[i] != 0.f) {
+        if (!guard || !is_hidden(pv[i])) {
           acc[i4 + i][0] = fmaf(pv[i], v4.x, acc[i4 + i][0]);
           acc[i4 + i][1] = fmaf(pv[i], v4.y, acc[i4 + i][1]);
           acc[i4 + i][2] = fmaf(pv[i], v4.z, acc[i4 + i][2]);
@@ -475,6 +487,12 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
     // P rows of this thread's row group come from the same half warp
     __syncwarp();
     auto product = [&](auto guarded) {
+      int from[RM], keys[RM];  // keys [from, from + keys) of the tile are the row's
+#pragma unroll
+      for (int i = 0; i < RM; ++i) {
+        from[i] = lo[i] - t0;
+        keys[i] = max(hi[i] - lo[i], 0);
+      }
 #pragma unroll 2
       for (int kk = 0; kk < BK; kk += 4) {
         float4 p4[RM];
@@ -489,7 +507,7 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
             for (int i = 0; i < RM; ++i) {
               const float pv = u == 0 ? p4[i].x : u == 1 ? p4[i].y : u == 2 ? p4[i].z : p4[i].w;
               float* o = acc[i] + cc * 4;
-              if (!decltype(guarded)::value || pv != 0.f) {
+              if (!decltype(guarded)::value || (unsigned)(kk + u - from[i]) < (unsigned)keys[i]) {
                 o[0] = fmaf(pv, v4.x, o[0]);
                 o[1] = fmaf(pv, v4.y, o[1]);
                 o[2] = fmaf(pv, v4.z, o[2]);
@@ -500,8 +518,8 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
         }
       }
     };
-    // A key that a row does not see has P = 0; its V may still be NaN or
-    // infinite, so tiles with hidden keys skip those products.
+    // A row's hidden keys have P = 0, and V may be anything there: tiles with
+    // some skip those products.  (Not every product with P = 0, as above.)
     if (__any_sync(0xffffffffu, masked)) product(std::true_type());
     else product(std::false_type());
   }

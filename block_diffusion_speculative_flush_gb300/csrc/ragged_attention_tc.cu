@@ -1305,6 +1305,7 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
 #pragma unroll
       for (int o = PP / 2; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
       // a part that saw no key has weight 0 and its sums were not written; the NaN of a part stays one
+      const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
       const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
       float L = wt == 0.f ? 0.f : ml.y * wt;
 #pragma unroll
@@ -1323,7 +1324,9 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
           for (int k = 0; k < RW; ++k) {
             w[u][k] = __shfl_sync(0xffffffffu, wt, k * PP + ((q0 + u) & (PP - 1)));
             if (q0 + u >= parts) w[u][k] = 0.f;
-            load_if<C>(v[u][k], part_o<D>(a, p, slot_of(q0 + u), row0 + 8 * k) + lane * C, w[u][k] != 0.f);
+            // (a weight that underflows still takes its sums along: 0 x NaN is NaN)
+            load_if<C>(v[u][k], part_o<D>(a, p, slot_of(q0 + u), row0 + 8 * k) + lane * C,
+                       q0 + u < parts && ((saw >> (k * PP + q0 + u)) & 1u));
           }
 #pragma unroll
         for (int u = 0; u < 2; ++u)
@@ -1360,7 +1363,8 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
         load(0);
         const float Mn = fmaxf(M, warp_max(ml.x)), mref = Mn == -INFINITY ? 0.f : Mn;
         const float f = M == -INFINITY ? 0.f : exp2f(M - mref);
-        // a part that saw no key has weight 0 and its sums were not written; the NaN of a part stays one
+        // (weights as above)
+        const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
         const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
         M = Mn;
         L = L * f + warp_sum(wt == 0.f ? 0.f : ml.y * wt);
@@ -1371,8 +1375,9 @@ __global__ void __launch_bounds__(256, 4) k_ragged_merge(Ragged r, AttnCall a, P
 #pragma unroll
           for (int q = 0; q < 8; ++q) {
             const float wq = q0 + q < cnt ? __shfl_sync(0xffffffffu, wt, (q0 + q) & 31) : 0.f;
+            const bool yes = q0 + q < cnt && ((saw >> (q0 + q)) & 1u);
 #pragma unroll
-            for (int j = 0; j < C; ++j) acc[j] = fmaf(wq, wq == 0.f ? 0.f : v[q][j], acc[j]);
+            for (int j = 0; j < C; ++j) acc[j] = fmaf(wq, yes ? v[q][j] : 0.f, acc[j]);
           }
         }
       }

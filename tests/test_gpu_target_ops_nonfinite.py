@@ -83,3 +83,38 @@ def test_scores_of_minus_infinity(layout):
     out, lse, _, _ = run_paged(B, True, 0, append=False)
     check_attention(out[:s1], lse[:s1], (*ref[:2], *tol), s1)
     assert bool(torch.isnan(out[s1:n]).all()) and bool(torch.isneginf(lse[s1:n]).all())
+
+
+@pytest.mark.parametrize("layout", range(len(LAYOUTS)), ids=IDS)
+@pytest.mark.parametrize("which", ["first_new", "last_cached", "first_half"])
+def test_a_seen_value_whose_probability_underflows(layout, which):
+    """V is NaN at a key that every row sees and whose probability is 0 in fp32 (its score is 256 below the
+    others'): 0 x NaN is NaN in that column, in tiles with and without hidden keys and in parts of weight 0."""
+    dtype, rows, lens, hq = LAYOUTS[layout]
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=layout)
+    B.kp, B.vp = B.appended()
+    B.q[:] = 8.0
+    n = B.starts[-1]
+    for b, L in enumerate(lens):
+        first = L - rows[b]
+        far = {"first_new": [first], "last_cached": [max(first - 1, 0)], "first_half": list(range(max(1, first // 2)))}[which]
+        if first == 0 or (which == "first_new" and rows[b] == 1):
+            far = []   # a row's only key, or no row beside it
+        for p in range(L):
+            pg, sl = int(B.table[b, p // 16]), p % 16
+            B.kp[pg, sl] = -2.0 if p in far else 2.0
+            if p in far[:1]:
+                B.vp[pg, sl, :, 7] = math.nan
+        rows_b = slice(B.starts[b], B.starts[b + 1])
+        B.far = getattr(B, "far", torch.zeros(n, dtype=torch.bool))
+        B.far[rows_b] = bool(far)
+        if which == "first_new" and far:
+            B.far[B.starts[b]] = False   # its own row may see nothing else
+    fixed = B.vp.nan_to_num(0, 0, 0)
+    ref = O.attention(B.q[:n], O.gather(B.kp, lens, B.table), O.gather(fixed, lens, B.table), B.starts, lens, True, 0,
+                      0.125, dtype == "bf16")
+    out, lse, _, _ = run_paged(B, True, 0, append=False)
+    out, lse = out[:n].cpu(), lse[:n].cpu()
+    assert bool(torch.isnan(out[B.far][..., 7]).all())
+    keep = [c for c in range(64) if c != 7]
+    check_attention(out[..., keep], lse, (ref[0][..., keep], ref[1], ref[2][..., keep], ref[3]), n)
