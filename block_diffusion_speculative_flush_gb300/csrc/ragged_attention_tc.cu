@@ -27,9 +27,9 @@
 //          are what limits it), 6.0 with pages of 64 (89% of a measured copy).  Few
 //          short items are latency: 15 us for one block of 16 tokens over 4096.
 // V rows of hidden keys may hold anything, and 0 * NaN is NaN: in tiles with
-// hidden keys the fixer zeroes the rows behind the sequence and looks for
-// non-finite numbers in the others; if it finds one, the softmax warps redo
-// their rows on the CUDA cores from the definition (redo_rows).
+// hidden keys the fixer zeroes the rows behind the sequence and puts non-finite
+// numbers in the others to 0; the softmax warps then add those to the rows that
+// see them (add_nonfinite).
 //
 // Work is laid out on the device from the lengths there, in one of three ways:
 //   items   whole items, longest first (by key tiles, counted by binary search,
@@ -90,7 +90,7 @@ struct Work {
   int32_t nt[2];         // key tiles of each 128-row tile
   int32_t part;          // partial slot, or -1: the whole item
   int32_t clean_lo, clean_hi;  // keys that every row sees
-  int32_t bad;           // set by the fixer, a bit per 128-row tile: a hidden key's V is not finite
+  int32_t bad;           // set by the fixer, a bit per 128-row tile: values of V were put to 0
   int32_t done;
 };
 
@@ -265,85 +265,66 @@ __device__ __forceinline__ void store_stats(const AttnCall& a, const Plan& p, in
     a.lse[(int64_t)tok * a.Hq + h] = lse_of(m, l);
   }
 }
-__device__ __forceinline__ bf16* row_out(const AttnCall& a, const Work& w, int i, int h) {
-  return reinterpret_cast<bf16*>(a.out) + (int64_t)(w.start + i) * a.o_row + (int64_t)h * a.o_head;
-}
 
-// The rows of tile x of a work stretch, from the definition, on the CUDA
-// cores: lanes over the keys for the scores, over the columns for the sums.
-// Only for stretches with a non-finite V among their hidden keys.
+// Halves of a pair of bf16 with an exponent of ones (infinities and NaN): bits 15 and 31.
+__device__ __forceinline__ uint32_t nonfinite_bits(uint32_t w) { return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u; }
+__device__ __forceinline__ uint32_t nonfinite_bits(uint4 q) {
+  return nonfinite_bits(q.x) | nonfinite_bits(q.y) | nonfinite_bits(q.z) | nonfinite_bits(q.w);
+}
+__device__ __forceinline__ uint32_t finite_or_0(uint32_t w) { return w & ~((nonfinite_bits(w) >> 15) * 0xffffu); }
+
+// Adds the values that the fixer put to 0 in a stretch's V tiles to the rows that
+// see them: an infinity or a NaN times a probability, which is above 0, is itself.
+// A row per lane, token i's; its O in TMEM.  V is read again from the cache, only
+// in the tiles that the fixer looked at.  Those lie at the two edges of an item's
+// keys, at most tok / 128 + 2 at each: what this takes does not grow with the length
+// (one block of 16 over 4096: 14 us, 24 with one such key, 35 with 15).
 template <int D>
-__device__ __noinline__ void redo_rows(Ragged r, AttnCall a, KVView kv, Plan p, const Work& w, int x, int warp4,
-                                       float* c_o, float2* c_ml) {
-  constexpr int C = D / 32;
-  const int lane = threadIdx.x & 31, G = a.Hq / a.Hkv, ctx = w.len - w.n;
-  const int rows = min(p.tpt, min(p.tok, w.n - w.i0) - x * p.tpt) * G;
-  const float sl2 = a.scale * kLog2e;
-  const int k0 = w.t0 * KT, k1 = min((w.t0 + max(w.nt[0], w.nt[1])) * KT, w.len);
-  for (int rr = warp4; rr < rows; rr += 4) {
-    const int i = w.i0 + x * p.tpt + rr / G, h = w.kvh * G + rr % G, pos = ctx + i;
-    const int lo = max(vis_lo(pos, a.window), k0), hi = min(vis_hi(pos, w.len, a.causal), k1);
-    const bf16* q = reinterpret_cast<const bf16*>(a.q) + (int64_t)(w.start + i) * a.q_row + (int64_t)h * a.q_head;
-    float m = -INFINITY, l = 0.f, acc[C];
-#pragma unroll
-    for (int c = 0; c < C; ++c) acc[c] = 0.f;
-    for (int base = lo; base < hi; base += 32) {
+__device__ __noinline__ void add_nonfinite(Ragged r, KVView kv, const Work& w, uint32_t tO, int i, int window,
+                                           int causal) {
+  const int pos = w.len - w.n + i, lo = vis_lo(pos, window), hi = vis_hi(pos, w.len, causal);
+  const int lane = threadIdx.x & 31, T = max(w.nt[0], w.nt[1]);
+  for (int t = 0; t < T; ++t) {
+    const int kt = (w.t0 + t) * KT, in = min(KT, w.len - kt);
+    if (kt >= w.clean_lo && kt + in <= w.clean_hi) {  // and so are all up to the edge
+      t = max(t, w.clean_hi / KT - 1 - w.t0);
+      continue;
+    }
+    for (int base = kt; base < kt + in; base += 32) {
       const int j = base + lane;
-      float s = -INFINITY;
-      int64_t vo = -1;
-      if (j < hi) {
-        int64_t ko;
-        bool ok = true;
+      const uint4* v = nullptr;
+      uint32_t found = 0;
+      if (j < kt + in) {
+        int64_t at = (int64_t)(w.start + j) * kv.v_slot;
+        bool there = true;
         if (kv.paged) {
           const int pg = r.table[(int64_t)w.b * r.table_stride + (j >> kv.page_shift)];
-          const int sl = j & ((1 << kv.page_shift) - 1);
-          ok = pg >= 0 && pg < kv.n_pages;
-          ko = pg * kv.page + sl * kv.k_slot;
-          vo = pg * kv.page + sl * kv.v_slot;
-        } else {
-          ko = (int64_t)(w.start + j) * kv.k_slot;
-          vo = (int64_t)(w.start + j) * kv.v_slot;
+          there = pg >= 0 && pg < kv.n_pages;  // (otherwise zeros)
+          at = pg * kv.page + (j & ((1 << kv.page_shift) - 1)) * kv.v_slot;
         }
-        s = 0.f;
-        if (ok) {
-          const bf16* k = reinterpret_cast<const bf16*>(kv.k) + ko + w.kvh * kv.k_head;
-          for (int c = 0; c < D; ++c) s = fmaf(__bfloat162float(q[c]), __bfloat162float(k[c]), s);
-          s *= sl2;
-        } else {
-          vo = -1;
+        if (there) {
+          v = reinterpret_cast<const uint4*>(reinterpret_cast<const bf16*>(kv.v) + at + w.kvh * kv.v_head);
+          for (int c = 0; c < D / 8; ++c) found |= nonfinite_bits(v[c]);
         }
       }
-      const float mn = fmaxf(m, warp_max(s)), mref = mn == -INFINITY ? 0.f : mn;
-      const float f = m == -INFINITY ? 0.f : exp2f(m - mref);
-      const float pv = j < hi ? exp2f(s - mref) : 0.f;
-      l = l * f + warp_sum(pv);
-      m = mn;
+      uint32_t todo = __ballot_sync(0xffffffffu, found != 0);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const bf16* e = reinterpret_cast<const bf16*>(__shfl_sync(0xffffffffu, (unsigned long long)v, src));
+        const bool see = base + src >= lo && base + src < hi;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tO + c, o);
 #pragma unroll
-      for (int c = 0; c < C; ++c) acc[c] *= f;
-      const int cnt = min(32, hi - base);
-      for (int u = 0; u < cnt; ++u) {
-        const float pu = __shfl_sync(0xffffffffu, pv, u);
-        const int64_t o = __shfl_sync(0xffffffffu, vo, u);
-        if (o < 0) continue;
-        const bf16* v = reinterpret_cast<const bf16*>(kv.v) + o + w.kvh * kv.v_head;
-#pragma unroll
-        for (int c = 0; c < C; ++c) acc[c] = fmaf(pu, __bfloat162float(v[lane * C + c]), acc[c]);
+          for (int k = 0; k < 32; ++k) {
+            const float x = __bfloat162float(e[c + k]);
+            if (see && !isfinite(x)) o[k] += x;
+          }
+          tmem_st32(tO + c, o);
+        }
       }
-    }
-    const bool cluster = p.mode == kModeCluster;
-    if (lane == 0) {
-      if (cluster) c_ml[rr] = part_stats(m, l);
-      else store_stats<D>(a, p, w.part, x, rr, w.start + i, h, m, l);
-    }
-    if (w.part >= 0) {
-      float* o = (cluster ? c_o + rr * (D + 4) : part_o<D>(a, p, w.part, x * 128 + rr)) + lane * C;
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = acc[c];
-    } else {
-      bf16* o = row_out(a, w, i, h) + lane * C;
-      const float inv = 1.f / l;
-#pragma unroll
-      for (int c = 0; c < C; ++c) o[c] = __float2bfloat16_rn(acc[c] * inv);
     }
   }
 }
@@ -936,18 +917,19 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           if (kt < w.clean_lo || kt + in > w.clean_hi) {
             uint32_t found = 0;
             for (int e = lane; e < in * 8; e += 32)
-              for (int c = 0; c < NB; ++c) {
-                const uint4 q = *reinterpret_cast<const uint4*>(v + c * (SLOT / NB) + e * 16);
-                // an exponent of ones carries into bit 15 (or 31)
-                found |= (q.x & 0x7f807f80u) + 0x00800080u;
-                found |= (q.y & 0x7f807f80u) + 0x00800080u;
-                found |= (q.z & 0x7f807f80u) + 0x00800080u;
-                found |= (q.w & 0x7f807f80u) + 0x00800080u;
-              }
-            // (only for the tiles that take this product: their warps all look
-            // behind it, a tile that has ended already might see it in some)
-            if (__any_sync(0xffffffffu, (found & 0x80008000u) != 0) && lane == 0)
-              works[ws].bad |= (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0);
+              for (int c = 0; c < NB; ++c)
+                found |= nonfinite_bits(*reinterpret_cast<const uint4*>(v + c * (SLOT / NB) + e * 16));
+            if (__builtin_expect(__any_sync(0xffffffffu, found != 0), 0)) {
+#pragma unroll 1
+              for (int e = lane; e < in * 32; e += 32)
+                for (int c = 0; c < NB; ++c) {
+                  uint32_t* pair = reinterpret_cast<uint32_t*>(v + c * (SLOT / NB)) + e;
+                  *pair = finite_or_0(*pair);
+                }
+              // (only for the row tiles that take this product: their warps all look
+              // behind it, a tile that has ended already might see it in some)
+              if (lane == 0) works[ws].bad |= (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0);
+            }
           }
           fence_proxy_async();
           __syncwarp();
@@ -1057,20 +1039,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       // of the stores: behind them the arrival, a release, would wait for them.
       const int part = w.part, tok = w.start + i;
       const bool bad = T > 0 && ((*(volatile const int32_t*)&w.bad >> x) & 1);
-      auto give_back = [&] {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&w_empty[ws]);
-      };
-      if (!bad) give_back();
+      if (__builtin_expect(bad && live, 0)) add_nonfinite<D>(r, kv, w, tO, i, a.window, a.causal);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&w_empty[ws]);
       // Up to 8 rows of a warp (single tokens) each lane stores its own, which is
       // little code; more go through shared memory.
       const uint32_t rows = __ballot_sync(0xffffffffu, valid);
-      const bool staged = NQ == 2 || (live && !bad && p.mode != kModeCluster && __popc(rows) > 8);
+      const bool staged = NQ == 2 || (live && p.mode != kModeCluster && __popc(rows) > 8);
       if (NQ == 1 && T > 0 && !staged && lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
-      if (bad) {
-        redo_rows<D>(r, a, kv, p, w, x, warp & 3, c_o, c_ml);  // rows in turn over all four warps
-        give_back();
-      } else if (live) {
+      if (live) {
         const float inv = 1.f / l;  // (every row sees its own key: l is 0 only where all scores are -inf)
         if (NQ == 1 && p.mode == kModeCluster) {
 #pragma unroll 1

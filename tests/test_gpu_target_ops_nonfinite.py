@@ -118,3 +118,57 @@ def test_a_seen_value_whose_probability_underflows(layout, which):
     assert bool(torch.isnan(out[B.far][..., 7]).all())
     keep = [c for c in range(64) if c != 7]
     check_attention(out[..., keep], lse, (ref[0][..., keep], ref[1], ref[2][..., keep], ref[3]), n)
+
+
+def test_a_hidden_value_that_is_not_finite_in_a_long_cache():
+    """15 chunks of 300 tokens as whole items over a million cached keys (one set of pages serves them all but for
+    the last): the value of one new token is NaN. The rows in front of it are right, the ones that see it NaN, and
+    the call takes no longer for it than its waits allow (status 0)."""
+    D = lib()
+    seqs, n, L, page, h, d = 15, 300, 1_000_000, 1024, 8, 64
+    g = torch.Generator(device="cuda").manual_seed(4)
+    per = L // page + 1
+    kp, vp = (torch.randn((per - 1 + seqs, page, h, d), device="cuda", generator=g).bfloat16() for _ in range(2))
+    q = torch.randn((seqs * n, h, d), device="cuda", generator=g).bfloat16()
+    table = torch.arange(per, dtype=torch.int32, device="cuda").repeat(seqs, 1)
+    table[:, per - 1] += torch.arange(seqs, dtype=torch.int32, device="cuda")
+    assert (L - n) // page == per - 1   # every sequence's new rows are in its own last page
+    at = L - n + 255
+    clean = vp[per - 1, at % page].clone()
+    vp[per - 1, at % page, :, 9] = math.nan
+    st, out, lse = i32([0]), torch.full_like(q, 7.0), torch.empty((seqs * n, h), device="cuda")
+    D.dflash_paged_attention(q, kp, vp, i32([b * n for b in range(seqs + 1)]), i32([L] * seqs), table, out, max_rows=n,
+                             max_len=L, lse=lse, status=st)
+    assert int(st.item()) == 0
+    assert bool(torch.isnan(out[255:n, :, 9]).all())
+    assert int(torch.isnan(out).sum()) == (n - 255) * h
+    vp[per - 1, at % page] = clean
+    for head in (0, 7):
+        k, v = (x[:per, :, head].reshape(-1, d)[:L].cpu().double() for x in (kp, vp))
+        rows = torch.tensor([0, 127, 128, 254])
+        ref = O.attention_row_block(q[:n][rows, head].cpu().double(), k, v, L - n + rows, L, True, 0, 0.125, True)
+        check_attention(out[:n][rows, head][:, None], lse[:n][rows, head][:, None], tuple(x[:, None] for x in ref), 4)
+
+
+@pytest.mark.parametrize("layout", range(4), ids=IDS[:4])
+@pytest.mark.parametrize("value", [math.inf, -math.inf])
+def test_infinities_beside_hidden_keys(layout, value):
+    """V is infinite at every new key, in the column of its number: rows that see it answer that infinity there,
+    all other columns and rows stay finite and right."""
+    dtype, rows, lens, hq = LAYOUTS[layout]
+    B = Batch(dtype, hq, 2, 64, 16, rows, lens, seed=layout)
+    B.kp, B.vp = B.appended()
+    ref = O.attention(B.q[:B.starts[-1]], O.gather(B.kp, lens, B.table), O.gather(B.vp, lens, B.table), B.starts, lens,
+                      True, 0, 0.125, dtype == "bf16")
+    seen = torch.zeros((B.starts[-1], 64), dtype=torch.bool)
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        for i in range(min(n, 60)):
+            p = L - n + i
+            B.vp[int(B.table[b, p // 16]), p % 16, :, i] = value
+            seen[B.starts[b] + i:B.starts[b + 1], i] = True
+    out, lse, _, _ = run_paged(B, True, 0, append=False)
+    out = out[:B.starts[-1]].cpu()
+    hit = seen[:, None].expand_as(out)
+    assert bool((out[hit] == value).all())
+    out, o, tol = (torch.where(hit, 0.0, x.double()) for x in (out, ref[0], ref[2]))
+    check_attention(out, lse, (o, ref[1], tol, ref[3]), B.starts[-1])
