@@ -420,7 +420,7 @@ __global__ void __launch_bounds__(TileCfg<DP>::NG * 128) k_attn_tiles(Ragged r, 
     for (int e = tid; e < BK * (DP / 4); e += 128) {
       const int kk = e / (DP / 4), c = e % (DP / 4) * 4, pos = t0 + kk;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f), y = x;
-      if (pos < k_hi && c < a.d) {
+      if (pos >= k_lo && pos < k_hi && c < a.d) {
         int64_t ko, vo;
         if (kv_at(r, kv, b, s.start, pos, ko, vo)) {
           x = load4(Kb + ko + c);

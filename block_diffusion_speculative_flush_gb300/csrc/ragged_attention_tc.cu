@@ -704,7 +704,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         const int next = page_of(t + 1);
         const bool mine = issuer && (!kv.paged || kt + box * page_rows < w.len);
         if (kv.paged && mine && (pg < 0 || pg >= kv.n_pages)) {
-          flag_status(r.status, DFLASH_STATUS_PAGE);
+          // (in front of every row's window it may be gone)
+          if (kt + (box + 1) * page_rows > vis_lo(w.len - w.n + w.i0, a.window)) flag_status(r.status, DFLASH_STATUS_PAGE);
           pg = kv.n_pages;  // just outside the map: zeros arrive
         }
         const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * 128;

@@ -526,7 +526,9 @@ DFLASH_API int dflash_target_exactness_probe(dflash_target* t, const int32_t* to
  * zeroes, or NULL) and never read or written through:
  *   2  a sequence's starts or length break the bounds below: its rows are left
  *      as they were (starts that decrease: so may other sequences' rows be);
- *   4  a page id outside [0, n_pages): read as zeros, an append to it dropped;
+ *   4  a page id outside [0, n_pages) where a row sees a key (pages that the window
+ *      of every row has left behind may be gone): read as zeros, an append to it
+ *      dropped;
  *   1  a token id that is neither -1 nor in [0, vocab) (dflash_token_logprobs);
  *   8  a bounded wait expired: the outputs are incomplete.
  * dflash_status_check reads and clears the word. */
