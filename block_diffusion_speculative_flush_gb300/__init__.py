@@ -643,15 +643,27 @@ def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
         _check(lib.dflash_kv_append(_abi.PACK_PAGES(*p), r, kh, vh, _stream_of(stream, device)))
 
 
-def dflash_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages) -> int:
-    """Bytes a dflash_paged_attention call of these tensors and bounds needs."""
+def dflash_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages,
+                               causal: bool = True, window: int = 0) -> int:
+    """Bytes a dflash_paged_attention call of these tensors, bounds, causal and window needs. With lens and
+    table None: those of a dflash_prompt_attention call, k_pages and v_pages being its k and v (max_len is
+    not used)."""
     device = _same_device(q, out, starts, lens, table, k_pages, v_pages)
-    p = _pages(k_pages, v_pages)
-    r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, None)
-    qh = _heads(q, q.shape, k_pages.dtype, "q")
-    a = _abi.PACK_ATTENTION(p[0], q.shape[1], p[1], p[2], 1, 0, 1.0, *qh, *qh, 0, 0, 0)
+    shape = q.shape
+    qh = _heads(q, shape, k_pages.dtype, "q")
+    if (lens is None) != (table is None):
+        raise ValueError("lens and table go together")
+    if lens is None:
+        if q.dtype not in _DTYPES or k_pages.dim() != 3:
+            raise ValueError("k, v: fp32 or bf16 [rows, n_kv_heads, head_dim]")
+        dtype, kv_heads, pages = _DTYPES[q.dtype], k_pages.shape[1], None
+    else:
+        p = _pages(k_pages, v_pages)
+        dtype, kv_heads, pages = p[0], p[1], _abi.PACK_PAGES(*p)
+    r = _ragged(starts, lens, table, shape[0], max_rows, max_len, None)
+    a = _abi.PACK_ATTENTION(dtype, shape[1], kv_heads, shape[2], 1 if causal else 0, int(window), 1.0, *qh, *qh, 0, 0, 0)
     with _on_device(device):
-        return _check(lib.dflash_attention_workspace(a, r, _abi.PACK_PAGES(*p)))
+        return _check(lib.dflash_attention_workspace(a, r, pages))
 
 
 def dflash_paged_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, starts: torch.Tensor,

@@ -1456,8 +1456,9 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
   p.cluster = 1;
   if (h.nq == 1 && p.mode == kModeRanges) {
     const int64_t all = (int64_t)r.batch * a.Hkv;
-    const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
-    const int64_t most = (span + KT - 1) / KT + (a.window ? 1 : 0);
+    // (a window's keys may begin anywhere in a tile, but it has no more tiles than the sequence)
+    const int64_t span = std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows);
+    const int64_t most = a.window ? std::min<int64_t>(tiles, (span + KT - 1) / KT + 1) : tiles;
     for (int S = 2; S <= kMaxCluster && S <= 2 * most && all * S <= sms; S *= 2)
       if (all <= clusters_at_once(a.d, S) && most <= 7 * S && most > 1) {
         p.mode = kModeCluster;

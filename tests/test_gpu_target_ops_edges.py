@@ -4,7 +4,7 @@ sized ahead, status words."""
 import pytest
 import torch
 
-from tests.test_gpu_target_ops import Batch, check_attention, i32, ref_paged, run_paged
+from tests.test_gpu_target_ops import DT, Batch, check_attention, i32, lib, ref_paged, run_paged, same_bits
 
 pytestmark = pytest.mark.gpu
 
@@ -29,3 +29,40 @@ def test_pages_behind_the_window_may_be_gone(dtype, rows, lens, hq):
     B.table[b, (lens[b] - rows[b] - W + 1) // 16] = -1
     run_paged(B, True, W, append=False, status=status)
     assert int(status.item()) == 4
+
+
+@pytest.mark.parametrize("window", [0, 100, 1 << 20])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("tiles", [7, 14, 27, 28, 29, 55, 56, 57, 111, 112, 113])
+def test_a_workspace_of_the_reported_size_serves_the_call(tiles, causal, window):
+    """bf16 blocks of 16 with 8 KV heads around the lengths (7 key tiles for each CTA of a cluster) where the
+    layout of the work, and with it the workspace, changes."""
+    D = lib()
+    L, page, hkv, hq, d, n = tiles * 128, 256, 8, 16, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(tiles)
+    kp, vp = (torch.randn((tiles // 2 + 1, page, hkv, d), device="cuda", generator=g).bfloat16() for _ in range(2))
+    q = torch.randn((n, hq, d), device="cuda", generator=g).bfloat16()
+    table = torch.arange(tiles // 2 + 1, dtype=torch.int32, device="cuda")[None]
+    args = i32([0, n]), i32([L]), table
+    want, got = torch.empty_like(q), torch.empty_like(q)
+    need = D.dflash_attention_workspace(q, got, *args, n, L, kp, vp, causal=causal, window=window)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    D.dflash_paged_attention(q, kp, vp, *args, got, n, max_len=L, causal=causal, window=window, workspace=ws)
+    D.dflash_paged_attention(q, kp, vp, *args, want, n, max_len=L, causal=causal, window=window)
+    assert same_bits(got.cpu(), want.cpu())
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("rows,hq", [([9], 4), ([300, 1500], 8), ([2000], 2)])
+def test_a_workspace_of_the_reported_size_serves_a_prompt(dtype, rows, hq):
+    D = lib()
+    n = sum(rows)
+    q, k, v = (torch.randn((n, h, 64), device="cuda").to(DT[dtype]) for h in (hq, 2, 2))
+    st = i32([0] + [sum(rows[:i + 1]) for i in range(len(rows))])
+    for window in (0, 200):
+        want, got = torch.empty_like(q), torch.empty_like(q)
+        need = D.dflash_attention_workspace(q, got, st, None, None, max(rows), 0, k, v, window=window)
+        ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+        D.dflash_prompt_attention(q, k, v, st, got, max(rows), window=window, workspace=ws)
+        D.dflash_prompt_attention(q, k, v, st, want, max(rows), window=window)
+        assert same_bits(got.cpu(), want.cpu())
