@@ -31,14 +31,17 @@ namespace cg = cooperative_groups;
 // ---------------------------------------------------------------------------
 // One warp per new row: 16 bytes of K and of V per lane and step.  Bound by
 // memory (2 reads and 2 writes of a row's Hkv d elements) for many rows: 6257 of
-// 8 heads of 128 in 6.4 us, 8.0 TB/s, as they stay in L2.  64 rows are the
+// 8 heads of 128 in 6.6 us, 7.7 TB/s, as they stay in L2.  64 rows are the
 // latency of starts, length, table, row: 3 us.
-__global__ void __launch_bounds__(256) k_kv_append(Ragged r, const uint4* __restrict__ k, const uint4* __restrict__ v,
-                                                   int64_t k_row, int64_t k_head, int64_t v_row, int64_t v_head,
-                                                   uint4* kp, uint4* vp, int64_t page_st, int64_t slot_st,
-                                                   int64_t head_st, int page_shift, int n_pages, int heads, int chunks) {
+__global__ void __launch_bounds__(256) k_kv_append(Ragged r, const uint4* k, const uint4* v, int64_t k_row,
+                                                   int64_t k_head, int64_t v_row, int64_t v_head,
+                                                   uint4* __restrict__ kp, uint4* __restrict__ vp, int64_t page_st,
+                                                   int64_t slot_st, int64_t head_st, int page_shift, int n_pages,
+                                                   int heads, int chunks) {
   pdl_trigger();
   pdl_wait();
+  k = after_wait(k);  // the rows may be the previous kernel's
+  v = after_wait(v);
   const int row = (int)(blockIdx.x * 8 + (threadIdx.x >> 5)), lane = threadIdx.x & 31;
   if (row >= r.total) return;
   const int b = seq_of_row(r, row);

@@ -3,6 +3,8 @@ bad argument is answered with a status before any device work, and the binding
 refuses tensors that the library would read or write out of bounds."""
 import ctypes as C
 import math
+import os
+import re
 
 import pytest
 import torch
@@ -209,3 +211,28 @@ def test_oracle_logprobs_by_hand():
     assert abs(float(lp[0]) - math.log(0.6)) < 1e-7
     assert abs(float(ent[0]) + 0.6 * math.log(0.6) + 0.4 * math.log(0.2)) < 1e-7
     assert ids[0].tolist() == [1, 0, 3, 2] and math.isinf(float(tlp[0, 3]))
+
+
+CSRC = os.path.join(os.path.dirname(D.__file__), "csrc")
+# read-only loads of these are right: weights, and tables that the host copied before the first launch
+CONSTANT = {"E", "W", "rope"}
+
+
+def kernels(source):
+    """(name, parameters, body) of every __global__ function of a file."""
+    text = open(os.path.join(CSRC, source)).read()
+    for m in re.finditer(r"__global__ void (?:__launch_bounds__\((?:[^()]|\([^()]*\))*\)\s+)?(\w+)\(", text):
+        end = text.index(") {\n", m.end())
+        yield m.group(1), text[m.end():end], text[end:text.index("\n}\n", end)]
+
+
+@pytest.mark.parametrize("source", ["ragged_attention.cu", "ragged_attention_tc.cu", "token_logprobs.cu"])
+def test_kernels_read_a_predecessors_rows_after_their_wait(source):
+    """A kernel starts while its predecessor still runs: what that one may write is never behind a const
+    __restrict__ pointer (which permits read-only loads, and loads before the wait) unless the pointer passes
+    through after_wait."""
+    found = list(kernels(source))
+    assert found
+    for name, params, body in found:
+        for p in re.findall(r"const [\w:]+\* __restrict__ (\w+)", params):
+            assert p in CONSTANT or f"{p} = after_wait({p})" in body, (name, p)
