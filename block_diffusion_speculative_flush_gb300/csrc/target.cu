@@ -46,6 +46,7 @@ __global__ void k_gather_rows(const float* __restrict__ E, const int32_t* __rest
                               float* __restrict__ x, int32_t* __restrict__ err) {
   pdl_trigger();
   pdl_wait();
+  tokens = after_wait(tokens);
   const int r = blockIdx.x;
   int t = tokens[r];
   if (t < 0 || t >= V) {
@@ -63,6 +64,7 @@ __global__ void k_target_qkv(const float* __restrict__ qkv, const float2* __rest
                              int64_t start, int64_t cap, int layer, float* __restrict__ Q, float* __restrict__ kv) {
   pdl_trigger();
   pdl_wait();
+  qkv = after_wait(qkv);  // the product just before
   const int r = blockIdx.x, h = blockIdx.y;
   const int half = d / 2, qd = nh * d;
   const float* row = qkv + (int64_t)r * 3 * qd;
@@ -152,6 +154,7 @@ void launch_gemm_rows(const float* X, int64_t ldx, const float* W, int64_t ldw, 
 __global__ void k_row_argmax(const float* __restrict__ logits, int V, int32_t* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
+  logits = after_wait(logits);
   const int r = blockIdx.x;
   ArgMax best{-INFINITY, INT32_MAX};
   for (int v = threadIdx.x; v < V; v += blockDim.x) best = better(best, ArgMax{logits[(int64_t)r * V + v], v});
@@ -202,6 +205,8 @@ __global__ void __launch_bounds__(256) k_logits_compare(const float* __restrict_
                                                         dflash_exactness_row* __restrict__ out) {
   pdl_trigger();
   pdl_wait();
+  block = after_wait(block);
+  chain = after_wait(chain);
   const int r = blockIdx.x;
   const ArgMax none{-INFINITY, INT32_MAX};
   Top2 tb{none, none}, tc{none, none};

@@ -226,7 +226,7 @@ def kernels(source):
         yield m.group(1), text[m.end():end], text[end:text.index("\n}\n", end)]
 
 
-@pytest.mark.parametrize("source", ["ragged_attention.cu", "ragged_attention_tc.cu", "token_logprobs.cu"])
+@pytest.mark.parametrize("source", ["ragged_attention.cu", "ragged_attention_tc.cu", "token_logprobs.cu", "target.cu"])
 def test_kernels_read_a_predecessors_rows_after_their_wait(source):
     """A kernel starts while its predecessor still runs: what that one may write is never behind a const
     __restrict__ pointer (which permits read-only loads, and loads before the wait) unless the pointer passes
