@@ -625,8 +625,14 @@ DFLASH_API int dflash_target_device_status(dflash_target* t) {
   if (rc != DFLASH_OK) return rc;
   int32_t e = 0;
   if ((rc = tcheck(cudaMemcpy(&e, t->d_err, 4, cudaMemcpyDeviceToHost), "target status")) != DFLASH_OK) return rc;
-  if (e) return tfail(DFLASH_ERR_DEVICE, "target: a token id outside [0, vocab)");
-  return !t->table ? DFLASH_OK : dflash_status_check(t->d_err + 1, t->st);
+  const char* bad_token = "target: a token id outside [0, vocab)";
+  // a paged target has the operators' word beside its own: read and cleared whatever this one says
+  rc = t->table ? dflash_status_check(t->d_err + 1, t->st) : DFLASH_OK;
+  if (!e || (rc != DFLASH_OK && rc != DFLASH_ERR_DEVICE)) return rc;
+  if (rc == DFLASH_OK) return tfail(DFLASH_ERR_DEVICE, bad_token);
+  char both[320];
+  snprintf(both, sizeof both, "%s; %s", bad_token, dflash_last_error());
+  return tfail(DFLASH_ERR_DEVICE, both);
 }
 
 }  // extern "C"

@@ -626,7 +626,7 @@ DFLASH_API int dflash_prompt_attention(const dflash_attention* a, const dflash_r
  * table_width * page_size, else DFLASH_ERR_CAPACITY.  The table is read at each
  * forward, so pages may be entered as the sequence grows.  All other calls take
  * the target as any other; dflash_target_device_status also reports the
- * operators' status. */
+ * operators' status, and clears it. */
 DFLASH_API int dflash_target_create_paged(const dflash_target_config* cfg, const dflash_target_weights* w,
                                           const dflash_kv_pages* pages, const int32_t* table, int32_t table_width,
                                           int64_t max_ctx, void* stream, dflash_target** out);

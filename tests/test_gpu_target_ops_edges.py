@@ -4,7 +4,9 @@ sized ahead, status words."""
 import pytest
 import torch
 
+from tests.test_gpu_paged_target import fwd, pool, table_of, weights_on_gpu
 from tests.test_gpu_target_ops import DT, Batch, check_attention, i32, lib, ref_paged, run_paged, same_bits
+from synthetic.target import TARGET_TINY
 
 pytestmark = pytest.mark.gpu
 
@@ -66,3 +68,22 @@ def test_a_workspace_of_the_reported_size_serves_a_prompt(dtype, rows, hq):
         D.dflash_prompt_attention(q, k, v, st, got, max(rows), window=window, workspace=ws)
         D.dflash_prompt_attention(q, k, v, st, want, max(rows), window=window)
         assert same_bits(got.cpu(), want.cpu())
+
+
+def test_a_paged_target_reports_both_status_words():
+    """A bad token id does not hide a bad page, before or after it; the page is reported once."""
+    D = lib()
+    _, dw = weights_on_gpu()
+    shape = TARGET_TINY
+    t = D.dflash_target_create_paged(shape.as_dict(), dw, pool(shape, 4, 16), table_of([0, 9, 2, 3]))
+    fwd(D, t, [1, shape.vocab, 2], 0, shape)
+    with pytest.raises(D.DFlashError) as e:
+        D.dflash_target_device_status(t)
+    assert "token id" in str(e.value) and "page" not in str(e.value)
+    fwd(D, t, [1] * 20, 3, shape)
+    with pytest.raises(D.DFlashError) as e:
+        D.dflash_target_device_status(t)
+    assert e.value.status == D.DFLASH_ERR_DEVICE and "page" in str(e.value) and "token id" in str(e.value)
+    with pytest.raises(D.DFlashError) as e:
+        D.dflash_target_device_status(t)
+    assert "page" not in str(e.value)
