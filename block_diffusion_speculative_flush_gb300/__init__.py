@@ -556,9 +556,10 @@ def _heads(t: torch.Tensor, shape, dtype: torch.dtype, what: str) -> tuple:
     st = t.stride()
     if t.dtype != dtype or len(shape) != 3 or (st[2] != 1 and shape[2] > 1):
         raise ValueError(f"{what}: a CUDA {dtype} tensor [rows, heads, head_dim] with a dense last dimension")
-    # torch may report any stride for a dimension of one entry; the library asks for one a head fits in
+    # torch may report any stride for a dimension of one entry, and nothing uses it; the library asks for
+    # one that is aligned and that a head fits in
     rows, heads, d = shape
-    return (t.data_ptr() if rows else 0, st[0] if rows > 1 else max(st[0], heads * d), st[1] if heads > 1 else d)
+    return (t.data_ptr() if rows else 0, st[0] if rows > 1 else heads * d, st[1] if heads > 1 else d)
 
 
 def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> tuple:
@@ -570,7 +571,7 @@ def _pages(k_pages: torch.Tensor, v_pages: torch.Tensor) -> tuple:
         raise ValueError("k_pages, v_pages: CUDA fp32 or bf16 [n_pages, page_size, n_kv_heads, head_dim] of one shape "
                          "and stride, with a dense last dimension")
     n, page, heads, d = shape
-    return (dtype, heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(), st[0] if n > 1 else max(st[0], d), st[1],
+    return (dtype, heads, d, page, n, k_pages.data_ptr(), v_pages.data_ptr(), st[0] if n > 1 else d, st[1],
             st[2] if heads > 1 else d)
 
 
@@ -591,7 +592,7 @@ def _ragged(starts, lens, table, total: int, max_rows: int, max_len: int, status
     if table.dtype != torch.int32 or len(shape) != 2 or shape[0] != batch or (st[1] != 1 and shape[1] > 1):
         raise ValueError(f"table: CUDA int32 [{batch}, pages per sequence] with a dense last dimension")
     return _abi.PACK_RAGGED(batch, total, max_rows, max_len, first, _int_vector(lens, batch, "lens"), table.data_ptr(),
-                            shape[1], st[0] if batch > 1 else max(st[0], shape[1]), word)
+                            shape[1], st[0] if batch > 1 else shape[1], word)
 
 
 def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse, ragged: bytes, pages, workspace,
@@ -728,7 +729,7 @@ def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: 
             raise ValueError("top_ids int32 and top_logprobs fp32: contiguous CUDA [rows, k] of one shape")
         top = top_ids.shape[1]
     ptr = lambda t: 0 if t is None else t.data_ptr()
-    a = _abi.PACK_LOGPROBS(logits.data_ptr(), st[0] if R > 1 else max(st[0], V), dtype, R, V, top, float(temperature),
+    a = _abi.PACK_LOGPROBS(logits.data_ptr(), st[0] if R > 1 else V, dtype, R, V, top, float(temperature),
                            tok, logprobs.data_ptr(), ptr(entropy), ptr(top_ids), ptr(top_logprobs),
                            0 if status is None else _int_vector(status, 1, "status"))
     with _on_device(device):

@@ -70,6 +70,25 @@ def test_a_workspace_of_the_reported_size_serves_a_prompt(dtype, rows, hq):
         assert same_bits(got.cpu(), want.cpu())
 
 
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+def test_the_stride_of_a_single_entry_does_not_matter(dtype):
+    """One row, one page, one sequence: torch may report any stride for such a dimension (a slice of a wider
+    buffer keeps the buffer's), and nothing ever uses it."""
+    D = lib()
+    B = Batch(dtype, 4, 2, 64, 16, [1], [9], tail=0, spare=0)
+    ref = ref_paged(B, True, 0)
+    odd = lambda t: torch.as_strided(t.cuda().contiguous(), t.shape, (1003, *t.contiguous().stride()[1:]))
+    q, k, v, kp, vp = (odd(t) for t in (B.q, B.k, B.v, B.kp, B.vp))
+    assert q.stride(0) == 1003 and kp.stride(0) == 1003
+    args = i32(B.starts), i32(B.lens), odd(B.table)
+    out, lse = odd(torch.full_like(B.q, 7.0)), torch.empty((1, 4), device="cuda")
+    D.dflash_kv_append(k, v, kp, vp, *args)
+    D.dflash_paged_attention(q, kp, vp, *args, out, max_rows=1, lse=lse)
+    check_attention(out, lse, ref, 1)
+    D.dflash_prompt_attention(q, k, v, i32([0, 1]), out, max_rows=1, lse=lse)
+    assert same_bits(out.cpu(), B.v.repeat_interleave(2, 1))   # its only key is itself
+
+
 def test_a_paged_target_reports_both_status_words():
     """A bad token id does not hide a bad page, before or after it; the page is reported once."""
     D = lib()
