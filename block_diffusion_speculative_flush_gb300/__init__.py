@@ -639,7 +639,8 @@ def dflash_kv_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_
     kh = _abi.PACK_HEADS(*_heads(k, shape, k_pages.dtype, "k"))
     vh = _abi.PACK_HEADS(*_heads(v, shape, k_pages.dtype, "v"))
     rows = shape[0]
-    r = _ragged(starts, lens, table, rows, max(1, rows), 1 << 30, status)
+    # (max_rows bounds the rows of a sequence, not of the call: the widest that the library takes)
+    r = _ragged(starts, lens, table, rows, max(1, min(rows, 1 << 24)), 1 << 30, status)
     with _on_device(device):
         _check(lib.dflash_kv_append(_abi.PACK_PAGES(*p), r, kh, vh, _stream_of(stream, device)))
 

@@ -89,6 +89,22 @@ def test_the_stride_of_a_single_entry_does_not_matter(dtype):
     assert same_bits(out.cpu(), B.v.repeat_interleave(2, 1))   # its only key is itself
 
 
+def test_an_append_of_more_rows_than_a_sequence_may_have():
+    """2^24 + 16 rows of two sequences: the bound on a sequence's rows is not one on the call's."""
+    D = lib()
+    n, page = (1 << 23) + 8, 1024
+    k, v = (torch.arange(2 * n * 4, device="cuda", dtype=torch.float32).view(2 * n, 1, 4) + i for i in range(2))
+    per = (n + page - 1) // page
+    kp, vp = (torch.zeros((2 * per, page, 1, 4), device="cuda") for _ in range(2))
+    st = i32([0])
+    D.dflash_kv_append(k, v, kp, vp, i32([0, n, 2 * n]), i32([n, n]), torch.arange(2 * per, dtype=torch.int32,
+                                                                                  device="cuda").view(2, per), status=st)
+    assert int(st.item()) == 0
+    for x, p in ((k, kp), (v, vp)):
+        p = p.view(2, per * page, 4)
+        assert torch.equal(p[:, :n].reshape(2 * n, 1, 4), x) and not bool(p[:, n:].any())
+
+
 def test_a_paged_target_reports_both_status_words():
     """A bad token id does not hide a bad page, before or after it; the page is reported once."""
     D = lib()
