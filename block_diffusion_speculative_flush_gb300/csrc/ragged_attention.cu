@@ -739,7 +739,9 @@ int check_attention(const char* call, const dflash_attention* a, bool pointers, 
     return rfail(DFLASH_ERR_SHAPE, call, "n_q_heads: a multiple of n_kv_heads, at most 128 per KV head");
   if ((a->causal != 0 && a->causal != 1) || a->window < 0 || a->window > (1 << 30))
     return rfail(DFLASH_ERR_INVALID_ARG, call, "causal 0 or 1, window 0 or 1..2^30");
-  if (!(a->scale > 0.f) || !std::isfinite(a->scale)) return rfail(DFLASH_ERR_INVALID_ARG, call, "scale: finite, > 0");
+  // (the kernels work with scale log2(e); an infinite one makes NaN of a score of 0)
+  if (!(a->scale > 0.f) || !std::isfinite(1.5f * a->scale))
+    return rfail(DFLASH_ERR_INVALID_ARG, call, "scale: > 0, 1.5 x scale finite");
   if (!pointers) return DFLASH_OK;
   if (int rc = check_heads(call, &a->q, a->dtype, a->n_q_heads, a->head_dim, rows)) return rc;
   if (int rc = check_heads(call, &a->out, a->dtype, a->n_q_heads, a->head_dim, rows)) return rc;

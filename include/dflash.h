@@ -593,7 +593,7 @@ typedef struct dflash_attention {
   int32_t head_dim;
   int32_t causal;      /* 0 or 1 */
   int32_t window;      /* 0 or 1..2^30 */
-  float scale;         /* finite, > 0 */
+  float scale;         /* > 0, 1.5 x scale finite */
   dflash_heads q;      /* [total_rows][n_q_heads][head_dim] */
   dflash_heads out;    /* the same shape */
   float* lse;          /* [total_rows][n_q_heads] natural log of the softmax sum, or NULL */

@@ -83,6 +83,14 @@ def test_bad_attention_is_refused(bad, code):
     assert D.lib.dflash_prompt_attention(C.byref(a), C.byref(b), C.byref(h), C.byref(h), None) == code
 
 
+def test_a_scale_that_overflows_in_the_exp2_domain_is_refused():
+    p, b, h = pages(), batch(total_rows=0), heads()
+    for scale, code in ((2.2e38, 0), (2.4e38, INVALID), (3.4e38, INVALID)):
+        a = attention(scale=scale)
+        assert D.lib.dflash_paged_attention(C.byref(a), C.byref(b), C.byref(p), None) == code
+        assert D.lib.dflash_prompt_attention(C.byref(a), C.byref(b), C.byref(h), C.byref(h), None) == code
+
+
 def test_null_and_mismatched_arguments_are_refused():
     p, b, h, a = pages(), batch(), heads(), attention()
     r = C.byref
