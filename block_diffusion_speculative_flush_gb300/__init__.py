@@ -404,6 +404,7 @@ def dflash_target_create_paged(cfg: dict, weights: dict, pages, table: torch.Ten
     pages = list(pages)
     if len(pages) != cfg["n_layers"]:
         raise ValueError("pages: one (k_pages, v_pages) pair per layer")
+    _same_device(weights["embed"], table, *(t for kv in pages for t in kv))
     arr = (_abi.dflash_kv_pages * len(pages))(*[_abi.dflash_kv_pages(*_pages(k, v)) for k, v in pages])
     width = table.numel()
     _int_vector(table, width, "table")

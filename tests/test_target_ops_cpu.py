@@ -188,6 +188,30 @@ def test_the_binding_refuses_host_tensors_and_wrong_shapes():
         D.dflash_status_check(i(1))
 
 
+def test_a_paged_target_refuses_pages_and_tables_of_another_device(monkeypatch):
+    """The kernels would read them through this device's pointers."""
+    class On:
+        def __init__(self, device):
+            self.device = device
+
+        def get_device(self):
+            return self.device
+
+    class Reached(Exception):
+        pass
+
+    def reached(*a):
+        raise Reached
+    monkeypatch.setattr(D, "_target_args", lambda cfg, weights: (None, None, [], []))
+    monkeypatch.setattr(D, "_pages", reached)
+    call = lambda w, k, v, t: D.dflash_target_create_paged(dict(n_layers=1), dict(embed=On(w)), [(On(k), On(v))], On(t))
+    for bad in ((0, 0, 0, 1), (0, 1, 0, 0), (0, 0, 1, 0), (1, 0, 0, 0), (-1, -1, -1, -1)):
+        with pytest.raises(ValueError):
+            call(*bad)
+    with pytest.raises(Reached):
+        call(1, 1, 1, 1)
+
+
 def test_the_packed_layouts_are_the_structs():
     for name, struct, n in (("PACK_HEADS", _abi.dflash_heads, 3), ("PACK_PAGES", _abi.dflash_kv_pages, 10),
                             ("PACK_RAGGED", _abi.dflash_ragged, 10), ("PACK_LOGPROBS", _abi.dflash_logprobs, 13)):
