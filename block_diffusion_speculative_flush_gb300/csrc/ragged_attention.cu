@@ -354,12 +354,12 @@ __global__ void __launch_bounds__(256) k_attn_few(Ragged r, AttnCall a, KVView k
 
 // 32 packed rows per CTA, 64 keys per step and group of 8 x 16 threads, each
 // with 4 rows x 4 keys of the scores and 4 rows x DP / 16 columns of the output:
-// 12 shared-memory passes for 64 products a thread.  Bound by the fp32 pipe, but
-// a group's step (load, scores, softmax, product) is one chain of about 9000
-// cycles: NG groups take every NG-th tile of keys, and their (m, l, O) meet in
-// shared memory.  The tiles with the most keys start first.  Causal prompts of 99
-// to 1200, 4 heads of 64: 61 us, 21 TFLOP/s, 28% of the fp32 pipe; one group before
-// took 142.
+// 12 shared-memory passes for 64 products a thread.  A group's step (load, scores,
+// softmax, product) is one chain between barriers: NG groups take every NG-th tile
+// of keys, and their (m, l, O) meet in shared memory.  Bound by that chain still: a
+// step of four groups takes about 20000 cycles, of which the FMAs need 8200.  The
+// tiles with the most keys start first.  Causal prompts of 99 to 1200, 4 heads of
+// 64: 61 us, 21 TFLOP/s, 28% of the fp32 pipe; one group before took 142.
 constexpr int BK = 64;
 template <int DP> struct TileCfg {
   static constexpr int NG = DP == 64 ? 4 : 2, BR = 32, LQ = DP + 4, LP = BK + 4;

@@ -20,10 +20,10 @@
 //   NQ = 2 (more than 128 rows): the two tiles share each K/V tile and alternate, one's
 //          softmax under the other's two products.  Bound by that chain: about 3060
 //          cycles for a key tile of both, of which the products alone are 2050.
-//          8192 tokens, 32 over 8 heads of 128, all keys visible: 0.71 ms, 1.55
-//          PFLOP/s (83% of a measured cuBLAS peak); causal 1.46; head dim 64 0.83.
+//          8192 tokens, 32 over 8 heads of 128, all keys visible: 0.72 ms, 1.53
+//          PFLOP/s (82% of a measured cuBLAS peak); causal 1.43; head dim 64 0.82.
 //   NQ = 1: one tile, S double-buffered; bound by the K/V stream: 64 single tokens
-//          over 4096, 8 KV heads of 128: 5.6 TB/s with pages of 16 (TMA boxes of 4 KB
+//          over 4096, 8 KV heads of 128: 5.8 TB/s with pages of 16 (TMA boxes of 4 KB
 //          are what limits it), 6.0 with pages of 64 (89% of a measured copy).  Few
 //          short items are latency: 15 us for one block of 16 tokens over 4096.
 // V rows of hidden keys may hold anything, and 0 * NaN is NaN: in tiles with
