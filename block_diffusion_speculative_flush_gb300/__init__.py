@@ -32,6 +32,9 @@ __all__ = [
     "dflash_logits_compare", "dflash_exactness_summarize", "dflash_target_exactness_probe", "exactness_rows",
     "dflash_target_create_paged", "dflash_kv_append", "dflash_paged_attention", "dflash_prompt_attention", "dflash_attention_workspace",
     "dflash_token_logprobs", "dflash_status_check",
+    "RopeTable", "dflash_rope_table", "dflash_rope", "dflash_kv8_append", "dflash_kv8_attention",
+    "dflash_kv8_attention_workspace", "PageBuffers", "dflash_page_buffers", "dflash_pages_copy", "dflash_pages_reorder",
+    "dflash_pages_resize", "dflash_pages_compact",
 ]
 
 
@@ -597,7 +600,7 @@ def _ragged(starts, lens, table, total: int, max_rows: int, max_len: int, status
 
 
 def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse, ragged: bytes, pages, workspace,
-               stream) -> tuple:
+               stream, workspace_of=lib.dflash_attention_workspace) -> tuple:
     """The packed dflash_attention, and its workspace: the caller's, or one from torch's allocator on the
     call's stream."""
     dtype, shape = _DTYPES.get(q.dtype), q.shape
@@ -612,7 +615,7 @@ def _attention(q, out, n_kv_heads: int, causal, window: int, scale, lse, ragged:
     head = (dtype, heads, n_kv_heads, d, 1 if causal else 0, int(window), d ** -0.5 if scale is None else float(scale),
             *qh, *oh, 0 if lse is None else lse.data_ptr())
     if workspace is None:
-        need = lib.dflash_attention_workspace(_abi.PACK_ATTENTION(*head, 0, 0), ragged, pages)
+        need = workspace_of(_abi.PACK_ATTENTION(*head, 0, 0), ragged, pages)
         if need < 0:
             _check(need)
         if need == 0:
@@ -736,6 +739,279 @@ def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: 
                            0 if status is None else _int_vector(status, 1, "status"))
     with _on_device(device):
         _check(lib.dflash_token_logprobs(a, _stream_of(stream, device)))
+
+
+# ---------------------------------------------------------------------------
+# the compressed cache
+# ---------------------------------------------------------------------------
+_ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
+_ROPE_SCALINGS = {"linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
+
+
+class RopeTable:
+    """What dflash_rope_table made: the library's table (host memory), and its fields."""
+
+    def __init__(self, table):
+        self.table = table
+        self.rot_dim, self.offset, self.amplitude = table.rot_dim, table.offset, table.amplitude
+        self.address = C.addressof(table)
+
+
+def dflash_rope_table(rot_dim: int, theta: float, layout: str = "half", scaling: dict | None = None, offset: int = 0,
+                      amplitude: float | None = None) -> RopeTable:
+    """The rotary table of a model, made once: rot_dim elements of each head from offset on, base theta,
+    layout "half" (pairs i, i + rot_dim / 2) or "interleaved" (pairs 2i, 2i + 1).  scaling for long contexts:
+    dict(kind="linear" or "ntk", factor=), dict(kind="bands" or "yarn", factor=, original_len=, low=, high=) with
+    low and high in turns over the original context.  amplitude: the factor on cos and sin (None: 1, for
+    "yarn" 0.1 ln(factor) + 1)."""
+    if layout not in _ROPE_LAYOUTS:
+        raise ValueError(f"layout: one of {sorted(_ROPE_LAYOUTS)}")
+    p = dict(scaling or {})
+    kind = p.pop("kind", None)
+    if scaling is not None and kind not in _ROPE_SCALINGS:
+        raise ValueError(f"scaling: a dict with kind, one of {sorted(_ROPE_SCALINGS)}")
+    want = set() if kind is None else {"factor"} if kind in ("linear", "ntk") else {"factor", "original_len", "low", "high"}
+    if set(p) != want:
+        raise ValueError(f"scaling {kind}: takes {sorted(want)}")
+    if amplitude is not None and not amplitude > 0:
+        raise ValueError("amplitude: > 0")
+    c = _abi.dflash_rope_config(rot_dim=rot_dim, offset=offset, layout=_ROPE_LAYOUTS[layout],
+                                scaling=_ROPE_SCALINGS.get(kind, 0), theta=theta, amplitude=amplitude or 0.0, **p)
+    t = _abi.dflash_rope_table()
+    _check(lib.dflash_rope_init(C.byref(c), C.byref(t)))
+    return RopeTable(t)
+
+
+def _rope_ragged(starts, lens, total: int, status) -> bytes:
+    first = _int_vector(starts, None, "starts [batch + 1]")
+    batch = starts.shape[0] - 1
+    word = 0 if status is None else _int_vector(status, 1, "status")
+    return _abi.PACK_RAGGED(batch, total, 1 << 24, 1 << 30, first, 0 if lens is None else _int_vector(lens, batch, "lens"),
+                            0, 0, 0, word)
+
+
+def dflash_rope(table: RopeTable, q: torch.Tensor | None, k: torch.Tensor | None, starts: torch.Tensor,
+                lens: torch.Tensor | None, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                transpose: bool = False, status=None, stream=None) -> None:
+    """Turns q [rows, n_q_heads, head_dim] and k [rows, n_k_heads, head_dim] (either may be None) of a ragged
+    batch by their positions: row i of sequence b is at lens[b] - n_b + i, or at i with lens None.  In place, or
+    into q_out and k_out.  transpose: the transposed map, which takes a gradient back."""
+    one = q if q is not None else k
+    if one is None:
+        raise ValueError("q or k")
+    device = _same_device(one, q, k, starts, lens, q_out, k_out, status)
+    dtype = _DTYPES.get(one.dtype)
+    if dtype is None:
+        raise ValueError("q, k: fp32 or bf16")
+    packed, heads = [], []
+    rows, d = one.shape[0], one.shape[-1]
+    for x, y, what in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if y is not None:
+                raise ValueError(f"{what}_out without {what}")
+            heads.append(0)
+            packed.append(((0, 0, 0), (0, 0, 0)))
+            continue
+        shape = x.shape
+        if len(shape) != 3 or shape[0] != rows or shape[2] != d or (y is not None and y.shape != shape):
+            raise ValueError("q, k and their outputs: [rows, heads, head_dim] of the same rows and head_dim")
+        xh = _heads(x, shape, one.dtype, what)
+        heads.append(shape[1])
+        packed.append((xh, xh if y is None else _heads(y, shape, one.dtype, what + "_out")))
+    a = _abi.PACK_ROPE(dtype, d, heads[0], heads[1], 1 if transpose else 0, *packed[0][0], *packed[1][0], *packed[0][1],
+                       *packed[1][1])
+    r = _rope_ragged(starts, lens, rows, status)
+    with _on_device(device):
+        _check(lib.dflash_rope(table.address, r, a, _stream_of(stream, device)))
+
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _kv8_pages(k_pages, v_pages, k_scale, v_scale) -> tuple:
+    """The fields of dflash_kv8_pages: codes [n_pages, page_size, n_kv_heads, head_dim] and scales
+    [n_pages, n_kv_heads], each pair of one shape and stride."""
+    shape, st, ss = k_pages.shape, k_pages.stride(), k_scale.stride()
+    if k_pages.dtype not in _CODES or v_pages.dtype not in _CODES or len(shape) != 4 or st[3] != 1 or \
+            v_pages.shape != shape or v_pages.stride() != st:
+        raise ValueError("k_pages, v_pages: CUDA float8_e4m3fn (or uint8) [n_pages, page_size, n_kv_heads, head_dim] of "
+                         "one shape and stride, with a dense last dimension")
+    n, page, heads, d = shape
+    if k_scale.dtype != torch.float32 or v_scale.dtype != torch.float32 or k_scale.shape != (n, heads) or \
+            v_scale.shape != (n, heads) or v_scale.stride() != ss:
+        raise ValueError("k_scale, v_scale: CUDA fp32 [n_pages, n_kv_heads] of one stride")
+    return (heads, d, page, 0, n, k_pages.data_ptr(), v_pages.data_ptr(), st[0] if n > 1 else d, st[1],
+            st[2] if heads > 1 else d, k_scale.data_ptr(), v_scale.data_ptr(), ss[0] if n > 1 else 1,
+            ss[1] if heads > 1 else 1)
+
+
+def dflash_kv8_append(k: torch.Tensor, v: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor,
+                      k_scale: torch.Tensor, v_scale: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor,
+                      table: torch.Tensor, status=None, stream=None) -> None:
+    """dflash_kv_append into 8-bit pages: codes float8_e4m3fn [n_pages, page_size, n_kv_heads, head_dim] with
+    fp32 scales [n_pages, n_kv_heads], which become the powers of two that their pages need."""
+    device = _same_device(k_pages, k, v, v_pages, k_scale, v_scale, starts, lens, table, status)
+    p = _kv8_pages(k_pages, v_pages, k_scale, v_scale)
+    shape, dtype = k.shape, _DTYPES.get(k.dtype)
+    if dtype is None or v.shape != shape or len(shape) != 3 or shape[1] != p[0] or shape[2] != p[1]:
+        raise ValueError(f"k, v: fp32 or bf16 [rows, {p[0]}, {p[1]}]")
+    kh = _abi.PACK_HEADS(*_heads(k, shape, k.dtype, "k"))
+    vh = _abi.PACK_HEADS(*_heads(v, shape, k.dtype, "v"))
+    rows = shape[0]
+    r = _ragged(starts, lens, table, rows, max(1, min(rows, 1 << 24)), 1 << 30, status)
+    with _on_device(device):
+        _check(lib.dflash_kv8_append(_abi.PACK_KV8(*p), r, dtype, kh, vh, _stream_of(stream, device)))
+
+
+def dflash_kv8_attention_workspace(q, out, starts, lens, table, max_rows: int, max_len: int, k_pages, v_pages, k_scale,
+                                   v_scale, causal: bool = True, window: int = 0) -> int:
+    """Bytes a dflash_kv8_attention call of these tensors, bounds, causal and window needs."""
+    device = _same_device(q, out, starts, lens, table, k_pages, v_pages, k_scale, v_scale)
+    shape, dtype = q.shape, _DTYPES.get(q.dtype)
+    if dtype is None:
+        raise ValueError("q: fp32 or bf16")
+    qh = _heads(q, shape, q.dtype, "q")
+    p = _kv8_pages(k_pages, v_pages, k_scale, v_scale)
+    r = _ragged(starts, lens, table, shape[0], max_rows, max_len, None)
+    a = _abi.PACK_ATTENTION(dtype, shape[1], p[0], shape[2], 1 if causal else 0, int(window), 1.0, *qh, *qh, 0, 0, 0)
+    with _on_device(device):
+        return _check(lib.dflash_kv8_attention_workspace(a, r, _abi.PACK_KV8(*p)))
+
+
+def dflash_kv8_attention(q: torch.Tensor, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor,
+                         v_scale: torch.Tensor, starts: torch.Tensor, lens: torch.Tensor, table: torch.Tensor,
+                         out: torch.Tensor, max_rows: int, max_len: int | None = None, causal: bool = True,
+                         window: int = 0, scale: float | None = None, lse: torch.Tensor | None = None, workspace=None,
+                         status=None, stream=None) -> None:
+    """dflash_paged_attention over 8-bit pages (dflash_kv8_append): value = code * scale of its page and head."""
+    device = _same_device(q, k_pages, v_pages, k_scale, v_scale, starts, lens, table, out, lse, workspace, status)
+    p = _kv8_pages(k_pages, v_pages, k_scale, v_scale)
+    if max_len is None:
+        max_len = min(1 << 30, table.shape[-1] * p[2])
+    r = _ragged(starts, lens, table, q.shape[0], max_rows, max_len, status)
+    pages = _abi.PACK_KV8(*p)
+    with _on_device(device):
+        a, keep = _attention(q, out, p[0], causal, window, scale, lse, r, pages, workspace, stream,
+                             lib.dflash_kv8_attention_workspace)
+        _check(lib.dflash_kv8_attention(a, r, pages, _stream_of(stream, device)))
+
+
+class PageBuffers:
+    """What lies in a pool's pages: the library's list of buffers (host memory), made once, with the tensors
+    that it points into."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("at least one tensor")
+        self.device = _same_device(*self.tensors)
+        self.n_pages = self.tensors[0].shape[0] if self.tensors[0].dim() else 0
+        packed = []
+        for t in self.tensors:
+            if t.dim() < 1 or t.shape[0] != self.n_pages or self.n_pages < 1:
+                raise ValueError("buffers: tensors [n_pages, ...] of one pool")
+            if not t[0].is_contiguous():
+                raise ValueError("buffers: a page is one dense run")
+            size, es = t[0].numel() * t.element_size(), t.element_size()
+            packed.append(_abi.PACK_BUFFER(t.data_ptr(), t.stride(0) * es if self.n_pages > 1 else size, size))
+        self.packed, self.count = b"".join(packed), len(packed)
+
+
+def dflash_page_buffers(tensors) -> PageBuffers:
+    """The buffers of a pool: one tensor [n_pages, ...] for each run of bytes that a page has (a layer's K, V
+    and their scales), each page dense and a multiple of 4 bytes."""
+    return PageBuffers(tensors)
+
+
+def _page_rows(table: torch.Tensor, lens: torch.Tensor, page_size: int, what: str) -> bytes:
+    shape, st = table.shape, table.stride()
+    if table.dtype != torch.int32 or len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
+        raise ValueError(f"{what}table: CUDA int32 [rows, pages of a row] with a dense last dimension")
+    return _abi.PACK_ROWS(shape[0], shape[1], st[0] if shape[0] > 1 else shape[1], page_size, table.data_ptr(),
+                          _int_vector(lens, shape[0], f"{what}lens"))
+
+
+def _pages_workspace(workspace, n_pages: int, rows: int, device: int, stream):
+    if workspace is not None:
+        if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
+            raise ValueError("workspace: a contiguous CUDA uint8 tensor")
+        return workspace
+    need = _check(lib.dflash_pages_workspace(n_pages, rows))
+    if stream is None:
+        return torch.empty(need, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(need, dtype=torch.uint8, device=device)
+
+
+def dflash_pages_copy(buffers: PageBuffers, src: torch.Tensor, dst: torch.Tensor, status=None, stream=None) -> None:
+    """Copies page src[i] to page dst[i] (int32) in every buffer."""
+    device = _same_device(src, dst, buffers.tensors[0], status)
+    n = src.shape[0] if src.dim() == 1 else -1
+    s, t = _int_vector(src, None, "src"), _int_vector(dst, n, "dst")
+    with _on_device(device):
+        _check(lib.dflash_pages_copy(buffers.packed, buffers.count, buffers.n_pages, s, t, n,
+                                     0 if status is None else _int_vector(status, 1, "status"), _stream_of(stream, device)))
+
+
+def dflash_pages_reorder(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
+                         new_table: torch.Tensor, new_lens: torch.Tensor, page_size: int, status=None,
+                         stream=None) -> None:
+    """Rows of the next step: row i of new_table and new_lens becomes row parents[i] (int32, -1: empty) of table
+    and lens; refs (int32 [n_pages]) follows.  A row named twice is forked, one that is not named is freed."""
+    device = _same_device(refs, table, lens, parents, new_table, new_lens, status)
+    a, b = _page_rows(table, lens, page_size, ""), _page_rows(new_table, new_lens, page_size, "new_")
+    with _on_device(device):
+        _check(lib.dflash_pages_reorder(_int_vector(refs, None, "refs"), refs.shape[0], a,
+                                        _int_vector(parents, new_table.shape[0], "parents"), b,
+                                        0 if status is None else _int_vector(status, 1, "status"),
+                                        _stream_of(stream, device)))
+
+
+def dflash_pages_resize(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, new_lens: torch.Tensor,
+                        buffers: PageBuffers | None, page_size: int, free_pages: torch.Tensor | None = None,
+                        workspace=None, status=None, stream=None) -> None:
+    """Sets the rows' lengths to new_lens: pages behind them go back, new ones are the lowest free ids, and a
+    begun last page that others hold too is copied before its row grows."""
+    device = _same_device(refs, table, lens, new_lens, free_pages, workspace, status,
+                          None if buffers is None else buffers.tensors[0])
+    rows = _page_rows(table, lens, page_size, "")
+    n_pages = refs.shape[0] if refs.dim() == 1 else 0
+    if buffers is not None and buffers.n_pages != n_pages:
+        raise ValueError("refs: int32 [n_pages] of the buffers' pool")
+    with _on_device(device):
+        ws = _pages_workspace(workspace, n_pages, table.shape[0], device, stream)
+        _check(lib.dflash_pages_resize(_int_vector(refs, None, "refs"), n_pages, rows,
+                                       _int_vector(new_lens, table.shape[0], "new_lens"),
+                                       None if buffers is None else buffers.packed, 0 if buffers is None else buffers.count,
+                                       0 if free_pages is None else _int_vector(free_pages, 1, "free_pages"),
+                                       ws.data_ptr(), ws.numel(),
+                                       0 if status is None else _int_vector(status, 1, "status"),
+                                       _stream_of(stream, device)))
+
+
+def dflash_pages_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, new_refs: torch.Tensor,
+                         new_table: torch.Tensor, buffers: PageBuffers | None, page_size: int,
+                         new_lens: torch.Tensor | None = None, used: torch.Tensor | None = None, workspace=None,
+                         status=None, stream=None) -> None:
+    """Moves the pages in use to the lowest ids: new_refs and new_table (which may be refs and table) say where
+    they are then, used (int32 [1]) how many.  new_lens None: lens stays what it is."""
+    new_lens = lens if new_lens is None else new_lens
+    device = _same_device(refs, table, lens, new_refs, new_table, new_lens, used, workspace, status,
+                          None if buffers is None else buffers.tensors[0])
+    n_pages = refs.shape[0] if refs.dim() == 1 else 0
+    if buffers is not None and buffers.n_pages != n_pages:
+        raise ValueError("refs: int32 [n_pages] of the buffers' pool")
+    if new_table.shape != table.shape:
+        raise ValueError("new_table: the shape of table")
+    a, b = _page_rows(table, lens, page_size, ""), _page_rows(new_table, new_lens, page_size, "new_")
+    with _on_device(device):
+        ws = _pages_workspace(workspace, n_pages, table.shape[0], device, stream)
+        _check(lib.dflash_pages_compact(_int_vector(refs, None, "refs"), _int_vector(new_refs, n_pages, "new_refs"),
+                                        n_pages, a, b, None if buffers is None else buffers.packed,
+                                        0 if buffers is None else buffers.count,
+                                        0 if used is None else _int_vector(used, 1, "used"), ws.data_ptr(), ws.numel(),
+                                        0 if status is None else _int_vector(status, 1, "status"),
+                                        _stream_of(stream, device)))
 
 
 def dflash_status_check(status: torch.Tensor, stream=None) -> None:

@@ -114,6 +114,39 @@ class dflash_logprobs(C.Structure):
                 ("top_logprobs", C.c_void_p), ("status", C.c_void_p)]
 
 
+class dflash_rope_config(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("offset", C.c_int32), ("layout", C.c_int32), ("scaling", C.c_int32),
+                ("theta", C.c_double), ("factor", C.c_double), ("original_len", C.c_double), ("low", C.c_double),
+                ("high", C.c_double), ("amplitude", C.c_double)]
+
+
+class dflash_rope_table(C.Structure):
+    _fields_ = [("rot_dim", C.c_int32), ("offset", C.c_int32), ("layout", C.c_int32), ("amplitude", C.c_float),
+                ("turns", C.c_uint64 * 128)]
+
+
+class dflash_rope_call(C.Structure):
+    _fields_ = [("dtype", C.c_int32), ("head_dim", C.c_int32), ("n_q_heads", C.c_int32), ("n_k_heads", C.c_int32),
+                ("transpose", C.c_int32), ("q", dflash_heads), ("k", dflash_heads), ("q_out", dflash_heads),
+                ("k_out", dflash_heads)]
+
+
+class dflash_kv8_pages(C.Structure):
+    _fields_ = [("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32), ("reserved", C.c_int32),
+                ("n_pages", C.c_int64), ("k", C.c_void_p), ("v", C.c_void_p), ("page_stride", C.c_int64),
+                ("slot_stride", C.c_int64), ("head_stride", C.c_int64), ("k_scale", C.c_void_p),
+                ("v_scale", C.c_void_p), ("scale_page_stride", C.c_int64), ("scale_head_stride", C.c_int64)]
+
+
+class dflash_page_rows(C.Structure):
+    _fields_ = [("rows", C.c_int32), ("width", C.c_int32), ("stride", C.c_int32), ("page_size", C.c_int32),
+                ("table", C.c_void_p), ("lens", C.c_void_p)]
+
+
+class dflash_page_buffer(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("page_stride", C.c_int64), ("page_bytes", C.c_int64)]
+
+
 # The same layouts for struct.pack (native alignment), several times faster to
 # fill in than a ctypes structure: these calls' host time bounds small batches.
 PACK_HEADS = struct.Struct("@Pqq").pack
@@ -121,6 +154,10 @@ PACK_PAGES = struct.Struct("@4iqPP3q").pack
 PACK_RAGGED = struct.Struct("@4i3P2iP").pack
 PACK_ATTENTION = struct.Struct("@6ifPqqPqqPPq").pack
 PACK_LOGPROBS = struct.Struct("@Pq4if6P").pack
+PACK_ROPE = struct.Struct("@5iPqqPqqPqqPqq").pack
+PACK_KV8 = struct.Struct("@4iqPP3qPPqq").pack
+PACK_ROWS = struct.Struct("@4iPP").pack
+PACK_BUFFER = struct.Struct("@Pqq").pack
 
 P = C.c_void_p
 SessArr = C.POINTER(C.c_void_p)
@@ -179,6 +216,16 @@ SIGNATURES = {
                                              C.POINTER(dflash_kv_pages), P, C.c_int32, C.c_int64, P,
                                              C.POINTER(C.c_void_p)]),
     "dflash_token_logprobs": (C.c_int, [P, P]),
+    "dflash_rope_init": (C.c_int, [C.POINTER(dflash_rope_config), C.POINTER(dflash_rope_table)]),
+    "dflash_rope": (C.c_int, [P, P, P, P]),
+    "dflash_kv8_append": (C.c_int, [P, P, C.c_int32, P, P, P]),
+    "dflash_kv8_attention_workspace": (C.c_int64, [P, P, P]),
+    "dflash_kv8_attention": (C.c_int, [P, P, P, P]),
+    "dflash_pages_copy": (C.c_int, [P, C.c_int32, C.c_int64, P, P, C.c_int32, P, P]),
+    "dflash_pages_reorder": (C.c_int, [P, C.c_int64, P, P, P, P, P]),
+    "dflash_pages_workspace": (C.c_int64, [C.c_int64, C.c_int32]),
+    "dflash_pages_resize": (C.c_int, [P, C.c_int64, P, P, P, C.c_int32, P, P, C.c_int64, P, P]),
+    "dflash_pages_compact": (C.c_int, [P, P, C.c_int64, P, P, P, C.c_int32, P, P, C.c_int64, P, P]),
     "dflash_status_check": (C.c_int, [P, P]),
 }
 

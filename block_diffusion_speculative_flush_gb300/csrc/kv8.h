@@ -1,0 +1,50 @@
+// Internal interface of the 8-bit paged cache: its view for kernels, and the
+// conversions of e4m3 codes.
+#pragma once
+
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "ragged.h"
+
+namespace dfl {
+
+// The cache of one layer: code of page p, slot s, head h, element c at
+// p * page + s * slot + h * head + c; its scale at p * s_page + h * s_head.
+struct Kv8View {
+  uint8_t* k;
+  uint8_t* v;
+  float* ks;
+  float* vs;
+  int64_t page, slot, head, s_page, s_head;
+  int32_t page_shift, n_pages;
+};
+
+// Two codes (the lower byte first) as fp16: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint16_t c) {
+  uint32_t h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
+  return h;
+}
+__device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t c) {
+  const uint32_t h = e4m3x2_to_h2(c);
+  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+__device__ __forceinline__ float4 e4m3x4_to_f4(uint32_t c) {
+  const float2 a = e4m3x2_to_f2((uint16_t)c), b = e4m3x2_to_f2((uint16_t)(c >> 16));
+  return make_float4(a.x, a.y, b.x, b.y);
+}
+// Nearest codes, ties to even, beyond 448: 448; NaN: 0x7f.  a is the lower byte.
+__device__ __forceinline__ uint16_t f2_to_e4m3x2(float a, float b) {
+  uint16_t c;
+  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
+  return c;
+}
+// whether x is not finite (from its bits: fast-math flags do not change that)
+__device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+
+// The CUDA-core path (any rows, fp32 and bf16, head_dim a multiple of 16).
+int64_t kv8_simt_workspace(const Ragged& r, const AttnCall& a, int sms);
+cudaError_t launch_kv8_simt(const Ragged& r, const AttnCall& a, const Kv8View& kv, bool is_bf16, int sms, cudaStream_t st);
+
+}  // namespace dfl

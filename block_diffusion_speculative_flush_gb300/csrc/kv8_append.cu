@@ -1,0 +1,236 @@
+// New K/V rows into 8-bit pages with a scale for each page and KV head.
+//
+// For the new rows x of a page and head:  s = the smallest power of two with
+// |x| <= 448 s, at least the page's scale if it holds rows in front of them;
+// code = e4m3(x / s).  Powers of two make x / s exact, and a scale that grows only
+// shifts the exponents of the codes that are there.
+#include "common.cuh"
+#include "kv8.h"
+#include "launch.h"
+#include "target_checks.h"
+#include "kv8_checks.h"
+
+namespace dfl {
+namespace {
+
+constexpr int kThreads = 256, kWarps = kThreads / 32;
+constexpr int kHold = 4;  // steps of a warp whose rows stay in registers between the two passes
+
+template <typename T> struct Eight;  // eight elements
+template <> struct Eight<bf16> {
+  uint4 a;
+  __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float* f) const {
+    const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      f[2 * i] = __uint_as_float(w[i] << 16);
+      f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Eight<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const float4*>(p);
+    b = *reinterpret_cast<const float4*>(p + 4);
+  }
+  __device__ __forceinline__ void get(float* f) const {
+    f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
+    f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
+  }
+};
+
+// The exponent of the smallest power of two s with most <= 448 s = 1.75 2^8 s.
+__device__ __forceinline__ float scale_for(float most) {
+  const uint32_t u = __float_as_uint(most);
+  const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return __uint_as_float((uint32_t)(min(max(e, -60), 60) + 127) << 23);
+}
+
+// Pieces of a sequence: the pages that receive its new rows.
+__device__ __forceinline__ int pieces_of(const Seq& s, int shift) {
+  return s.ok && s.n > 0 ? ((s.len - 1) >> shift) - ((s.len - s.n) >> shift) + 1 : 0;
+}
+
+struct Rows8 {
+  const void* x[2];
+  int64_t row[2], head[2];
+};
+
+// A CTA takes 8 / WPT tasks of one piece, WPT warps each; a task is K or V of one head.
+// d / 8 lanes a row.  The rows of up to kHold steps stay in registers between the
+// pass that finds the scale and the one that writes; longer pieces are read again (L1).
+template <typename T, int WPT>
+__global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8View kv, int heads, int d) {
+  __shared__ float most_w[kWarps];
+  pdl_trigger();
+  pdl_wait();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  r.starts = after_wait(r.starts);
+  r.lens = after_wait(r.lens);
+  // the piece's sequence and page: every warp finds it for itself
+  int rest = blockIdx.x, b = -1, j = 0;
+  Seq s{0, 0, 0, false};
+  for (int base = 0; base < r.batch; base += 32) {
+    Seq c{0, 0, 0, false};
+    if (base + lane < r.batch) {
+      c = load_seq(r, base + lane);
+      if (!c.ok && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+    }
+    const int n = pieces_of(c, kv.page_shift);
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    const unsigned found = __ballot_sync(0xffffffffu, incl > rest);
+    if (found) {
+      const int src = __ffs(found) - 1;
+      j = rest - __shfl_sync(0xffffffffu, incl - n, src);
+      b = base + src;
+      s.start = __shfl_sync(0xffffffffu, c.start, src);
+      s.n = __shfl_sync(0xffffffffu, c.n, src);
+      s.len = __shfl_sync(0xffffffffu, c.len, src);
+      break;
+    }
+    rest -= __shfl_sync(0xffffffffu, incl, 31);
+    if (rest < 0) break;  // (lengths that overflow: no one's piece)
+  }
+  if (b < 0) return;
+  const int first = s.len - s.n, page = (first >> kv.page_shift) + j, size = 1 << kv.page_shift;
+  const int p0 = max(first, page << kv.page_shift), p1 = min(s.len, (page + 1) << kv.page_shift);
+  const int s0 = p0 & (size - 1), n = p1 - p0, row0 = s.start + p0 - first;
+  const int task = blockIdx.y * (kWarps / WPT) + warp / WPT, part = warp % WPT;
+  const int pg = r.table[(int64_t)b * r.table_stride + page];
+  if (pg < 0 || pg >= kv.n_pages) {
+    if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_PAGE);
+    return;
+  }
+  const bool live = task < 2 * heads;  // (a warp without a task still meets the barrier)
+  const int w = task >= heads, h = live ? task - w * heads : 0;
+  float* scale = (w ? kv.vs : kv.ks) + (int64_t)pg * kv.s_page + h * kv.s_head;
+  const float old = s0 > 0 ? *scale : 0.f;
+  const int lpr = d / 8, rpw = 32 / lpr, mine = lane / lpr, col = (lane - mine * lpr) * 8;
+  const bool in = live && mine < rpw;
+  const T* src = reinterpret_cast<const T*>(w ? x.x[1] : x.x[0]) + (int64_t)row0 * (w ? x.row[1] : x.row[0]) +
+                 h * (w ? x.head[1] : x.head[0]) + col;
+  const int64_t src_row = w ? x.row[1] : x.row[0];
+  const int step = rpw * WPT, steps = (n + step - 1) / step, at = part * rpw + mine;
+  Eight<T> hold[kHold];
+  float most = 0.f;
+  auto look = [&](const Eight<T>& e) {
+    float f[8];
+    e.get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) most = fmaxf(most, nonfinite(f[i]) ? 0.f : fabsf(f[i]));
+  };
+#pragma unroll
+  for (int t = 0; t < kHold; ++t)
+    if (in && at + t * step < n) hold[t].load(src + (at + t * step) * src_row);
+#pragma unroll
+  for (int t = 0; t < kHold; ++t)
+    if (in && at + t * step < n) look(hold[t]);
+#pragma unroll 4
+  for (int t = kHold; t < steps; ++t) {
+    Eight<T> e;
+    if (in && at + t * step < n) {
+      e.load(src + (int64_t)(at + t * step) * src_row);
+      look(e);
+    }
+  }
+  most = warp_max(most);
+  if (WPT > 1) {
+    if (lane == 0) most_w[warp] = most;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < WPT; ++i) most = fmaxf(most, most_w[warp - part + i]);
+  }
+  if (!live) return;
+  const float now = s0 > 0 ? fmaxf(scale_for(most), old) : scale_for(most);
+  uint8_t* dst = (w ? kv.v : kv.k) + (int64_t)pg * kv.page + h * kv.head + col;
+  // an old scale may be any number: a power of two's reciprocal is exact, others divide
+  const bool exact = (__float_as_uint(now) & 0x807fffffu) == 0;
+  const float inv = 1.f / now;
+  auto write = [&](const Eight<T>& e, int slot) {
+    float f[8];
+    e.get(f);
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float q = exact ? f[i] * inv : f[i] / now;
+      f[i] = nonfinite(f[i]) ? __uint_as_float(0x7fffffffu) : q;
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      c[i] = (uint32_t)f2_to_e4m3x2(f[4 * i], f[4 * i + 1]) | (uint32_t)f2_to_e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
+    *reinterpret_cast<uint2*>(dst + slot * kv.slot) = make_uint2(c[0], c[1]);
+  };
+#pragma unroll
+  for (int t = 0; t < kHold; ++t)
+    if (in && at + t * step < n) write(hold[t], s0 + at + t * step);
+#pragma unroll 2
+  for (int t = kHold; t < steps; ++t)
+    if (in && at + t * step < n) {
+      Eight<T> e;
+      e.load(src + (int64_t)(at + t * step) * src_row);
+      write(e, s0 + at + t * step);
+    }
+  if (s0 > 0 && now != old) {
+    // the rows in front of the new ones: their codes at the new scale
+    const float f = old / now;
+    for (int slot = at; slot < s0; slot += step)
+      if (in) {
+        uint2* p = reinterpret_cast<uint2*>(dst + slot * kv.slot);
+        const uint2 c = *p;
+        const float4 a = e4m3x4_to_f4(c.x), b4 = e4m3x4_to_f4(c.y);
+        *p = make_uint2((uint32_t)f2_to_e4m3x2(a.x * f, a.y * f) | (uint32_t)f2_to_e4m3x2(a.z * f, a.w * f) << 16,
+                        (uint32_t)f2_to_e4m3x2(b4.x * f, b4.y * f) | (uint32_t)f2_to_e4m3x2(b4.z * f, b4.w * f) << 16);
+      }
+  }
+  if (part == 0 && lane == 0 && now != old) *scale = now;
+}
+
+template <typename T, int WPT>
+cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads, int d, cudaStream_t st) {
+  const int64_t pieces = (int64_t)(r.total >> kv.page_shift) + 2ll * std::min(r.batch, r.total);
+  const int per = kWarps / WPT;
+  return launch_k(k_kv8_append<T, WPT>, dim3((unsigned)std::min<int64_t>(pieces, r.total), (2 * heads + per - 1) / per),
+                  kThreads, 0, st, r, x, kv, heads, d);
+}
+template <typename T>
+cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads, int d, cudaStream_t st) {
+  // warps a task: as many as its rows, those of a full page or the average sequence's, keep busy for one or
+  // two steps
+  const int rows = std::min(1 << kv.page_shift, std::max(1, r.total / r.batch)), steps = (rows * d / 8 + 31) / 32;
+  return steps <= 2   ? launch<T, 1>(r, x, kv, heads, d, st)
+         : steps <= 4 ? launch<T, 2>(r, x, kv, heads, d, st)
+         : steps <= 8 ? launch<T, 4>(r, x, kv, heads, d, st)
+                      : launch<T, 8>(r, x, kv, heads, d, st);
+}
+
+}  // namespace
+}  // namespace dfl
+
+using namespace dfl;
+
+extern "C" DFLASH_API int dflash_kv8_append(const dflash_kv8_pages* pages, const dflash_ragged* batch, int32_t dtype,
+                                            const dflash_heads* k, const dflash_heads* v, void* stream) {
+  const char* call = "dflash_kv8_append";
+  if (int rc = check_kv8_pages(call, pages)) return rc;
+  if (dtype != DFLASH_DTYPE_F32 && dtype != DFLASH_DTYPE_BF16) return rfail(DFLASH_ERR_INVALID_ARG, call, "dtype");
+  const dflash_kv_pages like = kv8_as_pages(pages);
+  if (int rc = check_ragged(call, batch, &like, true)) return rc;
+  const bool rows = batch->total_rows > 0;
+  if (int rc = check_heads(call, k, dtype, pages->n_kv_heads, pages->head_dim, rows)) return rc;
+  if (int rc = check_heads(call, v, dtype, pages->n_kv_heads, pages->head_dim, rows)) return rc;
+  if (!rows) return DFLASH_OK;
+  const Ragged r = make_ragged(batch, &like);
+  const Rows8 x{{k->data, v->data}, {k->row_stride, v->row_stride}, {k->head_stride, v->head_stride}};
+  const Kv8View kv = kv8_view(pages);
+  cudaStream_t st = (cudaStream_t)stream;
+  return rcheck(dtype == DFLASH_DTYPE_F32 ? launch<float>(r, x, kv, pages->n_kv_heads, pages->head_dim, st)
+                                          : launch<bf16>(r, x, kv, pages->n_kv_heads, pages->head_dim, st),
+                call);
+}

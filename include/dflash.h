@@ -657,6 +657,173 @@ typedef struct dflash_logprobs {
 } dflash_logprobs;
 DFLASH_API int dflash_token_logprobs(const dflash_logprobs* a, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The compressed cache.
+ *
+ * What a target's layer does around a K/V cache held in 8 bits: rotary positions
+ * of the new rows, their codes into pages, attention over those, and the pages
+ * themselves as sequences fork, grow, shrink and end.  The conventions are those
+ * of the target-side operators above: caller-owned device buffers, lengths and
+ * tables read on the device, captured steps follow them, reasons in *status.
+ */
+#define DFLASH_STATUS_FULL 16 /* no free page left: sequences were not grown (dflash_pages_resize) */
+
+/* Rotary positions.  Pair i of a head's rotated part (i < rot_dim / 2) at
+ * position p turns by the angle p f_i:
+ *   (a, b) -> A (a cos - b sin, b cos + a sin)
+ * Pairs are elements (offset + i, offset + i + rot_dim / 2) in the half layout
+ * and (offset + 2i, offset + 2i + 1) in the interleaved one; the other elements
+ * pass through.  With R = rot_dim, f_i = theta^(-2i / R), and by scaling
+ *   LINEAR  f / factor
+ *   NTK     theta becomes theta factor^(R / (R - 2))
+ *   BANDS   u = original_len f / (2 pi) turns in the original context; the share
+ *           s = clamp((u - low) / (high - low), 0, 1) keeps f, the rest has f / factor
+ *   YARN    (Peng et al., "YaRN") the ramp from pair floor(c(high)) to ceil(c(low)),
+ *           c(u) = R ln(original_len / (2 pi u)) / (2 ln theta), clamped to 0 .. R - 1,
+ *           goes from f to f / factor; A = amplitude, or 0.1 ln(factor) + 1 if that is 0
+ * else A = amplitude, or 1 if that is 0. */
+#define DFLASH_ROPE_HALF 0
+#define DFLASH_ROPE_INTERLEAVED 1
+#define DFLASH_ROPE_NONE 0
+#define DFLASH_ROPE_LINEAR 1
+#define DFLASH_ROPE_NTK 2
+#define DFLASH_ROPE_BANDS 3
+#define DFLASH_ROPE_YARN 4
+#define DFLASH_ROPE_MAX_DIM 256
+typedef struct dflash_rope_config {
+  int32_t rot_dim;       /* even, 2..256 */
+  int32_t offset;        /* even, where the rotated part begins */
+  int32_t layout, scaling;
+  double theta;          /* > 1 */
+  double factor;         /* all but NONE: > 0 (YARN: >= 1) */
+  double original_len;   /* BANDS, YARN: > 0 */
+  double low, high;      /* BANDS, YARN: 0 < low < high (turns) */
+  double amplitude;      /* >= 0 */
+} dflash_rope_config;
+
+/* Filled in by dflash_rope_init, kept by the caller (host).  turns[i]: f_i / (2 pi)
+ * mod 1 in units of 2^-64, so that p turns[i] in 64 bits is the angle mod 1 turn,
+ * exactly, at any position. */
+typedef struct dflash_rope_table {
+  int32_t rot_dim, offset, layout;
+  float amplitude;
+  uint64_t turns[DFLASH_ROPE_MAX_DIM / 2];
+} dflash_rope_table;
+
+typedef struct dflash_rope_call {
+  int32_t dtype;        /* DFLASH_DTYPE_F32 or DFLASH_DTYPE_BF16 */
+  int32_t head_dim;     /* a multiple of 8, at most 256 */
+  int32_t n_q_heads;    /* 0..1024; 0: no q */
+  int32_t n_k_heads;    /* 0..1024; 0: no k */
+  int32_t transpose;    /* 1: the transposed map (angles negated): the gradient's way back */
+  dflash_heads q, k;    /* [total_rows][heads][head_dim] */
+  dflash_heads q_out, k_out;  /* the same data and strides (in place), or no overlap with any input */
+} dflash_rope_call;
+
+/* Bad fields: DFLASH_ERR_INVALID_ARG, sizes: DFLASH_ERR_SHAPE. */
+DFLASH_API int dflash_rope_init(const dflash_rope_config* config, dflash_rope_table* table);
+/* Rows of a ragged batch: row i of sequence b is at position lens[b] - n_b + i
+ * (lens NULL: i).  Of the batch, batch, total_rows, max_len (with lens), starts, lens
+ * and status are used.  The arithmetic is fp32, one rounding to dtype. */
+DFLASH_API int dflash_rope(const dflash_rope_table* table, const dflash_ragged* batch, const dflash_rope_call* call,
+                           void* stream);
+
+/* A paged K/V cache in 8 bits: e4m3 codes (4 exponent and 3 mantissa bits, bias 7,
+ * no infinities, 0x7f and 0xff are NaN) with one fp32 scale per page and KV head,
+ * of K and of V: value = code * scale.  Codes lie as in dflash_kv_pages, strides in
+ * codes (bytes); the scale of page p and head h is at p * scale_page_stride + h *
+ * scale_head_stride floats.  Scales are finite and positive (attention is exact
+ * to its type for scales in 2^-60 .. 2^60, which is what append writes). */
+typedef struct dflash_kv8_pages {
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* a multiple of 16 up to 128 */
+  int32_t page_size;    /* a power of two in 16..1024 */
+  int32_t reserved;     /* 0 */
+  int64_t n_pages;      /* 1..2^31 - 1 */
+  void* k;              /* 16-byte aligned */
+  void* v;
+  int64_t page_stride, slot_stride, head_stride;  /* multiples of 16 */
+  float* k_scale;
+  float* v_scale;
+  int64_t scale_page_stride, scale_head_stride;   /* floats, >= 1 */
+} dflash_kv8_pages;
+
+/* Writes the new rows of K and V (dtype fp32 or bf16) into their pages as codes.
+ * The scale of a page and head that receives rows becomes the smallest power of two
+ * (2^-60 .. 2^60) with which every finite new element is at most 448 codes, and is
+ * never below what it was if the page holds rows in front of the new ones; where it
+ * grows, those rows' codes are rounded again (exact, save where a value falls below
+ * the smallest normal code, if the old scale is a power of two).  Codes round to nearest
+ * even and saturate; elements that are not finite become NaN.  Slots behind the new
+ * rows keep their bits.  Pages as in dflash_kv_append. */
+DFLASH_API int dflash_kv8_append(const dflash_kv8_pages* pages, const dflash_ragged* batch, int32_t dtype,
+                                 const dflash_heads* k, const dflash_heads* v, void* stream);
+/* dflash_paged_attention over such pages: the same call, masks, layout of heads and
+ * treatment of what a row does not see; dtype (of q and out) fp32 or bf16, head_dim the
+ * pages'.  A bf16 call with head_dim 64 or 128 rounds the probabilities to fp16 for the
+ * second product, other calls keep fp32. */
+DFLASH_API int64_t dflash_kv8_attention_workspace(const dflash_attention* a, const dflash_ragged* batch,
+                                                  const dflash_kv8_pages* pages);
+DFLASH_API int dflash_kv8_attention(const dflash_attention* a, const dflash_ragged* batch,
+                                    const dflash_kv8_pages* pages, void* stream);
+
+/* Pages of a cache.  refs (device [n_pages]) counts the table entries that name a page;
+ * 0 is free.  A row of the table (one sequence) holds the pages of its first
+ * ceil(lens / page_size) entries, the others are -1.  What the calls below answer
+ * depends on their inputs alone: free pages are given out lowest id first, to the rows
+ * in order. */
+typedef struct dflash_page_rows {
+  int32_t rows;          /* 1..32768 */
+  int32_t width;         /* entries of a row, 1..2^20 */
+  int32_t stride;        /* entries from one row to the next, >= width */
+  int32_t page_size;     /* tokens, a power of two in 8..1024 */
+  int32_t* table;        /* device [rows][stride] */
+  int32_t* lens;         /* device [rows] tokens */
+} dflash_page_rows;
+
+/* What lies in a page: one run of page_bytes for each buffer, page p at data + p *
+ * page_stride bytes (a layer's K, V or scales; all layers of a cache share its page
+ * ids).  Everything a multiple of 4 bytes. */
+typedef struct dflash_page_buffer {
+  void* data;
+  int64_t page_stride, page_bytes;
+} dflash_page_buffer;
+
+/* Copies page src[i] to page dst[i] in every buffer, i < count; src, dst device
+ * [count].  No page is named twice as a target, or as a target and a source (else
+ * either's bytes are left there).  Ids outside [0, n_pages): skipped with status 4. */
+DFLASH_API int dflash_pages_copy(const dflash_page_buffer* buffers, int32_t n_buffers, int64_t n_pages,
+                                 const int32_t* src, const int32_t* dst, int32_t count, int32_t* status, void* stream);
+/* Rows of the next step: row i of `to` becomes row parents[i] of `from` (device
+ * [to->rows]; -1: an empty row).  A row named several times is forked (its pages are
+ * shared), one that is not named is freed.  `to` overlaps `from` nowhere; n_pages and
+ * refs are the pool's.  Status 2: a parent outside -1 .. from->rows - 1 or a length that
+ * its row cannot hold, taken as empty; 4: a page id outside the pool, left out. */
+DFLASH_API int dflash_pages_reorder(int32_t* refs, int64_t n_pages, const dflash_page_rows* from,
+                                    const int32_t* parents, const dflash_page_rows* to, int32_t* status, void* stream);
+/* Bytes of workspace of dflash_pages_resize and dflash_pages_compact (4-byte
+ * aligned), or a negative status. */
+DFLASH_API int64_t dflash_pages_workspace(int64_t n_pages, int32_t rows);
+/* Sets each row's length to new_lens (device [rows]).  Shorter: pages behind it are
+ * given back.  Longer: pages are added, and a begun last page that other rows hold too is
+ * replaced by a copy of its own first, in every buffer (of rows that all write to
+ * one page that no one else holds, the first keeps it).  Rows whose pages, together with those of the rows in
+ * front of them, are not there keep their length and pages (status 16); a new length
+ * outside 0 .. width * page_size likewise (status 2).  Page ids outside the pool: status 4.
+ * free_pages (device, or NULL): the pages that are free then. */
+DFLASH_API int dflash_pages_resize(int32_t* refs, int64_t n_pages, const dflash_page_rows* rows,
+                                   const int32_t* new_lens, const dflash_page_buffer* buffers, int32_t n_buffers,
+                                   int32_t* free_pages, void* workspace, int64_t workspace_bytes, int32_t* status,
+                                   void* stream);
+/* Moves the pages in use to the lowest ids, in every buffer: those at or above the
+ * count of pages in use go, in order, to the free ids below it, in order.  The answer is in
+ * `to` (rows, width and page_size of `from`; table and lens may be the same) and new_refs
+ * (may be refs); used (device, or NULL): the count. */
+DFLASH_API int dflash_pages_compact(const int32_t* refs, int32_t* new_refs, int64_t n_pages,
+                                    const dflash_page_rows* from, const dflash_page_rows* to,
+                                    const dflash_page_buffer* buffers, int32_t n_buffers, int32_t* used,
+                                    void* workspace, int64_t workspace_bytes, int32_t* status, void* stream);
+
 /* Waits for the stream, then reads and clears a status word (device): 0, or
  * DFLASH_ERR_DEVICE with the reasons in dflash_last_error. */
 DFLASH_API int dflash_status_check(int32_t* status, void* stream);
