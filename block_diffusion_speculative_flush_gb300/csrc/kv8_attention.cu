@@ -403,8 +403,13 @@ int kv8_sms() {
   return sms;
 }
 
+// The kernel of a call: bf16 with head_dim 64 or 128 runs on the tensor cores.
+bool kv8_few(const dflash_attention* a, const Ragged& r) {
+  return a->dtype == DFLASH_DTYPE_BF16 && (a->head_dim == 64 || a->head_dim == 128) &&
+         (int64_t)r.max_rows * (a->n_q_heads / a->n_kv_heads) <= 64;
+}
 int64_t kv8_workspace(const dflash_attention* a, const Ragged& r, int sms) {
-  return kv8_simt_workspace(r, kv8_call(a), sms);
+  return kv8_few(a, r) ? kv8_few_workspace(r, kv8_call(a), sms) : kv8_simt_workspace(r, kv8_call(a), sms);
 }
 
 }  // namespace
@@ -440,7 +445,12 @@ DFLASH_API int dflash_kv8_attention(const dflash_attention* a, const dflash_ragg
   const int64_t need = kv8_workspace(a, r, sms);
   if (need > 0 && (!a->workspace || a->workspace_bytes < need || (uintptr_t)a->workspace % 32))
     return rfail(DFLASH_ERR_INVALID_ARG, call, "workspace: 32-byte aligned, at least dflash_kv8_attention_workspace bytes");
-  return rcheck(launch_kv8_simt(r, kv8_call(a), kv8_view(pages), a->dtype == DFLASH_DTYPE_BF16, sms, (cudaStream_t)stream), call);
+  const AttnCall c = kv8_call(a);
+  const Kv8View kv = kv8_view(pages);
+  cudaStream_t st = (cudaStream_t)stream;
+  return rcheck(kv8_few(a, r) ? launch_kv8_few(r, c, kv, sms, st)
+                              : launch_kv8_simt(r, c, kv, a->dtype == DFLASH_DTYPE_BF16, sms, st),
+                call);
 }
 
 }  // extern "C"

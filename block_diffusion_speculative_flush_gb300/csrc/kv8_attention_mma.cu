@@ -1,0 +1,659 @@
+// Attention of few rows (single tokens, verified blocks) over an 8-bit paged cache:
+// bf16, head_dim 64 or 128.
+//
+// Bound by the stream of codes, so nothing of a code's way is wasted: a lane copies
+// (cp.async) the very bytes that it multiplies, into a ring of its own, and no two lanes
+// ever wait for one another's.  That works because a contraction may take its index in any
+// order and a result its rows in any order:
+//   S^T = K Q^T   A = 16 keys of K: lane (g, t) of the m16n8k16 fragment holds keys g and
+//                 g + 8 at any 4 d's per step, here 16 bytes in a row of each
+//   O^T = V^T P^T A = V^T, 16 d's by 16 keys: lane (g, t) holds keys 2t, 2t + 1, 2t + 8, 2t + 9 at
+//                 the d's 16 g .. 16 g + 15, 16 bytes of each key's row
+// with N = 8 rows (token, query head of the group) a fragment, so that a decode step's few rows
+// fill it.  Codes become fp16 exactly (cvt).  P goes from the first product's result to the
+// second one's operand by a transpose of 8 x 8 in registers (movmatrix).
+//
+// Numbers.  q is scaled by a power of two for its row, so that its largest element lies in
+// [2^14, 2^15): fp16 holds bf16's 8 bits for elements down to 2^-29 of that, an error that
+// fp32 sums of such products have too.  Scores: (S ks) (scale 2^-e log2 e), fp32.  P is
+// rounded to fp16 once, as p r 2^10 with p <= 2^4 (the maximum moves only when it grew by more)
+// and r = vs / u <= 1, u the largest scale of V so far: half a step is 2^-12 of it, below its
+// smallest normal number 2^-25 of 2^10, that is 2^-35 of what the largest scale and
+// probability give.  m, l, O and merges are fp32.
+//
+// Work: the 16-key chunks of all (sequence, tile of rows, KV head) items one after another, cut
+// into even ranges, one per CTA; the 8 warps of a CTA take its chunks in turn and meet in
+// shared memory, the parts of a cut item in k_kv8_few_merge.  The order of every sum is
+// fixed by the lengths.
+#include <algorithm>
+#include <atomic>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kv8.h"
+#include "launch.h"
+
+namespace dfl {
+namespace {
+
+constexpr int kChunk = 16;  // keys of a chunk: never more than a page
+constexpr int kWarps = 8;
+constexpr float kSlack = 4.f, kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kUnit = 1024.f;  // 2^10, of P in fp16
+
+struct FewPlan {
+  int32_t pad;        // what the start of an item costs, in chunks
+  int32_t min_units;  // chunks that a CTA gets at least
+  int32_t slots;      // partials there is room for
+};
+
+template <int D, int NB>
+struct FewCfg {
+  static constexpr int RB = 8 * NB;               // rows of a tile
+  static constexpr int CTAS = NB <= 2 ? 2 : 1;    // of an SM
+  static constexpr int BYTES = kChunk * 2 * D;    // codes of a chunk
+  static constexpr int STAGES = (NB <= 2 ? 3 : 6) * (128 / D);
+  static constexpr int LO = D + 4;                // floats of a row where the warps meet
+  static constexpr int RING = kWarps * STAGES * BYTES, MEET = kWarps * RB * LO * 4;
+  static constexpr size_t SMEM = (RING > MEET ? RING : MEET) + kWarps * STAGES * 8 + kWarps * RB * 8 + RB * 8;
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int N> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
+  // (size 0: zeros, the address is not looked at)
+  const int n = there ? N : 0;
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// D += A B, m16n8k16, fp16 operands, fp32 sums
+__device__ __forceinline__ void mma(float* c, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_h2(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ uint32_t lo_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)c); }
+__device__ __forceinline__ uint32_t hi_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)(c >> 16)); }
+// bytes of codes that are NaN: bit 7 of each
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+
+// ---------------------------------------------------------------------------
+// the layout of the work
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ int64_t few_tiles(const Seq& s, int G, int RB) {
+  return s.ok && s.n > 0 ? ((int64_t)s.n * G + RB - 1) / RB : 0;
+}
+__device__ __forceinline__ int few_first(const Seq& s, int window) { return vis_lo(s.len - s.n, window) / kChunk; }
+__device__ __forceinline__ int few_chunks(const Seq& s, int window) {
+  return (s.len + kChunk - 1) / kChunk - few_first(s, window);
+}
+__device__ __forceinline__ int64_t warp_sum64(int64_t v) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  return v;
+}
+__device__ __forceinline__ int64_t warp_scan64(int64_t v, int lane) {  // inclusive
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
+  }
+  return v;
+}
+struct FewRanges {
+  int64_t units, each, rest;
+  int n;
+  __device__ __forceinline__ FewRanges(int64_t u, const FewPlan& p, int grid) {
+    units = u;
+    n = (int)max((int64_t)1, min((int64_t)grid, u / p.min_units));
+    each = u / n;
+    rest = u - each * n;
+  }
+  __device__ __forceinline__ int64_t start(int c) const { return c * each + min((int64_t)c, rest); }
+  __device__ __forceinline__ int of(int64_t u) const {
+    const int64_t head = rest * (each + 1);
+    return (int)(u < head ? u / (each + 1) : rest + (u - head) / each);
+  }
+};
+__device__ __forceinline__ Seq few_bcast(const Seq& s, int src) {
+  Seq o;
+  o.start = __shfl_sync(0xffffffffu, s.start, src);
+  o.n = __shfl_sync(0xffffffffu, s.n, src);
+  o.len = __shfl_sync(0xffffffffu, s.len, src);
+  o.ok = __shfl_sync(0xffffffffu, (int)s.ok, src) != 0;
+  return o;
+}
+// Partials: O in ws [slots][RB][D], (m, l) behind it, [slots][RB].
+template <int D, int RB> __device__ __forceinline__ float* few_o(const AttnCall& a, int slot, int row) {
+  return a.ws + ((int64_t)slot * RB + row) * D;
+}
+template <int D, int RB> __device__ __forceinline__ float2* few_ml(const AttnCall& a, const FewPlan& p, int slot, int row) {
+  return reinterpret_cast<float2*>(a.ws + (int64_t)p.slots * RB * D) + (int64_t)slot * RB + row;
+}
+__device__ __forceinline__ float lse_of(float m, float l) { return (m + log2f(l)) * kLn2; }
+// (m, l) for a merge: a part with a NaN score has l NaN, and m may still be -inf, what a part without a key
+// has; NaN, it cannot be taken for one.
+__device__ __forceinline__ float2 part_stats(float m, float l) { return make_float2(l != l ? l : m, l); }
+
+template <int D> __device__ __forceinline__ void store_row(const AttnCall& a, int tok, int h, int lane, const float* v, float f) {
+  constexpr int C = D / 32;
+  bf16* o = reinterpret_cast<bf16*>(a.out) + (int64_t)tok * a.o_row + (int64_t)h * a.o_head + lane * C;
+#pragma unroll
+  for (int j = 0; j < C; j += 2) *reinterpret_cast<__nv_bfloat162*>(o + j) = __floats2bfloat162_rn(v[j] * f, v[j + 1] * f);
+}
+
+template <int D, int NB>
+__global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ragged r, AttnCall a, Kv8View kv, FewPlan plan) {
+  using C = FewCfg<D, NB>;
+  constexpr int RB = C::RB, S = C::STAGES, KS = D / 16, MT = D / 16;  // steps of the first product, tiles of the second
+  constexpr int VB = D / 8;                                          // bytes of a lane's piece of a V row
+  extern __shared__ __align__(16) uint8_t smem[];
+  constexpr int AREA = C::RING > C::MEET ? C::RING : C::MEET;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * S * C::BYTES;                       // this warp's stages
+  float2* scales = reinterpret_cast<float2*>(smem + AREA) + warp * S;  // (ks, vs) of a stage's page
+  float2* s_ml = reinterpret_cast<float2*>(smem + AREA) + kWarps * S;  // [warps][RB], later [RB] weights' sums
+  float* meet = reinterpret_cast<float*>(smem);                     // [warps][RB][LO]
+  pdl_trigger();
+  pdl_wait();
+  r.starts = after_wait(r.starts);
+  r.lens = after_wait(r.lens);
+  r.table = after_wait(r.table);
+  const int G = a.Hq / a.Hkv, cta = blockIdx.x, grid = gridDim.x;
+  const float sl2 = a.scale * kLog2e;
+  // every warp lays the work out for itself
+  const bool one = r.batch <= 32;
+  Seq mine{0, 0, 0, false};
+  if (one && lane < r.batch) mine = load_seq(r, lane);
+  auto seq_at = [&](int b) { return one ? mine : load_seq(r, b); };
+  auto units_of = [&](const Seq& s) {
+    return s.ok && s.n > 0 ? few_tiles(s, G, RB) * a.Hkv * (few_chunks(s, a.window) + plan.pad) : (int64_t)0;
+  };
+  int64_t total = 0;
+  for (int b = lane; b < r.batch; b += 32) {
+    const Seq s = seq_at(b);
+    if (!s.ok && cta == 0 && warp == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+    total += units_of(s);
+  }
+  const FewRanges rg(warp_sum64(total), plan, grid);
+  int64_t u = cta < rg.n ? rg.start(cta) : rg.units;
+  const int64_t u1 = cta < rg.n ? rg.start(cta + 1) : rg.units;
+  int64_t before = 0;
+  int seg = 0;
+  for (int base = 0; base < r.batch && u < u1; base += 32) {
+    Seq ls{0, 0, 0, false};
+    if (base + lane < r.batch) ls = seq_at(base + lane);
+    const int64_t mine_u = units_of(ls), incl = warp_scan64(mine_u, lane);
+    const int64_t chunk_end = before + __shfl_sync(0xffffffffu, incl, 31);
+    while (u < u1 && u < chunk_end) {
+      const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
+      const Seq s = few_bcast(ls, src);
+      const int b = base + src;
+      const int64_t off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
+      const int T = few_chunks(s, a.window);
+      const int64_t item = off / (T + plan.pad);
+      const int rt = (int)(item / a.Hkv), kvh = (int)(item - (int64_t)rt * a.Hkv);
+      const int64_t at = off - item * (T + plan.pad) - plan.pad;  // < 0: in front of the item's chunks
+      const int64_t most = u1 - u;
+      const int c0 = (int)max(at, (int64_t)0), take = (int)(min((int64_t)T, at + most) - c0);
+      u += min(T - at, most);
+      if (take <= 0) continue;
+      const int part = take == T ? -1 : 2 * cta + (seg > 0);
+      ++seg;
+      // ---- one stretch: rows r0 .. of the sequence, chunks [c0, c0 + take) behind the first
+      const int r0 = rt * RB, ctx = s.len - s.n, R = (int)min((int64_t)RB, (int64_t)s.n * G - r0);
+      const int p_first = ctx + r0 / G, p_last = ctx + (r0 + R - 1) / G;
+      const int k_lo = vis_lo(p_first, a.window), k_hi = vis_hi(p_last, s.len, a.causal);
+      const int clean_lo = vis_lo(p_last, a.window), clean_hi = vis_hi(p_first, s.len, a.causal);
+      const int chunk0 = few_first(s, a.window) + c0;
+      const int n_mine = take > warp ? (take - warp + kWarps - 1) / kWarps : 0;  // chunks chunk0 + warp + 8 i
+      const int32_t* tab = r.table + (int64_t)b * r.table_stride;
+      // pages and scales of this warp's next 32 chunks, one a lane
+      int pg = -1;
+      float ks = 0.f, vs = 0.f;
+      auto look_up = [&](int i0) {
+        const int i = i0 + lane, key = (chunk0 + warp + kWarps * i) * kChunk;
+        pg = -1;
+        ks = 1.f;
+        vs = 0.f;
+        if (i < n_mine && key < k_hi && key + kChunk > k_lo) {
+          pg = tab[key >> kv.page_shift];
+          if (pg < 0 || pg >= kv.n_pages) {
+            flag_status(r.status, DFLASH_STATUS_PAGE);
+            pg = -1;
+          } else {
+            ks = kv.ks[pg * kv.s_page + kvh * kv.s_head];
+            vs = kv.vs[pg * kv.s_page + kvh * kv.s_head];
+          }
+        }
+      };
+      auto issue = [&](int i) {  // chunk i of this warp into stage i % S
+        if (i < n_mine) {
+          if ((i & 31) == 0) look_up(i);
+          const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+          const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
+          if (lane == 0) scales[i % S] = make_float2(k1, v1);
+          const int key0 = (chunk0 + warp + kWarps * i) * kChunk;
+          const int64_t at = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot + kvh * kv.head;
+          const uint8_t* kp = kv.k + at;
+          const uint8_t* vp = kv.v + at;
+          const uint32_t dst = smem_addr(ring + (i % S) * C::BYTES) + lane * 16;
+          // (keys that no row of the tile sees arrive as zeros)
+          auto seen = [&](int j) { return page >= 0 && key0 + j >= k_lo && key0 + j < k_hi; };
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              cp_async<16>(dst + (h * (D / 64) + c) * 512, kp + (g + 8 * h) * kv.slot + 64 * c + 16 * t, seen(g + 8 * h));
+          const uint32_t vdst = smem_addr(ring + (i % S) * C::BYTES) + kChunk * D + lane * VB;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int j = 2 * t + (q & 1) + 8 * (q >> 1);
+            cp_async<VB>(vdst + q * 32 * VB, vp + j * kv.slot + VB * g, seen(j));
+          }
+        }
+        cp_commit();
+      };
+      // (the stages' first chunks are on their way while q is made ready)
+#pragma unroll
+      for (int i = 0; i < S - 1; ++i) issue(i);
+      // ---- q: lane (g, t) has rows g (+ 8 n) at the d's that it has of K
+      uint32_t qf[NB][KS][2];
+      float rowf[NB][2];  // of rows 2t, 2t + 1: scale 2^-e log2 e
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        const int row = 8 * n + g;
+        uint4 w[D / 32];
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) w[c] = make_uint4(0, 0, 0, 0);
+        if (row < R) {
+          const int i = (r0 + row) / G, h = kvh * G + (r0 + row) % G;
+          const bf16* q = reinterpret_cast<const bf16*>(a.q) + (int64_t)(s.start + i) * a.q_row + (int64_t)h * a.q_head;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) w[2 * c + k] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t + 8 * k);
+        }
+        const uint32_t* ww = reinterpret_cast<const uint32_t*>(w);
+        float most = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float x = fabsf(__uint_as_float(ww[k] << 16)), y = fabsf(__uint_as_float(ww[k] & 0xffff0000u));
+          most = fmaxf(most, fmaxf(nonfinite(x) ? 0.f : x, nonfinite(y) ? 0.f : y));
+        }
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+        // most 2^e in [2^14, 2^15); 2^e in two factors, either of them a normal number
+        const int e = most > 0.f ? 14 - ilogbf(most) : 0, e0 = e / 2;
+        const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+          const float x = __uint_as_float(ww[k] << 16) * f0 * f1, y = __uint_as_float(ww[k] & 0xffff0000u) * f0 * f1;
+          qf[n][k / 2][k & 1] = pack_h2(x, y);
+        }
+        const float f = ldexpf(sl2, -e);
+        // rows 2t, 2t + 1 of this tile are those of lanes g = 2t, 2t + 1
+        rowf[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+        rowf[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+      }
+      float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+#pragma unroll
+        for (int k = 0; k < MT; ++k)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+      }
+      for (int i = 0; i < n_mine; ++i) {
+        cp_wait<S - 2>();
+        __syncwarp();  // (the stage's scales are lane 0's; what was read of the next stage to be filled has been)
+        issue(i + S - 1);
+        const uint8_t* stage = ring + (i % S) * C::BYTES;
+        const float2 sc = scales[i % S];
+        const int key0 = (chunk0 + warp + kWarps * i) * kChunk;
+        // ---- S^T
+        float x[NB][4];
+        {
+          float acc[2][NB][4];
+#pragma unroll
+          for (int p = 0; p < 2; ++p)
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.f;
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            const uint4 k0 = *reinterpret_cast<const uint4*>(stage + c * 512 + lane * 16);
+            const uint4 k8 = *reinterpret_cast<const uint4*>(stage + (D / 64 + c) * 512 + lane * 16);
+            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w8[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint32_t a0 = lo_h2(w0[j]), a1 = lo_h2(w8[j]), a2 = hi_h2(w0[j]), a3 = hi_h2(w8[j]);
+#pragma unroll
+              for (int n = 0; n < NB; ++n) mma(acc[j & 1][n], a0, a1, a2, a3, qf[n][4 * c + j][0], qf[n][4 * c + j][1]);
+            }
+          }
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) x[n][j] = (acc[0][n][j] + acc[1][n][j]) * sc.x * rowf[n][j & 1];
+        }
+        const bool clean = key0 >= clean_lo && key0 + kChunk <= clean_hi;
+        auto sees = [&](int n, int j, int key) {  // row 2t + (j & 1) of tile n
+          const int row = r0 + 8 * n + 2 * t + (j & 1), p = ctx + row / G;
+          return row < r0 + R && key >= vis_lo(p, a.window) && key < vis_hi(p, s.len, a.causal);
+        };
+        if (!clean) {
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              if (!sees(n, j, key0 + g + (j >> 1) * 8)) x[n][j] = -INFINITY;
+        }
+        // ---- the maximum moves when a score is more than 2^kSlack above it; the unit when V's scale is above it
+        bool grow = sc.y > unit;
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack;
+          grow |= fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
+        }
+        if (__any_sync(0xffffffffu, grow)) {
+          const float was = unit;
+          if (sc.y > unit) unit = 2.f * sc.y;  // (some room, so that it does not move again at once)
+          const float fu = was > 0.f ? was / unit : 1.f;
+#pragma unroll
+          for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              float mx = fmaxf(x[n][j], x[n][j + 2]);
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+              const float mn = mx > m[n][j] + kSlack ? mx : m[n][j];
+              const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - mn);  // (sums so far are 0 or NaN there)
+              m[n][j] = mn;
+              l[n][j] *= f;
+#pragma unroll
+              for (int k = 0; k < MT; ++k) {
+                o[n][k][j] *= f * fu;
+                o[n][k][j + 2] *= f * fu;
+              }
+            }
+        }
+        // ---- P, its sums, and P^T as the second product's operand
+        const float rv = unit > 0.f ? sc.y / unit * kUnit : 0.f;
+        uint32_t pb[NB][2];
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          float p[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            p[j] = ex2(x[n][j] - (m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1]));
+            l[n][j & 1] += p[j];
+          }
+          pb[n][0] = transpose8(pack_h2(p[0] * rv, p[1] * rv));
+          pb[n][1] = transpose8(pack_h2(p[2] * rv, p[3] * rv));
+        }
+        // ---- O^T
+        constexpr int VW = VB / 4;  // words of a lane's piece
+        uint32_t vw[4][VW];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const uint8_t* p = stage + kChunk * D + q * 32 * VB + lane * VB;
+          if constexpr (VW == 4) {
+            const uint4 v = *reinterpret_cast<const uint4*>(p);
+            vw[q][0] = v.x, vw[q][1] = v.y, vw[q][2] = v.z, vw[q][3] = v.w;
+          } else {
+            const uint2 v = *reinterpret_cast<const uint2*>(p);
+            vw[q][0] = v.x, vw[q][1] = v.y;
+          }
+        }
+        if (!clean) {
+          // A key that a row does not see may hold a NaN, and 0 x NaN is NaN: such codes become 0, and the rows
+          // that do see them get the NaN by hand.
+          uint32_t found = 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < VW; ++k) found |= nan_bytes(vw[q][k]);
+          if (__any_sync(0xffffffffu, found != 0)) {
+#pragma unroll 1
+            for (int st = 0; st < 4; ++st)
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int key = key0 + 2 * st + (q & 1) + 8 * (q >> 1);
+#pragma unroll
+                for (int k = 0; k < VW; ++k) {
+                  const uint32_t bad = nan_bytes(__shfl_sync(0xffffffffu, vw[q][k], 4 * g + st));
+#pragma unroll
+                  for (int e = 0; e < 4; ++e)  // d 16 g + 4 k + e: tile 2 k + e / 2, its row g + 8 (e & 1)
+                    if ((bad >> (8 * e + 7)) & 1u)
+#pragma unroll
+                      for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int j = 0; j < 2; ++j)
+                          if (sees(n, j, key)) o[n][2 * k + e / 2][2 * (e & 1) + j] = __uint_as_float(0x7fffffffu);
+                }
+              }
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+#pragma unroll
+              for (int k = 0; k < VW; ++k) vw[q][k] &= ~((nan_bytes(vw[q][k]) >> 7) * 0xffu);
+          }
+        }
+#pragma unroll
+        for (int k = 0; k < VW; ++k) {
+          const uint32_t e0 = __byte_perm(vw[0][k], vw[1][k], 0x5140), e1 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
+          const uint32_t f0 = __byte_perm(vw[2][k], vw[3][k], 0x5140), f1 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
+          const uint32_t a0 = lo_h2(e0), a1 = hi_h2(e0), a2 = lo_h2(f0), a3 = hi_h2(f0);
+          const uint32_t b0 = lo_h2(e1), b1 = hi_h2(e1), b2 = lo_h2(f1), b3 = hi_h2(f1);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            mma(o[n][2 * k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            mma(o[n][2 * k + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+      cp_wait<0>();
+      // ---- the warps meet: O [row][d] and (m, l) of each
+      __syncthreads();  // every warp has read its ring
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          float sum = l[n][j];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int row = 8 * n + 2 * t + j;
+          if (g == 0) s_ml[warp * RB + row] = part_stats(m[n][j], sum);
+          float* dst = meet + (warp * RB + row) * C::LO + VB * g;
+          const float f = unit * (1.f / kUnit);
+#pragma unroll
+          for (int k = 0; k < MT; k += 2)
+            *reinterpret_cast<float4*>(dst + 2 * k) =
+                make_float4(o[n][k][j] * f, o[n][k][j + 2] * f, o[n][k + 1][j] * f, o[n][k + 1][j + 2] * f);
+        }
+      __syncthreads();
+      for (int row = warp; row < R; row += kWarps) {
+        float2 ml = make_float2(-INFINITY, 0.f);
+        if (lane < kWarps) ml = s_ml[lane * RB + row];
+        const float M = warp_max(ml.x);
+        // a warp that saw no key has weight 0, the NaN of one with a NaN score stays one
+        const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+        const float L = warp_sum(wt == 0.f ? 0.f : ml.y * wt);
+        const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
+        float acc[D / 32];
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          const float ww = __shfl_sync(0xffffffffu, wt, w);
+          const float* v = meet + (w * RB + row) * C::LO + lane * (D / 32);
+          // (a weight that underflows still takes its sums along: 0 x NaN is NaN)
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(ww, (saw >> w) & 1u ? v[j] : 0.f, acc[j]);
+        }
+        const int tok = s.start + (r0 + row) / G, h = kvh * G + (r0 + row) % G;
+        if (part >= 0) {
+          float* w = few_o<D, RB>(a, part, row) + lane * (D / 32);
+#pragma unroll
+          for (int j = 0; j < D / 32; ++j) w[j] = acc[j];
+          if (lane == 0) *few_ml<D, RB>(a, plan, part, row) = part_stats(M, L);
+        } else {
+          store_row<D>(a, tok, h, lane, acc, 1.f / L);
+          if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
+        }
+      }
+      __syncthreads();  // the rings are free again
+    }
+    before = chunk_end;
+  }
+}
+
+// Merge of the parts of each item that a range boundary cut, in key order.  CTA (c - 1, y): boundary c, if it
+// is the first inside its item; a warp per row.
+template <int D, int RB>
+__global__ void __launch_bounds__(256) k_kv8_few_merge(Ragged r, AttnCall a, FewPlan plan, int grid) {
+  constexpr int C = D / 32;
+  pdl_trigger();
+  pdl_wait();
+  r.starts = after_wait(r.starts);
+  r.lens = after_wait(r.lens);
+  a.ws = after_wait(a.ws);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, G = a.Hq / a.Hkv, c = blockIdx.x + 1;
+  const bool one = r.batch <= 32;
+  Seq mine{0, 0, 0, false};
+  if (one && lane < r.batch) mine = load_seq(r, lane);
+  auto units_of = [&](const Seq& s) {
+    return s.ok && s.n > 0 ? few_tiles(s, G, RB) * a.Hkv * (few_chunks(s, a.window) + plan.pad) : (int64_t)0;
+  };
+  int64_t total = 0;
+  for (int b = lane; b < r.batch; b += 32) total += units_of(one ? mine : load_seq(r, b));
+  const FewRanges rg(warp_sum64(total), plan, grid);
+  if (c >= rg.n) return;
+  const int64_t u = rg.start(c);
+  int64_t before = 0;
+  for (int base = 0; base < r.batch; base += 32) {
+    Seq ls{0, 0, 0, false};
+    if (base + lane < r.batch) ls = one ? mine : load_seq(r, base + lane);
+    const int64_t mine_u = units_of(ls), incl = warp_scan64(mine_u, lane);
+    const int64_t end = before + __shfl_sync(0xffffffffu, incl, 31);
+    if (u >= end) {
+      before = end;
+      continue;
+    }
+    const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
+    const int64_t seq_u = before + __shfl_sync(0xffffffffu, incl - mine_u, src);
+    const Seq s = few_bcast(ls, src);
+    const int T = few_chunks(s, a.window) + plan.pad;
+    const int64_t item = (u - seq_u) / T, i_begin = seq_u + item * T;
+    // no cut here (in front of the item's chunks), or not the item's first
+    if (u <= i_begin + plan.pad || rg.start(c - 1) > i_begin + plan.pad) return;
+    const int rt = (int)(item / a.Hkv), kvh = (int)(item - (int64_t)rt * a.Hkv);
+    const int parts = rg.of(i_begin + T - 1) - (c - 1) + 1;
+    const int slot0 = 2 * (c - 1) + (rg.start(c - 1) < i_begin);
+    auto slot_of = [&](int q) { return q == 0 ? slot0 : 2 * (c - 1 + q); };
+    const int r0 = rt * RB, R = (int)min((int64_t)RB, (int64_t)s.n * G - r0), row = blockIdx.y * 8 + warp;
+    if (row >= R) return;
+    float M = -INFINITY, L = 0.f, acc[C];
+#pragma unroll
+    for (int j = 0; j < C; ++j) acc[j] = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (p0 + lane < parts) ml = *few_ml<D, RB>(a, plan, slot_of(p0 + lane), row);
+      const int cnt = min(32, parts - p0);
+      const float Mn = fmaxf(M, warp_max(ml.x)), mref = Mn == -INFINITY ? 0.f : Mn;
+      const float f = M == -INFINITY ? 0.f : exp2f(M - mref);
+      const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
+      const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - mref);
+      // (sums so far under a maximum of -inf are 0, or the NaN of a NaN score, which stays one)
+      L = (M == -INFINITY ? L : L * f) + warp_sum(wt == 0.f ? 0.f : ml.y * wt);
+#pragma unroll
+      for (int j = 0; j < C; ++j) acc[j] *= M == -INFINITY ? 1.f : f;
+      M = Mn;
+#pragma unroll 4
+      for (int q = 0; q < cnt; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, wt, q);
+        const float* v = few_o<D, RB>(a, slot_of(p0 + q), row) + lane * C;
+        const bool yes = (saw >> q) & 1u;
+#pragma unroll
+        for (int j = 0; j < C; ++j) acc[j] = fmaf(wq, yes ? v[j] : 0.f, acc[j]);
+      }
+    }
+    const int tok = s.start + (r0 + row) / G, h = kvh * G + (r0 + row) % G;
+    store_row<D>(a, tok, h, lane, acc, 1.f / L);
+    if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
+    return;
+  }
+}
+
+int rows_of(const Ragged& r, const AttnCall& a) {
+  return (int)std::min<int64_t>((int64_t)r.max_rows * (a.Hq / a.Hkv), 1 << 20);
+}
+int few_nb(const Ragged& r, const AttnCall& a) {
+  const int rows = rows_of(r, a);
+  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
+}
+FewPlan few_plan(int nb, int sms) {
+  FewPlan p;
+  p.pad = 8;
+  p.min_units = 8;
+  p.slots = 2 * sms * (nb <= 2 ? 2 : 1);
+  return p;
+}
+
+template <int D, int NB>
+cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
+  using C = FewCfg<D, NB>;
+  static std::atomic<bool> done[64];
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev >= 64 || !done[dev]) {
+    e = cudaFuncSetAttribute(k_kv8_few<D, NB>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)C::SMEM);
+    if (e != cudaSuccess) return e;
+    if (dev < 64) done[dev] = true;
+  }
+  const FewPlan p = few_plan(NB, sms);
+  const int grid = sms * C::CTAS;
+  e = launch_k(k_kv8_few<D, NB>, grid, kWarps * 32, C::SMEM, st, r, a, kv, p);
+  if (e != cudaSuccess) return e;
+  const int rows = std::min(rows_of(r, a), C::RB);
+  return launch_k(k_kv8_few_merge<D, C::RB>, dim3(grid - 1, (rows + 7) / 8), 256, 0, st, r, a, p, grid);
+}
+template <int D>
+cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
+  const int nb = few_nb(r, a);
+  return nb == 1 ? launch_few<D, 1>(r, a, kv, sms, st) : nb == 2 ? launch_few<D, 2>(r, a, kv, sms, st) : launch_few<D, 4>(r, a, kv, sms, st);
+}
+
+}  // namespace
+
+int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms) {
+  const int nb = few_nb(r, a);
+  return (int64_t)few_plan(nb, sms).slots * 8 * nb * (a.d + 2) * 4;
+}
+cudaError_t launch_kv8_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
+  return a.d == 64 ? launch_few<64>(r, a, kv, sms, st) : launch_few<128>(r, a, kv, sms, st);
+}
+
+}  // namespace dfl
