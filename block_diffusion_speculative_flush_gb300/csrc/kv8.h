@@ -40,6 +40,9 @@ __device__ __forceinline__ uint16_t f2_to_e4m3x2(float a, float b) {
   asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c) : "f"(b), "f"(a));
   return c;
 }
+// Bit 7 of each byte that is a NaN, and the word with those bytes 0.
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
+__device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
 // whether x is not finite (from its bits: fast-math flags do not change that)
 __device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
 
@@ -50,5 +53,8 @@ cudaError_t launch_kv8_simt(const Ragged& r, const AttnCall& a, const Kv8View& k
 // Few rows on the tensor cores (bf16, head_dim 64 or 128).
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms);
 cudaError_t launch_kv8_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st);
+
+// Many rows on the tensor cores (bf16, head_dim 64 or 128): attn_tc_workspace with kv8.
+cudaError_t launch_attn_tc8(const Ragged& r, const AttnCall& a, const Kv8View& kv, cudaStream_t st);
 
 }  // namespace dfl

@@ -404,12 +404,19 @@ int kv8_sms() {
 }
 
 // The kernel of a call: bf16 with head_dim 64 or 128 runs on the tensor cores.
-bool kv8_few(const dflash_attention* a, const Ragged& r) {
-  return a->dtype == DFLASH_DTYPE_BF16 && (a->head_dim == 64 || a->head_dim == 128) &&
-         (int64_t)r.max_rows * (a->n_q_heads / a->n_kv_heads) <= 64;
+enum class Path { kSimt, kFew, kTiles };
+Path kv8_path(const dflash_attention* a, const Ragged& r) {
+  if (a->dtype != DFLASH_DTYPE_BF16 || (a->head_dim != 64 && a->head_dim != 128)) return Path::kSimt;
+  return (int64_t)r.max_rows * (a->n_q_heads / a->n_kv_heads) <= 64 ? Path::kFew : Path::kTiles;
 }
 int64_t kv8_workspace(const dflash_attention* a, const Ragged& r, int sms) {
-  return kv8_few(a, r) ? kv8_few_workspace(r, kv8_call(a), sms) : kv8_simt_workspace(r, kv8_call(a), sms);
+  const AttnCall c = kv8_call(a);
+  int64_t bytes = 0;
+  switch (kv8_path(a, r)) {
+    case Path::kSimt: return kv8_simt_workspace(r, c, sms);
+    case Path::kFew: return kv8_few_workspace(r, c, sms);
+    default: attn_tc_workspace(r, c, &bytes, true); return bytes;
+  }
 }
 
 }  // namespace
@@ -448,9 +455,11 @@ DFLASH_API int dflash_kv8_attention(const dflash_attention* a, const dflash_ragg
   const AttnCall c = kv8_call(a);
   const Kv8View kv = kv8_view(pages);
   cudaStream_t st = (cudaStream_t)stream;
-  return rcheck(kv8_few(a, r) ? launch_kv8_few(r, c, kv, sms, st)
-                              : launch_kv8_simt(r, c, kv, a->dtype == DFLASH_DTYPE_BF16, sms, st),
-                call);
+  switch (kv8_path(a, r)) {
+    case Path::kSimt: return rcheck(launch_kv8_simt(r, c, kv, a->dtype == DFLASH_DTYPE_BF16, sms, st), call);
+    case Path::kFew: return rcheck(launch_kv8_few(r, c, kv, sms, st), call);
+    default: return rcheck(launch_attn_tc8(r, c, kv, st), call);
+  }
 }
 
 }  // extern "C"

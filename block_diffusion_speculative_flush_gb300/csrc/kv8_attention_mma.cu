@@ -90,8 +90,6 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
 }
 __device__ __forceinline__ uint32_t lo_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)c); }
 __device__ __forceinline__ uint32_t hi_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)(c >> 16)); }
-// bytes of codes that are NaN: bit 7 of each
-__device__ __forceinline__ uint32_t nan_bytes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 
 // ---------------------------------------------------------------------------
 // the layout of the work
@@ -433,7 +431,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
           for (int q = 0; q < 4; ++q)
 #pragma unroll
-            for (int k = 0; k < VW; ++k) found |= nan_bytes(vw[q][k]);
+            for (int k = 0; k < VW; ++k) found |= nan_codes(vw[q][k]);
           if (__any_sync(0xffffffffu, found != 0)) {
 #pragma unroll 1
             for (int st = 0; st < 4; ++st)
@@ -442,7 +440,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
                 const int key = key0 + 2 * st + (q & 1) + 8 * (q >> 1);
 #pragma unroll
                 for (int k = 0; k < VW; ++k) {
-                  const uint32_t bad = nan_bytes(__shfl_sync(0xffffffffu, vw[q][k], 4 * g + st));
+                  const uint32_t bad = nan_codes(__shfl_sync(0xffffffffu, vw[q][k], 4 * g + st));
 #pragma unroll
                   for (int e = 0; e < 4; ++e)  // d 16 g + 4 k + e: tile 2 k + e / 2, its row g + 8 (e & 1)
                     if ((bad >> (8 * e + 7)) & 1u)
@@ -456,7 +454,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-              for (int k = 0; k < VW; ++k) vw[q][k] &= ~((nan_bytes(vw[q][k]) >> 7) * 0xffu);
+              for (int k = 0; k < VW; ++k) vw[q][k] = without_nan(vw[q][k]);
           }
         }
 #pragma unroll

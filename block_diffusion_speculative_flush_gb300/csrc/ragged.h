@@ -76,7 +76,7 @@ int64_t attn_simt_workspace(const Ragged& r, const AttnCall& a);
 cudaError_t launch_attn_simt(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st);
 
 // The tensor-core path (bf16, head_dim 64 or 128).
-cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes);
+cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes, bool kv8 = false);
 cudaError_t launch_attn_tc(const Ragged& r, const AttnCall& a, const KVView& kv, cudaStream_t st);
 
 }  // namespace dfl

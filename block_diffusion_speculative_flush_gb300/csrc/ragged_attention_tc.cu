@@ -49,6 +49,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "kv8.h"
 #include "launch.h"
 #include "ragged.h"
 #include "tc_ptx.cuh"
@@ -94,19 +95,31 @@ struct Work {
   int32_t done;
 };
 
-template <int D, int NQ>
+// Scales of an 8-bit tile's keys, a pair for each 16 of them.
+struct __align__(16) TileScales {
+  float ks[KT / 16], vs[KT / 16];
+  float most_v;    // the largest of vs
+  int32_t mixed;   // not all alike
+  int32_t pad[2];
+};
+
+template <int D, int NQ, bool KV8 = false>
 struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
   // 128 bytes of 32 rows for each softmax warp (NQ = 1: in the Q tile it has done with)
   static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;
   static constexpr int RING = (7 * 32768 - STAGE) / SLOT - 2;  // K/V tiles in flight
   static constexpr int DATA = (RING + 2) * SLOT + STAGE;  // 224 KB
-  static constexpr int THREADS = (4 * NQ + 4) * 32;
+  static constexpr int THREADS = (4 * NQ + (KV8 ? 8 : 4)) * 32;
   // NQ = 2: registers of the softmax warps and of the other four; the launch's
   // 168 for all spilled 100 bytes in the key loop (452 -> 424 us for the packed
   // prompts of 1 to 8192 tokens).  8 x 200 + 4 x 104 = 12 x 168.
-  static constexpr int R_SOFTMAX = 200, R_REST = 104;
-  static constexpr size_t SMEM = DATA + 768;  // + barriers and descriptors
+  // With converters: 8 x 184 + 4 x 56 + 4 x 88 = 16 x 128.
+  static constexpr int R_SOFTMAX = KV8 ? 184 : 200, R_REST = KV8 ? 56 : 104, R_CONVERT = 88;
+  static constexpr int EXTRA = 768;  // barriers and descriptors
+  // scales of as many tiles as the ring holds, the one that is being read and the next
+  static constexpr int NSCALES = 8;
+  static constexpr size_t SMEM = DATA + EXTRA + (KV8 ? NSCALES * sizeof(TileScales) + 2 * 2 * 128 * 2 : 0);
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -438,11 +451,172 @@ __device__ __noinline__ bool softmax_tile_call(const TileArgs a, float& m, float
   return softmax_tile<D, 1>(a, m, l, pv_done, parity, abort_flag);
 }
 
-template <int D, int NQ>
-__global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
-    k_ragged_tc(Ragged r, AttnCall a, KVView kv, Plan p, const __grid_constant__ CUtensorMap mq,
+// The same over an 8-bit cache (NQ = 2): scores of the codes times the key's scale, P in
+// fp16 as p (vs / u) 2^7, u the largest scale of V so far.  p <= 2^8, so P <= 2^15.
+// a.sl2: scale log2(e) 2^-e of the row.
+constexpr float kUnit8 = 128.f;
+__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
+  uint64_t z;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
+  return z;
+}
+template <int D>
+__device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScales& ts, float& m, float& l, float& unit) {
+  float s[128];
+  fence_after();
+  tmem_ld128_halves(a.tS, s);
+  const bool mixed = ts.mixed != 0;
+  float k = a.sl2;
+  if (mixed) {
+#pragma unroll
+    for (int q = 0; q < KT / 16; ++q) {
+      const float f = ts.ks[q];
+      const uint64_t f2 = f2pack(f, f);
+#pragma unroll
+      for (int j = 0; j < 16; j += 2) {
+        const float2 v = f2unpack(mul2(f2pack(s[16 * q + j], s[16 * q + j + 1]), f2));
+        s[16 * q + j] = v.x;
+        s[16 * q + j + 1] = v.y;
+      }
+    }
+  } else {
+    k *= ts.ks[0];
+  }
+  if (a.masked_hi) {
+#pragma unroll
+    for (int c = 0; c < 128; c += 32) {
+      const int n = min(max(a.hi - c, 0), 32);
+      const uint32_t keep = n == 32 ? 0xffffffffu : (1u << n) - 1u;
+#pragma unroll
+      for (int j = 0; j < 32; ++j) s[c + j] = (keep >> j) & 1u ? s[c + j] : -INFINITY;
+    }
+  }
+  if (a.masked_lo) {
+#pragma unroll
+    for (int j = 0; j < 128; ++j) s[j] = j >= a.lo ? s[j] : -INFINITY;
+  }
+  float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+#pragma unroll
+  for (int j = 4; j < 124; j += 8) {
+    m0 = max3(m0, s[j], s[j + 1]);
+    m1 = max3(m1, s[j + 2], s[j + 3]);
+    m2 = max3(m2, s[j + 4], s[j + 5]);
+    m3 = max3(m3, s[j + 6], s[j + 7]);
+  }
+  m0 = max3(m0, s[124], s[125]);
+  m1 = max3(m1, s[126], s[127]);
+  const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * k;
+  const bool grow = a.valid && mt > m + 8.f, first = m == -INFINITY;
+  const float most_v = ts.most_v;
+  if (__any_sync(0xffffffffu, (grow && !first) || (most_v > unit && unit > 0.f))) {
+    const float fm = grow && !first ? ex2(m - mt) : 1.f;
+    const float f = most_v > unit && unit > 0.f ? fm * (unit / most_v) : fm;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+      float o[32];
+      tmem_ld32(a.tO + c, o);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] *= f;
+      tmem_st32(a.tO + c, o);
+    }
+    l *= fm;
+  }
+  unit = fmaxf(unit, most_v);
+  if (grow) m = mt;
+  const float mref = m == -INFINITY ? 0.f : m;
+  const bool weigh = mixed || ts.vs[0] != unit;
+  // where all scales of V are the unit, 2^7 goes into the exponent
+  const uint64_t k2 = f2pack(k, k);
+  const float c1 = weigh ? -mref : 7.f - mref;
+  const uint64_t c2 = f2pack(c1, c1);
+  uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
+  const float to_unit = unit > 0.f ? kUnit8 / unit : 0.f;
+  auto probs = [&](int c) {  // 32 keys
+    uint32_t pk[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) {
+      uint64_t e2;
+      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
+      const float2 e = f2unpack(e2);
+      uint64_t p2 = f2pack(ex2(e.x), ex2(e.y));
+      if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(p2));
+      else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(p2));
+      if (weigh) {
+        const float w = ts.vs[(c + 2 * j) / 16] * to_unit;
+        p2 = mul2(p2, f2pack(w, w));
+      }
+      const float2 p = f2unpack(p2);
+      const __half2 h2 = __floats2half2_rn(p.x, p.y);
+      pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
+    }
+    tmem_st16u(a.tS + c / 2, pk);
+  };
+  probs(0);
+  probs(32);
+  probs(64);
+  probs(96);
+  const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
+  const float sum = (s0.x + s0.y) + (s1.x + s1.y);
+  l += weigh ? sum : sum * (1.f / kUnit8);
+}
+
+// A NaN among V's codes that the converters put to 0, given to the rows that see it (as
+// add_nonfinite does).
+template <int D>
+__device__ __noinline__ void add_nan8(Ragged r, Kv8View kv, const Work& w, uint32_t tO, int i, int window, int causal) {
+  const int pos = w.len - w.n + i, lo = vis_lo(pos, window), hi = vis_hi(pos, w.len, causal);
+  const int lane = threadIdx.x & 31, T = max(w.nt[0], w.nt[1]);
+  for (int t = 0; t < T; ++t) {
+    const int kt = (w.t0 + t) * KT, in = min(KT, w.len - kt);
+    if (kt >= w.clean_lo && kt + in <= w.clean_hi) {  // and so are all up to the edge
+      t = max(t, w.clean_hi / KT - 1 - w.t0);
+      continue;
+    }
+    for (int base = kt; base < kt + in; base += 32) {
+      const int j = base + lane;
+      const uint32_t* v = nullptr;
+      uint32_t found = 0;
+      if (j < kt + in) {
+        const int pg = r.table[(int64_t)w.b * r.table_stride + (j >> kv.page_shift)];
+        if (pg >= 0 && pg < kv.n_pages) {
+          v = reinterpret_cast<const uint32_t*>(kv.v + pg * kv.page + (j & ((1 << kv.page_shift) - 1)) * kv.slot + w.kvh * kv.head);
+          for (int c = 0; c < D / 4; ++c) found |= nan_codes(v[c]);
+        }
+      }
+      uint32_t todo = __ballot_sync(0xffffffffu, found != 0);
+      while (todo) {
+        const int src = __ffs(todo) - 1;
+        todo &= todo - 1;
+        const uint32_t* e = reinterpret_cast<const uint32_t*>(__shfl_sync(0xffffffffu, (unsigned long long)v, src));
+        const bool see = base + src >= lo && base + src < hi;
+#pragma unroll 1
+        for (int c = 0; c < D; c += 32) {
+          float o[32];
+          tmem_ld32(tO + c, o);
+#pragma unroll
+          for (int k = 0; k < 32; ++k)
+            if (see && (nan_codes(e[(c + k) / 4]) >> (8 * (k % 4) + 7)) & 1u) o[k] = __uint_as_float(0x7fffffffu);
+          tmem_st32(tO + c, o);
+        }
+      }
+    }
+  }
+}
+
+// Sixteen codes as fp16, the first eight and the others.
+__device__ __forceinline__ void codes_to_h16(const uint4& c, uint4& lo, uint4& hi) {
+  lo = make_uint4(e4m3x2_to_h2((uint16_t)c.x), e4m3x2_to_h2((uint16_t)(c.x >> 16)), e4m3x2_to_h2((uint16_t)c.y),
+                  e4m3x2_to_h2((uint16_t)(c.y >> 16)));
+  hi = make_uint4(e4m3x2_to_h2((uint16_t)c.z), e4m3x2_to_h2((uint16_t)(c.z >> 16)), e4m3x2_to_h2((uint16_t)c.w),
+                  e4m3x2_to_h2((uint16_t)(c.w >> 16)));
+}
+
+template <int D, int NQ, bool KV8>
+__global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
+    k_ragged_tc(Ragged r, AttnCall a, typename std::conditional<KV8, Kv8View, KVView>::type kv, Plan p, const __grid_constant__ CUtensorMap mq,
                 const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
-  using C = Cfg<D, NQ>;
+  using C = Cfg<D, NQ, KV8>;
+  static_assert(!KV8 || (NQ == 2 && C::RING / 2 + 2 <= C::NSCALES), "8-bit tiles: two row tiles, scales of what is in flight");
   constexpr int SLOT = C::SLOT, RING = C::RING, NB = D / 64;
   constexpr int SW = 4 * NQ;  // the first warp behind the softmax
   extern __shared__ __align__(1024) uint8_t smem[];
@@ -463,15 +637,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(all_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Work* works = (Work*)(tmem_slot + 2);
+  // 8 bits: scales of the last tiles, the rows' exponents of Q [stretch & 1][tile][row], and (in
+  // place of what the fixer signals) Q as fp16
+  TileScales* tscales = (TileScales*)(sS + C::STAGE + C::EXTRA);
+  int16_t* q_exp = (int16_t*)(tscales + C::NSCALES);
+  uint64_t* q_ready = v_fix;
   static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
 
   if (tid == 0) {
     for (int s = 0; s < RING; ++s) {
-      mbar_init(&full[s], 1);
-      mbar_init(&empty[s], 2);  // the MMAs (seen by a softmax warp, or a commit) and the fixer
-      mbar_init(&v_fix[s], 1);
+      mbar_init(&full[s], KV8 ? 4 : 1);
+      mbar_init(&empty[s], KV8 ? 1 : 2);  // the MMAs (seen by a softmax warp, or a commit) and the fixer
+      mbar_init(&v_fix[s], KV8 ? 4 : 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&q_full[s], 1);
@@ -482,7 +661,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], SW + 3);  // all warps but the scheduler
+      mbar_init(&w_empty[s], KV8 ? SW + 6 : SW + 3);  // all warps but the scheduler (8 bits: nor the fixer)
     }
     mbar_init(all_done, 1);
     *abort_flag = 0;
@@ -508,8 +687,187 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
   };
 
   if (warp >= SW) {
-  if constexpr (NQ == 2) regs_dec<C::R_REST>();
-  if (warp == SW + 3) {
+  if constexpr (KV8) {
+    if (warp >= SW + 4) regs_dec<C::R_CONVERT>();
+    else regs_dec<C::R_REST>();
+  } else if constexpr (NQ == 2) {
+    regs_dec<C::R_REST>();
+  }
+  if (KV8 && warp >= SW + 4) {
+    if constexpr (KV8) {
+      // ---- converters: codes from memory, as fp16 into the ring.  A thread has 16 codes of each of N keys of
+      // a tile; as one is stored, the same piece of the next tile is asked for.
+      constexpr int PIECES = D / 16, KEYS = 128 / PIECES, N = KT / KEYS;
+      const int ct = tid & 127, cw = ct >> 5, piece = ct % PIECES, key = ct / PIECES;
+      r.table = after_wait(r.table);
+      uint32_t it = 0, q_use[2] = {0, 0};
+      bool ok = true;
+      // where the piece's two 16-byte chunks lie in a tile, less the key's row (keys of a thread agree mod 8).
+      // D = 128: lanes of the second block store their chunks in turn, so that no two of a phase meet in a bank.
+      const bool swap = D == 128 && piece >= 4;
+      const int block = piece / 4 * (SLOT / NB), c0 = 2 * (piece % 4) + swap, c1 = 2 * (piece % 4) + !swap;
+      const int at0 = block + ((c0 ^ (key & 7)) << 4), at1 = block + ((c1 ^ (key & 7)) << 4);
+      for (int k = 0; ok; ++k) {
+        const int ws = k % NW;
+        if (!__all_sync(0xffffffffu, mbar_wait(&w_full[ws], (uint32_t)(k / NW) & 1u, abort_flag))) {
+          ok = false;
+          break;
+        }
+        Work& w = works[ws];
+        const int T = max(w.nt[0], w.nt[1]);
+        if (w.done) break;
+        const int len = w.len, lo_out = vis_lo(w.len - w.n + w.i0, a.window);
+        const int32_t* tab = r.table + (int64_t)w.b * r.table_stride;
+        const uint8_t* kb = kv.k + (int64_t)w.kvh * kv.head + piece * 16;
+        const uint8_t* vb = kv.v + (int64_t)w.kvh * kv.head + piece * 16;
+        const int64_t s_at = w.kvh * kv.s_head;
+        const int tile0 = w.t0;
+        // the page and scales of 16 keys of a tile, a lane each (lanes 0 .. 7)
+        int pg = -1;
+        float ks = 1.f, vs = 0.f;
+        auto look_up = [&](int t) {
+          pg = -1;
+          ks = 1.f;
+          vs = 0.f;
+          const int first = (tile0 + t) * KT + 16 * lane;
+          if (lane < KT / 16 && t < T && first < len) {
+            pg = tab[first >> kv.page_shift];
+            if (pg < 0 || pg >= kv.n_pages) {
+              // (a page that the window of every row has left behind may be gone)
+              flag_status(((first >> kv.page_shift) + 1) << kv.page_shift > lo_out ? r.status : nullptr, DFLASH_STATUS_PAGE);
+              pg = -1;
+            } else if (first + 16 > lo_out) {
+              ks = kv.ks[pg * kv.s_page + s_at];
+              vs = kv.vs[pg * kv.s_page + s_at];
+            }
+          }
+        };
+        uint4 q[N];
+        auto load = [&](int i, int t, const uint8_t* base, int pages) {
+          const int j = key + KEYS * i, pos = (tile0 + t) * KT + j;
+          const int page = __shfl_sync(0xffffffffu, pages, j / 16);
+          q[i] = make_uint4(0, 0, 0, 0);
+          if (t < T && page >= 0 && pos < len)
+            q[i] = *reinterpret_cast<const uint4*>(base + page * kv.page + (int64_t)(pos & ((1 << kv.page_shift) - 1)) * kv.slot);
+        };
+        auto slot = [&](uint32_t i) {  // the ring's entry i, free
+          if (i >= (uint32_t)RING && !__all_sync(0xffffffffu, mbar_wait(&empty[i % RING], (i / RING - 1) & 1u, abort_flag))) ok = false;
+          return sR + (i % RING) * SLOT;
+        };
+        auto store = [&](int i, uint8_t* tile) {
+          uint4 lo, hi;
+          codes_to_h16(q[i], lo, hi);
+          uint8_t* row = tile + (key + KEYS * i) * 128;
+          *reinterpret_cast<uint4*>(row + at0) = swap ? hi : lo;
+          *reinterpret_cast<uint4*>(row + at1) = swap ? lo : hi;
+        };
+        auto done = [&](uint64_t* bar) {
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar);
+        };
+        if (T > 0) {
+          look_up(0);
+#pragma unroll
+          for (int i = 0; i < N; ++i) load(i, 0, kb, pg);
+        }
+        for (int t = 0; t < T && ok; ++t) {
+          const int pages = pg;
+          const float ks_t = ks, vs_t = vs;
+          look_up(t + 1);
+          uint8_t* tile = slot(it + 2 * t);
+          if (!ok) break;
+          if (cw == 0) {  // (the entry is free: the ring's is)
+            TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
+            const float k0 = __shfl_sync(0xffffffffu, ks_t, 0), v0 = __shfl_sync(0xffffffffu, vs_t, 0);
+            const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks_t == k0 && vs_t == v0));
+            const float most = warp_max(lane < KT / 16 ? vs_t : 0.f);
+            if (lane < KT / 16) {
+              ts.ks[lane] = ks_t;
+              ts.vs[lane] = vs_t;
+            }
+            if (lane == 0) {
+              ts.most_v = most;
+              ts.mixed = mixed;
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            store(i, tile);
+            load(i, t, vb, pages);
+          }
+          done(&full[(it + 2 * t) % RING]);
+          if (t == 0) {
+            // Q tiles: a row a thread, in place, scaled by a power of two so that its largest element lies in
+            // [2^14, 2^15) (fp16 then holds all of bf16's bits down to 2^-29 of it)
+            for (int x = 0; x < 2 && ok; ++x) {
+              if (w.nt[x] == 0) continue;
+              if (!__all_sync(0xffffffffu, mbar_wait(&q_full[x], q_use[x] & 1u, abort_flag))) {
+                ok = false;
+                break;
+              }
+              uint8_t* row = sQ + x * SLOT + ct * 128;
+              float most = 0.f;
+#pragma unroll 4
+              for (int c = 0; c < D / 8; ++c) {
+                const uint4 u = *reinterpret_cast<const uint4*>(row + c / 8 * (SLOT / NB) + (((c & 7) ^ (ct & 7)) << 4));
+                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float f = fabsf(__uint_as_float(v[e] << 16)), g = fabsf(__uint_as_float(v[e] & 0xffff0000u));
+                  most = fmaxf(most, fmaxf(nonfinite(f) ? 0.f : f, nonfinite(g) ? 0.f : g));
+                }
+              }
+              const int e = most > 0.f ? 14 - ilogbf(most) : 0, e0 = e / 2;
+              const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
+#pragma unroll 4
+              for (int c = 0; c < D / 8; ++c) {
+                uint4* at = reinterpret_cast<uint4*>(row + c / 8 * (SLOT / NB) + (((c & 7) ^ (ct & 7)) << 4));
+                uint4 u = *at;
+                uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const __half2 h = __floats2half2_rn(__uint_as_float(v[e] << 16) * f0 * f1, __uint_as_float(v[e] & 0xffff0000u) * f0 * f1);
+                  v[e] = *reinterpret_cast<const uint32_t*>(&h);
+                }
+                *at = make_uint4(v[0], v[1], v[2], v[3]);
+              }
+              q_exp[((q_use[x] & 1u) * 2 + x) * 128 + ct] = (int16_t)e;
+              ++q_use[x];
+              done(&q_ready[x]);
+            }
+            if (!ok) break;
+          }
+          const int kt = (tile0 + t) * KT;
+          tile = slot(it + 2 * t + 1);
+          if (!ok) break;
+          if (kt < w.clean_lo || kt + min(KT, len - kt) > w.clean_hi) {
+            // keys that a row does not see: 0 x NaN is NaN, such codes become 0 here and are given to the rows
+            // that see them at the stretch's end (only for row tiles that take this product)
+            uint32_t found = 0;
+#pragma unroll
+            for (int i = 0; i < N; ++i) found |= nan_codes(q[i].x) | nan_codes(q[i].y) | nan_codes(q[i].z) | nan_codes(q[i].w);
+            if (__builtin_expect(__any_sync(0xffffffffu, found != 0), 0)) {
+#pragma unroll
+              for (int i = 0; i < N; ++i)
+                q[i] = make_uint4(without_nan(q[i].x), without_nan(q[i].y), without_nan(q[i].z), without_nan(q[i].w));
+              if (lane == 0) atomicOr(&w.bad, (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0));
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            store(i, tile);
+            load(i, t + 1, kb, pg);
+          }
+          done(&full[(it + 2 * t + 1) % RING]);
+        }
+        it += 2 * T;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&w_empty[ws]);
+      }
+      if (!ok) give_up();
+    }
+  } else if (warp == SW + 3) {
     // ---- scheduler
     r.starts = after_wait(r.starts);
     if (r.lens) r.lens = after_wait(r.lens);
@@ -651,7 +1009,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     if (r.table) r.table = after_wait(r.table);
     uint32_t it = 0, q_use[2] = {0, 0};
     bool ok = true;
-    const int page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
+    int page_rows = KT;
+    if constexpr (!KV8) page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
     const int boxes = KT / page_rows;
     // a copy per lane (the box of a page, one of its 128-byte halves), so that a
     // tile goes out in one instruction whatever the page size
@@ -685,6 +1044,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         }
         ++q_use[buf];
       };
+      if constexpr (KV8) {  // (K and V are the converters')
+        for (int x = 0; x < NQ && ok; ++x)
+          if (w.nt[x] > 0) load_q(x, x);
+      } else {
       const int32_t* tab = kv.paged ? r.table + (int64_t)w.b * r.table_stride : nullptr;
       // page of this lane's box of a tile; lanes past the sequence load nothing
       auto page_of = [&](int t) {
@@ -728,6 +1091,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         }
         pg = next;
       }
+      }
     }
     if (!ok || *abort_flag) {
       // let this CTA's own copies land before leaving
@@ -747,7 +1111,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     // is idle time, a commit 75 to 150 cycles of it (measured).  NQ = 2, which is
     // bound by this pipe, commits once per S: the softmax warps, who see it,
     // give the K/V and Q tiles back that were read in front of it.
-    constexpr uint32_t idS = idesc_bf16(128, KT), idPV = idesc_bf16(128, D) | kIdescBMnMajor;
+    constexpr uint32_t idS = KV8 ? idesc_f16(128, KT) : idesc_bf16(128, KT);
+    constexpr uint32_t idPV = (KV8 ? idesc_f16(128, D) : idesc_bf16(128, D)) | kIdescBMnMajor;
     uint32_t it = 0, fixpar = 0;
     uint32_t q_cnt0 = 0, q_cnt1 = 0;    // Q tiles used (NQ = 1: one count, the buffers alternate)
     uint32_t pv_cnt0 = 0, pv_cnt1 = 0;  // products P V of each stream
@@ -803,7 +1168,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     auto wait_v = [&](const Span& w, int t, uint32_t i) {
       if (!ring_full(i)) return;
       const int kt = (w.t0 + t) * KT;
-      if (kt < w.clean_lo || kt + KT > w.clean_hi) {  // the fixer looks at it first
+      if (!KV8 && (kt < w.clean_lo || kt + KT > w.clean_hi)) {  // the fixer looks at it first
         wait(&v_fix[i % RING], (fixpar >> (i % RING)) & 1u);
         fixpar ^= 1u << (i % RING);
       }
@@ -820,7 +1185,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
         ++q_cnt0;
         ++s_cnt;
       } else {
-        if (!wait(&q_full[x], x ? q_cnt1 : q_cnt0) || !ring_full(ring)) return;
+        if (!wait(KV8 ? &q_ready[x] : &q_full[x], x ? q_cnt1 : q_cnt0) || !ring_full(ring)) return;
         issue_s(x, ring % RING, x);
         if (x) ++q_cnt1;
         else ++q_cnt0;
@@ -884,7 +1249,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
     const uint64_t t0 = globaltimer_ns();
     while (!mbar_try_wait(all_done, 0) && globaltimer_ns() - t0 < kWaitLimitNs) {
     }
-  } else if (warp == SW + 2) {
+  } else if (!KV8 && warp == SW + 2) {
     // ---- fixer: V tiles with hidden keys
     uint32_t it = 0;
     bool ok = true;
@@ -986,6 +1351,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
+      float unit = 0.f, row_sl2 = 0.f;  // 8 bits: the unit of V's scales, the row's factor of scores
       auto kt_of = [&](int t) { return (w.t0 + t) * KT; };
       for (int t = 0; t < T; ++t, ++cnt) {
         const int sb = NQ == 2 ? x : (int)(cnt & 1u);
@@ -1011,9 +1377,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
           return ok;
         };
         if (live) {
+          if (KV8 && t == 0) row_sl2 = ldexpf(sl2, -(int)q_exp[((q_cnt & 1u) * 2 + x) * 128 + row]);
           const TileArgs ta{tmem + lrow + sb * 128, tO, hi - kt_of(t), lo - kt_of(t), hi_min < kt_of(t) + KT, lo_max > kt_of(t),
-                            valid, sl2};
-          if constexpr (NQ == 1) ok = softmax_tile_call<D>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
+                            valid, KV8 ? row_sl2 : sl2};
+          if constexpr (KV8) softmax_tile8<D>(ta, tscales[((it >> 1) + t) % C::NSCALES], m, l, unit);
+          else if constexpr (NQ == 1) ok = softmax_tile_call<D>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
           else ok = softmax_tile<D, NQ>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
           if (!ok) break;
           tmem_wait_st();
@@ -1042,7 +1410,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       // of the stores: behind them the arrival, a release, would wait for them.
       const int part = w.part, tok = w.start + i;
       const bool bad = T > 0 && ((*(volatile const int32_t*)&w.bad >> x) & 1);
-      if (__builtin_expect(bad && live, 0)) add_nonfinite<D>(r, kv, w, tO, i, a.window, a.causal);
+      if (__builtin_expect(bad && live, 0)) {
+        if constexpr (KV8) add_nan8<D>(r, kv, w, tO, i, a.window, a.causal);
+        else add_nonfinite<D>(r, kv, w, tO, i, a.window, a.causal);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&w_empty[ws]);
       // Up to 8 rows of a warp (single tokens) each lane stores its own, which is
@@ -1051,7 +1422,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
       const bool staged = NQ == 2 || (live && p.mode != kModeCluster && __popc(rows) > 8);
       if (NQ == 1 && T > 0 && !staged && lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
       if (live) {
-        const float inv = 1.f / l;  // (every row sees its own key: l is 0 only where all scores are -inf)
+        const float o_unit = KV8 ? unit * (1.f / kUnit8) : 1.f;
+        const float inv = o_unit / l;  // (every row sees its own key: l is 0 only where all scores are -inf)
         if (NQ == 1 && p.mode == kModeCluster) {
 #pragma unroll 1
           for (int c = 0; c < D; c += 32) {
@@ -1112,6 +1484,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ>::THREADS, 1)
               for (int c = 0; c < D; c += 32) {
                 float v[32];
                 tmem_ld32(tO + c, v);
+                if (KV8) {
+#pragma unroll
+                  for (int j = 0; j < 32; ++j) v[j] *= o_unit;
+                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) put(j, *reinterpret_cast<const uint4*>(v + 4 * j));
                 flush(c / 4);
@@ -1398,10 +1774,10 @@ int query_clusters(int S) {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaFuncSetAttribute(k_ragged_tc<D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, 1>::SMEM) !=
+  if (cudaFuncSetAttribute(k_ragged_tc<D, 1, false>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, 1>::SMEM) !=
           cudaSuccess ||
-      cudaFuncSetAttribute(k_ragged_tc<D, 1>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
-      cudaOccupancyMaxActiveClusters(&n, k_ragged_tc<D, 1>, &cfg) != cudaSuccess) {
+      cudaFuncSetAttribute(k_ragged_tc<D, 1, false>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+      cudaOccupancyMaxActiveClusters(&n, k_ragged_tc<D, 1, false>, &cfg) != cudaSuccess) {
     cudaGetLastError();
     n = 0;
   }
@@ -1425,12 +1801,12 @@ struct HostPlan {
   int merge;    // parts may have to meet
 };
 
-HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms) {
+HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms, bool kv8 = false) {
   const int G = a.Hq / a.Hkv;
   HostPlan h{};
   Plan& p = h.p;
   p.tpt = std::min(128 / G, std::max(r.max_rows, 1));
-  h.nq = (int64_t)r.max_rows * G <= (int64_t)p.tpt * G ? 1 : 2;
+  h.nq = !kv8 && (int64_t)r.max_rows * G <= (int64_t)p.tpt * G ? 1 : 2;
   p.tok = p.tpt * h.nq;
   p.ws_rows = h.nq == 1 ? p.tpt * G : 256;
   p.max_items = (int)std::min<int64_t>(std::min<int64_t>((int64_t)r.total / p.tok + std::min(r.batch, r.total), r.total),
@@ -1495,35 +1871,47 @@ cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
              : cudaErrorInvalidValue;
 }
 
-template <int D, int NQ>
-cudaError_t launch_tc(const Ragged& r, const AttnCall& a, const KVView& kv, const Plan& p, int sms,
+template <int D, int NQ, bool KV8 = false>
+cudaError_t launch_tc(const Ragged& r, const AttnCall& a,
+                      const typename std::conditional<KV8, Kv8View, KVView>::type& kv, const Plan& p, int sms,
                       const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, cudaStream_t st) {
   static std::atomic<bool> attr[64];
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   if (dev >= 64 || !attr[dev]) {
-    e = cudaFuncSetAttribute(k_ragged_tc<D, NQ>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, NQ>::SMEM);
-    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_ragged_tc<D, NQ>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    e = cudaFuncSetAttribute(k_ragged_tc<D, NQ, KV8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Cfg<D, NQ, KV8>::SMEM);
+    if (e == cudaSuccess) e = cudaFuncSetAttribute(k_ragged_tc<D, NQ, KV8>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
     if (e != cudaSuccess) return e;
     if (dev < 64) attr[dev] = true;
   }
   const int grid = p.mode == kModeCluster ? r.batch * a.Hkv * p.cluster : sms;
-  return launch_kc(k_ragged_tc<D, NQ>, grid, Cfg<D, NQ>::THREADS, Cfg<D, NQ>::SMEM, st, p.cluster, r, a, kv, p, mq, mk,
+  return launch_kc(k_ragged_tc<D, NQ, KV8>, grid, Cfg<D, NQ, KV8>::THREADS, Cfg<D, NQ, KV8>::SMEM, st, p.cluster, r, a, kv, p, mq, mk,
                    mv);
+}
+
+cudaError_t encode_q(CUtensorMap* mq, const Ragged& r, const AttnCall& a, const HostPlan& h) {
+  const cuuint64_t dims[3] = {(cuuint64_t)a.d, (cuuint64_t)a.Hq, (cuuint64_t)r.total};
+  // (the stride of a dimension of one entry is never used, but may not be 0)
+  const cuuint64_t strides[2] = {std::max<cuuint64_t>(a.q_head * 2, 16), (cuuint64_t)a.q_row * 2};
+  const cuuint32_t box[3] = {64, (cuuint32_t)(a.Hq / a.Hkv), (cuuint32_t)h.p.tpt};
+  return encode(mq, a.q, 3, dims, strides, box);
+}
+
+template <int D>
+cudaError_t launch_d8(const Ragged& r, const AttnCall& a, const Kv8View& kv, const HostPlan& h, int sms, cudaStream_t st) {
+  CUtensorMap mq;
+  cudaError_t e = encode_q(&mq, r, a, h);
+  if (e == cudaSuccess) e = launch_tc<D, 2, true>(r, a, kv, h.p, sms, mq, mq, mq, st);
+  if (e != cudaSuccess || !h.merge) return e;
+  return launch_k(k_ragged_merge<D, 4>, dim3(sms - 1, 256 / 32), 256, 0, st, r, a, h.p, sms);
 }
 
 template <int D>
 cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const HostPlan& h, int sms, cudaStream_t st) {
   const int G = a.Hq / a.Hkv;
   CUtensorMap mq, mk, mv;
-  {
-    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a.Hq, (cuuint64_t)r.total};
-    // (the stride of a dimension of one entry is never used, but may not be 0)
-    const cuuint64_t strides[2] = {std::max<cuuint64_t>(a.q_head * 2, 16), (cuuint64_t)a.q_row * 2};
-    const cuuint32_t box[3] = {64, (cuuint32_t)G, (cuuint32_t)h.p.tpt};
-    if (cudaError_t e = encode(&mq, a.q, 3, dims, strides, box)) return e;
-  }
+  if (cudaError_t e = encode_q(&mq, r, a, h)) return e;
   for (int i = 0; i < 2; ++i) {
     const cuuint64_t slot = (cuuint64_t)(i ? kv.v_slot : kv.k_slot) * 2, head = (cuuint64_t)(i ? kv.v_head : kv.k_head) * 2;
     const cuuint64_t dims[4] = {(cuuint64_t)D, kv.paged ? (cuuint64_t)1 << kv.page_shift : (cuuint64_t)kv.packed_rows,
@@ -1544,14 +1932,14 @@ cudaError_t launch_d(const Ragged& r, const AttnCall& a, const KVView& kv, const
 
 }  // namespace
 
-cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes) {
+cudaError_t attn_tc_workspace(const Ragged& r, const AttnCall& a, int64_t* bytes, bool kv8) {
   int sms = 0;
   // without a device (argument checks on a host) the largest part's count of SMs stands in
   if (current_sms(&sms) != cudaSuccess) {
     cudaGetLastError();
     sms = 152;
   }
-  const HostPlan h = make_plan(r, a, sms);
+  const HostPlan h = make_plan(r, a, sms, kv8);
   *bytes = h.merge ? (int64_t)h.p.slots * h.p.ws_rows * (a.d + 2) * 4 : 0;
   return cudaSuccess;
 }
@@ -1561,6 +1949,13 @@ cudaError_t launch_attn_tc(const Ragged& r, const AttnCall& a, const KVView& kv,
   if (cudaError_t e = current_sms(&sms)) return e;
   const HostPlan h = make_plan(r, a, sms);
   return a.d == 64 ? launch_d<64>(r, a, kv, h, sms, st) : launch_d<128>(r, a, kv, h, sms, st);
+}
+
+cudaError_t launch_attn_tc8(const Ragged& r, const AttnCall& a, const Kv8View& kv, cudaStream_t st) {
+  int sms = 0;
+  if (cudaError_t e = current_sms(&sms)) return e;
+  const HostPlan h = make_plan(r, a, sms, true);
+  return a.d == 64 ? launch_d8<64>(r, a, kv, h, sms, st) : launch_d8<128>(r, a, kv, h, sms, st);
 }
 
 }  // namespace dfl
