@@ -108,14 +108,15 @@ struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
   // 128 bytes of 32 rows for each softmax warp (NQ = 1: in the Q tile it has done with)
   static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;
-  static constexpr int RING = (7 * 32768 - STAGE) / SLOT - 2;  // K/V tiles in flight
-  static constexpr int DATA = (RING + 2) * SLOT + STAGE;  // 224 KB
+  static constexpr int CODES = KV8 ? 2 * KT * D : 0;      // a K and a V tile on their way to the converters
+  static constexpr int RING = (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
+  static constexpr int DATA = (RING + 2) * SLOT + STAGE + CODES;  // 224 KB
   static constexpr int THREADS = (4 * NQ + (KV8 ? 8 : 4)) * 32;
   // NQ = 2: registers of the softmax warps and of the other four; the launch's
   // 168 for all spilled 100 bytes in the key loop (452 -> 424 us for the packed
   // prompts of 1 to 8192 tokens).  8 x 200 + 4 x 104 = 12 x 168.
-  // With converters: 8 x 184 + 4 x 56 + 4 x 88 = 16 x 128.
-  static constexpr int R_SOFTMAX = KV8 ? 184 : 200, R_REST = KV8 ? 56 : 104, R_CONVERT = 88;
+  // With converters: 8 x 184 + 4 x 80 + 4 x 64 = 16 x 128.
+  static constexpr int R_SOFTMAX = KV8 ? 184 : 200, R_REST = KV8 ? 80 : 104, R_CONVERT = 64;
   static constexpr int EXTRA = 768;  // barriers and descriptors
   // scales of as many tiles as the ring holds, the one that is being read and the next
   static constexpr int NSCALES = 8;
@@ -531,30 +532,40 @@ __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScale
   const uint64_t c2 = f2pack(c1, c1);
   uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
   const float to_unit = unit > 0.f ? kUnit8 / unit : 0.f;
-  auto probs = [&](int c) {  // 32 keys
+  // (both forms whole: a branch at each pair took three times the time of its arithmetic)
+  auto probs = [&](auto weighted, int c) {  // 32 keys
     uint32_t pk[16];
 #pragma unroll
-    for (int j = 0; j < 16; ++j) {
-      uint64_t e2;
-      asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
-      const float2 e = f2unpack(e2);
-      uint64_t p2 = f2pack(ex2(e.x), ex2(e.y));
-      if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(p2));
-      else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(p2));
-      if (weigh) {
-        const float w = ts.vs[(c + 2 * j) / 16] * to_unit;
-        p2 = mul2(p2, f2pack(w, w));
+    for (int g = 0; g < 2; ++g) {
+      float w = 1.f;
+      if constexpr (decltype(weighted)::value) w = ts.vs[c / 16 + g] * to_unit;
+#pragma unroll
+      for (int j = 8 * g; j < 8 * g + 8; ++j) {
+        uint64_t e2;
+        asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
+        const float2 e = f2unpack(e2);
+        uint64_t p2 = f2pack(ex2(e.x), ex2(e.y));
+        if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(p2));
+        else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(p2));
+        if constexpr (decltype(weighted)::value) p2 = mul2(p2, f2pack(w, w));
+        const float2 p = f2unpack(p2);
+        const __half2 h2 = __floats2half2_rn(p.x, p.y);
+        pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      const float2 p = f2unpack(p2);
-      const __half2 h2 = __floats2half2_rn(p.x, p.y);
-      pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
     }
     tmem_st16u(a.tS + c / 2, pk);
   };
-  probs(0);
-  probs(32);
-  probs(64);
-  probs(96);
+  if (weigh) {
+    probs(std::true_type(), 0);
+    probs(std::true_type(), 32);
+    probs(std::true_type(), 64);
+    probs(std::true_type(), 96);
+  } else {
+    probs(std::false_type(), 0);
+    probs(std::false_type(), 32);
+    probs(std::false_type(), 64);
+    probs(std::false_type(), 96);
+  }
   const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
   const float sum = (s0.x + s0.y) + (s1.x + s1.y);
   l += weigh ? sum : sum * (1.f / kUnit8);
@@ -623,7 +634,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   uint8_t* sQ = smem;
   uint8_t* sR = sQ + 2 * SLOT;
   uint8_t* sS = sR + RING * SLOT;
-  uint64_t* full = (uint64_t*)(sS + C::STAGE);
+  uint64_t* full = (uint64_t*)(sS + C::STAGE + C::CODES);
   uint64_t* empty = full + RING;
   uint64_t* v_fix = empty + RING;
   uint64_t* q_full = v_fix + RING;
@@ -639,7 +650,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   Work* works = (Work*)(tmem_slot + 2);
   // 8 bits: scales of the last tiles, the rows' exponents of Q [stretch & 1][tile][row], and (in
   // place of what the fixer signals) Q as fp16
-  TileScales* tscales = (TileScales*)(sS + C::STAGE + C::EXTRA);
+  uint8_t* sC = sS + C::STAGE;
+  TileScales* tscales = (TileScales*)(sC + C::CODES + C::EXTRA);
   int16_t* q_exp = (int16_t*)(tscales + C::NSCALES);
   uint64_t* q_ready = v_fix;
   static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
@@ -696,7 +708,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   if (KV8 && warp >= SW + 4) {
     if constexpr (KV8) {
       // ---- converters: codes from memory, as fp16 into the ring.  A thread has 16 codes of each of N keys of
-      // a tile; as one is stored, the same piece of the next tile is asked for.
+      // a tile, which it copies to a place of its own (so that no one waits for anyone) a tile ahead of time:
+      // as a piece of K is stored, that of the next K tile is asked for, and so for V.
       constexpr int PIECES = D / 16, KEYS = 128 / PIECES, N = KT / KEYS;
       const int ct = tid & 127, cw = ct >> 5, piece = ct % PIECES, key = ct / PIECES;
       r.table = after_wait(r.table);
@@ -722,16 +735,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         const uint8_t* vb = kv.v + (int64_t)w.kvh * kv.head + piece * 16;
         const int64_t s_at = w.kvh * kv.s_head;
         const int tile0 = w.t0;
-        // the page and scales of 16 keys of a tile, a lane each (lanes 0 .. 7)
+        // the page and scales of 16 keys of a tile, a lane each (lanes 0 .. 7).  Their loads depend on one
+        // another and would hold the warp up, so the table is read two tiles ahead and the scales one.
+        auto entry_of = [&](int t) {
+          const int first = (tile0 + t) * KT + 16 * lane;
+          return lane < KT / 16 && t < T && first < len ? tab[first >> kv.page_shift] : -1;
+        };
         int pg = -1;
         float ks = 1.f, vs = 0.f;
-        auto look_up = [&](int t) {
-          pg = -1;
+        auto look_up = [&](int t, int entry) {
+          pg = entry;
           ks = 1.f;
           vs = 0.f;
           const int first = (tile0 + t) * KT + 16 * lane;
           if (lane < KT / 16 && t < T && first < len) {
-            pg = tab[first >> kv.page_shift];
             if (pg < 0 || pg >= kv.n_pages) {
               // (a page that the window of every row has left behind may be gone)
               flag_status(((first >> kv.page_shift) + 1) << kv.page_shift > lo_out ? r.status : nullptr, DFLASH_STATUS_PAGE);
@@ -742,21 +759,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
             }
           }
         };
-        uint4 q[N];
-        auto load = [&](int i, int t, const uint8_t* base, int pages) {
+        // this thread's piece i of the K (v: V) tile that is on its way
+        auto mine = [&](int i, int v) { return sC + v * (KT * D) + (i * 128 + ct) * 16; };
+        auto load = [&](int i, int v, int t, const uint8_t* base, int pages) {
           const int j = key + KEYS * i, pos = (tile0 + t) * KT + j;
           const int page = __shfl_sync(0xffffffffu, pages, j / 16);
-          q[i] = make_uint4(0, 0, 0, 0);
-          if (t < T && page >= 0 && pos < len)
-            q[i] = *reinterpret_cast<const uint4*>(base + page * kv.page + (int64_t)(pos & ((1 << kv.page_shift) - 1)) * kv.slot);
+          const bool there = t < T && page >= 0 && pos < len;  // (else zeros)
+          const uint8_t* src = base + (there ? page * kv.page + (int64_t)(pos & ((1 << kv.page_shift) - 1)) * kv.slot : 0);
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(mine(i, v))), "l"(src), "r"(there ? 16 : 0) : "memory");
         };
         auto slot = [&](uint32_t i) {  // the ring's entry i, free
           if (i >= (uint32_t)RING && !__all_sync(0xffffffffu, mbar_wait(&empty[i % RING], (i / RING - 1) & 1u, abort_flag))) ok = false;
           return sR + (i % RING) * SLOT;
         };
-        auto store = [&](int i, uint8_t* tile) {
+        auto store = [&](const uint4& q, int i, uint8_t* tile) {
           uint4 lo, hi;
-          codes_to_h16(q[i], lo, hi);
+          codes_to_h16(q, lo, hi);
           uint8_t* row = tile + (key + KEYS * i) * 128;
           *reinterpret_cast<uint4*>(row + at0) = swap ? hi : lo;
           *reinterpret_cast<uint4*>(row + at1) = swap ? lo : hi;
@@ -766,15 +784,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(bar);
         };
+        int ahead = -1;
         if (T > 0) {
-          look_up(0);
+          const int first = entry_of(0);
+          ahead = entry_of(1);
+          look_up(0, first);
 #pragma unroll
-          for (int i = 0; i < N; ++i) load(i, 0, kb, pg);
+          for (int i = 0; i < N; ++i) load(i, 0, 0, kb, pg);
+          asm volatile("cp.async.commit_group;" ::: "memory");
+#pragma unroll
+          for (int i = 0; i < N; ++i) load(i, 1, 0, vb, pg);
+          asm volatile("cp.async.commit_group;" ::: "memory");
         }
         for (int t = 0; t < T && ok; ++t) {
-          const int pages = pg;
           const float ks_t = ks, vs_t = vs;
-          look_up(t + 1);
+          look_up(t + 1, ahead);
+          ahead = entry_of(t + 2);
           uint8_t* tile = slot(it + 2 * t);
           if (!ok) break;
           if (cw == 0) {  // (the entry is free: the ring's is)
@@ -791,11 +816,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
               ts.mixed = mixed;
             }
           }
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            store(i, tile);
-            load(i, t, vb, pages);
+            store(*reinterpret_cast<const uint4*>(mine(i, 0)), i, tile);
+            load(i, 0, t + 1, kb, pg);
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
           done(&full[(it + 2 * t) % RING]);
           if (t == 0) {
             // Q tiles: a row a thread, in place, scaled by a power of two so that its largest element lies in
@@ -841,30 +868,30 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           const int kt = (tile0 + t) * KT;
           tile = slot(it + 2 * t + 1);
           if (!ok) break;
-          if (kt < w.clean_lo || kt + min(KT, len - kt) > w.clean_hi) {
-            // keys that a row does not see: 0 x NaN is NaN, such codes become 0 here and are given to the rows
-            // that see them at the stretch's end (only for row tiles that take this product)
-            uint32_t found = 0;
-#pragma unroll
-            for (int i = 0; i < N; ++i) found |= nan_codes(q[i].x) | nan_codes(q[i].y) | nan_codes(q[i].z) | nan_codes(q[i].w);
-            if (__builtin_expect(__any_sync(0xffffffffu, found != 0), 0)) {
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                q[i] = make_uint4(without_nan(q[i].x), without_nan(q[i].y), without_nan(q[i].z), without_nan(q[i].w));
-              if (lane == 0) atomicOr(&w.bad, (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0));
-            }
-          }
+          // keys that a row does not see: 0 x NaN is NaN, such codes become 0 here and are given to the rows
+          // that see them at the stretch's end (only for row tiles that take this product)
+          const bool edge = kt < w.clean_lo || kt + min(KT, len - kt) > w.clean_hi;
+          asm volatile("cp.async.wait_group 1;" ::: "memory");
 #pragma unroll
           for (int i = 0; i < N; ++i) {
-            store(i, tile);
-            load(i, t + 1, kb, pg);
+            uint4 q = *reinterpret_cast<const uint4*>(mine(i, 1));
+            if (edge) {
+              if (nan_codes(q.x) | nan_codes(q.y) | nan_codes(q.z) | nan_codes(q.w)) {
+                q = make_uint4(without_nan(q.x), without_nan(q.y), without_nan(q.z), without_nan(q.w));
+                atomicOr(&w.bad, (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0));
+              }
+            }
+            store(q, i, tile);
+            load(i, 1, t + 1, vb, pg);
           }
+          asm volatile("cp.async.commit_group;" ::: "memory");
           done(&full[(it + 2 * t + 1) % RING]);
         }
         it += 2 * T;
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_empty[ws]);
       }
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (!ok) give_up();
     }
   } else if (warp == SW + 3) {
