@@ -111,16 +111,15 @@ struct Cfg {
   static constexpr int CODES = KV8 ? 2 * KT * D : 0;      // a K and a V tile on their way to the converters
   static constexpr int RING = (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
   static constexpr int DATA = (RING + 2) * SLOT + STAGE + CODES;  // 224 KB
-  static constexpr int THREADS = (4 * NQ + (KV8 ? 8 : 4)) * 32;
+  static constexpr int THREADS = (4 * NQ + 4) * 32;
   // NQ = 2: registers of the softmax warps and of the other four; the launch's
   // 168 for all spilled 100 bytes in the key loop (452 -> 424 us for the packed
   // prompts of 1 to 8192 tokens).  8 x 200 + 4 x 104 = 12 x 168.
-  // With converters: 8 x 184 + 4 x 80 + 4 x 64 = 16 x 128.
-  static constexpr int R_SOFTMAX = KV8 ? 184 : 200, R_REST = KV8 ? 80 : 104, R_CONVERT = 64;
+  static constexpr int R_SOFTMAX = 200, R_REST = 104;
   static constexpr int EXTRA = 768;  // barriers and descriptors
   // scales of as many tiles as the ring holds, the one that is being read and the next
   static constexpr int NSCALES = 8;
-  static constexpr size_t SMEM = DATA + EXTRA + (KV8 ? NSCALES * sizeof(TileScales) + 2 * 2 * 128 * 2 : 0);
+  static constexpr size_t SMEM = DATA + EXTRA + (KV8 ? NSCALES * sizeof(TileScales) + 4 * 8 : 0);
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -465,7 +464,7 @@ template <int D>
 __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScales& ts, float& m, float& l, float& unit) {
   float s[128];
   fence_after();
-  tmem_ld128_halves(a.tS, s);
+  tmem_ld128(a.tS, s);
   const bool mixed = ts.mixed != 0;
   float k = a.sl2;
   if (mixed) {
@@ -622,6 +621,41 @@ __device__ __forceinline__ void codes_to_h16(const uint4& c, uint4& lo, uint4& h
                   e4m3x2_to_h2((uint16_t)(c.w >> 16)));
 }
 
+// A row of a Q tile (128 bytes of it in each of D / 64 blocks `block` bytes apart, its 16-byte chunks
+// swizzled by row mod 8), bf16 to fp16 in place, times 2^e so that its largest finite element lies in
+// [2^14, 2^15): fp16 then holds all of bf16's bits down to 2^-29 of that.  Returns e.
+template <int D>
+__device__ __forceinline__ int q_to_h16(uint8_t* row, int block, int swizzle) {
+  auto chunk = [&](int c) { return reinterpret_cast<uint4*>(row + c / 8 * block + (((c & 7) ^ swizzle) << 4)); };
+  uint32_t most2 = 0;  // largest magnitudes: finite bf16 order as integers do
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    const uint4 u = *chunk(c);
+    const uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a = v[k] & 0x7fff7fffu;
+      most2 = __vmaxu2(most2, a & ~((nonfinite_bits(a) >> 15) * 0xffffu));
+    }
+  }
+  const uint32_t most = max(most2 & 0xffffu, most2 >> 16);
+  const int e = most ? 14 - ilogbf(__uint_as_float(most << 16)) : 0, e0 = e / 2;
+  const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);  // two factors, either of them a normal number
+#pragma unroll 4
+  for (int c = 0; c < D / 8; ++c) {
+    uint4* at = chunk(c);
+    const uint4 u = *at;
+    uint32_t v[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __half2 h = __floats2half2_rn(__uint_as_float(v[k] << 16) * f0 * f1, __uint_as_float(v[k] & 0xffff0000u) * f0 * f1);
+      v[k] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    *at = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  return e;
+}
+
 template <int D, int NQ, bool KV8>
 __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     k_ragged_tc(Ragged r, AttnCall a, typename std::conditional<KV8, Kv8View, KVView>::type kv, Plan p, const __grid_constant__ CUtensorMap mq,
@@ -648,11 +682,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(all_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Work* works = (Work*)(tmem_slot + 2);
-  // 8 bits: scales of the last tiles, the rows' exponents of Q [stretch & 1][tile][row], and (in
-  // place of what the fixer signals) Q as fp16
+  // 8 bits: scales of the last tiles, the K and the V tile of codes, and (in place of what the fixer
+  // signals) Q as fp16
   uint8_t* sC = sS + C::STAGE;
   TileScales* tscales = (TileScales*)(sC + C::CODES + C::EXTRA);
-  int16_t* q_exp = (int16_t*)(tscales + C::NSCALES);
+  uint64_t* c_full = (uint64_t*)(tscales + C::NSCALES);
+  uint64_t* c_empty = c_full + 2;
   uint64_t* q_ready = v_fix;
   static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -660,7 +695,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
 
   if (tid == 0) {
     for (int s = 0; s < RING; ++s) {
-      mbar_init(&full[s], KV8 ? 4 : 1);
+      mbar_init(&full[s], KV8 ? 2 : 1);
       mbar_init(&empty[s], KV8 ? 1 : 2);  // the MMAs (seen by a softmax warp, or a commit) and the fixer
       mbar_init(&v_fix[s], KV8 ? 4 : 1);
     }
@@ -670,10 +705,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
+      if (KV8) {
+        mbar_init(&c_full[s], 1);
+        mbar_init(&c_empty[s], 2);
+      }
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(&w_full[s], 1);
-      mbar_init(&w_empty[s], KV8 ? SW + 6 : SW + 3);  // all warps but the scheduler (8 bits: nor the fixer)
+      mbar_init(&w_empty[s], SW + 3);  // all warps but the scheduler
     }
     mbar_init(all_done, 1);
     *abort_flag = 0;
@@ -699,21 +738,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   };
 
   if (warp >= SW) {
-  if constexpr (KV8) {
-    if (warp >= SW + 4) regs_dec<C::R_CONVERT>();
-    else regs_dec<C::R_REST>();
-  } else if constexpr (NQ == 2) {
-    regs_dec<C::R_REST>();
-  }
-  if (KV8 && warp >= SW + 4) {
+  if constexpr (NQ == 2) regs_dec<C::R_REST>();
+  if (KV8 && (warp == SW || warp == SW + 2)) {
     if constexpr (KV8) {
-      // ---- converters: codes from memory, as fp16 into the ring.  A thread has 16 codes of each of N keys of
-      // a tile, which it copies to a place of its own (so that no one waits for anyone) a tile ahead of time:
-      // as a piece of K is stored, that of the next K tile is asked for, and so for V.
-      constexpr int PIECES = D / 16, KEYS = 128 / PIECES, N = KT / KEYS;
-      const int ct = tid & 127, cw = ct >> 5, piece = ct % PIECES, key = ct / PIECES;
+      // ---- converters: tiles of codes, which come by TMA, as fp16 into the ring.  A thread has 16 codes
+      // of each of N keys.
+      constexpr int PIECES = D / 16, KEYS = 64 / PIECES, N = KT / KEYS, H = 8;  // H pieces at a time
+      const int cw = warp == SW ? 0 : 1, ct = cw * 32 + lane, piece = ct % PIECES, key = ct / PIECES;
       r.table = after_wait(r.table);
-      uint32_t it = 0, q_use[2] = {0, 0};
+      uint32_t it = 0, c_use = 0;
       bool ok = true;
       // where the piece's two 16-byte chunks lie in a tile, less the key's row (keys of a thread agree mod 8).
       // D = 128: lanes of the second block store their chunks in turn, so that no two of a phase meet in a bank.
@@ -731,175 +764,167 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         if (w.done) break;
         const int len = w.len, lo_out = vis_lo(w.len - w.n + w.i0, a.window);
         const int32_t* tab = r.table + (int64_t)w.b * r.table_stride;
-        const uint8_t* kb = kv.k + (int64_t)w.kvh * kv.head + piece * 16;
-        const uint8_t* vb = kv.v + (int64_t)w.kvh * kv.head + piece * 16;
         const int64_t s_at = w.kvh * kv.s_head;
         const int tile0 = w.t0;
-        // the page and scales of 16 keys of a tile, a lane each (lanes 0 .. 7).  Their loads depend on one
+        // the scales of 16 keys of a tile, a lane each (lanes 0 .. 7).  Their loads depend on one
         // another and would hold the warp up, so the table is read two tiles ahead and the scales one.
         auto entry_of = [&](int t) {
           const int first = (tile0 + t) * KT + 16 * lane;
           return lane < KT / 16 && t < T && first < len ? tab[first >> kv.page_shift] : -1;
         };
-        int pg = -1;
         float ks = 1.f, vs = 0.f;
         auto look_up = [&](int t, int entry) {
-          pg = entry;
           ks = 1.f;
           vs = 0.f;
           const int first = (tile0 + t) * KT + 16 * lane;
           if (lane < KT / 16 && t < T && first < len) {
-            if (pg < 0 || pg >= kv.n_pages) {
-              // (a page that the window of every row has left behind may be gone)
-              flag_status(((first >> kv.page_shift) + 1) << kv.page_shift > lo_out ? r.status : nullptr, DFLASH_STATUS_PAGE);
-              pg = -1;
-            } else if (first + 16 > lo_out) {
-              ks = kv.ks[pg * kv.s_page + s_at];
-              vs = kv.vs[pg * kv.s_page + s_at];
+            if (entry >= 0 && entry < kv.n_pages && first + 16 > lo_out) {
+              ks = kv.ks[entry * kv.s_page + s_at];
+              vs = kv.vs[entry * kv.s_page + s_at];
             }
           }
-        };
-        // this thread's piece i of the K (v: V) tile that is on its way
-        auto mine = [&](int i, int v) { return sC + v * (KT * D) + (i * 128 + ct) * 16; };
-        auto load = [&](int i, int v, int t, const uint8_t* base, int pages) {
-          const int j = key + KEYS * i, pos = (tile0 + t) * KT + j;
-          const int page = __shfl_sync(0xffffffffu, pages, j / 16);
-          const bool there = t < T && page >= 0 && pos < len;  // (else zeros)
-          const uint8_t* src = base + (there ? page * kv.page + (int64_t)(pos & ((1 << kv.page_shift) - 1)) * kv.slot : 0);
-          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(mine(i, v))), "l"(src), "r"(there ? 16 : 0) : "memory");
-        };
-        auto slot = [&](uint32_t i) {  // the ring's entry i, free
-          if (i >= (uint32_t)RING && !__all_sync(0xffffffffu, mbar_wait(&empty[i % RING], (i / RING - 1) & 1u, abort_flag))) ok = false;
-          return sR + (i % RING) * SLOT;
-        };
-        auto store = [&](const uint4& q, int i, uint8_t* tile) {
-          uint4 lo, hi;
-          codes_to_h16(q, lo, hi);
-          uint8_t* row = tile + (key + KEYS * i) * 128;
-          *reinterpret_cast<uint4*>(row + at0) = swap ? hi : lo;
-          *reinterpret_cast<uint4*>(row + at1) = swap ? lo : hi;
-        };
-        auto done = [&](uint64_t* bar) {
-          fence_proxy_async();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(bar);
         };
         int ahead = -1;
         if (T > 0) {
           const int first = entry_of(0);
           ahead = entry_of(1);
           look_up(0, first);
-#pragma unroll
-          for (int i = 0; i < N; ++i) load(i, 0, 0, kb, pg);
-          asm volatile("cp.async.commit_group;" ::: "memory");
-#pragma unroll
-          for (int i = 0; i < N; ++i) load(i, 1, 0, vb, pg);
-          asm volatile("cp.async.commit_group;" ::: "memory");
         }
-        for (int t = 0; t < T && ok; ++t) {
-          const float ks_t = ks, vs_t = vs;
-          look_up(t + 1, ahead);
-          ahead = entry_of(t + 2);
-          uint8_t* tile = slot(it + 2 * t);
-          if (!ok) break;
-          if (cw == 0) {  // (the entry is free: the ring's is)
-            TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
-            const float k0 = __shfl_sync(0xffffffffu, ks_t, 0), v0 = __shfl_sync(0xffffffffu, vs_t, 0);
-            const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks_t == k0 && vs_t == v0));
-            const float most = warp_max(lane < KT / 16 ? vs_t : 0.f);
-            if (lane < KT / 16) {
-              ts.ks[lane] = ks_t;
-              ts.vs[lane] = vs_t;
-            }
-            if (lane == 0) {
-              ts.most_v = most;
-              ts.mixed = mixed;
-            }
+        // K and V tiles in turn by the same few instructions (unrolled over both they were fetched anew each time)
+#pragma unroll 1
+        for (int u = 0; u < 2 * T; ++u) {
+          const int t = u >> 1, v = u & 1, kt = (tile0 + t) * KT;
+          const uint32_t e = it + u;
+          // the ring's entry is free, and the codes are there
+          if ((e >= (uint32_t)RING && !__all_sync(0xffffffffu, mbar_wait(&empty[e % RING], (e / RING - 1) & 1u, abort_flag))) ||
+              !__all_sync(0xffffffffu, mbar_wait(&c_full[v], c_use & 1u, abort_flag))) {
+            ok = false;
+            break;
           }
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
-#pragma unroll
-          for (int i = 0; i < N; ++i) {
-            store(*reinterpret_cast<const uint4*>(mine(i, 0)), i, tile);
-            load(i, 0, t + 1, kb, pg);
-          }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          done(&full[(it + 2 * t) % RING]);
-          if (t == 0) {
-            // Q tiles: a row a thread, in place, scaled by a power of two so that its largest element lies in
-            // [2^14, 2^15) (fp16 then holds all of bf16's bits down to 2^-29 of it)
-            for (int x = 0; x < 2 && ok; ++x) {
-              if (w.nt[x] == 0) continue;
-              if (!__all_sync(0xffffffffu, mbar_wait(&q_full[x], q_use[x] & 1u, abort_flag))) {
-                ok = false;
-                break;
+          uint8_t* tile = sR + (e % RING) * SLOT;
+          if (v == 0) {
+            if (cw == 0) {
+              TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
+              const float k0 = __shfl_sync(0xffffffffu, ks, 0), v0 = __shfl_sync(0xffffffffu, vs, 0);
+              const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks == k0 && vs == v0));
+              const float most = warp_max(lane < KT / 16 ? vs : 0.f);
+              if (lane < KT / 16) {
+                ts.ks[lane] = ks;
+                ts.vs[lane] = vs;
               }
-              uint8_t* row = sQ + x * SLOT + ct * 128;
-              float most = 0.f;
-#pragma unroll 4
-              for (int c = 0; c < D / 8; ++c) {
-                const uint4 u = *reinterpret_cast<const uint4*>(row + c / 8 * (SLOT / NB) + (((c & 7) ^ (ct & 7)) << 4));
-                const uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float f = fabsf(__uint_as_float(v[e] << 16)), g = fabsf(__uint_as_float(v[e] & 0xffff0000u));
-                  most = fmaxf(most, fmaxf(nonfinite(f) ? 0.f : f, nonfinite(g) ? 0.f : g));
-                }
+              if (lane == 0) {
+                ts.most_v = most;
+                ts.mixed = mixed;
               }
-              const int e = most > 0.f ? 14 - ilogbf(most) : 0, e0 = e / 2;
-              const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
-#pragma unroll 4
-              for (int c = 0; c < D / 8; ++c) {
-                uint4* at = reinterpret_cast<uint4*>(row + c / 8 * (SLOT / NB) + (((c & 7) ^ (ct & 7)) << 4));
-                uint4 u = *at;
-                uint32_t v[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const __half2 h = __floats2half2_rn(__uint_as_float(v[e] << 16) * f0 * f1, __uint_as_float(v[e] & 0xffff0000u) * f0 * f1);
-                  v[e] = *reinterpret_cast<const uint32_t*>(&h);
-                }
-                *at = make_uint4(v[0], v[1], v[2], v[3]);
-              }
-              q_exp[((q_use[x] & 1u) * 2 + x) * 128 + ct] = (int16_t)e;
-              ++q_use[x];
-              done(&q_ready[x]);
+              look_up(t + 1, ahead);
+              ahead = entry_of(t + 2);
             }
-            if (!ok) break;
+          } else {
+            ++c_use;
           }
-          const int kt = (tile0 + t) * KT;
-          tile = slot(it + 2 * t + 1);
-          if (!ok) break;
-          // keys that a row does not see: 0 x NaN is NaN, such codes become 0 here and are given to the rows
-          // that see them at the stretch's end (only for row tiles that take this product)
-          const bool edge = kt < w.clean_lo || kt + min(KT, len - kt) > w.clean_hi;
-          asm volatile("cp.async.wait_group 1;" ::: "memory");
+          // keys that a row does not see (slots behind the sequence hold anything): 0 x NaN is NaN, such codes of V
+          // become 0 here and are given to the rows that see them at the stretch's end (only for row tiles
+          // that take this product)
+          const bool edge = v && (kt < w.clean_lo || kt + KT > w.clean_hi);
+#pragma unroll 1
+          for (int i0 = 0; i0 < N; i0 += H) {
+            uint4 q[H];
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            uint4 q = *reinterpret_cast<const uint4*>(mine(i, 1));
+            for (int i = 0; i < H; ++i) q[i] = *reinterpret_cast<const uint4*>(sC + v * (KT * D) + ((i0 + i) * 64 + ct) * 16);
             if (edge) {
-              if (nan_codes(q.x) | nan_codes(q.y) | nan_codes(q.z) | nan_codes(q.w)) {
-                q = make_uint4(without_nan(q.x), without_nan(q.y), without_nan(q.z), without_nan(q.w));
+              uint32_t found = 0;
+#pragma unroll
+              for (int i = 0; i < H; ++i) found |= nan_codes(q[i].x) | nan_codes(q[i].y) | nan_codes(q[i].z) | nan_codes(q[i].w);
+              if (found) {
+#pragma unroll
+                for (int i = 0; i < H; ++i)
+                  q[i] = make_uint4(without_nan(q[i].x), without_nan(q[i].y), without_nan(q[i].z), without_nan(q[i].w));
                 atomicOr(&w.bad, (t < w.nt[0] ? 1 : 0) | (t < w.nt[1] ? 2 : 0));
               }
             }
-            store(q, i, tile);
-            load(i, 1, t + 1, vb, pg);
+            uint8_t* rows = tile + (key + KEYS * i0) * 128;
+#pragma unroll
+            for (int i = 0; i < H; ++i) {
+              uint4 lo, hi;
+              codes_to_h16(q[i], lo, hi);
+              *reinterpret_cast<uint4*>(rows + KEYS * 128 * i + at0) = swap ? hi : lo;
+              *reinterpret_cast<uint4*>(rows + KEYS * 128 * i + at1) = swap ? lo : hi;
+            }
           }
-          asm volatile("cp.async.commit_group;" ::: "memory");
-          done(&full[(it + 2 * t + 1) % RING]);
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) {
+            mbar_arrive(&c_empty[v]);
+            mbar_arrive(&full[e % RING]);
+          }
         }
         it += 2 * T;
         __syncwarp();
         if (lane == 0) mbar_arrive(&w_empty[ws]);
       }
-      asm volatile("cp.async.wait_group 0;" ::: "memory");
       if (!ok) give_up();
     }
   } else if (warp == SW + 3) {
     // ---- scheduler
     r.starts = after_wait(r.starts);
     if (r.lens) r.lens = after_wait(r.lens);
+    if (KV8) r.table = after_wait(r.table);
     int k = 0;
     bool ok = true;
+    // 8 bits: this warp asks for the tiles too, Q and then K and V in turn (a copy per lane, the box of a page)
+    uint32_t q_use[2] = {0, 0}, c_use[2] = {0, 0};
+    Work last;
+    auto produce = [&](const Work& w) {
+      if constexpr (KV8) {
+        const int page_rows = min(1 << kv.page_shift, KT), boxes = KT / page_rows, box = lane & (boxes - 1);
+        const bool issuer = lane < boxes;
+        const int32_t* tab = r.table + (int64_t)w.b * r.table_stride;
+        const int T = max(w.nt[0], w.nt[1]), lo_out = vis_lo(w.len - w.n + w.i0, a.window);
+        auto page_of = [&](int t) {
+          const int pos = (w.t0 + t) * KT + box * page_rows;
+          return t < T && issuer && pos < w.len ? tab[pos >> kv.page_shift] : -1;
+        };
+        int pg = page_of(0);
+        for (int t = 0; t < T && ok; ++t) {
+          const int kt = (w.t0 + t) * KT, pos = kt + box * page_rows, next = page_of(t + 1);
+          const bool mine = issuer && pos < w.len;
+          if (mine && (pg < 0 || pg >= kv.n_pages)) {
+            // (a page that the window of every row has left behind may be gone)
+            flag_status(pos + page_rows > lo_out ? r.status : nullptr, DFLASH_STATUS_PAGE);
+            pg = kv.n_pages;  // just outside the map: zeros arrive
+          }
+          const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * D;
+          for (int v = 0; v < 2; ++v) {
+            if (c_use[v] > 0 && !__all_sync(0xffffffffu, mbar_wait(&c_empty[v], (c_use[v] - 1) & 1u, abort_flag))) {
+              ok = false;
+              return;
+            }
+            if (lane == 0) mbar_expect_tx(&c_full[v], bytes);
+            __syncwarp();
+            ++c_use[v];
+            if (mine)
+              tma_load_4d(sC + v * (KT * D) + box * page_rows * D, v ? &mv : &mk, &c_full[v], 0,
+                          kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
+            if (t == 0 && v == 0) {
+              for (int x = 0; x < 2; ++x) {
+                if (w.nt[x] == 0) continue;
+                if (q_use[x] > 0 && !__all_sync(0xffffffffu, mbar_wait(&q_empty[x], (q_use[x] - 1) & 1u, abort_flag))) {
+                  ok = false;
+                  return;
+                }
+                if (lane == 0) {
+                  mbar_expect_tx(&q_full[x], (uint32_t)(G * p.tpt * 128 * NB));
+                  for (int c = 0; c < NB; ++c)
+                    tma_load_3d(sQ + x * SLOT + c * (SLOT / NB), &mq, &q_full[x], 64 * c, w.kvh * G, w.start + w.i0 + x * p.tpt);
+                }
+                ++q_use[x];
+              }
+            }
+          }
+          pg = next;
+        }
+      }
+    };
     auto emit = [&](const Work& w) {
       const int s = k % NW;
       if (k >= NW && !__all_sync(0xffffffffu, mbar_wait(&w_empty[s], (uint32_t)(k / NW - 1) & 1u, abort_flag))) {
@@ -912,6 +937,11 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       }
       __syncwarp();
       ++k;
+      if constexpr (KV8) {
+        // the tiles of the stretch before: its successor is known by then, nobody waits for the search
+        if (k > 1) produce(last);
+        last = w;
+      }
     };
     const int cta = blockIdx.x, grid = gridDim.x;
     const bool one = r.batch <= 32;  // then each lane keeps its sequence
@@ -1031,13 +1061,23 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     w.done = 1;
     if (ok) emit(w);
     if (!ok) give_up();
-  } else if (warp == SW) {
+    if (KV8 && (!ok || *abort_flag)) {
+      // let this CTA's own copies land before leaving
+      const uint64_t t0 = globaltimer_ns();
+      for (int x = 0; x < 2; ++x) {
+        while (q_use[x] > 0 && !mbar_try_wait(&q_full[x], (q_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+        while (c_use[x] > 0 && !mbar_try_wait(&c_full[x], (c_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
+    }
+  } else if (!KV8 && warp == SW) {
+    if constexpr (!KV8) {
     // ---- TMA producer: Q tiles, then K and V tiles in turn through one ring
     if (r.table) r.table = after_wait(r.table);
     uint32_t it = 0, q_use[2] = {0, 0};
     bool ok = true;
-    int page_rows = KT;
-    if constexpr (!KV8) page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
+    const int page_rows = kv.paged ? min(1 << kv.page_shift, KT) : KT;
     const int boxes = KT / page_rows;
     // a copy per lane (the box of a page, one of its 128-byte halves), so that a
     // tile goes out in one instruction whatever the page size
@@ -1071,10 +1111,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         }
         ++q_use[buf];
       };
-      if constexpr (KV8) {  // (K and V are the converters')
-        for (int x = 0; x < NQ && ok; ++x)
-          if (w.nt[x] > 0) load_q(x, x);
-      } else {
       const int32_t* tab = kv.paged ? r.table + (int64_t)w.b * r.table_stride : nullptr;
       // page of this lane's box of a tile; lanes past the sequence load nothing
       auto page_of = [&](int t) {
@@ -1118,7 +1154,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         }
         pg = next;
       }
-      }
     }
     if (!ok || *abort_flag) {
       // let this CTA's own copies land before leaving
@@ -1130,6 +1165,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       for (int x = 0; x < 2; ++x)
         while (q_use[x] > 0 && !mbar_try_wait(&q_full[x], (q_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
+    }
     }
   } else if (warp == SW + 1) {
     // ---- MMA issuer: the whole warp decides, one elected lane issues.  The
@@ -1379,6 +1415,18 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
       float unit = 0.f, row_sl2 = 0.f;  // 8 bits: the unit of V's scales, the row's factor of scores
+      if constexpr (KV8) {
+        if (T > 0) {
+          if (!__all_sync(0xffffffffu, mbar_wait(&q_full[x], q_cnt & 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          row_sl2 = ldexpf(sl2, -q_to_h16<D>(sQ + x * SLOT + row * 128, SLOT / NB, row & 7));
+          fence_proxy_async();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&q_ready[x]);
+        }
+      }
       auto kt_of = [&](int t) { return (w.t0 + t) * KT; };
       for (int t = 0; t < T; ++t, ++cnt) {
         const int sb = NQ == 2 ? x : (int)(cnt & 1u);
@@ -1404,7 +1452,6 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           return ok;
         };
         if (live) {
-          if (KV8 && t == 0) row_sl2 = ldexpf(sl2, -(int)q_exp[((q_cnt & 1u) * 2 + x) * 128 + row]);
           const TileArgs ta{tmem + lrow + sb * 128, tO, hi - kt_of(t), lo - kt_of(t), hi_min < kt_of(t) + KT, lo_max > kt_of(t),
                             valid, KV8 ? row_sl2 : sl2};
           if constexpr (KV8) softmax_tile8<D>(ta, tscales[((it >> 1) + t) % C::NSCALES], m, l, unit);
@@ -1880,7 +1927,7 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms, bool kv8 = false
 }
 
 cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box) {
+                   const cuuint32_t* box, bool codes = false) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1891,9 +1938,9 @@ cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
   }();
   if (!fn) return cudaErrorNotSupported;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims, strides, box, one,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
+  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
 }
@@ -1927,9 +1974,16 @@ cudaError_t encode_q(CUtensorMap* mq, const Ragged& r, const AttnCall& a, const 
 
 template <int D>
 cudaError_t launch_d8(const Ragged& r, const AttnCall& a, const Kv8View& kv, const HostPlan& h, int sms, cudaStream_t st) {
-  CUtensorMap mq;
+  CUtensorMap mq, m[2];
   cudaError_t e = encode_q(&mq, r, a, h);
-  if (e == cudaSuccess) e = launch_tc<D, 2, true>(r, a, kv, h.p, sms, mq, mq, mq, st);
+  for (int i = 0; i < 2 && e == cudaSuccess; ++i) {
+    const cuuint64_t dims[4] = {(cuuint64_t)D, (cuuint64_t)1 << kv.page_shift, (cuuint64_t)a.Hkv, (cuuint64_t)kv.n_pages};
+    // (the stride of a dimension of one entry is never used, but may not be 0)
+    const cuuint64_t strides[3] = {(cuuint64_t)kv.slot, std::max<cuuint64_t>(kv.head, 16), std::max<cuuint64_t>(kv.page, 16)};
+    const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)std::min(1 << kv.page_shift, KT), 1, 1};
+    e = encode(&m[i], i ? kv.v : kv.k, 4, dims, strides, box, true);
+  }
+  if (e == cudaSuccess) e = launch_tc<D, 2, true>(r, a, kv, h.p, sms, mq, m[0], m[1], st);
   if (e != cudaSuccess || !h.merge) return e;
   return launch_k(k_ragged_merge<D, 4>, dim3(sms - 1, 256 / 32), 256, 0, st, r, a, h.p, sms);
 }
