@@ -20,18 +20,16 @@ struct Kv8View {
   int32_t page_shift, n_pages;
 };
 
-// Two codes (the lower byte first) as fp16: exact, NaN stays NaN.
-__device__ __forceinline__ uint32_t e4m3x2_to_h2(uint16_t c) {
-  uint32_t h;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(c));
-  return h;
-}
-__device__ __forceinline__ float2 e4m3x2_to_f2(uint16_t c) {
-  const uint32_t h = e4m3x2_to_h2(c);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+// Four codes (the lowest byte first) as fp16, two and two: exact, NaN stays NaN.
+__device__ __forceinline__ void e4m3x4_to_h4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(c));
 }
 __device__ __forceinline__ float4 e4m3x4_to_f4(uint32_t c) {
-  const float2 a = e4m3x2_to_f2((uint16_t)c), b = e4m3x2_to_f2((uint16_t)(c >> 16));
+  uint32_t lo, hi;
+  e4m3x4_to_h4(c, lo, hi);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&lo)), b = __half22float2(*reinterpret_cast<const __half2*>(&hi));
   return make_float4(a.x, a.y, b.x, b.y);
 }
 // Nearest codes, ties to even, beyond 448: 448; NaN: 0x7f.  a is the lower byte.

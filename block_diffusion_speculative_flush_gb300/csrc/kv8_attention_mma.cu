@@ -21,10 +21,15 @@
 // smallest normal number 2^-25 of 2^10, that is 2^-35 of what the largest scale and
 // probability give.  m, l, O and merges are fp32.
 //
-// Work: the 16-key chunks of all (sequence, tile of rows, KV head) items one after another, cut
-// into even ranges, one per CTA; the 8 warps of a CTA take its chunks in turn and meet in
-// shared memory, the parts of a cut item in k_kv8_few_merge.  The order of every sum is
-// fixed by the lengths.
+// Work, in one of two ways, by the host's bounds:
+//   ranges   the 16-key chunks of all (sequence, tile of rows, KV head) items one after another, cut
+//            into even ranges, one per CTA; the parts of a cut item meet in k_kv8_few_merge;
+//   cluster  few items of few chunks: a thread-block cluster an item, an even share of its chunks each,
+//            the parts meet in distributed shared memory (one launch, nothing to search).
+// The 8 warps of a CTA take its chunks in turn and meet in shared memory.  The order of every
+// sum is fixed by the lengths.
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <atomic>
 #include <type_traits>
@@ -38,10 +43,14 @@ namespace {
 
 constexpr int kChunk = 16;  // keys of a chunk: never more than a page
 constexpr int kWarps = 8;
+constexpr int kMaxCluster = 8;
+namespace cg = cooperative_groups;
 constexpr float kSlack = 4.f, kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kUnit = 1024.f;  // 2^10, of P in fp16
 
 struct FewPlan {
+  int32_t cluster;    // CTAs of an item; 0: ranges
+  int32_t tiles;      // cluster: tiles of rows that a sequence may have
   int32_t pad;        // what the start of an item costs, in chunks
   int32_t min_units;  // chunks that a CTA gets at least
   int32_t slots;      // partials there is room for
@@ -52,10 +61,15 @@ struct FewCfg {
   static constexpr int RB = 8 * NB;               // rows of a tile
   static constexpr int CTAS = NB <= 2 ? 2 : 1;    // of an SM
   static constexpr int BYTES = kChunk * 2 * D;    // codes of a chunk
-  static constexpr int STAGES = (NB <= 2 ? 3 : 6) * (128 / D);
+  static constexpr int STAGES = (NB <= 2 ? 3 : 5) * (128 / D);
+  static constexpr int SCALES = 16;               // of the chunks on their way
+  static_assert(STAGES + 2 <= SCALES, "an entry for each chunk on its way and the two in use");
   static constexpr int LO = D + 4;                // floats of a row where the warps meet
-  static constexpr int RING = kWarps * STAGES * BYTES, MEET = kWarps * RB * LO * 4;
-  static constexpr size_t SMEM = (RING > MEET ? RING : MEET) + kWarps * STAGES * 8 + kWarps * RB * 8 + RB * 8;
+  static constexpr int RING = kWarps * STAGES * BYTES, MEET = kWarps * RB * LO * 4, PART = RB * D * 4;
+  static constexpr int AREA = RING > MEET + PART ? RING : MEET + PART;
+  static constexpr bool QS = NB > 1;              // q's fragments in shared memory (registers otherwise)
+  static constexpr int QF = QS ? NB * (D / 16) * 32 * 8 : 0;
+  static constexpr size_t SMEM = AREA + QF + NB * 8 * 4 + kWarps * SCALES * 8 + kWarps * RB * 8 + RB * 8;
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -64,6 +78,10 @@ __device__ __forceinline__ float ex2(float x) {
   return y;
 }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
+template <int N> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
+  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
 template <int N> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
   // (size 0: zeros, the address is not looked at)
   const int n = there ? N : 0;
@@ -88,8 +106,6 @@ __device__ __forceinline__ uint32_t pack_h2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
 }
-__device__ __forceinline__ uint32_t lo_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)c); }
-__device__ __forceinline__ uint32_t hi_h2(uint32_t c) { return e4m3x2_to_h2((uint16_t)(c >> 16)); }
 
 // ---------------------------------------------------------------------------
 // the layout of the work
@@ -160,14 +176,18 @@ template <int D, int NB>
 __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ragged r, AttnCall a, Kv8View kv, FewPlan plan) {
   using C = FewCfg<D, NB>;
   constexpr int RB = C::RB, S = C::STAGES, KS = D / 16, MT = D / 16;  // steps of the first product, tiles of the second
-  constexpr int VB = D / 8;                                          // bytes of a lane's piece of a V row
+  constexpr int VB = D / 8, VW = VB / 4;                              // bytes and words of a lane's piece of a V row
+  constexpr int CC = D / 32;                                          // columns of a lane where rows are put together
   extern __shared__ __align__(16) uint8_t smem[];
-  constexpr int AREA = C::RING > C::MEET ? C::RING : C::MEET;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
-  uint8_t* ring = smem + warp * S * C::BYTES;                       // this warp's stages
-  float2* scales = reinterpret_cast<float2*>(smem + AREA) + warp * S;  // (ks, vs) of a stage's page
-  float2* s_ml = reinterpret_cast<float2*>(smem + AREA) + kWarps * S;  // [warps][RB], later [RB] weights' sums
-  float* meet = reinterpret_cast<float*>(smem);                     // [warps][RB][LO]
+  uint8_t* ring = smem + warp * S * C::BYTES;                     // this warp's stages
+  float* meet = reinterpret_cast<float*>(smem);                   // [warps][RB][LO]
+  float* part_o = reinterpret_cast<float*>(smem + C::MEET);       // [RB][D] this CTA's sums (cluster)
+  uint2* s_qf = reinterpret_cast<uint2*>(smem + C::AREA);         // [NB][KS][32]
+  float* s_rowf = reinterpret_cast<float*>(smem + C::AREA + C::QF);  // [RB]
+  float2* scales = reinterpret_cast<float2*>(s_rowf + RB) + warp * C::SCALES;  // (ks, vs) of a chunk's page
+  float2* s_ml = reinterpret_cast<float2*>(s_rowf + RB) + kWarps * C::SCALES;  // [warps][RB]
+  float2* part_ml = s_ml + kWarps * RB;                           // [RB]
   pdl_trigger();
   pdl_wait();
   r.starts = after_wait(r.starts);
@@ -175,7 +195,417 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
   r.table = after_wait(r.table);
   const int G = a.Hq / a.Hkv, cta = blockIdx.x, grid = gridDim.x;
   const float sl2 = a.scale * kLog2e;
-  // every warp lays the work out for itself
+  // One stretch of an item: rows rt RB .. of sequence b, chunks [c0, c0 + take) behind its first.  The rows' sums
+  // end in memory, or (part >= 0) unscaled in a partial, or (part == -2) in this CTA's part_o and part_ml.
+  auto stretch = [&](const Seq& s, int b, int rt, int kvh, int c0, int take, int part) {
+    const int r0 = rt * RB, ctx = s.len - s.n, R = (int)min((int64_t)RB, (int64_t)s.n * G - r0);
+    const int p_first = ctx + r0 / G, p_last = ctx + (r0 + R - 1) / G;
+    const int k_lo = vis_lo(p_first, a.window), k_hi = vis_hi(p_last, s.len, a.causal);
+    const int clean_lo = vis_lo(p_last, a.window), clean_hi = vis_hi(p_first, s.len, a.causal);
+    const int first_key = (few_first(s, a.window) + c0 + warp) * kChunk;  // chunk i of this warp: + 128 i
+    const int n_mine = take > warp ? (take - warp + kWarps - 1) / kWarps : 0;
+    const int32_t* tab = r.table + (int64_t)b * r.table_stride;
+    // pages and scales of this warp's next 32 chunks, one a lane
+    int pg = -1;
+    float ks = 0.f, vs = 0.f;
+    auto look_up = [&](int i0) {
+      const int i = i0 + lane, key = first_key + kWarps * kChunk * i;
+      pg = -1;
+      ks = 1.f;
+      vs = 0.f;
+      if (i < n_mine && key < k_hi && key + kChunk > k_lo) {
+        pg = tab[key >> kv.page_shift];
+        if (pg < 0 || pg >= kv.n_pages) {
+          flag_status(r.status, DFLASH_STATUS_PAGE);
+          pg = -1;
+        } else {
+          ks = kv.ks[pg * kv.s_page + kvh * kv.s_head];
+          vs = kv.vs[pg * kv.s_page + kvh * kv.s_head];
+        }
+      }
+    };
+    // this lane's pieces: of K rows g and g + 8, of V rows 2t, 2t + 1, 2t + 8, 2t + 9
+    const uint8_t* k_base = kv.k + kvh * kv.head + g * kv.slot + 16 * t;
+    const uint8_t* v_base = kv.v + kvh * kv.head + 2 * t * kv.slot + VB * g;
+    const int64_t slot8 = 8 * kv.slot;
+    const uint32_t k_dst = smem_addr(ring) + lane * 16, v_dst = smem_addr(ring) + kChunk * D + lane * VB;
+    int64_t at_v = 0;    // where the chunk whose V is asked for next lies
+    int page_v = -1;
+    // group j: K of chunk j + 1, V of chunk j (what step j uses)
+    auto issue = [&](int j) {
+      if (j >= 0 && j < n_mine) {
+        const uint8_t* p = v_base + at_v;
+        const uint32_t dst = v_dst + (j % S) * C::BYTES;
+        const int key0 = first_key + kWarps * kChunk * j;
+        if (page_v >= 0 && key0 >= k_lo && key0 + kChunk <= k_hi) {
+          cp_async<VB>(dst, p);
+          cp_async<VB>(dst + 32 * VB, p + kv.slot);
+          cp_async<VB>(dst + 64 * VB, p + slot8);
+          cp_async<VB>(dst + 96 * VB, p + slot8 + kv.slot);
+        } else {  // (keys that no row of the tile sees arrive as zeros)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = key0 + 2 * t + (q & 1) + 8 * (q >> 1);
+            cp_async<VB>(dst + q * 32 * VB, p + (q & 1) * kv.slot + (q >> 1) * slot8, page_v >= 0 && key >= k_lo && key < k_hi);
+          }
+        }
+      }
+      const int i = j + 1;
+      if (i < n_mine) {
+        if ((i & 31) == 0) look_up(i);
+        const int page = __shfl_sync(0xffffffffu, pg, i & 31);
+        const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
+        if (lane == 0) scales[i % C::SCALES] = make_float2(k1, v1);
+        const int key0 = first_key + kWarps * kChunk * i;
+        at_v = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot;
+        page_v = page;
+        const uint8_t* p = k_base + at_v;
+        const uint32_t dst = k_dst + (i % S) * C::BYTES;
+        if (page >= 0 && key0 >= k_lo && key0 + kChunk <= k_hi) {
+#pragma unroll
+          for (int c = 0; c < D / 64; ++c) {
+            cp_async<16>(dst + c * 512, p + 64 * c);
+            cp_async<16>(dst + (D / 64 + c) * 512, p + slot8 + 64 * c);
+          }
+        } else {
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c)
+              cp_async<16>(dst + (h * (D / 64) + c) * 512, p + h * slot8 + 64 * c,
+                           page >= 0 && key0 + g + 8 * h >= k_lo && key0 + g + 8 * h < k_hi);
+        }
+      }
+      cp_commit();
+    };
+#pragma unroll 1
+    for (int j = -1; j < S - 1; ++j) issue(j);
+    // ---- q: lane (g, t) has rows g (+ 8 n) at the d's that it has of K
+    uint32_t qf[C::QS ? 1 : NB][KS][2];
+    float rowf[NB][2];  // of rows 2t, 2t + 1: scale 2^-e log2 e
+    auto make_q = [&](int n, uint32_t (*f16)[2]) {
+      const int row = 8 * n + g;
+      uint4 w[D / 32];
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) w[c] = make_uint4(0, 0, 0, 0);
+      if (row < R) {
+        const int i = (r0 + row) / G, h = kvh * G + (r0 + row) % G;
+        const bf16* q = reinterpret_cast<const bf16*>(a.q) + (int64_t)(s.start + i) * a.q_row + (int64_t)h * a.q_head;
+#pragma unroll
+        for (int c = 0; c < D / 64; ++c)
+#pragma unroll
+          for (int k = 0; k < 2; ++k) w[2 * c + k] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t + 8 * k);
+      }
+      const uint32_t* ww = reinterpret_cast<const uint32_t*>(w);
+      float most = 0.f;
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k) {
+        const float x = fabsf(__uint_as_float(ww[k] << 16)), y = fabsf(__uint_as_float(ww[k] & 0xffff0000u));
+        most = fmaxf(most, fmaxf(nonfinite(x) ? 0.f : x, nonfinite(y) ? 0.f : y));
+      }
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+      most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+      // most 2^e in [2^14, 2^15); 2^e in two factors, either of them a normal number
+      const int e = most > 0.f ? 14 - ilogbf(most) : 0, e0 = e / 2;
+      const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
+#pragma unroll
+      for (int k = 0; k < D / 8; ++k)
+        f16[k / 2][k & 1] = pack_h2(__uint_as_float(ww[k] << 16) * f0 * f1, __uint_as_float(ww[k] & 0xffff0000u) * f0 * f1);
+      return ldexpf(sl2, -e);
+    };
+    if constexpr (C::QS) {
+      if (warp < NB) {  // a tile of rows a warp, for all of them
+        uint32_t f16[KS][2];
+        const float f = make_q(warp, f16);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) s_qf[(warp * KS + k) * 32 + lane] = make_uint2(f16[k][0], f16[k][1]);
+        if (t == 0) s_rowf[8 * warp + g] = f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        rowf[n][0] = s_rowf[8 * n + 2 * t];
+        rowf[n][1] = s_rowf[8 * n + 2 * t + 1];
+      }
+    } else {
+      const float f = make_q(0, qf[0]);
+      // rows 2t, 2t + 1 of this tile are those of lanes g = 2t, 2t + 1
+      rowf[0][0] = __shfl_sync(0xffffffffu, f, 8 * t);
+      rowf[0][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
+    }
+    float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f;
+#pragma unroll
+    for (int n = 0; n < NB; ++n) {
+#pragma unroll
+      for (int k = 0; k < MT; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
+      m[n][0] = m[n][1] = -INFINITY;
+      l[n][0] = l[n][1] = 0.f;
+    }
+    float acc[NB][4];  // S^T of the step to come
+    auto scores = [&](int i) {
+      const uint8_t* stage = ring + (i % S) * C::BYTES;
+      float two[2][NB][4];
+#pragma unroll
+      for (int p = 0; p < 2; ++p)
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) two[p][n][j] = 0.f;
+#pragma unroll
+      for (int c = 0; c < D / 64; ++c) {
+        const uint4 k0 = *reinterpret_cast<const uint4*>(stage + c * 512 + lane * 16);
+        const uint4 k8 = *reinterpret_cast<const uint4*>(stage + (D / 64 + c) * 512 + lane * 16);
+        const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w8[4] = {k8.x, k8.y, k8.z, k8.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          uint32_t a0, a1, a2, a3;
+          e4m3x4_to_h4(w0[j], a0, a2);
+          e4m3x4_to_h4(w8[j], a1, a3);
+#pragma unroll
+          for (int n = 0; n < NB; ++n) {
+            if constexpr (C::QS) {
+              const uint2 q = s_qf[(n * KS + 4 * c + j) * 32 + lane];
+              mma(two[j & 1][n], a0, a1, a2, a3, q.x, q.y);
+            } else {
+              mma(two[j & 1][n], a0, a1, a2, a3, qf[n][4 * c + j][0], qf[n][4 * c + j][1]);
+            }
+          }
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[n][j] = two[0][n][j] + two[1][n][j];
+    };
+    auto sees = [&](int n, int j, int key) {  // row 2t + (j & 1) of tile n
+      const int row = r0 + 8 * n + 2 * t + (j & 1), p = ctx + row / G;
+      return row < r0 + R && key >= vis_lo(p, a.window) && key < vis_hi(p, s.len, a.causal);
+    };
+    if (n_mine > 0) {
+      cp_wait<S - 1>();
+      __syncwarp();
+      scores(0);
+    }
+#pragma unroll 1
+    for (int i = 0; i < n_mine; ++i) {
+      cp_wait<S - 2>();
+      __syncwarp();  // (the scales are lane 0's)
+      const float2 sc = scales[i % C::SCALES];
+      const int key0 = first_key + kWarps * kChunk * i;
+      const bool clean = key0 >= clean_lo && key0 + kChunk <= clean_hi;
+      float x[NB][4];
+#pragma unroll
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[n][j] = acc[n][j] * sc.x * rowf[n][j & 1];
+      issue(i + S - 1);
+      // the next chunk's scores run under this one's softmax
+      if (i + 1 < n_mine) scores(i + 1);
+      if (!clean) {
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (!sees(n, j, key0 + g + (j >> 1) * 8)) x[n][j] = -INFINITY;
+      }
+      // ---- the maximum moves when a score is more than 2^kSlack above it; the unit when V's scale is above it
+      bool grow = sc.y > unit;
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack;
+        grow |= fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
+      }
+      if (__any_sync(0xffffffffu, grow)) {
+        const float was = unit;
+        if (sc.y > unit) unit = 2.f * sc.y;  // (some room, so that it does not move again at once)
+        const float fu = was > 0.f ? was / unit : 1.f;
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            float mx = fmaxf(x[n][j], x[n][j + 2]);
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+            const float mn = mx > m[n][j] + kSlack ? mx : m[n][j];
+            const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - mn);  // (sums so far are 0 or NaN there)
+            m[n][j] = mn;
+            l[n][j] *= f;
+#pragma unroll
+            for (int k = 0; k < MT; ++k) {
+              o[n][k][j] *= f * fu;
+              o[n][k][j + 2] *= f * fu;
+            }
+          }
+      }
+      // ---- P, its sums, and P^T as the second product's operand
+      const float rv = unit > 0.f ? sc.y / unit * kUnit : 0.f;
+      uint32_t pb[NB][2];
+#pragma unroll
+      for (int n = 0; n < NB; ++n) {
+        float p[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          p[j] = ex2(x[n][j] - (m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1]));
+          l[n][j & 1] += p[j];
+        }
+        pb[n][0] = transpose8(pack_h2(p[0] * rv, p[1] * rv));
+        pb[n][1] = transpose8(pack_h2(p[2] * rv, p[3] * rv));
+      }
+      // ---- O^T
+      uint32_t vw[4][VW];
+      const uint8_t* stage = ring + (i % S) * C::BYTES + kChunk * D + lane * VB;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if constexpr (VW == 4) {
+          const uint4 v = *reinterpret_cast<const uint4*>(stage + q * 32 * VB);
+          vw[q][0] = v.x, vw[q][1] = v.y, vw[q][2] = v.z, vw[q][3] = v.w;
+        } else {
+          const uint2 v = *reinterpret_cast<const uint2*>(stage + q * 32 * VB);
+          vw[q][0] = v.x, vw[q][1] = v.y;
+        }
+      }
+      if (!clean) {
+        // A key that a row does not see may hold a NaN, and 0 x NaN is NaN: such codes become 0, and the rows
+        // that do see them get the NaN by hand.
+        uint32_t found = 0;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+#pragma unroll
+          for (int k = 0; k < VW; ++k) found |= nan_codes(vw[q][k]);
+        if (__any_sync(0xffffffffu, found != 0)) {
+#pragma unroll 1
+          for (int st = 0; st < 4; ++st)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int key = key0 + 2 * st + (q & 1) + 8 * (q >> 1);
+#pragma unroll
+              for (int k = 0; k < VW; ++k) {
+                const uint32_t bad = nan_codes(__shfl_sync(0xffffffffu, vw[q][k], 4 * g + st));
+#pragma unroll
+                for (int e = 0; e < 4; ++e)  // d VB g + 4 k + e: tile 2 k + e / 2, its row g + 8 (e & 1)
+                  if ((bad >> (8 * e + 7)) & 1u)
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                      for (int j = 0; j < 2; ++j)
+                        if (sees(n, j, key)) o[n][2 * k + e / 2][2 * (e & 1) + j] = __uint_as_float(0x7fffffffu);
+              }
+            }
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int k = 0; k < VW; ++k) vw[q][k] = without_nan(vw[q][k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < VW; ++k) {
+        const uint32_t e0 = __byte_perm(vw[0][k], vw[1][k], 0x5140), e1 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
+        const uint32_t f0 = __byte_perm(vw[2][k], vw[3][k], 0x5140), f1 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
+        uint32_t a0, a1, a2, a3, b0, b1, b2, b3;
+        e4m3x4_to_h4(e0, a0, a1);
+        e4m3x4_to_h4(f0, a2, a3);
+        e4m3x4_to_h4(e1, b0, b1);
+        e4m3x4_to_h4(f1, b2, b3);
+#pragma unroll
+        for (int n = 0; n < NB; ++n) {
+          mma(o[n][2 * k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          mma(o[n][2 * k + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
+        }
+      }
+    }
+    cp_wait<0>();
+    // ---- the warps meet: O [row][d] and (m, l) of each
+    __syncthreads();  // every warp has read its ring
+#pragma unroll
+    for (int n = 0; n < NB; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float sum = l[n][j];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        const int row = 8 * n + 2 * t + j;
+        if (g == 0) s_ml[warp * RB + row] = part_stats(m[n][j], sum);
+        float* dst = meet + (warp * RB + row) * C::LO + VB * g;
+        const float f = unit * (1.f / kUnit);
+#pragma unroll
+        for (int k = 0; k < MT; k += 2)
+          *reinterpret_cast<float4*>(dst + 2 * k) =
+              make_float4(o[n][k][j] * f, o[n][k][j + 2] * f, o[n][k + 1][j] * f, o[n][k + 1][j + 2] * f);
+      }
+    __syncthreads();
+    for (int row = warp; row < R; row += kWarps) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < kWarps) ml = s_ml[lane * RB + row];
+      const float M = warp_max(ml.x);
+      // a warp that saw no key has weight 0, the NaN of one with a NaN score stays one
+      const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      const float L = warp_sum(wt == 0.f ? 0.f : ml.y * wt);
+      const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
+      float sum[CC];
+#pragma unroll
+      for (int j = 0; j < CC; ++j) sum[j] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float ww = __shfl_sync(0xffffffffu, wt, w);
+        const float* v = meet + (w * RB + row) * C::LO + lane * CC;
+        // (a weight that underflows still takes its sums along: 0 x NaN is NaN)
+#pragma unroll
+        for (int j = 0; j < CC; ++j) sum[j] = fmaf(ww, (saw >> w) & 1u ? v[j] : 0.f, sum[j]);
+      }
+      const int tok = s.start + (r0 + row) / G, h = kvh * G + (r0 + row) % G;
+      if (part == -1) {
+        store_row<D>(a, tok, h, lane, sum, 1.f / L);
+        if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
+      } else {
+        float* w = (part >= 0 ? few_o<D, RB>(a, part, row) : part_o + row * D) + lane * CC;
+#pragma unroll
+        for (int j = 0; j < CC; ++j) w[j] = sum[j];
+        if (lane == 0) *(part >= 0 ? few_ml<D, RB>(a, plan, part, row) : part_ml + row) = part_stats(M, L);
+      }
+    }
+  };
+
+  if (plan.cluster > 0) {
+    // ---- rank q of the cluster takes an even share of the item's chunks; the ranks finish its rows in turn
+    cg::cluster_group cl = cg::this_cluster();
+    const int N = plan.cluster, item = cta / N, q = cta - item * N, rest = item / a.Hkv, kvh = item - rest * a.Hkv;
+    const int b = rest / plan.tiles, rt = rest - b * plan.tiles;
+    const Seq s = load_seq(r, b);
+    if (!s.ok && tid == 0 && rt == 0 && kvh == 0 && q == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
+    const int R = s.ok ? (int)max((int64_t)0, min((int64_t)RB, (int64_t)s.n * G - (int64_t)rt * RB)) : 0;
+    if (R == 0) return;  // (the whole cluster: nobody waits)
+    const int T = few_chunks(s, a.window), c0 = (int)((int64_t)T * q / N), c1 = (int)((int64_t)T * (q + 1) / N);
+    stretch(s, b, rt, kvh, c0, c1 - c0, N == 1 ? -1 : -2);
+    if (N == 1) return;
+    cl.sync();
+    for (int row = q + N * warp; row < R; row += N * kWarps) {
+      float2 ml = make_float2(-INFINITY, 0.f);
+      if (lane < N) ml = *cl.map_shared_rank(part_ml + row, lane);
+      const float M = warp_max(ml.x), wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
+      const float L = warp_sum(wt == 0.f ? 0.f : ml.y * wt);
+      const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
+      float sum[CC];
+#pragma unroll
+      for (int j = 0; j < CC; ++j) sum[j] = 0.f;
+#pragma unroll 4
+      for (int u = 0; u < N; ++u) {
+        const float wu = __shfl_sync(0xffffffffu, wt, u);
+        const float* v = cl.map_shared_rank(part_o, u) + row * D + lane * CC;
+#pragma unroll
+        for (int j = 0; j < CC; ++j) sum[j] = fmaf(wu, (saw >> u) & 1u ? v[j] : 0.f, sum[j]);
+      }
+      const int tok = s.start + (rt * RB + row) / G, h = kvh * G + (rt * RB + row) % G;
+      store_row<D>(a, tok, h, lane, sum, 1.f / L);
+      if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
+    }
+    cl.sync();  // no CTA leaves while a peer reads its part
+    return;
+  }
+  // ---- ranges: every warp lays the work out for itself
   const bool one = r.batch <= 32;
   Seq mine{0, 0, 0, false};
   if (one && lane < r.batch) mine = load_seq(r, lane);
@@ -202,7 +632,6 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
     while (u < u1 && u < chunk_end) {
       const int src = __ffs(__ballot_sync(0xffffffffu, before + incl > u)) - 1;
       const Seq s = few_bcast(ls, src);
-      const int b = base + src;
       const int64_t off = u - (before + __shfl_sync(0xffffffffu, incl - mine_u, src));
       const int T = few_chunks(s, a.window);
       const int64_t item = off / (T + plan.pad);
@@ -212,315 +641,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       const int c0 = (int)max(at, (int64_t)0), take = (int)(min((int64_t)T, at + most) - c0);
       u += min(T - at, most);
       if (take <= 0) continue;
-      const int part = take == T ? -1 : 2 * cta + (seg > 0);
+      stretch(s, base + src, rt, kvh, c0, take, take == T ? -1 : 2 * cta + (seg > 0));
       ++seg;
-      // ---- one stretch: rows r0 .. of the sequence, chunks [c0, c0 + take) behind the first
-      const int r0 = rt * RB, ctx = s.len - s.n, R = (int)min((int64_t)RB, (int64_t)s.n * G - r0);
-      const int p_first = ctx + r0 / G, p_last = ctx + (r0 + R - 1) / G;
-      const int k_lo = vis_lo(p_first, a.window), k_hi = vis_hi(p_last, s.len, a.causal);
-      const int clean_lo = vis_lo(p_last, a.window), clean_hi = vis_hi(p_first, s.len, a.causal);
-      const int chunk0 = few_first(s, a.window) + c0;
-      const int n_mine = take > warp ? (take - warp + kWarps - 1) / kWarps : 0;  // chunks chunk0 + warp + 8 i
-      const int32_t* tab = r.table + (int64_t)b * r.table_stride;
-      // pages and scales of this warp's next 32 chunks, one a lane
-      int pg = -1;
-      float ks = 0.f, vs = 0.f;
-      auto look_up = [&](int i0) {
-        const int i = i0 + lane, key = (chunk0 + warp + kWarps * i) * kChunk;
-        pg = -1;
-        ks = 1.f;
-        vs = 0.f;
-        if (i < n_mine && key < k_hi && key + kChunk > k_lo) {
-          pg = tab[key >> kv.page_shift];
-          if (pg < 0 || pg >= kv.n_pages) {
-            flag_status(r.status, DFLASH_STATUS_PAGE);
-            pg = -1;
-          } else {
-            ks = kv.ks[pg * kv.s_page + kvh * kv.s_head];
-            vs = kv.vs[pg * kv.s_page + kvh * kv.s_head];
-          }
-        }
-      };
-      auto issue = [&](int i) {  // chunk i of this warp into stage i % S
-        if (i < n_mine) {
-          if ((i & 31) == 0) look_up(i);
-          const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-          const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
-          if (lane == 0) scales[i % S] = make_float2(k1, v1);
-          const int key0 = (chunk0 + warp + kWarps * i) * kChunk;
-          const int64_t at = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot + kvh * kv.head;
-          const uint8_t* kp = kv.k + at;
-          const uint8_t* vp = kv.v + at;
-          const uint32_t dst = smem_addr(ring + (i % S) * C::BYTES) + lane * 16;
-          // (keys that no row of the tile sees arrive as zeros)
-          auto seen = [&](int j) { return page >= 0 && key0 + j >= k_lo && key0 + j < k_hi; };
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              cp_async<16>(dst + (h * (D / 64) + c) * 512, kp + (g + 8 * h) * kv.slot + 64 * c + 16 * t, seen(g + 8 * h));
-          const uint32_t vdst = smem_addr(ring + (i % S) * C::BYTES) + kChunk * D + lane * VB;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int j = 2 * t + (q & 1) + 8 * (q >> 1);
-            cp_async<VB>(vdst + q * 32 * VB, vp + j * kv.slot + VB * g, seen(j));
-          }
-        }
-        cp_commit();
-      };
-      // (the stages' first chunks are on their way while q is made ready)
-#pragma unroll
-      for (int i = 0; i < S - 1; ++i) issue(i);
-      // ---- q: lane (g, t) has rows g (+ 8 n) at the d's that it has of K
-      uint32_t qf[NB][KS][2];
-      float rowf[NB][2];  // of rows 2t, 2t + 1: scale 2^-e log2 e
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        const int row = 8 * n + g;
-        uint4 w[D / 32];
-#pragma unroll
-        for (int c = 0; c < D / 32; ++c) w[c] = make_uint4(0, 0, 0, 0);
-        if (row < R) {
-          const int i = (r0 + row) / G, h = kvh * G + (r0 + row) % G;
-          const bf16* q = reinterpret_cast<const bf16*>(a.q) + (int64_t)(s.start + i) * a.q_row + (int64_t)h * a.q_head;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c)
-#pragma unroll
-            for (int k = 0; k < 2; ++k) w[2 * c + k] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t + 8 * k);
-        }
-        const uint32_t* ww = reinterpret_cast<const uint32_t*>(w);
-        float most = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const float x = fabsf(__uint_as_float(ww[k] << 16)), y = fabsf(__uint_as_float(ww[k] & 0xffff0000u));
-          most = fmaxf(most, fmaxf(nonfinite(x) ? 0.f : x, nonfinite(y) ? 0.f : y));
-        }
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-        most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
-        // most 2^e in [2^14, 2^15); 2^e in two factors, either of them a normal number
-        const int e = most > 0.f ? 14 - ilogbf(most) : 0, e0 = e / 2;
-        const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-          const float x = __uint_as_float(ww[k] << 16) * f0 * f1, y = __uint_as_float(ww[k] & 0xffff0000u) * f0 * f1;
-          qf[n][k / 2][k & 1] = pack_h2(x, y);
-        }
-        const float f = ldexpf(sl2, -e);
-        // rows 2t, 2t + 1 of this tile are those of lanes g = 2t, 2t + 1
-        rowf[n][0] = __shfl_sync(0xffffffffu, f, 8 * t);
-        rowf[n][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
-      }
-      float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f;
-#pragma unroll
-      for (int n = 0; n < NB; ++n) {
-#pragma unroll
-        for (int k = 0; k < MT; ++k)
-#pragma unroll
-          for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
-        m[n][0] = m[n][1] = -INFINITY;
-        l[n][0] = l[n][1] = 0.f;
-      }
-      for (int i = 0; i < n_mine; ++i) {
-        cp_wait<S - 2>();
-        __syncwarp();  // (the stage's scales are lane 0's; what was read of the next stage to be filled has been)
-        issue(i + S - 1);
-        const uint8_t* stage = ring + (i % S) * C::BYTES;
-        const float2 sc = scales[i % S];
-        const int key0 = (chunk0 + warp + kWarps * i) * kChunk;
-        // ---- S^T
-        float x[NB][4];
-        {
-          float acc[2][NB][4];
-#pragma unroll
-          for (int p = 0; p < 2; ++p)
-#pragma unroll
-            for (int n = 0; n < NB; ++n)
-#pragma unroll
-              for (int j = 0; j < 4; ++j) acc[p][n][j] = 0.f;
-#pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            const uint4 k0 = *reinterpret_cast<const uint4*>(stage + c * 512 + lane * 16);
-            const uint4 k8 = *reinterpret_cast<const uint4*>(stage + (D / 64 + c) * 512 + lane * 16);
-            const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w8[4] = {k8.x, k8.y, k8.z, k8.w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t a0 = lo_h2(w0[j]), a1 = lo_h2(w8[j]), a2 = hi_h2(w0[j]), a3 = hi_h2(w8[j]);
-#pragma unroll
-              for (int n = 0; n < NB; ++n) mma(acc[j & 1][n], a0, a1, a2, a3, qf[n][4 * c + j][0], qf[n][4 * c + j][1]);
-            }
-          }
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) x[n][j] = (acc[0][n][j] + acc[1][n][j]) * sc.x * rowf[n][j & 1];
-        }
-        const bool clean = key0 >= clean_lo && key0 + kChunk <= clean_hi;
-        auto sees = [&](int n, int j, int key) {  // row 2t + (j & 1) of tile n
-          const int row = r0 + 8 * n + 2 * t + (j & 1), p = ctx + row / G;
-          return row < r0 + R && key >= vis_lo(p, a.window) && key < vis_hi(p, s.len, a.causal);
-        };
-        if (!clean) {
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              if (!sees(n, j, key0 + g + (j >> 1) * 8)) x[n][j] = -INFINITY;
-        }
-        // ---- the maximum moves when a score is more than 2^kSlack above it; the unit when V's scale is above it
-        bool grow = sc.y > unit;
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack;
-          grow |= fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
-        }
-        if (__any_sync(0xffffffffu, grow)) {
-          const float was = unit;
-          if (sc.y > unit) unit = 2.f * sc.y;  // (some room, so that it does not move again at once)
-          const float fu = was > 0.f ? was / unit : 1.f;
-#pragma unroll
-          for (int n = 0; n < NB; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              float mx = fmaxf(x[n][j], x[n][j + 2]);
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-              mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-              const float mn = mx > m[n][j] + kSlack ? mx : m[n][j];
-              const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - mn);  // (sums so far are 0 or NaN there)
-              m[n][j] = mn;
-              l[n][j] *= f;
-#pragma unroll
-              for (int k = 0; k < MT; ++k) {
-                o[n][k][j] *= f * fu;
-                o[n][k][j + 2] *= f * fu;
-              }
-            }
-        }
-        // ---- P, its sums, and P^T as the second product's operand
-        const float rv = unit > 0.f ? sc.y / unit * kUnit : 0.f;
-        uint32_t pb[NB][2];
-#pragma unroll
-        for (int n = 0; n < NB; ++n) {
-          float p[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            p[j] = ex2(x[n][j] - (m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1]));
-            l[n][j & 1] += p[j];
-          }
-          pb[n][0] = transpose8(pack_h2(p[0] * rv, p[1] * rv));
-          pb[n][1] = transpose8(pack_h2(p[2] * rv, p[3] * rv));
-        }
-        // ---- O^T
-        constexpr int VW = VB / 4;  // words of a lane's piece
-        uint32_t vw[4][VW];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const uint8_t* p = stage + kChunk * D + q * 32 * VB + lane * VB;
-          if constexpr (VW == 4) {
-            const uint4 v = *reinterpret_cast<const uint4*>(p);
-            vw[q][0] = v.x, vw[q][1] = v.y, vw[q][2] = v.z, vw[q][3] = v.w;
-          } else {
-            const uint2 v = *reinterpret_cast<const uint2*>(p);
-            vw[q][0] = v.x, vw[q][1] = v.y;
-          }
-        }
-        if (!clean) {
-          // A key that a row does not see may hold a NaN, and 0 x NaN is NaN: such codes become 0, and the rows
-          // that do see them get the NaN by hand.
-          uint32_t found = 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int k = 0; k < VW; ++k) found |= nan_codes(vw[q][k]);
-          if (__any_sync(0xffffffffu, found != 0)) {
-#pragma unroll 1
-            for (int st = 0; st < 4; ++st)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int key = key0 + 2 * st + (q & 1) + 8 * (q >> 1);
-#pragma unroll
-                for (int k = 0; k < VW; ++k) {
-                  const uint32_t bad = nan_codes(__shfl_sync(0xffffffffu, vw[q][k], 4 * g + st));
-#pragma unroll
-                  for (int e = 0; e < 4; ++e)  // d 16 g + 4 k + e: tile 2 k + e / 2, its row g + 8 (e & 1)
-                    if ((bad >> (8 * e + 7)) & 1u)
-#pragma unroll
-                      for (int n = 0; n < NB; ++n)
-#pragma unroll
-                        for (int j = 0; j < 2; ++j)
-                          if (sees(n, j, key)) o[n][2 * k + e / 2][2 * (e & 1) + j] = __uint_as_float(0x7fffffffu);
-                }
-              }
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-#pragma unroll
-              for (int k = 0; k < VW; ++k) vw[q][k] = without_nan(vw[q][k]);
-          }
-        }
-#pragma unroll
-        for (int k = 0; k < VW; ++k) {
-          const uint32_t e0 = __byte_perm(vw[0][k], vw[1][k], 0x5140), e1 = __byte_perm(vw[0][k], vw[1][k], 0x7362);
-          const uint32_t f0 = __byte_perm(vw[2][k], vw[3][k], 0x5140), f1 = __byte_perm(vw[2][k], vw[3][k], 0x7362);
-          const uint32_t a0 = lo_h2(e0), a1 = hi_h2(e0), a2 = lo_h2(f0), a3 = hi_h2(f0);
-          const uint32_t b0 = lo_h2(e1), b1 = hi_h2(e1), b2 = lo_h2(f1), b3 = hi_h2(f1);
-#pragma unroll
-          for (int n = 0; n < NB; ++n) {
-            mma(o[n][2 * k], a0, a1, a2, a3, pb[n][0], pb[n][1]);
-            mma(o[n][2 * k + 1], b0, b1, b2, b3, pb[n][0], pb[n][1]);
-          }
-        }
-      }
-      cp_wait<0>();
-      // ---- the warps meet: O [row][d] and (m, l) of each
-      __syncthreads();  // every warp has read its ring
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          float sum = l[n][j];
-          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-          const int row = 8 * n + 2 * t + j;
-          if (g == 0) s_ml[warp * RB + row] = part_stats(m[n][j], sum);
-          float* dst = meet + (warp * RB + row) * C::LO + VB * g;
-          const float f = unit * (1.f / kUnit);
-#pragma unroll
-          for (int k = 0; k < MT; k += 2)
-            *reinterpret_cast<float4*>(dst + 2 * k) =
-                make_float4(o[n][k][j] * f, o[n][k][j + 2] * f, o[n][k + 1][j] * f, o[n][k + 1][j + 2] * f);
-        }
-      __syncthreads();
-      for (int row = warp; row < R; row += kWarps) {
-        float2 ml = make_float2(-INFINITY, 0.f);
-        if (lane < kWarps) ml = s_ml[lane * RB + row];
-        const float M = warp_max(ml.x);
-        // a warp that saw no key has weight 0, the NaN of one with a NaN score stays one
-        const float wt = ml.x == -INFINITY ? 0.f : exp2f(ml.x - M);
-        const float L = warp_sum(wt == 0.f ? 0.f : ml.y * wt);
-        const uint32_t saw = __ballot_sync(0xffffffffu, ml.y != 0.f);
-        float acc[D / 32];
-#pragma unroll
-        for (int j = 0; j < D / 32; ++j) acc[j] = 0.f;
-#pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          const float ww = __shfl_sync(0xffffffffu, wt, w);
-          const float* v = meet + (w * RB + row) * C::LO + lane * (D / 32);
-          // (a weight that underflows still takes its sums along: 0 x NaN is NaN)
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) acc[j] = fmaf(ww, (saw >> w) & 1u ? v[j] : 0.f, acc[j]);
-        }
-        const int tok = s.start + (r0 + row) / G, h = kvh * G + (r0 + row) % G;
-        if (part >= 0) {
-          float* w = few_o<D, RB>(a, part, row) + lane * (D / 32);
-#pragma unroll
-          for (int j = 0; j < D / 32; ++j) w[j] = acc[j];
-          if (lane == 0) *few_ml<D, RB>(a, plan, part, row) = part_stats(M, L);
-        } else {
-          store_row<D>(a, tok, h, lane, acc, 1.f / L);
-          if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
-        }
-      }
       __syncthreads();  // the rings are free again
     }
     before = chunk_end;
@@ -607,20 +729,35 @@ __global__ void __launch_bounds__(256) k_kv8_few_merge(Ragged r, AttnCall a, Few
 int rows_of(const Ragged& r, const AttnCall& a) {
   return (int)std::min<int64_t>((int64_t)r.max_rows * (a.Hq / a.Hkv), 1 << 20);
 }
-int few_nb(const Ragged& r, const AttnCall& a) {
-  const int rows = rows_of(r, a);
-  return rows <= 8 ? 1 : rows <= 16 ? 2 : 4;
-}
-FewPlan few_plan(int nb, int sms) {
+struct FewHost {
+  int nb;
   FewPlan p;
-  p.pad = 8;
-  p.min_units = 8;
-  p.slots = 2 * sms * (nb <= 2 ? 2 : 1);
-  return p;
+};
+FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
+  const int rows = rows_of(r, a), seqs = std::min(r.batch, std::max(r.total, 1));
+  FewHost h;
+  // 32 rows a CTA where there are many items (each tile of rows converts the codes anew), 16 where the
+  // calls are short and spread better
+  h.nb = rows <= 8 ? 1 : 2;
+  if (rows > 16 && (int64_t)seqs * a.Hkv * ((rows + 15) / 16) > 2 * sms) h.nb = 4;
+  const int rb = 8 * h.nb, ctas = sms * (h.nb <= 2 ? 2 : 1);
+  h.p.tiles = (rows + rb - 1) / rb;
+  h.p.pad = 8;
+  h.p.min_units = 8;
+  h.p.slots = 2 * ctas;
+  // cluster: an item's chunks over up to 8 CTAs, where all items run at once and none has more than 64 chunks
+  h.p.cluster = 0;
+  const int64_t items = (int64_t)r.batch * h.p.tiles * a.Hkv;
+  const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
+  const int64_t chunks = (span + kChunk - 1) / kChunk + 1;
+  for (int n = 1; n <= kMaxCluster && items * n <= ctas; n *= 2)
+    if (chunks <= 64 * n) h.p.cluster = n;
+  while (h.p.cluster > 1 && chunks <= 4 * h.p.cluster) h.p.cluster /= 2;
+  return h;
 }
 
 template <int D, int NB>
-cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
+cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, const FewPlan& p, int sms, cudaStream_t st) {
   using C = FewCfg<D, NB>;
   static std::atomic<bool> done[64];
   int dev = 0;
@@ -631,7 +768,8 @@ cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, in
     if (e != cudaSuccess) return e;
     if (dev < 64) done[dev] = true;
   }
-  const FewPlan p = few_plan(NB, sms);
+  if (p.cluster > 0)
+    return launch_kc(k_kv8_few<D, NB>, r.batch * p.tiles * a.Hkv * p.cluster, kWarps * 32, C::SMEM, st, p.cluster, r, a, kv, p);
   const int grid = sms * C::CTAS;
   e = launch_k(k_kv8_few<D, NB>, grid, kWarps * 32, C::SMEM, st, r, a, kv, p);
   if (e != cudaSuccess) return e;
@@ -640,15 +778,17 @@ cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, in
 }
 template <int D>
 cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
-  const int nb = few_nb(r, a);
-  return nb == 1 ? launch_few<D, 1>(r, a, kv, sms, st) : nb == 2 ? launch_few<D, 2>(r, a, kv, sms, st) : launch_few<D, 4>(r, a, kv, sms, st);
+  const FewHost h = few_plan(r, a, sms);
+  return h.nb == 1   ? launch_few<D, 1>(r, a, kv, h.p, sms, st)
+         : h.nb == 2 ? launch_few<D, 2>(r, a, kv, h.p, sms, st)
+                     : launch_few<D, 4>(r, a, kv, h.p, sms, st);
 }
 
 }  // namespace
 
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms) {
-  const int nb = few_nb(r, a);
-  return (int64_t)few_plan(nb, sms).slots * 8 * nb * (a.d + 2) * 4;
+  const FewHost h = few_plan(r, a, sms);
+  return h.p.cluster ? 0 : (int64_t)h.p.slots * 8 * h.nb * (a.d + 2) * 4;
 }
 cudaError_t launch_kv8_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st) {
   return a.d == 64 ? launch_few<64>(r, a, kv, sms, st) : launch_few<128>(r, a, kv, sms, st);

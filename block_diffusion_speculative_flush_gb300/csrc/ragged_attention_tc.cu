@@ -615,10 +615,10 @@ __device__ __noinline__ void add_nan8(Ragged r, Kv8View kv, const Work& w, uint3
 
 // Sixteen codes as fp16, the first eight and the others.
 __device__ __forceinline__ void codes_to_h16(const uint4& c, uint4& lo, uint4& hi) {
-  lo = make_uint4(e4m3x2_to_h2((uint16_t)c.x), e4m3x2_to_h2((uint16_t)(c.x >> 16)), e4m3x2_to_h2((uint16_t)c.y),
-                  e4m3x2_to_h2((uint16_t)(c.y >> 16)));
-  hi = make_uint4(e4m3x2_to_h2((uint16_t)c.z), e4m3x2_to_h2((uint16_t)(c.z >> 16)), e4m3x2_to_h2((uint16_t)c.w),
-                  e4m3x2_to_h2((uint16_t)(c.w >> 16)));
+  e4m3x4_to_h4(c.x, lo.x, lo.y);
+  e4m3x4_to_h4(c.y, lo.z, lo.w);
+  e4m3x4_to_h4(c.z, hi.x, hi.y);
+  e4m3x4_to_h4(c.w, hi.z, hi.w);
 }
 
 // A row of a Q tile (128 bytes of it in each of D / 64 blocks `block` bytes apart, its 16-byte chunks

@@ -396,12 +396,12 @@ def test_two_graphs_replayed_at_once(dtype, rows):
 
 def test_a_workspace_that_is_too_small_is_refused():
     D = lib()
-    B = Batch8("bf16", 8, 2, 128, 16, [1], [3000], tail=0)
+    B = Batch8("bf16", 8, 2, 128, 16, [1], [9000], tail=0)
     P = B.cuda(*B.appended())
     q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), B.table.cuda()
     o = torch.empty_like(q)
-    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 3000, *P)
+    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 9000, *P)
     assert need > 0
     with pytest.raises(D.DFlashError, match="workspace"):
-        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=3000,
+        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=9000,
                                workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
