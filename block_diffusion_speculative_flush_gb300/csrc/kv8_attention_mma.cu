@@ -62,8 +62,8 @@ struct FewCfg {
   static constexpr int CTAS = NB <= 2 ? 2 : 1;    // of an SM
   static constexpr int BYTES = kChunk * 2 * D;    // codes of a chunk
   static constexpr int STAGES = (NB <= 2 ? 3 : 5) * (128 / D);
-  static constexpr int SCALES = 16;               // of the chunks on their way
-  static_assert(STAGES + 2 <= SCALES, "an entry for each chunk on its way and the two in use");
+  static constexpr int SCALES = 64;               // of a warp's chunks: those looked up last and the 32 before
+  static_assert(STAGES < 32, "a chunk in use was looked up at most once ago");
   static constexpr int LO = D + 4;                // floats of a row where the warps meet
   static constexpr int RING = kWarps * STAGES * BYTES, MEET = kWarps * RB * LO * 4, PART = RB * D * 4;
   static constexpr int AREA = RING > MEET + PART ? RING : MEET + PART;
@@ -207,12 +207,10 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
     const int32_t* tab = r.table + (int64_t)b * r.table_stride;
     // pages and scales of this warp's next 32 chunks, one a lane
     int pg = -1;
-    float ks = 0.f, vs = 0.f;
     auto look_up = [&](int i0) {
       const int i = i0 + lane, key = first_key + kWarps * kChunk * i;
+      float ks = 1.f, vs = 0.f;
       pg = -1;
-      ks = 1.f;
-      vs = 0.f;
       if (i < n_mine && key < k_hi && key + kChunk > k_lo) {
         pg = tab[key >> kv.page_shift];
         if (pg < 0 || pg >= kv.n_pages) {
@@ -223,63 +221,51 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           vs = kv.vs[pg * kv.s_page + kvh * kv.s_head];
         }
       }
+      scales[i % C::SCALES] = make_float2(ks, vs);
     };
     // this lane's pieces: of K rows g and g + 8, of V rows 2t, 2t + 1, 2t + 8, 2t + 9
     const uint8_t* k_base = kv.k + kvh * kv.head + g * kv.slot + 16 * t;
     const uint8_t* v_base = kv.v + kvh * kv.head + 2 * t * kv.slot + VB * g;
     const int64_t slot8 = 8 * kv.slot;
     const uint32_t k_dst = smem_addr(ring) + lane * 16, v_dst = smem_addr(ring) + kChunk * D + lane * VB;
-    int64_t at_v = 0;    // where the chunk whose V is asked for next lies
-    int page_v = -1;
-    // group j: K of chunk j + 1, V of chunk j (what step j uses)
-    auto issue = [&](int j) {
-      if (j >= 0 && j < n_mine) {
-        const uint8_t* p = v_base + at_v;
-        const uint32_t dst = v_dst + (j % S) * C::BYTES;
-        const int key0 = first_key + kWarps * kChunk * j;
-        if (page_v >= 0 && key0 >= k_lo && key0 + kChunk <= k_hi) {
-          cp_async<VB>(dst, p);
-          cp_async<VB>(dst + 32 * VB, p + kv.slot);
-          cp_async<VB>(dst + 64 * VB, p + slot8);
-          cp_async<VB>(dst + 96 * VB, p + slot8 + kv.slot);
-        } else {  // (keys that no row of the tile sees arrive as zeros)
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int key = key0 + 2 * t + (q & 1) + 8 * (q >> 1);
-            cp_async<VB>(dst + q * 32 * VB, p + (q & 1) * kv.slot + (q >> 1) * slot8, page_v >= 0 && key >= k_lo && key < k_hi);
-          }
-        }
-      }
-      const int i = j + 1;
+    uint32_t to = 0;  // the stage that is filled next
+    auto issue = [&](int i) {  // chunk i
       if (i < n_mine) {
         if ((i & 31) == 0) look_up(i);
-        const int page = __shfl_sync(0xffffffffu, pg, i & 31);
-        const float k1 = __shfl_sync(0xffffffffu, ks, i & 31), v1 = __shfl_sync(0xffffffffu, vs, i & 31);
-        if (lane == 0) scales[i % C::SCALES] = make_float2(k1, v1);
-        const int key0 = first_key + kWarps * kChunk * i;
-        at_v = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot;
-        page_v = page;
-        const uint8_t* p = k_base + at_v;
-        const uint32_t dst = k_dst + (i % S) * C::BYTES;
+        const int page = __shfl_sync(0xffffffffu, pg, i & 31), key0 = first_key + kWarps * kChunk * i;
+        const int64_t at = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot;
+        const uint8_t* kp = k_base + at;
+        const uint8_t* vp = v_base + at;
+        const uint32_t kd = k_dst + to, vd = v_dst + to;
         if (page >= 0 && key0 >= k_lo && key0 + kChunk <= k_hi) {
 #pragma unroll
           for (int c = 0; c < D / 64; ++c) {
-            cp_async<16>(dst + c * 512, p + 64 * c);
-            cp_async<16>(dst + (D / 64 + c) * 512, p + slot8 + 64 * c);
+            cp_async<16>(kd + c * 512, kp + 64 * c);
+            cp_async<16>(kd + (D / 64 + c) * 512, kp + slot8 + 64 * c);
           }
-        } else {
+          cp_async<VB>(vd, vp);
+          cp_async<VB>(vd + 32 * VB, vp + kv.slot);
+          cp_async<VB>(vd + 64 * VB, vp + slot8);
+          cp_async<VB>(vd + 96 * VB, vp + slot8 + kv.slot);
+        } else {  // (keys that no row of the tile sees arrive as zeros)
 #pragma unroll
           for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int c = 0; c < D / 64; ++c)
-              cp_async<16>(dst + (h * (D / 64) + c) * 512, p + h * slot8 + 64 * c,
+              cp_async<16>(kd + (h * (D / 64) + c) * 512, kp + h * slot8 + 64 * c,
                            page >= 0 && key0 + g + 8 * h >= k_lo && key0 + g + 8 * h < k_hi);
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int key = key0 + 2 * t + (q & 1) + 8 * (q >> 1);
+            cp_async<VB>(vd + q * 32 * VB, vp + (q & 1) * kv.slot + (q >> 1) * slot8, page >= 0 && key >= k_lo && key < k_hi);
+          }
         }
+        to = to == (S - 1) * C::BYTES ? 0 : to + C::BYTES;
       }
       cp_commit();
     };
 #pragma unroll 1
-    for (int j = -1; j < S - 1; ++j) issue(j);
+    for (int i = 0; i < S - 1; ++i) issue(i);
     // ---- q: lane (g, t) has rows g (+ 8 n) at the d's that it has of K
     uint32_t qf[C::QS ? 1 : NB][KS][2];
     float rowf[NB][2];  // of rows 2t, 2t + 1: scale 2^-e log2 e
@@ -333,7 +319,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       rowf[0][0] = __shfl_sync(0xffffffffu, f, 8 * t);
       rowf[0][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
-    float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f;
+    float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f, per_unit = 0.f;  // per_unit: 2^10 / unit
+    float ref[NB][2];  // what scores are taken from: m, or 0 as long as that is -inf
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
@@ -341,11 +328,10 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
       m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = 0.f;
+      l[n][0] = l[n][1] = ref[n][0] = ref[n][1] = 0.f;
     }
-    float acc[NB][4];  // S^T of the step to come
-    auto scores = [&](int i) {
-      const uint8_t* stage = ring + (i % S) * C::BYTES;
+    uint32_t from = 0;  // the stage that is read next
+    auto scores = [&](const uint8_t* stage, const float2& sc, float (*x)[4]) {
       float two[2][NB][4];
 #pragma unroll
       for (int p = 0; p < 2; ++p)
@@ -377,32 +363,24 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[n][j] = two[0][n][j] + two[1][n][j];
+        for (int j = 0; j < 4; ++j) x[n][j] = (two[0][n][j] + two[1][n][j]) * sc.x * rowf[n][j & 1];
     };
     auto sees = [&](int n, int j, int key) {  // row 2t + (j & 1) of tile n
       const int row = r0 + 8 * n + 2 * t + (j & 1), p = ctx + row / G;
       return row < r0 + R && key >= vis_lo(p, a.window) && key < vis_hi(p, s.len, a.causal);
     };
-    if (n_mine > 0) {
-      cp_wait<S - 1>();
-      __syncwarp();
-      scores(0);
-    }
 #pragma unroll 1
     for (int i = 0; i < n_mine; ++i) {
       cp_wait<S - 2>();
-      __syncwarp();  // (the scales are lane 0's)
+      __syncwarp();  // (scales are other lanes')
+      issue(i + S - 1);
+      const uint8_t* stage = ring + from;
+      from = from == (S - 1) * C::BYTES ? 0 : from + C::BYTES;
       const float2 sc = scales[i % C::SCALES];
       const int key0 = first_key + kWarps * kChunk * i;
       const bool clean = key0 >= clean_lo && key0 + kChunk <= clean_hi;
       float x[NB][4];
-#pragma unroll
-      for (int n = 0; n < NB; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = acc[n][j] * sc.x * rowf[n][j & 1];
-      issue(i + S - 1);
-      // the next chunk's scores run under this one's softmax
-      if (i + 1 < n_mine) scores(i + 1);
+      scores(stage, sc, x);
       if (!clean) {
 #pragma unroll
         for (int n = 0; n < NB; ++n)
@@ -421,6 +399,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
         const float was = unit;
         if (sc.y > unit) unit = 2.f * sc.y;  // (some room, so that it does not move again at once)
         const float fu = was > 0.f ? was / unit : 1.f;
+        per_unit = unit > 0.f ? kUnit / unit : 0.f;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -432,6 +411,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
             const float mn = mx > m[n][j] + kSlack ? mx : m[n][j];
             const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - mn);  // (sums so far are 0 or NaN there)
             m[n][j] = mn;
+            ref[n][j] = mn == -INFINITY ? 0.f : mn;
             l[n][j] *= f;
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
@@ -441,14 +421,14 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           }
       }
       // ---- P, its sums, and P^T as the second product's operand
-      const float rv = unit > 0.f ? sc.y / unit * kUnit : 0.f;
+      const float rv = sc.y * per_unit;
       uint32_t pb[NB][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         float p[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          p[j] = ex2(x[n][j] - (m[n][j & 1] == -INFINITY ? 0.f : m[n][j & 1]));
+          p[j] = ex2(x[n][j] - ref[n][j & 1]);
           l[n][j & 1] += p[j];
         }
         pb[n][0] = transpose8(pack_h2(p[0] * rv, p[1] * rv));
@@ -456,14 +436,14 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       }
       // ---- O^T
       uint32_t vw[4][VW];
-      const uint8_t* stage = ring + (i % S) * C::BYTES + kChunk * D + lane * VB;
+      const uint8_t* v_stage = stage + kChunk * D + lane * VB;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         if constexpr (VW == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(stage + q * 32 * VB);
+          const uint4 v = *reinterpret_cast<const uint4*>(v_stage + q * 32 * VB);
           vw[q][0] = v.x, vw[q][1] = v.y, vw[q][2] = v.z, vw[q][3] = v.w;
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(stage + q * 32 * VB);
+          const uint2 v = *reinterpret_cast<const uint2*>(v_stage + q * 32 * VB);
           vw[q][0] = v.x, vw[q][1] = v.y;
         }
       }
