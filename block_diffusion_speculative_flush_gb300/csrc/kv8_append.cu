@@ -103,15 +103,9 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
   const int p0 = max(first, page << kv.page_shift), p1 = min(s.len, (page + 1) << kv.page_shift);
   const int s0 = p0 & (size - 1), n = p1 - p0, row0 = s.start + p0 - first;
   const int task = blockIdx.y * (kWarps / WPT) + warp / WPT, part = warp % WPT;
-  const int pg = r.table[(int64_t)b * r.table_stride + page];
-  if (pg < 0 || pg >= kv.n_pages) {
-    if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_PAGE);
-    return;
-  }
+  const int pg = r.table[(int64_t)b * r.table_stride + page];  // on its way while the rows are asked for
   const bool live = task < 2 * heads;  // (a warp without a task still meets the barrier)
   const int w = task >= heads, h = live ? task - w * heads : 0;
-  float* scale = (w ? kv.vs : kv.ks) + (int64_t)pg * kv.s_page + h * kv.s_head;
-  const float old = s0 > 0 ? *scale : 0.f;
   const int lpr = d / 8, rpw = 32 / lpr, mine = lane / lpr, col = (lane - mine * lpr) * 8;
   const bool in = live && mine < rpw;
   const T* src = reinterpret_cast<const T*>(w ? x.x[1] : x.x[0]) + (int64_t)row0 * (w ? x.row[1] : x.row[0]) +
@@ -129,6 +123,12 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
 #pragma unroll
   for (int t = 0; t < kHold; ++t)
     if (in && at + t * step < n) hold[t].load(src + (at + t * step) * src_row);
+  if (pg < 0 || pg >= kv.n_pages) {
+    if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_PAGE);
+    return;
+  }
+  float* scale = (w ? kv.vs : kv.ks) + (int64_t)pg * kv.s_page + h * kv.s_head;
+  const float old = s0 > 0 ? *scale : 0.f;
 #pragma unroll
   for (int t = 0; t < kHold; ++t)
     if (in && at + t * step < n) look(hold[t]);

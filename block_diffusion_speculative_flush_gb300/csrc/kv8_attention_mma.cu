@@ -722,7 +722,7 @@ FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
   if (rows > 16 && (int64_t)seqs * a.Hkv * ((rows + 15) / 16) > 2 * sms) h.nb = 4;
   const int rb = 8 * h.nb, ctas = sms * (h.nb <= 2 ? 2 : 1);
   h.p.tiles = (rows + rb - 1) / rb;
-  h.p.pad = 8;
+  h.p.pad = 28;
   h.p.min_units = 8;
   h.p.slots = 2 * ctas;
   // cluster: an item's chunks over up to 8 CTAs, where all items run at once and none has more than 64 chunks

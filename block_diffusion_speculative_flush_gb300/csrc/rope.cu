@@ -14,6 +14,16 @@
 namespace dfl {
 namespace {
 
+// n / d as n m / 2^32 with m = floor(2^32 / d) + 1: m is above 2^32 / d by at most 1, the quotient by
+// less than n / 2^32, which does not reach the next whole number as long as n d < 2^32.  (Here n < 2^21
+// and d <= 2^8, or n < 2^13 and d <= 2^11.)
+struct FastDiv {
+  uint32_t m;
+  int32_t d;
+};
+FastDiv fast_div_of(int d) { return FastDiv{(uint32_t)(((uint64_t)1 << 32) / (uint32_t)d + 1), d}; }
+__device__ __forceinline__ int fast_div(int n, const FastDiv& f) { return f.d == 1 ? n : (int)__umulhi((uint32_t)n, f.m); }
+
 struct RopeSide {
   const void* x;
   void* y;
@@ -24,6 +34,7 @@ struct RopeCall {
   int32_t heads[2];
   int32_t d, rot, off, copy;  // copy: the elements that pass through are written too
   float amplitude, sign;
+  FastDiv per, all_heads;  // by a head's tasks, and by the heads of a row
 };
 struct RopeTurns {
   uint64_t t[DFLASH_ROPE_MAX_DIM / 2];
@@ -81,50 +92,63 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(Ragged r, RopeCall c, con
   __syncthreads();
   const int turned = IL ? c.rot / V : half / V, passed = c.copy ? (c.d - c.rot) / V : 0, per = turned + passed;
   const int heads = c.heads[0] + c.heads[1], tasks = RPC * heads * per;
-  for (int e = tid; e < tasks; e += kRopeThreads) {
-    const int hh = e / per, j = e - hh * per, k = hh / heads, h = hh - k * heads;
-    if (pos[k] < 0) continue;
-    const int w = h >= c.heads[0], g = w ? h - c.heads[0] : h;
-    const RopeSide s = w ? c.side[1] : c.side[0];
-    const T* x = reinterpret_cast<const T*>(s.x) + (int64_t)(row0 + k) * s.x_row + g * s.x_head;
-    T* y = reinterpret_cast<T*>(s.y) + (int64_t)(row0 + k) * s.y_row + g * s.y_head;
-    Vec<T, V> a;
-    if (j >= turned) {  // in front of the rotated part, or behind it
-      int at = (j - turned) * V;
-      if (at >= c.off) at += c.rot;
-      a.load(x + at);
-      a.store(y + at);
-    } else if (IL) {
-      const int at = c.off + j * V;
-      a.load(x + at);
+  // U tasks of a thread at a time: their loads are in flight together
+  constexpr int U = RPC == 1 ? 2 : 4;
+  for (int e0 = tid; e0 < tasks; e0 += U * kRopeThreads) {
+    Vec<T, V> a[U], b[U];
+    const T* x[U];
+    T* y[U];
+    int cs_at[U];  // where the pair's cos and sin begin, -1: passes through, -2: nothing to do
 #pragma unroll
-      for (int q = 0; q < V / 2; ++q) {
-        const float2 t = cs[k * half + j * (V / 2) + q];
-        const float u = a.get(2 * q), v = a.get(2 * q + 1);
-        a.set(2 * q, u * t.x - v * t.y);
-        a.set(2 * q + 1, v * t.x + u * t.y);
-      }
-      a.store(y + at);
-    } else {
-      const int at = c.off + j * V;
-      Vec<T, V> b;
-      a.load(x + at);
-      b.load(x + at + half);
+    for (int u = 0; u < U; ++u) {
+      const int e = e0 + u * kRopeThreads;
+      cs_at[u] = -2;
+      if (e >= tasks) continue;
+      const int hh = fast_div(e, c.per), j = e - hh * per, k = fast_div(hh, c.all_heads), h = hh - k * heads;
+      if (pos[k] < 0) continue;
+      const int w = h >= c.heads[0], g = w ? h - c.heads[0] : h;
+      const RopeSide s = w ? c.side[1] : c.side[0];
+      int at = (j - turned) * V;  // in front of the rotated part, or behind it
+      if (j < turned) at = c.off + j * V;
+      else if (at >= c.off) at += c.rot;
+      x[u] = reinterpret_cast<const T*>(s.x) + (int64_t)(row0 + k) * s.x_row + g * s.x_head + at;
+      y[u] = reinterpret_cast<T*>(s.y) + (int64_t)(row0 + k) * s.y_row + g * s.y_head + at;
+      cs_at[u] = j >= turned ? -1 : k * half + j * (IL ? V / 2 : V);
+      a[u].load(x[u]);
+      if (!IL && j < turned) b[u].load(x[u] + half);
+    }
 #pragma unroll
-      for (int q = 0; q < V; ++q) {
-        const float2 t = cs[k * half + j * V + q];
-        const float u = a.get(q), v = b.get(q);
-        a.set(q, u * t.x - v * t.y);
-        b.set(q, v * t.x + u * t.y);
+    for (int u = 0; u < U; ++u) {
+      if (cs_at[u] == -2) continue;
+      if (cs_at[u] >= 0) {
+        if (IL) {
+#pragma unroll
+          for (int q = 0; q < V / 2; ++q) {
+            const float2 t = cs[cs_at[u] + q];
+            const float p = a[u].get(2 * q), v = a[u].get(2 * q + 1);
+            a[u].set(2 * q, p * t.x - v * t.y);
+            a[u].set(2 * q + 1, v * t.x + p * t.y);
+          }
+        } else {
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            const float2 t = cs[cs_at[u] + q];
+            const float p = a[u].get(q), v = b[u].get(q);
+            a[u].set(q, p * t.x - v * t.y);
+            b[u].set(q, v * t.x + p * t.y);
+          }
+          b[u].store(y[u] + half);
+        }
       }
-      a.store(y + at);
-      b.store(y + at + half);
+      a[u].store(y[u]);
     }
   }
 }
 
 template <typename T, int V, bool IL>
-cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, cudaStream_t st) {
+cudaError_t launch_rope(const Ragged& r, RopeCall c, const RopeTurns& t, cudaStream_t st) {
+  c.per = fast_div_of((IL ? c.rot / V : c.rot / 2 / V) + (c.copy ? (c.d - c.rot) / V : 0));
+  c.all_heads = fast_div_of(c.heads[0] + c.heads[1]);
   // few rows: one a CTA, so that they spread over the SMs
   if (r.total <= 608) return launch_k(k_rope<T, V, IL, 1>, (unsigned)r.total, kRopeThreads, 0, st, r, c, t);
   return launch_k(k_rope<T, V, IL, 4>, (unsigned)((r.total + 3) / 4), kRopeThreads, 0, st, r, c, t);
