@@ -14,10 +14,10 @@ namespace dfl {
 namespace {
 
 constexpr int kThreads = 256, kWarps = kThreads / 32;
-constexpr int kHold = 4;  // steps of a warp whose rows stay in registers between the two passes
 
 template <typename T> struct Eight;  // eight elements
 template <> struct Eight<bf16> {
+  static constexpr int HOLD = 8;  // steps of a warp whose rows stay in registers
   uint4 a;
   __device__ __forceinline__ void load(const bf16* p) { a = *reinterpret_cast<const uint4*>(p); }
   __device__ __forceinline__ void get(float* f) const {
@@ -28,8 +28,14 @@ template <> struct Eight<bf16> {
       f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
     }
   }
+  // The running maximum of magnitudes: bits of a float without its sign order as integers do, two bf16 a word.
+  __device__ __forceinline__ void most(uint32_t& m) const {
+    m = __vmaxu2(__vmaxu2(__vmaxu2(m, a.x & 0x7fff7fffu), __vmaxu2(a.y & 0x7fff7fffu, a.z & 0x7fff7fffu)), a.w & 0x7fff7fffu);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return max(m << 16, m & 0xffff0000u); }
 };
 template <> struct Eight<float> {
+  static constexpr int HOLD = 4;
   float4 a, b;
   __device__ __forceinline__ void load(const float* p) {
     a = *reinterpret_cast<const float4*>(p);
@@ -39,11 +45,17 @@ template <> struct Eight<float> {
     f[0] = a.x, f[1] = a.y, f[2] = a.z, f[3] = a.w;
     f[4] = b.x, f[5] = b.y, f[6] = b.z, f[7] = b.w;
   }
+  __device__ __forceinline__ void most(uint32_t& m) const {
+    float f[8];
+    get(f);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(f[i]) & 0x7fffffffu);
+  }
+  static __device__ __forceinline__ uint32_t bits(uint32_t m) { return m; }
 };
 
 // The exponent of the smallest power of two s with most <= 448 s = 1.75 2^8 s.
-__device__ __forceinline__ float scale_for(float most) {
-  const uint32_t u = __float_as_uint(most);
+__device__ __forceinline__ float scale_for(uint32_t u) {  // (bits of most)
   const int e = (int)(u >> 23) - 127 - 8 + ((u & 0x7fffffu) > 0x600000u ? 1 : 0);
   return __uint_as_float((uint32_t)(min(max(e, -60), 60) + 127) << 23);
 }
@@ -59,11 +71,15 @@ struct Rows8 {
 };
 
 // A CTA takes 8 / WPT tasks of one piece, WPT warps each; a task is K or V of one head.
-// d / 8 lanes a row.  The rows of up to kHold steps stay in registers between the
-// pass that finds the scale and the one that writes; longer pieces are read again (L1).
+// d / 8 lanes a row.  The rows of up to HOLD steps stay in registers between the pass that
+// finds the scale and the one that writes; longer pieces are read again.  Elements that are not finite are
+// looked for only where the largest magnitude is one.
+// Bound by instruction slots: a warp's way to its rows (lengths, page, scale: 300 instructions) and about 60 for
+// 16 rows' bytes a lane.  As few warps a task as hold its rows.
 template <typename T, int WPT>
-__global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8View kv, int heads, int d) {
-  __shared__ float most_w[kWarps];
+__global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8View kv, int heads, int d, int per_lane) {
+  constexpr int HOLD = Eight<T>::HOLD;
+  __shared__ uint32_t most_w[kWarps];
   pdl_trigger();
   pdl_wait();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -106,22 +122,16 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
   const int pg = r.table[(int64_t)b * r.table_stride + page];  // on its way while the rows are asked for
   const bool live = task < 2 * heads;  // (a warp without a task still meets the barrier)
   const int w = task >= heads, h = live ? task - w * heads : 0;
-  const int lpr = d / 8, rpw = 32 / lpr, mine = lane / lpr, col = (lane - mine * lpr) * 8;
+  // (lane / lpr as lane per_lane / 2^16)
+  const int lpr = d / 8, rpw = 32 * per_lane >> 16, mine = lane * per_lane >> 16, col = (lane - mine * lpr) * 8;
   const bool in = live && mine < rpw;
   const T* src = reinterpret_cast<const T*>(w ? x.x[1] : x.x[0]) + (int64_t)row0 * (w ? x.row[1] : x.row[0]) +
                  h * (w ? x.head[1] : x.head[0]) + col;
   const int64_t src_row = w ? x.row[1] : x.row[0];
   const int step = rpw * WPT, steps = (n + step - 1) / step, at = part * rpw + mine;
-  Eight<T> hold[kHold];
-  float most = 0.f;
-  auto look = [&](const Eight<T>& e) {
-    float f[8];
-    e.get(f);
+  Eight<T> hold[HOLD];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) most = fmaxf(most, nonfinite(f[i]) ? 0.f : fabsf(f[i]));
-  };
-#pragma unroll
-  for (int t = 0; t < kHold; ++t)
+  for (int t = 0; t < HOLD; ++t)
     if (in && at + t * step < n) hold[t].load(src + (at + t * step) * src_row);
   if (pg < 0 || pg >= kv.n_pages) {
     if (threadIdx.x == 0) flag_status(r.status, DFLASH_STATUS_PAGE);
@@ -129,23 +139,44 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
   }
   float* scale = (w ? kv.vs : kv.ks) + (int64_t)pg * kv.s_page + h * kv.s_head;
   const float old = s0 > 0 ? *scale : 0.f;
+  // f(element, slot) over this lane's rows
+  auto each = [&](auto f) {
 #pragma unroll
-  for (int t = 0; t < kHold; ++t)
-    if (in && at + t * step < n) look(hold[t]);
-#pragma unroll 4
-  for (int t = kHold; t < steps; ++t) {
-    Eight<T> e;
-    if (in && at + t * step < n) {
-      e.load(src + (int64_t)(at + t * step) * src_row);
-      look(e);
+    for (int t = 0; t < HOLD; ++t)
+      if (in && at + t * step < n) f(hold[t], at + t * step);
+#pragma unroll 2
+    for (int t = HOLD; t < steps; ++t)
+      if (in && at + t * step < n) {
+        Eight<T> e;
+        e.load(src + (int64_t)(at + t * step) * src_row);
+        f(e, at + t * step);
+      }
+  };
+  // the largest magnitude of the task's rows, over its warps
+  auto over_task = [&](uint32_t m) {
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (WPT > 1) {
+      __syncthreads();
+      if (lane == 0) most_w[warp] = m;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < WPT; ++i) m = max(m, most_w[warp - part + i]);
     }
-  }
-  most = warp_max(most);
-  if (WPT > 1) {
-    if (lane == 0) most_w[warp] = most;
-    __syncthreads();
+    return m;
+  };
+  uint32_t m = 0;
+  each([&](const Eight<T>& e, int) { e.most(m); });
+  uint32_t most = over_task(Eight<T>::bits(m));
+  const bool wild = most >= 0x7f800000u;
+  if (WPT > 1 ? __syncthreads_or(wild) : wild) {  // not finite: the largest of the others
+    uint32_t fin = 0;
+    each([&](const Eight<T>& e, int) {
+      float f[8];
+      e.get(f);
 #pragma unroll
-    for (int i = 0; i < WPT; ++i) most = fmaxf(most, most_w[warp - part + i]);
+      for (int i = 0; i < 8; ++i) fin = max(fin, nonfinite(f[i]) ? 0u : __float_as_uint(f[i]) & 0x7fffffffu);
+    });
+    most = over_task(fin);
   }
   if (!live) return;
   const float now = s0 > 0 ? fmaxf(scale_for(most), old) : scale_for(most);
@@ -160,23 +191,27 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float q = exact ? f[i] * inv : f[i] / now;
-      f[i] = nonfinite(f[i]) ? __uint_as_float(0x7fffffffu) : q;
+      f[i] = wild && nonfinite(f[i]) ? __uint_as_float(0x7fffffffu) : q;
     }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
       c[i] = (uint32_t)f2_to_e4m3x2(f[4 * i], f[4 * i + 1]) | (uint32_t)f2_to_e4m3x2(f[4 * i + 2], f[4 * i + 3]) << 16;
-    *reinterpret_cast<uint2*>(dst + slot * kv.slot) = make_uint2(c[0], c[1]);
+    *reinterpret_cast<uint2*>(dst + (s0 + slot) * kv.slot) = make_uint2(c[0], c[1]);
   };
+  if (exact && !wild) {
+    each([&](const Eight<T>& e, int slot) {
+      float f[8];
+      e.get(f);
+      uint32_t c[2];
 #pragma unroll
-  for (int t = 0; t < kHold; ++t)
-    if (in && at + t * step < n) write(hold[t], s0 + at + t * step);
-#pragma unroll 2
-  for (int t = kHold; t < steps; ++t)
-    if (in && at + t * step < n) {
-      Eight<T> e;
-      e.load(src + (int64_t)(at + t * step) * src_row);
-      write(e, s0 + at + t * step);
-    }
+      for (int i = 0; i < 2; ++i)
+        c[i] = (uint32_t)f2_to_e4m3x2(f[4 * i] * inv, f[4 * i + 1] * inv) |
+               (uint32_t)f2_to_e4m3x2(f[4 * i + 2] * inv, f[4 * i + 3] * inv) << 16;
+      *reinterpret_cast<uint2*>(dst + (s0 + slot) * kv.slot) = make_uint2(c[0], c[1]);
+    });
+  } else {
+    each(write);
+  }
   if (s0 > 0 && now != old) {
     // the rows in front of the new ones: their codes at the new scale
     const float f = old / now;
@@ -197,17 +232,17 @@ cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads
   const int64_t pieces = (int64_t)(r.total >> kv.page_shift) + 2ll * std::min(r.batch, r.total);
   const int per = kWarps / WPT;
   return launch_k(k_kv8_append<T, WPT>, dim3((unsigned)std::min<int64_t>(pieces, r.total), (2 * heads + per - 1) / per),
-                  kThreads, 0, st, r, x, kv, heads, d);
+                  kThreads, 0, st, r, x, kv, heads, d, 65536 / (d / 8) + 1);
 }
 template <typename T>
 cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads, int d, cudaStream_t st) {
-  // warps a task: as many as its rows, those of a full page or the average sequence's, keep busy for one or
-  // two steps
+  // warps a task: as few as hold its rows, those of a full page or the average sequence's, in registers
+  constexpr int HOLD = Eight<T>::HOLD;
   const int rows = std::min(1 << kv.page_shift, std::max(1, r.total / r.batch)), steps = (rows * d / 8 + 31) / 32;
-  return steps <= 2   ? launch<T, 1>(r, x, kv, heads, d, st)
-         : steps <= 4 ? launch<T, 2>(r, x, kv, heads, d, st)
-         : steps <= 8 ? launch<T, 4>(r, x, kv, heads, d, st)
-                      : launch<T, 8>(r, x, kv, heads, d, st);
+  return steps <= HOLD       ? launch<T, 1>(r, x, kv, heads, d, st)
+         : steps <= 2 * HOLD ? launch<T, 2>(r, x, kv, heads, d, st)
+         : steps <= 4 * HOLD ? launch<T, 4>(r, x, kv, heads, d, st)
+                             : launch<T, 8>(r, x, kv, heads, d, st);
 }
 
 }  // namespace

@@ -14,16 +14,6 @@
 namespace dfl {
 namespace {
 
-// n / d as n m / 2^32 with m = floor(2^32 / d) + 1: m is above 2^32 / d by at most 1, the quotient by
-// less than n / 2^32, which does not reach the next whole number as long as n d < 2^32.  (Here n < 2^21
-// and d <= 2^8, or n < 2^13 and d <= 2^11.)
-struct FastDiv {
-  uint32_t m;
-  int32_t d;
-};
-FastDiv fast_div_of(int d) { return FastDiv{(uint32_t)(((uint64_t)1 << 32) / (uint32_t)d + 1), d}; }
-__device__ __forceinline__ int fast_div(int n, const FastDiv& f) { return f.d == 1 ? n : (int)__umulhi((uint32_t)n, f.m); }
-
 struct RopeSide {
   const void* x;
   void* y;
@@ -34,7 +24,6 @@ struct RopeCall {
   int32_t heads[2];
   int32_t d, rot, off, copy;  // copy: the elements that pass through are written too
   float amplitude, sign;
-  FastDiv per, all_heads;  // by a head's tasks, and by the heads of a row
 };
 struct RopeTurns {
   uint64_t t[DFLASH_ROPE_MAX_DIM / 2];
@@ -51,18 +40,47 @@ struct Vec {
   typename Raw<V * (int)sizeof(T)>::type raw;
   __device__ __forceinline__ void load(const T* p) { raw = *reinterpret_cast<const decltype(raw)*>(p); }
   __device__ __forceinline__ void store(T* p) const { *reinterpret_cast<decltype(raw)*>(p) = raw; }
-  __device__ __forceinline__ float get(int i) const { return to_f<T>(reinterpret_cast<const T*>(&raw)[i]); }
-  __device__ __forceinline__ void set(int i, float v) { reinterpret_cast<T*>(&raw)[i] = from_f<T>(v); }
+  __device__ __forceinline__ void get(float* f) const {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) f[i] = reinterpret_cast<const float*>(&raw)[i];
+    } else if constexpr (V == 1) {
+      f[0] = __uint_as_float((uint32_t)raw << 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const uint32_t w = reinterpret_cast<const uint32_t*>(&raw)[i / 2];
+        f[i] = __uint_as_float(w << 16);
+        f[i + 1] = __uint_as_float(w & 0xffff0000u);
+      }
+    }
+  }
+  __device__ __forceinline__ void set(const float* f) {
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) reinterpret_cast<float*>(&raw)[i] = f[i];
+    } else if constexpr (V == 1) {
+      raw = __bfloat16_as_ushort(__float2bfloat16_rn(f[0]));
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; i += 2) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(f[i], f[i + 1]);
+        reinterpret_cast<uint32_t*>(&raw)[i / 2] = *reinterpret_cast<const uint32_t*>(&b);
+      }
+    }
+  }
 };
 
-// RPC rows per CTA: cos and sin of a row are worked out once, by as many threads as
-// there are pairs, and serve all its heads from shared memory.  A thread then takes V
-// elements (half layout: V of each half) at a time.
-// Bound by memory: one read and one write of the rotated heads.
+// RPC rows per CTA: cos and sin of a row are worked out once, by as many threads as there are pairs, and serve
+// all its heads from shared memory.  A thread has one place of a head (V elements; in the half layout V of
+// each half) and goes through (row, head) pairs `step` apart, U of them in flight: no index is divided,
+// and what it needs of cos and sin is two to four 16-byte loads.
+// Bound by memory traffic and by instruction slots about alike: 10300 rows of 40 heads of 128, half of
+// a head rotated: 211 MB.
 constexpr int kRopeThreads = 256;
 template <typename T, int V, bool IL, int RPC>
 __global__ void __launch_bounds__(kRopeThreads) k_rope(Ragged r, RopeCall c, const __grid_constant__ RopeTurns turns) {
-  __shared__ float2 cs[RPC * (DFLASH_ROPE_MAX_DIM / 2)];
+  __shared__ __align__(16) float2 cs[RPC * (DFLASH_ROPE_MAX_DIM / 2)];
   __shared__ int pos[RPC];
   pdl_trigger();
   pdl_wait();
@@ -90,53 +108,69 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(Ragged r, RopeCall c, con
     cs[e] = make_float2(cn * c.amplitude, sn * c.amplitude * c.sign);
   }
   __syncthreads();
-  const int turned = IL ? c.rot / V : half / V, passed = c.copy ? (c.d - c.rot) / V : 0, per = turned + passed;
-  const int heads = c.heads[0] + c.heads[1], tasks = RPC * heads * per;
-  // U tasks of a thread at a time: their loads are in flight together
-  constexpr int U = RPC == 1 ? 2 : 4;
-  for (int e0 = tid; e0 < tasks; e0 += U * kRopeThreads) {
+  constexpr int U = 4, P = IL ? V / 2 : V;  // pairs of a vector
+  const int turned = IL ? c.rot / V : half / V, per = turned + (c.copy ? (c.d - c.rot) / V : 0);
+  const int heads = c.heads[0] + c.heads[1], step = kRopeThreads / per, h0 = tid / per, j = tid - h0 * per;
+  if (h0 >= step) return;
+  const bool turns_here = j < turned;
+  int at = (j - turned) * V;  // elements in front of the rotated part, or behind it
+  if (turns_here) at = c.off + j * V;
+  else if (at >= c.off) at += c.rot;
+  int k = h0 / heads, h = h0 - k * heads;  // row and head of the next vector
+  while (k < RPC) {
     Vec<T, V> a[U], b[U];
-    const T* x[U];
     T* y[U];
-    int cs_at[U];  // where the pair's cos and sin begin, -1: passes through, -2: nothing to do
+    int row[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int e = e0 + u * kRopeThreads;
-      cs_at[u] = -2;
-      if (e >= tasks) continue;
-      const int hh = fast_div(e, c.per), j = e - hh * per, k = fast_div(hh, c.all_heads), h = hh - k * heads;
-      if (pos[k] < 0) continue;
-      const int w = h >= c.heads[0], g = w ? h - c.heads[0] : h;
-      const RopeSide s = w ? c.side[1] : c.side[0];
-      int at = (j - turned) * V;  // in front of the rotated part, or behind it
-      if (j < turned) at = c.off + j * V;
-      else if (at >= c.off) at += c.rot;
-      x[u] = reinterpret_cast<const T*>(s.x) + (int64_t)(row0 + k) * s.x_row + g * s.x_head + at;
-      y[u] = reinterpret_cast<T*>(s.y) + (int64_t)(row0 + k) * s.y_row + g * s.y_head + at;
-      cs_at[u] = j >= turned ? -1 : k * half + j * (IL ? V / 2 : V);
-      a[u].load(x[u]);
-      if (!IL && j < turned) b[u].load(x[u] + half);
+      row[u] = k < RPC && pos[min(k, RPC - 1)] >= 0 ? k : -1;
+      if (row[u] >= 0) {
+        const int w = h >= c.heads[0], g = w ? h - c.heads[0] : h;
+        const T* x = reinterpret_cast<const T*>(w ? c.side[1].x : c.side[0].x) +
+                     (int64_t)(row0 + k) * (w ? c.side[1].x_row : c.side[0].x_row) + g * (w ? c.side[1].x_head : c.side[0].x_head) + at;
+        y[u] = reinterpret_cast<T*>(w ? c.side[1].y : c.side[0].y) +
+               (int64_t)(row0 + k) * (w ? c.side[1].y_row : c.side[0].y_row) + g * (w ? c.side[1].y_head : c.side[0].y_head) + at;
+        a[u].load(x);
+        if (!IL && turns_here) b[u].load(x + half);
+      }
+      h += step;
+      while (h >= heads) {
+        h -= heads;
+        ++k;
+      }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      if (cs_at[u] == -2) continue;
-      if (cs_at[u] >= 0) {
-        if (IL) {
+      if (row[u] < 0) continue;
+      if (turns_here) {
+        float2 t[P];
+        const float2* src = cs + row[u] * half + j * P;
+        if constexpr (P % 2 == 0) {  // (then half is even too)
 #pragma unroll
-          for (int q = 0; q < V / 2; ++q) {
-            const float2 t = cs[cs_at[u] + q];
-            const float p = a[u].get(2 * q), v = a[u].get(2 * q + 1);
-            a[u].set(2 * q, p * t.x - v * t.y);
-            a[u].set(2 * q + 1, v * t.x + p * t.y);
-          }
+          for (int q = 0; q < P; q += 2) *reinterpret_cast<float4*>(t + q) = *reinterpret_cast<const float4*>(src + q);
         } else {
 #pragma unroll
-          for (int q = 0; q < V; ++q) {
-            const float2 t = cs[cs_at[u] + q];
-            const float p = a[u].get(q), v = b[u].get(q);
-            a[u].set(q, p * t.x - v * t.y);
-            b[u].set(q, v * t.x + p * t.y);
+          for (int q = 0; q < P; ++q) t[q] = src[q];
+        }
+        float f[V], g[V];
+        a[u].get(f);
+        if constexpr (IL) {
+#pragma unroll
+          for (int q = 0; q < P; ++q) {
+            g[2 * q] = f[2 * q] * t[q].x - f[2 * q + 1] * t[q].y;
+            g[2 * q + 1] = f[2 * q + 1] * t[q].x + f[2 * q] * t[q].y;
           }
+          a[u].set(g);
+        } else {
+          b[u].get(g);
+#pragma unroll
+          for (int q = 0; q < V; ++q) {
+            const float p = f[q] * t[q].x - g[q] * t[q].y;
+            g[q] = g[q] * t[q].x + f[q] * t[q].y;
+            f[q] = p;
+          }
+          a[u].set(f);
+          b[u].set(g);
           b[u].store(y[u] + half);
         }
       }
@@ -146,12 +180,10 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(Ragged r, RopeCall c, con
 }
 
 template <typename T, int V, bool IL>
-cudaError_t launch_rope(const Ragged& r, RopeCall c, const RopeTurns& t, cudaStream_t st) {
-  c.per = fast_div_of((IL ? c.rot / V : c.rot / 2 / V) + (c.copy ? (c.d - c.rot) / V : 0));
-  c.all_heads = fast_div_of(c.heads[0] + c.heads[1]);
+cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, cudaStream_t st) {
   // few rows: one a CTA, so that they spread over the SMs
   if (r.total <= 608) return launch_k(k_rope<T, V, IL, 1>, (unsigned)r.total, kRopeThreads, 0, st, r, c, t);
-  return launch_k(k_rope<T, V, IL, 4>, (unsigned)((r.total + 3) / 4), kRopeThreads, 0, st, r, c, t);
+  return launch_k(k_rope<T, V, IL, 8>, (unsigned)((r.total + 7) / 8), kRopeThreads, 0, st, r, c, t);
 }
 template <typename T>
 cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, bool il, cudaStream_t st) {
