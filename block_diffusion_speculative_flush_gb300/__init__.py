@@ -744,6 +744,17 @@ def dflash_token_logprobs(logits: torch.Tensor, tokens: torch.Tensor, logprobs: 
 # ---------------------------------------------------------------------------
 # the compressed cache
 # ---------------------------------------------------------------------------
+def _vector(t: torch.Tensor, n: int, what: str) -> int:
+    """The address of a contiguous int32 vector of n (a tensor that _same_device has seen)."""
+    if t.dtype is not torch.int32 or t.shape != (n,) or not t.is_contiguous():
+        raise ValueError(f"{what}: a contiguous CUDA int32 vector of {n}")
+    return t.data_ptr()
+
+
+def _word(t) -> int:
+    return 0 if t is None else _vector(t, 1, "status")
+
+
 _ROPE_LAYOUTS = {"half": 0, "interleaved": 1}
 _ROPE_SCALINGS = {"linear": 1, "ntk": 2, "bands": 3, "yarn": 4}
 
@@ -783,11 +794,9 @@ def dflash_rope_table(rot_dim: int, theta: float, layout: str = "half", scaling:
 
 
 def _rope_ragged(starts, lens, total: int, status) -> bytes:
-    first = _int_vector(starts, None, "starts [batch + 1]")
-    batch = starts.shape[0] - 1
-    word = 0 if status is None else _int_vector(status, 1, "status")
-    return _abi.PACK_RAGGED(batch, total, 1 << 24, 1 << 30, first, 0 if lens is None else _int_vector(lens, batch, "lens"),
-                            0, 0, 0, word)
+    batch = starts.numel() - 1
+    return _abi.PACK_RAGGED(batch, total, 1 << 24, 1 << 30, _vector(starts, batch + 1, "starts [batch + 1]"),
+                            0 if lens is None else _vector(lens, batch, "lens"), 0, 0, 0, _word(status))
 
 
 def dflash_rope(table: RopeTable, q: torch.Tensor | None, k: torch.Tensor | None, starts: torch.Tensor,
@@ -928,29 +937,29 @@ def _page_rows(table: torch.Tensor, lens: torch.Tensor, page_size: int, what: st
     if table.dtype != torch.int32 or len(shape) != 2 or (st[1] != 1 and shape[1] > 1):
         raise ValueError(f"{what}table: CUDA int32 [rows, pages of a row] with a dense last dimension")
     return _abi.PACK_ROWS(shape[0], shape[1], st[0] if shape[0] > 1 else shape[1], page_size, table.data_ptr(),
-                          _int_vector(lens, shape[0], f"{what}lens"))
+                          _vector(lens, shape[0], f"{what}lens"))
 
 
-def _pages_workspace(workspace, n_pages: int, rows: int, device: int, stream):
+def _pages_workspace(workspace, n_pages: int, rows: int, like: torch.Tensor, stream):
     if workspace is not None:
         if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous():
             raise ValueError("workspace: a contiguous CUDA uint8 tensor")
         return workspace
     need = _check(lib.dflash_pages_workspace(n_pages, rows))
     if stream is None:
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
     with torch.cuda.stream(stream):
-        return torch.empty(need, dtype=torch.uint8, device=device)
+        return torch.empty(need, dtype=torch.uint8, device=like.device)
 
 
 def dflash_pages_copy(buffers: PageBuffers, src: torch.Tensor, dst: torch.Tensor, status=None, stream=None) -> None:
     """Copies page src[i] to page dst[i] (int32) in every buffer."""
     device = _same_device(src, dst, buffers.tensors[0], status)
-    n = src.shape[0] if src.dim() == 1 else -1
-    s, t = _int_vector(src, None, "src"), _int_vector(dst, n, "dst")
+    n = src.numel()
+    s, t = _vector(src, n, "src"), _vector(dst, n, "dst")
     with _on_device(device):
         _check(lib.dflash_pages_copy(buffers.packed, buffers.count, buffers.n_pages, s, t, n,
-                                     0 if status is None else _int_vector(status, 1, "status"), _stream_of(stream, device)))
+                                     _word(status), _stream_of(stream, device)))
 
 
 def dflash_pages_reorder(refs: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, parents: torch.Tensor,
@@ -960,10 +969,11 @@ def dflash_pages_reorder(refs: torch.Tensor, table: torch.Tensor, lens: torch.Te
     and lens; refs (int32 [n_pages]) follows.  A row named twice is forked, one that is not named is freed."""
     device = _same_device(refs, table, lens, parents, new_table, new_lens, status)
     a, b = _page_rows(table, lens, page_size, ""), _page_rows(new_table, new_lens, page_size, "new_")
+    n_pages = refs.numel()
     with _on_device(device):
-        _check(lib.dflash_pages_reorder(_int_vector(refs, None, "refs"), refs.shape[0], a,
-                                        _int_vector(parents, new_table.shape[0], "parents"), b,
-                                        0 if status is None else _int_vector(status, 1, "status"),
+        _check(lib.dflash_pages_reorder(_vector(refs, n_pages, "refs [n_pages]"), n_pages, a,
+                                        _vector(parents, new_table.shape[0], "parents"), b,
+                                        _word(status),
                                         _stream_of(stream, device)))
 
 
@@ -975,17 +985,17 @@ def dflash_pages_resize(refs: torch.Tensor, table: torch.Tensor, lens: torch.Ten
     device = _same_device(refs, table, lens, new_lens, free_pages, workspace, status,
                           None if buffers is None else buffers.tensors[0])
     rows = _page_rows(table, lens, page_size, "")
-    n_pages = refs.shape[0] if refs.dim() == 1 else 0
+    n_pages = refs.numel()
     if buffers is not None and buffers.n_pages != n_pages:
         raise ValueError("refs: int32 [n_pages] of the buffers' pool")
     with _on_device(device):
-        ws = _pages_workspace(workspace, n_pages, table.shape[0], device, stream)
-        _check(lib.dflash_pages_resize(_int_vector(refs, None, "refs"), n_pages, rows,
-                                       _int_vector(new_lens, table.shape[0], "new_lens"),
+        ws = _pages_workspace(workspace, n_pages, table.shape[0], refs, stream)
+        _check(lib.dflash_pages_resize(_vector(refs, n_pages, "refs [n_pages]"), n_pages, rows,
+                                       _vector(new_lens, table.shape[0], "new_lens"),
                                        None if buffers is None else buffers.packed, 0 if buffers is None else buffers.count,
-                                       0 if free_pages is None else _int_vector(free_pages, 1, "free_pages"),
+                                       0 if free_pages is None else _vector(free_pages, 1, "free_pages"),
                                        ws.data_ptr(), ws.numel(),
-                                       0 if status is None else _int_vector(status, 1, "status"),
+                                       _word(status),
                                        _stream_of(stream, device)))
 
 
@@ -998,19 +1008,19 @@ def dflash_pages_compact(refs: torch.Tensor, table: torch.Tensor, lens: torch.Te
     new_lens = lens if new_lens is None else new_lens
     device = _same_device(refs, table, lens, new_refs, new_table, new_lens, used, workspace, status,
                           None if buffers is None else buffers.tensors[0])
-    n_pages = refs.shape[0] if refs.dim() == 1 else 0
+    n_pages = refs.numel()
     if buffers is not None and buffers.n_pages != n_pages:
         raise ValueError("refs: int32 [n_pages] of the buffers' pool")
     if new_table.shape != table.shape:
         raise ValueError("new_table: the shape of table")
     a, b = _page_rows(table, lens, page_size, ""), _page_rows(new_table, new_lens, page_size, "new_")
     with _on_device(device):
-        ws = _pages_workspace(workspace, n_pages, table.shape[0], device, stream)
-        _check(lib.dflash_pages_compact(_int_vector(refs, None, "refs"), _int_vector(new_refs, n_pages, "new_refs"),
+        ws = _pages_workspace(workspace, n_pages, table.shape[0], refs, stream)
+        _check(lib.dflash_pages_compact(_vector(refs, n_pages, "refs [n_pages]"), _vector(new_refs, n_pages, "new_refs"),
                                         n_pages, a, b, None if buffers is None else buffers.packed,
                                         0 if buffers is None else buffers.count,
-                                        0 if used is None else _int_vector(used, 1, "used"), ws.data_ptr(), ws.numel(),
-                                        0 if status is None else _int_vector(status, 1, "status"),
+                                        0 if used is None else _vector(used, 1, "used"), ws.data_ptr(), ws.numel(),
+                                        _word(status),
                                         _stream_of(stream, device)))
 
 

@@ -183,7 +183,7 @@ template <typename T, int V, bool IL>
 cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, cudaStream_t st) {
   // few rows: one a CTA, so that they spread over the SMs
   if (r.total <= 608) return launch_k(k_rope<T, V, IL, 1>, (unsigned)r.total, kRopeThreads, 0, st, r, c, t);
-  return launch_k(k_rope<T, V, IL, 8>, (unsigned)((r.total + 7) / 8), kRopeThreads, 0, st, r, c, t);
+  return launch_k(k_rope<T, V, IL, 4>, (unsigned)((r.total + 3) / 4), kRopeThreads, 0, st, r, c, t);
 }
 template <typename T>
 cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, bool il, cudaStream_t st) {
