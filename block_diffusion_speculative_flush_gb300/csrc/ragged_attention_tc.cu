@@ -108,9 +108,13 @@ struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
   // 128 bytes of 32 rows for each softmax warp (NQ = 1: in the Q tile it has done with)
   static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;
-  static constexpr int CODES = KV8 ? 2 * KT * D : 0;      // a K and a V tile on their way to the converters
-  static constexpr int RING = (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
-  static constexpr int DATA = (RING + 2) * SLOT + STAGE + CODES;  // 224 KB
+  // 8 bits: tiles of codes on their way to the converters, K and V, or only V where K is multiplied as it is (K8:
+  // its tiles are 3 of the ring's entries then, V's as fp16 the other 2)
+  static constexpr bool K8 = KV8 && D == 128;
+  static constexpr int CODES = K8 ? KT * D : KV8 ? 2 * KT * D : 0;
+  static constexpr int RING = K8 ? 5 : (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
+  static constexpr int RING_BYTES = K8 ? 3 * KT * D + 2 * SLOT : RING * SLOT;
+  static constexpr int DATA = 2 * SLOT + RING_BYTES + STAGE + CODES;  // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
   // NQ = 2: registers of the softmax warps and of the other four; the launch's
   // 168 for all spilled 100 bytes in the key loop (452 -> 424 us for the packed
@@ -656,6 +660,59 @@ __device__ __forceinline__ int q_to_h16(uint8_t* row, int block, int swizzle) {
   return e;
 }
 
+// A row of a Q tile as above into two e4m3 pieces q1 + q2 (each a tile of its own, one in each 64-element
+// block's place): 2^e q with its largest finite element in [2^7, 2^8), q1 its nearest code, q2 the code of what
+// is left.  A code has 4 significant bits and a bf16 number 8, so the sum is exact for elements down to
+// 2^-10 of the largest; smaller ones are off by at most 2^-18 of that.  Not finite: NaN.  Returns e.
+template <int D>
+__device__ __forceinline__ int q_to_e4m3(uint8_t* row, int block, int swizzle) {
+  static_assert(D == 128, "a piece is a row of 128 bytes");
+  uint4 u[D / 8];
+  uint32_t most2 = 0;
+#pragma unroll
+  for (int c = 0; c < D / 8; ++c) {
+    u[c] = *reinterpret_cast<const uint4*>(row + c / 8 * block + (((c & 7) ^ swizzle) << 4));
+    const uint32_t v[4] = {u[c].x, u[c].y, u[c].z, u[c].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const uint32_t a = v[k] & 0x7fff7fffu;
+      most2 = __vmaxu2(most2, a & ~((nonfinite_bits(a) >> 15) * 0xffffu));
+    }
+  }
+  const uint32_t most = max(most2 & 0xffffu, most2 >> 16);
+  const int e = most ? 7 - ilogbf(__uint_as_float(most << 16)) : 0, e0 = e / 2;
+  const float f0 = ldexpf(1.f, e0), f1 = ldexpf(1.f, e - e0);
+#pragma unroll
+  for (int c = 0; c < D / 16; ++c) {  // 16 elements: a chunk of each piece
+    uint32_t p1[4], p2[4];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const uint4 w4 = u[2 * c + k / 4];
+      const uint32_t w = k % 4 == 0 ? w4.x : k % 4 == 1 ? w4.y : k % 4 == 2 ? w4.z : w4.w;
+      float x = __uint_as_float(w << 16) * f0 * f1, y = __uint_as_float(w & 0xffff0000u) * f0 * f1;
+      // (a conversion saturates: infinities by hand)
+      x = nonfinite(x) ? __uint_as_float(0x7fffffffu) : x;
+      y = nonfinite(y) ? __uint_as_float(0x7fffffffu) : y;
+      const uint32_t c1 = f2_to_e4m3x2(x, y);
+      uint32_t lo, hi;
+      e4m3x4_to_h4(c1, lo, hi);
+      const float2 r = __half22float2(*reinterpret_cast<const __half2*>(&lo));
+      const uint32_t c2 = f2_to_e4m3x2(x - r.x, y - r.y);
+      if (k & 1) {
+        p1[k / 2] |= c1 << 16;
+        p2[k / 2] |= c2 << 16;
+      } else {
+        p1[k / 2] = c1;
+        p2[k / 2] = c2;
+      }
+    }
+    const int at = (c ^ swizzle) << 4;
+    *reinterpret_cast<uint4*>(row + at) = make_uint4(p1[0], p1[1], p1[2], p1[3]);
+    *reinterpret_cast<uint4*>(row + block + at) = make_uint4(p2[0], p2[1], p2[2], p2[3]);
+  }
+  return e;
+}
+
 template <int D, int NQ, bool KV8>
 __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     k_ragged_tc(Ragged r, AttnCall a, typename std::conditional<KV8, Kv8View, KVView>::type kv, Plan p, const __grid_constant__ CUtensorMap mq,
@@ -667,7 +724,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   extern __shared__ __align__(1024) uint8_t smem[];
   uint8_t* sQ = smem;
   uint8_t* sR = sQ + 2 * SLOT;
-  uint8_t* sS = sR + RING * SLOT;
+  uint8_t* sS = sR + C::RING_BYTES;
   uint64_t* full = (uint64_t*)(sS + C::STAGE + C::CODES);
   uint64_t* empty = full + RING;
   uint64_t* v_fix = empty + RING;
@@ -692,6 +749,14 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
+  // entry i of the ring (K tiles even, V tiles odd): its slot, how often that was used before, where it lies
+  constexpr bool K8 = C::K8;
+  auto r_slot = [](uint32_t i) { return K8 ? ((i & 1u) ? 3u + ((i >> 1) & 1u) : (i >> 1) % 3u) : i % RING; };
+  auto r_use = [](uint32_t i) { return K8 ? ((i & 1u) ? i >> 2 : (i >> 1) / 3u) : i / RING; };
+  auto r_addr = [&](uint32_t slot) {
+    if (K8) return sR + (slot < 3u ? slot * (KT * D) : 3u * (KT * D) + (slot - 3u) * SLOT);
+    return sR + slot * SLOT;
+  };
 
   if (tid == 0) {
     for (int s = 0; s < RING; ++s) {
@@ -743,7 +808,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     if constexpr (KV8) {
       // ---- converters: tiles of codes, which come by TMA, as fp16 into the ring.  A thread has 16 codes
       // of each of N keys.
-      constexpr int PIECES = D / 16, KEYS = 64 / PIECES, N = KT / KEYS, H = 8;  // H pieces at a time
+      constexpr int PIECES = D / 16, KEYS = 64 / PIECES, N = KT / KEYS, H = 2;  // H pieces at a time (188 us; 4: 191, 8: 198)
       const int cw = warp == SW ? 0 : 1, ct = cw * 32 + lane, piece = ct % PIECES, key = ct / PIECES;
       r.table = after_wait(r.table);
       uint32_t it = 0, c_use = 0;
@@ -790,35 +855,58 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           ahead = entry_of(1);
           look_up(0, first);
         }
-        // K and V tiles in turn by the same few instructions (unrolled over both they were fetched anew each time)
-#pragma unroll 1
-        for (int u = 0; u < 2 * T; ++u) {
-          const int t = u >> 1, v = u & 1, kt = (tile0 + t) * KT;
-          const uint32_t e = it + u;
-          // the ring's entry is free, and the codes are there
-          if ((e >= (uint32_t)RING && !__all_sync(0xffffffffu, mbar_wait(&empty[e % RING], (e / RING - 1) & 1u, abort_flag))) ||
-              !__all_sync(0xffffffffu, mbar_wait(&c_full[v], c_use & 1u, abort_flag))) {
+        auto wait_empty = [&](uint32_t e) {
+          return r_use(e) == 0 || __all_sync(0xffffffffu, mbar_wait(&empty[r_slot(e)], (r_use(e) - 1) & 1u, abort_flag));
+        };
+        // The scales of tile t, for whoever sees its S: written when the K tile's entry is free, and told with
+        // the tile (K8: as one of the two arrivals that it takes, the copy's being the other)
+        auto put_scales = [&](int t) {
+          TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
+          const float k0 = __shfl_sync(0xffffffffu, ks, 0), v0 = __shfl_sync(0xffffffffu, vs, 0);
+          const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks == k0 && vs == v0));
+          const float most = warp_max(lane < KT / 16 ? vs : 0.f);
+          if (lane < KT / 16) {
+            ts.ks[lane] = ks;
+            ts.vs[lane] = vs;
+          }
+          if (lane == 0) {
+            ts.most_v = most;
+            ts.mixed = mixed;
+          }
+          look_up(t + 1, ahead);
+          ahead = entry_of(t + 2);
+          if (K8) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[r_slot(it + 2 * t)]);
+          }
+        };
+        if (K8 && T > 0 && cw == 0) {
+          if (!wait_empty(it)) {
             ok = false;
             break;
           }
-          uint8_t* tile = sR + (e % RING) * SLOT;
-          if (v == 0) {
-            if (cw == 0) {
-              TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
-              const float k0 = __shfl_sync(0xffffffffu, ks, 0), v0 = __shfl_sync(0xffffffffu, vs, 0);
-              const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks == k0 && vs == v0));
-              const float most = warp_max(lane < KT / 16 ? vs : 0.f);
-              if (lane < KT / 16) {
-                ts.ks[lane] = ks;
-                ts.vs[lane] = vs;
-              }
-              if (lane == 0) {
-                ts.most_v = most;
-                ts.mixed = mixed;
-              }
-              look_up(t + 1, ahead);
-              ahead = entry_of(t + 2);
+          put_scales(0);
+        }
+        // K and V tiles in turn by the same few instructions (unrolled over both they were fetched anew each time)
+#pragma unroll 1
+        for (int u = K8 ? 1 : 0; u < 2 * T; u += K8 ? 2 : 1) {
+          const int t = u >> 1, v = u & 1, kt = (tile0 + t) * KT;
+          const uint32_t e = it + u;
+          if (K8 && cw == 0 && t + 1 < T) {
+            if (!wait_empty(e + 1)) {
+              ok = false;
+              break;
             }
+            put_scales(t + 1);
+          }
+          // the ring's entry is free, and the codes are there
+          if (!wait_empty(e) || !__all_sync(0xffffffffu, mbar_wait(&c_full[v], c_use & 1u, abort_flag))) {
+            ok = false;
+            break;
+          }
+          uint8_t* tile = r_addr(r_slot(e));
+          if (v == 0) {
+            if (cw == 0) put_scales(t);
           } else {
             ++c_use;
           }
@@ -830,7 +918,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           for (int i0 = 0; i0 < N; i0 += H) {
             uint4 q[H];
 #pragma unroll
-            for (int i = 0; i < H; ++i) q[i] = *reinterpret_cast<const uint4*>(sC + v * (KT * D) + ((i0 + i) * 64 + ct) * 16);
+            for (int i = 0; i < H; ++i) q[i] = *reinterpret_cast<const uint4*>(sC + (K8 ? 0 : v * (KT * D)) + ((i0 + i) * 64 + ct) * 16);
             if (edge) {
               uint32_t found = 0;
 #pragma unroll
@@ -855,7 +943,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&c_empty[v]);
-            mbar_arrive(&full[e % RING]);
+            mbar_arrive(&full[r_slot(e)]);
           }
         }
         it += 2 * T;
@@ -872,7 +960,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     int k = 0;
     bool ok = true;
     // 8 bits: this warp asks for the tiles too, Q and then K and V in turn (a copy per lane, the box of a page)
-    uint32_t q_use[2] = {0, 0}, c_use[2] = {0, 0};
+    uint32_t q_use[2] = {0, 0}, c_use[2] = {0, 0}, k_it = 0;  // (k_it: K8, the ring's entry of the next K tile)
     Work last;
     auto produce = [&](const Work& w) {
       if constexpr (KV8) {
@@ -895,16 +983,20 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           }
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * D;
           for (int v = 0; v < 2; ++v) {
-            if (c_use[v] > 0 && !__all_sync(0xffffffffu, mbar_wait(&c_empty[v], (c_use[v] - 1) & 1u, abort_flag))) {
+            const bool direct = K8 && v == 0;  // into the ring
+            uint64_t *const there = direct ? &full[r_slot(k_it)] : &c_full[v], *const free_ = direct ? &empty[r_slot(k_it)] : &c_empty[v];
+            const uint32_t use = direct ? r_use(k_it) : c_use[v];
+            if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(free_, (use - 1) & 1u, abort_flag))) {
               ok = false;
               return;
             }
-            if (lane == 0) mbar_expect_tx(&c_full[v], bytes);
+            uint8_t* const to = direct ? r_addr(r_slot(k_it)) : sC + (K8 ? 0 : v * (KT * D));
+            if (direct) k_it += 2;
+            else ++c_use[v];
+            if (lane == 0) mbar_expect_tx(there, bytes);
             __syncwarp();
-            ++c_use[v];
             if (mine)
-              tma_load_4d(sC + v * (KT * D) + box * page_rows * D, v ? &mv : &mk, &c_full[v], 0,
-                          kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
+              tma_load_4d(to + box * page_rows * D, v ? &mv : &mk, there, 0, kt & ((1 << kv.page_shift) - 1), w.kvh, pg);
             if (t == 0 && v == 0) {
               for (int x = 0; x < 2; ++x) {
                 if (w.nt[x] == 0) continue;
@@ -1070,6 +1162,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         while (c_use[x] > 0 && !mbar_try_wait(&c_full[x], (c_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
       }
+      for (uint32_t i = k_it > 6 ? k_it - 6 : 0; i < k_it; i += 2) {  // (K8: the arrival of its scales may be missing)
+        while (!mbar_try_wait(&full[r_slot(i)], r_use(i) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+        }
+      }
     }
   } else if (!KV8 && warp == SW) {
     if constexpr (!KV8) {
@@ -1185,19 +1281,28 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       if (ok && !__all_sync(0xffffffffu, mbar_wait(bar, parity & 1u, abort_flag))) ok = false;
       return ok;
     };
-    auto ring_full = [&](uint32_t i) { return wait(&full[i % RING], i / RING); };
+    auto ring_full = [&](uint32_t i) { return wait(&full[r_slot(i)], r_use(i)); };
+    // (8 bits: with one more stream of instructions in the SM, the converters', code is fetched anew all the
+    // time, and loops are faster: chunked prefill 188 -> 173 us)
+    constexpr int MMA_UNROLL = KV8 ? 1 : 8;
     auto issue_s = [&](int qbuf, uint32_t st, int sbuf) {
-      const uint32_t q0 = smem_u32(sQ + qbuf * SLOT), k0 = smem_u32(sR + st * SLOT), tS = tmem + sbuf * 128;
-#pragma unroll
-      for (int ks = 0; ks < D / 16; ++ks) {
+      const uint32_t q0 = smem_u32(sQ + qbuf * SLOT), k0 = smem_u32(r_addr(st)), tS = tmem + sbuf * 128;
+      if constexpr (K8) {  // both pieces of q (q_to_e4m3) times K's codes
+#pragma unroll 1
+        for (int ks = 0; ks < 2 * (D / 32); ++ks)
+          umma_e4m3_warp(tS, sdesc_sw128(q0 + ks / (D / 32) * (SLOT / NB) + ks % (D / 32) * 32),
+                         sdesc_sw128(k0 + ks % (D / 32) * 32), idS, ks > 0 ? 1u : 0u);
+      }
+#pragma unroll(MMA_UNROLL)
+      for (int ks = 0; ks < (K8 ? 0 : D / 16); ++ks) {
         umma_bf16_warp(tS, sdesc_sw128(q0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32),
                        sdesc_sw128(k0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
       }
       umma_commit_warp(&s_full[sbuf]);
     };
     auto issue_pv = [&](int x, uint32_t st, int sbuf, bool first) {
-      const uint32_t v0 = smem_u32(sR + st * SLOT), tP = tmem + sbuf * 128, tO = tmem + O_COL + x * D;
-#pragma unroll
+      const uint32_t v0 = smem_u32(r_addr(st)), tP = tmem + sbuf * 128, tO = tmem + O_COL + x * D;
+#pragma unroll(MMA_UNROLL)
       for (int ks = 0; ks < KT / 16; ++ks) {
         umma_bf16_ts_warp(tO, tP + ks * 8, sdesc_sw128_mn(v0 + ks * 2048, SLOT / NB), idPV, first && ks == 0 ? 0u : 1u);
       }
@@ -1243,13 +1348,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       if (nt == 0) return;
       if (NQ == 1) {
         if (!wait(&q_full[q_cnt0 & 1u], q_cnt0 >> 1) || !ring_full(ring)) return;
-        issue_s((int)(q_cnt0 & 1u), ring % RING, (int)(s_cnt & 1u));
-        umma_commit_warp(&empty[ring % RING]);
+        issue_s((int)(q_cnt0 & 1u), r_slot(ring), (int)(s_cnt & 1u));
+        umma_commit_warp(&empty[r_slot(ring)]);
         ++q_cnt0;
         ++s_cnt;
       } else {
         if (!wait(KV8 ? &q_ready[x] : &q_full[x], x ? q_cnt1 : q_cnt0) || !ring_full(ring)) return;
-        issue_s(x, ring % RING, x);
+        issue_s(x, r_slot(ring), x);
         if (x) ++q_cnt1;
         else ++q_cnt0;
       }
@@ -1264,7 +1369,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       bool more = false;
       for (int t = 0; t < w.T && ok; ++t) {
         const bool last = t + 1 == w.T;
-        const uint32_t iv = it + 2 * t + 1, ik = it + 2 * (t + 1), sv = iv % RING, sk = ik % RING;
+        const uint32_t iv = it + 2 * t + 1, ik = it + 2 * (t + 1), sv = r_slot(iv), sk = r_slot(ik);
         if (last) more = fetch(nx);
         if (NQ == 1) {
           // S of the next tile in the stream goes ahead of this tile's product
@@ -1285,7 +1390,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           ++pv_cnt0;
         } else {
           wait_v(w, t, iv);
-#pragma unroll
+#pragma unroll(KV8 ? 1 : 2)
           for (int x = 0; x < 2; ++x) {
             const int nt = x ? w.nt1 : w.nt0;
             uint32_t& cnt = x ? pv_cnt1 : pv_cnt0;
@@ -1421,7 +1526,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
             ok = false;
             break;
           }
-          row_sl2 = ldexpf(sl2, -q_to_h16<D>(sQ + x * SLOT + row * 128, SLOT / NB, row & 7));
+          uint8_t* const q_row = sQ + x * SLOT + row * 128;
+          if constexpr (K8) row_sl2 = ldexpf(sl2, -q_to_e4m3<D>(q_row, SLOT / NB, row & 7));
+          else row_sl2 = ldexpf(sl2, -q_to_h16<D>(q_row, SLOT / NB, row & 7));
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) mbar_arrive(&q_ready[x]);
@@ -1438,8 +1545,8 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         if (teller) {
           // S of this tile is through, and with it the product before it.  K
           // goes back with the later stream's S, V with its product.
-          if (x == 1 || t >= nt_other) mbar_arrive_relaxed(&empty[(it + 2 * t) % RING]);
-          if (t > 0 && (x == 1 || t > nt_other)) mbar_arrive_relaxed(&empty[(it + 2 * t - 1) % RING]);
+          if (x == 1 || t >= nt_other) mbar_arrive_relaxed(&empty[r_slot(it + 2 * t)]);
+          if (t > 0 && (x == 1 || t > nt_other)) mbar_arrive_relaxed(&empty[r_slot(it + 2 * t - 1)]);
           if (t + 1 == T) mbar_arrive_relaxed(&q_empty[x]);
         }
         // NQ = 1: every warp sees each of pv_done's phases, in order, before it
@@ -1474,7 +1581,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           ok = false;
           break;
         }
-        if (teller && (x == 1 || T > nt_other)) mbar_arrive_relaxed(&empty[(it + 2 * T - 1) % RING]);
+        if (teller && (x == 1 || T > nt_other)) mbar_arrive_relaxed(&empty[r_slot(it + 2 * T - 1)]);
         q_used = q_cnt;
         ++q_cnt;
         fence_after();
@@ -1926,8 +2033,9 @@ HostPlan make_plan(const Ragged& r, const AttnCall& a, int sms, bool kv8 = false
   return h;
 }
 
+enum Tile { kBf16, kCodes, kCodesSwizzled };
 cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-                   const cuuint32_t* box, bool codes = false) {
+                   const cuuint32_t* box, Tile tile = kBf16) {
   static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -1938,8 +2046,8 @@ cudaError_t encode(CUtensorMap* m, const void* base, int rank, const cuuint64_t*
   }();
   if (!fn) return cudaErrorNotSupported;
   const cuuint32_t one[4] = {1, 1, 1, 1};
-  return fn(m, codes ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank, const_cast<void*>(base), dims,
-            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, codes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+  return fn(m, tile == kBf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_UINT8, rank, const_cast<void*>(base), dims,
+            strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, tile == kCodes ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS
              ? cudaSuccess
              : cudaErrorInvalidValue;
@@ -1981,7 +2089,7 @@ cudaError_t launch_d8(const Ragged& r, const AttnCall& a, const Kv8View& kv, con
     // (the stride of a dimension of one entry is never used, but may not be 0)
     const cuuint64_t strides[3] = {(cuuint64_t)kv.slot, std::max<cuuint64_t>(kv.head, 16), std::max<cuuint64_t>(kv.page, 16)};
     const cuuint32_t box[4] = {(cuuint32_t)D, (cuuint32_t)std::min(1 << kv.page_shift, KT), 1, 1};
-    e = encode(&m[i], i ? kv.v : kv.k, 4, dims, strides, box, true);
+    e = encode(&m[i], i ? kv.v : kv.k, 4, dims, strides, box, i == 0 && Cfg<D, 2, true>::K8 ? kCodesSwizzled : kCodes);
   }
   if (e == cudaSuccess) e = launch_tc<D, 2, true>(r, a, kv, h.p, sms, mq, m[0], m[1], st);
   if (e != cudaSuccess || !h.merge) return e;
