@@ -1,10 +1,9 @@
 // Attention of few rows (single tokens, verified blocks) over an 8-bit paged cache:
 // bf16, head_dim 64 or 128.
 //
-// Bound by the stream of codes, so nothing of a code's way is wasted: a lane copies
-// (cp.async) the very bytes that it multiplies, into a ring of its own, and no two lanes
-// ever wait for one another's.  That works because a contraction may take its index in any
-// order and a result its rows in any order:
+// A warp copies its chunks of 16 keys (cp.async) into a ring of its own and waits for no other
+// warp; each lane multiplies 16 bytes of each row that its place in the fragments has.  That works
+// because a contraction may take its index in any order and a result its rows in any order:
 //   S^T = K Q^T   A = 16 keys of K: lane (g, t) of the m16n8k16 fragment holds keys g and
 //                 g + 8 at any 4 d's per step, here 16 bytes in a row of each
 //   O^T = V^T P^T A = V^T, 16 d's by 16 keys: lane (g, t) holds keys 2t, 2t + 1, 2t + 8, 2t + 9 at
@@ -79,14 +78,11 @@ __device__ __forceinline__ float ex2(float x) {
 }
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 template <int N> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src) {
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], %2;" ::"r"(dst), "l"(src), "n"(N) : "memory");
 }
 template <int N> __device__ __forceinline__ void cp_async(uint32_t dst, const void* src, bool there) {
   // (size 0: zeros, the address is not looked at)
-  const int n = there ? N : 0;
-  if constexpr (N == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  asm volatile("cp.async.cg.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(there ? N : 0) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -223,11 +219,21 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       }
       scales[i % C::SCALES] = make_float2(ks, vs);
     };
-    // this lane's pieces: of K rows g and g + 8, of V rows 2t, 2t + 1, 2t + 8, 2t + 9
-    const uint8_t* k_base = kv.k + kvh * kv.head + g * kv.slot + 16 * t;
-    const uint8_t* v_base = kv.v + kvh * kv.head + 2 * t * kv.slot + VB * g;
-    const int64_t slot8 = 8 * kv.slot;
-    const uint32_t k_dst = smem_addr(ring) + lane * 16, v_dst = smem_addr(ring) + kChunk * D + lane * VB;
+    // What this lane copies: 16 bytes of every RI-th row, as many lanes side by side as a row has, so that memory
+    // sees whole rows (32 bytes of four rows in eight lanes, the pieces that a lane multiplies, reached half the
+    // rate).  Row r's 16-byte chunk c lies at chunk c ^ (r mod 8) (64-byte rows: c ^ (r / 2 mod 4)), which no
+    // reader meets another's bank at.
+    constexpr int CH = D / 16, RI = 32 / CH, NI = kChunk / RI;  // chunks of a row, rows and instructions of a copy
+    const int row_l = lane / CH, chunk_l = lane % CH;
+    const uint8_t* k_base = kv.k + kvh * kv.head + row_l * kv.slot + 16 * chunk_l;
+    const uint8_t* v_base = kv.v + kvh * kv.head + row_l * kv.slot + 16 * chunk_l;
+    const int64_t rows_st = RI * kv.slot;
+    auto place = [](int r, int c) { return r * D + ((D == 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4); };
+    const uint32_t dst0 = smem_addr(ring) + place(row_l, chunk_l), dst1 = smem_addr(ring) + place(row_l + RI, chunk_l);
+    // what it reads: of K rows g and g + 8, of V rows 2t, 2t + 1, 2t + 8, 2t + 9
+    const int k_at0 = place(g, D == 128 ? 2 * t : t), k_at1 = place(g, 2 * t + 1);
+    const int v_at0 = kChunk * D + (D == 128 ? place(2 * t, g) : place(2 * t, g >> 1) + (g & 1) * 8);
+    const int v_at1 = kChunk * D + (D == 128 ? place(2 * t + 1, g) : place(2 * t + 1, g >> 1) + (g & 1) * 8);
     uint32_t to = 0;  // the stage that is filled next
     auto issue = [&](int i) {  // chunk i
       if (i < n_mine) {
@@ -236,28 +242,25 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
         const int64_t at = page * kv.page + (int64_t)(key0 & ((1 << kv.page_shift) - 1)) * kv.slot;
         const uint8_t* kp = k_base + at;
         const uint8_t* vp = v_base + at;
-        const uint32_t kd = k_dst + to, vd = v_dst + to;
         if (page >= 0 && key0 >= k_lo && key0 + kChunk <= k_hi) {
 #pragma unroll
-          for (int c = 0; c < D / 64; ++c) {
-            cp_async<16>(kd + c * 512, kp + 64 * c);
-            cp_async<16>(kd + (D / 64 + c) * 512, kp + slot8 + 64 * c);
+          for (int q = 0; q < NI; ++q) {
+            const uint32_t d = (q & 1 ? dst1 - RI * D : dst0) + to + q * RI * D;
+            cp_async<16>(d, kp);
+            cp_async<16>(d + kChunk * D, vp);
+            kp += rows_st;
+            vp += rows_st;
           }
-          cp_async<VB>(vd, vp);
-          cp_async<VB>(vd + 32 * VB, vp + kv.slot);
-          cp_async<VB>(vd + 64 * VB, vp + slot8);
-          cp_async<VB>(vd + 96 * VB, vp + slot8 + kv.slot);
         } else {  // (keys that no row of the tile sees arrive as zeros)
 #pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int c = 0; c < D / 64; ++c)
-              cp_async<16>(kd + (h * (D / 64) + c) * 512, kp + h * slot8 + 64 * c,
-                           page >= 0 && key0 + g + 8 * h >= k_lo && key0 + g + 8 * h < k_hi);
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const int key = key0 + 2 * t + (q & 1) + 8 * (q >> 1);
-            cp_async<VB>(vd + q * 32 * VB, vp + (q & 1) * kv.slot + (q >> 1) * slot8, page >= 0 && key >= k_lo && key < k_hi);
+          for (int q = 0; q < NI; ++q) {
+            const uint32_t d = (q & 1 ? dst1 - RI * D : dst0) + to + q * RI * D;
+            const int key = key0 + q * RI + row_l;
+            const bool seen = page >= 0 && key >= k_lo && key < k_hi;
+            cp_async<16>(d, kp, seen);
+            cp_async<16>(d + kChunk * D, vp, seen);
+            kp += rows_st;
+            vp += rows_st;
           }
         }
         to = to == (S - 1) * C::BYTES ? 0 : to + C::BYTES;
@@ -280,7 +283,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
         for (int c = 0; c < D / 64; ++c)
 #pragma unroll
-          for (int k = 0; k < 2; ++k) w[2 * c + k] = *reinterpret_cast<const uint4*>(q + 64 * c + 16 * t + 8 * k);
+          for (int k = 0; k < 2; ++k)
+            w[2 * c + k] = *reinterpret_cast<const uint4*>(q + (D == 128 ? 32 * t + 16 * c : 16 * t) + 8 * k);
       }
       const uint32_t* ww = reinterpret_cast<const uint32_t*>(w);
       float most = 0.f;
@@ -341,8 +345,8 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           for (int j = 0; j < 4; ++j) two[p][n][j] = 0.f;
 #pragma unroll
       for (int c = 0; c < D / 64; ++c) {
-        const uint4 k0 = *reinterpret_cast<const uint4*>(stage + c * 512 + lane * 16);
-        const uint4 k8 = *reinterpret_cast<const uint4*>(stage + (D / 64 + c) * 512 + lane * 16);
+        const uint8_t* kp = stage + (c ? k_at1 : k_at0);
+        const uint4 k0 = *reinterpret_cast<const uint4*>(kp), k8 = *reinterpret_cast<const uint4*>(kp + 8 * D);
         const uint32_t w0[4] = {k0.x, k0.y, k0.z, k0.w}, w8[4] = {k8.x, k8.y, k8.z, k8.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -372,7 +376,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll 1
     for (int i = 0; i < n_mine; ++i) {
       cp_wait<S - 2>();
-      __syncwarp();  // (scales are other lanes')
+      __syncwarp();  // (what a lane reads has come through others; what is overwritten now has been read)
       issue(i + S - 1);
       const uint8_t* stage = ring + from;
       from = from == (S - 1) * C::BYTES ? 0 : from + C::BYTES;
@@ -436,14 +440,14 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       }
       // ---- O^T
       uint32_t vw[4][VW];
-      const uint8_t* v_stage = stage + kChunk * D + lane * VB;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
+        const uint8_t* vp = stage + (q & 1 ? v_at1 : v_at0) + (q >> 1) * 8 * D;
         if constexpr (VW == 4) {
-          const uint4 v = *reinterpret_cast<const uint4*>(v_stage + q * 32 * VB);
+          const uint4 v = *reinterpret_cast<const uint4*>(vp);
           vw[q][0] = v.x, vw[q][1] = v.y, vw[q][2] = v.z, vw[q][3] = v.w;
         } else {
-          const uint2 v = *reinterpret_cast<const uint2*>(v_stage + q * 32 * VB);
+          const uint2 v = *reinterpret_cast<const uint2*>(vp);
           vw[q][0] = v.x, vw[q][1] = v.y;
         }
       }
