@@ -336,9 +336,10 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
     }
     uint32_t from = 0;  // the stage that is read next
     auto scores = [&](const uint8_t* stage, const float2& sc, float (*x)[4]) {
-      float two[2][NB][4];
+      constexpr int CHAINS = NB == 1 ? 2 : 1;  // of dependent products a tile of rows
+      float two[CHAINS][NB][4];
 #pragma unroll
-      for (int p = 0; p < 2; ++p)
+      for (int p = 0; p < CHAINS; ++p)
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -357,9 +358,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           for (int n = 0; n < NB; ++n) {
             if constexpr (C::QS) {
               const uint2 q = s_qf[(n * KS + 4 * c + j) * 32 + lane];
-              mma(two[j & 1][n], a0, a1, a2, a3, q.x, q.y);
+              mma(two[j % CHAINS][n], a0, a1, a2, a3, q.x, q.y);
             } else {
-              mma(two[j & 1][n], a0, a1, a2, a3, qf[n][4 * c + j][0], qf[n][4 * c + j][1]);
+              mma(two[j % CHAINS][n], a0, a1, a2, a3, qf[n][4 * c + j][0], qf[n][4 * c + j][1]);
             }
           }
         }
@@ -367,7 +368,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
 #pragma unroll
       for (int n = 0; n < NB; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[n][j] = (two[0][n][j] + two[1][n][j]) * sc.x * rowf[n][j & 1];
+        for (int j = 0; j < 4; ++j) x[n][j] = (CHAINS == 2 ? two[0][n][j] + two[CHAINS - 1][n][j] : two[0][n][j]) * sc.x * rowf[n][j & 1];
     };
     auto sees = [&](int n, int j, int key) {  // row 2t + (j & 1) of tile n
       const int row = r0 + 8 * n + 2 * t + (j & 1), p = ctx + row / G;

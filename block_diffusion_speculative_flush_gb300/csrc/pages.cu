@@ -177,13 +177,14 @@ __global__ void __launch_bounds__(256) k_pages_reorder(int32_t* refs, int n_page
 // ---------------------------------------------------------------------------
 constexpr int kCluster = 8, kScanThreads = 1024;
 
-// Sums over the threads of a cluster: each thread's exclusive prefix of v in (rank, thread) order, and
-// the total.  64 bits: two counts ride in one word.
-struct ClusterScan {
+// Sums over the threads of a cluster (ONE: of one CTA): each thread's exclusive prefix of v in (rank,
+// thread) order, and the total.  64 bits: two counts ride in one word.
+template <bool ONE>
+struct Scan {
   uint64_t* warps;  // [32] of this CTA
   uint64_t* ctas;   // [1] of this CTA, read by its peers
   uint64_t prefix, total;
-  __device__ __forceinline__ void run(uint64_t v, cg::cluster_group& cl) {
+  __device__ __forceinline__ void run(uint64_t v) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint64_t incl = v;
 #pragma unroll
@@ -203,6 +204,13 @@ struct ClusterScan {
       warps[lane] = wi - w;
       if (lane == 31) *ctas = wi;
     }
+    if (ONE) {
+      __syncthreads();
+      prefix = warps[warp] + incl - v;
+      total = *ctas;
+      return;
+    }
+    cg::cluster_group cl = cg::this_cluster();
     cl.sync();
     prefix = warps[warp] + incl - v;
     total = 0;
@@ -243,18 +251,27 @@ __device__ __forceinline__ Ask ask_of(const Rows& t, const int32_t* new_lens, in
 
 // One cluster.  A thread has a stretch of rows and a stretch of pages, both contiguous, so that ranks
 // are prefix sums over the threads.  Bound by latency: five cluster barriers and the loads between them.
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
-    k_pages_resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws, int32_t* free_pages,
-                   int32_t* status) {
+// ONE: a small pool and little to copy, one CTA, whose working arrays are in shared memory and which makes
+// the copies itself (a user's four candidates, 76 pages, 2 layers: one launch in place of two).
+constexpr int kSmallPages = 2048, kSmallRows = 1024, kSmallBytes = 512 << 10;
+template <bool ONE>
+__device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws,
+                                       int32_t* free_pages, int32_t* status) {
   __shared__ uint64_t s_warps[2][32], s_cta[2];
+  auto sync = [] {
+    if constexpr (ONE) __syncthreads();
+    else cg::this_cluster().sync();
+  };
+  // (working arrays: shared memory, or written by other SMs)
+  auto get = [](const int32_t* p) { return ONE ? *p : load_now(p); };
   pdl_trigger();
   pdl_wait();
   t.table = after_wait(t.table);
   t.lens = after_wait(t.lens);
   new_lens = after_wait(new_lens);
   refs = after_wait(refs);
-  cg::cluster_group cl = cg::this_cluster();
-  const int tid = (int)cl.block_rank() * kScanThreads + threadIdx.x, threads = kCluster * kScanThreads;
+  const int rank = ONE ? 0 : (int)cg::this_cluster().block_rank();
+  const int tid = rank * kScanThreads + threadIdx.x, threads = (ONE ? 1 : kCluster) * kScanThreads;
   const int lane = threadIdx.x & 31, gwarp = tid >> 5, gwarps = threads >> 5;
   int bad = 0;
   auto entry = [&](int row, int j) { return t.table + (int64_t)row * t.stride + j; };
@@ -283,7 +300,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
       }
     }
   }
-  cl.sync();
+  sync();
   // 2: who writes to begun pages
   for (int row = tid; row < t.n; row += threads) {
     const Ask a = ask_of(t, new_lens, row);
@@ -298,8 +315,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   const int per_p = (n_pages + threads - 1) / threads, p0 = min(tid * (int64_t)per_p, (int64_t)n_pages), p1 = min(p0 + per_p, n_pages);
   int mine = 0;
   for (int p = p0; p < p1; ++p) mine += load_now(refs + p) <= 0;
-  ClusterScan fs{s_warps[0], &s_cta[0], 0, 0};
-  fs.run((uint64_t)mine, cl);  // (its barrier ends 2)
+  Scan<ONE> fs{s_warps[0], &s_cta[0], 0, 0};
+  fs.run((uint64_t)mine);  // (its barrier ends 2)
   {
     int at = (int)fs.prefix;
     if (mine)
@@ -313,7 +330,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
     const int p = *entry(row, a.have - 1);
     if (!there(p)) return false;
     const int n = load_now(refs + p);
-    return n > 1 && !(n == load_now(ws.writers + p) && load_now(ws.owner + p) == row);
+    return n > 1 && !(n == get(ws.writers + p) && get(ws.owner + p) == row);
   };
   uint64_t sum = 0;  // pages << 32 | copies
   for (int row = r0; row < r1; ++row) {
@@ -322,9 +339,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
     const bool c = copies(row, a);
     sum += (uint64_t)(max(a.need - a.have, 0) + c) << 32 | (uint64_t)c;
   }
-  ClusterScan rs{s_warps[1], &s_cta[1], 0, 0};
+  Scan<ONE> rs{s_warps[1], &s_cta[1], 0, 0};
   if (free_pages && tid == 0) *free_pages = (int)fs.total;
-  rs.run(sum, cl);
+  rs.run(sum);
   const int64_t n_free = (int64_t)fs.total;
   int64_t pages = (int64_t)(rs.prefix >> 32), made = (int64_t)(rs.prefix & 0xffffffffu);
   // 4: rows take their pages, behind those of the rows in front of them.  Once one does not get
@@ -342,11 +359,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
       if (c) {
         copied |= 1u << (row - r0);
         ws.src[made] = *entry(row, a.have - 1);
-        ws.dst[made] = load_now(ws.free_ + at++);
+        ws.dst[made] = get(ws.free_ + at++);
         ++made;
       }
       for (int j = a.have; j < a.need; ++j) {
-        const int p = load_now(ws.free_ + at++);
+        const int p = get(ws.free_ + at++);
         *entry(row, j) = p;
         refs[p] = 1;
       }
@@ -358,7 +375,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   }
   if (copied) atomicAdd(ws.count, __popc(copied));
   if (given && free_pages) atomicSub(free_pages, given);
-  cl.sync();  // every row has looked at the begun pages' counts
+  sync();  // every row has looked at the begun pages' counts
   // 5: the copies' pages take the places of those that they are copies of; lengths
   made -= __popc(copied);
   for (int row = r0; row < r1; ++row) {
@@ -373,6 +390,21 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
     t.lens[row] = new_lens[row];
   }
   if (bad) flag_status(status, bad);
+}
+
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
+    k_pages_resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws, int32_t* free_pages,
+                   int32_t* status) {
+  resize<false>(refs, n_pages, t, new_lens, ws, free_pages, status);
+}
+__global__ void __launch_bounds__(kScanThreads) k_pages_resize_one(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens,
+                                                                   int32_t* free_pages, int32_t* status,
+                                                                   const __grid_constant__ Buffers bufs) {
+  __shared__ int32_t owner[kSmallPages], writers[kSmallPages], free_list[kSmallPages], src[kSmallRows], dst[kSmallRows], count;
+  __shared__ int first[kBuffers + 1];
+  resize<true>(refs, n_pages, t, new_lens, ResizeWs{owner, writers, free_list, src, dst, &count}, free_pages, status);
+  __syncthreads();
+  if (bufs.n > 0) copy_pages(CopyList{src, dst, &count, 0, n_pages, status}, bufs, first);
 }
 
 // ---------------------------------------------------------------------------
@@ -398,8 +430,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   const int per = (n_pages + threads - 1) / threads, p0 = min(tid * (int64_t)per, (int64_t)n_pages), p1 = min(p0 + per, n_pages);
   int mine = 0;
   for (int p = p0; p < p1; ++p) mine += refs[p] > 0;
-  ClusterScan us{s_warps[0], &s_cta[0], 0, 0};
-  us.run((uint64_t)mine, cl);
+  Scan<false> us{s_warps[0], &s_cta[0], 0, 0};
+  us.run((uint64_t)mine);
   const int U = (int)us.total;
   uint64_t sum = 0;  // holes << 32 | movers
   for (int p = p0; p < p1; ++p) {
@@ -407,8 +439,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
     if (p < U && !in) sum += 1ull << 32;
     if (p >= U && in) sum += 1;
   }
-  ClusterScan ms{s_warps[1], &s_cta[1], 0, 0};
-  ms.run(sum, cl);
+  Scan<false> ms{s_warps[1], &s_cta[1], 0, 0};
+  ms.run(sum);
   int hole = (int)(ms.prefix >> 32), mover = (int)(ms.prefix & 0xffffffffu);
   const int moves = (int)(ms.total & 0xffffffffu);
   for (int p = p0; p < p1; ++p) {
@@ -596,6 +628,12 @@ DFLASH_API int dflash_pages_resize(int32_t* refs, int64_t n_pages, const dflash_
   int32_t* w = (int32_t*)workspace;
   const ResizeWs ws{w, w + n_pages, w + 2 * n_pages, w + 3 * n_pages, w + 3 * n_pages + rows->rows,
                     w + 3 * n_pages + 2 * (int64_t)rows->rows};
+  int64_t page = 0;  // bytes of a page in all buffers
+  for (int i = 0; i < n_buffers; ++i) page += buffers[i].page_bytes;
+  if (n_pages <= kSmallPages && rows->rows <= kSmallRows && n_buffers <= kBuffers && page * rows->rows <= kSmallBytes)
+    return rcheck(launch_k(k_pages_resize_one, 1, kScanThreads, 0, st, refs, (int)n_pages, rows_of(rows), new_lens, free_pages,
+                           status, buffers_of(buffers, 0, n_buffers)),
+                  call);
   if (int rc = rcheck(launch_k(k_pages_resize, kCluster, kScanThreads, 0, st, refs, (int)n_pages, rows_of(rows), new_lens,
                                ws, free_pages, status),
                       call))
