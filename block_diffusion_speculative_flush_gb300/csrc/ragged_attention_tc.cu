@@ -663,7 +663,7 @@ __device__ __forceinline__ int q_to_h16(uint8_t* row, int block, int swizzle) {
 // A row of a Q tile as above into two e4m3 pieces q1 + q2 (each a tile of its own, one in each 64-element
 // block's place): 2^e q with its largest finite element in [2^7, 2^8), q1 its nearest code, q2 the code of what
 // is left.  A code has 4 significant bits and a bf16 number 8, so the sum is exact for elements down to
-// 2^-10 of the largest; smaller ones are off by at most 2^-18 of that.  Not finite: NaN.  Returns e.
+// 2^-9 of the largest; smaller ones are off by at most 2^-17 of that (half a step of 2^-9, the largest being 2^7 or more).  Not finite: NaN.  Returns e.
 template <int D>
 __device__ __forceinline__ int q_to_e4m3(uint8_t* row, int block, int swizzle) {
   static_assert(D == 128, "a piece is a row of 128 bytes");

@@ -115,14 +115,17 @@ def gather8(codes, scale, lens, table):
     return T.gather(decode(codes, scale), lens, table)
 
 
-def attention8(q, seq_k, seq_v, starts, lens, causal, window, scale, bf16, tensor_cores):
+def attention8(q, seq_k, seq_v, starts, lens, causal, window, scale, bf16, tensor_cores, q_pieces=False):
     """As T.attention over the decoded values, with the bounds of these kernels.
 
     fp32 arithmetic is T's, with the two scales' products (2 2^-24 of a score and of a value, within its d + 4 and
     its sums' slack).  The output is rounded once.  On the tensor cores a probability is rounded to fp16 (2^-11
     relative) and so may a value be at a scale that is not its tile's (2^-11); both have steps of 2^-24 below
     their smallest normal number, which is 2^-31 of the largest value a key may add (probabilities are held at
-    2^6 or more times their size, values at the size of the largest scale)."""
+    2^6 or more times their size, values at the size of the largest scale).  q_pieces: q is the sum of two e4m3
+    pieces, scaled so that its largest element is 2^7 or more; the second piece is off by at most half its step
+    of 2^-9, that is 2^-17 of the largest, where an element is below 2^-9 of that (larger ones are exact): twice
+    that error of a score for a weight, once for the log-sum-exp."""
     o, lse, tol, tol_lse = T.attention(q, seq_k, seq_v, starts, lens, causal, window, scale, False)
     for b, L in enumerate(lens):
         s, e = starts[b], starts[b + 1]
@@ -131,6 +134,14 @@ def attention8(q, seq_k, seq_v, starts, lens, causal, window, scale, bf16, tenso
             most = float(fin(seq_v[b]).max()) * 448 if L else 0.0
             av = T.attention(q[s:e], [seq_k[b]], [fin(seq_v[b])], [0, e - s], [L], causal, window, scale, False)[0]
             tol[s:e] += av * 2.0 ** -10 + L * 2.0 ** -31 * most
+            if q_pieces and L:
+                x = fin(q[s:e].double())
+                top = x.amax(-1, keepdim=True)
+                off = torch.where(x < top * 2.0 ** -9, top * 2.0 ** -17, 0.0)                  # [n, hq, d]
+                g = q.shape[1] // seq_k[b].shape[1]
+                ds = torch.stack([(off[:, h] @ fin(seq_k[b][:, h // g]).t()).amax(-1) for h in range(q.shape[1])], 1) * scale
+                tol[s:e] += av * 2 * ds[..., None]
+                tol_lse[s:e] += ds
     if bf16:
         tol = tol + o.abs() * 2.0 ** -8
     return o, lse, tol, tol_lse

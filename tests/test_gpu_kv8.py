@@ -116,7 +116,7 @@ def ref8(B, causal, window, scale=None, pages=None):
     bf16 = B.dt == torch.bfloat16
     return O.attention8(B.q[:B.starts[-1]], O.gather8(kp, ks, B.lens, B.table), O.gather8(vp, vs, B.lens, B.table),
                         B.starts, B.lens, causal, window, scale if scale is not None else B.d ** -0.5, bf16,
-                        bf16 and B.d in (64, 128))
+                        bf16 and B.d in (64, 128), bf16 and B.d == 128 and max(B.rows) * (B.hq // B.hkv) > 64)
 
 
 SHAPES = [  # hq, hkv, page, rows, lens
@@ -200,21 +200,21 @@ def test_attention_with_many_key_tiles(rows, hq, d):
     check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows,lens,hq", [([16], [3000], 4), ([1, 5], [900, 2000], 8), ([200, 90], [900, 700], 4),
                                           ([3] * 20, [1000 + 13 * b for b in range(20)], 8)])
-def test_hidden_codes_that_are_nan(dtype, rows, lens, hq):
+def test_hidden_codes_that_are_nan(dtype, d, rows, lens, hq):
     """A window of 100, NaN outside it and in the block's last key: what a row does not see never reaches it, and
     who sees the last key answers NaN where it is."""
-    B = Batch8(dtype, hq, 2, 64, 16, rows, lens, seed=3)
+    B = Batch8(dtype, hq, 2, d, 16, rows, lens, seed=3)
     kp, vp, ks, vs = B.appended()
     clean = tuple(x.clone() for x in (kp, vp, ks, vs))
     for b, (n, L) in enumerate(zip(rows, lens)):
         for p in list(range(0, L - n - 100)) + ([L - 1] if n > 1 else []):
             pg, sl = int(B.table[b, p // 16]), p % 16
-            vp[pg, sl, :, p % 64] = 0x7F
+            vp[pg, sl, :, p % d] = 0x7F
             if p < L - 1:
-                kp[pg, sl, :, (p + 1) % 64] = 0xFF
+                kp[pg, sl, :, (p + 1) % d] = 0xFF
     ref = ref8(B, True, 100, pages=clean)
     out, lse, _ = run8(B, True, 100, append=False, pages=B.cuda(kp, vp, ks, vs))
     for b, n in enumerate(rows):
@@ -222,26 +222,26 @@ def test_hidden_codes_that_are_nan(dtype, rows, lens, hq):
         sl = slice(B.starts[b], last + (0 if n > 1 else 1))
         check_attention(out[sl], lse[sl], tuple(x[sl] for x in ref), sl.stop - sl.start)
         if n > 1:   # only that column of the last row
-            c = (lens[b] - 1) % 64
+            c = (lens[b] - 1) % d
             assert bool(torch.isnan(out[last, :, c]).all())
-            rest = [i for i in range(64) if i != c]
+            rest = [i for i in range(d) if i != c]
             check_attention(out[last:last + 1, :, rest], lse[last:last + 1],
                             (ref[0][last:last + 1, :, rest], ref[1][last:last + 1], ref[2][last:last + 1, :, rest],
                              ref[3][last:last + 1]), 1)
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[1], [3], [40], [150]])
-def test_a_nan_that_a_row_sees(dtype, rows):
+def test_a_nan_that_a_row_sees(dtype, d, rows):
     """A NaN in K makes all of a row NaN, one in V the columns where it is."""
-    B = Batch8(dtype, 4, 1, 64, 16, rows, [400], seed=11, tail=0)
+    B = Batch8(dtype, 4, 1, d, 16, rows, [400], seed=11, tail=0)
     kp, vp, ks, vs = B.appended()
     pg = int(B.table[0, 3])
     v2 = vp.clone()
     v2[pg, 5, 0, 17] = 0x7F
     out, lse, _ = run8(B, True, 0, append=False, pages=B.cuda(kp, v2, ks, vs))
     assert bool(torch.isnan(out[..., 17]).all()) and bool(torch.isfinite(lse).all())
-    rest = [c for c in range(64) if c != 17]
+    rest = [c for c in range(d) if c != 17]
     ref = ref8(B, True, 0, pages=(kp, vp, ks, vs))
     check_attention(out[..., rest], lse, (ref[0][..., rest], ref[1], ref[2][..., rest], ref[3]), rows[0])
     kp[pg, 5, 0, 17] = 0x7F
@@ -271,19 +271,20 @@ def test_wide_groups(dtype, hq, hkv, rows, lens):
 
 
 @pytest.mark.parametrize("dtype,scale,big", [("bf16", 1e-30, 1e30), ("bf16", 1e20, 1e-22), ("f32", 1e-30, 1e30)])
+@pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [[1], [40], [200]])
-def test_queries_and_scales_of_any_size(dtype, scale, big, rows):
-    B = Batch8(dtype, 4, 1, 64, 16, rows, [300], seed=17, tail=0)
+def test_queries_and_scales_of_any_size(dtype, scale, big, d, rows):
+    B = Batch8(dtype, 4, 1, d, 16, rows, [300], seed=17, tail=0)
     B.q = (B.q.float() * big * 0.1).to(B.dt)
     out, lse, _ = run8(B, True, 0, scale=scale)
     check_attention(out, lse, ref8(B, True, 0, scale=scale), rows[0])
 
 
-@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[2, 1], [100, 20]])
-def test_missing_pages_read_as_zeros_and_are_told(dtype, rows):
+def test_missing_pages_read_as_zeros_and_are_told(dtype, d, rows):
     D = lib()
-    B = Batch8(dtype, 4, 2, 64, 16, rows, [300, 200], seed=19)
+    B = Batch8(dtype, 4, 2, d, 16, rows, [300, 200], seed=19)
     want = B.appended()
     B2 = B.table.clone()
     for bad in (-1, 1 << 30, int(want[0].shape[0])):
@@ -405,3 +406,76 @@ def test_a_workspace_that_is_too_small_is_refused():
     with pytest.raises(D.DFlashError, match="workspace"):
         D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=9000,
                                workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [[1], [12], [30], [200]])
+def test_queries_with_elements_far_apart(d, rows):
+    """Elements of q that differ by up to 2^20 within a row, and rows of zeros."""
+    B = Batch8("bf16", 4, 1, d, 32, rows, [500], seed=29, tail=0)
+    g = torch.Generator().manual_seed(1)
+    B.q = (B.q.float() * torch.exp2(torch.randint(-20, 1, B.q.shape, generator=g).float())).bfloat16()
+    B.q[0, 1] = 0
+    out, lse, _ = run8(B, True, 0)
+    check_attention(out, lse, ref8(B, True, 0), rows[0])
+
+
+@pytest.mark.parametrize("bits", [math.nan, math.inf])
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("rows", [[1], [30], [150]])
+def test_a_query_that_is_not_finite_is_its_rows_own(dtype, d, rows, bits):
+    B = Batch8(dtype, 4, 1, d, 16, rows, [400], seed=31, tail=0)
+    ref = ref8(B, True, 0)
+    B.q[0, 2, 5] = bits
+    out, lse, _ = run8(B, True, 0)
+    assert bool(torch.isnan(out[0, 2]).all())
+    out[0, 2], lse[0, 2] = ref[0][0, 2].to(out), ref[1][0, 2].to(lse)
+    check_attention(out, lse, ref, rows[0])
+
+
+def test_a_stream_of_its_own_and_a_strided_cache():
+    """K, V and their scales side by side in one allocation each, another stream than the current one."""
+    D = lib()
+    B = Batch8("bf16", 8, 2, 128, 16, [5, 1], [700, 90], seed=37, tail=0)
+    want = B.appended()
+    n = B.kp.shape[0]
+    codes = torch.zeros((n, 2, 16, 2, 128), dtype=torch.uint8, device="cuda")
+    scales = torch.zeros((n, 2, 2), device="cuda")
+    codes[:, 0], codes[:, 1] = B.kp.cuda(), B.vp.cuda()
+    scales[:, 0], scales[:, 1] = B.ks.cuda(), B.vs.cuda()
+    P = (codes[:, 0], codes[:, 1], scales[:, 0], scales[:, 1])
+    args = (i32(B.starts), i32(B.lens), B.table.cuda())
+    q, k, v = B.q.cuda(), B.k.cuda(), B.v.cuda()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    D.dflash_kv8_append(k, v, *P, *args, stream=s)
+    D.dflash_kv8_attention(q, *P, *args, out, max_rows=5, lse=lse, stream=s)
+    torch.cuda.current_stream().wait_stream(s)
+    assert same_codes(codes[:, 0], want[0]) and same_codes(codes[:, 1], want[1])
+    assert same_scales(scales[:, 0], want[2]) and same_scales(scales[:, 1], want[3])
+    check_attention(out, lse, ref8(B, True, 0), 6)
+
+
+@pytest.mark.parametrize("rows,lens", [([1] * 5, [300, 1, 900, 17, 2000]), ([40, 90], [500, 400])])
+def test_the_same_call_twice_gives_the_same_bits(rows, lens):
+    B = Batch8("bf16", 8, 2, 128, 16, rows, lens, seed=41)
+    P = B.cuda(*B.appended())
+    a = run8(B, True, 0, append=False, pages=P)
+    for _ in range(5):
+        b = run8(B, True, 0, append=False, pages=P)
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_many_short_sequences():
+    """More sequences than a warp looks at in one go, most of them of a few tokens, some without new rows."""
+    rows = [(b * 7) % 3 for b in range(300)]
+    lens = [r + (b * 37) % 50 for b, r in enumerate(rows)]
+    for dtype in ("bf16", "f32"):
+        B = Batch8(dtype, 4, 2, 64, 16, rows, lens, seed=43)
+        status = i32([0])
+        out, lse, P = run8(B, True, 0, status=status)
+        lib().dflash_status_check(status)
+        want = B.appended()
+        assert same_codes(P[0], want[0]) and same_scales(P[3], want[3])
+        check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
