@@ -49,6 +49,7 @@ int64_t kv8_simt_workspace(const Ragged& r, const AttnCall& a, int sms);
 cudaError_t launch_kv8_simt(const Ragged& r, const AttnCall& a, const Kv8View& kv, bool is_bf16, int sms, cudaStream_t st);
 
 // Few rows on the tensor cores (bf16, head_dim 64 or 128).
+bool kv8_few(const Ragged& r, const AttnCall& a, int sms);
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms);
 cudaError_t launch_kv8_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, int sms, cudaStream_t st);
 

@@ -236,7 +236,8 @@ cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads
 }
 template <typename T>
 cudaError_t launch(const Ragged& r, const Rows8& x, const Kv8View& kv, int heads, int d, cudaStream_t st) {
-  // warps a task: as few as hold its rows, those of a full page or the average sequence's, in registers
+  // Warps a task: as few as hold its rows, those of a full page or the average sequence's, in registers.  bf16, 8
+  // heads of 128, 8 x 300 rows: pages of 16 with 1, 2, 4 warps 4.0, 5.4, 8.1 us, pages of 64 13.5, 7.6, 4.1 (8: 6.0).
   constexpr int HOLD = Eight<T>::HOLD;
   const int rows = std::min(1 << kv.page_shift, std::max(1, r.total / r.batch)), steps = (rows * d / 8 + 31) / 32;
   return steps <= HOLD       ? launch<T, 1>(r, x, kv, heads, d, st)

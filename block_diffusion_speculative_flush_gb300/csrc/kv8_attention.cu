@@ -306,16 +306,18 @@ __global__ void __launch_bounds__(256) k_kv8_simt_merge(Ragged r, AttnCall a, in
   if (a.lse && lane == 0) a.lse[(int64_t)tok * a.Hq + h] = lse_of(M, L);
 }
 
-int simt_rows(const Ragged& r, const AttnCall& a) {  // packed rows of a CTA
-  const int64_t rows = (int64_t)r.max_rows * (a.Hq / a.Hkv);
-  return rows <= 4 ? 4 : rows <= 8 ? 8 : 16;
+// Packed rows of a CTA.  fp32, 32 over 8 heads of 128: 64 single tokens over 4096 in 4 rows 288 us (8: 550), blocks
+// of 16 of 8 users 468 (8: 470), 100 rows of 4 over 2000 682 (8: 658, 16: 723).
+int simt_rows(const Ragged& r, const AttnCall& a) {
+  return (int64_t)r.max_rows * (a.Hq / a.Hkv) <= 4 ? 4 : 8;
 }
-// Splits: enough CTAs for two on each SM, none of less than a tile.
+// Splits: CTAs for eight turns of each SM, so that uneven lengths even out, none of less than a tile.  64 single tokens over
+// 4096: two turns 364 us, four 308, eight 288; blocks of 4 of 8 users 165, 151, 137.
 int simt_splits(const Ragged& r, const AttnCall& a, int sms) {
   const int br = simt_rows(r, a);
   const int64_t ctas = ((int64_t)r.max_rows * (a.Hq / a.Hkv) + br - 1) / br * std::min(r.batch, std::max(r.total, 1)) * a.Hkv;
   const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
-  return (int)std::max<int64_t>(1, std::min<int64_t>({(2 * sms + ctas - 1) / ctas, (span + kTile - 1) / kTile, 64}));
+  return (int)std::max<int64_t>(1, std::min<int64_t>({(8 * sms + ctas - 1) / ctas, (span + kTile - 1) / kTile, 64}));
 }
 
 template <typename T, int DP, int BR>
@@ -339,8 +341,7 @@ template <typename T, int DP>
 cudaError_t launch_simt(const Ragged& r, const AttnCall& a, const Kv8View& kv, int splits, cudaStream_t st) {
   const int br = simt_rows(r, a);
   return br == 4   ? launch_simt<T, DP, 4>(r, a, kv, splits, st)
-         : br == 8 ? launch_simt<T, DP, 8>(r, a, kv, splits, st)
-                   : launch_simt<T, DP, 16>(r, a, kv, splits, st);
+                   : launch_simt<T, DP, 8>(r, a, kv, splits, st);
 }
 
 cudaError_t sms_of_device(int* sms) {
@@ -405,14 +406,14 @@ int kv8_sms() {
 
 // The kernel of a call: bf16 with head_dim 64 or 128 runs on the tensor cores.
 enum class Path { kSimt, kFew, kTiles };
-Path kv8_path(const dflash_attention* a, const Ragged& r) {
+Path kv8_path(const dflash_attention* a, const Ragged& r, const AttnCall& c, int sms) {
   if (a->dtype != DFLASH_DTYPE_BF16 || (a->head_dim != 64 && a->head_dim != 128)) return Path::kSimt;
-  return (int64_t)r.max_rows * (a->n_q_heads / a->n_kv_heads) <= 64 ? Path::kFew : Path::kTiles;
+  return kv8_few(r, c, sms) ? Path::kFew : Path::kTiles;
 }
 int64_t kv8_workspace(const dflash_attention* a, const Ragged& r, int sms) {
   const AttnCall c = kv8_call(a);
   int64_t bytes = 0;
-  switch (kv8_path(a, r)) {
+  switch (kv8_path(a, r, c, sms)) {
     case Path::kSimt: return kv8_simt_workspace(r, c, sms);
     case Path::kFew: return kv8_few_workspace(r, c, sms);
     default: attn_tc_workspace(r, c, &bytes, true); return bytes;
@@ -455,7 +456,7 @@ DFLASH_API int dflash_kv8_attention(const dflash_attention* a, const dflash_ragg
   const AttnCall c = kv8_call(a);
   const Kv8View kv = kv8_view(pages);
   cudaStream_t st = (cudaStream_t)stream;
-  switch (kv8_path(a, r)) {
+  switch (kv8_path(a, r, c, sms)) {
     case Path::kSimt: return rcheck(launch_kv8_simt(r, c, kv, a->dtype == DFLASH_DTYPE_BF16, sms, st), call);
     case Path::kFew: return rcheck(launch_kv8_few(r, c, kv, sms, st), call);
     default: return rcheck(launch_attn_tc8(r, c, kv, st), call);

@@ -43,6 +43,7 @@ namespace {
 constexpr int kChunk = 16;  // keys of a chunk: never more than a page
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
+constexpr int kMaxShare = 128;  // chunks of a CTA of a cluster
 namespace cg = cooperative_groups;
 constexpr float kSlack = 4.f, kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kUnit = 1024.f;  // 2^10, of P in fp16
@@ -718,27 +719,37 @@ struct FewHost {
   int nb;
   FewPlan p;
 };
-FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
-  const int rows = rows_of(r, a), seqs = std::min(r.batch, std::max(r.total, 1));
-  FewHost h;
-  // 32 rows a CTA where there are many items (each tile of rows converts the codes anew), 16 where the
-  // calls are short and spread better
-  h.nb = rows <= 8 ? 1 : 2;
-  if (rows > 16 && (int64_t)seqs * a.Hkv * ((rows + 15) / 16) > 2 * sms) h.nb = 4;
-  const int rb = 8 * h.nb, ctas = sms * (h.nb <= 2 ? 2 : 1);
-  h.p.tiles = (rows + rb - 1) / rb;
-  h.p.pad = 28;
-  h.p.min_units = 8;
-  h.p.slots = 2 * ctas;
-  // cluster: an item's chunks over up to 8 CTAs, where all items run at once and none has more than 64 chunks
-  h.p.cluster = 0;
-  const int64_t items = (int64_t)r.batch * h.p.tiles * a.Hkv;
+// CTAs of a cluster per item, or 0 for ranges: where all items run at once and no CTA has more than
+// kMaxShare chunks.  32 over 8 heads of 128, one user's single token: 6.6 us over 300 tokens (ranges 12.3), 10.7
+// over 4000 (22.4), 19 over 16000 (27); 8 users over 8000, 4 CTAs an item: 28 (43); 32 over 2000, 1 CTA: 26 (41).
+// A longer share would gain as much for even lengths, but one long sequence among short ones has the CTAs
+// of its own items only.
+int few_cluster(const Ragged& r, const AttnCall& a, int tiles, int ctas) {
+  const int64_t items = (int64_t)r.batch * tiles * a.Hkv;
   const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
   const int64_t chunks = (span + kChunk - 1) / kChunk + 1;
+  int cluster = 0;
   for (int n = 1; n <= kMaxCluster && items * n <= ctas; n *= 2)
-    if (chunks <= 64 * n) h.p.cluster = n;
-  while (h.p.cluster > 1 && chunks <= 4 * h.p.cluster) h.p.cluster /= 2;
-  return h;
+    if (chunks <= kMaxShare * n) cluster = n;
+  while (cluster > 1 && chunks <= 4 * cluster) cluster /= 2;
+  return cluster;
+}
+FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
+  const int rows = rows_of(r, a);
+  FewHost h;
+  // what an item costs besides its chunks; 64 single tokens over 1k to 16k: 4 158 us, 16 151, 28 133, 44 133
+  h.p.pad = 28;
+  h.p.min_units = 8;
+  // A tile of rows converts the codes anew, so 32 rows a CTA (one an SM) where ranges are cut: 64 users' blocks of 8
+  // over 2048 tokens 132 us (16 rows 156), 8 users' 43 (49).  16 where they run as clusters, whose items then
+  // spread over twice the CTAs: one user's block of 16 over 4096 18.4 us (32 rows 35).
+  for (h.nb = rows <= 8 ? 1 : 2;; h.nb = 4) {
+    const int rb = 8 * h.nb, ctas = sms * (h.nb <= 2 ? 2 : 1);
+    h.p.tiles = (rows + rb - 1) / rb;
+    h.p.slots = 2 * ctas;
+    h.p.cluster = few_cluster(r, a, h.p.tiles, ctas);
+    if (h.p.cluster || rows <= 16 || h.nb == 4) return h;
+  }
 }
 
 template <int D, int NB>
@@ -771,6 +782,11 @@ cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, in
 
 }  // namespace
 
+// Few rows, or many that are a short call: a KV head's rows of a sequence fill a quarter of the 128-row tiles or less,
+// or all items run at once as clusters.  32 over 8 heads of 128, this and the tiles: 64 sequences of 32 rows over 2048
+// 132 and 188 us, of 64 rows 231 and 189; 8 of 32 over 16000 101 and 150, of 48 160 and 151; one user's 64 rows over
+// 4096 in clusters 18 and 36, 128 over 500 13 and 24.
+bool kv8_few(const Ragged& r, const AttnCall& a, int sms) { return rows_of(r, a) <= 32 || few_plan(r, a, sms).p.cluster > 0; }
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms) {
   const FewHost h = few_plan(r, a, sms);
   return h.p.cluster ? 0 : (int64_t)h.p.slots * 8 * h.nb * (a.d + 2) * 4;

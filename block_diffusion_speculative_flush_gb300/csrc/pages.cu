@@ -252,7 +252,8 @@ __device__ __forceinline__ Ask ask_of(const Rows& t, const int32_t* new_lens, in
 // One cluster.  A thread has a stretch of rows and a stretch of pages, both contiguous, so that ranks
 // are prefix sums over the threads.  Bound by latency: five cluster barriers and the loads between them.
 // ONE: a small pool and little to copy, one CTA, whose working arrays are in shared memory and which makes
-// the copies itself (a user's four candidates, 76 pages, 2 layers: one launch in place of two).
+// the copies itself: one launch in place of two.  A user's four candidates, 76 pages, 2 layers, with the reorder in
+// front: 13.3 us, 14.3 otherwise, and 20.6 against 23 of host time.
 constexpr int kSmallPages = 2048, kSmallRows = 1024, kSmallBytes = 512 << 10;
 template <bool ONE>
 __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws,

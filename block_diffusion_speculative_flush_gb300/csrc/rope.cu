@@ -181,8 +181,9 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(Ragged r, RopeCall c, con
 
 template <typename T, int V, bool IL>
 cudaError_t launch_rope(const Ragged& r, const RopeCall& c, const RopeTurns& t, cudaStream_t st) {
-  // few rows: one a CTA, so that they spread over the SMs
-  if (r.total <= 608) return launch_k(k_rope<T, V, IL, 1>, (unsigned)r.total, kRopeThreads, 0, st, r, c, t);
+  // Few rows: one a CTA, so that they spread over the SMs, as long as all CTAs run at once (three an SM).  40 heads
+  // of 128: 64 rows 3.4 us (four a CTA 5.4), 456 4.3 (5.4), 608 7.1 (5.4), 2000 15.3 (13.0).
+  if (r.total <= 456) return launch_k(k_rope<T, V, IL, 1>, (unsigned)r.total, kRopeThreads, 0, st, r, c, t);
   return launch_k(k_rope<T, V, IL, 4>, (unsigned)((r.total + 3) / 4), kRopeThreads, 0, st, r, c, t);
 }
 template <typename T>

@@ -96,7 +96,13 @@ def check_attention(o, lse, ref, rows):
     assert not bad.any(), (int(bad.sum()), float(el[bad][0]), bad.nonzero()[:4].tolist())
 
 
-def run8(B, causal, window, scale=None, max_len=None, append=True, status=None, pages=None):
+def bound(B):
+    """A bound of the new rows with which calls of more than 32 rows a group take the kernel of many rows, short ones too."""
+    rows = max(max(B.rows), 1)
+    return 1 << 15 if rows * (B.hq // B.hkv) > 32 else rows
+
+
+def run8(B, causal, window, scale=None, max_len=None, append=True, status=None, pages=None, max_rows=None):
     D = lib()
     P = B.cuda(B.kp, B.vp, B.ks, B.vs) if pages is None else pages
     starts, lens, table = i32(B.starts), i32(B.lens), B.table.cuda()
@@ -105,18 +111,18 @@ def run8(B, causal, window, scale=None, max_len=None, append=True, status=None, 
     q = B.q.cuda()
     out = torch.full_like(q, 7.0)
     lse = torch.full(q.shape[:2], 7.0, device="cuda")
-    D.dflash_kv8_attention(q, *P, starts, lens, table, out, max_rows=max(max(B.rows), 1), max_len=max_len, causal=causal,
+    D.dflash_kv8_attention(q, *P, starts, lens, table, out, max_rows=max_rows or bound(B), max_len=max_len, causal=causal,
                            window=window, scale=scale, lse=lse, status=status)
     torch.cuda.synchronize()
     return out, lse, P
 
 
-def ref8(B, causal, window, scale=None, pages=None):
+def ref8(B, causal, window, scale=None, pages=None, many=None):
     kp, vp, ks, vs = B.appended() if pages is None else pages
     bf16 = B.dt == torch.bfloat16
     return O.attention8(B.q[:B.starts[-1]], O.gather8(kp, ks, B.lens, B.table), O.gather8(vp, vs, B.lens, B.table),
                         B.starts, B.lens, causal, window, scale if scale is not None else B.d ** -0.5, bf16,
-                        bf16 and B.d in (64, 128), bf16 and B.d == 128 and max(B.rows) * (B.hq // B.hkv) > 64)
+                        bf16 and B.d in (64, 128), bf16 and B.d == 128 and (bound(B) > max(B.rows) if many is None else many))
 
 
 SHAPES = [  # hq, hkv, page, rows, lens
@@ -181,6 +187,17 @@ def test_append_at_the_borders_of_a_scale():
                 codes, scale = O.append8(codes, scale, x[i:i + 1], [0, 1], [i + 1], tb)
             assert same_codes(dev[0], codes) and same_codes(dev[1], codes), (first, second)
             assert same_scales(dev[2], scale) and same_scales(dev[3], scale), (first, second)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 37)])
+@pytest.mark.parametrize("rows,lens,hq,hkv", [([40], [600], 4, 1), ([33, 1, 90], [33, 1000, 400], 5, 1),
+                                              ([200, 7], [900, 2000], 4, 2), ([16, 16], [4096, 300], 32, 8)])
+def test_many_rows_of_short_calls(rows, lens, hq, hkv, causal, window, d):
+    """Tight bounds: items that all run at once as clusters."""
+    B = Batch8("bf16", hq, hkv, d, 16, rows, lens, seed=31)
+    out, lse, _ = run8(B, causal, window, max_len=max(lens), max_rows=max(rows))
+    check_attention(out, lse, ref8(B, causal, window, many=False), sum(rows))
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
@@ -377,11 +394,11 @@ def test_two_graphs_replayed_at_once(dtype, rows):
         P = B.cuda(*B.appended())
         q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), B.table.cuda()
         o, l = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
-        need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, rows[0], 2700, *P)
+        need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, bound(B), 2700, *P)
         ws = torch.empty(max(need, 32), dtype=torch.uint8, device="cuda")
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
-            D.dflash_kv8_attention(q, *P, st, ln, tb, o, rows[0], max_len=2700, lse=l, workspace=ws)
+            D.dflash_kv8_attention(q, *P, st, ln, tb, o, bound(B), max_len=2700, lse=l, workspace=ws)
         state.append((P, q, st, ln, tb, o, l, ws))
         graphs.append(g)
     streams = [torch.cuda.Stream() for _ in Bs]
@@ -397,14 +414,14 @@ def test_two_graphs_replayed_at_once(dtype, rows):
 
 def test_a_workspace_that_is_too_small_is_refused():
     D = lib()
-    B = Batch8("bf16", 8, 2, 128, 16, [1], [9000], tail=0)
+    B = Batch8("bf16", 8, 2, 128, 16, [1], [20000], tail=0)
     P = B.cuda(*B.appended())
     q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), B.table.cuda()
     o = torch.empty_like(q)
-    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 9000, *P)
+    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 20000, *P)
     assert need > 0
     with pytest.raises(D.DFlashError, match="workspace"):
-        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=9000,
+        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=20000,
                                workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
 
 
