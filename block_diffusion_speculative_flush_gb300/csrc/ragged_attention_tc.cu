@@ -26,6 +26,15 @@
 //          over 4096, 8 KV heads of 128: 5.8 TB/s with pages of 16 (TMA boxes of 4 KB
 //          are what limits it), 6.0 with pages of 64 (89% of a measured copy).  Few
 //          short items are latency: 15 us for one block of 16 tokens over 4096.
+//   KV8 (NQ = 2): an 8-bit cache.  Codes come by TMA, asked for by the scheduler warp; two warps (those of the
+//          producer and the fixer) make V's, and for heads of 64 K's, fp16 in the ring.  For heads of 128 K's codes are
+//          multiplied as they are (kind::f8f6f4) with q as a sum of two e4m3 numbers, the softmax warps' first
+//          work on a stretch, so that K takes a quarter of the room and no conversion.  The softmax takes the
+//          scales (softmax_tile8).  4 x 2048 new rows over 6000 tokens, 32 over 8 heads of 128: 0.84 ms, 1.12
+//          PFLOP/s (57% of a measured cuBLAS peak), heads of 64 0.69; 6 chunks of 145 to 477 rows over 1.9k to 4.8k
+//          136 us, 0.69 PFLOP/s (whole items, two or one a CTA, leave a sixth of the SMs' time empty).
+//          Bound by the softmax of two tiles in turn: with the softmax left out 0.69 ms, the converters 0.84, a
+//          half or seven eighths of either product 0.86; the products alone are 0.48.
 // V rows of hidden keys may hold anything, and 0 * NaN is NaN: in tiles with
 // hidden keys the fixer zeroes the rows behind the sequence and puts non-finite
 // numbers in the others to 0; the softmax warps then add those to the rows that
@@ -97,10 +106,9 @@ struct Work {
 
 // Scales of an 8-bit tile's keys, a pair for each 16 of them.
 struct __align__(16) TileScales {
-  float ks[KT / 16], vs[KT / 16];
-  float most_v;    // the largest of vs
-  int32_t mixed;   // not all alike
-  int32_t pad[2];
+  float2 key[KT / 16];  // K's, log2 of V's (-200: none)
+  float most;           // the largest of V's logarithms
+  int32_t pad[3];
 };
 
 template <int D, int NQ, bool KV8 = false>
@@ -108,12 +116,13 @@ struct Cfg {
   static constexpr int SLOT = KT * D * 2;                 // one K or V tile, one Q tile
   // 128 bytes of 32 rows for each softmax warp (NQ = 1: in the Q tile it has done with)
   static constexpr int STAGE = NQ == 2 ? 8 * 4096 : 0;
-  // 8 bits: tiles of codes on their way to the converters, K and V, or only V where K is multiplied as it is (K8:
-  // its tiles are 3 of the ring's entries then, V's as fp16 the other 2)
+  // 8 bits: NC tiles of codes on their way to the converters, of K and V in turn, or only of V where K is multiplied
+  // as it is (K8: its tiles are 2 of the ring's entries then, V's as fp16 the other 2)
   static constexpr bool K8 = KV8 && D == 128;
-  static constexpr int CODES = K8 ? KT * D : KV8 ? 2 * KT * D : 0;
-  static constexpr int RING = K8 ? 5 : (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
-  static constexpr int RING_BYTES = K8 ? 3 * KT * D + 2 * SLOT : RING * SLOT;
+  static constexpr int NC = K8 ? 2 : 4;
+  static constexpr int CODES = KV8 ? NC * KT * D : 0;
+  static constexpr int RING = K8 ? 4 : (7 * 32768 - STAGE - CODES) / SLOT - 2;  // K/V tiles in flight
+  static constexpr int RING_BYTES = K8 ? 2 * KT * D + 2 * SLOT : RING * SLOT;
   static constexpr int DATA = 2 * SLOT + RING_BYTES + STAGE + CODES;  // 224 KB
   static constexpr int THREADS = (4 * NQ + 4) * 32;
   // NQ = 2: registers of the softmax warps and of the other four; the launch's
@@ -123,7 +132,7 @@ struct Cfg {
   static constexpr int EXTRA = 768;  // barriers and descriptors
   // scales of as many tiles as the ring holds, the one that is being read and the next
   static constexpr int NSCALES = 8;
-  static constexpr size_t SMEM = DATA + EXTRA + (KV8 ? NSCALES * sizeof(TileScales) + 4 * 8 : 0);
+  static constexpr size_t SMEM = DATA + EXTRA + (KV8 ? NSCALES * sizeof(TileScales) + 2 * NC * 8 : 0);
 };
 
 __device__ __forceinline__ float max3(float a, float b, float c) {
@@ -455,37 +464,20 @@ __device__ __noinline__ bool softmax_tile_call(const TileArgs a, float& m, float
   return softmax_tile<D, 1>(a, m, l, pv_done, parity, abort_flag);
 }
 
-// The same over an 8-bit cache (NQ = 2): scores of the codes times the key's scale, P in
-// fp16 as p (vs / u) 2^7, u the largest scale of V so far.  p <= 2^8, so P <= 2^15.
+// The same over an 8-bit cache (NQ = 2): scores of the codes times the key's scale, P in fp16 as p (vs / u) 2^7, u
+// the largest scale of V so far.  p <= 2^8, so P <= 2^15.  The scales come for 16 keys at a time and cost next to
+// nothing: K's goes into the factor of its keys' scores (their maximum is taken before, the scale is
+// positive), V's as a logarithm into the exponent, and l takes the sum of each 16 P's by the inverse of their
+// weight.  (Two multiplications for each pair of keys, in a form of their own for tiles of several scales: 979 us
+// where tiles of one scale took 793, 4 x 2048 rows over 8000.)  lu: log2 u.  A weight below 2^-64 is taken as that: P
+// is 0 in fp16 either way, and l does not lose the keys.
 // a.sl2: scale log2(e) 2^-e of the row.
-constexpr float kUnit8 = 128.f;
-__device__ __forceinline__ uint64_t mul2(uint64_t x, uint64_t y) {
-  uint64_t z;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(z) : "l"(x), "l"(y));
-  return z;
-}
+constexpr float kUnitLog8 = 7.f, kNoUnit = -1000.f;
 template <int D>
-__device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScales& ts, float& m, float& l, float& unit) {
+__device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScales& ts, float& m, float& l, float& lu) {
   float s[128];
   fence_after();
   tmem_ld128(a.tS, s);
-  const bool mixed = ts.mixed != 0;
-  float k = a.sl2;
-  if (mixed) {
-#pragma unroll
-    for (int q = 0; q < KT / 16; ++q) {
-      const float f = ts.ks[q];
-      const uint64_t f2 = f2pack(f, f);
-#pragma unroll
-      for (int j = 0; j < 16; j += 2) {
-        const float2 v = f2unpack(mul2(f2pack(s[16 * q + j], s[16 * q + j + 1]), f2));
-        s[16 * q + j] = v.x;
-        s[16 * q + j + 1] = v.y;
-      }
-    }
-  } else {
-    k *= ts.ks[0];
-  }
   if (a.masked_hi) {
 #pragma unroll
     for (int c = 0; c < 128; c += 32) {
@@ -499,22 +491,27 @@ __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScale
 #pragma unroll
     for (int j = 0; j < 128; ++j) s[j] = j >= a.lo ? s[j] : -INFINITY;
   }
-  float m0 = s[0], m1 = s[1], m2 = s[2], m3 = s[3];
+  // (never 0 nor infinite: a hidden key's -inf stays one, and a score of 0 is 0)
+  float kq[KT / 16];
 #pragma unroll
-  for (int j = 4; j < 124; j += 8) {
-    m0 = max3(m0, s[j], s[j + 1]);
-    m1 = max3(m1, s[j + 2], s[j + 3]);
-    m2 = max3(m2, s[j + 4], s[j + 5]);
-    m3 = max3(m3, s[j + 6], s[j + 7]);
+  for (int q = 0; q < KT / 16; ++q) kq[q] = fminf(fmaxf(a.sl2 * ts.key[q].x, 1.17549435e-38f), 3.4e38f);
+  float mt = -INFINITY;
+#pragma unroll
+  for (int q = 0; q < KT / 16; ++q) {
+    const float* v = s + 16 * q;
+    float m0 = max3(v[0], v[1], v[2]), m1 = max3(v[3], v[4], v[5]);
+    m0 = max3(m0, v[6], v[7]);
+    m1 = max3(m1, v[8], v[9]);
+    m0 = max3(m0, v[10], v[11]);
+    m1 = max3(m1, v[12], v[13]);
+    m0 = max3(m0, v[14], v[15]);
+    mt = fmaxf(mt, fmaxf(m0, m1) * kq[q]);
   }
-  m0 = max3(m0, s[124], s[125]);
-  m1 = max3(m1, s[126], s[127]);
-  const float mt = fmaxf(fmaxf(m0, m1), fmaxf(m2, m3)) * k;
   const bool grow = a.valid && mt > m + 8.f, first = m == -INFINITY;
-  const float most_v = ts.most_v;
-  if (__any_sync(0xffffffffu, (grow && !first) || (most_v > unit && unit > 0.f))) {
-    const float fm = grow && !first ? ex2(m - mt) : 1.f;
-    const float f = most_v > unit && unit > 0.f ? fm * (unit / most_v) : fm;
+  const float most = ts.most, was = lu;
+  lu = fmaxf(lu, most);
+  if (__any_sync(0xffffffffu, (grow && !first) || (lu > was && was > kNoUnit))) {
+    const float fm = grow && !first ? ex2(m - mt) : 1.f, f = fm * ex2(fmaxf(was - lu, -140.f));
 #pragma unroll 1
     for (int c = 0; c < D; c += 32) {
       float o[32];
@@ -525,53 +522,30 @@ __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScale
     }
     l *= fm;
   }
-  unit = fmaxf(unit, most_v);
   if (grow) m = mt;
   const float mref = m == -INFINITY ? 0.f : m;
-  const bool weigh = mixed || ts.vs[0] != unit;
-  // where all scales of V are the unit, 2^7 goes into the exponent
-  const uint64_t k2 = f2pack(k, k);
-  const float c1 = weigh ? -mref : 7.f - mref;
-  const uint64_t c2 = f2pack(c1, c1);
-  uint64_t sum0 = f2pack(0.f, 0.f), sum1 = sum0;
-  const float to_unit = unit > 0.f ? kUnit8 / unit : 0.f;
-  // (both forms whole: a branch at each pair took three times the time of its arithmetic)
-  auto probs = [&](auto weighted, int c) {  // 32 keys
+#pragma unroll
+  for (int c = 0; c < 128; c += 32) {
     uint32_t pk[16];
 #pragma unroll
     for (int g = 0; g < 2; ++g) {
-      float w = 1.f;
-      if constexpr (decltype(weighted)::value) w = ts.vs[c / 16 + g] * to_unit;
+      const float k = kq[c / 16 + g], w = kUnitLog8 + fmaxf(ts.key[c / 16 + g].y - lu, -64.f);
+      const uint64_t k2 = f2pack(k, k), c2 = f2pack(w - mref, w - mref);
+      uint64_t sum = f2pack(0.f, 0.f);
 #pragma unroll
       for (int j = 8 * g; j < 8 * g + 8; ++j) {
         uint64_t e2;
         asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(e2) : "l"(f2pack(s[c + 2 * j], s[c + 2 * j + 1])), "l"(k2), "l"(c2));
-        const float2 e = f2unpack(e2);
-        uint64_t p2 = f2pack(ex2(e.x), ex2(e.y));
-        if (j & 1) asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum1) : "l"(p2));
-        else asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum0) : "l"(p2));
-        if constexpr (decltype(weighted)::value) p2 = mul2(p2, f2pack(w, w));
-        const float2 p = f2unpack(p2);
+        const float2 e = f2unpack(e2), p = make_float2(ex2(e.x), ex2(e.y));
+        asm("add.rn.f32x2 %0, %0, %1;" : "+l"(sum) : "l"(f2pack(p.x, p.y)));
         const __half2 h2 = __floats2half2_rn(p.x, p.y);
         pk[j] = *reinterpret_cast<const uint32_t*>(&h2);
       }
+      const float2 both = f2unpack(sum);
+      l = fmaf(both.x + both.y, ex2(-w), l);
     }
     tmem_st16u(a.tS + c / 2, pk);
-  };
-  if (weigh) {
-    probs(std::true_type(), 0);
-    probs(std::true_type(), 32);
-    probs(std::true_type(), 64);
-    probs(std::true_type(), 96);
-  } else {
-    probs(std::false_type(), 0);
-    probs(std::false_type(), 32);
-    probs(std::false_type(), 64);
-    probs(std::false_type(), 96);
   }
-  const float2 s0 = f2unpack(sum0), s1 = f2unpack(sum1);
-  const float sum = (s0.x + s0.y) + (s1.x + s1.y);
-  l += weigh ? sum : sum * (1.f / kUnit8);
 }
 
 // A NaN among V's codes that the converters put to 0, given to the rows that see it (as
@@ -739,22 +713,22 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
   uint32_t* tmem_slot = (uint32_t*)(all_done + 1);
   volatile int* abort_flag = (volatile int*)(tmem_slot + 1);
   Work* works = (Work*)(tmem_slot + 2);
-  // 8 bits: scales of the last tiles, the K and the V tile of codes, and (in place of what the fixer
+  // 8 bits: scales of the last tiles, the tiles of codes, and (in place of what the fixer
   // signals) Q as fp16
   uint8_t* sC = sS + C::STAGE;
   TileScales* tscales = (TileScales*)(sC + C::CODES + C::EXTRA);
   uint64_t* c_full = (uint64_t*)(tscales + C::NSCALES);
-  uint64_t* c_empty = c_full + 2;
+  uint64_t* c_empty = c_full + C::NC;
   uint64_t* q_ready = v_fix;
   static_assert((3 * 12 + 10 + 2 * NW + 1) * 8 + 8 + NW * sizeof(Work) <= 768, "barriers and descriptors");
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int G = a.Hq / a.Hkv;
   // entry i of the ring (K tiles even, V tiles odd): its slot, how often that was used before, where it lies
   constexpr bool K8 = C::K8;
-  auto r_slot = [](uint32_t i) { return K8 ? ((i & 1u) ? 3u + ((i >> 1) & 1u) : (i >> 1) % 3u) : i % RING; };
-  auto r_use = [](uint32_t i) { return K8 ? ((i & 1u) ? i >> 2 : (i >> 1) / 3u) : i / RING; };
+  auto r_slot = [](uint32_t i) { return K8 ? (i & 1u) * 2u + ((i >> 1) & 1u) : i % RING; };
+  auto r_use = [](uint32_t i) { return i / RING; };
   auto r_addr = [&](uint32_t slot) {
-    if (K8) return sR + (slot < 3u ? slot * (KT * D) : 3u * (KT * D) + (slot - 3u) * SLOT);
+    if (K8) return sR + (slot < 2u ? slot * (KT * D) : 2u * (KT * D) + (slot - 2u) * SLOT);
     return sR + slot * SLOT;
   };
 
@@ -770,10 +744,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       mbar_init(&s_full[s], 1);
       mbar_init(&p_full[s], 4);
       mbar_init(&pv_done[s], 1);
-      if (KV8) {
-        mbar_init(&c_full[s], 1);
-        mbar_init(&c_empty[s], 2);
-      }
+    }
+    for (int s = 0; KV8 && s < C::NC; ++s) {
+      mbar_init(&c_full[s], 1);
+      mbar_init(&c_empty[s], 2);
     }
     for (int s = 0; s < NW; ++s) {
       mbar_init(&w_full[s], 1);
@@ -808,10 +782,10 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     if constexpr (KV8) {
       // ---- converters: tiles of codes, which come by TMA, as fp16 into the ring.  A thread has 16 codes
       // of each of N keys.
-      constexpr int PIECES = D / 16, KEYS = 64 / PIECES, N = KT / KEYS, H = 2;  // H pieces at a time (188 us; 4: 191, 8: 198)
+      constexpr int PIECES = D / 16, KEYS = 64 / PIECES, N = KT / KEYS, H = 2;  // H pieces at a time (more code is fetched anew more often)
       const int cw = warp == SW ? 0 : 1, ct = cw * 32 + lane, piece = ct % PIECES, key = ct / PIECES;
       r.table = after_wait(r.table);
-      uint32_t it = 0, c_use = 0;
+      uint32_t it = 0, c_it = 0;  // tiles of the ring, of codes
       bool ok = true;
       // where the piece's two 16-byte chunks lie in a tile, less the key's row (keys of a thread agree mod 8).
       // D = 128: lanes of the second block store their chunks in turn, so that no two of a phase meet in a bank.
@@ -862,17 +836,9 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         // the tile (K8: as one of the two arrivals that it takes, the copy's being the other)
         auto put_scales = [&](int t) {
           TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
-          const float k0 = __shfl_sync(0xffffffffu, ks, 0), v0 = __shfl_sync(0xffffffffu, vs, 0);
-          const bool mixed = __any_sync(0xffffffffu, lane < KT / 16 && !(ks == k0 && vs == v0));
-          const float most = warp_max(lane < KT / 16 ? vs : 0.f);
-          if (lane < KT / 16) {
-            ts.ks[lane] = ks;
-            ts.vs[lane] = vs;
-          }
-          if (lane == 0) {
-            ts.most_v = most;
-            ts.mixed = mixed;
-          }
+          const float lv = vs > 0.f ? log2f(vs) : -200.f, most = warp_max(lane < KT / 16 ? lv : -200.f);
+          if (lane < KT / 16) ts.key[lane] = make_float2(ks, lv);
+          if (lane == 0) ts.most = most;
           look_up(t + 1, ahead);
           ahead = entry_of(t + 2);
           if (K8) {
@@ -891,7 +857,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
 #pragma unroll 1
         for (int u = K8 ? 1 : 0; u < 2 * T; u += K8 ? 2 : 1) {
           const int t = u >> 1, v = u & 1, kt = (tile0 + t) * KT;
-          const uint32_t e = it + u;
+          const uint32_t e = it + u, cs = c_it % C::NC;
           if (K8 && cw == 0 && t + 1 < T) {
             if (!wait_empty(e + 1)) {
               ok = false;
@@ -900,16 +866,13 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
             put_scales(t + 1);
           }
           // the ring's entry is free, and the codes are there
-          if (!wait_empty(e) || !__all_sync(0xffffffffu, mbar_wait(&c_full[v], c_use & 1u, abort_flag))) {
+          if (!wait_empty(e) || !__all_sync(0xffffffffu, mbar_wait(&c_full[cs], c_it / C::NC & 1u, abort_flag))) {
             ok = false;
             break;
           }
           uint8_t* tile = r_addr(r_slot(e));
-          if (v == 0) {
-            if (cw == 0) put_scales(t);
-          } else {
-            ++c_use;
-          }
+          ++c_it;
+          if (v == 0 && cw == 0) put_scales(t);
           // keys that a row does not see (slots behind the sequence hold anything): 0 x NaN is NaN, such codes of V
           // become 0 here and are given to the rows that see them at the stretch's end (only for row tiles
           // that take this product)
@@ -918,7 +881,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           for (int i0 = 0; i0 < N; i0 += H) {
             uint4 q[H];
 #pragma unroll
-            for (int i = 0; i < H; ++i) q[i] = *reinterpret_cast<const uint4*>(sC + (K8 ? 0 : v * (KT * D)) + ((i0 + i) * 64 + ct) * 16);
+            for (int i = 0; i < H; ++i) q[i] = *reinterpret_cast<const uint4*>(sC + cs * (KT * D) + ((i0 + i) * 64 + ct) * 16);
             if (edge) {
               uint32_t found = 0;
 #pragma unroll
@@ -942,7 +905,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           fence_proxy_async();
           __syncwarp();
           if (lane == 0) {
-            mbar_arrive(&c_empty[v]);
+            mbar_arrive(&c_empty[cs]);
             mbar_arrive(&full[r_slot(e)]);
           }
         }
@@ -960,7 +923,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
     int k = 0;
     bool ok = true;
     // 8 bits: this warp asks for the tiles too, Q and then K and V in turn (a copy per lane, the box of a page)
-    uint32_t q_use[2] = {0, 0}, c_use[2] = {0, 0}, k_it = 0;  // (k_it: K8, the ring's entry of the next K tile)
+    uint32_t q_use[2] = {0, 0}, c_it = 0, k_it = 0;  // (k_it: K8, the ring's entry of the next K tile)
     Work last;
     auto produce = [&](const Work& w) {
       if constexpr (KV8) {
@@ -984,15 +947,15 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
           const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, mine)) * page_rows * D;
           for (int v = 0; v < 2; ++v) {
             const bool direct = K8 && v == 0;  // into the ring
-            uint64_t *const there = direct ? &full[r_slot(k_it)] : &c_full[v], *const free_ = direct ? &empty[r_slot(k_it)] : &c_empty[v];
-            const uint32_t use = direct ? r_use(k_it) : c_use[v];
+            const uint32_t cs = c_it % C::NC, use = direct ? r_use(k_it) : c_it / C::NC;
+            uint64_t *const there = direct ? &full[r_slot(k_it)] : &c_full[cs], *const free_ = direct ? &empty[r_slot(k_it)] : &c_empty[cs];
             if (use > 0 && !__all_sync(0xffffffffu, mbar_wait(free_, (use - 1) & 1u, abort_flag))) {
               ok = false;
               return;
             }
-            uint8_t* const to = direct ? r_addr(r_slot(k_it)) : sC + (K8 ? 0 : v * (KT * D));
+            uint8_t* const to = direct ? r_addr(r_slot(k_it)) : sC + cs * (KT * D);
             if (direct) k_it += 2;
-            else ++c_use[v];
+            else ++c_it;
             if (lane == 0) mbar_expect_tx(there, bytes);
             __syncwarp();
             if (mine)
@@ -1159,10 +1122,12 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       for (int x = 0; x < 2; ++x) {
         while (q_use[x] > 0 && !mbar_try_wait(&q_full[x], (q_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
-        while (c_use[x] > 0 && !mbar_try_wait(&c_full[x], (c_use[x] - 1) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
+      }
+      for (uint32_t i = c_it > C::NC ? c_it - C::NC : 0; i < c_it; ++i) {
+        while (!mbar_try_wait(&c_full[i % C::NC], i / C::NC & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
       }
-      for (uint32_t i = k_it > 6 ? k_it - 6 : 0; i < k_it; i += 2) {  // (K8: the arrival of its scales may be missing)
+      for (uint32_t i = k_it > 4 ? k_it - 4 : 0; i < k_it; i += 2) {  // (K8: the arrival of its scales may be missing)
         while (!mbar_try_wait(&full[r_slot(i)], r_use(i) & 1u) && globaltimer_ns() - t0 < kWaitLimitNs) {
         }
       }
@@ -1282,29 +1247,45 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       return ok;
     };
     auto ring_full = [&](uint32_t i) { return wait(&full[r_slot(i)], r_use(i)); };
-    // (8 bits: with one more stream of instructions in the SM, the converters', code is fetched anew all the
-    // time, and loops are faster: chunked prefill 188 -> 173 us)
-    constexpr int MMA_UNROLL = KV8 ? 1 : 8;
+    // (8 bits: the converters are one more stream of instructions in the SM, and code is fetched anew all the time; a
+    // loop that is too short issues too slowly.  Chunked prefill with one, four and eight MMAs a turn: 143, 137, 140 us,
+    // with both descriptors put together for each 163.)
+    constexpr int MMA_UNROLL = 4;
     auto issue_s = [&](int qbuf, uint32_t st, int sbuf) {
       const uint32_t q0 = smem_u32(sQ + qbuf * SLOT), k0 = smem_u32(r_addr(st)), tS = tmem + sbuf * 128;
       if constexpr (K8) {  // both pieces of q (q_to_e4m3) times K's codes
-#pragma unroll 1
-        for (int ks = 0; ks < 2 * (D / 32); ++ks)
-          umma_e4m3_warp(tS, sdesc_sw128(q0 + ks / (D / 32) * (SLOT / NB) + ks % (D / 32) * 32),
-                         sdesc_sw128(k0 + ks % (D / 32) * 32), idS, ks > 0 ? 1u : 0u);
-      }
+        constexpr int N = D / 32;
+        const uint32_t qd = (uint32_t)sdesc_sw128(q0), kd = (uint32_t)sdesc_sw128(k0);
+        constexpr uint32_t hi = (uint32_t)(sdesc_sw128(0) >> 32);
 #pragma unroll(MMA_UNROLL)
-      for (int ks = 0; ks < (K8 ? 0 : D / 16); ++ks) {
-        umma_bf16_warp(tS, sdesc_sw128(q0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32),
-                       sdesc_sw128(k0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
+        for (int ks = 0; ks < 2 * N; ++ks)
+          umma_e4m3_warp_lo(tS, qd + ks / N * (SLOT / NB / 16) + ks % N * 2, kd + ks % N * 2, hi, idS, ks > 0 ? 1u : 0u);
+      } else if constexpr (KV8) {
+        const uint32_t qd = (uint32_t)sdesc_sw128(q0), kd = (uint32_t)sdesc_sw128(k0);
+        constexpr uint32_t hi = (uint32_t)(sdesc_sw128(0) >> 32);
+#pragma unroll(MMA_UNROLL)
+        for (int ks = 0; ks < D / 16; ++ks) umma_bf16_warp_lo(tS, qd + ks * 2, kd + ks * 2, hi, idS, ks > 0 ? 1u : 0u);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < D / 16; ++ks) {
+          umma_bf16_warp(tS, sdesc_sw128(q0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32),
+                         sdesc_sw128(k0 + (ks >> 2) * (SLOT / NB) + (ks & 3) * 32), idS, ks > 0 ? 1u : 0u);
+        }
       }
       umma_commit_warp(&s_full[sbuf]);
     };
     auto issue_pv = [&](int x, uint32_t st, int sbuf, bool first) {
       const uint32_t v0 = smem_u32(r_addr(st)), tP = tmem + sbuf * 128, tO = tmem + O_COL + x * D;
+      if constexpr (KV8) {
+        const uint32_t vd = (uint32_t)sdesc_sw128_mn(v0, SLOT / NB);
+        constexpr uint32_t hi = (uint32_t)(sdesc_sw128_mn(0, SLOT / NB) >> 32);
 #pragma unroll(MMA_UNROLL)
-      for (int ks = 0; ks < KT / 16; ++ks) {
-        umma_bf16_ts_warp(tO, tP + ks * 8, sdesc_sw128_mn(v0 + ks * 2048, SLOT / NB), idPV, first && ks == 0 ? 0u : 1u);
+        for (int ks = 0; ks < KT / 16; ++ks) umma_bf16_ts_warp_lo(tO, tP + ks * 8, vd + ks * 128, hi, idPV, first && ks == 0 ? 0u : 1u);
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < KT / 16; ++ks) {
+          umma_bf16_ts_warp(tO, tP + ks * 8, sdesc_sw128_mn(v0 + ks * 2048, SLOT / NB), idPV, first && ks == 0 ? 0u : 1u);
+        }
       }
     };
     int k = 0;
@@ -1519,7 +1500,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
-      float unit = 0.f, row_sl2 = 0.f;  // 8 bits: the unit of V's scales, the row's factor of scores
+      float lu = kNoUnit, row_sl2 = 0.f;  // 8 bits: log2 of the unit of V's scales, the row's factor of scores
       if constexpr (KV8) {
         if (T > 0) {
           if (!__all_sync(0xffffffffu, mbar_wait(&q_full[x], q_cnt & 1u, abort_flag))) {
@@ -1561,7 +1542,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         if (live) {
           const TileArgs ta{tmem + lrow + sb * 128, tO, hi - kt_of(t), lo - kt_of(t), hi_min < kt_of(t) + KT, lo_max > kt_of(t),
                             valid, KV8 ? row_sl2 : sl2};
-          if constexpr (KV8) softmax_tile8<D>(ta, tscales[((it >> 1) + t) % C::NSCALES], m, l, unit);
+          if constexpr (KV8) softmax_tile8<D>(ta, tscales[((it >> 1) + t) % C::NSCALES], m, l, lu);
           else if constexpr (NQ == 1) ok = softmax_tile_call<D>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
           else ok = softmax_tile<D, NQ>(ta, m, l, &pv_done[x], (cnt - 1) & 1u, abort_flag);
           if (!ok) break;
@@ -1603,7 +1584,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       const bool staged = NQ == 2 || (live && p.mode != kModeCluster && __popc(rows) > 8);
       if (NQ == 1 && T > 0 && !staged && lane == 0) mbar_arrive_relaxed(&q_empty[q_used & 1u]);
       if (live) {
-        const float o_unit = KV8 ? unit * (1.f / kUnit8) : 1.f;
+        const float o_unit = KV8 ? exp2f(lu - kUnitLog8) : 1.f;
         const float inv = o_unit / l;  // (every row sees its own key: l is 0 only where all scores are -inf)
         if (NQ == 1 && p.mode == kModeCluster) {
 #pragma unroll 1

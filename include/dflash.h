@@ -761,8 +761,8 @@ DFLASH_API int dflash_kv8_append(const dflash_kv8_pages* pages, const dflash_rag
 /* dflash_paged_attention over such pages: the same call, masks, layout of heads and
  * treatment of what a row does not see; dtype (of q and out) fp32 or bf16, head_dim the
  * pages'.  A bf16 call with head_dim 64 or 128 rounds the probabilities to fp16 for the
- * second product; with head_dim 128 and more than 64 rows (max_rows x n_q_heads / n_kv_heads) it also
- * takes q as a sum of two e4m3 numbers (exact but for elements below 2^-9 of the row's largest, which
+ * second product; with head_dim 128 and more than 32 rows (max_rows x n_q_heads / n_kv_heads) it may
+ * also take q as a sum of two e4m3 numbers (exact but for elements below 2^-9 of the row's largest, which
  * are off by at most 2^-17 of that), where an infinity counts as NaN.  Other calls keep fp32. */
 DFLASH_API int64_t dflash_kv8_attention_workspace(const dflash_attention* a, const dflash_ragged* batch,
                                                   const dflash_kv8_pages* pages);

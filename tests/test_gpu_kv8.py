@@ -279,6 +279,33 @@ def test_scales_far_apart(dtype, d, rows):
     check_attention(out, lse, ref8(B, True, 0, pages=(kp, vp, ks, vs)), B.starts[-1])
 
 
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("rows", [[1, 2], [30, 9], [140, 3]])
+@pytest.mark.parametrize("far", [0, 60])
+def test_scales_that_are_no_powers_of_two(dtype, d, rows, far):
+    """Any positive scales (a cache that another program filled), within 2^-60 .. 2^60."""
+    B = Batch8(dtype, 4, 2, d, 16, rows, [500, 200], seed=15)
+    kp, vp, ks, vs = B.appended()
+    g = torch.Generator().manual_seed(2)
+    ks *= 1 + torch.rand(ks.shape, generator=g)
+    vs *= (1 + torch.rand(vs.shape, generator=g)) * torch.exp2(torch.randint(-far // 2, far // 2 + 1, vs.shape, generator=g).float())
+    out, lse, _ = run8(B, True, 0, append=False, pages=B.cuda(kp, vp, ks, vs))
+    check_attention(out, lse, ref8(B, True, 0, pages=(kp, vp, ks, vs)), B.starts[-1])
+
+
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("rows", [[3], [40], [150]])
+@pytest.mark.parametrize("window", [0, 50])
+def test_scores_that_vanish(dtype, d, rows, window):
+    """Queries of 2^-100 and a small scale: every factor of a score underflows, the mask holds all the same."""
+    B = Batch8(dtype, 4, 1, d, 16, rows, [300], seed=33)
+    B.q = B.q * 2.0 ** -100
+    kp, vp, ks, vs = B.appended()
+    ks = ks * 0 + 2.0 ** -60
+    out, lse, _ = run8(B, True, window, scale=2.0 ** -20, append=False, pages=B.cuda(kp, vp, ks, vs))
+    check_attention(out, lse, ref8(B, True, window, scale=2.0 ** -20, pages=(kp, vp, ks, vs)), B.starts[-1])
+
+
 @pytest.mark.parametrize("dtype,hq,hkv", [("bf16", 24, 1), ("bf16", 128, 1), ("bf16", 100, 2), ("f32", 24, 1)])
 @pytest.mark.parametrize("rows,lens", [([1, 2], [200, 150]), ([7, 30], [77, 300])])
 def test_wide_groups(dtype, hq, hkv, rows, lens):
