@@ -23,7 +23,7 @@
 // Work, in one of two ways, by the host's bounds:
 //   ranges   the 16-key chunks of all (sequence, tile of rows, KV head) items one after another, cut
 //            into even ranges, one per CTA; the parts of a cut item meet in k_kv8_few_merge;
-//   cluster  few items of few chunks: a thread-block cluster an item, an even share of its chunks each,
+//   cluster  where no item's chunks are too many: a thread-block cluster an item, an even share of its chunks each,
 //            the parts meet in distributed shared memory (one launch, nothing to search).
 // The 8 warps of a CTA take its chunks in turn and meet in shared memory.  The order of every
 // sum is fixed by the lengths.
@@ -43,13 +43,16 @@ namespace {
 constexpr int kChunk = 16;  // keys of a chunk: never more than a page
 constexpr int kWarps = 8;
 constexpr int kMaxCluster = 8;
-constexpr int kMaxShare = 128;  // chunks of a CTA of a cluster
+constexpr int kFewRows = 32;   // of a sequence and KV head, for this kernel in any case
+constexpr int kMaxShare = 256;  // chunks of a CTA of a cluster where all run at once
+constexpr int kSorted = 256;    // sequences that are put in order
 namespace cg = cooperative_groups;
 constexpr float kSlack = 4.f, kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kUnit = 1024.f;  // 2^10, of P in fp16
 
 struct FewPlan {
   int32_t cluster;    // CTAs of an item; 0: ranges
+  int32_t in_turn;    // cluster: more CTAs than run at once
   int32_t tiles;      // cluster: tiles of rows that a sequence may have
   int32_t pad;        // what the start of an item costs, in chunks
   int32_t min_units;  // chunks that a CTA gets at least
@@ -559,7 +562,29 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
     // ---- rank q of the cluster takes an even share of the item's chunks; the ranks finish its rows in turn
     cg::cluster_group cl = cg::this_cluster();
     const int N = plan.cluster, item = cta / N, q = cta - item * N, rest = item / a.Hkv, kvh = item - rest * a.Hkv;
-    const int b = rest / plan.tiles, rt = rest - b * plan.tiles;
+    const int turn = rest / plan.tiles, rt = rest - turn * plan.tiles;
+    // Items that wait for their turn go longest first: sequence b is the turn-th by chunks.
+    int b = turn;
+    if (plan.in_turn && r.batch <= kSorted) {
+      int* size = reinterpret_cast<int*>(smem);  // [kSorted]
+      int* found = size + kSorted;
+      int mine = -1;
+      if (tid < r.batch) {
+        const Seq s = load_seq(r, tid);
+        mine = s.ok && s.n > 0 ? few_chunks(s, a.window) : 0;
+      }
+      size[tid] = mine;
+      __syncthreads();
+      if (tid < r.batch) {
+        int before = 0;
+#pragma unroll 4
+        for (int j = 0; j < r.batch; ++j) before += size[j] > mine || (size[j] == mine && j < tid);
+        if (before == turn) *found = tid;
+      }
+      __syncthreads();
+      b = *found;
+      __syncthreads();  // (the ring begins here)
+    }
     const Seq s = load_seq(r, b);
     if (!s.ok && tid == 0 && rt == 0 && kvh == 0 && q == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
     const int R = s.ok ? (int)max((int64_t)0, min((int64_t)RB, (int64_t)s.n * G - (int64_t)rt * RB)) : 0;
@@ -719,19 +744,27 @@ struct FewHost {
   int nb;
   FewPlan p;
 };
-// CTAs of a cluster per item, or 0 for ranges: where all items run at once and no CTA has more than
-// kMaxShare chunks.  32 over 8 heads of 128, one user's single token: 6.6 us over 300 tokens (ranges 12.3), 10.7
-// over 4000 (22.4), 19 over 16000 (27); 8 users over 8000, 4 CTAs an item: 28 (43); 32 over 2000, 1 CTA: 26 (41).
-// A longer share would gain as much for even lengths, but one long sequence among short ones has the CTAs
-// of its own items only.
-int few_cluster(const Ragged& r, const AttnCall& a, int tiles, int ctas) {
+// CTAs of a cluster per item, or 0 for ranges.  A cut item costs its rows' start and end again, and a launch that
+// puts the parts together; 32 over 8 heads of 128, single tokens but for the last:
+//   all at once, the largest share of a CTA kMaxShare (36 of 8 CTAs fit, not 38: 12 and 20 us).  One user over 300
+//     tokens 6.6 us (ranges 12.3), over 16000 19 (27); 8 users over 8000 28 (43), over 16000 48 (64).
+//   in turn, longest first, so that the last to end are short: one CTA an item while the longest (by the bound of
+//     lengths) has at most 300 chunks for each item that a CTA's place gets, two up to 1000.  64 users over 1k to 16k
+//     with one, two, four CTAs and ranges 134, 115, 142, 133 us (in the batch's order 150, 133, 136), over 1k to 8k
+//     75, 88, 111, 91, over 100 to 2k 21, 38, 62, 33; 128 over 1k to 16k 227, 260, 313, 270; 128 blocks of 8 over 1k
+//     to 8k 298, 381, 549, 365.
+int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int ctas) {
   const int64_t items = (int64_t)r.batch * tiles * a.Hkv;
   const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
   const int64_t chunks = (span + kChunk - 1) / kChunk + 1;
   int cluster = 0;
-  for (int n = 1; n <= kMaxCluster && items * n <= ctas; n *= 2)
+  for (int n = 1; n <= kMaxCluster && items * n <= (n == 8 ? ctas * 15 / 16 : ctas); n *= 2)
     if (chunks <= kMaxShare * n) cluster = n;
   while (cluster > 1 && chunks <= 4 * cluster) cluster /= 2;
+  if (!cluster && items > ctas && rows <= kFewRows && items <= INT32_MAX / 8) {
+    const int64_t turn = items * 300 / ctas;
+    cluster = chunks <= turn ? 1 : 3 * chunks <= 10 * turn ? 2 : 0;
+  }
   return cluster;
 }
 FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
@@ -740,16 +773,19 @@ FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
   // what an item costs besides its chunks; 64 single tokens over 1k to 16k: 4 158 us, 16 151, 28 133, 44 133
   h.p.pad = 28;
   h.p.min_units = 8;
+  h.nb = rows <= 8 ? 1 : 2;
+  h.p.tiles = (rows + 8 * h.nb - 1) / (8 * h.nb);
+  h.p.cluster = few_cluster(r, a, rows, h.p.tiles, 2 * sms);
+  h.p.in_turn = h.p.cluster && (int64_t)r.batch * h.p.tiles * a.Hkv * h.p.cluster > 2 * sms;
+  h.p.slots = 4 * sms;
   // A tile of rows converts the codes anew, so 32 rows a CTA (one an SM) where ranges are cut: 64 users' blocks of 8
-  // over 2048 tokens 132 us (16 rows 156), 8 users' 43 (49).  16 where they run as clusters, whose items then
-  // spread over twice the CTAs: one user's block of 16 over 4096 18.4 us (32 rows 35).
-  for (h.nb = rows <= 8 ? 1 : 2;; h.nb = 4) {
-    const int rb = 8 * h.nb, ctas = sms * (h.nb <= 2 ? 2 : 1);
-    h.p.tiles = (rows + rb - 1) / rb;
-    h.p.slots = 2 * ctas;
-    h.p.cluster = few_cluster(r, a, h.p.tiles, ctas);
-    if (h.p.cluster || rows <= 16 || h.nb == 4) return h;
+  // over 2048 tokens 132 us (16 rows 156), 8 users' 43 (49).
+  if (!h.p.cluster && rows > 16) {
+    h.nb = 4;
+    h.p.tiles = (rows + 31) / 32;
+    h.p.slots = 2 * sms;
   }
+  return h;
 }
 
 template <int D, int NB>
@@ -786,7 +822,7 @@ cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, in
 // or all items run at once as clusters.  32 over 8 heads of 128, this and the tiles: 64 sequences of 32 rows over 2048
 // 132 and 188 us, of 64 rows 231 and 189; 8 of 32 over 16000 101 and 150, of 48 160 and 151; one user's 64 rows over
 // 4096 in clusters 18 and 36, 128 over 500 13 and 24.
-bool kv8_few(const Ragged& r, const AttnCall& a, int sms) { return rows_of(r, a) <= 32 || few_plan(r, a, sms).p.cluster > 0; }
+bool kv8_few(const Ragged& r, const AttnCall& a, int sms) { return rows_of(r, a) <= kFewRows || few_plan(r, a, sms).p.cluster > 0; }
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms) {
   const FewHost h = few_plan(r, a, sms);
   return h.p.cluster ? 0 : (int64_t)h.p.slots * 8 * h.nb * (a.d + 2) * 4;

@@ -102,10 +102,26 @@ def bound(B):
     return 1 << 15 if rows * (B.hq // B.hkv) > 32 else rows
 
 
+WIDE = False
+
+
+@pytest.fixture(params=["tight", "wide"])
+def span(request):
+    """wide: a table that could hold 200000 tokens a row, with which few rows' work is laid out as ranges."""
+    global WIDE
+    WIDE = request.param == "wide"
+    yield
+    WIDE = False
+
+
+def widen(table, page):
+    return torch.nn.functional.pad(table, (0, 200000 // page), value=-1) if WIDE else table
+
+
 def run8(B, causal, window, scale=None, max_len=None, append=True, status=None, pages=None, max_rows=None):
     D = lib()
     P = B.cuda(B.kp, B.vp, B.ks, B.vs) if pages is None else pages
-    starts, lens, table = i32(B.starts), i32(B.lens), B.table.cuda()
+    starts, lens, table = i32(B.starts), i32(B.lens), widen(B.table, B.page).cuda()
     if append:
         D.dflash_kv8_append(B.k.cuda(), B.v.cuda(), *P, starts, lens, table, status=status)
     q = B.q.cuda()
@@ -137,6 +153,7 @@ SHAPES = [  # hq, hkv, page, rows, lens
 ]
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("f32", 128), ("bf16", 64), ("bf16", 128), ("bf16", 48), ("f32", 16)])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 37), (False, 130)])
 @pytest.mark.parametrize("shape", range(len(SHAPES)))
@@ -189,6 +206,7 @@ def test_append_at_the_borders_of_a_scale():
             assert same_scales(dev[2], scale) and same_scales(dev[3], scale), (first, second)
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 37)])
 @pytest.mark.parametrize("rows,lens,hq,hkv", [([40], [600], 4, 1), ([33, 1, 90], [33, 1000, 400], 5, 1),
@@ -200,6 +218,7 @@ def test_many_rows_of_short_calls(rows, lens, hq, hkv, causal, window, d):
     check_attention(out, lse, ref8(B, causal, window, many=False), sum(rows))
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
 @pytest.mark.parametrize("rows,lens", [([16], [5000]), ([1] * 9, [1, 4096, 5, 2999, 64, 128, 127, 129, 1000]),
                                        ([300, 2, 150], [2100, 3000, 150])])
@@ -209,6 +228,7 @@ def test_attention_over_long_caches(dtype, rows, lens):
     check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows,hq", [([1, 1, 1], 2), ([20, 9, 1], 4), ([3, 3, 2], 16)])
 def test_attention_with_many_key_tiles(rows, hq, d):
@@ -217,6 +237,7 @@ def test_attention_with_many_key_tiles(rows, hq, d):
     check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows,lens,hq", [([16], [3000], 4), ([1, 5], [900, 2000], 8), ([200, 90], [900, 700], 4),
                                           ([3] * 20, [1000 + 13 * b for b in range(20)], 8)])
@@ -247,6 +268,7 @@ def test_hidden_codes_that_are_nan(dtype, d, rows, lens, hq):
                              ref[3][last:last + 1]), 1)
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[1], [3], [40], [150]])
 def test_a_nan_that_a_row_sees(dtype, d, rows):
@@ -266,6 +288,7 @@ def test_a_nan_that_a_row_sees(dtype, d, rows):
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(lse).all())
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[1, 2], [30, 9], [140, 3]])
 def test_scales_far_apart(dtype, d, rows):
@@ -279,6 +302,7 @@ def test_scales_far_apart(dtype, d, rows):
     check_attention(out, lse, ref8(B, True, 0, pages=(kp, vp, ks, vs)), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[1, 2], [30, 9], [140, 3]])
 @pytest.mark.parametrize("far", [0, 60])
@@ -293,6 +317,7 @@ def test_scales_that_are_no_powers_of_two(dtype, d, rows, far):
     check_attention(out, lse, ref8(B, True, 0, pages=(kp, vp, ks, vs)), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[3], [40], [150]])
 @pytest.mark.parametrize("window", [0, 50])
@@ -306,6 +331,7 @@ def test_scores_that_vanish(dtype, d, rows, window):
     check_attention(out, lse, ref8(B, True, window, scale=2.0 ** -20, pages=(kp, vp, ks, vs)), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,hq,hkv", [("bf16", 24, 1), ("bf16", 128, 1), ("bf16", 100, 2), ("f32", 24, 1)])
 @pytest.mark.parametrize("rows,lens", [([1, 2], [200, 150]), ([7, 30], [77, 300])])
 def test_wide_groups(dtype, hq, hkv, rows, lens):
@@ -314,6 +340,7 @@ def test_wide_groups(dtype, hq, hkv, rows, lens):
     check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,scale,big", [("bf16", 1e-30, 1e30), ("bf16", 1e20, 1e-22), ("f32", 1e-30, 1e30)])
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [[1], [40], [200]])
@@ -324,6 +351,7 @@ def test_queries_and_scales_of_any_size(dtype, scale, big, d, rows):
     check_attention(out, lse, ref8(B, True, 0, scale=scale), rows[0])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[2, 1], [100, 20]])
 def test_missing_pages_read_as_zeros_and_are_told(dtype, d, rows):
@@ -441,17 +469,18 @@ def test_two_graphs_replayed_at_once(dtype, rows):
 
 def test_a_workspace_that_is_too_small_is_refused():
     D = lib()
-    B = Batch8("bf16", 8, 2, 128, 16, [1], [20000], tail=0)
+    B = Batch8("bf16", 8, 2, 128, 16, [1], [900], tail=0)
     P = B.cuda(*B.appended())
-    q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), B.table.cuda()
+    q, st, ln, tb = B.q.cuda(), i32(B.starts), i32(B.lens), torch.nn.functional.pad(B.table, (0, 2500), value=-1).cuda()
     o = torch.empty_like(q)
-    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 20000, *P)
+    need = D.dflash_kv8_attention_workspace(q, o, st, ln, tb, 1, 40000, *P)
     assert need > 0
     with pytest.raises(D.DFlashError, match="workspace"):
-        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=20000,
+        D.dflash_kv8_attention(q, *P, st, ln, tb, o, 1, max_len=40000,
                                workspace=torch.empty(need - 1, dtype=torch.uint8, device="cuda"))
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("rows", [[1], [12], [30], [200]])
 def test_queries_with_elements_far_apart(d, rows):
@@ -464,6 +493,7 @@ def test_queries_with_elements_far_apart(d, rows):
     check_attention(out, lse, ref8(B, True, 0), rows[0])
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("bits", [math.nan, math.inf])
 @pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
 @pytest.mark.parametrize("rows", [[1], [30], [150]])
@@ -501,6 +531,7 @@ def test_a_stream_of_its_own_and_a_strided_cache():
     check_attention(out, lse, ref8(B, True, 0), 6)
 
 
+@pytest.mark.usefixtures("span")
 @pytest.mark.parametrize("rows,lens", [([1] * 5, [300, 1, 900, 17, 2000]), ([40, 90], [500, 400])])
 def test_the_same_call_twice_gives_the_same_bits(rows, lens):
     B = Batch8("bf16", 8, 2, 128, 16, rows, lens, seed=41)
@@ -511,6 +542,20 @@ def test_the_same_call_twice_gives_the_same_bits(rows, lens):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
 
 
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("batch,hkv,most", [(90, 4, 3), (70, 8, 1), (50, 8, 12), (257, 2, 2)])
+def test_items_that_take_turns(batch, hkv, most, d):
+    """More items than run at once, of uneven lengths, some of them alike and some without rows."""
+    rows = [(b * 5) % (most + 1) for b in range(batch)]
+    lens = [max(r, (b * 131) % 700 // 50 * 50) for b, r in enumerate(rows)]
+    B = Batch8("bf16", 2 * hkv, hkv, d, 16, rows, lens, seed=47)
+    out, lse, _ = run8(B, True, 0)
+    check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
+    out, lse, _ = run8(B, True, 100)
+    check_attention(out, lse, ref8(B, True, 100), B.starts[-1])
+
+
+@pytest.mark.usefixtures("span")
 def test_many_short_sequences():
     """More sequences than a warp looks at in one go, most of them of a few tokens, some without new rows."""
     rows = [(b * 7) % 3 for b in range(300)]
