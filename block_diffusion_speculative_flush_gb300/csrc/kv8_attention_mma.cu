@@ -749,7 +749,8 @@ struct FewHost {
 //   all at once, the largest share of a CTA kMaxShare (36 of 8 CTAs fit, not 38: 12 and 20 us).  One user over 300
 //     tokens 6.6 us (ranges 12.3), over 16000 19 (27); 8 users over 8000 28 (43), over 16000 48 (64).
 //   in turn, longest first, so that the last to end are short: one CTA an item while the longest (by the bound of
-//     lengths) has at most 300 chunks for each item that a CTA's place gets, two up to 1000.  64 users over 1k to 16k
+//     lengths) has at most 300 chunks for each item that a CTA's place gets, two up to 1000, and where items are
+//     fewer than places four up to 2400: 16 users over 1k to 16k 38 us (ranges 46), 24 53 (62).  64 users over 1k to 16k
 //     with one, two, four CTAs and ranges 134, 115, 142, 133 us (in the batch's order 150, 133, 136), over 1k to 8k
 //     75, 88, 111, 91, over 100 to 2k 21, 38, 62, 33; 128 over 1k to 16k 227, 260, 313, 270; 128 blocks of 8 over 1k
 //     to 8k 298, 381, 549, 365.
@@ -761,9 +762,9 @@ int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int cta
   for (int n = 1; n <= kMaxCluster && items * n <= (n == 8 ? ctas * 15 / 16 : ctas); n *= 2)
     if (chunks <= kMaxShare * n) cluster = n;
   while (cluster > 1 && chunks <= 4 * cluster) cluster /= 2;
-  if (!cluster && items > ctas && rows <= kFewRows && items <= INT32_MAX / 8) {
+  if (!cluster && rows <= kFewRows && items <= INT32_MAX / 8) {
     const int64_t turn = items * 300 / ctas;
-    cluster = chunks <= turn ? 1 : 3 * chunks <= 10 * turn ? 2 : 0;
+    cluster = chunks <= turn ? 1 : 3 * chunks <= 10 * turn ? 2 : items <= ctas && chunks <= 8 * turn ? 4 : 0;
   }
   return cluster;
 }
