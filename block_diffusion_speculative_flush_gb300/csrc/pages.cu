@@ -156,17 +156,26 @@ __global__ void __launch_bounds__(256) k_pages_reorder(int32_t* refs, int n_page
   const int32_t* src = from.table + (int64_t)max(parent, 0) * from.stride;
   int32_t* dst = to.table + (int64_t)row * to.stride;
   const int end = gives ? pages : to.width;
-  for (int j = lane; j < end; j += 32) {
-    int e = j < pages ? src[j] : -1;
-    if (j < pages) {
-      if (e >= 0 && e < n_pages) {
-        atomicAdd(refs + e, gives ? -1 : 1);
-      } else {
-        bad |= gives && len == 0 ? 0 : DFLASH_STATUS_PAGE;
-        e = -1;
+  constexpr int U = 8;  // entries in flight
+  for (int j0 = lane; j0 < end; j0 += 32 * U) {
+    int es[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) es[u] = j0 + 32 * u < pages ? src[j0 + 32 * u] : -1;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int j = j0 + 32 * u;
+      if (j >= end) break;
+      int e = es[u];
+      if (j < pages) {
+        if (e >= 0 && e < n_pages) {
+          atomicAdd(refs + e, gives ? -1 : 1);
+        } else {
+          bad |= gives && len == 0 ? 0 : DFLASH_STATUS_PAGE;
+          e = -1;
+        }
       }
+      if (!gives) dst[j] = e;
     }
-    if (!gives) dst[j] = e;
   }
   if (!gives && lane == 0) to.lens[row] = len;
   if (bad) flag_status(status, bad);
@@ -250,10 +259,12 @@ __device__ __forceinline__ Ask ask_of(const Rows& t, const int32_t* new_lens, in
 }
 
 // One cluster.  A thread has a stretch of rows and a stretch of pages, both contiguous, so that ranks
-// are prefix sums over the threads.  Bound by latency: five cluster barriers and the loads between them.
+// are prefix sums over the threads.  Bound by latency: five cluster barriers and the loads between them (32 prompts
+// of 8 samples, with the reorder in front and the copies behind it: 26.7 us, 31.1 when rows and entries were read again
+// in each step and one at a time).
 // ONE: a small pool and little to copy, one CTA, whose working arrays are in shared memory and which makes
 // the copies itself: one launch in place of two.  A user's four candidates, 76 pages, 2 layers, with the reorder in
-// front: 13.3 us, 14.3 otherwise, and 20.6 against 23 of host time.
+// front: 12.1 us, some 13 otherwise, and 20.6 against 23 of host time.
 constexpr int kSmallPages = 2048, kSmallRows = 1024, kSmallBytes = 512 << 10;
 template <bool ONE>
 __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws,
@@ -302,42 +313,56 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
     }
   }
   sync();
-  // 2: who writes to begun pages
+  // 2: who writes to begun pages.  With a row per thread, what it has read of its row stays in registers.
+  const bool own = t.n <= threads;
+  Ask mine_a{0, 0, 0, 0, false, false};
+  int mine_page = -1, mine_refs = 0;
   for (int row = tid; row < t.n; row += threads) {
     const Ask a = ask_of(t, new_lens, row);
+    mine_a = a;
     if (!a.writes) continue;
-    const int p = *entry(row, a.have - 1);
-    if (there(p) && load_now(refs + p) > 1) {
+    const int p = *entry(row, a.have - 1), n = there(p) ? load_now(refs + p) : 0;
+    mine_page = p;
+    mine_refs = n;
+    if (n > 1) {
       atomicMin(ws.owner + p, row);
       atomicAdd(ws.writers + p, 1);
     }
   }
+  auto ask = [&](int row) { return own ? mine_a : ask_of(t, new_lens, row); };
   // meanwhile the free pages are counted and listed
   const int per_p = (n_pages + threads - 1) / threads, p0 = min(tid * (int64_t)per_p, (int64_t)n_pages), p1 = min(p0 + per_p, n_pages);
   int mine = 0;
-  for (int p = p0; p < p1; ++p) mine += load_now(refs + p) <= 0;
+  uint32_t which = 0;  // of up to 32
+#pragma unroll 4
+  for (int p = p0; p < p1; ++p) {
+    const bool is = load_now(refs + p) <= 0;
+    mine += is;
+    which |= (uint32_t)is << ((p - p0) & 31);
+  }
   Scan<ONE> fs{s_warps[0], &s_cta[0], 0, 0};
   fs.run((uint64_t)mine);  // (its barrier ends 2)
   {
     int at = (int)fs.prefix;
     if (mine)
       for (int p = p0; p < p1; ++p)
-        if (load_now(refs + p) <= 0) ws.free_[at++] = p;
+        if (per_p <= 32 ? (which >> (p - p0)) & 1u : load_now(refs + p) <= 0) ws.free_[at++] = p;
   }
   // 3: what each row needs
   const int per_r = (t.n + threads - 1) / threads, r0 = min(tid * (int64_t)per_r, (int64_t)t.n), r1 = min(r0 + per_r, t.n);
   auto copies = [&](int row, const Ask& a) {
     if (!a.writes) return false;
-    const int p = *entry(row, a.have - 1);
+    const int p = own ? mine_page : *entry(row, a.have - 1);
     if (!there(p)) return false;
-    const int n = load_now(refs + p);
+    const int n = own ? mine_refs : load_now(refs + p);
     return n > 1 && !(n == get(ws.writers + p) && get(ws.owner + p) == row);
   };
   uint64_t sum = 0;  // pages << 32 | copies
+  bool mine_c = false;
   for (int row = r0; row < r1; ++row) {
-    const Ask a = ask_of(t, new_lens, row);
+    const Ask a = ask(row);
     if (!a.ok) continue;
-    const bool c = copies(row, a);
+    const bool c = mine_c = copies(row, a);
     sum += (uint64_t)(max(a.need - a.have, 0) + c) << 32 | (uint64_t)c;
   }
   Scan<ONE> rs{s_warps[1], &s_cta[1], 0, 0};
@@ -351,15 +376,15 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
   uint32_t granted = 0, copied = 0;  // a bit per row of this thread
   int given = 0;
   for (int row = r0; row < r1; ++row) {
-    const Ask a = ask_of(t, new_lens, row);
+    const Ask a = ask(row);
     if (!a.ok) continue;
-    const int c = copies(row, a), n = max(a.need - a.have, 0) + c;
+    const int c = own ? mine_c : copies(row, a), n = max(a.need - a.have, 0) + c;
     if (n == 0 || pages + n <= n_free) {
       granted |= 1u << (row - r0);
       int64_t at = pages;
       if (c) {
         copied |= 1u << (row - r0);
-        ws.src[made] = *entry(row, a.have - 1);
+        ws.src[made] = own ? mine_page : *entry(row, a.have - 1);
         ws.dst[made] = get(ws.free_ + at++);
         ++made;
       }
@@ -383,12 +408,12 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
     if (!((granted >> (row - r0)) & 1u)) continue;
     if ((copied >> (row - r0)) & 1u) {
       const int p = ws.dst[made++];
-      int32_t* e = entry(row, pages_of(t.lens[row], t) - 1);
-      atomicSub(refs + *e, 1);
+      int32_t* e = entry(row, ask(row).have - 1);
+      atomicSub(refs + (own ? mine_page : *e), 1);
       refs[p] = 1;
       *e = p;
     }
-    t.lens[row] = new_lens[row];
+    t.lens[row] = ask(row).new_len;
   }
   if (bad) flag_status(status, bad);
 }
@@ -430,6 +455,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScanThreads)
   const int tid = (int)cl.block_rank() * kScanThreads + threadIdx.x, threads = kCluster * kScanThreads;
   const int per = (n_pages + threads - 1) / threads, p0 = min(tid * (int64_t)per, (int64_t)n_pages), p1 = min(p0 + per, n_pages);
   int mine = 0;
+#pragma unroll 4
   for (int p = p0; p < p1; ++p) mine += refs[p] > 0;
   Scan<false> us{s_warps[0], &s_cta[0], 0, 0};
   us.run((uint64_t)mine);
@@ -495,15 +521,20 @@ __global__ void __launch_bounds__(kCopyThreads) k_pages_compact_move(CopyList l,
       }
       const int32_t* s = from.table + (int64_t)row * from.stride;
       int32_t* d = into.table + (int64_t)row * into.stride;
-      for (int j = lane; j < from.width; j += 32) {
-        int e = -1;
-        if (j < pages) {
-          e = s[j];
-          if (e >= U && e < n_pages) e = to[e];
-          else if (e >= n_pages) e = -1;
-          if (e < 0) bad |= DFLASH_STATUS_PAGE;
+      constexpr int W = 4;  // entries in flight
+      for (int j0 = lane; j0 < from.width; j0 += 32 * W) {
+        int es[W];
+#pragma unroll
+        for (int u = 0; u < W; ++u) es[u] = j0 + 32 * u < pages ? s[j0 + 32 * u] : -1;
+#pragma unroll
+        for (int u = 0; u < W; ++u) es[u] = es[u] >= n_pages ? -1 : es[u] >= U ? to[es[u]] : es[u];
+#pragma unroll
+        for (int u = 0; u < W; ++u) {
+          const int j = j0 + 32 * u;
+          if (j >= from.width) break;
+          if (j < pages && es[u] < 0) bad |= DFLASH_STATUS_PAGE;
+          d[j] = max(es[u], -1);
         }
-        d[j] = max(e, -1);
       }
       __syncwarp();
       if (lane == 0) into.lens[row] = len;
