@@ -759,7 +759,7 @@ struct FewHost {
 //     fewer than places four up to 2400: 16 users over 1k to 16k 38 us (ranges 46), 24 53 (62).  64 users over 1k to 16k
 //     with one, two, four CTAs and ranges 134, 115, 142, 133 us (in the batch's order 150, 133, 136), over 1k to 8k
 //     75, 88, 111, 91, over 100 to 2k 21, 38, 62, 33; 128 over 1k to 16k 227, 260, 313, 270; 128 blocks of 8 over 1k
-//     to 8k 298, 381, 549, 365.
+//     to 8k 298, 381, 549, 365.  (A batch whose places are mostly empty has its few long sequences on few CTAs then.)
 int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int ctas) {
   const int64_t items = (int64_t)r.batch * tiles * a.Hkv;
   const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
@@ -769,8 +769,8 @@ int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int cta
     if (chunks <= kMaxShare * n) cluster = n;
   while (cluster > 1 && chunks <= 4 * cluster) cluster /= 2;
   if (!cluster && rows <= kFewRows && items <= INT32_MAX / 8) {
-    const int64_t turn = items * 300 / ctas;
-    cluster = chunks <= turn ? 1 : 3 * chunks <= 10 * turn ? 2 : items <= ctas && chunks <= 8 * turn ? 4 : 0;
+    const int64_t live = std::min<int64_t>(r.batch, std::max(r.total, 1)) * tiles * a.Hkv, turn = live * 300 / ctas;
+    cluster = chunks <= turn ? 1 : 3 * chunks <= 10 * turn ? 2 : live <= ctas && chunks <= 8 * turn ? 4 : 0;
   }
   return cluster;
 }
