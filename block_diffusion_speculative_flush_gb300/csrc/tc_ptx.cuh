@@ -152,18 +152,8 @@ __device__ __forceinline__ void umma_bf16_warp(uint32_t d_tmem, uint64_t adesc, 
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
       : "memory");
 }
-// kind::f8f6f4 with e4m3 A and B (idesc_f16's bits: format 0 is e4m3 there), 32 of K a product.
-__device__ __forceinline__ void umma_e4m3_warp(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                               uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, e;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "elect.sync _|e, 0xffffffff;\n\t"
-      "@e tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-// The same with descriptors that share their upper word (and K-major A and B), so that a step is an addition to the lower one.
+// The same with descriptors that share their upper word, so that a step is an addition to the lower one: K-major A and
+// B, with kind::f8f6f4 e4m3 (idesc_f16's bits: format 0 is e4m3 there, 32 of K a product), and with A from tensor memory.
 __device__ __forceinline__ void umma_bf16_warp_lo(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                                   uint32_t accumulate) {
   asm volatile(
