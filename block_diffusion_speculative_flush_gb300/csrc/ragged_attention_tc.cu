@@ -556,7 +556,7 @@ __device__ __noinline__ void add_nan8(Ragged r, Kv8View kv, const Work& w, uint3
   const int lane = threadIdx.x & 31, T = max(w.nt[0], w.nt[1]);
   for (int t = 0; t < T; ++t) {
     const int kt = (w.t0 + t) * KT, in = min(KT, w.len - kt);
-    if (kt >= w.clean_lo && kt + in <= w.clean_hi) {  // and so are all up to the edge
+    if (kt >= w.clean_lo && kt + KT <= w.clean_hi) {  // what the converters left alone; and so are all up to the edge
       t = max(t, w.clean_hi / KT - 1 - w.t0);
       continue;
     }

@@ -568,3 +568,29 @@ def test_many_short_sequences():
         want = B.appended()
         assert same_codes(P[0], want[0]) and same_scales(P[3], want[3])
         check_attention(out, lse, ref8(B, True, 0), B.starts[-1])
+
+
+# ---- a NaN among V's codes in the last, partial tile of keys
+@pytest.mark.usefixtures("span")
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("causal,window", [(False, 0), (False, 50), (True, 0), (True, 50)])
+@pytest.mark.parametrize("rows,lens", [([40], [400]), ([65], [400]), ([150], [400]), ([1], [400]), ([33, 2], [130, 257])])
+@pytest.mark.parametrize("back", [0, 7])
+def test_a_nan_in_the_last_tile_reaches_who_sees_it(dtype, d, causal, window, rows, lens, back):
+    B = Batch8(dtype, 4, 1, d, 16, rows, lens, seed=51, tail=0)
+    kp, vp, ks, vs = B.appended()
+    ref = ref8(B, causal, window, pages=(kp, vp, ks, vs))
+    v2 = vp.clone()
+    at = [L - 1 - back for L in lens]
+    for b, p in enumerate(at):
+        v2[int(B.table[b, p // 16]), p % 16, 0, 17] = 0x7F
+    out, lse, _ = run8(B, causal, window, append=False, pages=B.cuda(kp, v2, ks, vs))
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        pos = torch.arange(L - n, L)
+        see = (pos >= at[b] if causal else torch.ones(n, dtype=torch.bool)) & (pos - at[b] < window if window else True)
+        got = torch.isnan(out[B.starts[b]:B.starts[b + 1], :, 17].cpu())
+        assert torch.equal(got, see[:, None].expand_as(got)), (b, got[:, 0].tolist(), see.tolist())
+    o = torch.where(torch.isnan(out), ref[0].to(out), out)
+    check_attention(o, lse, ref, sum(rows))
+    rest = [c for c in range(d) if c != 17]
+    assert bool(torch.isfinite(out[..., rest]).all())
