@@ -41,6 +41,9 @@ __device__ __forceinline__ uint16_t f2_to_e4m3x2(float a, float b) {
 // Bit 7 of each byte that is a NaN, and the word with those bytes 0.
 __device__ __forceinline__ uint32_t nan_codes(uint32_t w) { return ((w & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u; }
 __device__ __forceinline__ uint32_t without_nan(uint32_t w) { return w & ~((nan_codes(w) >> 7) * 0xffu); }
+// log2 of a scale as the kernels add it to exponents; that of a page that is missing (its codes are zeros): the smallest.
+constexpr float kNoScaleLog2 = -60.f;
+__device__ __forceinline__ float scale_log2(float s) { return s > 0.f ? log2f(s) : kNoScaleLog2; }
 // whether x is not finite (from its bits: fast-math flags do not change that)
 __device__ __forceinline__ bool nonfinite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
 

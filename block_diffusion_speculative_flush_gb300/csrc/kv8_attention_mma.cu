@@ -15,10 +15,13 @@
 // Numbers.  q is scaled by a power of two for its row, so that its largest element lies in
 // [2^14, 2^15): fp16 holds bf16's 8 bits for elements down to 2^-29 of that, an error that
 // fp32 sums of such products have too.  Scores: (S ks) (scale 2^-e log2 e), fp32.  P is
-// rounded to fp16 once, as p r 2^10 with p <= 2^4 (the maximum moves only when it grew by more)
-// and r = vs / u <= 1, u the largest scale of V so far: half a step is 2^-12 of it, below its
-// smallest normal number 2^-25 of 2^10, that is 2^-35 of what the largest scale and
-// probability give.  m, l, O and merges are fp32.
+// rounded to fp16 once, as p (vs / u) 2^10 with p = 2^(s - m) <= 2^4 (the maximum moves only when it grew
+// by more).  u is a row's own: the largest p vs of the keys that it sees was between u and 2^4 u when the row met it,
+// so neither a scale that it does not see nor one with next to no probability takes bits from the others.
+// Half a step is 2^-11 of P or less, below fp16's smallest normal number 2^-25, that is 2^-35 of the row's largest p vs.
+// V's scale is a logarithm in the exponent of P, which l takes back: what it adds is P by the inverse of its weight.
+// A weight below 2^-64 is taken as that: P is 0 in fp16 either way, and l does not lose the keys (scales lie
+// up to 2^120 apart).  m, l, O and merges are fp32.
 //
 // Work, in one of two ways, by the host's bounds (few_cluster):
 //   cluster  a thread-block cluster of 1 to 8 CTAs per (sequence, tile of rows, KV head) item, an even share of
@@ -54,7 +57,8 @@ constexpr int kMaxShare = 256;  // chunks of a CTA of a cluster where all run at
 constexpr int kSorted = 256;    // sequences that are put in order
 namespace cg = cooperative_groups;
 constexpr float kSlack = 4.f, kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
-constexpr float kUnit = 1024.f;  // 2^10, of P in fp16
+constexpr float kUnitLog2 = 10.f;  // of P in fp16
+constexpr float kNoMax = -3.402823466e38f, kNoUnit = -1000.f;  // before the first key: finite, so that no difference is a NaN
 
 struct FewPlan {
   int32_t cluster;    // CTAs of an item; 0: ranges
@@ -191,7 +195,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
   float* part_o = reinterpret_cast<float*>(smem + C::MEET);       // [RB][D] this CTA's sums (cluster)
   uint2* s_qf = reinterpret_cast<uint2*>(smem + C::AREA);         // [NB][KS][32]
   float* s_rowf = reinterpret_cast<float*>(smem + C::AREA + C::QF);  // [RB]
-  float2* scales = reinterpret_cast<float2*>(s_rowf + RB) + warp * C::SCALES;  // (ks, vs) of a chunk's page
+  float2* scales = reinterpret_cast<float2*>(s_rowf + RB) + warp * C::SCALES;  // ks, log2 vs of a chunk's page
   float2* s_ml = reinterpret_cast<float2*>(s_rowf + RB) + kWarps * C::SCALES;  // [warps][RB]
   float2* part_ml = s_ml + kWarps * RB;                           // [RB]
   pdl_trigger();
@@ -227,7 +231,7 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           vs = kv.vs[pg * kv.s_page + kvh * kv.s_head];
         }
       }
-      scales[i % C::SCALES] = make_float2(ks, vs);
+      scales[i % C::SCALES] = make_float2(ks, scale_log2(vs));
     };
     // What this lane copies: 16 bytes of every RI-th row, as many lanes side by side as a row has, so that memory
     // sees whole rows (32 bytes of four rows in eight lanes, the pieces that a lane multiplies, reached half the
@@ -333,16 +337,16 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
       rowf[0][0] = __shfl_sync(0xffffffffu, f, 8 * t);
       rowf[0][1] = __shfl_sync(0xffffffffu, f, 8 * t + 4);
     }
-    float o[NB][MT][4], m[NB][2], l[NB][2], unit = 0.f, per_unit = 0.f;  // per_unit: 2^10 / unit
-    float ref[NB][2];  // what scores are taken from: m, or 0 as long as that is -inf
+    float o[NB][MT][4], m[NB][2], l[NB][2], lu[NB][2];  // lu: log2 of the unit of p vs
 #pragma unroll
     for (int n = 0; n < NB; ++n) {
 #pragma unroll
       for (int k = 0; k < MT; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) o[n][k][j] = 0.f;
-      m[n][0] = m[n][1] = -INFINITY;
-      l[n][0] = l[n][1] = ref[n][0] = ref[n][1] = 0.f;
+      m[n][0] = m[n][1] = kNoMax;
+      lu[n][0] = lu[n][1] = kNoUnit;
+      l[n][0] = l[n][1] = 0.f;
     }
     uint32_t from = 0;  // the stage that is read next
     auto scores = [&](const uint8_t* stage, const float2& sc, float (*x)[4]) {
@@ -403,18 +407,13 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
           for (int j = 0; j < 4; ++j)
             if (!sees(n, j, key0 + g + (j >> 1) * 8)) x[n][j] = -INFINITY;
       }
-      // ---- the maximum moves when a score is more than 2^kSlack above it; the unit when V's scale is above it
-      bool grow = sc.y > unit;
+      // ---- the maximum and the unit move when a score, or p vs, is more than 2^kSlack above them
+      bool grow = false;
 #pragma unroll
-      for (int n = 0; n < NB; ++n) {
-        grow |= fmaxf(x[n][0], x[n][2]) > m[n][0] + kSlack;
-        grow |= fmaxf(x[n][1], x[n][3]) > m[n][1] + kSlack;
-      }
+      for (int n = 0; n < NB; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) grow |= fmaxf(x[n][j], x[n][j + 2]) - m[n][j] + fmaxf(sc.y - lu[n][j], 0.f) > kSlack;
       if (__any_sync(0xffffffffu, grow)) {
-        const float was = unit;
-        if (sc.y > unit) unit = 2.f * sc.y;  // (some room, so that it does not move again at once)
-        const float fu = was > 0.f ? was / unit : 1.f;
-        per_unit = unit > 0.f ? kUnit / unit : 0.f;
 #pragma unroll
         for (int n = 0; n < NB; ++n)
 #pragma unroll
@@ -423,31 +422,34 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-            const float mn = mx > m[n][j] + kSlack ? mx : m[n][j];
-            const float f = m[n][j] == -INFINITY ? 1.f : ex2(m[n][j] - mn);  // (sums so far are 0 or NaN there)
+            // the unit so far, from the new maximum: O stays what it is where that will do.  (Before the first key
+            // sums are 0 or NaN, and their factors 0.)
+            const float mn = mx > m[n][j] + kSlack ? mx : m[n][j], shift = m[n][j] - mn, was = lu[n][j] + shift;
+            const float top = mx - mn + sc.y, unit = top > was + kSlack ? top : was, f = ex2(was - unit);
             m[n][j] = mn;
-            ref[n][j] = mn == -INFINITY ? 0.f : mn;
-            l[n][j] *= f;
+            lu[n][j] = unit;
+            l[n][j] *= ex2(shift);
 #pragma unroll
             for (int k = 0; k < MT; ++k) {
-              o[n][k][j] *= f * fu;
-              o[n][k][j + 2] *= f * fu;
+              o[n][k][j] *= f;
+              o[n][k][j + 2] *= f;
             }
           }
       }
       // ---- P, its sums, and P^T as the second product's operand
-      const float rv = sc.y * per_unit;
       uint32_t pb[NB][2];
 #pragma unroll
       for (int n = 0; n < NB; ++n) {
         float p[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          p[j] = ex2(x[n][j] - ref[n][j & 1]);
-          l[n][j & 1] += p[j];
+        for (int j = 0; j < 2; ++j) {
+          const float w = fmaxf(sc.y - lu[n][j], -64.f) + kUnitLog2, c = w - m[n][j];
+          p[j] = ex2(x[n][j] + c);
+          p[j + 2] = ex2(x[n][j + 2] + c);
+          l[n][j] = fmaf(p[j] + p[j + 2], ex2(-w), l[n][j]);
         }
-        pb[n][0] = transpose8(pack_h2(p[0] * rv, p[1] * rv));
-        pb[n][1] = transpose8(pack_h2(p[2] * rv, p[3] * rv));
+        pb[n][0] = transpose8(pack_h2(p[0], p[1]));
+        pb[n][1] = transpose8(pack_h2(p[2], p[3]));
       }
       // ---- O^T
       uint32_t vw[4][VW];
@@ -523,9 +525,9 @@ __global__ void __launch_bounds__(kWarps * 32, FewCfg<D, NB>::CTAS) k_kv8_few(Ra
         sum += __shfl_xor_sync(0xffffffffu, sum, 8);
         sum += __shfl_xor_sync(0xffffffffu, sum, 16);
         const int row = 8 * n + 2 * t + j;
-        if (g == 0) s_ml[warp * RB + row] = part_stats(m[n][j], sum);
+        if (g == 0) s_ml[warp * RB + row] = part_stats(m[n][j] == kNoMax ? -INFINITY : m[n][j], sum);
         float* dst = meet + (warp * RB + row) * C::LO + VB * g;
-        const float f = unit * (1.f / kUnit);
+        const float f = ex2(lu[n][j] - kUnitLog2);
 #pragma unroll
         for (int k = 0; k < MT; k += 2)
           *reinterpret_cast<float4*>(dst + 2 * k) =

@@ -106,7 +106,7 @@ struct Work {
 
 // Scales of an 8-bit tile's keys, a pair for each 16 of them.
 struct __align__(16) TileScales {
-  float2 key[KT / 16];  // K's, log2 of V's (-200: none)
+  float2 key[KT / 16];  // K's, log2 of V's
   float most;           // the largest of V's logarithms
   int32_t pad[3];
 };
@@ -464,13 +464,15 @@ __device__ __noinline__ bool softmax_tile_call(const TileArgs a, float& m, float
   return softmax_tile<D, 1>(a, m, l, pv_done, parity, abort_flag);
 }
 
-// The same over an 8-bit cache (NQ = 2): scores of the codes times the key's scale, P in fp16 as p (vs / u) 2^7, u
-// the largest scale of V so far.  p <= 2^8, so P <= 2^15.  The scales come for 16 keys at a time and cost next to
-// nothing: K's goes into the factor of its keys' scores (their maximum is taken before, the scale is
-// positive), V's as a logarithm into the exponent, and l takes the sum of each 16 P's by the inverse of their
-// weight.  (Two multiplications for each pair of keys, in a form of their own for tiles of several scales: 979 us
-// where tiles of one scale took 793, 4 x 2048 rows over 8000.)  lu: log2 u.  A weight below 2^-64 is taken as that: P
-// is 0 in fp16 either way, and l does not lose the keys.
+// The same over an 8-bit cache (NQ = 2): scores of the codes times the key's scale, P in fp16 as p (vs / u) 2^7.  u is
+// the row's own: the largest p vs of the keys that it sees was between u and 2^8 u when the row met it, so P <= 2^15,
+// and neither a scale that the row does not see nor one with next to no probability takes bits from the others.  The
+// tile's largest scale bounds p vs; only where that is above 2^8 u are the 16 keys' own looked at.  The scales
+// come for 16 keys at a time and cost next to nothing: K's goes into the factor of its keys' scores (their maximum is
+// taken before, the scale is positive), V's as a logarithm into the exponent, and l takes the sum of each 16 P's by
+// the inverse of their weight.  (Two multiplications for each pair of keys, in a form of their own for tiles of
+// several scales: 979 us where tiles of one scale took 793, 4 x 2048 rows over 8000.)  lu: log2 u, from m.  A weight
+// below 2^-64 is taken as that: P is 0 in fp16 either way, and l does not lose the keys.
 // a.sl2: scale log2(e) 2^-e of the row.
 constexpr float kUnitLog8 = 7.f, kNoUnit = -1000.f;
 template <int D>
@@ -495,7 +497,7 @@ __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScale
   float kq[KT / 16];
 #pragma unroll
   for (int q = 0; q < KT / 16; ++q) kq[q] = fminf(fmaxf(a.sl2 * ts.key[q].x, 1.17549435e-38f), 3.4e38f);
-  float mt = -INFINITY;
+  float mt = -INFINITY, top[KT / 16];
 #pragma unroll
   for (int q = 0; q < KT / 16; ++q) {
     const float* v = s + 16 * q;
@@ -505,24 +507,33 @@ __device__ __forceinline__ void softmax_tile8(const TileArgs& a, const TileScale
     m0 = max3(m0, v[10], v[11]);
     m1 = max3(m1, v[12], v[13]);
     m0 = max3(m0, v[14], v[15]);
-    mt = fmaxf(mt, fmaxf(m0, m1) * kq[q]);
+    top[q] = fmaxf(m0, m1) * kq[q];
+    mt = fmaxf(mt, top[q]);
   }
-  const bool grow = a.valid && mt > m + 8.f, first = m == -INFINITY;
-  const float most = ts.most, was = lu;
-  lu = fmaxf(lu, most);
-  if (__any_sync(0xffffffffu, (grow && !first) || (lu > was && was > kNoUnit))) {
-    const float fm = grow && !first ? ex2(m - mt) : 1.f, f = fm * ex2(fmaxf(was - lu, -140.f));
-#pragma unroll 1
-    for (int c = 0; c < D; c += 32) {
-      float o[32];
-      tmem_ld32(a.tO + c, o);
+  // (NaN, which is no growth, where both are -inf)
+  if (__any_sync(0xffffffffu, a.valid && mt - m + fmaxf(ts.most - lu, 0.f) > 8.f)) {
+    const bool grow = a.valid && mt > m + 8.f, first = m == -INFINITY;
+    const float mn = grow ? mt : m, base = mn == -INFINITY ? 0.f : mn, shift = grow && !first ? m - mn : 0.f;
+    float pv = -INFINITY;  // log2 of the largest p vs
 #pragma unroll
-      for (int j = 0; j < 32; ++j) o[j] *= f;
-      tmem_st32(a.tO + c, o);
+    for (int q = 0; q < KT / 16; ++q) pv = fmaxf(pv, top[q] - base + ts.key[q].y);
+    const float was = lu + shift;  // the unit so far, from the new maximum: O stays what it is where that will do
+    const bool move = a.valid && pv > was + 8.f;
+    lu = move ? pv : was;
+    if (__any_sync(0xffffffffu, move && !first)) {
+      const float f = move && !first ? ex2(was - lu) : 1.f;
+#pragma unroll 1
+      for (int c = 0; c < D; c += 32) {
+        float o[32];
+        tmem_ld32(a.tO + c, o);
+#pragma unroll
+        for (int j = 0; j < 32; ++j) o[j] *= f;
+        tmem_st32(a.tO + c, o);
+      }
     }
-    l *= fm;
+    l *= ex2(shift);
+    m = mn;
   }
-  if (grow) m = mt;
   const float mref = m == -INFINITY ? 0.f : m;
 #pragma unroll
   for (int c = 0; c < 128; c += 32) {
@@ -836,7 +847,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
         // the tile (K8: as one of the two arrivals that it takes, the copy's being the other)
         auto put_scales = [&](int t) {
           TileScales& ts = tscales[((it >> 1) + t) % C::NSCALES];
-          const float lv = vs > 0.f ? log2f(vs) : -200.f, most = warp_max(lane < KT / 16 ? lv : -200.f);
+          const float lv = scale_log2(vs), most = warp_max(lane < KT / 16 ? lv : kNoScaleLog2);
           if (lane < KT / 16) ts.key[lane] = make_float2(ks, lv);
           if (lane == 0) ts.most = most;
           look_up(t + 1, ahead);
@@ -1500,7 +1511,7 @@ __global__ void __launch_bounds__(Cfg<D, NQ, KV8>::THREADS, 1)
       const int lo_max = __reduce_max_sync(0xffffffffu, lo);
       const int T = w.nt[x], nt_other = w.nt[x ^ 1];
       float m = -INFINITY, l = 0.f;
-      float lu = kNoUnit, row_sl2 = 0.f;  // 8 bits: log2 of the unit of V's scales, the row's factor of scores
+      float lu = kNoUnit, row_sl2 = 0.f;  // 8 bits: log2 of the unit of p vs, the row's factor of scores
       if constexpr (KV8) {
         if (T > 0) {
           if (!__all_sync(0xffffffffu, mbar_wait(&q_full[x], q_cnt & 1u, abort_flag))) {

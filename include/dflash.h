@@ -732,8 +732,8 @@ DFLASH_API int dflash_rope(const dflash_rope_table* table, const dflash_ragged* 
  * no infinities, 0x7f and 0xff are NaN) with one fp32 scale per page and KV head,
  * of K and of V: value = code * scale.  Codes lie as in dflash_kv_pages, strides in
  * codes (bytes); the scale of page p and head h is at p * scale_page_stride + h *
- * scale_head_stride floats.  Scales are finite and positive (attention is exact
- * to its type for scales in 2^-60 .. 2^60, which is what append writes). */
+ * scale_head_stride floats.  Scales are finite and positive (what attention says of
+ * its errors holds for scales in 2^-60 .. 2^60, which is what append writes). */
 typedef struct dflash_kv8_pages {
   int32_t n_kv_heads;
   int32_t head_dim;     /* a multiple of 16 up to 128 */
@@ -760,8 +760,9 @@ DFLASH_API int dflash_kv8_append(const dflash_kv8_pages* pages, const dflash_rag
                                  const dflash_heads* k, const dflash_heads* v, void* stream);
 /* dflash_paged_attention over such pages: the same call, masks, layout of heads and
  * treatment of what a row does not see; dtype (of q and out) fp32 or bf16, head_dim the
- * pages'.  A bf16 call with head_dim 64 or 128 rounds the probabilities to fp16 for the
- * second product; with head_dim 128 and more than 32 rows (max_rows x n_q_heads / n_kv_heads) it may
+ * pages'.  A bf16 call with head_dim 64 or 128 rounds each probability times its key's scale of V to
+ * fp16 for the second product, off by at most 2^-11 of itself, or 2^-32 of the largest such number among the
+ * keys that the row sees; with head_dim 128 and more than 32 rows (max_rows x n_q_heads / n_kv_heads) it may
  * also take q as a sum of two e4m3 numbers (exact but for elements below 2^-9 of the row's largest, which
  * are off by at most 2^-17 of that), where an infinity counts as NaN.  Other calls keep fp32. */
 DFLASH_API int64_t dflash_kv8_attention_workspace(const dflash_attention* a, const dflash_ragged* batch,

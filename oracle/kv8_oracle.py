@@ -115,14 +115,30 @@ def gather8(codes, scale, lens, table):
     return T.gather(decode(codes, scale), lens, table)
 
 
+def largest_share(q, k, v, L, causal, window, scale):
+    """[n, hq]: the largest probability times value (its size) of the keys that a row sees."""
+    n, hq, _ = q.shape
+    out = torch.zeros((n, hq), dtype=torch.float64)
+    if not n:
+        return out
+    g = hq // k.shape[1]
+    rel = torch.arange(L - n, L)[:, None] - torch.arange(L)[None, :]
+    see = (rel >= 0 if causal else torch.ones_like(rel, dtype=torch.bool)) & (rel < window if window else True)
+    for h in range(hq):
+        s = torch.where(see, (q[:, h].double() @ k[:, h // g].double().t()) * scale, -math.inf)
+        out[:, h] = torch.nan_to_num(torch.softmax(s, 1) * v[:, h // g].amax(-1), nan=0.0).amax(1)
+    return out
+
+
 def attention8(q, seq_k, seq_v, starts, lens, causal, window, scale, bf16, tensor_cores, q_pieces=False):
     """As T.attention over the decoded values, with the bounds of these kernels.
 
     fp32 arithmetic is T's, with the two scales' products (2 2^-24 of a score and of a value, within its d + 4 and
-    its sums' slack).  The output is rounded once.  On the tensor cores a probability is rounded to fp16 (2^-11
-    relative) and so may a value be at a scale that is not its tile's (2^-11); both have steps of 2^-24 below
-    their smallest normal number, which is 2^-31 of the largest value a key may add (probabilities are held at
-    2^6 or more times their size, values at the size of the largest scale).  q_pieces: q is the sum of two e4m3
+    its sums' slack).  The output is rounded once.  On the tensor cores a probability times its key's scale of V is
+    rounded to fp16: 2^-11 relative, and half a step of 2^-24 below the smallest normal number.  The row's unit is such
+    that the largest such product of the keys that the row sees is 2^7 or more, so that half step is at most 2^-32 of
+    it, for each key, times a code of up to 448.  (A key's largest code is at least 1 here: its largest value stands for
+    its scale.)  q_pieces: q is the sum of two e4m3
     pieces, scaled so that its largest element is 2^7 or more; the second piece is off by at most half its step
     of 2^-9, that is 2^-17 of the largest, where an element is below 2^-9 of that (larger ones are exact): twice
     that error of a score for a weight, once for the log-sum-exp."""
@@ -131,9 +147,9 @@ def attention8(q, seq_k, seq_v, starts, lens, causal, window, scale, bf16, tenso
         s, e = starts[b], starts[b + 1]
         if tensor_cores:
             fin = lambda x: torch.where(torch.isfinite(x), x, 0.0).abs()
-            most = float(fin(seq_v[b]).max()) * 448 if L else 0.0
             av = T.attention(q[s:e], [seq_k[b]], [fin(seq_v[b])], [0, e - s], [L], causal, window, scale, False)[0]
-            tol[s:e] += av * 2.0 ** -10 + L * 2.0 ** -31 * most
+            most = largest_share(q[s:e], seq_k[b], fin(seq_v[b]), L, causal, window, scale)
+            tol[s:e] += av * 2.0 ** -10 + L * 2.0 ** -32 * 448 * most[..., None]
             if q_pieces and L:
                 x = fin(q[s:e].double())
                 top = x.amax(-1, keepdim=True)

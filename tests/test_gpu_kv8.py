@@ -594,3 +594,62 @@ def test_a_nan_in_the_last_tile_reaches_who_sees_it(dtype, d, causal, window, ro
     check_attention(o, lse, ref, sum(rows))
     rest = [c for c in range(d) if c != 17]
     assert bool(torch.isfinite(out[..., rest]).all())
+
+
+# ---- scales of V that a row does not see, or that come with next to no probability
+@pytest.mark.usefixtures("span")
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("rows,lens", [([3], [2266]), ([30], [2266]), ([3, 40], [2266, 2270]), ([150], [2266])])
+@pytest.mark.parametrize("window", [0, 2010])
+def test_scales_of_hidden_pages_do_not_matter(dtype, d, rows, lens, window):
+    """Pages that only the later rows see (without a window), or only the earlier ones (with one), have scales 2^40
+    above the others: the rows that do not see them keep all their bits."""
+    B = Batch8(dtype, 4, 1, d, 16, rows, lens, seed=53, tail=0)
+    kp, vp, ks, vs = B.appended()
+    for b, (n, L) in enumerate(zip(rows, lens)):
+        for j in range(O.n_pages_of(L, 16)):
+            if 16 * j + 16 <= L - window if window else 16 * j > L - n:
+                vs[int(B.table[b, j])] *= 2.0 ** 40
+    out, lse, _ = run8(B, True, window, append=False, pages=B.cuda(kp, vp, ks, vs))
+    check_attention(out, lse, ref8(B, True, window, pages=(kp, vp, ks, vs)), sum(rows))
+
+
+@pytest.mark.usefixtures("span")
+@pytest.mark.parametrize("dtype,d", [("f32", 64), ("bf16", 64), ("bf16", 128)])
+@pytest.mark.parametrize("rows", [[1], [3], [30], [150]])
+@pytest.mark.parametrize("bits", [40, 120])
+@pytest.mark.parametrize("where", [0, 17, 131])
+def test_a_large_scale_of_small_probability(dtype, d, rows, bits, where):
+    """One page whose values are 2^bits times the others' and whose probabilities are as much smaller: both matter."""
+    B = Batch8(dtype, 4, 1, d, 16, rows, [2450], seed=57, tail=0)
+    B.q = B.q.abs()
+    kp, vp, ks, vs = B.appended()
+    pg = int(B.table[0, where])
+    vs = torch.exp2(torch.round(torch.log2(vs)) - bits // 2)
+    ks = ks * 0.25
+    vs[pg] *= 2.0 ** bits
+    vs = vs.clamp(2.0 ** -60, 2.0 ** 60)
+    kp[pg] = 0xB8                                                   # -1
+    ks[pg] = bits * math.log(2) / (0.8 * d * d ** -0.5)             # the mean of |q| is 0.8
+    out, lse, _ = run8(B, True, 0, append=False, pages=B.cuda(kp, vp, ks, vs))
+    check_attention(out, lse, ref8(B, True, 0, pages=(kp, vp, ks, vs)), rows[0])
+
+
+@pytest.mark.usefixtures("span")
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("rows", [[1], [30], [150]])
+def test_one_key_of_a_huge_score(d, rows):
+    """Scores of some 2^17 apart: a row is its best key's value, whose scale is its own page's, to bf16's last bit."""
+    B = Batch8("bf16", 4, 1, d, 16, rows, [300], seed=59, tail=0)
+    B.q = B.q.abs() + 1
+    kp, vp, ks, vs = B.appended()
+    best = 100                                                       # a key that every row sees
+    pg, sl = int(B.table[0, best // 16]), best % 16
+    kp[:] = 0xB8
+    kp[pg, sl] = 0x38                                                # 1 at one key, -1 elsewhere
+    ks[:] = 2.0 ** 12
+    vs *= torch.exp2(torch.arange(len(vs), dtype=torch.float32) % 7 - 3)[:, None]
+    out, lse, _ = run8(B, True, 0, append=False, pages=B.cuda(kp, vp, ks, vs))
+    want = (O.decode(vp, vs)[pg, sl, 0]).expand(rows[0], 4, d)
+    err = (out.cpu().double() - want).abs()
+    assert bool((err <= want.abs() * (2.0 ** -8 + 2.0 ** -11)).all()), float((err / want.abs().clamp(min=1e-30)).max())
