@@ -259,7 +259,8 @@ __device__ __forceinline__ Ask ask_of(const Rows& t, const int32_t* new_lens, in
 }
 
 // One cluster.  A thread has a stretch of rows and a stretch of pages, both contiguous, so that ranks
-// are prefix sums over the threads.  Bound by latency: five cluster barriers and the loads between them (32 prompts
+// are prefix sums over the threads.  Bound by latency: four cluster barriers (five where pages run out) and the loads
+// between them (32 prompts
 // of 8 samples, with the reorder in front and the copies behind it: 26.7 us, 31.1 when rows and entries were read again
 // in each step and one at a time).
 // ONE: a small pool and little to copy, one CTA, whose working arrays are in shared memory and which makes
@@ -358,11 +359,12 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
     return n > 1 && !(n == get(ws.writers + p) && get(ws.owner + p) == row);
   };
   uint64_t sum = 0;  // pages << 32 | copies
-  bool mine_c = false;
+  uint32_t own_copy = 0;  // a bit per row of this thread: its begun page has to be copied
   for (int row = r0; row < r1; ++row) {
     const Ask a = ask(row);
     if (!a.ok) continue;
-    const bool c = mine_c = copies(row, a);
+    const bool c = copies(row, a);
+    own_copy |= (uint32_t)c << (row - r0);
     sum += (uint64_t)(max(a.need - a.have, 0) + c) << 32 | (uint64_t)c;
   }
   Scan<ONE> rs{s_warps[1], &s_cta[1], 0, 0};
@@ -373,16 +375,40 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
   // 4: rows take their pages, behind those of the rows in front of them.  Once one does not get
   // its pages none behind it does (their sums only grow), so the copies that are made are the
   // first of the list.
+  auto asks = [&](int row, const Ask& a) { return max(a.need - a.have, 0) + (int)((own_copy >> (row - r0)) & 1u); };
   uint32_t granted = 0, copied = 0;  // a bit per row of this thread
+  int64_t sum_to = pages;
+  for (int row = r0; row < r1; ++row) {
+    const Ask a = ask(row);
+    if (!a.ok) continue;
+    const int n = asks(row, a);
+    if (n == 0 || sum_to + n <= n_free) granted |= 1u << (row - r0);
+    sum_to += n;
+  }
+  if ((int64_t)(rs.total >> 32) > n_free) {
+    // Some rows are refused (the same answer in every thread).  One that does not get its copy still names the page
+    // that it shares, which the row that would keep it must not write to then: that one is refused too.
+    for (int row = r0; row < r1; ++row)
+      if ((own_copy & ~granted) >> (row - r0) & 1u) ws.owner[own ? mine_page : *entry(row, ask(row).have - 1)] = -1;
+    sync();
+    for (int row = r0; row < r1; ++row) {
+      const uint32_t bit = 1u << (row - r0);
+      const Ask a = ask(row);
+      if (a.writes && (granted & ~own_copy & bit)) {
+        const int p = own ? mine_page : *entry(row, a.have - 1);
+        if (there(p) && (own ? mine_refs : load_now(refs + p)) > 1 && get(ws.owner + p) < 0) granted &= ~bit;
+      }
+      if (a.ok && !(granted & bit)) bad |= DFLASH_STATUS_FULL;
+    }
+  }
   int given = 0;
   for (int row = r0; row < r1; ++row) {
     const Ask a = ask(row);
     if (!a.ok) continue;
-    const int c = own ? mine_c : copies(row, a), n = max(a.need - a.have, 0) + c;
-    if (n == 0 || pages + n <= n_free) {
-      granted |= 1u << (row - r0);
+    const int n = asks(row, a);
+    if ((granted >> (row - r0)) & 1u) {
       int64_t at = pages;
-      if (c) {
+      if ((own_copy >> (row - r0)) & 1u) {
         copied |= 1u << (row - r0);
         ws.src[made] = own ? mine_page : *entry(row, a.have - 1);
         ws.dst[made] = get(ws.free_ + at++);
@@ -394,8 +420,6 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
         refs[p] = 1;
       }
       given += n;
-    } else {
-      bad |= DFLASH_STATUS_FULL;
     }
     pages += n;
   }

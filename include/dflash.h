@@ -811,7 +811,8 @@ DFLASH_API int64_t dflash_pages_workspace(int64_t n_pages, int32_t rows);
  * given back.  Longer: pages are added, and a begun last page that other rows hold too is
  * replaced by a copy of its own first, in every buffer (of rows that all write to
  * one page that no one else holds, the first keeps it).  Rows whose pages, together with those of the rows in
- * front of them, are not there keep their length and pages (status 16); a new length
+ * front of them, are not there keep their length and pages (status 16), and so does a row that
+ * would keep a page which one of those still holds; a new length
  * outside 0 .. width * page_size likewise (status 2).  Page ids outside the pool: status 4.
  * free_pages (device, or NULL): the pages that are free then. */
 DFLASH_API int dflash_pages_resize(int32_t* refs, int64_t n_pages, const dflash_page_rows* rows,

@@ -192,36 +192,39 @@ def resize(refs, table, lens, new_lens, page):
         for j in range(n_pages_of(m, page), n_pages_of(n, page)):
             refs[table[i][j]] -= 1
             table[i][j] = -1
-    writers = {}
+    writers, begun, asks = {}, {}, []
     for i, (n, m) in enumerate(zip(lens, new_lens)):
         if m > n and n % page:
-            writers.setdefault(table[i][n_pages_of(n, page) - 1], []).append(i)
+            begun[i] = table[i][n_pages_of(n, page) - 1]
+            writers.setdefault(begun[i], []).append(i)
     free = [p for p, c in enumerate(refs) if c <= 0]
-    taken, copies, refused, before = 0, [], [], list(refs)
+    taken, copies, refused, before = 0, [], set(), list(refs)
     for i, (n, m) in enumerate(zip(lens, new_lens)):
-        have, need = n_pages_of(n, page), n_pages_of(m, page)
-        copy = False
-        if m > n and n % page:
-            p = table[i][have - 1]
-            copy = before[p] > 1 and not (before[p] == len(writers[p]) and writers[p][0] == i)
-        want = max(need - have, 0) + copy
-        if want and taken + want > len(free):
-            refused.append(i)
-            taken = len(free) + 1          # nor does any row behind it that asks for pages
+        p = begun.get(i)
+        copy = p is not None and before[p] > 1 and not (before[p] == len(writers[p]) and writers[p][0] == i)
+        ask = max(n_pages_of(m, page) - n_pages_of(n, page), 0) + copy
+        asks.append((taken, copy))
+        taken += ask
+        if ask and taken > len(free):          # nor does any row behind it that asks for pages
+            refused.add(i)
+    # the row that would keep a page writes to it only if all others that hold it have their copies
+    refused |= {i for i, p in begun.items() if not asks[i][1] and before[p] > 1 and any(w in refused for w in writers[p])}
+    for i, (n, m) in enumerate(zip(lens, new_lens)):
+        if i in refused:
             continue
+        at, copy = asks[i]
         if copy:
-            p = table[i][have - 1]
-            copies.append((p, free[taken]))
-            refs[p] -= 1
-            refs[free[taken]] = 1
-            table[i][have - 1] = free[taken]
-            taken += 1
-        for j in range(have, need):
-            table[i][j] = free[taken]
-            refs[free[taken]] = 1
-            taken += 1
+            copies.append((begun[i], free[at]))
+            refs[begun[i]] -= 1
+            refs[free[at]] = 1
+            table[i][n_pages_of(n, page) - 1] = free[at]
+            at += 1
+        for j in range(n_pages_of(n, page), n_pages_of(m, page)):
+            table[i][j] = free[at]
+            refs[free[at]] = 1
+            at += 1
         lens[i] = m
-    return refs, table, lens, copies, refused
+    return refs, table, lens, copies, sorted(refused)
 
 
 def compact(refs, table, lens, page):

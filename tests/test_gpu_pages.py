@@ -276,3 +276,63 @@ def test_a_captured_step_of_the_whole_cache():
                                         [0, 2], [41], True, 0, d ** -0.5, True, True)
             err = (a["out"][layer][sl].double().cpu() - o).abs()
             assert bool((err <= tol).all()), float((err - tol).max())
+
+
+def grown(refs, table, lens, want, page, bufs=None):
+    """dflash_pages_resize of lists: refs, table and lens afterwards, the free pages and the status word."""
+    D = lib()
+    r, t, l, free, status = i32(refs), i32(table), i32(lens), i32([-1]), i32([0])
+    D.dflash_pages_resize(r, t, l, i32(want), None if bufs is None else D.dflash_page_buffers(bufs), page_size=page,
+                          free_pages=free, status=status)
+    return r.tolist(), t.tolist(), l.tolist(), free.item(), status.item()
+
+
+SHARED = [  # refs, table, lens, want: rows that write to begun pages of one another in a pool without pages for all
+    ([2, 2], [[0, 1], [0, 1]], [18, 20], [21, 22]),
+    ([2, 2], [[0, 1], [0, 1]], [20, 18], [21, 22]),
+    ([3, 3, 0], [[0, 1], [0, 1], [0, 1]], [18, 20, 19], [21, 22, 23]),
+    ([3, 3, 0, 0], [[0, 1], [0, 1], [0, 1]], [18, 20, 19], [21, 22, 23]),
+    ([3, 3, 0, 0], [[0, 1, -1], [0, 1, -1], [0, 1, -1]], [18, 20, 19], [40, 22, 23]),
+    ([2, 2, 1, 0], [[0, 1, -1], [2, -1, -1], [0, 1, -1]], [18, 16, 20], [21, 48, 22]),
+    ([2, 2, 2, 2, 0], [[0, 1, -1], [0, 1, -1], [2, 3, -1], [2, 3, -1]], [18, 20, 18, 20], [21, 22, 21, 22]),
+    ([2, 2, 0, 0, 0], [[0, 1, -1, -1], [0, 1, -1, -1]], [18, 20], [50, 60]),
+]
+
+
+@pytest.mark.parametrize("case", range(len(SHARED)))
+@pytest.mark.parametrize("clusters", [False, True])
+def test_nobody_writes_to_a_page_that_a_refused_row_still_holds(case, clusters):
+    refs, table, lens, want = SHARED[case]
+    n_pages, rows = len(refs), len(lens)
+    if clusters:   # the form of large pools: rows of nothing behind these
+        table = table + [[-1] * len(table[0])] * 1100
+        lens, want = lens + [0] * 1100, want + [0] * 1100
+    r, t, l, free, status = grown(refs, table, lens, want, 16)
+    er, et, el, copies, refused = O.resize(refs, table, lens, want, 16)
+    assert (r, t, l) == (er, et, el) and free == sum(c <= 0 for c in er) and status == (16 if refused else 0)
+    for i in range(rows):
+        if l[i] == want[i] and want[i] > lens[i] and lens[i] % 16:
+            assert r[t[i][(lens[i] - 1) // 16]] == 1, (i, r, t)
+        if l[i] != want[i]:
+            assert t[i] == table[i] and l[i] == lens[i]
+
+
+@pytest.mark.parametrize("seed", range(8))
+def test_forks_that_grow_in_a_pool_without_room(seed):
+    """Rows forked, some of them cut back within the shared page, all grown with any number of pages left."""
+    rng = random.Random(100 + seed)
+    n, page, width = [3, 8, 40, 500, 9000, 5, 17, 300][seed], [16, 8, 16, 8, 8, 64, 16, 16][seed], 6
+    heads = max(1, n // 4)
+    lens = [rng.randrange(1, 3 * page) for _ in range(heads)]
+    P = Pool(sum(O.n_pages_of(x, page) for x in lens) + 1 + rng.randrange(0, n), page, lens, width, seed)
+    P.refs, P.table, P.lens = O.reorder(P.refs, P.table, P.lens, [rng.randrange(heads) for _ in range(n)], page, width)
+    back = [x - rng.randrange(0, (x - 1) % page + 1) if x else 0 for x in P.lens]      # within the last page
+    P.refs, P.table, P.lens, _, _ = O.resize(P.refs, P.table, P.lens, back, page)
+    want = [rng.choice([x, x + 1, x + rng.randrange(0, page)]) for x in P.lens]
+    r, t, l, free, status = grown(P.refs, P.table, P.lens, want, page)
+    er, et, el, copies, refused = O.resize(P.refs, P.table, P.lens, want, page)
+    assert r == er and t == et and l == el and free == sum(c <= 0 for c in er)
+    assert status == (16 if refused else 0)
+    for i in range(n):
+        if l[i] > P.lens[i] and P.lens[i] % page:
+            assert r[t[i][(P.lens[i] - 1) // page]] == 1

@@ -263,3 +263,33 @@ def test_bookkeeping_keeps_the_counts():
                 if p >= 0:
                     count[p] += 1
         assert count == refs
+
+
+def test_a_full_pool_leaves_no_page_with_a_writer_and_a_reader():
+    """Rows that share begun pages at other lengths, all grown, any number of pages left: who is refused keeps length
+    and pages, who grows writes to pages of its own, and what anyone holds is counted."""
+    import random
+    rng = random.Random(1)
+    page, width, hit = 8, 4, 0
+    for _ in range(400):
+        heads, spare = rng.randrange(1, 4), rng.randrange(0, 5)
+        lens = [rng.randrange(1, 2 * page + 1) for _ in range(heads)]
+        refs, table = [], []
+        for n in lens:
+            table.append(list(range(len(refs), len(refs) + O.n_pages_of(n, page))))
+            refs += [1] * O.n_pages_of(n, page)
+        refs += [0] * spare
+        table = [t + [-1] * (width - len(t)) for t in table]
+        refs, table, lens = O.reorder(refs, table, lens, [rng.randrange(heads) for _ in range(rng.randrange(1, 6))], page, width)
+        refs, table, lens, _, _ = O.resize(refs, table, lens, [n - rng.randrange(0, (n - 1) % page + 1) for n in lens], page)
+        want = [n + rng.randrange(0, 2 * page) for n in lens]
+        r, t, l, copies, refused = O.resize(refs, table, lens, want, page)
+        assert all((l[i], t[i]) == (lens[i], table[i]) for i in refused)
+        assert [l[i] for i in range(len(l)) if i not in refused] == [want[i] for i in range(len(l)) if i not in refused]
+        count = [sum(p in row for row in t) for p in range(len(r))]
+        assert count == r and len({b for _, b in copies}) == len(copies)
+        for i in range(len(l)):
+            if l[i] > lens[i] and lens[i] % page:
+                assert r[t[i][(lens[i] - 1) // page]] == 1
+        hit += len(refused) > 0
+    assert hit > 20
