@@ -358,20 +358,20 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
     const int n = own ? mine_refs : load_now(refs + p);
     return n > 1 && !(n == get(ws.writers + p) && get(ws.owner + p) == row);
   };
-  uint64_t sum = 0;  // pages << 32 | copies
+  uint64_t sum = 0;  // pages << 16 | copies: up to 2^15 rows ask for 2^35 + 2^15 pages and 2^15 copies
   uint32_t own_copy = 0;  // a bit per row of this thread: its begun page has to be copied
   for (int row = r0; row < r1; ++row) {
     const Ask a = ask(row);
     if (!a.ok) continue;
     const bool c = copies(row, a);
     own_copy |= (uint32_t)c << (row - r0);
-    sum += (uint64_t)(max(a.need - a.have, 0) + c) << 32 | (uint64_t)c;
+    sum += (uint64_t)(max(a.need - a.have, 0) + c) << 16 | (uint64_t)c;
   }
   Scan<ONE> rs{s_warps[1], &s_cta[1], 0, 0};
   if (free_pages && tid == 0) *free_pages = (int)fs.total;
   rs.run(sum);
   const int64_t n_free = (int64_t)fs.total;
-  int64_t pages = (int64_t)(rs.prefix >> 32), made = (int64_t)(rs.prefix & 0xffffffffu);
+  int64_t pages = (int64_t)(rs.prefix >> 16), made = (int64_t)(rs.prefix & 0xffffu);
   // 4: rows take their pages, behind those of the rows in front of them.  Once one does not get
   // its pages none behind it does (their sums only grow), so the copies that are made are the
   // first of the list.
@@ -385,7 +385,7 @@ __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const
     if (n == 0 || sum_to + n <= n_free) granted |= 1u << (row - r0);
     sum_to += n;
   }
-  if ((int64_t)(rs.total >> 32) > n_free) {
+  if ((int64_t)(rs.total >> 16) > n_free) {
     // Some rows are refused (the same answer in every thread).  One that does not get its copy still names the page
     // that it shares, which the row that would keep it must not write to then: that one is refused too.
     for (int row = r0; row < r1; ++row)

@@ -336,3 +336,22 @@ def test_forks_that_grow_in_a_pool_without_room(seed):
     for i in range(n):
         if l[i] > P.lens[i] and P.lens[i] % page:
             assert r[t[i][(P.lens[i] - 1) // page]] == 1
+
+
+def test_pages_asked_for_beyond_two_to_the_32():
+    """Rows ask for 2^32 pages together in front of a last one that asks for one: it does not get what the first has."""
+    D = lib()
+    rows, width, page, n_pages = 4098, 1 << 20, 8, 64
+    table = torch.empty((rows, width), dtype=torch.int32, device="cuda")       # (16 GiB, looked at in a few places)
+    table[0, :2], table[rows - 1, :2] = -1, -1
+    lens = torch.zeros(rows, dtype=torch.int32, device="cuda")
+    want = torch.full((rows,), width * page, dtype=torch.int32, device="cuda")
+    want[0], want[1], want[rows - 1] = page, (width - 1) * page, page
+    assert int(((want.long() + page - 1) // page)[:-1].sum()) == 1 << 32
+    refs, free, status = torch.zeros(n_pages, dtype=torch.int32, device="cuda"), i32([-1]), i32([0])
+    D.dflash_pages_resize(refs, table, lens, want, None, page_size=page, free_pages=free, status=status)
+    with pytest.raises(D.DFlashError, match="free page"):
+        D.dflash_status_check(status)
+    assert table[0, 0].item() == 0 and table[rows - 1, 0].item() == -1
+    assert lens[0].item() == page and int(lens[1:].abs().sum()) == 0
+    assert refs.tolist() == [1] + [0] * (n_pages - 1) and free.item() == n_pages - 1
