@@ -90,10 +90,7 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
   Seq s{0, 0, 0, false};
   for (int base = 0; base < r.batch; base += 32) {
     Seq c{0, 0, 0, false};
-    if (base + lane < r.batch) {
-      c = load_seq(r, base + lane);
-      if (!c.ok && blockIdx.x == 0 && blockIdx.y == 0 && warp == 0) flag_status(r.status, DFLASH_STATUS_BOUNDS);
-    }
+    if (base + lane < r.batch) c = load_seq(r, base + lane);
     const int n = pieces_of(c, kv.page_shift);
     int incl = n;
 #pragma unroll
@@ -114,6 +111,10 @@ __global__ void __launch_bounds__(kThreads) k_kv8_append(Ragged r, Rows8 x, Kv8V
     rest -= __shfl_sync(0xffffffffu, incl, 31);
     if (rest < 0) break;  // (lengths that overflow: no one's piece)
   }
+  // one warp tells of bad sequences, all of them: in the last CTA, which has the last piece or none
+  if (blockIdx.x == gridDim.x - 1 && blockIdx.y == 0 && warp == 0)
+    for (int i = lane; i < r.batch; i += 32)
+      if (!load_seq(r, i).ok) flag_status(r.status, DFLASH_STATUS_BOUNDS);
   if (b < 0) return;
   const int first = s.len - s.n, page = (first >> kv.page_shift) + j, size = 1 << kv.page_shift;
   const int p0 = max(first, page << kv.page_shift), p1 = min(s.len, (page + 1) << kv.page_shift);

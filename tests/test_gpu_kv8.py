@@ -653,3 +653,32 @@ def test_one_key_of_a_huge_score(d, rows):
     want = (O.decode(vp, vs)[pg, sl, 0]).expand(rows[0], 4, d)
     err = (out.cpu().double() - want).abs()
     assert bool((err <= want.abs() * (2.0 ** -8 + 2.0 ** -11)).all()), float((err / want.abs().clamp(min=1e-30)).max())
+
+
+# ---- a bad sequence behind the first 32
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("batch,bad", [(64, 40), (64, 63), (300, 33), (300, 299), (33, 32), (20, 19)])
+@pytest.mark.parametrize("rows", [1, 0, 40])
+def test_append_tells_of_a_bad_sequence_anywhere(dtype, batch, bad, rows):
+    """The sequence at index bad has `rows` new rows (the others one) and a length outside its bounds."""
+    D = lib()
+    n = [1] * batch
+    n[bad] = rows
+    lens = [5 + b % 40 for b in range(batch)]
+    lens[bad] = 50
+    B = Batch8(dtype, 2, 2, 64, 16, n, lens, seed=61, tail=0, pow2=True)
+    want = B.appended()
+    for length in (-1, 16 * B.table.shape[1] + 1) + ((rows - 1,) if rows > 1 else ()):
+        P = B.cuda(B.kp, B.vp, B.ks, B.vs)
+        told = list(lens)
+        told[bad] = length
+        status = i32([0])
+        D.dflash_kv8_append(B.k.cuda(), B.v.cuda(), *P, i32(B.starts), i32(told), B.table.cuda(), status=status)
+        with pytest.raises(D.DFlashError, match="bounds"):
+            D.dflash_status_check(status)
+        ids = B.table[bad].long()
+        ids = ids[ids >= 0]
+        w = [x.clone() for x in want]
+        for x, y in zip(w, (B.kp, B.vp, B.ks, B.vs)):
+            x[ids] = y[ids]                                          # its pages keep what they held
+        assert same_codes(P[0], w[0]) and same_codes(P[1], w[1]) and same_scales(P[2], w[2]) and same_scales(P[3], w[3])
