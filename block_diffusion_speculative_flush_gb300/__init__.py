@@ -981,7 +981,8 @@ def dflash_pages_resize(refs: torch.Tensor, table: torch.Tensor, lens: torch.Ten
                         buffers: PageBuffers | None, page_size: int, free_pages: torch.Tensor | None = None,
                         workspace=None, status=None, stream=None) -> None:
     """Sets the rows' lengths to new_lens: pages behind them go back, new ones are the lowest free ids, and a
-    begun last page that others hold too is copied before its row grows."""
+    begun last page that others hold too is copied before its row grows.  A row whose pages are not there, or whose
+    begun page a row without its own copy still holds, stays as it is (status 16)."""
     device = _same_device(refs, table, lens, new_lens, free_pages, workspace, status,
                           None if buffers is None else buffers.tensors[0])
     rows = _page_rows(table, lens, page_size, "")

@@ -35,12 +35,11 @@
 // Bound by memory where calls are long: 64 single tokens over 1k to 16k, 8 KV heads of 128, pages of 16, 665 MB in
 // 116 us, 5.7 TB/s (86% of a measured copy; loads in flight and issue slots keep it there).  Short calls are
 // latency, the chain length -> table -> scales and codes -> products -> cluster: one user's block of 16 over 4096
-// 18.4 us.
+// 18.2 us.
 #include <cooperative_groups.h>
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "common.cuh"
 #include "kv8.h"
@@ -755,13 +754,13 @@ struct FewHost {
 // CTAs of a cluster per item, or 0 for ranges.  A cut item costs its rows' start and end again, and a launch that
 // puts the parts together; 32 over 8 heads of 128, single tokens but for the last:
 //   all at once, the largest share of a CTA kMaxShare (36 of 8 CTAs fit, not 38: 12 and 20 us).  One user over 300
-//     tokens 6.6 us (ranges 12.3), over 16000 19 (27); 8 users over 8000 28 (43), over 16000 48 (64).
+//     tokens 6.6 us (ranges 11.4), over 16000 19 (27); 8 users over 8000 28 (43), over 16000 49 (65).
 //   in turn, longest first, so that the last to end are short: one CTA an item while the longest (by the bound of
 //     lengths) has at most 300 chunks for each item that a CTA's place gets, two up to 1000, and where items are
-//     fewer than places four up to 2400: 16 users over 1k to 16k 38 us (ranges 46), 24 53 (62).  64 users over 1k to 16k
-//     with one, two, four CTAs and ranges 134, 115, 142, 133 us (in the batch's order 150, 133, 136), over 1k to 8k
-//     75, 88, 111, 91, over 100 to 2k 21, 38, 62, 33; 128 over 1k to 16k 227, 260, 313, 270; 128 blocks of 8 over 1k
-//     to 8k 298, 381, 549, 365.  (A batch whose places are mostly empty has its few long sequences on few CTAs then.)
+//     fewer than places four up to 2400: 16 users over 1k to 16k 37 us (ranges 47), 24 52 (61).  64 users over 1k to 16k
+//     with one, two, four CTAs and ranges 136, 114, 139, 132 us (in the batch's order 150, 133, 136), over 1k to 8k
+//     76, 87, 110, 90, over 100 to 2k 21, 38, 62, 32; 128 over 1k to 16k 226, 258, 313, 269; 128 blocks of 8 over 1k
+//     to 8k 298, 378, 543, 369.  (A batch whose places are mostly empty has its few long sequences on few CTAs then.)
 int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int ctas) {
   const int64_t items = (int64_t)r.batch * tiles * a.Hkv;
   const int64_t span = a.window ? std::min<int64_t>(r.max_len, (int64_t)a.window + r.max_rows) : r.max_len;
@@ -779,7 +778,7 @@ int few_cluster(const Ragged& r, const AttnCall& a, int rows, int tiles, int cta
 FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
   const int rows = rows_of(r, a);
   FewHost h;
-  // what an item costs besides its chunks; 64 single tokens over 1k to 16k: 4 158 us, 16 151, 28 133, 44 133
+  // what an item costs besides its chunks; 64 single tokens over 1k to 16k: 4 140 us, 16 134, 28 132, 44 130
   h.p.pad = 28;
   h.p.min_units = 8;
   h.nb = rows <= 8 ? 1 : 2;
@@ -788,7 +787,7 @@ FewHost few_plan(const Ragged& r, const AttnCall& a, int sms) {
   h.p.in_turn = h.p.cluster && (int64_t)r.batch * h.p.tiles * a.Hkv * h.p.cluster > 2 * sms;
   h.p.slots = 4 * sms;
   // A tile of rows converts the codes anew, so 32 rows a CTA (one an SM) where ranges are cut: 64 users' blocks of 8
-  // over 2048 tokens 132 us (16 rows 156), 8 users' 43 (49).
+  // over 2048 tokens 134 us (16 rows 152), 8 users' 34 (34).
   if (!h.p.cluster && rows > 16) {
     h.nb = 4;
     h.p.tiles = (rows + 31) / 32;
@@ -829,8 +828,8 @@ cudaError_t launch_few(const Ragged& r, const AttnCall& a, const Kv8View& kv, in
 
 // Few rows, or many that are a short call: a KV head's rows of a sequence fill a quarter of the 128-row tiles or less,
 // or all items run at once as clusters.  32 over 8 heads of 128, this and the tiles: 64 sequences of 32 rows over 2048
-// 132 and 188 us, of 64 rows 231 and 189; 8 of 32 over 16000 101 and 150, of 48 160 and 151; one user's 64 rows over
-// 4096 in clusters 18 and 36, 128 over 500 13 and 24.
+// 109 and 169 us, of 64 rows 236 and 167; 8 of 32 over 16000 109 and 133, of 48 167 and 132; one user's 64 rows over
+// 4096 in clusters 18 and 35, 128 over 500 13 and 22.
 bool kv8_few(const Ragged& r, const AttnCall& a, int sms) { return rows_of(r, a) <= kFewRows || few_plan(r, a, sms).p.cluster > 0; }
 int64_t kv8_few_workspace(const Ragged& r, const AttnCall& a, int sms) {
   const FewHost h = few_plan(r, a, sms);

@@ -7,7 +7,6 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
-#include <vector>
 
 #include "common.cuh"
 #include "launch.h"
@@ -265,7 +264,7 @@ __device__ __forceinline__ Ask ask_of(const Rows& t, const int32_t* new_lens, in
 // in each step and one at a time).
 // ONE: a small pool and little to copy, one CTA, whose working arrays are in shared memory and which makes
 // the copies itself: one launch in place of two.  A user's four candidates, 76 pages, 2 layers, with the reorder in
-// front: 12.1 us, some 13 otherwise, and 20.6 against 23 of host time.
+// front: 12.5 us, some 13 otherwise, and 20.6 against 23 of host time.
 constexpr int kSmallPages = 2048, kSmallRows = 1024, kSmallBytes = 512 << 10;
 template <bool ONE>
 __device__ __forceinline__ void resize(int32_t* refs, int n_pages, Rows t, const int32_t* new_lens, ResizeWs ws,

@@ -30,10 +30,10 @@
 //          producer and the fixer) make V's, and for heads of 64 K's, fp16 in the ring.  For heads of 128 K's codes are
 //          multiplied as they are (kind::f8f6f4) with q as a sum of two e4m3 numbers, the softmax warps' first
 //          work on a stretch, so that K takes a quarter of the room and no conversion.  The softmax takes the
-//          scales (softmax_tile8).  4 x 2048 new rows over 6000 tokens, 32 over 8 heads of 128: 0.84 ms, 1.12
-//          PFLOP/s (57% of a measured cuBLAS peak), heads of 64 0.69; 6 chunks of 145 to 477 rows over 1.9k to 4.8k
-//          136 us, 0.69 PFLOP/s (whole items, two or one a CTA, leave a sixth of the SMs' time empty).
-//          Bound by the softmax of two tiles in turn: with the softmax left out 0.69 ms, the converters 0.84, a
+//          scales (softmax_tile8).  4 x 2048 new rows over 6000 tokens, 32 over 8 heads of 128: 0.86 ms, 1.10
+//          PFLOP/s (56% of a measured cuBLAS peak), heads of 64 0.69 ms (0.68); 6 chunks of 145 to 477 rows over 1.9k to
+//          4.8k 138 us, 0.67 PFLOP/s (whole items, two or one a CTA, leave a sixth of the SMs' time empty).
+//          Bound by the softmax of two tiles in turn (0.84 ms when its parts were timed): with the softmax left out 0.69 ms, the converters 0.84, a
 //          half or seven eighths of either product 0.86; the products alone are 0.48.
 // V rows of hidden keys may hold anything, and 0 * NaN is NaN: in tiles with
 // hidden keys the fixer zeroes the rows behind the sequence and puts non-finite

@@ -753,7 +753,8 @@ typedef struct dflash_kv8_pages {
  * (2^-60 .. 2^60) with which every finite new element is at most 448 codes, and is
  * never below what it was if the page holds rows in front of the new ones; where it
  * grows, those rows' codes are rounded again (exact, save where a value falls below
- * the smallest normal code, if the old scale is a power of two).  Codes round to nearest
+ * the smallest normal code, if the old scale is a power of two), and stay so when the length
+ * goes back.  Codes round to nearest
  * even and saturate; elements that are not finite become NaN.  Slots behind the new
  * rows keep their bits.  Pages as in dflash_kv_append. */
 DFLASH_API int dflash_kv8_append(const dflash_kv8_pages* pages, const dflash_ragged* batch, int32_t dtype,
